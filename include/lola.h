@@ -260,7 +260,11 @@ typedef enum {
     LOLA_KERNEL_HOLA_STATE = 7,  /* ... the delta-rule state path (chunked, tensor cores), scores */
     LOLA_KERNEL_HOLA_CACHE = 8,  /* ... the persistent cache at every chunk start */
     LOLA_KERNEL_HOLA_READ = 9,   /* ... the cache read and the gated sum */
-    LOLA_KERNEL_COUNT = 10
+    LOLA_KERNEL_ATTN = 10,       /* exact attention over packed prompts */
+    LOLA_KERNEL_APPEND = 11,     /* rotation and append to the paged cache */
+    LOLA_KERNEL_PAGED = 12,      /* exact attention of one token over the paged cache */
+    LOLA_KERNEL_PAGED_JOIN = 13, /* ... joining the pieces of split sequences */
+    LOLA_KERNEL_COUNT = 14
 } lola_kernel_id;
 
 /* enable != 0: clear the totals and start recording (process-wide); 0: stop recording. */
@@ -358,6 +362,121 @@ int32_t lola_hola_prefill(const lola_hola_config* cfg, int32_t n, const void* Q,
  * head is 0, else LOLA_ERR_DEVICE. */
 int32_t lola_hola_status(const lola_hola_config* cfg, int32_t n, const void* workspace, int32_t* host_status,
                          void* stream);
+
+/* ---- exact softmax attention: packed prompts and a paged key-value cache ------------------
+ * The exact layers of a stack that mixes LoLA layers with softmax attention, and the exact
+ * attention a LoLA layer stands in for.  With scale c, query head h of a row i reads key/value
+ * head h / (Hq / Hkv):
+ *   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(c q_i . k_j),  lse_i = log sum_j p_ij
+ * over the keys j that the row sees.  A row that sees no key gets o = 0 and lse = -infinity;
+ * keys a row does not see have no influence on it, whatever their bits (NaN included).
+ * Scores, maxima, sums and the running output are float32; with bfloat16 io the weights p are
+ * rounded to bfloat16 for the product with V (at most 2^-8 relative each, as the output's
+ * own rounding, and averaged over the keys), the sum is taken over the unrounded weights,
+ * and o is rounded once.  Device-side anomalies go to a word per device read with lola_attn_status(). */
+typedef struct {
+    int32_t Hq;      /* query heads */
+    int32_t Hkv;     /* key/value heads; Hq is a multiple of Hkv */
+    int32_t d;       /* head width of q, k and v: 64 or 128 */
+    int32_t dtype;   /* lola_dtype of q, k, v and o */
+    float scale;     /* c > 0; 0 means 1 / sqrt(d) */
+} lola_attn_config;
+
+/* Rows of heads: element (t, h, i) at data[t * row + h * head + i] (strides in elements).
+ * data is 16-byte aligned and both strides are positive multiples of 16 bytes.  Output rows
+ * must not overlap: head >= d and row >= heads * head, or row >= d and head >= rows * row. */
+typedef struct {
+    void* data;
+    int64_t row;
+    int64_t head;
+} lola_rows;
+
+/* Causal attention over packed prompts.  Sequence b has the query rows cu_q[b] .. cu_q[b+1] and
+ * the key/value rows cu_k[b] .. cu_k[b+1]; its last query sees all its keys and each earlier
+ * query one key less (query i of Lq sees keys j <= i + Lk - Lq: Lk = Lq is a whole prompt,
+ * Lk > Lq a later piece of one, and the first Lq - Lk queries see nothing where Lk < Lq).
+ *   Q, O  total_q rows of Hq heads      K, V  total_k rows of Hkv heads
+ *   cu_q, cu_k  device int32 [n_seq + 1], non-decreasing; cu_k may be NULL: the same as cu_q
+ *   lse   nullable device float32 [Hq, total_q]
+ * Rows of Q outside cu_q[0] .. cu_q[n_seq] are left as they were in O and lse.  Offsets that
+ * decrease or pass total_q / total_k make their sequence empty and set LOLA_ATTN_BAD_OFFSETS.
+ * total_q = 0 is a call that does nothing.  Stream-ordered; no workspace. */
+int32_t lola_attn_prefill(const lola_attn_config* cfg, int32_t n_seq, int32_t total_q, int32_t total_k,
+                          const int32_t* cu_q, const int32_t* cu_k, const lola_rows* Q, const lola_rows* K,
+                          const lola_rows* V, const lola_rows* O, float* lse, void* stream);
+
+/* A paged key-value cache of one layer.  Token t of sequence b is slot t % page of page
+ * table[b * table_stride + t / page]. */
+typedef struct {
+    void* K;               /* device io [n_pages, Hkv, page, d], 16-byte aligned */
+    void* V;
+    int32_t n_pages;
+    int32_t page;          /* tokens per page: 16, 32, 64, 128 or 256 */
+    int32_t n_seq;
+    int32_t width;         /* page-table columns */
+    int64_t table_stride;  /* elements from one sequence's table row to the next, >= width */
+    const int32_t* table;  /* device int32; entries behind a sequence's pages are not read */
+    const int32_t* kv_len; /* device int32 [n_seq]: tokens of each sequence, the tokens that a
+                            * lola_paged_append appends included; <= 0 means none */
+} lola_paged_kv;
+
+/* The element offset in K (and V) of token `pos` of sequence `seq`, head `head`, with the
+ * table and kv_len read on the host (a cache description with host pointers), or -1 where the
+ * position has no slot: pos outside [0, kv_len) or the table, or a page outside [0, n_pages).
+ * The kernels resolve positions with the same function. */
+int64_t lola_paged_slot(const lola_attn_config* cfg, const lola_paged_kv* kv, int32_t seq, int32_t head, int64_t pos);
+
+/* Channel pairs of the rotation over the first `rot` channels: (i, i + rot/2) or (2i, 2i + 1). */
+typedef enum { LOLA_PAIRS_HALVES = 0, LOLA_PAIRS_NEIGHBOURS = 1 } lola_pairs;
+
+/* Appends the new tokens' keys and values to the cache, rotating the keys (and the queries) on
+ * the way: a pair (a, b) of a token at position p becomes (a cos x - b sin x, b cos x + a sin x)
+ * with x = p * inv_freq[i] for pair i; channels from `rot` on are copied.
+ *   cu_new  device int32 [n_seq + 1]: the rows of each sequence's new tokens, which are its
+ *           last tokens: row cu_new[b] + j is token kv_len[b] - (cu_new[b+1] - cu_new[b]) + j.
+ *           NULL: one new token per sequence, row b for sequence b (n_tokens = n_seq)
+ *   K, V    n_tokens rows of Hkv heads;  Q  nullable: n_tokens rows of Hq heads
+ *   QO      the rotated queries (NULL with Q); may be Q itself
+ *   inv_freq  device float32 [rot / 2]; NULL: no rotation (Q must be NULL too)
+ *   rot     rotated channels: a multiple of 16, at most d (not read without inv_freq)
+ *   positions  nullable device int32 [n_tokens] >= 0: p of each row; NULL: the token's index in
+ *           its sequence
+ * x is taken modulo one turn in 64-bit integers, so that far positions lose nothing.  Rows
+ * outside cu_new, and rows whose token index is negative (an empty sequence of a padded batch),
+ * are skipped: nothing is written for them, QO included.  A token without a slot (no table
+ * column or a page outside the cache) sets LOLA_ATTN_BAD_PAGE and only its query is written.
+ * No two new tokens may share a slot. */
+int32_t lola_paged_append(const lola_attn_config* cfg, const lola_paged_kv* kv, int32_t n_tokens,
+                          const int32_t* cu_new, const lola_rows* K, const lola_rows* V, const lola_rows* Q,
+                          const lola_rows* QO, const float* inv_freq, int32_t rot, int32_t pairs,
+                          const int32_t* positions, void* stream);
+
+/* Bytes of device workspace a lola_paged_decode needs (negative: the lola_status of an invalid
+ * cfg).  It does not depend on the cache's lengths. */
+int64_t lola_paged_decode_workspace_bytes(const lola_attn_config* cfg);
+
+/* Attention of one query token per sequence over its kv_len cached tokens (the token's own key
+ * included, when it was appended before).  Row b of Q and O is sequence b.
+ *   lse  nullable device float32 [n_seq, Hq]
+ *   workspace  device, 16-byte aligned; its contents mean nothing before or after the call, and
+ *        calls that may run at the same time need one each
+ * The work is cut along the cache's length into equal pieces for the GPU's SMs, and a second
+ * kernel joins the pieces of each sequence in order: the same inputs give the same bits.  A page
+ * outside the cache sets LOLA_ATTN_BAD_PAGE and its tokens are not seen; a kv_len beyond
+ * width * page sets it too and counts as width * page. */
+int32_t lola_paged_decode(const lola_attn_config* cfg, const lola_paged_kv* kv, const lola_rows* Q,
+                          const lola_rows* O, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Anomalies of the exact-attention calls since the last lola_attn_status on this device. */
+typedef enum {
+    LOLA_ATTN_BAD_OFFSETS = 1, /* packed offsets that decrease or leave their rows */
+    LOLA_ATTN_BAD_PAGE = 2,    /* a page-table entry or length outside the cache */
+    LOLA_ATTN_TIMEOUT = 4      /* a bounded wait gave up: the call's outputs are not valid */
+} lola_attn_bits;
+
+/* Synchronises `stream`, returns the current device's bits in *host_bits (host, nullable) and
+ * clears them.  LOLA_OK if none is set, else LOLA_ERR_DEVICE. */
+int32_t lola_attn_status(int32_t* host_bits, void* stream);
 
 /* ---- self-test of the bounded waits -----------------------------------------------------
  * No counterpart in the LoLA paper.  Every wait of the library's kernels on an mbarrier (the

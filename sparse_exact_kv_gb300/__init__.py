@@ -34,6 +34,12 @@ LOLA_SCORE_KERNEL_SQ = 1
 LOLA_SCORE_KERNEL_ABS = 2
 LOLA_SCORE_KERNEL_RATIO = 3
 LOLA_SCORE_ATTENTION = 4
+LOLA_PAIRS_HALVES = 0
+LOLA_PAIRS_NEIGHBOURS = 1
+PAIRS = {"halves": 0, "neighbours": 1}
+LOLA_ATTN_BAD_OFFSETS = 1
+LOLA_ATTN_BAD_PAGE = 2
+LOLA_ATTN_TIMEOUT = 4
 SCORES = {"sre": 0, "kernel_sq": 1, "kernel_abs": 2, "kernel_ratio": 3, "attention": 4}
 
 # every symbol include/lola.h declares
@@ -41,11 +47,13 @@ EXPORTS = ("lola_version", "lola_status_string", "lola_last_cuda_error", "lola_c
            "lola_state_layout_of", "lola_state_bytes", "lola_prefill_workspace_bytes", "lola_state_init",
            "lola_prefill", "lola_decode_step", "lola_read_status", "lola_kernel_timing", "lola_kernel_time",
            "lola_kernel_name", "lola_prefill_noalloc", "lola_selftest_bounded_wait", "lola_sre_map",
-           "lola_sre_map_relative", "lola_hola_workspace_bytes", "lola_hola_prefill", "lola_hola_status")
+           "lola_sre_map_relative", "lola_hola_workspace_bytes", "lola_hola_prefill", "lola_hola_status",
+           "lola_attn_prefill", "lola_paged_slot", "lola_paged_append", "lola_paged_decode_workspace_bytes",
+           "lola_paged_decode", "lola_attn_status")
 # size of the fixed scratch array behind lola_prefill_noalloc (include/lola.h)
 LOLA_NOALLOC_SCRATCH_BYTES = 32 << 20
 KERNELS = ("state_init", "phi", "select", "output", "decode", "phi_q", "hola_prep", "hola_state", "hola_cache",
-           "hola_read")
+           "hola_read", "attn", "append", "paged", "paged_join")
 
 
 class lola_config(ctypes.Structure):
@@ -58,6 +66,21 @@ class lola_config(ctypes.Structure):
 class lola_hola_config(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("Hh", ctypes.c_int32), ("d_k", ctypes.c_int32), ("d_v", ctypes.c_int32),
                 ("w", ctypes.c_int32), ("chunk", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class lola_attn_config(ctypes.Structure):
+    _fields_ = [("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class lola_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class lola_paged_kv(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("n_seq", ctypes.c_int32), ("width", ctypes.c_int32), ("table_stride", ctypes.c_int64),
+                ("table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p)]
 
 
 class lola_state_layout(ctypes.Structure):
@@ -83,6 +106,9 @@ def _load():
     P = ctypes.c_void_p
     C = ctypes.POINTER(lola_config)
     HC = ctypes.POINTER(lola_hola_config)
+    AC = ctypes.POINTER(lola_attn_config)
+    PK = ctypes.POINTER(lola_paged_kv)
+    R = ctypes.POINTER(lola_rows)
     sig = {
         "lola_version": ([], ctypes.c_int32),
         "lola_status_string": ([ctypes.c_int32], ctypes.c_char_p),
@@ -107,6 +133,13 @@ def _load():
         "lola_hola_workspace_bytes": ([HC, ctypes.c_int32], ctypes.c_int64),
         "lola_hola_prefill": ([HC, ctypes.c_int32] + [P] * 14 + [ctypes.c_size_t, P], ctypes.c_int32),
         "lola_hola_status": ([HC, ctypes.c_int32, P, P, P], ctypes.c_int32),
+        "lola_attn_prefill": ([AC] + [ctypes.c_int32] * 3 + [P, P, R, R, R, R, P, P], ctypes.c_int32),
+        "lola_paged_slot": ([AC, PK, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64], ctypes.c_int64),
+        "lola_paged_append": ([AC, PK, ctypes.c_int32, P, R, R, R, R, P, ctypes.c_int32, ctypes.c_int32, P, P],
+                              ctypes.c_int32),
+        "lola_paged_decode_workspace_bytes": ([AC], ctypes.c_int64),
+        "lola_paged_decode": ([AC, PK, R, R, P, P, ctypes.c_size_t, P], ctypes.c_int32),
+        "lola_attn_status": ([ctypes.POINTER(ctypes.c_int32), P], ctypes.c_int32),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -280,8 +313,219 @@ def lola_hola_status(cfg: lola_hola_config, n: int, workspace, stream=None):
 
 
 # ---------------------------------------------------------------------------------------
+# Exact softmax attention: packed prompts and a paged key-value cache (include/lola.h)
+# ---------------------------------------------------------------------------------------
+
+def make_attn_config(Hq, Hkv, d, dtype, scale=None) -> lola_attn_config:
+    """``scale``: the logit scale, None for 1 / sqrt(d)."""
+    dt = dtype if isinstance(dtype, int) else {"f32": LOLA_F32, "bf16": LOLA_BF16,
+                                               torch.float32: LOLA_F32, torch.bfloat16: LOLA_BF16}[dtype]
+    return lola_attn_config(Hq, Hkv, d, dt, 0.0 if scale is None else scale)
+
+
+def _rows(t):
+    """lola_rows of a [rows, heads, d] tensor (a size-1 axis' stride is made a packed one)."""
+    if t is None:
+        return None
+    n, h, d = t.shape
+    row, head, one = t.stride()
+    if one != 1:
+        raise ValueError("the head width must be the contiguous axis")
+    if h == 1:
+        head = d
+    if n == 1:
+        row = h * head
+    return lola_rows(t.data_ptr(), row, head)
+
+
+def _paged(k_pool, v_pool, kv_len, table):
+    return lola_paged_kv(k_pool.data_ptr(), v_pool.data_ptr(), k_pool.shape[0], k_pool.shape[2], kv_len.shape[0],
+                         table.shape[1], max(table.stride(0), table.shape[1]), table.data_ptr(), kv_len.data_ptr())
+
+
+def lola_attn_prefill(cfg: lola_attn_config, Q, K, V, O, cu_q, cu_k=None, lse=None, stream=None) -> None:
+    """Q, O: [total_q, Hq, d]; K, V: [total_k, Hkv, d]; cu_q, cu_k: int32 [n_seq + 1] on the device."""
+    _check(_lib.lola_attn_prefill(ctypes.byref(cfg), cu_q.shape[0] - 1, Q.shape[0], K.shape[0], _ptr(cu_q), _ptr(cu_k),
+                                  _rows(Q), _rows(K), _rows(V), _rows(O), _ptr(lse), _stream(stream)),
+           "lola_attn_prefill")
+
+
+def lola_paged_slot(cfg: lola_attn_config, kv: lola_paged_kv, seq: int, head: int, pos: int) -> int:
+    """Element offset of a token's row in the pools, or -1 (``kv`` with host pointers)."""
+    return _lib.lola_paged_slot(ctypes.byref(cfg), ctypes.byref(kv), seq, head, pos)
+
+
+def lola_paged_append(cfg: lola_attn_config, kv: lola_paged_kv, K, V, cu_new=None, Q=None, QO=None, inv_freq=None,
+                      pairs=LOLA_PAIRS_HALVES, positions=None, stream=None) -> None:
+    """K, V: [n, Hkv, d]; Q, QO: [n, Hq, d]; inv_freq: float32 [rot / 2]."""
+    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
+    _check(_lib.lola_paged_append(ctypes.byref(cfg), ctypes.byref(kv), K.shape[0], _ptr(cu_new), _rows(K), _rows(V),
+                                  _rows(Q), _rows(QO), _ptr(inv_freq), rot, pairs, _ptr(positions), _stream(stream)),
+           "lola_paged_append")
+
+
+def lola_paged_decode_workspace_bytes(cfg: lola_attn_config) -> int:
+    b = _lib.lola_paged_decode_workspace_bytes(ctypes.byref(cfg))
+    if b < 0:
+        raise LolaError(int(b), "lola_paged_decode_workspace_bytes")
+    return int(b)
+
+
+def lola_paged_decode(cfg: lola_attn_config, kv: lola_paged_kv, Q, O, workspace, lse=None, stream=None) -> None:
+    """Q, O: [n_seq, Hq, d]; lse: float32 [n_seq, Hq]."""
+    _check(_lib.lola_paged_decode(ctypes.byref(cfg), ctypes.byref(kv), _rows(Q), _rows(O), _ptr(lse), _ptr(workspace),
+                                  workspace.numel() * workspace.element_size(), _stream(stream)), "lola_paged_decode")
+
+
+def lola_attn_status(stream=None):
+    """Synchronises the stream; (status, LOLA_ATTN_* bits of the device since the last call)."""
+    bits = ctypes.c_int32(0)
+    st = _lib.lola_attn_status(ctypes.byref(bits), _stream(stream))
+    return st, bits.value
+
+
+# ---------------------------------------------------------------------------------------
 # Convenience: buffers allocated through torch, then the C ABI
 # ---------------------------------------------------------------------------------------
+
+class ExactAttention:
+    """One layer's exact softmax attention: packed prompts, and single tokens over a paged cache.
+
+    ``k_pool``, ``v_pool``: [n_pages, Hkv, page, d] (``allocate`` makes them); a layer that only
+    runs ``prefill`` needs none.  Outputs and the decode step's workspace are allocated through
+    torch on the current stream, so calls on several streams do not share any."""
+
+    __slots__ = ("cfg", "Hq", "Hkv", "d", "dtype", "k_pool", "v_pool", "_ws")
+
+    def __init__(self, Hq, Hkv, d, dtype=torch.bfloat16, k_pool=None, v_pool=None, scale=None):
+        self.cfg = make_attn_config(Hq, Hkv, d, dtype, scale)
+        self._ws = lola_paged_decode_workspace_bytes(self.cfg)     # (checks the config)
+        self.Hq, self.Hkv, self.d, self.dtype = Hq, Hkv, d, dtype
+        if (k_pool is None) != (v_pool is None):
+            raise ValueError("k_pool and v_pool come together")
+        if k_pool is not None:
+            for t in (k_pool, v_pool):
+                if t.dim() != 4 or t.shape[1] != Hkv or t.shape[3] != d or t.dtype != dtype or not t.is_contiguous():
+                    raise ValueError("pools are contiguous [n_pages, Hkv, page, d] of the layer's dtype")
+            if k_pool.shape != v_pool.shape or k_pool.device != v_pool.device:
+                raise ValueError("k_pool and v_pool differ in shape or device")
+        self.k_pool, self.v_pool = k_pool, v_pool
+
+    @classmethod
+    def allocate(cls, Hq, Hkv, d, n_pages, page=64, dtype=torch.bfloat16, device="cuda", scale=None):
+        pool = lambda: torch.zeros(n_pages, Hkv, page, d, dtype=dtype, device=device)  # noqa: E731
+        return cls(Hq, Hkv, d, dtype, pool(), pool(), scale)
+
+    def _heads(self, t, heads, n, dev, what):
+        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.d or t.dtype != self.dtype or t.device != dev:
+            raise ValueError(f"{what}: want [n, {heads}, {self.d}] {self.dtype} on {dev}")
+        if n is not None and t.shape[0] != n:
+            raise ValueError(f"{what}: want {n} rows, got {t.shape[0]}")
+
+    @staticmethod
+    def _ints(t, shape, dev, what, dtype=torch.int32):
+        if t.dtype != dtype or t.device != dev or t.dim() != len(shape) or (t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1) \
+                or any(want is not None and got != want for got, want in zip(t.shape, shape)):
+            raise ValueError(f"{what}: want {dtype} {list(shape)} on {dev}, innermost axis contiguous")
+
+    @staticmethod
+    def _empty(shape, dtype, dev, stream):
+        """torch.empty on the call's stream, so that torch reuses the memory in its order."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=dev)
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream):
+            return torch.empty(shape, dtype=dtype, device=dev)
+
+    @staticmethod
+    def _current(dev):
+        if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+            raise ValueError(f"tensors are on {dev}, not on the current CUDA device")
+
+    def prefill(self, q, k, v, cu_q, cu_k=None, out=None, lse=None, stream=None):
+        """Causal attention over packed prompts: q [total_q, Hq, d], k, v [total_k, Hkv, d] (any row
+        and head strides), cu_q, cu_k int32 [n_seq + 1].  Returns out [total_q, Hq, d]; ``lse``
+        float32 [Hq, total_q] receives the log normalisers.  A fresh ``out`` is not initialised
+        outside the sequences."""
+        dev = q.device
+        self._heads(q, self.Hq, None, dev, "q")
+        self._heads(k, self.Hkv, None, dev, "k")
+        self._heads(v, self.Hkv, k.shape[0], dev, "v")
+        self._ints(cu_q, (None,), dev, "cu_q")
+        if cu_k is not None:
+            self._ints(cu_k, (cu_q.shape[0],), dev, "cu_k")
+        if out is None:
+            out = self._empty((q.shape[0], self.Hq, self.d), self.dtype, dev, stream)
+        else:
+            self._heads(out, self.Hq, q.shape[0], dev, "out")
+        if lse is not None:
+            self._ints(lse, (self.Hq, q.shape[0]), dev, "lse", torch.float32)
+            if not lse.is_contiguous():
+                raise ValueError("lse must be contiguous")
+        self._current(dev)
+        lola_attn_prefill(self.cfg, q, k, v, out, cu_q, cu_k, lse, stream)
+        return out
+
+    def _cache(self, kv_len, table):
+        if self.k_pool is None:
+            raise ValueError("this layer has no key-value pools")
+        dev = self.k_pool.device
+        self._ints(kv_len, (None,), dev, "kv_len")
+        self._ints(table, (kv_len.shape[0], None), dev, "table")
+        self._current(dev)
+        return _paged(self.k_pool, self.v_pool, kv_len, table)
+
+    def append(self, k, v, kv_len, table, cu_new=None, q=None, inv_freq=None, q_out=None, pairs="halves",
+               positions=None, stream=None):
+        """Appends k, v [n, Hkv, d] to the cache and returns the rotated q (None without q).
+
+        ``kv_len`` int32 [n_seq] counts the new tokens in; ``table`` int32 [n_seq, width]; ``cu_new``
+        int32 [n_seq + 1] the rows of each sequence's new tokens (None: one each); ``inv_freq``
+        float32 [rot / 2] radians per position (None: no rotation); ``pairs`` the channel pairs of
+        the rotation, "halves" or "neighbours"; ``positions`` int32 [n] in place of the tokens'
+        indexes.  ``q_out`` may be q itself."""
+        kv = self._cache(kv_len, table)
+        dev, n = k.device, k.shape[0]
+        if dev != self.k_pool.device:
+            raise ValueError("k is not on the pools' device")
+        self._heads(k, self.Hkv, None, dev, "k")
+        self._heads(v, self.Hkv, n, dev, "v")
+        if cu_new is not None:
+            self._ints(cu_new, (kv_len.shape[0] + 1,), dev, "cu_new")
+        if inv_freq is not None:
+            self._ints(inv_freq, (None,), dev, "inv_freq", torch.float32)
+        if positions is not None:
+            self._ints(positions, (n,), dev, "positions")
+        if q is not None:
+            self._heads(q, self.Hq, n, dev, "q")
+            if q_out is None:
+                q_out = self._empty((n, self.Hq, self.d), self.dtype, dev, stream)
+            else:
+                self._heads(q_out, self.Hq, n, dev, "q_out")
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        lola_paged_append(self.cfg, kv, k, v, cu_new, q, q_out, inv_freq, PAIRS[pairs], positions, stream)
+        return q_out
+
+    def decode_step(self, q, kv_len, table, out=None, lse=None, workspace=None, stream=None):
+        """One query token per sequence, q [n_seq, Hq, d], over its kv_len cached tokens; returns out
+        [n_seq, Hq, d].  ``lse`` float32 [n_seq, Hq].  ``workspace``: a buffer of
+        lola_paged_decode_workspace_bytes; by default one is allocated for the call."""
+        kv = self._cache(kv_len, table)
+        dev, n = self.k_pool.device, kv_len.shape[0]
+        self._heads(q, self.Hq, n, dev, "q")
+        if out is None:
+            out = self._empty((n, self.Hq, self.d), self.dtype, dev, stream)
+        else:
+            self._heads(out, self.Hq, n, dev, "out")
+        if lse is not None:
+            self._ints(lse, (n, self.Hq), dev, "lse", torch.float32)
+            if not lse.is_contiguous():
+                raise ValueError("lse must be contiguous")
+        if workspace is None:
+            workspace = self._empty(self._ws, torch.uint8, dev, stream)
+        lola_paged_decode(self.cfg, kv, q, out, workspace, lse, stream)
+        return out
+
 
 class Lola:
     """One layer's LoLA memory for B x Hh heads: owns the state and the prefill workspace."""

@@ -1,0 +1,165 @@
+// Shared by the exact-attention kernels: argument blocks, the packed sequences' and the paged
+// cache's index arithmetic, and the launchers.
+#pragma once
+
+#include "lola_internal.cuh"
+
+namespace lola {
+
+constexpr float kAttnLog2e = 1.4426950408889634f;
+constexpr float kAttnLn2 = 0.6931471805599453f;
+
+struct Rows {
+    char* data;
+    int64_t row, head;   // elements
+};
+
+// one lola_attn_prefill
+struct AttnArgs {
+    int n_seq, total_q, total_k, Hq, G, dtype, d;
+    const int32_t* cu_q;
+    const int32_t* cu_k;
+    Rows Q, K, V, O;
+    float* lse;          // [Hq][total_q] or null
+    float scale_log2;    // c log2(e): scores are kept in log2 units
+};
+
+// a paged cache and one decode step over it
+struct PagedArgs {
+    char* K;
+    char* V;
+    int n_pages, page, page_log2, n_seq, width;
+    int64_t table_stride;
+    const int32_t* table;
+    const int32_t* kv_len;
+    int Hq, Hkv, G, d, dtype;
+};
+
+// ---- packed sequences ----
+// Rows [begin, begin + len) of sequence b; malformed offsets make it empty (*bad set).
+__host__ __device__ inline void seq_rows(const int32_t* cu, int b, int total, int* begin, int* len, bool* bad) {
+    const int lo = cu[b], hi = cu[b + 1];
+    if (lo < 0 || hi < lo || hi > total) {
+        *bad = true;
+        *begin = 0;
+        *len = 0;
+        return;
+    }
+    *begin = lo;
+    *len = hi - lo;
+}
+
+// ---- the paged cache ----
+__host__ __device__ inline int64_t paged_tokens(const PagedArgs& p, int len) {
+    const int64_t most = (int64_t)p.width << p.page_log2;
+    return len <= 0 ? 0 : (len > most ? most : len);
+}
+// the page of token pos of sequence b (pos < width * page), or -1 where it is not in the pool
+__host__ __device__ inline int paged_page(const PagedArgs& p, int b, int64_t pos) {
+    const int e = p.table[(int64_t)b * p.table_stride + (pos >> p.page_log2)];
+    return e >= 0 && e < p.n_pages ? e : -1;
+}
+__host__ __device__ inline int64_t paged_offset(const PagedArgs& p, int page, int head, int64_t pos) {
+    return (((int64_t)page * p.Hkv + head) * p.page + (pos & (p.page - 1))) * p.d;
+}
+
+// Piece c of n equal pieces of `total` units: [split_at(c), split_at(c + 1))
+__host__ __device__ inline int64_t split_at(int64_t total, int n, int c) { return total * c / n; }
+// the piece that holds unit u < total
+__host__ __device__ inline int split_of(int64_t total, int n, int64_t u) {
+    int c = (int)(u * n / total);
+    while (c + 1 < n && split_at(total, n, c + 1) <= u) ++c;
+    while (c > 0 && split_at(total, n, c) > u) --c;
+    return c;
+}
+
+// ---- block-wide sums over sequences (NT threads, all of them) ----
+template <int NT>
+__device__ __forceinline__ int64_t block_total(int64_t x, int64_t* sm) {
+    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    __syncthreads();
+    if (lane == 0) sm[warp] = x;
+    __syncthreads();
+    int64_t t = 0;
+#pragma unroll
+    for (int w = 0; w < NT / kWarp; ++w) t += sm[w];
+    return t;
+}
+// sum of count(b) over all sequences
+template <int NT, typename F>
+__device__ __forceinline__ int64_t seq_total(int n_seq, F&& count, int64_t* sm) {
+    int64_t x = 0;
+    for (int b = threadIdx.x; b < n_seq; b += NT) x += count(b);
+    return block_total<NT>(x, sm);
+}
+// the sequence b that holds unit `u` (0 <= u < the total) of the units counted in order, and its
+// unit number inside b
+template <int NT, typename F>
+__device__ __forceinline__ void seq_find(int n_seq, F&& count, int64_t u, int64_t* sm, int* b_out, int64_t* rem_out) {
+    __shared__ int found_b;
+    __shared__ int64_t found_r;
+    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+    int64_t before = 0;
+    for (int base = 0; base < n_seq; base += NT) {
+        const int b = base + (int)threadIdx.x;
+        const int64_t own = b < n_seq ? count(b) : 0;
+        int64_t inc = own;
+#pragma unroll
+        for (int o = 1; o < kWarp; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        __syncthreads();
+        if (lane == kWarp - 1) sm[warp] = inc;
+        __syncthreads();
+        int64_t pre = before, all = before;
+#pragma unroll
+        for (int w = 0; w < NT / kWarp; ++w) {
+            if (w < warp) pre += sm[w];
+            all += sm[w];
+        }
+        const int64_t lo = pre + inc - own;
+        if (u >= lo && u < lo + own) {
+            found_b = b;
+            found_r = u - lo;
+        }
+        if (u < all) break;
+        before = all;
+    }
+    __syncthreads();
+    *b_out = found_b;
+    *rem_out = found_r;
+}
+
+// ---- launchers ----
+cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t st);
+struct AppendArgs {
+    PagedArgs p;
+    int n_tokens, rot, pairs;
+    const int32_t* cu_new;
+    Rows K, V, Q, QO;        // Q.data null: keys and values only
+    const float* inv_freq;
+    const int32_t* positions;
+};
+cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t st);
+int64_t paged_decode_workspace(int Hq, int Hkv, int d);
+struct DecodeArgs {
+    PagedArgs p;
+    Rows Q, O;
+    float* lse;
+    float* part;             // workspace
+    float scale_log2;
+};
+// traced as two kernels by the caller: the pieces, then their join (a no-op where nothing is split)
+cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t st);
+cudaError_t launch_paged_join(const DecodeArgs& a, cudaStream_t st);
+// whether some sequence may span more than one piece
+bool paged_decode_splits(const DecodeArgs& a);
+// reads and clears the anomaly words of a translation unit (after the stream's work)
+cudaError_t attn_status_take(int32_t* bits, cudaStream_t st);
+cudaError_t append_status_take(int32_t* bits, cudaStream_t st);
+cudaError_t paged_status_take(int32_t* bits, cudaStream_t st);
+
+}  // namespace lola

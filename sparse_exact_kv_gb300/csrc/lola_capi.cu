@@ -1,10 +1,12 @@
 // Host side of the C ABI declared in include/lola.h: argument validation, the state and
 // workspace layouts, and the stream-ordered sequence of kernels of each call.
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
 #include <vector>
 
+#include "lola_attn.cuh"
 #include "lola_internal.cuh"
 #include "lola_tc.cuh"
 
@@ -268,6 +270,69 @@ HolaWs hola_carve(const HolaDims& d, int n, void* base) {
 }
 }  // namespace
 
+// ---- exact attention: argument checks ----
+namespace {
+int32_t attn_check(const lola_attn_config* c) {
+    if (!c) return LOLA_ERR_INVALID_ARG;
+    if (c->Hq < 1 || c->Hkv < 1 || c->Hq % c->Hkv != 0 || c->d < 1 || (c->dtype != LOLA_F32 && c->dtype != LOLA_BF16))
+        return LOLA_ERR_INVALID_ARG;
+    if (!(c->scale >= 0.f) || !std::isfinite(c->scale)) return LOLA_ERR_INVALID_ARG;
+    if ((c->d != 64 && c->d != 128) || c->Hq > (1 << 20)) return LOLA_ERR_UNSUPPORTED;
+    return LOLA_OK;
+}
+float attn_scale_log2(const lola_attn_config* c) {
+    return (c->scale > 0.f ? c->scale : 1.f / std::sqrt((float)c->d)) * kAttnLog2e;
+}
+// rows of `heads` heads: aligned, strides positive multiples of 16 bytes; an output's rows must
+// not overlap
+bool rows_ok(const lola_attn_config* c, const lola_rows* r, int64_t rows, int64_t heads, bool out) {
+    const int64_t unit = c->dtype == LOLA_BF16 ? 8 : 4;
+    if (!r || !r->data || !aligned16(r->data)) return false;
+    if (r->row < 1 || r->head < 1 || r->row % unit != 0 || r->head % unit != 0) return false;
+    // strides that no memory holds (and whose offsets might pass 64 bits)
+    const int64_t most = (int64_t)1 << 40;
+    if (r->row > most || r->head > most || (double)(rows - 1) * r->row + (double)(heads - 1) * r->head > most) return false;
+    if (!out) return true;
+    const bool by_row = r->head >= c->d && r->row >= heads * r->head;
+    const bool by_head = r->row >= c->d && r->head >= rows * r->row;
+    return by_row || by_head;
+}
+Rows to_rows(const lola_rows* r) { return r ? Rows{static_cast<char*>(r->data), r->row, r->head} : Rows{nullptr, 0, 0}; }
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+int32_t paged_check(const lola_attn_config* c, const lola_paged_kv* kv, PagedArgs* p) {
+    const int32_t s = attn_check(c);
+    if (s != LOLA_OK) return s;
+    if (!kv || !kv->K || !kv->V || !kv->table || !kv->kv_len || !aligned16(kv->K) || !aligned16(kv->V) ||
+        !aligned4(kv->table) || !aligned4(kv->kv_len))
+        return LOLA_ERR_INVALID_ARG;
+    if (kv->n_pages < 1 || kv->n_seq < 1 || kv->width < 1 || kv->table_stride < kv->width) return LOLA_ERR_INVALID_ARG;
+    int log2 = 0;
+    while (log2 < 8 && (1 << log2) < kv->page) ++log2;
+    if (kv->page < 1) return LOLA_ERR_INVALID_ARG;
+    if (kv->page < 16 || (1 << log2) != kv->page) return LOLA_ERR_UNSUPPORTED;
+    // tensor-map coordinates and token indexes are 32-bit
+    if ((int64_t)kv->n_pages * c->Hkv > 0x7fffffff || (int64_t)kv->width * kv->page > 0x7fffffff) return LOLA_ERR_UNSUPPORTED;
+    p->K = static_cast<char*>(kv->K);
+    p->V = static_cast<char*>(kv->V);
+    p->n_pages = kv->n_pages;
+    p->page = kv->page;
+    p->page_log2 = log2;
+    p->n_seq = kv->n_seq;
+    p->width = kv->width;
+    p->table_stride = kv->table_stride;
+    p->table = kv->table;
+    p->kv_len = kv->kv_len;
+    p->Hq = c->Hq;
+    p->Hkv = c->Hkv;
+    p->G = c->Hq / c->Hkv;
+    p->d = c->d;
+    p->dtype = c->dtype;
+    return LOLA_OK;
+}
+}  // namespace
+
 }  // namespace lola
 
 using namespace lola;
@@ -481,7 +546,8 @@ int32_t lola_kernel_time(int32_t id, double* total_ms, int64_t* launches) {
 
 const char* lola_kernel_name(int32_t id) {
     static const char* names[LOLA_KERNEL_COUNT] = {"state_init", "phi",        "select",     "output",     "decode",
-                                                        "phi_q",      "hola_prep",  "hola_state", "hola_cache", "hola_read"};
+                                                        "phi_q",      "hola_prep",  "hola_state", "hola_cache", "hola_read",
+                                                        "attn",       "append",     "paged",      "paged_join"};
     return (id >= 0 && id < LOLA_KERNEL_COUNT) ? names[id] : "";
 }
 
@@ -591,6 +657,126 @@ int32_t lola_hola_status(const lola_hola_config* cfg, int32_t n, const void* wor
         bad |= words[4 * (size_t)i + HDR_STATUS];
     }
     return bad ? LOLA_ERR_DEVICE : LOLA_OK;
+}
+
+int32_t lola_attn_prefill(const lola_attn_config* cfg, int32_t n_seq, int32_t total_q, int32_t total_k,
+                          const int32_t* cu_q, const int32_t* cu_k, const lola_rows* Q, const lola_rows* K,
+                          const lola_rows* V, const lola_rows* O, float* lse, void* stream) {
+    const int32_t s = attn_check(cfg);
+    if (s != LOLA_OK) return s;
+    if (n_seq < 1 || total_q < 0 || total_k < 0 || !cu_q || !aligned4(cu_q) || !aligned4(cu_k) || !aligned4(lse))
+        return LOLA_ERR_INVALID_ARG;
+    if (!cu_k && total_k != total_q) return LOLA_ERR_INVALID_ARG;
+    if (total_q == 0) return LOLA_OK;
+    if (!rows_ok(cfg, Q, total_q, cfg->Hq, false) || !rows_ok(cfg, O, total_q, cfg->Hq, true)) return LOLA_ERR_INVALID_ARG;
+    if (total_k > 0 && (!rows_ok(cfg, K, total_k, cfg->Hkv, false) || !rows_ok(cfg, V, total_k, cfg->Hkv, false)))
+        return LOLA_ERR_INVALID_ARG;
+    if (((int64_t)total_q + 64ll * n_seq) * cfg->Hq / 64 > 0x40000000) return LOLA_ERR_UNSUPPORTED;   // the grid
+    AttnArgs a;
+    a.n_seq = n_seq;
+    a.total_q = total_q;
+    a.total_k = total_k;
+    a.Hq = cfg->Hq;
+    a.G = cfg->Hq / cfg->Hkv;
+    a.dtype = cfg->dtype;
+    a.d = cfg->d;
+    a.cu_q = cu_q;
+    a.cu_k = cu_k ? cu_k : cu_q;
+    a.Q = to_rows(Q);
+    a.O = to_rows(O);
+    a.K = total_k > 0 ? to_rows(K) : a.Q;      // (no key is read when there is none)
+    a.V = total_k > 0 ? to_rows(V) : a.Q;
+    a.lse = lse;
+    a.scale_log2 = attn_scale_log2(cfg);
+    cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = traced(LOLA_KERNEL_ATTN, st, [&]() { return launch_attn_prefill(a, st); });
+    return e == cudaSuccess ? LOLA_OK : cuda_fail(e, "prompt attention");
+}
+
+int64_t lola_paged_slot(const lola_attn_config* cfg, const lola_paged_kv* kv, int32_t seq, int32_t head, int64_t pos) {
+    PagedArgs p;
+    if (paged_check(cfg, kv, &p) != LOLA_OK || seq < 0 || seq >= p.n_seq || head < 0 || head >= p.Hkv) return -1;
+    if (pos < 0 || pos >= paged_tokens(p, p.kv_len[seq])) return -1;
+    const int page = paged_page(p, seq, pos);
+    return page < 0 ? -1 : paged_offset(p, page, head, pos);
+}
+
+int32_t lola_paged_append(const lola_attn_config* cfg, const lola_paged_kv* kv, int32_t n_tokens,
+                          const int32_t* cu_new, const lola_rows* K, const lola_rows* V, const lola_rows* Q,
+                          const lola_rows* QO, const float* inv_freq, int32_t rot, int32_t pairs,
+                          const int32_t* positions, void* stream) {
+    AppendArgs a;
+    const int32_t s = paged_check(cfg, kv, &a.p);
+    if (s != LOLA_OK) return s;
+    if (n_tokens < 0 || !aligned4(cu_new) || !aligned4(inv_freq) || !aligned4(positions)) return LOLA_ERR_INVALID_ARG;
+    if (!cu_new && n_tokens != kv->n_seq) return LOLA_ERR_INVALID_ARG;
+    if (!Q != !QO || (Q && !inv_freq)) return LOLA_ERR_INVALID_ARG;
+    if (inv_freq && (rot < 1 || rot > cfg->d || (pairs != LOLA_PAIRS_HALVES && pairs != LOLA_PAIRS_NEIGHBOURS)))
+        return LOLA_ERR_INVALID_ARG;
+    if (inv_freq && rot % 16 != 0) return LOLA_ERR_UNSUPPORTED;
+    if (n_tokens == 0) return LOLA_OK;
+    if (!rows_ok(cfg, K, n_tokens, cfg->Hkv, false) || !rows_ok(cfg, V, n_tokens, cfg->Hkv, false))
+        return LOLA_ERR_INVALID_ARG;
+    if (Q) {
+        if (!rows_ok(cfg, Q, n_tokens, cfg->Hq, false) || !rows_ok(cfg, QO, n_tokens, cfg->Hq, true))
+            return LOLA_ERR_INVALID_ARG;
+        // in place: the same rows
+        if (Q->data == QO->data && (Q->row != QO->row || Q->head != QO->head)) return LOLA_ERR_INVALID_ARG;
+    }
+    a.n_tokens = n_tokens;
+    a.rot = rot;
+    a.pairs = pairs;
+    a.cu_new = cu_new;
+    a.K = to_rows(K);
+    a.V = to_rows(V);
+    a.Q = to_rows(Q);
+    a.QO = to_rows(QO);
+    a.inv_freq = inv_freq;
+    a.positions = positions;
+    cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = traced(LOLA_KERNEL_APPEND, st, [&]() { return launch_paged_append(a, st); });
+    return e == cudaSuccess ? LOLA_OK : cuda_fail(e, "paged append");
+}
+
+int64_t lola_paged_decode_workspace_bytes(const lola_attn_config* cfg) {
+    const int32_t s = attn_check(cfg);
+    return s == LOLA_OK ? paged_decode_workspace(cfg->Hq, cfg->Hkv, cfg->d) : s;
+}
+
+int32_t lola_paged_decode(const lola_attn_config* cfg, const lola_paged_kv* kv, const lola_rows* Q,
+                          const lola_rows* O, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    DecodeArgs a;
+    const int32_t s = paged_check(cfg, kv, &a.p);
+    if (s != LOLA_OK) return s;
+    if (!rows_ok(cfg, Q, kv->n_seq, cfg->Hq, false) || !rows_ok(cfg, O, kv->n_seq, cfg->Hq, true) || !aligned4(lse))
+        return LOLA_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace)) return LOLA_ERR_INVALID_ARG;
+    if ((int64_t)workspace_bytes < paged_decode_workspace(cfg->Hq, cfg->Hkv, cfg->d)) return LOLA_ERR_WORKSPACE;
+    a.Q = to_rows(Q);
+    a.O = to_rows(O);
+    a.lse = lse;
+    a.part = static_cast<float*>(workspace);
+    a.scale_log2 = attn_scale_log2(cfg);
+    cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e = traced(LOLA_KERNEL_PAGED, st, [&]() { return launch_paged_decode(a, st); });
+    if (e == cudaSuccess && paged_decode_splits(a))
+        e = traced(LOLA_KERNEL_PAGED_JOIN, st, [&]() { return launch_paged_join(a, st); });
+    return e == cudaSuccess ? LOLA_OK : cuda_fail(e, "paged decode");
+}
+
+int32_t lola_attn_status(int32_t* host_bits, void* stream) {
+    cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e = cudaStreamSynchronize(st);
+    int32_t bits = 0;
+    cudaError_t (*const take[])(int32_t*, cudaStream_t) = {attn_status_take, append_status_take, paged_status_take};
+    for (auto f : take) {
+        int32_t x = 0;
+        if (e == cudaSuccess) e = f(&x, st);
+        bits |= x;
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "lola_attn_status");
+    if (host_bits) *host_bits = bits;
+    return bits ? LOLA_ERR_DEVICE : LOLA_OK;
 }
 
 }  // extern "C"
