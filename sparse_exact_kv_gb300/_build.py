@@ -15,7 +15,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblola.so")
 SOURCES = ["lola_capi.cu", "lola_phi.cu", "lola_select.cu", "lola_chunk.cu", "lola_output.cu", "lola_output_tc.cu",
            "lola_decode.cu", "lola_noalloc.cu", "lola_relsre.cu",
-           "lola_fixed.cu", "lola_hola.cu", "lola_hola_tc.cu", "lola_attn.cu", "lola_append.cu", "lola_paged.cu"]
+           "lola_fixed.cu", "lola_hola.cu", "lola_hola_tc.cu", "lola_attn.cu",
+           "lola_attn_tc.cu", "lola_append.cu", "lola_paged.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -241,7 +241,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
 
 cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t st) {
     if (a.dtype == LOLA_F32) return a.d == 128 ? launch<float, 128>(a, st) : launch<float, 64>(a, st);
-    return a.d == 128 ? launch<__nv_bfloat16, 128>(a, st) : launch<__nv_bfloat16, 64>(a, st);
+    return launch_attn_tc(a, st);
 }
 
 cudaError_t attn_status_take(int32_t* bits, cudaStream_t st) {

@@ -135,6 +135,7 @@ __device__ __forceinline__ void seq_find(int n_seq, F&& count, int64_t u, int64_
 
 // ---- launchers ----
 cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t st);
+cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t st);       // bf16 (lola_attn_tc.cu)
 struct AppendArgs {
     PagedArgs p;
     int n_tokens, rot, pairs;
@@ -159,6 +160,7 @@ cudaError_t launch_paged_join(const DecodeArgs& a, cudaStream_t st);
 bool paged_decode_splits(const DecodeArgs& a);
 // reads and clears the anomaly words of a translation unit (after the stream's work)
 cudaError_t attn_status_take(int32_t* bits, cudaStream_t st);
+cudaError_t attn_tc_status_take(int32_t* bits, cudaStream_t st);
 cudaError_t append_status_take(int32_t* bits, cudaStream_t st);
 cudaError_t paged_status_take(int32_t* bits, cudaStream_t st);
 

@@ -768,7 +768,8 @@ int32_t lola_attn_status(int32_t* host_bits, void* stream) {
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e = cudaStreamSynchronize(st);
     int32_t bits = 0;
-    cudaError_t (*const take[])(int32_t*, cudaStream_t) = {attn_status_take, append_status_take, paged_status_take};
+    cudaError_t (*const take[])(int32_t*, cudaStream_t) = {attn_status_take, attn_tc_status_take, append_status_take,
+                                                        paged_status_take};
     for (auto f : take) {
         int32_t x = 0;
         if (e == cudaSuccess) e = f(&x, st);

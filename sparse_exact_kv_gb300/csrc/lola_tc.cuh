@@ -179,6 +179,10 @@ __device__ __forceinline__ void bulk_wait0() { asm volatile("cp.async.bulk.wait_
 // the runtime.  False when the driver call fails.
 bool make_tmap3(CUtensorMap* m, CUtensorMapDataType type, int elem_bytes, const void* base, int64_t inner,
                 int64_t rows, int64_t depth, int box_inner, int box_rows);
+// Host: a 3-D tensor map over bf16 [rows][heads][d] with row and head strides in elements, boxes of
+// box_rows rows x 1 head x 64 channels, 128-byte swizzle, rows past the tensor zero-filled.
+bool make_tmap_rows(CUtensorMap* m, const void* base, int64_t rows, int heads, int d, int64_t row, int64_t head,
+                    int box_rows);
 
 __device__ __forceinline__ void cp_async16(uint32_t dst_smem, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src) : "memory");
