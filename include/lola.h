@@ -263,8 +263,7 @@ typedef enum {
     LOLA_KERNEL_ATTN = 10,       /* exact attention over packed prompts */
     LOLA_KERNEL_APPEND = 11,     /* rotation and append to the paged cache */
     LOLA_KERNEL_PAGED = 12,      /* exact attention of one token over the paged cache */
-    LOLA_KERNEL_PAGED_JOIN = 13, /* ... joining the pieces of split sequences */
-    LOLA_KERNEL_COUNT = 14
+    LOLA_KERNEL_COUNT = 13
 } lola_kernel_id;
 
 /* enable != 0: clear the totals and start recording (process-wide); 0: stop recording. */
@@ -460,8 +459,8 @@ int64_t lola_paged_decode_workspace_bytes(const lola_attn_config* cfg);
  *   lse  nullable device float32 [n_seq, Hq]
  *   workspace  device, 16-byte aligned; its contents mean nothing before or after the call, and
  *        calls that may run at the same time need one each
- * The work is cut along the cache's length into equal pieces for the GPU's SMs, and a second
- * kernel joins the pieces of each sequence in order: the same inputs give the same bits.  A page
+ * The work is cut along the cache's length into equal pieces for the GPU's SMs, and the last
+ * piece of a sequence to be done joins them, in their order: the same inputs give the same bits.  A page
  * outside the cache sets LOLA_ATTN_BAD_PAGE and its tokens are not seen; a kv_len beyond
  * width * page sets it too and counts as width * page. */
 int32_t lola_paged_decode(const lola_attn_config* cfg, const lola_paged_kv* kv, const lola_rows* Q,

@@ -10,6 +10,7 @@ is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -53,7 +54,7 @@ EXPORTS = ("lola_version", "lola_status_string", "lola_last_cuda_error", "lola_c
 # size of the fixed scratch array behind lola_prefill_noalloc (include/lola.h)
 LOLA_NOALLOC_SCRATCH_BYTES = 32 << 20
 KERNELS = ("state_init", "phi", "select", "output", "decode", "phi_q", "hola_prep", "hola_state", "hola_cache",
-           "hola_read", "attn", "append", "paged", "paged_join")
+           "hola_read", "attn", "append", "paged")
 
 
 class lola_config(ctypes.Structure):
@@ -338,16 +339,35 @@ def _rows(t):
     return lola_rows(t.data_ptr(), row, head)
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream, index):
+    """The cudaStream_t of ``stream``; None: torch's current stream of device ``index`` (looked up
+    without making a Stream object, 3 us a call)."""
+    if stream is None:
+        return _raw_stream(index) if _raw_stream else torch.cuda.current_stream(index).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def _paged(k_pool, v_pool, kv_len, table):
-    return lola_paged_kv(k_pool.data_ptr(), v_pool.data_ptr(), k_pool.shape[0], k_pool.shape[2], kv_len.shape[0],
-                         table.shape[1], max(table.stride(0), table.shape[1]), table.data_ptr(), kv_len.data_ptr())
+    pages, _, page, _ = k_pool.shape
+    n, width = table.shape
+    stride = table.stride(0)
+    return lola_paged_kv(k_pool.data_ptr(), v_pool.data_ptr(), pages, page, n, width, stride if stride > width else width,
+                         table.data_ptr(), kv_len.data_ptr())
 
 
 def lola_attn_prefill(cfg: lola_attn_config, Q, K, V, O, cu_q, cu_k=None, lse=None, stream=None) -> None:
     """Q, O: [total_q, Hq, d]; K, V: [total_k, Hkv, d]; cu_q, cu_k: int32 [n_seq + 1] on the device."""
-    _check(_lib.lola_attn_prefill(ctypes.byref(cfg), cu_q.shape[0] - 1, Q.shape[0], K.shape[0], _ptr(cu_q), _ptr(cu_k),
-                                  _rows(Q), _rows(K), _rows(V), _rows(O), _ptr(lse), _stream(stream)),
-           "lola_attn_prefill")
+    st = _lib.lola_attn_prefill(cfg, cu_q.shape[0] - 1, Q.shape[0], K.shape[0], cu_q.data_ptr(), _addr(cu_k), _rows(Q),
+                                _rows(K), _rows(V), _rows(O), _addr(lse), _stream_of(stream, Q.get_device()))
+    if st:
+        raise LolaError(st, "lola_attn_prefill")
 
 
 def lola_paged_slot(cfg: lola_attn_config, kv: lola_paged_kv, seq: int, head: int, pos: int) -> int:
@@ -359,9 +379,10 @@ def lola_paged_append(cfg: lola_attn_config, kv: lola_paged_kv, K, V, cu_new=Non
                       pairs=LOLA_PAIRS_HALVES, positions=None, stream=None) -> None:
     """K, V: [n, Hkv, d]; Q, QO: [n, Hq, d]; inv_freq: float32 [rot / 2]."""
     rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
-    _check(_lib.lola_paged_append(ctypes.byref(cfg), ctypes.byref(kv), K.shape[0], _ptr(cu_new), _rows(K), _rows(V),
-                                  _rows(Q), _rows(QO), _ptr(inv_freq), rot, pairs, _ptr(positions), _stream(stream)),
-           "lola_paged_append")
+    st = _lib.lola_paged_append(cfg, kv, K.shape[0], _addr(cu_new), _rows(K), _rows(V), _rows(Q), _rows(QO),
+                                _addr(inv_freq), rot, pairs, _addr(positions), _stream_of(stream, K.get_device()))
+    if st:
+        raise LolaError(st, "lola_paged_append")
 
 
 def lola_paged_decode_workspace_bytes(cfg: lola_attn_config) -> int:
@@ -373,8 +394,10 @@ def lola_paged_decode_workspace_bytes(cfg: lola_attn_config) -> int:
 
 def lola_paged_decode(cfg: lola_attn_config, kv: lola_paged_kv, Q, O, workspace, lse=None, stream=None) -> None:
     """Q, O: [n_seq, Hq, d]; lse: float32 [n_seq, Hq]."""
-    _check(_lib.lola_paged_decode(ctypes.byref(cfg), ctypes.byref(kv), _rows(Q), _rows(O), _ptr(lse), _ptr(workspace),
-                                  workspace.numel() * workspace.element_size(), _stream(stream)), "lola_paged_decode")
+    st = _lib.lola_paged_decode(cfg, kv, _rows(Q), _rows(O), _addr(lse), workspace.data_ptr(), workspace.nbytes,
+                                _stream_of(stream, Q.get_device()))
+    if st:
+        raise LolaError(st, "lola_paged_decode")
 
 
 def lola_attn_status(stream=None):
@@ -388,27 +411,39 @@ def lola_attn_status(stream=None):
 # Convenience: buffers allocated through torch, then the C ABI
 # ---------------------------------------------------------------------------------------
 
+@functools.lru_cache(maxsize=256)
+def _attn_plan(Hq, Hkv, d, dtype, scale):
+    """The config of a kind of layer and the decode step's workspace bytes (checks the config)."""
+    cfg = make_attn_config(Hq, Hkv, d, dtype, scale)
+    return cfg, lola_paged_decode_workspace_bytes(cfg)
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
 class ExactAttention:
     """One layer's exact softmax attention: packed prompts, and single tokens over a paged cache.
 
     ``k_pool``, ``v_pool``: [n_pages, Hkv, page, d] (``allocate`` makes them); a layer that only
     runs ``prefill`` needs none.  Outputs and the decode step's workspace are allocated through
-    torch on the current stream, so calls on several streams do not share any."""
+    torch on the call's stream, so calls on several streams do not share any.  Shapes, types and
+    devices are checked here, strides and alignment by the library; all tensors are on the current
+    CUDA device."""
 
     __slots__ = ("cfg", "Hq", "Hkv", "d", "dtype", "k_pool", "v_pool", "_ws")
 
     def __init__(self, Hq, Hkv, d, dtype=torch.bfloat16, k_pool=None, v_pool=None, scale=None):
-        self.cfg = make_attn_config(Hq, Hkv, d, dtype, scale)
-        self._ws = lola_paged_decode_workspace_bytes(self.cfg)     # (checks the config)
+        self.cfg, self._ws = _attn_plan(Hq, Hkv, d, dtype, scale)
         self.Hq, self.Hkv, self.d, self.dtype = Hq, Hkv, d, dtype
-        if (k_pool is None) != (v_pool is None):
-            raise ValueError("k_pool and v_pool come together")
+        _need((k_pool is None) == (v_pool is None), "k_pool and v_pool come together")
         if k_pool is not None:
-            for t in (k_pool, v_pool):
-                if t.dim() != 4 or t.shape[1] != Hkv or t.shape[3] != d or t.dtype != dtype or not t.is_contiguous():
-                    raise ValueError("pools are contiguous [n_pages, Hkv, page, d] of the layer's dtype")
-            if k_pool.shape != v_pool.shape or k_pool.device != v_pool.device:
-                raise ValueError("k_pool and v_pool differ in shape or device")
+            shape = k_pool.shape
+            _need(len(shape) == 4 and shape[1] == Hkv and shape[3] == d and k_pool.dtype == dtype and k_pool.is_contiguous(),
+                  "pools are contiguous [n_pages, Hkv, page, d] of the layer's dtype")
+            _need(v_pool.shape == shape and v_pool.dtype == dtype and v_pool.is_contiguous()
+                  and v_pool.device == k_pool.device, "k_pool and v_pool differ in shape, type or device")
         self.k_pool, self.v_pool = k_pool, v_pool
 
     @classmethod
@@ -417,16 +452,23 @@ class ExactAttention:
         return cls(Hq, Hkv, d, dtype, pool(), pool(), scale)
 
     def _heads(self, t, heads, n, dev, what):
-        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.d or t.dtype != self.dtype or t.device != dev:
-            raise ValueError(f"{what}: want [n, {heads}, {self.d}] {self.dtype} on {dev}")
-        if n is not None and t.shape[0] != n:
-            raise ValueError(f"{what}: want {n} rows, got {t.shape[0]}")
+        """lola_rows of t, which has to be [n, heads, d] of the layer's type on ``dev``."""
+        if t.shape != (n, heads, self.d) or t.dtype != self.dtype or t.device != dev:
+            raise ValueError(f"{what}: want [{n}, {heads}, {self.d}] {self.dtype} on {dev}")
+        row, head, one = t.stride()
+        if one != 1 or n < 2 or heads < 2:
+            return _rows(t)
+        return lola_rows(t.data_ptr(), row, head)
 
     @staticmethod
-    def _ints(t, shape, dev, what, dtype=torch.int32):
-        if t.dtype != dtype or t.device != dev or t.dim() != len(shape) or (t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1) \
-                or any(want is not None and got != want for got, want in zip(t.shape, shape)):
-            raise ValueError(f"{what}: want {dtype} {list(shape)} on {dev}, innermost axis contiguous")
+    def _vector(t, n, dev, what, dtype=torch.int32):
+        if t.shape != (n,) or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{what}: want a contiguous {dtype} [{n}] on {dev}")
+
+    @staticmethod
+    def _lse(t, shape, dev):
+        if not (t.shape == shape and t.dtype == torch.float32 and t.device == dev and t.is_contiguous()):
+            raise ValueError(f"lse: want a contiguous float32 {list(shape)} on {dev}")
 
     @staticmethod
     def _empty(shape, dtype, dev, stream):
@@ -446,33 +488,39 @@ class ExactAttention:
         and head strides), cu_q, cu_k int32 [n_seq + 1].  Returns out [total_q, Hq, d]; ``lse``
         float32 [Hq, total_q] receives the log normalisers.  A fresh ``out`` is not initialised
         outside the sequences."""
-        dev = q.device
-        self._heads(q, self.Hq, None, dev, "q")
-        self._heads(k, self.Hkv, None, dev, "k")
-        self._heads(v, self.Hkv, k.shape[0], dev, "v")
-        self._ints(cu_q, (None,), dev, "cu_q")
+        dev, n, m, n1 = q.device, q.shape[0], k.shape[0], cu_q.shape[0]
+        rq = self._heads(q, self.Hq, n, dev, "q")
+        rk = self._heads(k, self.Hkv, m, dev, "k")
+        rv = self._heads(v, self.Hkv, m, dev, "v")
+        self._vector(cu_q, n1, dev, "cu_q")
         if cu_k is not None:
-            self._ints(cu_k, (cu_q.shape[0],), dev, "cu_k")
-        if out is None:
-            out = self._empty((q.shape[0], self.Hq, self.d), self.dtype, dev, stream)
-        else:
-            self._heads(out, self.Hq, q.shape[0], dev, "out")
+            self._vector(cu_k, n1, dev, "cu_k")
         if lse is not None:
-            self._ints(lse, (self.Hq, q.shape[0]), dev, "lse", torch.float32)
-            if not lse.is_contiguous():
-                raise ValueError("lse must be contiguous")
+            self._lse(lse, (self.Hq, n), dev)
+        if out is not None:
+            ro = self._heads(out, self.Hq, n, dev, "out")
         self._current(dev)
-        lola_attn_prefill(self.cfg, q, k, v, out, cu_q, cu_k, lse, stream)
+        if out is None:
+            out = self._empty((n, self.Hq, self.d), self.dtype, dev, stream)
+            ro = lola_rows(out.data_ptr(), self.Hq * self.d, self.d)
+        st = _lib.lola_attn_prefill(self.cfg, n1 - 1, n, m, cu_q.data_ptr(), _addr(cu_k), rq, rk, rv, ro, _addr(lse),
+                                    _stream_of(stream, dev.index))
+        if st:
+            raise LolaError(st, "lola_attn_prefill")
         return out
 
     def _cache(self, kv_len, table):
-        if self.k_pool is None:
+        pool = self.k_pool
+        if pool is None:
             raise ValueError("this layer has no key-value pools")
-        dev = self.k_pool.device
-        self._ints(kv_len, (None,), dev, "kv_len")
-        self._ints(table, (kv_len.shape[0], None), dev, "table")
+        dev, (n, width), (stride, one) = pool.device, table.shape, table.stride()
+        self._vector(kv_len, n, dev, "kv_len")
+        if table.dtype != torch.int32 or table.device != dev or (one != 1 and width != 1):
+            raise ValueError(f"table: want int32 [{n}, width] on {dev}, rows contiguous")
         self._current(dev)
-        return _paged(self.k_pool, self.v_pool, kv_len, table)
+        pages, _, page, _ = pool.shape
+        return lola_paged_kv(pool.data_ptr(), self.v_pool.data_ptr(), pages, page, n, width,
+                             stride if stride > width else width, table.data_ptr(), kv_len.data_ptr()), dev, n
 
     def append(self, k, v, kv_len, table, cu_new=None, q=None, inv_freq=None, q_out=None, pairs="halves",
                positions=None, stream=None):
@@ -483,47 +531,59 @@ class ExactAttention:
         float32 [rot / 2] radians per position (None: no rotation); ``pairs`` the channel pairs of
         the rotation, "halves" or "neighbours"; ``positions`` int32 [n] in place of the tokens'
         indexes.  ``q_out`` may be q itself."""
-        kv = self._cache(kv_len, table)
-        dev, n = k.device, k.shape[0]
-        if dev != self.k_pool.device:
-            raise ValueError("k is not on the pools' device")
-        self._heads(k, self.Hkv, None, dev, "k")
-        self._heads(v, self.Hkv, n, dev, "v")
+        kv, dev, n_seq = self._cache(kv_len, table)
+        n = k.shape[0]
+        rk = self._heads(k, self.Hkv, n, dev, "k")
+        rv = self._heads(v, self.Hkv, n, dev, "v")
+        rq = ro = freq = None
+        rot = 0
         if cu_new is not None:
-            self._ints(cu_new, (kv_len.shape[0] + 1,), dev, "cu_new")
+            self._vector(cu_new, n_seq + 1, dev, "cu_new")
         if inv_freq is not None:
-            self._ints(inv_freq, (None,), dev, "inv_freq", torch.float32)
+            rot = 2 * inv_freq.shape[0]
+            self._vector(inv_freq, rot // 2, dev, "inv_freq", torch.float32)
+            freq = inv_freq.data_ptr()
         if positions is not None:
-            self._ints(positions, (n,), dev, "positions")
+            self._vector(positions, n, dev, "positions")
         if q is not None:
-            self._heads(q, self.Hq, n, dev, "q")
-            if q_out is None:
-                q_out = self._empty((n, self.Hq, self.d), self.dtype, dev, stream)
+            rq = self._heads(q, self.Hq, n, dev, "q")
+            if q_out is not None:
+                ro = self._heads(q_out, self.Hq, n, dev, "q_out")
             else:
-                self._heads(q_out, self.Hq, n, dev, "q_out")
+                q_out = self._empty((n, self.Hq, self.d), self.dtype, dev, stream)
+                ro = lola_rows(q_out.data_ptr(), self.Hq * self.d, self.d)
         elif q_out is not None:
             raise ValueError("q_out without q")
-        lola_paged_append(self.cfg, kv, k, v, cu_new, q, q_out, inv_freq, PAIRS[pairs], positions, stream)
+        st = _lib.lola_paged_append(self.cfg, kv, n, _addr(cu_new), rk, rv, rq, ro, freq, rot, PAIRS[pairs],
+                                    _addr(positions), _stream_of(stream, dev.index))
+        if st:
+            raise LolaError(st, "lola_paged_append")
         return q_out
 
     def decode_step(self, q, kv_len, table, out=None, lse=None, workspace=None, stream=None):
         """One query token per sequence, q [n_seq, Hq, d], over its kv_len cached tokens; returns out
         [n_seq, Hq, d].  ``lse`` float32 [n_seq, Hq].  ``workspace``: a buffer of
         lola_paged_decode_workspace_bytes; by default one is allocated for the call."""
-        kv = self._cache(kv_len, table)
-        dev, n = self.k_pool.device, kv_len.shape[0]
-        self._heads(q, self.Hq, n, dev, "q")
-        if out is None:
-            out = self._empty((n, self.Hq, self.d), self.dtype, dev, stream)
-        else:
-            self._heads(out, self.Hq, n, dev, "out")
+        kv, dev, n = self._cache(kv_len, table)
+        rq = self._heads(q, self.Hq, n, dev, "q")
         if lse is not None:
-            self._ints(lse, (n, self.Hq), dev, "lse", torch.float32)
-            if not lse.is_contiguous():
-                raise ValueError("lse must be contiguous")
+            self._lse(lse, (n, self.Hq), dev)
+        if out is not None:
+            ro = self._heads(out, self.Hq, n, dev, "out")
+        else:
+            out = self._empty((n, self.Hq, self.d), self.dtype, dev, stream)
+            ro = lola_rows(out.data_ptr(), self.Hq * self.d, self.d)
+        size = self._ws
         if workspace is None:
-            workspace = self._empty(self._ws, torch.uint8, dev, stream)
-        lola_paged_decode(self.cfg, kv, q, out, workspace, lse, stream)
+            workspace = self._empty(size, torch.uint8, dev, stream)
+        else:
+            size = workspace.nbytes
+            if workspace.device != dev or not workspace.is_contiguous():
+                raise ValueError(f"workspace: want a contiguous buffer on {dev}")
+        st = _lib.lola_paged_decode(self.cfg, kv, rq, ro, _addr(lse), workspace.data_ptr(), size,
+                                    _stream_of(stream, dev.index))
+        if st:
+            raise LolaError(st, "lola_paged_decode")
         return out
 
 

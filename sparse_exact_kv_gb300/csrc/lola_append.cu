@@ -181,13 +181,6 @@ cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t st) {
     return a.p.d == 128 ? launch<__nv_bfloat16, 128>(a, st) : launch<__nv_bfloat16, 64>(a, st);
 }
 
-cudaError_t append_status_take(int32_t* bits, cudaStream_t st) {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(bits, g_status, sizeof(int32_t), 0, cudaMemcpyDeviceToHost, st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e != cudaSuccess || *bits == 0) return e;
-    const int32_t zero = 0;
-    e = cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st);
-    return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
-}
+cudaError_t append_status_take(int32_t* bits, cudaStream_t st) { return take_word(g_status, bits, st); }
 
 }  // namespace lola

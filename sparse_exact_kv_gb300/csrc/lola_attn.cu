@@ -229,7 +229,8 @@ __global__ void __launch_bounds__(kNT, 2) attn_prefill_kernel(const AttnArgs a) 
 template <typename T, int D>
 cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
     const size_t smem = sizeof(float) * (2 * D * kLd + kT * D + kT * kLd);
-    cudaError_t e = cudaFuncSetAttribute(attn_prefill_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = opt_in_smem(attn_prefill_kernel<T, D>, (int)smem, done);
     if (e != cudaSuccess) return e;
     // at most this many tiles for any cut of total_q rows into n_seq sequences
     const int64_t tiles = ((int64_t)a.total_q + (int64_t)a.n_seq * (kT - 1)) / kT;
@@ -244,13 +245,6 @@ cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t st) {
     return launch_attn_tc(a, st);
 }
 
-cudaError_t attn_status_take(int32_t* bits, cudaStream_t st) {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(bits, g_status, sizeof(int32_t), 0, cudaMemcpyDeviceToHost, st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e != cudaSuccess || *bits == 0) return e;
-    const int32_t zero = 0;
-    e = cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st);
-    return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
-}
+cudaError_t attn_status_take(int32_t* bits, cudaStream_t st) { return take_word(g_status, bits, st); }
 
 }  // namespace lola

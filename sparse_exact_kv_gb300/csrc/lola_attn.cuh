@@ -2,6 +2,8 @@
 // cache's index arithmetic, and the launchers.
 #pragma once
 
+#include <atomic>
+
 #include "lola_internal.cuh"
 
 namespace lola {
@@ -133,6 +135,31 @@ __device__ __forceinline__ void seq_find(int n_seq, F&& count, int64_t u, int64_
     *rem_out = found_r;
 }
 
+// Opts a kernel in to `bytes` of dynamic shared memory, once per device (`done`: the kernel's own,
+// one bit per device; the call costs about a microsecond).
+template <typename K>
+cudaError_t opt_in_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
+// Reads a translation unit's anomaly word and clears it (after the stream's work).
+template <typename S>
+cudaError_t take_word(S& word, int32_t* bits, cudaStream_t st) {
+    cudaError_t e = cudaMemcpyFromSymbolAsync(bits, word, sizeof(int32_t), 0, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e != cudaSuccess || *bits == 0) return e;
+    const int32_t zero = 0;
+    e = cudaMemcpyToSymbolAsync(word, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st);
+    return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
+}
+
 // ---- launchers ----
 cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t st);
 cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t st);       // bf16 (lola_attn_tc.cu)
@@ -145,19 +172,16 @@ struct AppendArgs {
     const int32_t* positions;
 };
 cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t st);
-int64_t paged_decode_workspace(int Hq, int Hkv, int d);
+int64_t paged_decode_workspace(int d);
 struct DecodeArgs {
     PagedArgs p;
     Rows Q, O;
     float* lse;
     float* part;             // workspace
+    uint64_t tag;            // a number no other call has
     float scale_log2;
 };
-// traced as two kernels by the caller: the pieces, then their join (a no-op where nothing is split)
 cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t st);
-cudaError_t launch_paged_join(const DecodeArgs& a, cudaStream_t st);
-// whether some sequence may span more than one piece
-bool paged_decode_splits(const DecodeArgs& a);
 // reads and clears the anomaly words of a translation unit (after the stream's work)
 cudaError_t attn_status_take(int32_t* bits, cudaStream_t st);
 cudaError_t attn_tc_status_take(int32_t* bits, cudaStream_t st);

@@ -401,7 +401,8 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
     if (!make_map(&maps.q, a.Q, a.total_q, a.Hq, D) || !make_map(&maps.k, a.K, rows_k, Hkv, D) ||
         !make_map(&maps.v, a.V, rows_k, Hkv, D))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = opt_in_smem(attn_tc_kernel<D>, Cfg<D>::kSmem, done);
     if (e != cudaSuccess) return e;
     const int64_t tiles = ((int64_t)a.total_q + (int64_t)a.n_seq * (kQ - 1)) / kQ;
     attn_tc_kernel<D><<<(unsigned)(tiles * a.Hq), kThreads, Cfg<D>::kSmem, st>>>(maps, a);
@@ -412,13 +413,6 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
 
 cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t st) { return a.d == 128 ? launch<128>(a, st) : launch<64>(a, st); }
 
-cudaError_t attn_tc_status_take(int32_t* bits, cudaStream_t st) {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(bits, g_status, sizeof(int32_t), 0, cudaMemcpyDeviceToHost, st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e != cudaSuccess || *bits == 0) return e;
-    const int32_t zero = 0;
-    e = cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st);
-    return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
-}
+cudaError_t attn_tc_status_take(int32_t* bits, cudaStream_t st) { return take_word(g_status, bits, st); }
 
 }  // namespace lola

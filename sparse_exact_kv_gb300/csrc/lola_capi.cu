@@ -1,5 +1,7 @@
 // Host side of the C ABI declared in include/lola.h: argument validation, the state and
 // workspace layouts, and the stream-ordered sequence of kernels of each call.
+#include <atomic>
+#include <chrono>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -301,6 +303,18 @@ Rows to_rows(const lola_rows* r) { return r ? Rows{static_cast<char*>(r->data), 
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
+// A number of 56 bits that no other call of this process has, and that memory hardly holds by
+// chance (a mix of a counter and the process's start).
+uint64_t call_tag() {
+    static const uint64_t seed = (uint64_t)std::chrono::steady_clock::now().time_since_epoch().count();
+    static std::atomic<uint64_t> count{0};
+    uint64_t z = seed + (count.fetch_add(1, std::memory_order_relaxed) + 1) * 0x9e3779b97f4a7c15ull;   // SplitMix64
+    z = (z ^ (z >> 30)) * 0xbf58476d1ce4e5b9ull;
+    z = (z ^ (z >> 27)) * 0x94d049bb133111ebull;
+    z = (z ^ (z >> 31)) >> 8;
+    return z ? z : 1;
+}
+
 int32_t paged_check(const lola_attn_config* c, const lola_paged_kv* kv, PagedArgs* p) {
     const int32_t s = attn_check(c);
     if (s != LOLA_OK) return s;
@@ -547,7 +561,7 @@ int32_t lola_kernel_time(int32_t id, double* total_ms, int64_t* launches) {
 const char* lola_kernel_name(int32_t id) {
     static const char* names[LOLA_KERNEL_COUNT] = {"state_init", "phi",        "select",     "output",     "decode",
                                                         "phi_q",      "hola_prep",  "hola_state", "hola_cache", "hola_read",
-                                                        "attn",       "append",     "paged",      "paged_join"};
+                                                        "attn",       "append",     "paged"};
     return (id >= 0 && id < LOLA_KERNEL_COUNT) ? names[id] : "";
 }
 
@@ -740,7 +754,7 @@ int32_t lola_paged_append(const lola_attn_config* cfg, const lola_paged_kv* kv, 
 
 int64_t lola_paged_decode_workspace_bytes(const lola_attn_config* cfg) {
     const int32_t s = attn_check(cfg);
-    return s == LOLA_OK ? paged_decode_workspace(cfg->Hq, cfg->Hkv, cfg->d) : s;
+    return s == LOLA_OK ? paged_decode_workspace(cfg->d) : s;
 }
 
 int32_t lola_paged_decode(const lola_attn_config* cfg, const lola_paged_kv* kv, const lola_rows* Q,
@@ -751,16 +765,15 @@ int32_t lola_paged_decode(const lola_attn_config* cfg, const lola_paged_kv* kv, 
     if (!rows_ok(cfg, Q, kv->n_seq, cfg->Hq, false) || !rows_ok(cfg, O, kv->n_seq, cfg->Hq, true) || !aligned4(lse))
         return LOLA_ERR_INVALID_ARG;
     if (!workspace || !aligned16(workspace)) return LOLA_ERR_INVALID_ARG;
-    if ((int64_t)workspace_bytes < paged_decode_workspace(cfg->Hq, cfg->Hkv, cfg->d)) return LOLA_ERR_WORKSPACE;
+    if ((int64_t)workspace_bytes < paged_decode_workspace(cfg->d)) return LOLA_ERR_WORKSPACE;
     a.Q = to_rows(Q);
     a.O = to_rows(O);
     a.lse = lse;
     a.part = static_cast<float*>(workspace);
     a.scale_log2 = attn_scale_log2(cfg);
     cudaStream_t st = (cudaStream_t)stream;
-    cudaError_t e = traced(LOLA_KERNEL_PAGED, st, [&]() { return launch_paged_decode(a, st); });
-    if (e == cudaSuccess && paged_decode_splits(a))
-        e = traced(LOLA_KERNEL_PAGED_JOIN, st, [&]() { return launch_paged_join(a, st); });
+    a.tag = call_tag();
+    const cudaError_t e = traced(LOLA_KERNEL_PAGED, st, [&]() { return launch_paged_decode(a, st); });
     return e == cudaSuccess ? LOLA_OK : cuda_fail(e, "paged decode");
 }
 

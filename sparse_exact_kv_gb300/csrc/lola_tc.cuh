@@ -183,6 +183,11 @@ bool make_tmap3(CUtensorMap* m, CUtensorMapDataType type, int elem_bytes, const 
 // box_rows rows x 1 head x 64 channels, 128-byte swizzle, rows past the tensor zero-filled.
 bool make_tmap_rows(CUtensorMap* m, const void* base, int64_t rows, int heads, int d, int64_t row, int64_t head,
                     int box_rows);
+// Host: a 4-D tensor map over a page pool [depth][page][d] of elem_bytes bytes, a row as d *
+// elem_bytes / 128 columns of 128 bytes: boxes of box_rows rows of one page and head, column by column,
+// 128-byte swizzle.
+bool make_tmap_pages(CUtensorMap* m, CUtensorMapDataType type, int elem_bytes, const void* base, int d, int page,
+                     int64_t depth, int box_rows);
 
 __device__ __forceinline__ void cp_async16(uint32_t dst_smem, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src) : "memory");

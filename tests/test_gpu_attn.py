@@ -587,6 +587,6 @@ def test_kernel_timing_counts_the_new_kernels(L, gen):
     lay.decode_step(q, c.kv_len, c.table)
     lay.prefill(q, k, k, offsets([1]))
     L.lola_kernel_timing(False)
-    for name in ("attn", "append", "paged", "paged_join"):
+    for name in ("attn", "append", "paged"):
         ms, n = L.lola_kernel_time(name)
         assert n == 1 and ms > 0, name
