@@ -87,31 +87,15 @@ __global__ void __launch_bounds__(kNT, 2) attn_prefill_kernel(const AttnArgs a) 
     float* Ks = Qs + D * kLd;         // [D][kLd]
     float* Vs = Ks + D * kLd;         // [kT][D]
     float* Ps = Vs + kT * D;          // [key][kLd]
-    __shared__ int64_t scan[kNT / kWarp];
     constexpr int CW = D / 16;        // O columns per thread
 
-    // tile -> (sequence, query tile): sequences in order, a sequence's last (longest) tile first
-    // when the grid is read backwards
-    bool bad = false;
-    auto tiles = [&](int b) -> int64_t {
-        int lo, len;
-        seq_rows(a.cu_q, b, a.total_q, &lo, &len, &bad);
-        return (len + kT - 1) / kT;
-    };
-    const int64_t total = seq_total<kNT>(a.n_seq, tiles, scan);
-    const int64_t u = (int64_t)blockIdx.x / a.Hq;
-    const int h = blockIdx.x % a.Hq;
-    if (bad) atomicOr(&g_status, (int)LOLA_ATTN_BAD_OFFSETS);
-    if (u >= total) return;
-    int b;
-    int64_t rem;
-    seq_find<kNT>(a.n_seq, tiles, total - 1 - u, scan, &b, &rem);
-    int q0, lq, k0, lk;
-    seq_rows(a.cu_q, b, a.total_q, &q0, &lq, &bad);
-    bool badk = false;
-    seq_rows(a.cu_k, b, a.total_k, &k0, &lk, &badk);
-    if (badk && threadIdx.x == 0) atomicOr(&g_status, (int)LOLA_ATTN_BAD_OFFSETS);
-    const int r0 = (int)rem * kT, rows = min(kT, lq - r0), shift = lk - lq;
+    const int h = blockIdx.x % (unsigned)a.Hq;
+    TilePos at;
+    const bool live = find_tile<kNT, kT>(a, (int)(blockIdx.x / (unsigned)a.Hq), &at);
+    if (at.bad) atomicOr(&g_status, (int)LOLA_ATTN_BAD_OFFSETS);
+    if (!live) return;
+    const int q0 = at.q0, lq = at.lq, k0 = at.k0, lk = at.lk;
+    const int r0 = at.tile * kT, rows = min(kT, lq - r0), shift = lk - lq;
     const int keys = max(0, min(lk, r0 + rows + shift));      // keys some row of the tile sees
 
     const T* Q = reinterpret_cast<const T*>(a.Q.data) + (int64_t)(q0 + r0) * a.Q.row + (int64_t)h * a.Q.head;

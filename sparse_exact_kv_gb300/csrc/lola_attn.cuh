@@ -76,63 +76,80 @@ __host__ __device__ inline int split_of(int64_t total, int n, int64_t u) {
 }
 
 // ---- block-wide sums over sequences (NT threads, all of them) ----
-template <int NT>
-__device__ __forceinline__ int64_t block_total(int64_t x, int64_t* sm) {
+template <int NT, typename I>
+__device__ __forceinline__ I block_total(I x, I* sm) {
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     __syncthreads();
     if (lane == 0) sm[warp] = x;
     __syncthreads();
-    int64_t t = 0;
+    I t = 0;
 #pragma unroll
     for (int w = 0; w < NT / kWarp; ++w) t += sm[w];
     return t;
 }
-// sum of count(b) over all sequences
-template <int NT, typename F>
-__device__ __forceinline__ int64_t seq_total(int n_seq, F&& count, int64_t* sm) {
-    int64_t x = 0;
-    for (int b = threadIdx.x; b < n_seq; b += NT) x += count(b);
-    return block_total<NT>(x, sm);
-}
-// the sequence b that holds unit `u` (0 <= u < the total) of the units counted in order, and its
-// unit number inside b
-template <int NT, typename F>
-__device__ __forceinline__ void seq_find(int n_seq, F&& count, int64_t u, int64_t* sm, int* b_out, int64_t* rem_out) {
-    __shared__ int found_b;
-    __shared__ int64_t found_r;
+// Tile u of the packed queries (NT threads, all of them): the sequences' tiles of `rows` query rows are
+// counted in order and taken backwards, so that the CTAs that start last have the first sequence's first
+// (shortest) tiles.  False if there is no such tile.  Each thread looks at one sequence of up to NT, all
+// four of its offsets at once: one round of loads, then a scan.
+struct TilePos {
+    int q0, lq, k0, lk, tile;
+    bool bad;            // some offsets are malformed (thread-local: what this thread has seen)
+};
+template <int NT, int rows>
+__device__ __forceinline__ bool find_tile(const AttnArgs& a, int u, TilePos* pos) {
+    __shared__ int sums[NT / kWarp];
+    __shared__ TilePos found;
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
-    int64_t before = 0;
-    for (int base = 0; base < n_seq; base += NT) {
-        const int b = base + (int)threadIdx.x;
-        const int64_t own = b < n_seq ? count(b) : 0;
-        int64_t inc = own;
+    TilePos own;
+    pos->bad = false;
+    auto look = [&](int b) -> int {
+        own.q0 = own.lq = own.k0 = own.lk = 0;
+        if (b >= a.n_seq) return 0;
+        bool bad = false, badk = false;
+        seq_rows(a.cu_q, b, a.total_q, &own.q0, &own.lq, &bad);
+        seq_rows(a.cu_k, b, a.total_k, &own.k0, &own.lk, &badk);
+        pos->bad |= bad | badk;
+        return (own.lq + rows - 1) / rows;
+    };
+    int n = 0;
+    for (int b = threadIdx.x + NT; b < a.n_seq; b += NT) n += look(b);
+    const int n0 = look(threadIdx.x);
+    const int total = block_total<NT>(n + n0, sums);
+    if (u >= total) return false;
+    const int want = total - 1 - u;
+    int before = 0;
+    for (int base = 0; base < a.n_seq; base += NT) {
+        const int x = base == 0 ? n0 : look(base + threadIdx.x);
+        int inc = x;
 #pragma unroll
         for (int o = 1; o < kWarp; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += y;
         }
         __syncthreads();
-        if (lane == kWarp - 1) sm[warp] = inc;
+        if (lane == kWarp - 1) sums[warp] = inc;
         __syncthreads();
-        int64_t pre = before, all = before;
+        int pre = before, all = before;
 #pragma unroll
         for (int w = 0; w < NT / kWarp; ++w) {
-            if (w < warp) pre += sm[w];
-            all += sm[w];
+            if (w < warp) pre += sums[w];
+            all += sums[w];
         }
-        const int64_t lo = pre + inc - own;
-        if (u >= lo && u < lo + own) {
-            found_b = b;
-            found_r = u - lo;
+        const int lo = pre + inc - x;
+        if (want >= lo && want < lo + x) {
+            found = own;
+            found.tile = want - lo;
         }
-        if (u < all) break;
+        if (want < all) break;
         before = all;
     }
     __syncthreads();
-    *b_out = found_b;
-    *rem_out = found_r;
+    const bool bad = pos->bad;
+    *pos = found;
+    pos->bad = bad;
+    return true;
 }
 
 // Opts a kernel in to `bytes` of dynamic shared memory, once per device (`done`: the kernel's own,

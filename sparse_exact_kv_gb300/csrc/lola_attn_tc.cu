@@ -36,13 +36,13 @@ constexpr int kQ = 2 * kM;               // queries per CTA
 constexpr int kN = 128;                  // keys per block
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kCleanWarp0 = 10;
 constexpr int kThreads = 384;
+constexpr int kPairs = 4;                // barriers of the pairs (see the kernel)
 constexpr float kRaise = 8.0f;           // m is raised when a block's maximum passes it by this (log2)
 constexpr uint64_t kWaitNs = 1000000000ull;
 
 template <int D> struct Cfg {
     static constexpr int kTileBytes = kM * D * 2;          // a Q tile, a K block or a V block
     static constexpr int kStages = D == 128 ? 5 : 8;       // K and V blocks in the ring
-    static constexpr int kCleanPeriod = kStages % 2 ? kStages : kStages / 2;   // blocks until a V uses the same stage
     static constexpr int kSmem = (2 + kStages) * kTileBytes + 1024;
     __device__ static constexpr uint32_t TS(int i) { return 128u * i; }          // S (P over its first half)
     __device__ static constexpr uint32_t TO(int i) { return 256u + (uint32_t)D * i; }
@@ -59,6 +59,51 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Products whose shared-memory descriptors come as a low word (address and leading offset in 16-byte
+// units) and a high word that all of them share (stride 1024, version, swizzle): one thread issues 32 of
+// them a block, and building the 64-bit descriptors each time took longer than the products.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | ((lbo >> 4) << 16); }
+__device__ __forceinline__ void mma_ss(uint32_t tmem, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}\n" ::"r"(tmem),
+        "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void mma_ts(uint32_t tmem, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tmov.b64 db, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}\n" ::"r"(tmem),
+        "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc));
+}
+// 16 consecutive 32-bit columns of this thread's TMEM lane (warp-collective)
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+// two float32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t x, y, z, r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c.x), "f"(c.y));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    float2 o;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+    return o;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t x, y, r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    float2 o;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+    return o;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
     using C = Cfg<D>;
@@ -66,38 +111,48 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(sm);
     enum {
-        B_Q = 0, B_S = 2, B_P = 4, B_O = 6, B_DONE = 8, B_FULL = 9, B_EMPTY = B_FULL + C::kStages,
-        B_CLEAN = B_EMPTY + C::kStages, B_N = B_CLEAN + C::kStages
+        B_Q = 0, B_S = 2, B_P = 4, B_O = 6, B_DONE = 8, B_FULL = 9, B_EMPTY = B_FULL + kPairs, B_CLEAN = B_EMPTY + kPairs,
+        B_ARMED = B_CLEAN + kPairs, B_N = B_ARMED + kPairs
     };
     __shared__ __align__(8) uint64_t bars[B_N];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_sm, odd_sm;
-    __shared__ int64_t scan[kThreads / kWarp];
     const int tid = threadIdx.x, warp = tid / kWarp, lane = tid % kWarp;
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
 
-    // ---- this CTA's tile: sequences in order, read backwards, so that the CTAs that start last
-    // have the first sequence's first (shortest) tiles ----
-    bool bad = false;
-    auto tiles = [&](int b) -> int64_t {
-        int lo, len;
-        seq_rows(a.cu_q, b, a.total_q, &lo, &len, &bad);
-        return (len + kQ - 1) / kQ;
-    };
-    const int64_t total = seq_total<kThreads>(a.n_seq, tiles, scan);
-    const int64_t u = (int64_t)blockIdx.x / a.Hq;
-    const int h = blockIdx.x % a.Hq;
-    if (bad) atomicOr(&g_status, (int)LOLA_ATTN_BAD_OFFSETS);
-    if (u >= total) return;
-    int b;
-    int64_t rem;
-    seq_find<kThreads>(a.n_seq, tiles, total - 1 - u, scan, &b, &rem);
-    int q0, lq, k0, lk;
-    seq_rows(a.cu_q, b, a.total_q, &q0, &lq, &bad);
-    bool badk = false;
-    seq_rows(a.cu_k, b, a.total_k, &k0, &lk, &badk);
-    if (badk && tid == 0) atomicOr(&g_status, (int)LOLA_ATTN_BAD_OFFSETS);
-    const int r0 = (int)rem * kQ, shift = lk - lq;
+    if (tid == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.q)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.v)) : "memory");
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(B_Q + i), 1);
+            mbar_init(bar(B_S + i), 1);
+            mbar_init(bar(B_P + i), 4);
+            mbar_init(bar(B_O + i), 1);
+        }
+        mbar_init(bar(B_DONE), 1);
+        for (int s = 0; s < kPairs; ++s) {
+            mbar_init(bar(B_CLEAN + s), 2);
+            mbar_init(bar(B_ARMED + s), 1);
+            mbar_init(bar(B_FULL + s), 1);
+            mbar_init(bar(B_EMPTY + s), 1);
+        }
+        abort_sm = 0;
+        odd_sm = 0;
+    }
+    if (warp == kMmaWarp) tmem_alloc<512>(smem_u32(&tmem_base));
+    const int h = blockIdx.x % (unsigned)a.Hq;
+    TilePos at;
+    const bool live = find_tile<kThreads, kQ>(a, (int)(blockIdx.x / (unsigned)a.Hq), &at);
+    if (at.bad) atomicOr(&g_status, (int)LOLA_ATTN_BAD_OFFSETS);
+    if (!live) {
+        if (warp == kMmaWarp) {
+            __syncwarp();
+            tmem_dealloc<512>(*reinterpret_cast<volatile uint32_t*>(&tmem_base));
+        }
+        return;
+    }
+    const int q0 = at.q0, lq = at.lq, k0 = at.k0, lk = at.lk, r0 = at.tile * kQ, shift = lk - lq;
     // blocks that tile i reads, and those that all its rows see whole
     int nb[2], nf = 0x7fffffff;
 #pragma unroll
@@ -108,23 +163,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     }
     const int nmax = max(nb[0], nb[1]);
 
-    if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(B_Q + i), 1);
-            mbar_init(bar(B_S + i), 1);
-            mbar_init(bar(B_P + i), 4);
-            mbar_init(bar(B_O + i), 1);
-        }
-        mbar_init(bar(B_DONE), 1);
-        for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(bar(B_CLEAN + s), 2);
-            mbar_init(bar(B_FULL + s), 1);
-            mbar_init(bar(B_EMPTY + s), 1);
-        }
-        abort_sm = 0;
-        odd_sm = 0;
-    }
-    if (warp == kMmaWarp) tmem_alloc<512>(smem_u32(&tmem_base));
     fence_before();
     __syncthreads();
     fence_after();
@@ -151,9 +189,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             }
         }
     };
-    // ring: block j's K is load 2 j, its V load 2 j + 1
+    // Ring: block j's K is load 2 j, its V load 2 j + 1.  Pair p is what the products of one turn read, V of
+    // block p - 1 and K of block p (pair 0: only K): it has one barrier for "loaded" and one for "read",
+    // p % 4 of either (a pair's barrier comes again four pairs later, and fewer than four are in the ring).
     auto stage = [&](int x) { return x % C::kStages; };
-    auto phase = [&](int x) { return (uint32_t)(x / C::kStages) & 1u; };
+    auto pair = [&](int p) { return p & (kPairs - 1); };
+    auto phase = [&](int p) { return (uint32_t)(p / kPairs) & 1u; };
     auto ring = [&](int x) { return sb + (uint32_t)(2 + stage(x)) * C::kTileBytes; };
 
     if (warp >= kMmaWarp) {
@@ -166,65 +207,69 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     mbar_expect(bar(bi), C::kTileBytes);
                     for (int x = 0; x < D / 64; ++x) tma_load3(dst + 16384u * x, m, 64 * x, head, row, bar(bi));
                 };
+                if (nb[0] > 0) load(&maps.q, q0 + r0, h, sb, B_Q);
                 bool ok = true;
-                int n = 0;
-                for (; n < 2 * nmax; ++n) {
-                    if (n >= C::kStages && !(ok = wait(B_EMPTY + stage(n), phase(n - C::kStages)))) break;
-                    if (n == 0 && nb[0] > 0) load(&maps.q, q0 + r0, h, sb, B_Q);
-                    load(n & 1 ? &maps.v : &maps.k, k0 + (n >> 1) * kN, hk, ring(n), B_FULL + stage(n));
-                    if (n == 0 && nb[1] > 0) load(&maps.q, q0 + r0 + kM, h, sb + C::kTileBytes, B_Q + 1);
+                int p = 0, waited = 0;
+                for (; p <= nmax && ok; ++p) {
+                    const int last = p < nmax ? 2 * p : 2 * p - 1;              // the pair's last load
+                    // the stages it takes: their loads' pairs have been read
+                    while (ok && last >= C::kStages && waited <= (last - C::kStages + 1) / 2) {
+                        ok = wait(B_EMPTY + pair(waited), phase(waited));
+                        ++waited;
+                    }
+                    if (!ok) break;
+                    const int full = B_FULL + pair(p);
+                    mbar_expect(bar(full), (uint32_t)((p > 0) + (p < nmax)) * C::kTileBytes);
+                    if (p > nf) mbar_arrive1(bar(B_ARMED + pair(p)));
+                    for (int n = max(0, 2 * p - 1); n <= last; ++n)
+                        for (int x = 0; x < D / 64; ++x)
+                            tma_load3(ring(n) + 16384u * x, n & 1 ? &maps.v : &maps.k, 64 * x, hk, k0 + (n >> 1) * kN, bar(full));
+                    if (p == 0 && nb[1] > 0) load(&maps.q, q0 + r0 + kM, h, sb + C::kTileBytes, B_Q + 1);
                 }
                 // leave no copy in flight
-                for (int i = max(0, n - C::kStages); i < n; ++i) mbar_wait(bar(B_FULL + stage(i)), phase(i), kWaitNs);
-                if (n > 0)
-                    for (int i = 0; i < 2; ++i)
-                        if (nb[i] > 0) mbar_wait(bar(B_Q + i), 0, kWaitNs);
+                for (int x = max(0, p - kPairs); x < p; ++x) mbar_wait(bar(B_FULL + pair(x)), phase(x), kWaitNs);
+                for (int i = 0; i < 2; ++i)
+                    if (nb[i] > 0) mbar_wait(bar(B_Q + i), 0, kWaitNs);
             }
         } else if (warp == kMmaWarp) {
             // ================================ MMA issue ================================
             if (lane == 0 && nmax > 0) {
                 constexpr uint32_t id_s = idesc_bf16(kM, kN, 0), id_o = idesc_bf16(kM, D, 1);
+                constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
                 auto s_mma = [&](int i, int j) {
-                    const uint32_t q = sb + (uint32_t)i * C::kTileBytes, k = ring(2 * j);
+                    const uint32_t q = desc_lo(sb + (uint32_t)i * C::kTileBytes, 16), k = desc_lo(ring(2 * j), 16);
 #pragma unroll
                     for (int x = 0; x < D / 16; ++x) {
-                        const uint32_t o = (uint32_t)(x >> 2) * 16384u + (uint32_t)(x & 3) * 32u;
-                        mma_bf16(tb + C::TS(i), sdesc(q + o, 16, 1024), sdesc(k + o, 16, 1024), id_s, x > 0);
+                        const uint32_t o = (uint32_t)(x >> 2) * 1024u + (uint32_t)(x & 3) * 2u;   // 16-byte units
+                        mma_ss(tb + C::TS(i), q + o, k + o, hi, id_s, x > 0);
                     }
                     mma_commit(bar(B_S + i));
                 };
-                bool ok = wait(B_FULL + stage(0), phase(0));
+                bool ok = wait(B_FULL, 0);
                 for (int i = 0; i < 2 && ok; ++i)
                     if (nb[i] > 0) {
                         ok = wait(B_Q + i, 0);
                         fence_after();
                         if (ok) s_mma(i, 0);
                     }
-                mma_commit(bar(B_EMPTY + stage(0)));
+                mma_commit(bar(B_EMPTY));
                 for (int j = 0; j < nmax && ok; ++j) {
-                    bool have_k = false;
-                    ok = wait(B_FULL + stage(2 * j + 1), phase(2 * j + 1));
-                    if (ok && j >= nf) ok = wait(B_CLEAN + stage(2 * j + 1), (uint32_t)((j - nf) / C::kCleanPeriod) & 1u);
+                    // V of block j and K of block j + 1
+                    ok = wait(B_FULL + pair(j + 1), phase(j + 1));
+                    if (ok && j >= nf) ok = wait(B_CLEAN + pair(j + 1), (uint32_t)((j - nf) / kPairs) & 1u);
+                    const uint32_t v = desc_lo(ring(2 * j + 1), 16384);
                     for (int i = 0; i < 2 && ok; ++i) {
                         if (j < nb[i]) {
                             if (!(ok = wait(B_P + i, (uint32_t)j & 1u))) break;
                             fence_after();
-                            const uint32_t v = ring(2 * j + 1);
 #pragma unroll
                             for (int x = 0; x < kN / 16; ++x)
-                                mma_bf16_ts(tb + C::TO(i), tb + C::TS(i) + 8 * x, sdesc(v + 2048u * x, 16384, 1024), id_o,
-                                            j > 0 || x > 0);
-                            mma_commit(bar(B_O + i));
+                                mma_ts(tb + C::TO(i), tb + C::TS(i) + 8 * x, v + 128u * x, hi, id_o, x > 0 ? 1u : (uint32_t)j);
                         }
-                        if (j + 1 < nb[i]) {
-                            if (!have_k && !(ok = wait(B_FULL + stage(2 * j + 2), phase(2 * j + 2)))) break;
-                            have_k = true;
-                            fence_after();
-                            s_mma(i, j + 1);
-                        }
+                        if (j + 1 < nb[i]) s_mma(i, j + 1);
+                        else if (j + 1 == nb[i]) mma_commit(bar(B_O + i));
                     }
-                    mma_commit(bar(B_EMPTY + stage(2 * j + 1)));
-                    if (j + 1 < nmax) mma_commit(bar(B_EMPTY + stage(2 * j + 2)));
+                    mma_commit(bar(B_EMPTY + pair(j + 1)));
                 }
                 // leave no product in flight
                 mma_commit(bar(B_DONE));
@@ -235,41 +280,51 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             // ================================ cleaners ================================
             const int ct = tid - kCleanWarp0 * kWarp;
             bool ok = true;
-            for (int j = 0; j < nmax && nf < nmax && ok; ++j) {
-                // (every load is waited for, in order: a barrier tells only the last two phases apart)
-                ok = wait(B_FULL + stage(2 * j), phase(2 * j)) && wait(B_FULL + stage(2 * j + 1), phase(2 * j + 1));
+            for (int j = nf; j < nmax && ok; ++j) {
+                // (a pair's "loaded" can be told from the one four pairs before only once it is armed)
+                ok = wait(B_ARMED + pair(j + 1), (uint32_t)((j - nf) / kPairs) & 1u) && wait(B_FULL + pair(j + 1), phase(j + 1));
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                if (j < nf) continue;
                 uint8_t* v = sm + (size_t)(2 + stage(2 * j + 1)) * C::kTileBytes;
                 const int valid = min(kN, lk - j * kN);
+                // 16-byte chunks in memory order, eight in flight; a bfloat16 is not finite iff adding 1
+                // to its exponent carries into the sign
                 bool odd = false;
-                for (int x = ct; x < kN * D / 8; x += 64) {          // 16-byte chunks, in memory order
-                    const int row = (x >> 3) & (kN - 1);
-                    uint4* p = reinterpret_cast<uint4*>(v) + x;
-                    if (row >= valid) {
-                        *p = make_uint4(0, 0, 0, 0);
-                        continue;
-                    }
-                    const uint4 y = *p;
-                    uint32_t w[4] = {y.x, y.y, y.z, y.w};
-                    bool hit = false;
+                uint4* p = reinterpret_cast<uint4*>(v) + ct;
+#pragma unroll 1
+                for (int x0 = 0; x0 < kN * D / 8 / 64; x0 += 8) {
+                    uint4 y[8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const bool lo = (w[e] & 0x7f80u) == 0x7f80u, hi = (w[e] & 0x7f800000u) == 0x7f800000u;
-                        hit |= lo | hi;
-                        w[e] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0xffffu : ~0u);
+                    for (int x = 0; x < 8; ++x) y[x] = p[64 * (x0 + x)];
+                    uint32_t hit = 0;
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const int row = ((ct + 64 * (x0 + x)) >> 3) & (kN - 1);
+                        const uint32_t t = ((y[x].x & 0x7f807f80u) + 0x00800080u) | ((y[x].y & 0x7f807f80u) + 0x00800080u) |
+                                           ((y[x].z & 0x7f807f80u) + 0x00800080u) | ((y[x].w & 0x7f807f80u) + 0x00800080u);
+                        if (row < valid) hit |= t;
+                        else p[64 * (x0 + x)] = make_uint4(0, 0, 0, 0);
                     }
-                    if (hit) {
-                        *p = make_uint4(w[0], w[1], w[2], w[3]);
-                        odd = true;
+                    if (!(hit & 0x80008000u)) continue;
+                    odd = true;
+#pragma unroll 1
+                    for (int x = 0; x < 8; ++x) {
+                        uint4* c = p + 64 * (x0 + x);
+                        const uint4 z = *c;
+                        uint32_t w[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const bool lo = (w[e] & 0x7f80u) == 0x7f80u, hi = (w[e] & 0x7f800000u) == 0x7f800000u;
+                            w[e] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0xffffu : ~0u);
+                        }
+                        *c = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
                 if (odd) *reinterpret_cast<volatile int*>(&odd_sm) = 1;
                 fence_async_smem();
                 __threadfence_block();
                 __syncwarp();
-                if (lane == 0) mbar_arrive1(bar(B_CLEAN + stage(2 * j + 1)));
+                if (lane == 0) mbar_arrive1(bar(B_CLEAN + pair(j + 1)));
             }
         }
     } else {
@@ -291,9 +346,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             for (int x = 0; x < kN; x += 32) tmem_ld32(ts + x, s + x);
             tmem_wait_ld();
             if (j >= wfull) {
-                const int lim = last - j * kN;
+                const int lim = last - j * kN, w0 = __reduce_min_sync(0xffffffffu, lim);
 #pragma unroll
-                for (int x = 0; x < kN; ++x) s[x] = x <= lim ? s[x] : -INFINITY;
+                for (int x = 0; x < kN; x += 32) {
+                    if (w0 >= x + 31) continue;
+#pragma unroll
+                    for (int y = x; y < x + 32; ++y) s[y] = y <= lim ? s[y] : -INFINITY;
+                }
             }
             float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -303,51 +362,56 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             if (j == 0) {
                 m = bm;
             } else if (__any_sync(0xffffffffu, need)) {
-                // O_i is quiet once the product before this block is done
-                if (!(ok = __all_sync(0xffffffffu, wait(B_O + i, (uint32_t)(j - 1) & 1u)))) break;
-                fence_after();
+                // (O_i is quiet: S of this block was issued behind the block before's P V, and is done)
                 const float f = need ? ex2(m - bm) : 1.f;
                 l *= f;
-#pragma unroll
-                for (int x = 0; x < D; x += 32) {
-                    float o[32];
-                    tmem_ld32(to + x, o);
+                // (rare, and with S in registers: 16 columns at a time)
+#pragma unroll 1
+                for (int x = 0; x < D; x += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(to + x, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int y = 0; y < 32; ++y) o[y] *= f;
-                    tmem_st32(to + x, o);
+                    for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                    tmem_st16(to + x, o);
                 }
                 if (need) m = bm;
             }
             const float base = m == -INFINITY ? 0.f : m;
-            float ls[4] = {0.f, 0.f, 0.f, 0.f};
+            float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
 #pragma unroll
             for (int x = 0; x < kN; x += 32) {
                 uint32_t p[16];
 #pragma unroll
                 for (int y = 0; y < 16; ++y) {
-                    const float e0 = ex2(fmaf(s[x + 2 * y], c, -base)), e1 = ex2(fmaf(s[x + 2 * y + 1], c, -base));
-                    ls[(2 * y) & 3] += e0;
-                    ls[(2 * y + 1) & 3] += e1;
-                    const __nv_bfloat162 bp = __floats2bfloat162_rn(e0, e1);
+                    float2 e = fma2(make_float2(s[x + 2 * y], s[x + 2 * y + 1]), c2, b2);
+                    e.x = ex2(e.x);
+                    e.y = ex2(e.y);
+                    ls[y & 1] = add2(ls[y & 1], e);
+                    const __nv_bfloat162 bp = __floats2bfloat162_rn(e.x, e.y);
                     p[y] = *reinterpret_cast<const uint32_t*>(&bp);
                 }
                 tmem_st16(ts + x / 2, p);
             }
-            l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
             tmem_wait_st();
             fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive1(bar(B_P + i));
+            l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
         }
         // ---- o = O / l ----
-        if (n > 0 && ok) ok = __all_sync(0xffffffffu, wait(B_O + i, (uint32_t)(n - 1) & 1u));
+        if (n > 0 && ok) ok = __all_sync(0xffffffffu, wait(B_O + i, 0));
         fence_after();
-        const bool none = last < 0 || n == 0, live = row < lq && ok;
+        const bool none = last < 0 || n == 0, own = row < lq && ok;
         const float inv = 1.f / l;
-        __nv_bfloat16* O = reinterpret_cast<__nv_bfloat16*>(a.O.data) + (int64_t)(q0 + row) * a.O.row + (int64_t)h * a.O.head;
         const bool odd = *reinterpret_cast<volatile int*>(&odd_sm) != 0;
-#pragma unroll
+        // the tile's Q rows have been read: their place takes o (the same swizzled layout), from where
+        // whole rows go out, 512 bytes a warp and store
+        uint8_t* stagep = sm + (size_t)i * C::kTileBytes;
+        const int r = (warp & 3) * 32 + lane;
+        // (loops, not unrolled: straight code that runs once is fetched slower than it executes)
+#pragma unroll 1
         for (int x = 0; x < D; x += 32) {
             float o[32];
             if (n > 0) {
@@ -357,29 +421,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             uint32_t p[16];
 #pragma unroll
             for (int y = 0; y < 32; ++y) o[y] = none ? 0.f : o[y] * inv;
-            if (odd && live) {
-                // values that are not finite and were kept out of the products: for the keys the row sees
-                const __nv_bfloat16* V = reinterpret_cast<const __nv_bfloat16*>(a.V.data) +
-                                         (int64_t)(h / a.G) * a.V.head + x;
-                for (int key = nf * kN; key <= last; ++key)
-#pragma unroll
-                    for (int y = 0; y < 32; ++y) {
-                        const float v = __bfloat162float(V[(int64_t)(k0 + key) * a.V.row + y]);
-                        if (!(fabsf(v) <= 3.4e38f)) o[y] += v;
-                    }
-            }
 #pragma unroll
             for (int y = 0; y < 16; ++y) {
                 const __nv_bfloat162 bp = __floats2bfloat162_rn(o[2 * y], o[2 * y + 1]);
                 p[y] = *reinterpret_cast<const uint32_t*>(&bp);
             }
-            if (live) {
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    *reinterpret_cast<uint4*>(O + x + 8 * y) = make_uint4(p[4 * y], p[4 * y + 1], p[4 * y + 2], p[4 * y + 3]);
+            for (int y = 0; y < 4; ++y)
+                *reinterpret_cast<uint4*>(stagep + (x >> 6) * 16384 + kmaj_chunk(r, ((x & 63) >> 3) + y)) =
+                    make_uint4(p[4 * y], p[4 * y + 1], p[4 * y + 2], p[4 * y + 3]);
+        }
+        if (odd && own) {
+            // values that are not finite and were kept out of the products: for the keys the row sees
+            // (rare, so small code: one channel at a time)
+#pragma unroll 1
+            for (int x = 0; x < D; ++x) {
+                const __nv_bfloat16* V = reinterpret_cast<const __nv_bfloat16*>(a.V.data) + (int64_t)(h / a.G) * a.V.head + x;
+                float add = 0.f;
+#pragma unroll 1
+                for (int key = nf * kN; key <= last; ++key) {
+                    const float v = __bfloat162float(V[(int64_t)(k0 + key) * a.V.row]);
+                    if (!(fabsf(v) <= 3.4e38f)) add += v;
+                }
+                __nv_bfloat16* z = reinterpret_cast<__nv_bfloat16*>(stagep + (x >> 6) * 16384 + kmaj_chunk(r, (x & 63) >> 3)) + (x & 7);
+                if (add != 0.f) *z = __float2bfloat16_rn(__bfloat162float(*z) + add);
             }
         }
-        if (a.lse && live)
+        __syncwarp();
+        constexpr int CH = D / 8, RW = 32 / CH;                 // chunks of a row, rows of a store
+        __nv_bfloat16* O = reinterpret_cast<__nv_bfloat16*>(a.O.data) + (int64_t)(q0 + row - lane) * a.O.row +
+                           (int64_t)h * a.O.head;
+        const int rest = ok ? lq - (row - lane) : 0;            // rows of the warp inside the sequence
+        const int ch = lane % CH;
+#pragma unroll 4
+        for (int x = 0; x < 32; x += RW) {
+            const int y = x + lane / CH;
+            const uint4 z = *reinterpret_cast<const uint4*>(stagep + (ch >> 3) * 16384 + kmaj_chunk((warp & 3) * 32 + y, ch & 7));
+            if (y < rest) *reinterpret_cast<uint4*>(O + (int64_t)y * a.O.row + 8 * ch) = z;
+        }
+        if (a.lse && own)
             a.lse[(int64_t)h * a.total_q + q0 + row] = none ? -INFINITY : (m + log2f(l)) * kAttnLn2;
     }
     fence_before();
