@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     };
     // Ring: block j's K is load 2 j, its V load 2 j + 1.  Pair p is what the products of one turn read, V of
     // block p - 1 and K of block p (pair 0: only K): it has one barrier for "loaded" and one for "read",
-    // p % 4 of either (a pair's barrier comes again four pairs later, and fewer than four are in the ring).
+    // p % 4 of either, so a pair is loaded only when the one four before it has been read.
     auto stage = [&](int x) { return x % C::kStages; };
     auto pair = [&](int p) { return p & (kPairs - 1); };
     auto phase = [&](int p) { return (uint32_t)(p / kPairs) & 1u; };
@@ -212,8 +212,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 int p = 0, waited = 0;
                 for (; p <= nmax && ok; ++p) {
                     const int last = p < nmax ? 2 * p : 2 * p - 1;              // the pair's last load
-                    // the stages it takes: their loads' pairs have been read
-                    while (ok && last >= C::kStages && waited <= (last - C::kStages + 1) / 2) {
+                    // what its stages and its barriers held before has been read
+                    const int held = last >= C::kStages ? (last - C::kStages + 1) / 2 : -1;
+                    while (ok && waited <= max(held, p - kPairs)) {
                         ok = wait(B_EMPTY + pair(waited), phase(waited));
                         ++waited;
                     }

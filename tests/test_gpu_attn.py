@@ -58,6 +58,18 @@ def test_prefill_lengths(L, gen, dtype, d, Hq, Hkv, lens):
     check_prefill(q, k, v, lq, lk, out, lse)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [384, 512, 640, 768, 896, 1024, 1152])
+def test_prefill_every_ring_length(L, gen, d, n):
+    """Many sequences of three to nine key blocks: the ring of key and value blocks ends at every one
+    of its stages (at four blocks of d = 64 the whole sequence fits the ring)."""
+    B, H = 24, 4
+    q, k, v = (randn(gen, B * n, H, d, dtype=BF) for _ in range(3))
+    out = L.ExactAttention(H, H, d).prefill(q, k, v, offsets([n] * B))
+    quiet(L)
+    check_prefill(q, k, v, [n] * B, [n] * B, out, heads=[0, 3], rows=[0, 127, 128, 255, 256, n - 129, n - 1])
+
+
 @pytest.mark.parametrize("dtype,d,Hq,Hkv,n", [(BF, 128, 8, 1, 2100), (BF, 64, 4, 4, 3001), (F32, 64, 2, 1, 1500)])
 def test_prefill_longer(L, gen, dtype, d, Hq, Hkv, n):
     """Many key blocks; scores grow along the sequence, so the running maximum moves all the time."""
