@@ -6,20 +6,31 @@
 // m is raised lazily: O and l are rescaled (in TMEM) only when a block's maximum passes m by more
 // than 2^8, so that P and l stay far inside float32 and bfloat16, and blocks rarely wait for O.
 //
-// One CTA takes 256 queries of one head as two tiles of 128 (MMA M = 128, TMEM lane = query) that
-// share every K and V block; while the tensor core works for one tile, the other tile's softmax runs:
-//   * warp 9 (loader): Q, K and V tiles by TMA, 128-byte swizzle, into a ring of K and V blocks;
-//   * warp 8 (MMA, one thread): per block and tile O_i += P_i V_j, then S_i = Q_i K_{j+1}^T.  P_i
+// A CTA takes 256 queries of one head as two tiles of 128 (MMA M = 128, TMEM lane = query) that share
+// every K and V block; while the tensor core works for one tile, the other tile's softmax runs.  Short
+// sequences take one tile per CTA and two CTAs per SM instead, each in half an SM (see one_tile below).
+// Warps (of two tiles):
+//   * 9 (loader): Q, K and V tiles by TMA, 128-byte swizzle, into a ring of K and V blocks;
+//   * 8 (MMA, one thread): per block and tile O_i += P_i V_j, then S_i = Q_i K_{j+1}^T.  P_i
 //     (bf16, read from TMEM as the A operand) lies over S_i's columns: the products of one thread
 //     run in order, so S_i of the next block cannot overtake the read of P_i;
-//   * warps 0-3, 4-7 (softmax of tile 0, 1; one thread per query): the row of S into registers,
+//   * 0-3, 4-7 (softmax of tile 0, 1; one thread per query): the row of S into registers,
 //     mask on the blocks that some row does not see whole, maximum, weights, P into TMEM;
-//   * warps 10-11 (cleaners): on those same blocks, V rows behind the sequence and values that are
+//   * 10-11 (cleaners): on those same blocks, V rows behind the sequence and values that are
 //     not finite are zeroed in shared memory before the product (0 x NaN would reach rows
-//     that do not see them); what was finite-less is added back in the epilogue, row by row, for
-//     the rows that see it.
+//     that do not see them); the values taken out are added back in the epilogue, for the rows
+//     that see them.
+// What bounds it: for long sequences the tensor core and its power (16 heads of 32768 tokens, d = 128:
+// 2.96 ms, 1483 TFLOP/s of the measured 1849); a block pair's products take about 2300 cycles of the
+// issuing thread's 2900-3200, the rest is its wait for the weights (a softmax is 1100 cycles, behind it
+// the other tile's products).  For short ones the start and end of a CTA: about 2200 cycles of tile
+// lookup, 3500 until the first scores, 2500 of epilogue.
+// Tried and slower: releasing P in halves, comparing S by column groups while it loads, one MMA thread
+// for each tile (their products interleave: 3.20 ms), the next pair's waits between the products.
 // Every wait is bounded (1 s, then LOLA_ATTN_TIMEOUT).
 #include <cuda.h>
+
+#include <cmath>
 
 #include "lola_attn.cuh"
 #include "lola_tc.cuh"
@@ -32,20 +43,23 @@ using namespace tc;
 __device__ int32_t g_status;
 
 constexpr int kM = 128;                  // queries per tile
-constexpr int kQ = 2 * kM;               // queries per CTA
 constexpr int kN = 128;                  // keys per block
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kCleanWarp0 = 10;
-constexpr int kThreads = 384;
 constexpr int kPairs = 4;                // barriers of the pairs (see the kernel)
 constexpr float kRaise = 8.0f;           // m is raised when a block's maximum passes it by this (log2)
 constexpr uint64_t kWaitNs = 1000000000ull;
 
-template <int D> struct Cfg {
+// NT: query tiles of a CTA.  Two: one CTA per SM, K and V blocks shared by 256 queries.  One: two CTAs
+// per SM, each with its own ring (half the shared memory, half of TMEM).
+template <int D, int NT> struct Cfg {
+    static constexpr int kQ = NT * kM;                     // queries per CTA
+    static constexpr int kThreads = (NT + 1) * 128;
+    static constexpr int kMmaWarp = 4 * NT, kLoadWarp = kMmaWarp + 1, kCleanWarp0 = kMmaWarp + 2;
     static constexpr int kTileBytes = kM * D * 2;          // a Q tile, a K block or a V block
-    static constexpr int kStages = D == 128 ? 5 : 8;       // K and V blocks in the ring
-    static constexpr int kSmem = (2 + kStages) * kTileBytes + 1024;
-    __device__ static constexpr uint32_t TS(int i) { return 128u * i; }          // S (P over its first half)
-    __device__ static constexpr uint32_t TO(int i) { return 256u + (uint32_t)D * i; }
+    static constexpr int kStages = NT == 2 ? (D == 128 ? 5 : 8) : (D == 128 ? 2 : 5);   // K and V blocks in the ring
+    static constexpr int kSmem = (NT + kStages) * kTileBytes + 1024;
+    static constexpr int kTmem = 256 * NT;                 // columns
+    __device__ static constexpr uint32_t TS(int i) { return 128u * i; }            // S (P over its first half)
+    __device__ static constexpr uint32_t TO(int i) { return 128u * NT + (uint32_t)D * i; }
 };
 
 struct Maps {
@@ -104,9 +118,10 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return o;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
-    using C = Cfg<D>;
+template <int D, int NT>
+__global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
+    using C = Cfg<D, NT>;
+    constexpr int kMmaWarp = C::kMmaWarp, kLoadWarp = C::kLoadWarp, kCleanWarp0 = C::kCleanWarp0, kQ = C::kQ;
     extern __shared__ __align__(1024) uint8_t smraw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(sm);
@@ -124,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.q)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.v)) : "memory");
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NT; ++i) {
             mbar_init(bar(B_Q + i), 1);
             mbar_init(bar(B_S + i), 1);
             mbar_init(bar(B_P + i), 4);
@@ -140,28 +155,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         abort_sm = 0;
         odd_sm = 0;
     }
-    if (warp == kMmaWarp) tmem_alloc<512>(smem_u32(&tmem_base));
+    if (warp == kMmaWarp) tmem_alloc<C::kTmem>(smem_u32(&tmem_base));
     const int h = blockIdx.x % (unsigned)a.Hq;
     TilePos at;
-    const bool live = find_tile<kThreads, kQ>(a, (int)(blockIdx.x / (unsigned)a.Hq), &at);
+    const bool live = find_tile<C::kThreads, kQ>(a, (int)(blockIdx.x / (unsigned)a.Hq), &at);
     if (at.bad) atomicOr(&g_status, (int)LOLA_ATTN_BAD_OFFSETS);
     if (!live) {
         if (warp == kMmaWarp) {
             __syncwarp();
-            tmem_dealloc<512>(*reinterpret_cast<volatile uint32_t*>(&tmem_base));
+            tmem_dealloc<C::kTmem>(*reinterpret_cast<volatile uint32_t*>(&tmem_base));
         }
         return;
     }
     const int q0 = at.q0, lq = at.lq, k0 = at.k0, lk = at.lk, r0 = at.tile * kQ, shift = lk - lq;
     // blocks that tile i reads, and those that all its rows see whole
-    int nb[2], nf = 0x7fffffff;
+    int nb[NT], nf = 0x7fffffff, nmax = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NT; ++i) {
         const int first = r0 + kM * i, last = min(first + kM, lq) - 1;      // the tile's rows
         nb[i] = first < lq ? (max(0, min(lk, last + shift + 1)) + kN - 1) / kN : 0;
         if (nb[i] > 0) nf = min(nf, max(0, min(lk, first + shift + 1)) / kN);
+        nmax = max(nmax, nb[i]);
     }
-    const int nmax = max(nb[0], nb[1]);
 
     fence_before();
     __syncthreads();
@@ -195,10 +210,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     auto stage = [&](int x) { return x % C::kStages; };
     auto pair = [&](int p) { return p & (kPairs - 1); };
     auto phase = [&](int p) { return (uint32_t)(p / kPairs) & 1u; };
-    auto ring = [&](int x) { return sb + (uint32_t)(2 + stage(x)) * C::kTileBytes; };
+    auto ring = [&](int x) { return sb + (uint32_t)(NT + stage(x)) * C::kTileBytes; };
 
     if (warp >= kMmaWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        // (what the block was launched with, 168 or 128 a thread, given out anew)
+        if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == kLoadWarp) {
             // ================================ loader ================================
             if (lane == 0 && nmax > 0) {
@@ -225,11 +242,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     for (int n = max(0, 2 * p - 1); n <= last; ++n)
                         for (int x = 0; x < D / 64; ++x)
                             tma_load3(ring(n) + 16384u * x, n & 1 ? &maps.v : &maps.k, 64 * x, hk, k0 + (n >> 1) * kN, bar(full));
-                    if (p == 0 && nb[1] > 0) load(&maps.q, q0 + r0 + kM, h, sb + C::kTileBytes, B_Q + 1);
+                    if (NT == 2 && p == 0 && nb[NT - 1] > 0) load(&maps.q, q0 + r0 + kM, h, sb + C::kTileBytes, B_Q + 1);
                 }
                 // leave no copy in flight
                 for (int x = max(0, p - kPairs); x < p; ++x) mbar_wait(bar(B_FULL + pair(x)), phase(x), kWaitNs);
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < NT; ++i)
                     if (nb[i] > 0) mbar_wait(bar(B_Q + i), 0, kWaitNs);
             }
         } else if (warp == kMmaWarp) {
@@ -247,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     mma_commit(bar(B_S + i));
                 };
                 bool ok = wait(B_FULL, 0);
-                for (int i = 0; i < 2 && ok; ++i)
+                for (int i = 0; i < NT && ok; ++i)
                     if (nb[i] > 0) {
                         ok = wait(B_Q + i, 0);
                         fence_after();
@@ -259,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     ok = wait(B_FULL + pair(j + 1), phase(j + 1));
                     if (ok && j >= nf) ok = wait(B_CLEAN + pair(j + 1), (uint32_t)((j - nf) / kPairs) & 1u);
                     const uint32_t v = desc_lo(ring(2 * j + 1), 16384);
-                    for (int i = 0; i < 2 && ok; ++i) {
+                    for (int i = 0; i < NT && ok; ++i) {
                         if (j < nb[i]) {
                             if (!(ok = wait(B_P + i, (uint32_t)j & 1u))) break;
                             fence_after();
@@ -286,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 ok = wait(B_ARMED + pair(j + 1), (uint32_t)((j - nf) / kPairs) & 1u) && wait(B_FULL + pair(j + 1), phase(j + 1));
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                uint8_t* v = sm + (size_t)(2 + stage(2 * j + 1)) * C::kTileBytes;
+                uint8_t* v = sm + (size_t)(NT + stage(2 * j + 1)) * C::kTileBytes;
                 const int valid = min(kN, lk - j * kN);
                 // 16-byte chunks in memory order, eight in flight; a bfloat16 is not finite iff adding 1
                 // to its exponent carries into the sign
@@ -330,7 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         }
     } else {
         // ================================ softmax ================================
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         const int i = warp >> 2, row = r0 + kM * i + (warp & 3) * 32 + lane;    // (may lie behind the sequence)
         const uint32_t lo = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tb + lo + C::TS(i), to = tb + lo + C::TO(i);
@@ -467,15 +485,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     __syncthreads();
     fence_after();
     if (abort_sm && tid == 0) atomicOr(&g_status, (int)LOLA_ATTN_TIMEOUT);
-    if (warp == kMmaWarp) tmem_dealloc<512>(tb);
+    if (warp == kMmaWarp) tmem_dealloc<C::kTmem>(tb);
 }
 
 bool make_map(CUtensorMap* m, const Rows& r, int64_t rows, int heads, int d) {
     return make_tmap_rows(m, r.data, rows, heads, d, r.row, r.head, kM);
 }
 
-template <int D>
+template <int D, int NT>
 cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
+    using C = Cfg<D, NT>;
     Maps maps;
     const int Hkv = a.Hq / a.G;
     const int64_t rows_k = a.total_k > 0 ? a.total_k : 1;
@@ -483,16 +502,41 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
         !make_map(&maps.v, a.V, rows_k, Hkv, D))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = opt_in_smem(attn_tc_kernel<D>, Cfg<D>::kSmem, done);
+    cudaError_t e = opt_in_smem(attn_tc_kernel<D, NT>, C::kSmem, done);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = ((int64_t)a.total_q + (int64_t)a.n_seq * (kQ - 1)) / kQ;
-    attn_tc_kernel<D><<<(unsigned)(tiles * a.Hq), kThreads, Cfg<D>::kSmem, st>>>(maps, a);
+    // at most this many tiles for any cut of total_q rows into n_seq sequences
+    const int64_t tiles = ((int64_t)a.total_q + (int64_t)a.n_seq * (C::kQ - 1)) / C::kQ;
+    attn_tc_kernel<D, NT><<<(unsigned)(tiles * a.Hq), C::kThreads, C::kSmem, st>>>(maps, a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t st) { return a.d == 128 ? launch<128>(a, st) : launch<64>(a, st); }
+// One or two tiles per CTA?  A CTA costs about o + s B microseconds, B the key blocks its tiles read on
+// average: measured on prompts of 128 to 8192 tokens, 8 heads (us; two tiles: a round of 152 CTAs, one
+// tile: a round of 304, two on an SM),
+//            d = 128, two: 9.7 + 1.47 B   one: 8.3 + 1.94 B      d = 64, two: 8.0 + 1.19 B   one: 6.5 + 1.32 B
+// so one tile for short sequences (304 of 128 tokens, d = 128: 90 against 136 us; 19 of 4096: 645 against
+// 545), and where its finer cut saves a round (10 tiles of ~50 blocks, 16 heads, d = 64: 84 against
+// 126 us).  The tiles of a ragged batch are not known here: half a tile is added for each sequence, or
+// what the grid may come to where the rounds are few and a tile more can cost a whole one.
+static bool one_tile(const AttnArgs& a) {
+    const double n = a.n_seq, lq = a.total_q / n, lk = a.total_k / n;
+    const double blocks = (lk > lq ? lk - lq / 2 : lk / 2) / kN + 0.5;
+    auto cost = [&](int nt, double o, double s) {
+        const double q = nt * kM, slots = nt == 2 ? 152 : 304;
+        const double most = (double)(((int64_t)a.total_q + (int64_t)a.n_seq * (int64_t)(q - 1)) / (int64_t)q) * a.Hq / slots;
+        const double mean = (a.total_q / q + 0.5 * n) * a.Hq / slots;
+        return (most <= 4 ? std::ceil(most) : std::ceil(mean)) * (o + s * blocks);
+    };
+    return a.d == 128 ? cost(1, 8.3, 1.94) < 0.95 * cost(2, 9.7, 1.47) : cost(1, 6.5, 1.32) < 0.95 * cost(2, 8.0, 1.19);
+}
+
+cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t st) {
+    const bool one = one_tile(a);
+    if (a.d == 128) return one ? launch<128, 1>(a, st) : launch<128, 2>(a, st);
+    return one ? launch<64, 1>(a, st) : launch<64, 2>(a, st);
+}
 
 cudaError_t attn_tc_status_take(int32_t* bits, cudaStream_t st) { return take_word(g_status, bits, st); }
 

@@ -164,6 +164,35 @@ def test_prefill_values_that_are_not_finite_reach_only_who_sees_them(L, gen, dty
     assert bool(torch.isfinite(out[:130][first[:130]]).all())
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_short_sequences_beside_a_long_one(L, gen, d):
+    """A long sequence makes the whole call take two query tiles per CTA: the short ones' edges (lengths
+    around the tiles, pieces with earlier keys, rows that see nothing, values that are not finite,
+    rows of a wider tensor, rows outside the sequences) under that form."""
+    lq = [20000, 512, 384, 1, 640, 257, 0, 130, 100, 3]
+    lk = [20000, 512, 384, 700, 640, 300, 5, 129, 60, 0]
+    Hq, Hkv, nq, nk = 16, 4, sum(lq) + 40, sum(lk) + 40
+    rows = randn(gen, nq, Hq + 3, d, dtype=BF)
+    q = rows[:, 2:2 + Hq]
+    k, v = randn(gen, nk, Hkv, d, dtype=BF), randn(gen, nk, Hkv, d, dtype=BF)
+    for t, used in ((rows, sum(lq)), (k, sum(lk)), (v, sum(lk))):
+        t[:17] = math.nan
+        t[17 + used:] = math.nan
+    a = 17 + 20000                                              # the sequence of 512
+    v[a + 130, 0, 3], v[a + 255, 1, 4], v[a + 300, 2, 5] = math.inf, math.nan, -math.inf
+    b = a + 512 + 384 + 700                                     # ... of 640
+    v[b + 5, 3, 0], v[b + 639, 0] = math.nan, math.nan
+    out = torch.full((nq, Hq, d), 5.0, dtype=BF, device="cuda")
+    lse = torch.full((Hq, nq), 5.0, dtype=F32, device="cuda")
+    L.ExactAttention(Hq, Hkv, d).prefill(q, k, v, offsets(lq, 17), offsets(lk, 17), out=out, lse=lse)
+    quiet(L)
+    check_prefill(q, k, v, lq, lk, out, lse, start=17, start_k=17, heads=[0, 5, 10, 15],
+                  rows=[0, 1, 2, 60, 99, 127, 128, 129, 130, 131, 254, 255, 256, 257, 300, 301, 383, 511, 512, 638, 639,
+                        10000, 19967, 19968, 19999])
+    for t in (out[:17], out[17 + sum(lq):], lse[:, :17], lse[:, 17 + sum(lq):]):
+        assert bool((t == 5).all())
+
+
 def test_prefill_offsets_past_32_bits(L, gen):
     """Rows so far apart that element offsets pass 2^31."""
     n, d, apart = 700, 128, 3_200_000
