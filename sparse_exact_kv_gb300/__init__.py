@@ -346,6 +346,14 @@ def _addr(t):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+def _index_of(dev):
+    """The index of ``dev``, which has to be the current CUDA device."""
+    i = dev.index
+    if i is None or dev.type != "cuda" or i != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors are on {dev}, not on the current CUDA device")
+    return i
+
+
 def _stream_of(stream, index):
     """The cudaStream_t of ``stream``; None: torch's current stream of device ``index`` (looked up
     without making a Stream object, 3 us a call)."""
@@ -478,10 +486,13 @@ class ExactAttention:
         with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream):
             return torch.empty(shape, dtype=dtype, device=dev)
 
-    @staticmethod
-    def _current(dev):
-        if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-            raise ValueError(f"tensors are on {dev}, not on the current CUDA device")
+    def _like(self, q, stream):
+        """A fresh output of q's shape, and its lola_rows."""
+        if stream is None:
+            out = torch.empty_like(q)            # (a third of the time of torch.empty)
+        else:
+            out = self._empty(q.shape, q.dtype, q.device, stream)
+        return out, _rows(out)
 
     def prefill(self, q, k, v, cu_q, cu_k=None, out=None, lse=None, stream=None):
         """Causal attention over packed prompts: q [total_q, Hq, d], k, v [total_k, Hkv, d] (any row
@@ -499,12 +510,11 @@ class ExactAttention:
             self._lse(lse, (self.Hq, n), dev)
         if out is not None:
             ro = self._heads(out, self.Hq, n, dev, "out")
-        self._current(dev)
+        index = _index_of(dev)
         if out is None:
-            out = self._empty((n, self.Hq, self.d), self.dtype, dev, stream)
-            ro = lola_rows(out.data_ptr(), self.Hq * self.d, self.d)
+            out, ro = self._like(q, stream)
         st = _lib.lola_attn_prefill(self.cfg, n1 - 1, n, m, cu_q.data_ptr(), _addr(cu_k), rq, rk, rv, ro, _addr(lse),
-                                    _stream_of(stream, dev.index))
+                                    _stream_of(stream, index))
         if st:
             raise LolaError(st, "lola_attn_prefill")
         return out
@@ -517,10 +527,9 @@ class ExactAttention:
         self._vector(kv_len, n, dev, "kv_len")
         if table.dtype != torch.int32 or table.device != dev or (one != 1 and width != 1):
             raise ValueError(f"table: want int32 [{n}, width] on {dev}, rows contiguous")
-        self._current(dev)
         pages, _, page, _ = pool.shape
         return lola_paged_kv(pool.data_ptr(), self.v_pool.data_ptr(), pages, page, n, width,
-                             stride if stride > width else width, table.data_ptr(), kv_len.data_ptr()), dev, n
+                             stride if stride > width else width, table.data_ptr(), kv_len.data_ptr()), dev, n, _index_of(dev)
 
     def append(self, k, v, kv_len, table, cu_new=None, q=None, inv_freq=None, q_out=None, pairs="halves",
                positions=None, stream=None):
@@ -531,7 +540,7 @@ class ExactAttention:
         float32 [rot / 2] radians per position (None: no rotation); ``pairs`` the channel pairs of
         the rotation, "halves" or "neighbours"; ``positions`` int32 [n] in place of the tokens'
         indexes.  ``q_out`` may be q itself."""
-        kv, dev, n_seq = self._cache(kv_len, table)
+        kv, dev, n_seq, index = self._cache(kv_len, table)
         n = k.shape[0]
         rk = self._heads(k, self.Hkv, n, dev, "k")
         rv = self._heads(v, self.Hkv, n, dev, "v")
@@ -550,12 +559,11 @@ class ExactAttention:
             if q_out is not None:
                 ro = self._heads(q_out, self.Hq, n, dev, "q_out")
             else:
-                q_out = self._empty((n, self.Hq, self.d), self.dtype, dev, stream)
-                ro = lola_rows(q_out.data_ptr(), self.Hq * self.d, self.d)
+                q_out, ro = self._like(q, stream)
         elif q_out is not None:
             raise ValueError("q_out without q")
         st = _lib.lola_paged_append(self.cfg, kv, n, _addr(cu_new), rk, rv, rq, ro, freq, rot, PAIRS[pairs],
-                                    _addr(positions), _stream_of(stream, dev.index))
+                                    _addr(positions), _stream_of(stream, index))
         if st:
             raise LolaError(st, "lola_paged_append")
         return q_out
@@ -564,15 +572,14 @@ class ExactAttention:
         """One query token per sequence, q [n_seq, Hq, d], over its kv_len cached tokens; returns out
         [n_seq, Hq, d].  ``lse`` float32 [n_seq, Hq].  ``workspace``: a buffer of
         lola_paged_decode_workspace_bytes; by default one is allocated for the call."""
-        kv, dev, n = self._cache(kv_len, table)
+        kv, dev, n, index = self._cache(kv_len, table)
         rq = self._heads(q, self.Hq, n, dev, "q")
         if lse is not None:
             self._lse(lse, (n, self.Hq), dev)
         if out is not None:
             ro = self._heads(out, self.Hq, n, dev, "out")
         else:
-            out = self._empty((n, self.Hq, self.d), self.dtype, dev, stream)
-            ro = lola_rows(out.data_ptr(), self.Hq * self.d, self.d)
+            out, ro = self._like(q, stream)
         size = self._ws
         if workspace is None:
             workspace = self._empty(size, torch.uint8, dev, stream)
@@ -581,7 +588,7 @@ class ExactAttention:
             if workspace.device != dev or not workspace.is_contiguous():
                 raise ValueError(f"workspace: want a contiguous buffer on {dev}")
         st = _lib.lola_paged_decode(self.cfg, kv, rq, ro, _addr(lse), workspace.data_ptr(), size,
-                                    _stream_of(stream, dev.index))
+                                    _stream_of(stream, index))
         if st:
             raise LolaError(st, "lola_paged_decode")
         return out

@@ -16,7 +16,7 @@ namespace {
 
 __device__ int32_t g_status;
 
-constexpr int kNT = 128;
+constexpr int kFew = 1024;   // tokens up to which a CTA takes one
 
 // the sequence that row t belongs to, one warp: the last b with cu[b] <= t, found 32 offsets at a
 // time; -1 if none
@@ -59,52 +59,65 @@ template <> __device__ __forceinline__ uint4 pack<__nv_bfloat16>(const float (&v
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One unit of work: 2 x 16 bytes of one head of one token.
-//   u < rot_units        rotated chunk pair
-//   then                 copied 32-byte chunks (channels from rot on)
-template <typename T, int D>
-__device__ __forceinline__ void move_unit(const T* src, T* dst, int u, int rot, bool neighbours, const float2* cs) {
+// One unit of work: 2 x 16 bytes of one head of one token -- a chunk of a rotated pair's first channels and
+// the one of its second channels, or (from channel `rot` on) 32 bytes to copy.
+template <typename T> struct Unit {
+    const float4* cs;    // the unit's first two (cos, sin) pairs; null: copied
+    T* dst;              // null: nothing to do
+    int c0, c1;          // channels of the two chunks
+    uint4 x, y;
+};
+// cs: float4 (i, u) at i * units + u holds pairs 2 i and 2 i + 1 of unit u, so that the lanes of a warp,
+// whose units follow each other, read side by side
+template <typename T>
+__device__ __forceinline__ void load_unit(Unit<T>& n, const T* src, T* dst, int u, int rot, bool neighbours, const float4* cs) {
     constexpr int VN = 16 / sizeof(T);
     const int ru = rot / (2 * VN);
-    if (u >= ru) {
-        const int c = rot + (u - ru) * 2 * VN;
-        const uint4 x = *reinterpret_cast<const uint4*>(src + c), y = *reinterpret_cast<const uint4*>(src + c + VN);
-        *reinterpret_cast<uint4*>(dst + c) = x;
-        *reinterpret_cast<uint4*>(dst + c + VN) = y;
-        return;
-    }
-    const int c0 = neighbours ? u * 2 * VN : u * VN, c1 = neighbours ? c0 + VN : c0 + rot / 2;
-    const uint4 x = *reinterpret_cast<const uint4*>(src + c0), y = *reinterpret_cast<const uint4*>(src + c1);
-    float a[VN], b[VN];
-    unpack<T>(x, a);
-    unpack<T>(y, b);
-    if (neighbours) {
-        // 2 VN consecutive channels: pairs u VN .. u VN + VN - 1
+    const bool turn = u < ru;
+    n.c0 = turn && !neighbours ? u * VN : u * 2 * VN;      // (copied: rot + 2 VN (u - ru) = 2 VN u)
+    n.c1 = turn && !neighbours ? n.c0 + rot / 2 : n.c0 + VN;
+    n.cs = turn ? cs + u : nullptr;
+    n.dst = dst;
+    n.x = *reinterpret_cast<const uint4*>(src + n.c0);
+    n.y = *reinterpret_cast<const uint4*>(src + n.c1);
+}
+template <typename T>
+__device__ __forceinline__ void finish_unit(Unit<T>& n, bool neighbours, int step) {
+    constexpr int VN = 16 / sizeof(T);
+    if (n.cs) {
+        float a[VN], b[VN];
+        unpack<T>(n.x, a);
+        unpack<T>(n.y, b);
 #pragma unroll
-        for (int i = 0; i < VN; i += 2) {
-            const float2 s = cs[u * VN + i / 2], t = cs[u * VN + VN / 2 + i / 2];
-            const float a0 = a[i], b0 = b[i];
-            a[i] = a0 * s.x - a[i + 1] * s.y;
-            a[i + 1] = a[i + 1] * s.x + a0 * s.y;
-            b[i] = b0 * t.x - b[i + 1] * t.y;
-            b[i + 1] = b[i + 1] * t.x + b0 * t.y;
+        for (int i = 0; i < VN / 2; ++i) {
+            const float4 c = n.cs[i * step];
+            // pairs 2 i and 2 i + 1: neighbours in the 2 VN channels, or element 2 i (+ 1) of either chunk
+            auto turn = [](float& x, float& y, float co, float si) {
+                const float x0 = x;
+                x = x0 * co - y * si;
+                y = y * co + x0 * si;
+            };
+            if (neighbours) {
+                float(&z)[VN] = 4 * i < VN ? a : b;
+                turn(z[4 * i % VN], z[4 * i % VN + 1], c.x, c.y);
+                turn(z[4 * i % VN + 2], z[4 * i % VN + 3], c.z, c.w);
+            } else {
+                turn(a[2 * i], b[2 * i], c.x, c.y);
+                turn(a[2 * i + 1], b[2 * i + 1], c.z, c.w);
+            }
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < VN; ++i) {
-            const float2 s = cs[u * VN + i];
-            const float a0 = a[i];
-            a[i] = a0 * s.x - b[i] * s.y;
-            b[i] = b[i] * s.x + a0 * s.y;
-        }
+        n.x = pack<T>(a);
+        n.y = pack<T>(b);
     }
-    *reinterpret_cast<uint4*>(dst + c0) = pack<T>(a);
-    *reinterpret_cast<uint4*>(dst + c1) = pack<T>(b);
+    *reinterpret_cast<uint4*>(n.dst + n.c0) = n.x;
+    *reinterpret_cast<uint4*>(n.dst + n.c1) = n.y;
 }
 
-template <typename T, int D, int TOK>
-__global__ void __launch_bounds__(kNT) paged_append_kernel(const AppendArgs a) {
-    __shared__ float2 cs[TOK][D / 2];
+// TOK tokens a CTA of NT threads; a thread has IN units in flight.
+template <typename T, int D, int TOK, int NT, int IN>
+__global__ void __launch_bounds__(NT) paged_append_kernel(const AppendArgs a) {
+    __shared__ __align__(16) float4 cs[TOK][D / 4];
+    __shared__ uint64_t turn_sm[D / 2];
     __shared__ int64_t slot[TOK];      // element offset of (page, head 0, slot), -1: no slot, -2: skip the row
     __shared__ int pos_sm[TOK];
     constexpr int VN = 16 / sizeof(T), UH = D / (2 * VN);   // units per head
@@ -112,14 +125,13 @@ __global__ void __launch_bounds__(kNT) paged_append_kernel(const AppendArgs a) {
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
     const PagedArgs& p = a.p;
 
-    for (int i = warp; i < nt; i += kNT / kWarp) {
+    for (int i = warp; i < nt; i += NT / kWarp) {
         const int t = t0 + i;
         int b = t;
         int64_t pos;
         if (a.cu_new) {
             b = warp_find_seq(a.cu_new, p.n_seq, t, lane);
             pos = b < 0 ? -1 : (int64_t)p.kv_len[b] - a.cu_new[b + 1] + t;
-            if (b >= 0 && t < a.cu_new[b]) pos = -1;          // (offsets that are not sorted)
         } else {
             pos = (int64_t)p.kv_len[b] - 1;
         }
@@ -135,42 +147,61 @@ __global__ void __launch_bounds__(kNT) paged_append_kernel(const AppendArgs a) {
         }
     }
     const int rot = a.inv_freq ? a.rot : 0;
-    __syncthreads();
-    for (int e = threadIdx.x; e < nt * (rot / 2); e += kNT) {
-        const int i = e / (rot / 2), f = e % (rot / 2);
+    // the turn of one position, by the last warps (the first ones look the tokens up)
+    for (int f = NT - 1 - (int)threadIdx.x; f < rot / 2; f += NT) {
         double turns = (double)a.inv_freq[f] * 0.15915494309189535;    // w / 2 pi
         turns -= floor(turns);
-        const uint64_t w = (uint64_t)(turns * 18446744073709551616.0);   // fraction of a turn, 2^-64
-        const uint64_t x = w * (uint64_t)(int64_t)pos_sm[i];             // modulo one turn
-        float s, c;
-        sincospif((float)(int32_t)(uint32_t)(x >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns
-        cs[i][f] = make_float2(c, s);
+        turn_sm[f] = (uint64_t)(turns * 18446744073709551616.0);         // fraction of a turn, 2^-64
     }
     __syncthreads();
-    const int hq = a.Q.data ? p.Hq : 0, heads = hq + 2 * p.Hkv;
+    const int ru = rot / (2 * VN);
+    for (int e = threadIdx.x; e < nt * (rot / 2); e += NT) {
+        const int i = TOK == 1 ? 0 : e / (rot / 2), f = e - i * (rot / 2);
+        const uint64_t x = turn_sm[f] * (uint64_t)(int64_t)pos_sm[i];    // modulo one turn
+        float s, c;
+        sincospif((float)(int32_t)(uint32_t)(x >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns
+        reinterpret_cast<float2*>(cs[i])[((f % VN / 2) * ru + f / VN) * 2 + (f & 1)] = make_float2(c, s);
+    }
+    __syncthreads();
+    const int hq = a.Q.data ? p.Hq : 0, heads = hq + 2 * p.Hkv, units = nt * heads * UH;
     const bool nb = a.pairs == LOLA_PAIRS_NEIGHBOURS;
-    for (int e = threadIdx.x; e < nt * heads * UH; e += kNT) {
-        const int u = e % UH, h = (e / UH) % heads, i = e / (UH * heads);
-        const int64_t t = t0 + i, s = slot[i];
-        if (s == -2 || (s < 0 && h >= hq)) continue;
-        if (h < hq) {
-            move_unit<T, D>(reinterpret_cast<const T*>(a.Q.data) + t * a.Q.row + h * a.Q.head,
-                            reinterpret_cast<T*>(a.QO.data) + t * a.QO.row + h * a.QO.head, u, rot, nb, cs[i]);
-        } else if (h < hq + p.Hkv) {
-            const int hk = h - hq;
-            move_unit<T, D>(reinterpret_cast<const T*>(a.K.data) + t * a.K.row + hk * a.K.head,
-                            reinterpret_cast<T*>(p.K) + s + (int64_t)hk * p.page * D, u, rot, nb, cs[i]);
-        } else {
-            const int hk = h - hq - p.Hkv;
-            move_unit<T, D>(reinterpret_cast<const T*>(a.V.data) + t * a.V.row + hk * a.V.head,
-                            reinterpret_cast<T*>(p.V) + s + (int64_t)hk * p.page * D, u, 0, nb, cs[i]);
+    for (int e0 = threadIdx.x; e0 < units; e0 += NT * IN) {
+        Unit<T> n[IN];
+#pragma unroll
+        for (int x = 0; x < IN; ++x) {
+            const int e = e0 + x * NT;
+            n[x].dst = nullptr;
+            if (e >= units) continue;
+            const int u = e % UH, th = e / UH;
+            int i = 0;                           // th / heads
+#pragma unroll
+            for (int z = 1; z < TOK; ++z) i += th >= z * heads;
+            const int h = th - i * heads;
+            const int64_t t = t0 + i, s = slot[i];
+            if (s == -2 || (s < 0 && h >= hq)) continue;
+            if (h < hq) {
+                load_unit<T>(n[x], reinterpret_cast<const T*>(a.Q.data) + t * a.Q.row + h * a.Q.head,
+                             reinterpret_cast<T*>(a.QO.data) + t * a.QO.row + h * a.QO.head, u, rot, nb, cs[i]);
+            } else {
+                const bool v = h >= hq + p.Hkv;
+                const int hk = h - hq - (v ? p.Hkv : 0);
+                const Rows& r = v ? a.V : a.K;
+                load_unit<T>(n[x], reinterpret_cast<const T*>(r.data) + t * r.row + hk * r.head,
+                             reinterpret_cast<T*>(v ? p.V : p.K) + s + (int64_t)hk * p.page * D, u, v ? 0 : rot, nb, cs[i]);
+            }
         }
+#pragma unroll
+        for (int x = 0; x < IN; ++x)
+            if (n[x].dst) finish_unit<T>(n[x], nb, ru);
     }
 }
 
+// Few tokens: one a CTA, so that none waits for another's page lookup; many: four, whose rows of a head
+// lie side by side in the page.
 template <typename T, int D>
 cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
-    paged_append_kernel<T, D, 1><<<a.n_tokens, kNT, 0, st>>>(a);
+    if (a.n_tokens <= kFew) paged_append_kernel<T, D, 1, 128, 3><<<a.n_tokens, 128, 0, st>>>(a);
+    else paged_append_kernel<T, D, 4, 256, 3><<<(a.n_tokens + 3) / 4, 256, 0, st>>>(a);
     return cudaGetLastError();
 }
 
