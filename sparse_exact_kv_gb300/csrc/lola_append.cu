@@ -16,7 +16,7 @@ namespace {
 
 __device__ int32_t g_status;
 
-constexpr int kFew = 1024;   // tokens up to which a CTA takes one
+constexpr int kFew = 512;   // tokens up to which a CTA takes one
 
 // the sequence that row t belongs to, one warp: the last b with cu[b] <= t, found 32 offsets at a
 // time; -1 if none
