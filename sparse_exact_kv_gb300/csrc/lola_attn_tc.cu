@@ -6,28 +6,33 @@
 // m is raised lazily: O and l are rescaled (in TMEM) only when a block's maximum passes m by more
 // than 2^8, so that P and l stay far inside float32 and bfloat16, and blocks rarely wait for O.
 //
-// A CTA takes 256 queries of one head as two tiles of 128 (MMA M = 128, TMEM lane = query) that share
-// every K and V block; while the tensor core works for one tile, the other tile's softmax runs.  Short
-// sequences take one tile per CTA and two CTAs per SM instead, each in half an SM (see one_tile below).
-// Warps (of two tiles):
+// An item is 256 queries of one head, two tiles of 128 (MMA M = 128, TMEM lane = query) that share every
+// K and V block; while the tensor core works for one tile, the other tile's softmax runs.  Short
+// sequences take one tile an item and two CTAs per SM instead, each in half an SM (see one_tile below).
+// A CTA goes from item to item, taking over blocks of the grid that have not started (cluster launch
+// control), so that an item's lookup, first loads and last stores run beside its neighbours' products;
+// barrier phases, ring places and tile counts run on over the items.  Warps (of two tiles):
+//   * 11 (items): the next block, its sequence and tile, published one item ahead;
 //   * 9 (loader): Q, K and V tiles by TMA, 128-byte swizzle, into a ring of K and V blocks;
 //   * 8 (MMA, one thread): per block and tile O_i += P_i V_j, then S_i = Q_i K_{j+1}^T.  P_i
 //     (bf16, read from TMEM as the A operand) lies over S_i's columns: the products of one thread
 //     run in order, so S_i of the next block cannot overtake the read of P_i;
 //   * 0-3, 4-7 (softmax of tile 0, 1; one thread per query): the row of S into registers,
-//     mask on the blocks that some row does not see whole, maximum, weights, P into TMEM;
-//   * 10-11 (cleaners): on those same blocks, V rows behind the sequence and values that are
-//     not finite are zeroed in shared memory before the product (0 x NaN would reach rows
-//     that do not see them); the values taken out are added back in the epilogue, for the rows
-//     that see them.
+//     mask on the blocks that some row does not see whole, maximum, weights, P into TMEM, and at the
+//     end the rows of o;
+//   * 10 (cleaner): on those same blocks, V rows behind the sequence and values that are not finite
+//     are zeroed in shared memory before the product (0 x NaN would reach rows that do not see
+//     them); the values taken out are added back in the epilogue, for the rows that see them.
 // What bounds it: for long sequences the tensor core and its power (16 heads of 32768 tokens, d = 128:
-// 2.96 ms, 1483 TFLOP/s of the measured 1849); a block pair's products take about 2300 cycles of the
-// issuing thread's 2900-3200, the rest is its wait for the weights (a softmax is 1100 cycles, behind it
-// the other tile's products).  For short ones the start and end of a CTA: about 2200 cycles of tile
-// lookup, 3500 until the first scores, 2500 of epilogue.
+// 2.73 ms, 1608 TFLOP/s, 87 % of the measured bf16 product; 4 x 4096 x 32 heads 417 us, 1318 TFLOP/s): a
+// block pair's products take about 2300 cycles of the issuing thread's 2700, the rest is its wait for
+// the weights (a softmax is 1100 cycles, behind it the other tile's products).  At d = 64 the
+// exponentials weigh twice as much against the products (1037 TFLOP/s); short sequences are bound by an
+// item's own chain: scores, weights, product, epilogue.
 // Tried and slower: releasing P in halves, comparing S by column groups while it loads, one MMA thread
-// for each tile (their products interleave: 3.20 ms), the next pair's waits between the products.
-// Every wait is bounded (1 s, then LOLA_ATTN_TIMEOUT).
+// for each tile (their products interleave, 9 %), the next pair's waits between the products, and one
+// block per CTA without taking over others (4 x 4096 x 32 heads 457 us, ragged prompts 362 against 335).
+// Every wait is bounded (1 s, those that may last a whole item 10 s, then LOLA_ATTN_TIMEOUT).
 #include <cuda.h>
 
 #include <cmath>
@@ -44,19 +49,21 @@ __device__ int32_t g_status;
 
 constexpr int kM = 128;                  // queries per tile
 constexpr int kN = 128;                  // keys per block
-constexpr int kPairs = 4;                // barriers of the pairs (see the kernel)
+constexpr int kClean = 4;                // barriers of the blocks to be cleaned
 constexpr float kRaise = 8.0f;           // m is raised when a block's maximum passes it by this (log2)
 constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr uint64_t kItemNs = 10000000000ull;   // ... of the waits that may last a whole item
 
 // NT: query tiles of a CTA.  Two: one CTA per SM, K and V blocks shared by 256 queries.  One: two CTAs
 // per SM, each with its own ring (half the shared memory, half of TMEM).
 template <int D, int NT> struct Cfg {
-    static constexpr int kQ = NT * kM;                     // queries per CTA
+    static constexpr int kQ = NT * kM;                     // queries per item
     static constexpr int kThreads = (NT + 1) * 128;
-    static constexpr int kMmaWarp = 4 * NT, kLoadWarp = kMmaWarp + 1, kCleanWarp0 = kMmaWarp + 2;
+    static constexpr int kMmaWarp = 4 * NT, kLoadWarp = kMmaWarp + 1, kItemWarp = kMmaWarp + 3;   // (kMmaWarp + 2: the cleaner)
     static constexpr int kTileBytes = kM * D * 2;          // a Q tile, a K block or a V block
-    static constexpr int kStages = NT == 2 ? (D == 128 ? 5 : 8) : (D == 128 ? 2 : 5);   // K and V blocks in the ring
-    static constexpr int kSmem = (NT + kStages) * kTileBytes + 1024;
+    static constexpr int kCap = NT == 2 ? (D == 128 ? 2 : 4) : (D == 128 ? 1 : 2);      // pairs in the ring
+    static constexpr int kStageBytes = kM * 64;            // 32 columns of a tile's output
+    static constexpr int kSmem = (NT + 2 * kCap) * kTileBytes + NT * kStageBytes + 1024;
     static constexpr int kTmem = 256 * NT;                 // columns
     __device__ static constexpr uint32_t TS(int i) { return 128u * i; }            // S (P over its first half)
     __device__ static constexpr uint32_t TO(int i) { return 128u * NT + (uint32_t)D * i; }
@@ -118,20 +125,111 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return o;
 }
 
+// One item: a query tile (or two) of one head.
+struct Item {
+    int q0, lq, k0, lk, r0, h, live;
+};
+// The blocks of 128 keys that its tiles read (nb, the most of them nmax) and those that all its rows see
+// whole (nf).
+template <int NT> struct Span {
+    int nb[NT], nmax, nf;
+    __device__ __forceinline__ explicit Span(const Item& t) {
+        nmax = 0;
+        nf = 0x7fffffff;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const int first = t.r0 + kM * i, last = min(first + kM, t.lq) - 1, shift = t.lk - t.lq;   // the tile's rows
+            nb[i] = first < t.lq ? (max(0, min(t.lk, last + shift + 1)) + kN - 1) / kN : 0;
+            if (nb[i] > 0) nf = min(nf, max(0, min(t.lk, first + shift + 1)) / kN);
+            nmax = max(nmax, nb[i]);
+        }
+    }
+};
+
+// Query tiles of ROWS rows, found by one warp: the sequences' tiles are counted in order and taken
+// backwards (a sequence's longest tiles first, the first sequence's shortest ones at the very end), 32
+// sequences in the lanes at a time.
+template <int ROWS> struct Finder {
+    int q0, lq, k0, lk;      // this lane's sequence of the 32 from cb on
+    int cb, own, inc;        // ... its tiles, and the tiles up to it in the lanes
+    int before, total;       // tiles before cb, tiles of all
+    bool bad;
+
+    __device__ __forceinline__ int look(const AttnArgs& a, int b) {
+        q0 = lq = k0 = lk = 0;
+        if (b < 0 || b >= a.n_seq) return 0;
+        seq_rows(a.cu_q, b, a.total_q, &q0, &lq, &bad);
+        seq_rows(a.cu_k, b, a.total_k, &k0, &lk, &bad);
+        return (lq + ROWS - 1) / ROWS;
+    }
+    __device__ __forceinline__ void chunk(const AttnArgs& a, int lane) {
+        own = inc = look(a, cb + lane);
+#pragma unroll
+        for (int o = 1; o < kWarp; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+    }
+    __device__ __forceinline__ void start(const AttnArgs& a, int lane) {
+        bad = false;
+        before = 0;
+        cb = (a.n_seq - 1) / kWarp * kWarp;
+        for (int b = 0; b < cb; b += kWarp) before += look(a, b + lane);
+        before = __reduce_add_sync(0xffffffffu, before);
+        chunk(a, lane);
+        total = before + __shfl_sync(0xffffffffu, inc, 31);
+        if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) atomicOr(&g_status, (int)LOLA_ATTN_BAD_OFFSETS);
+    }
+    // The number of tile `want` inside this lane's sequence, or -1 if another lane has it; no larger `want`
+    // than the last one.
+    __device__ __forceinline__ int tile(const AttnArgs& a, int want, int lane) {
+        while (want < before) {
+            cb -= kWarp;
+            chunk(a, lane);
+            before -= __shfl_sync(0xffffffffu, inc, 31);
+        }
+        const int at = want - before - (inc - own);
+        return at >= 0 && at < own ? at : -1;
+    }
+};
+
+// The next CTA of the grid that has not started is taken over (asynchronously; 16 bytes at `dst`, counted
+// on `bar`), and what came of it.
+__device__ __forceinline__ void steal_block(uint32_t dst, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+                 "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ bool stolen_block(uint32_t src, uint32_t* block) {
+    uint32_t ok, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}\n"
+        : "=r"(ok), "=r"(x)
+        : "r"(src)
+        : "memory");
+    *block = x;
+    return ok != 0;
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
     using C = Cfg<D, NT>;
-    constexpr int kMmaWarp = C::kMmaWarp, kLoadWarp = C::kLoadWarp, kCleanWarp0 = C::kCleanWarp0, kQ = C::kQ;
+    constexpr int kMmaWarp = C::kMmaWarp, kCap = C::kCap;
     extern __shared__ __align__(1024) uint8_t smraw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(sm);
     enum {
-        B_Q = 0, B_S = 2, B_P = 4, B_O = 6, B_DONE = 8, B_FULL = 9, B_EMPTY = B_FULL + kPairs, B_CLEAN = B_EMPTY + kPairs,
-        B_ARMED = B_CLEAN + kPairs, B_N = B_ARMED + kPairs
+        B_ITEM = 0, B_ITEMFREE = 2, B_STEAL = 4, B_Q = 5, B_QFREE = B_Q + NT, B_S = B_QFREE + NT, B_P = B_S + NT, B_O = B_P + NT,
+        B_DONE = B_O + NT, B_FULL, B_EMPTY = B_FULL + kCap, B_ARMED = B_EMPTY + kCap, B_CLEAN = B_ARMED + kClean,
+        B_N = B_CLEAN + kClean
     };
     __shared__ __align__(8) uint64_t bars[B_N];
+    __shared__ __align__(16) uint4 stolen;
+    __shared__ Item items[2];
     __shared__ uint32_t tmem_base;
-    __shared__ int abort_sm, odd_sm;
+    __shared__ int abort_sm, odd_sm[2];
     const int tid = threadIdx.x, warp = tid / kWarp, lane = tid % kWarp;
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
 
@@ -139,51 +237,40 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.q)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.v)) : "memory");
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(B_ITEM + i), 1);
+            mbar_init(bar(B_ITEMFREE + i), 4 * NT + 3);     // softmax warps, MMA, loader, cleaner
+        }
+        mbar_init(bar(B_STEAL), 1);
         for (int i = 0; i < NT; ++i) {
             mbar_init(bar(B_Q + i), 1);
+            mbar_init(bar(B_QFREE + i), 1);
             mbar_init(bar(B_S + i), 1);
             mbar_init(bar(B_P + i), 4);
             mbar_init(bar(B_O + i), 1);
         }
         mbar_init(bar(B_DONE), 1);
-        for (int s = 0; s < kPairs; ++s) {
-            mbar_init(bar(B_CLEAN + s), 2);
-            mbar_init(bar(B_ARMED + s), 1);
+        for (int s = 0; s < kCap; ++s) {
             mbar_init(bar(B_FULL + s), 1);
             mbar_init(bar(B_EMPTY + s), 1);
         }
+        for (int s = 0; s < kClean; ++s) {
+            mbar_init(bar(B_ARMED + s), 1);
+            mbar_init(bar(B_CLEAN + s), 1);
+        }
         abort_sm = 0;
-        odd_sm = 0;
     }
     if (warp == kMmaWarp) tmem_alloc<C::kTmem>(smem_u32(&tmem_base));
-    const int h = blockIdx.x % (unsigned)a.Hq;
-    TilePos at;
-    const bool live = find_tile<C::kThreads, kQ>(a, (int)(blockIdx.x / (unsigned)a.Hq), &at);
-    if (at.bad) atomicOr(&g_status, (int)LOLA_ATTN_BAD_OFFSETS);
-    if (!live) {
-        if (warp == kMmaWarp) {
-            __syncwarp();
-            tmem_dealloc<C::kTmem>(*reinterpret_cast<volatile uint32_t*>(&tmem_base));
-        }
-        return;
-    }
-    const int q0 = at.q0, lq = at.lq, k0 = at.k0, lk = at.lk, r0 = at.tile * kQ, shift = lk - lq;
-    // blocks that tile i reads, and those that all its rows see whole
-    int nb[NT], nf = 0x7fffffff, nmax = 0;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int first = r0 + kM * i, last = min(first + kM, lq) - 1;      // the tile's rows
-        nb[i] = first < lq ? (max(0, min(lk, last + shift + 1)) + kN - 1) / kN : 0;
-        if (nb[i] > 0) nf = min(nf, max(0, min(lk, first + shift + 1)) / kN);
-        nmax = max(nmax, nb[i]);
-    }
-
+    Finder<C::kQ> find;
+    // (before the barriers are there, as nothing of it needs them: five short prompts 11.2 -> 10.4 us; with two
+    // tiles it costs the softmax registers, 4 x 4096 x 32 heads 415 -> 431 us)
+    if (NT == 1 && warp == C::kItemWarp) find.start(a, lane);
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tb = tmem_base;
 
-    auto wait = [&](int i, uint32_t parity) -> bool {
+    auto wait_for = [&](int i, uint32_t parity, uint64_t limit) -> bool {
         const uint32_t x = bar(i);
         uint64_t start = 0;
         for (int it = 0;; ++it) {
@@ -198,96 +285,181 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
             if (*reinterpret_cast<volatile int*>(&abort_sm)) return false;
             const uint64_t now = globaltimer_ns();
             if (it == 0) start = now;
-            else if (now - start > kWaitNs) {
+            else if (now - start > limit) {
                 abort_sm = 1;
                 return false;
             }
         }
     };
-    // Ring: block j's K is load 2 j, its V load 2 j + 1.  Pair p is what the products of one turn read, V of
-    // block p - 1 and K of block p (pair 0: only K): it has one barrier for "loaded" and one for "read",
-    // p % 4 of either, so a pair is loaded only when the one four before it has been read.
-    auto stage = [&](int x) { return x % C::kStages; };
-    auto pair = [&](int p) { return p & (kPairs - 1); };
-    auto phase = [&](int p) { return (uint32_t)(p / kPairs) & 1u; };
-    auto ring = [&](int x) { return sb + (uint32_t)(NT + stage(x)) * C::kTileBytes; };
+    auto wait = [&](int i, uint32_t parity) -> bool { return wait_for(i, parity, kWaitNs); };
+    // Every role walks the same items: item n is in slot n & 1; `last` of them has live = 0.
+    auto get_item = [&](int n, Item* t) -> bool {
+        if (!wait_for(B_ITEM + (n & 1), (uint32_t)(n >> 1) & 1u, kItemNs)) return false;
+        *t = items[n & 1];
+        return t->live != 0;
+    };
+    // Pairs, counted over all items: pair P is what the products of one turn read, V of a block and K of
+    // the block behind it (an item's first pair: only K; its last: only V).  It has one barrier for
+    // "loaded", one for "read" and one place in the ring, P % kCap of each, so that it is loaded when pair
+    // P - kCap has been read.
+    auto full_of = [&](int P) { return B_FULL + P % kCap; };
+    auto empty_of = [&](int P) { return B_EMPTY + P % kCap; };
+    auto phase = [&](int P) { return (uint32_t)(P / kCap) & 1u; };
+    auto v_of = [&](int P) { return (uint32_t)(NT + 2 * (P % kCap)) * C::kTileBytes; };       // offset of its V
+    auto k_of = [&](int P) { return (uint32_t)(NT + 2 * (P % kCap) + 1) * C::kTileBytes; };   // ... of its K
 
     if (warp >= kMmaWarp) {
         // (what the block was launched with, 168 or 128 a thread, given out anew)
         if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (warp == kLoadWarp) {
-            // ================================ loader ================================
-            if (lane == 0 && nmax > 0) {
-                const int hk = h / a.G;
-                auto load = [&](const CUtensorMap* m, int row, int head, uint32_t dst, int bi) {
-                    mbar_expect(bar(bi), C::kTileBytes);
-                    for (int x = 0; x < D / 64; ++x) tma_load3(dst + 16384u * x, m, 64 * x, head, row, bar(bi));
-                };
-                if (nb[0] > 0) load(&maps.q, q0 + r0, h, sb, B_Q);
-                bool ok = true;
-                int p = 0, waited = 0;
-                for (; p <= nmax && ok; ++p) {
-                    const int last = p < nmax ? 2 * p : 2 * p - 1;              // the pair's last load
-                    // what its stages and its barriers held before has been read
-                    const int held = last >= C::kStages ? (last - C::kStages + 1) / 2 : -1;
-                    while (ok && waited <= max(held, p - kPairs)) {
-                        ok = wait(B_EMPTY + pair(waited), phase(waited));
-                        ++waited;
-                    }
+        if (warp == C::kItemWarp) {
+            // ================================ items ================================
+            // This CTA's own block first, then blocks of the grid that have not started, one ahead of the
+            // work: no CTA has more than one item waiting, and none starts, looks tiles up or loads its
+            // first tiles while the tensor core waits.
+            if (NT == 2) find.start(a, lane);
+            bool ok = true, more = true;
+            uint32_t block = blockIdx.x;
+            int n = 0, steals = 0;
+            while (ok && more) {
+                const unsigned u = block / (unsigned)a.Hq;
+                if (u < (unsigned)find.total) {
+                    const int at = find.tile(a, find.total - 1 - (int)u, lane);
+                    if (n >= 2) ok = __all_sync(0xffffffffu, wait_for(B_ITEMFREE + (n & 1), (uint32_t)(n / 2 - 1) & 1u, kItemNs));
                     if (!ok) break;
-                    const int full = B_FULL + pair(p);
-                    mbar_expect(bar(full), (uint32_t)((p > 0) + (p < nmax)) * C::kTileBytes);
-                    if (p > nf) mbar_arrive1(bar(B_ARMED + pair(p)));
-                    for (int n = max(0, 2 * p - 1); n <= last; ++n)
+                    if (at >= 0) {
+                        Item& t = items[n & 1];
+                        t.q0 = find.q0;
+                        t.lq = find.lq;
+                        t.k0 = find.k0;
+                        t.lk = find.lk;
+                        t.r0 = at * C::kQ;
+                        t.h = (int)(block - u * (unsigned)a.Hq);
+                        t.live = 1;
+                        odd_sm[n & 1] = 0;
+                        mbar_arrive1(bar(B_ITEM + (n & 1)));
+                    }
+                    __syncwarp();
+                    ++n;
+                }
+                // (a slot is free before the next block is taken)
+                if (n >= 2) ok = __all_sync(0xffffffffu, wait_for(B_ITEMFREE + (n & 1), (uint32_t)(n / 2 - 1) & 1u, kItemNs));
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_expect(bar(B_STEAL), 16);
+                    steal_block(smem_u32(&stolen), bar(B_STEAL));
+                }
+                __syncwarp();
+                ok = __all_sync(0xffffffffu, wait(B_STEAL, (uint32_t)steals & 1u));
+                ++steals;
+                if (ok) more = stolen_block(smem_u32(&stolen), &block);
+                fence_async_smem();                                    // (read before the next answer lands there)
+                __syncwarp();
+            }
+            if (ok && lane == 0) {
+                items[n & 1].live = 0;
+                mbar_arrive1(bar(B_ITEM + (n & 1)));
+            }
+        } else if (warp == C::kLoadWarp) {
+            // ================================ loader ================================
+            if (lane == 0) {
+                Item t;
+                bool ok = true;
+                int P = 0, cleans = 0, nq[NT] = {};
+                for (int n = 0; ok && get_item(n, &t); ++n) {
+                    const Span<NT> sp(t);
+                    const int hk = t.h / a.G;
+                    auto load_q = [&](int i) {
+                        if (sp.nb[i] == 0) return;
+                        if (nq[i] > 0 && !(ok = wait(B_QFREE + i, (uint32_t)(nq[i] - 1) & 1u))) return;
+                        ++nq[i];
+                        mbar_expect(bar(B_Q + i), C::kTileBytes);
                         for (int x = 0; x < D / 64; ++x)
-                            tma_load3(ring(n) + 16384u * x, n & 1 ? &maps.v : &maps.k, 64 * x, hk, k0 + (n >> 1) * kN, bar(full));
-                    if (NT == 2 && p == 0 && nb[NT - 1] > 0) load(&maps.q, q0 + r0 + kM, h, sb + C::kTileBytes, B_Q + 1);
+                            tma_load3(sb + (uint32_t)i * C::kTileBytes + 16384u * x, &maps.q, 64 * x, t.h, t.q0 + t.r0 + kM * i, bar(B_Q + i));
+                    };
+                    if (sp.nmax > 0) {
+                        load_q(0);
+                        for (int p = 0; p <= sp.nmax && ok; ++p) {
+                            if (P >= kCap && !(ok = wait(empty_of(P), phase(P - kCap)))) break;
+                            const int full = full_of(P);
+                            mbar_expect(bar(full), (uint32_t)((p > 0) + (p < sp.nmax)) * C::kTileBytes);
+                            if (p > 0)
+                                for (int x = 0; x < D / 64; ++x)
+                                    tma_load3(sb + v_of(P) + 16384u * x, &maps.v, 64 * x, hk, t.k0 + (p - 1) * kN, bar(full));
+                            if (p < sp.nmax)
+                                for (int x = 0; x < D / 64; ++x)
+                                    tma_load3(sb + k_of(P) + 16384u * x, &maps.k, 64 * x, hk, t.k0 + p * kN, bar(full));
+                            if (p > sp.nf) mbar_arrive1(bar(B_ARMED + cleans++ % kClean));
+                            ++P;
+                            if (p == 0 && NT == 2) load_q(NT - 1);
+                        }
+                    }
+                    if (ok) mbar_arrive1(bar(B_ITEMFREE + (n & 1)));
                 }
                 // leave no copy in flight
-                for (int x = max(0, p - kPairs); x < p; ++x) mbar_wait(bar(B_FULL + pair(x)), phase(x), kWaitNs);
+                for (int x = max(0, P - kCap); x < P; ++x) mbar_wait(bar(full_of(x)), phase(x), kWaitNs);
                 for (int i = 0; i < NT; ++i)
-                    if (nb[i] > 0) mbar_wait(bar(B_Q + i), 0, kWaitNs);
+                    if (nq[i] > 0) mbar_wait(bar(B_Q + i), (uint32_t)(nq[i] - 1) & 1u, kWaitNs);
             }
+            __syncwarp();
         } else if (warp == kMmaWarp) {
             // ================================ MMA issue ================================
-            if (lane == 0 && nmax > 0) {
+            if (lane == 0) {
                 constexpr uint32_t id_s = idesc_bf16(kM, kN, 0), id_o = idesc_bf16(kM, D, 1);
                 constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
-                auto s_mma = [&](int i, int j) {
-                    const uint32_t q = desc_lo(sb + (uint32_t)i * C::kTileBytes, 16), k = desc_lo(ring(2 * j), 16);
+                Item t;
+                bool ok = true;
+                int P = 0, cleans = 0, nq[NT] = {}, ns[NT] = {};      // Q tiles, blocks of the tile before this item
+                for (int n = 0; ok && get_item(n, &t); ++n) {
+                    const Span<NT> sp(t);
+                    // S_i of block j (K in pair P0 + j); behind the item's last one Q_i may be overwritten
+                    auto s_mma = [&](int i, int j, int pk) {
+                        const uint32_t q = desc_lo(sb + (uint32_t)i * C::kTileBytes, 16), k = desc_lo(sb + k_of(pk), 16);
 #pragma unroll
-                    for (int x = 0; x < D / 16; ++x) {
-                        const uint32_t o = (uint32_t)(x >> 2) * 1024u + (uint32_t)(x & 3) * 2u;   // 16-byte units
-                        mma_ss(tb + C::TS(i), q + o, k + o, hi, id_s, x > 0);
-                    }
-                    mma_commit(bar(B_S + i));
-                };
-                bool ok = wait(B_FULL, 0);
-                for (int i = 0; i < NT && ok; ++i)
-                    if (nb[i] > 0) {
-                        ok = wait(B_Q + i, 0);
-                        fence_after();
-                        if (ok) s_mma(i, 0);
-                    }
-                mma_commit(bar(B_EMPTY));
-                for (int j = 0; j < nmax && ok; ++j) {
-                    // V of block j and K of block j + 1
-                    ok = wait(B_FULL + pair(j + 1), phase(j + 1));
-                    if (ok && j >= nf) ok = wait(B_CLEAN + pair(j + 1), (uint32_t)((j - nf) / kPairs) & 1u);
-                    const uint32_t v = desc_lo(ring(2 * j + 1), 16384);
-                    for (int i = 0; i < NT && ok; ++i) {
-                        if (j < nb[i]) {
-                            if (!(ok = wait(B_P + i, (uint32_t)j & 1u))) break;
-                            fence_after();
-#pragma unroll
-                            for (int x = 0; x < kN / 16; ++x)
-                                mma_ts(tb + C::TO(i), tb + C::TS(i) + 8 * x, v + 128u * x, hi, id_o, x > 0 ? 1u : (uint32_t)j);
+                        for (int x = 0; x < D / 16; ++x) {
+                            const uint32_t o = (uint32_t)(x >> 2) * 1024u + (uint32_t)(x & 3) * 2u;   // 16-byte units
+                            mma_ss(tb + C::TS(i), q + o, k + o, hi, id_s, x > 0);
                         }
-                        if (j + 1 < nb[i]) s_mma(i, j + 1);
-                        else if (j + 1 == nb[i]) mma_commit(bar(B_O + i));
+                        mma_commit(bar(B_S + i));
+                        if (j + 1 == sp.nb[i]) mma_commit(bar(B_QFREE + i));
+                    };
+                    if (sp.nmax > 0) {
+                        ok = wait(full_of(P), phase(P));
+#pragma unroll
+                        for (int i = 0; i < NT; ++i)
+                            if (ok && sp.nb[i] > 0) {
+                                ok = wait(B_Q + i, (uint32_t)nq[i]++ & 1u);
+                                fence_after();
+                                if (ok) s_mma(i, 0, P);
+                            }
+                        mma_commit(bar(empty_of(P)));
+                        ++P;
+                        for (int j = 0; j < sp.nmax && ok; ++j, ++P) {
+                            // V of block j and K of block j + 1
+                            ok = wait(full_of(P), phase(P));
+                            if (ok && j >= sp.nf) {
+                                ok = wait(B_CLEAN + cleans % kClean, (uint32_t)(cleans / kClean) & 1u);
+                                ++cleans;
+                            }
+                            const uint32_t v = desc_lo(sb + v_of(P), 16384);
+#pragma unroll
+                            for (int i = 0; i < NT; ++i) {
+                                if (ok && j < sp.nb[i]) {
+                                    if (!(ok = wait(B_P + i, (uint32_t)(ns[i] + j) & 1u))) break;
+                                    fence_after();
+#pragma unroll
+                                    for (int x = 0; x < kN / 16; ++x)
+                                        mma_ts(tb + C::TO(i), tb + C::TS(i) + 8 * x, v + 128u * x, hi, id_o, x > 0 ? 1u : (uint32_t)j);
+                                    if (j + 1 < sp.nb[i]) s_mma(i, j + 1, P);
+                                    else mma_commit(bar(B_O + i));
+                                }
+                            }
+                            mma_commit(bar(empty_of(P)));
+                        }
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) ns[i] += sp.nb[i];
                     }
-                    mma_commit(bar(B_EMPTY + pair(j + 1)));
+                    if (ok) mbar_arrive1(bar(B_ITEMFREE + (n & 1)));
                 }
                 // leave no product in flight
                 mma_commit(bar(B_DONE));
@@ -295,191 +467,202 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
             }
             __syncwarp();
         } else {
-            // ================================ cleaners ================================
-            const int ct = tid - kCleanWarp0 * kWarp;
+            // ================================ cleaner ================================
+            Item t;
+            int P = 0, cleans = 0;
             bool ok = true;
-            for (int j = nf; j < nmax && ok; ++j) {
-                // (a pair's "loaded" can be told from the one four pairs before only once it is armed)
-                ok = wait(B_ARMED + pair(j + 1), (uint32_t)((j - nf) / kPairs) & 1u) && wait(B_FULL + pair(j + 1), phase(j + 1));
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                uint8_t* v = sm + (size_t)(NT + stage(2 * j + 1)) * C::kTileBytes;
-                const int valid = min(kN, lk - j * kN);
-                // 16-byte chunks in memory order, eight in flight; a bfloat16 is not finite iff adding 1
-                // to its exponent carries into the sign
-                bool odd = false;
-                uint4* p = reinterpret_cast<uint4*>(v) + ct;
+            for (int n = 0; ok; ++n) {
+                if (!__all_sync(0xffffffffu, get_item(n, &t))) break;
+                const Span<NT> sp(t);
+                for (int j = sp.nf; j < sp.nmax && ok; ++j, ++cleans) {
+                    // (a pair's "loaded" can be told from the one before at its place only once it is armed)
+                    const int pv = P + j + 1, c = cleans % kClean;
+                    const uint32_t par = (uint32_t)(cleans / kClean) & 1u;
+                    ok = wait_for(B_ARMED + c, par, kItemNs) && wait(full_of(pv), phase(pv));
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const int valid = min(kN, t.lk - j * kN);
+                    // 16-byte chunks in memory order, eight in flight; a bfloat16 is not finite iff adding 1
+                    // to its exponent carries into the sign
+                    bool odd = false;
+                    uint4* p = reinterpret_cast<uint4*>(sm + v_of(pv)) + lane;
 #pragma unroll 1
-                for (int x0 = 0; x0 < kN * D / 8 / 64; x0 += 8) {
-                    uint4 y[8];
+                    for (int x0 = 0; x0 < kN * D / 8 / 32; x0 += 8) {
+                        uint4 y[8];
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) y[x] = p[64 * (x0 + x)];
-                    uint32_t hit = 0;
+                        for (int x = 0; x < 8; ++x) y[x] = p[32 * (x0 + x)];
+                        uint32_t hit = 0;
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        const int row = ((ct + 64 * (x0 + x)) >> 3) & (kN - 1);
-                        const uint32_t t = ((y[x].x & 0x7f807f80u) + 0x00800080u) | ((y[x].y & 0x7f807f80u) + 0x00800080u) |
-                                           ((y[x].z & 0x7f807f80u) + 0x00800080u) | ((y[x].w & 0x7f807f80u) + 0x00800080u);
-                        if (row < valid) hit |= t;
-                        else p[64 * (x0 + x)] = make_uint4(0, 0, 0, 0);
-                    }
-                    if (!(hit & 0x80008000u)) continue;
-                    odd = true;
-#pragma unroll 1
-                    for (int x = 0; x < 8; ++x) {
-                        uint4* c = p + 64 * (x0 + x);
-                        const uint4 z = *c;
-                        uint32_t w[4] = {z.x, z.y, z.z, z.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const bool lo = (w[e] & 0x7f80u) == 0x7f80u, hi = (w[e] & 0x7f800000u) == 0x7f800000u;
-                            w[e] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0xffffu : ~0u);
+                        for (int x = 0; x < 8; ++x) {
+                            const int row = ((lane + 32 * (x0 + x)) >> 3) & (kN - 1);
+                            const uint32_t w = ((y[x].x & 0x7f807f80u) + 0x00800080u) | ((y[x].y & 0x7f807f80u) + 0x00800080u) |
+                                               ((y[x].z & 0x7f807f80u) + 0x00800080u) | ((y[x].w & 0x7f807f80u) + 0x00800080u);
+                            if (row < valid) hit |= w;
+                            else p[32 * (x0 + x)] = make_uint4(0, 0, 0, 0);
                         }
-                        *c = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (!(hit & 0x80008000u)) continue;
+                        odd = true;
+#pragma unroll 1
+                        for (int x = 0; x < 8; ++x) {
+                            const uint4 z = p[32 * (x0 + x)];
+                            uint32_t w[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const bool lo = (w[e] & 0x7f80u) == 0x7f80u, up = (w[e] & 0x7f800000u) == 0x7f800000u;
+                                w[e] &= (lo ? 0xffff0000u : ~0u) & (up ? 0xffffu : ~0u);
+                            }
+                            p[32 * (x0 + x)] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
                     }
+                    if (odd) *reinterpret_cast<volatile int*>(&odd_sm[n & 1]) = 1;
+                    fence_async_smem();
+                    __threadfence_block();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive1(bar(B_CLEAN + c));
                 }
-                if (odd) *reinterpret_cast<volatile int*>(&odd_sm) = 1;
-                fence_async_smem();
-                __threadfence_block();
-                __syncwarp();
-                if (lane == 0) mbar_arrive1(bar(B_CLEAN + pair(j + 1)));
+                if (sp.nmax > 0) P += sp.nmax + 1;
+                if (ok && lane == 0) mbar_arrive1(bar(B_ITEMFREE + (n & 1)));
             }
         }
     } else {
         // ================================ softmax ================================
         if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-        const int i = warp >> 2, row = r0 + kM * i + (warp & 3) * 32 + lane;    // (may lie behind the sequence)
+        const int i = warp >> 2, r = (warp & 3) * 32 + lane;                    // tile, row of the tile
         const uint32_t lo = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tb + lo + C::TS(i), to = tb + lo + C::TO(i);
-        const int n = nb[i], last = min(row + shift, lk - 1);                   // the row's last key
-        const int wfull = max(0, min(lk, (row - lane) + shift + 1)) / kN;       // blocks the warp's rows see whole
         const float c = a.scale_log2;
-        float m = -INFINITY, l = 0.f;
-        bool ok = true;
-        for (int j = 0; j < n && ok; ++j) {
-            if (!(ok = __all_sync(0xffffffffu, wait(B_S + i, (uint32_t)j & 1u)))) break;
-            fence_after();
-            float s[kN];
+        uint8_t* stage = sm + (size_t)(NT + 2 * kCap) * C::kTileBytes + (size_t)i * C::kStageBytes;
+        int ns = 0, no = 0;                                                     // blocks, items with blocks so far
+        for (int it = 0;; ++it) {
+            Item t;
+            if (!__all_sync(0xffffffffu, get_item(it, &t))) break;
+            const Span<NT> sp(t);
+            const int row = t.r0 + kM * i + r, shift = t.lk - t.lq, n = sp.nb[i];   // (the row may lie behind the sequence)
+            const int last = min(row + shift, t.lk - 1);                            // the row's last key
+            const int wfull = max(0, min(t.lk, row - lane + shift + 1)) / kN;       // blocks the warp's rows see whole
+            float m = -INFINITY, l = 0.f;
+            bool ok = true;
+            for (int j = 0; j < n && ok; ++j) {
+                if (!(ok = __all_sync(0xffffffffu, wait(B_S + i, (uint32_t)(ns + j) & 1u)))) break;
+                fence_after();
+                float s[kN];
 #pragma unroll
-            for (int x = 0; x < kN; x += 32) tmem_ld32(ts + x, s + x);
-            tmem_wait_ld();
-            if (j >= wfull) {
-                const int lim = last - j * kN, w0 = __reduce_min_sync(0xffffffffu, lim);
+                for (int x = 0; x < kN; x += 32) tmem_ld32(ts + x, s + x);
+                tmem_wait_ld();
+                if (j >= wfull) {
+                    // 32 columns at a time: most are seen whole by the warp's rows even here
+                    const int lim = last - j * kN, w0 = __reduce_min_sync(0xffffffffu, lim);
+#pragma unroll
+                    for (int x = 0; x < kN; x += 32) {
+                        if (w0 >= x + 31) continue;
+#pragma unroll
+                        for (int y = x; y < x + 32; ++y) s[y] = y <= lim ? s[y] : -INFINITY;
+                    }
+                }
+                float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int x = 4; x < kN; ++x) mx[x & 3] = fmaxf(mx[x & 3], s[x]);
+                const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                const bool need = bm > m + kRaise;
+                if (j == 0) {
+                    m = bm;
+                } else if (__any_sync(0xffffffffu, need)) {
+                    // (O_i is quiet: S of this block was issued behind the block before's P V, and is done)
+                    const float f = need ? ex2(m - bm) : 1.f;
+                    l *= f;
+                    // (rare, and with S in registers: 16 columns at a time)
+#pragma unroll 1
+                    for (int x = 0; x < D; x += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(to + x, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                        tmem_st16(to + x, o);
+                    }
+                    if (need) m = bm;
+                }
+                const float base = m == -INFINITY ? 0.f : m;
+                float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
 #pragma unroll
                 for (int x = 0; x < kN; x += 32) {
-                    if (w0 >= x + 31) continue;
+                    uint32_t p[16];
 #pragma unroll
-                    for (int y = x; y < x + 32; ++y) s[y] = y <= lim ? s[y] : -INFINITY;
+                    for (int y = 0; y < 16; ++y) {
+                        float2 e = fma2(make_float2(s[x + 2 * y], s[x + 2 * y + 1]), c2, b2);
+                        e.x = ex2(e.x);
+                        e.y = ex2(e.y);
+                        ls[y & 1] = add2(ls[y & 1], e);
+                        const __nv_bfloat162 bp = __floats2bfloat162_rn(e.x, e.y);
+                        p[y] = *reinterpret_cast<const uint32_t*>(&bp);
+                    }
+                    tmem_st16(ts + x / 2, p);
                 }
+                l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+                tmem_wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(bar(B_P + i));
             }
-            float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-            for (int x = 4; x < kN; ++x) mx[x & 3] = fmaxf(mx[x & 3], s[x]);
-            const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-            const bool need = bm > m + kRaise;
-            if (j == 0) {
-                m = bm;
-            } else if (__any_sync(0xffffffffu, need)) {
-                // (O_i is quiet: S of this block was issued behind the block before's P V, and is done)
-                const float f = need ? ex2(m - bm) : 1.f;
-                l *= f;
-                // (rare, and with S in registers: 16 columns at a time)
+            // ---- o = O / l ----
+            if (n > 0 && ok) ok = __all_sync(0xffffffffu, wait(B_O + i, (uint32_t)no & 1u));
+            if (!ok) break;
+            fence_after();
+            ns += n;
+            no += n > 0;
+            const bool none = last < 0 || n == 0;
+            const float inv = 1.f / l;
+            const bool odd = *reinterpret_cast<volatile int*>(&odd_sm[it & 1]) != 0;
+            const int rest = t.lq - (row - lane);                   // rows of the warp inside the sequence
+            __nv_bfloat16* O = reinterpret_cast<__nv_bfloat16*>(a.O.data) + (int64_t)(t.q0 + row - lane) * a.O.row + (int64_t)t.h * a.O.head;
+            // 32 columns at a time through shared memory (64-byte rows, 16-byte chunks swizzled), so that
+            // whole sectors go out
 #pragma unroll 1
-                for (int x = 0; x < D; x += 16) {
-                    uint32_t o[16];
-                    tmem_ld16(to + x, o);
+            for (int x = 0; x < D; x += 32) {
+                float o[32];
+                if (n > 0) {
+                    tmem_ld32(to + x, o);
                     tmem_wait_ld();
-#pragma unroll
-                    for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-                    tmem_st16(to + x, o);
                 }
-                if (need) m = bm;
-            }
-            const float base = m == -INFINITY ? 0.f : m;
-            float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
 #pragma unroll
-            for (int x = 0; x < kN; x += 32) {
+                for (int y = 0; y < 32; ++y) o[y] = none ? 0.f : o[y] * inv;
+                if (odd && lane < rest) {
+                    // values that are not finite and were kept out of the products: for the keys the row sees
+                    const __nv_bfloat16* V = reinterpret_cast<const __nv_bfloat16*>(a.V.data) + (int64_t)(t.h / a.G) * a.V.head + x;
+#pragma unroll 1
+                    for (int key = sp.nf * kN; key <= last; ++key)
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) {
+                            const float v = __bfloat162float(V[(int64_t)(t.k0 + key) * a.V.row + y]);
+                            if (!(fabsf(v) <= 3.4e38f)) o[y] += v;
+                        }
+                }
                 uint32_t p[16];
 #pragma unroll
                 for (int y = 0; y < 16; ++y) {
-                    float2 e = fma2(make_float2(s[x + 2 * y], s[x + 2 * y + 1]), c2, b2);
-                    e.x = ex2(e.x);
-                    e.y = ex2(e.y);
-                    ls[y & 1] = add2(ls[y & 1], e);
-                    const __nv_bfloat162 bp = __floats2bfloat162_rn(e.x, e.y);
+                    const __nv_bfloat162 bp = __floats2bfloat162_rn(o[2 * y], o[2 * y + 1]);
                     p[y] = *reinterpret_cast<const uint32_t*>(&bp);
                 }
-                tmem_st16(ts + x / 2, p);
-            }
-            tmem_wait_st();
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive1(bar(B_P + i));
-            l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
-        }
-        // ---- o = O / l ----
-        if (n > 0 && ok) ok = __all_sync(0xffffffffu, wait(B_O + i, 0));
-        fence_after();
-        const bool none = last < 0 || n == 0, own = row < lq && ok;
-        const float inv = 1.f / l;
-        const bool odd = *reinterpret_cast<volatile int*>(&odd_sm) != 0;
-        // the tile's Q rows have been read: their place takes o (the same swizzled layout), from where
-        // whole rows go out, 512 bytes a warp and store
-        uint8_t* stagep = sm + (size_t)i * C::kTileBytes;
-        const int r = (warp & 3) * 32 + lane;
-        // (loops, not unrolled: straight code that runs once is fetched slower than it executes)
-#pragma unroll 1
-        for (int x = 0; x < D; x += 32) {
-            float o[32];
-            if (n > 0) {
-                tmem_ld32(to + x, o);
-                tmem_wait_ld();
-            }
-            uint32_t p[16];
 #pragma unroll
-            for (int y = 0; y < 32; ++y) o[y] = none ? 0.f : o[y] * inv;
+                for (int y = 0; y < 4; ++y)
+                    *reinterpret_cast<uint4*>(stage + r * 64 + ((y ^ (r >> 1)) & 3) * 16) = make_uint4(p[4 * y], p[4 * y + 1], p[4 * y + 2], p[4 * y + 3]);
+                __syncwarp();
 #pragma unroll
-            for (int y = 0; y < 16; ++y) {
-                const __nv_bfloat162 bp = __floats2bfloat162_rn(o[2 * y], o[2 * y + 1]);
-                p[y] = *reinterpret_cast<const uint32_t*>(&bp);
-            }
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-                *reinterpret_cast<uint4*>(stagep + (x >> 6) * 16384 + kmaj_chunk(r, ((x & 63) >> 3) + y)) =
-                    make_uint4(p[4 * y], p[4 * y + 1], p[4 * y + 2], p[4 * y + 3]);
-        }
-        if (odd && own) {
-            // values that are not finite and were kept out of the products: for the keys the row sees
-            // (rare, so small code: one channel at a time)
-#pragma unroll 1
-            for (int x = 0; x < D; ++x) {
-                const __nv_bfloat16* V = reinterpret_cast<const __nv_bfloat16*>(a.V.data) + (int64_t)(h / a.G) * a.V.head + x;
-                float add = 0.f;
-#pragma unroll 1
-                for (int key = nf * kN; key <= last; ++key) {
-                    const float v = __bfloat162float(V[(int64_t)(k0 + key) * a.V.row]);
-                    if (!(fabsf(v) <= 3.4e38f)) add += v;
+                for (int y = 0; y < 4; ++y) {
+                    const int rr = 8 * y + (lane >> 2), wr = (warp & 3) * 32 + rr;
+                    const uint4 z = *reinterpret_cast<const uint4*>(stage + wr * 64 + (((lane & 3) ^ (wr >> 1)) & 3) * 16);
+                    if (rr < rest) *reinterpret_cast<uint4*>(O + (int64_t)rr * a.O.row + x + 8 * (lane & 3)) = z;
                 }
-                __nv_bfloat16* z = reinterpret_cast<__nv_bfloat16*>(stagep + (x >> 6) * 16384 + kmaj_chunk(r, (x & 63) >> 3)) + (x & 7);
-                if (add != 0.f) *z = __float2bfloat16_rn(__bfloat162float(*z) + add);
+                __syncwarp();
             }
+            if (a.lse && lane < rest)
+                a.lse[(int64_t)t.h * a.total_q + t.q0 + row] = none ? -INFINITY : (m + log2f(l)) * kAttnLn2;
+            // (O_i and odd_sm are read: the next item's products wait for this warp's next weights)
+            fence_before();
+            if (lane == 0) mbar_arrive1(bar(B_ITEMFREE + (it & 1)));
         }
-        __syncwarp();
-        constexpr int CH = D / 8, RW = 32 / CH;                 // chunks of a row, rows of a store
-        __nv_bfloat16* O = reinterpret_cast<__nv_bfloat16*>(a.O.data) + (int64_t)(q0 + row - lane) * a.O.row +
-                           (int64_t)h * a.O.head;
-        const int rest = ok ? lq - (row - lane) : 0;            // rows of the warp inside the sequence
-        const int ch = lane % CH;
-#pragma unroll 4
-        for (int x = 0; x < 32; x += RW) {
-            const int y = x + lane / CH;
-            const uint4 z = *reinterpret_cast<const uint4*>(stagep + (ch >> 3) * 16384 + kmaj_chunk((warp & 3) * 32 + y, ch & 7));
-            if (y < rest) *reinterpret_cast<uint4*>(O + (int64_t)y * a.O.row + 8 * ch) = z;
-        }
-        if (a.lse && own)
-            a.lse[(int64_t)h * a.total_q + q0 + row] = none ? -INFINITY : (m + log2f(l)) * kAttnLn2;
     }
     fence_before();
     __syncthreads();
@@ -512,14 +695,15 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// One or two tiles per CTA?  A CTA costs about o + s B microseconds, B the key blocks its tiles read on
+// One or two tiles per CTA?  An item costs about o + s B microseconds, B the key blocks its tiles read on
 // average: measured on prompts of 128 to 8192 tokens, 8 heads (us; two tiles: a round of 152 CTAs, one
 // tile: a round of 304, two on an SM),
-//            d = 128, two: 9.7 + 1.47 B   one: 8.3 + 1.94 B      d = 64, two: 8.0 + 1.19 B   one: 6.5 + 1.32 B
-// so one tile for short sequences (304 of 128 tokens, d = 128: 90 against 136 us; 19 of 4096: 645 against
-// 545), and where its finer cut saves a round (10 tiles of ~50 blocks, 16 heads, d = 64: 84 against
-// 126 us).  The tiles of a ragged batch are not known here: half a tile is added for each sequence, or
-// what the grid may come to where the rounds are few and a tile more can cost a whole one.
+//            d = 128, two: 8.6 + 1.46 B   one: 6.8 + 1.69 B      d = 64, two: 6.4 + 1.13 B   one: 5.0 + 1.23 B
+// so two tiles for long sequences (19 prompts of 4096 tokens, d = 128: 518 against 560 us), and one for short
+// ones (304 of 128 tokens: 69 against 89 us) and where its finer cut saves a round (10 tiles of ~50 blocks,
+// 16 heads, d = 64: 80 against 125 us).  The tiles of a ragged batch are not known here: half a tile is
+// added for each sequence, or what the grid may come to where the rounds are few and a tile more can
+// cost a whole one.
 static bool one_tile(const AttnArgs& a) {
     const double n = a.n_seq, lq = a.total_q / n, lk = a.total_k / n;
     const double blocks = (lk > lq ? lk - lq / 2 : lk / 2) / kN + 0.5;
@@ -529,7 +713,7 @@ static bool one_tile(const AttnArgs& a) {
         const double mean = (a.total_q / q + 0.5 * n) * a.Hq / slots;
         return (most <= 4 ? std::ceil(most) : std::ceil(mean)) * (o + s * blocks);
     };
-    return a.d == 128 ? cost(1, 8.3, 1.94) < 0.95 * cost(2, 9.7, 1.47) : cost(1, 6.5, 1.32) < 0.95 * cost(2, 8.0, 1.19);
+    return a.d == 128 ? cost(1, 6.8, 1.69) < cost(2, 8.6, 1.46) : cost(1, 5.0, 1.23) < cost(2, 6.4, 1.13);
 }
 
 cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t st) {
