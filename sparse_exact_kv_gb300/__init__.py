@@ -150,6 +150,7 @@ def _load():
 
 
 _lib = _load()
+from . import _lola_py as _fast  # noqa: E402  (links liblola.so: after it is loaded)
 
 
 def make_config(B, Hh, d_k, d_v, D, eta, lam, chunk, dtype, read_mask=0, alloc=LOLA_ALLOC_TOKEN,
@@ -419,11 +420,17 @@ def lola_attn_status(stream=None):
 # Convenience: buffers allocated through torch, then the C ABI
 # ---------------------------------------------------------------------------------------
 
+_fast.setup(torch.empty_like, torch.empty, getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream),
+            getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device), torch.int32, torch.float32, torch.uint8)
+
+
 @functools.lru_cache(maxsize=256)
 def _attn_plan(Hq, Hkv, d, dtype, scale):
-    """The config of a kind of layer and the decode step's workspace bytes (checks the config)."""
+    """The config of a kind of layer, the decode step's workspace bytes (checks the config), and both as the
+    marshalling module takes them (the config by its address: a layer holds on to it)."""
     cfg = make_attn_config(Hq, Hkv, d, dtype, scale)
-    return cfg, lola_paged_decode_workspace_bytes(cfg)
+    size = lola_paged_decode_workspace_bytes(cfg)
+    return cfg, size, (ctypes.addressof(cfg), dtype, size)
 
 
 def _need(ok, what):
@@ -440,10 +447,10 @@ class ExactAttention:
     devices are checked here, strides and alignment by the library; all tensors are on the current
     CUDA device."""
 
-    __slots__ = ("cfg", "Hq", "Hkv", "d", "dtype", "k_pool", "v_pool", "_ws")
+    __slots__ = ("cfg", "Hq", "Hkv", "d", "dtype", "k_pool", "v_pool", "_ws", "_plan")
 
     def __init__(self, Hq, Hkv, d, dtype=torch.bfloat16, k_pool=None, v_pool=None, scale=None):
-        self.cfg, self._ws = _attn_plan(Hq, Hkv, d, dtype, scale)
+        self.cfg, self._ws, self._plan = _attn_plan(Hq, Hkv, d, dtype, scale)
         self.Hq, self.Hkv, self.d, self.dtype = Hq, Hkv, d, dtype
         _need((k_pool is None) == (v_pool is None), "k_pool and v_pool come together")
         if k_pool is not None:
@@ -499,6 +506,11 @@ class ExactAttention:
         and head strides), cu_q, cu_k int32 [n_seq + 1].  Returns out [total_q, Hq, d]; ``lse``
         float32 [Hq, total_q] receives the log normalisers.  A fresh ``out`` is not initialised
         outside the sequences."""
+        if out is None and lse is None and stream is None:
+            out = _fast.prefill(self._plan, q, k, v, cu_q, cu_k)
+            if out is not NotImplemented:
+                return out
+            out = None
         dev, n, m, n1 = q.device, q.shape[0], k.shape[0], cu_q.shape[0]
         rq = self._heads(q, self.Hq, n, dev, "q")
         rk = self._heads(k, self.Hkv, m, dev, "k")
@@ -540,6 +552,10 @@ class ExactAttention:
         float32 [rot / 2] radians per position (None: no rotation); ``pairs`` the channel pairs of
         the rotation, "halves" or "neighbours"; ``positions`` int32 [n] in place of the tokens'
         indexes.  ``q_out`` may be q itself."""
+        if q_out is None and positions is None and stream is None:
+            r = _fast.append(self._plan, self.k_pool, self.v_pool, k, v, kv_len, table, cu_new, q, inv_freq, PAIRS[pairs])
+            if r is not NotImplemented:
+                return r
         kv, dev, n_seq, index = self._cache(kv_len, table)
         n = k.shape[0]
         rk = self._heads(k, self.Hkv, n, dev, "k")
@@ -572,6 +588,11 @@ class ExactAttention:
         """One query token per sequence, q [n_seq, Hq, d], over its kv_len cached tokens; returns out
         [n_seq, Hq, d].  ``lse`` float32 [n_seq, Hq].  ``workspace``: a buffer of
         lola_paged_decode_workspace_bytes; by default one is allocated for the call."""
+        if out is None and lse is None and workspace is None and stream is None:
+            out = _fast.decode(self._plan, self.k_pool, self.v_pool, q, kv_len, table)
+            if out is not NotImplemented:
+                return out
+            out = None
         kv, dev, n, index = self._cache(kv_len, table)
         rq = self._heads(q, self.Hq, n, dev, "q")
         if lse is not None:

@@ -1,10 +1,12 @@
-"""Build liblola.so in place: one nvcc per translation unit (in parallel), sm_103a only."""
+"""Build liblola.so in place: one nvcc per translation unit (in parallel), sm_103a only; then the Python
+binding's marshalling module beside it."""
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +19,7 @@ SOURCES = ["lola_capi.cu", "lola_phi.cu", "lola_select.cu", "lola_chunk.cu", "lo
            "lola_decode.cu", "lola_noalloc.cu", "lola_relsre.cu",
            "lola_fixed.cu", "lola_hola.cu", "lola_hola_tc.cu", "lola_attn.cu",
            "lola_attn_tc.cu", "lola_append.cu", "lola_paged.cu"]
+PYMOD = os.path.join(PKG, "_lola_py.so")      # the binding's marshalling in C (csrc/lola_py.cpp)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -35,9 +38,9 @@ def _flags(verbose_ptxas: bool) -> list[str]:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(PYMOD):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(PYMOD))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "lola.h"), __file__]
     return any(os.path.getmtime(p) > t for p in deps)
 
@@ -68,6 +71,13 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = PYMOD + f".{os.getpid()}.tmp"
+    r = subprocess.run([cc, "-O2", "-std=c++17", "-shared", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I",
+                        sysconfig.get_paths()["include"], os.path.join(CSRC, "lola_py.cpp"), "-o", tmp, "-cudart", "none",
+                        "-L", PKG, "-l:liblola.so", "-Xlinker", "-rpath,$ORIGIN"], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building the binding's module failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, PYMOD)
     return LIB
 
 

@@ -619,6 +619,52 @@ def test_prompt_attention_is_the_limit_of_a_lola_layer(L, gen):
     assert float((got.float() - Y.float()).abs().max()) <= 2e-2
 
 
+def test_refused_calls_say_what_is_wrong(L, gen):
+    """The call's short form declines what it does not take for granted; the long one then raises, or
+    handles it.  Neither keeps a reference."""
+    import sys
+    c = Paged(gen, [40, 30], 2, 64, 16, BF)
+    lay = L.ExactAttention(4, 2, 64, BF, c.k_pool, c.v_pool)
+    q, k = randn(gen, 2, 4, 64, dtype=BF), randn(gen, 2, 2, 64, dtype=BF)
+    cu = offsets([1, 1])
+    good = lay.decode_step(q, c.kv_len, c.table)
+    for bad in (q.float(), q[:1], q[:, :3], q.cpu(), torch.empty(2, 64, 4, dtype=BF, device="cuda").transpose(1, 2)):
+        with pytest.raises(ValueError):
+            lay.decode_step(bad, c.kv_len, c.table)
+        with pytest.raises(ValueError):
+            lay.append(k, k, c.kv_len, c.table, q=bad, inv_freq=_freq(64))
+    for args in ((q, c.kv_len.long(), c.table), (q, c.kv_len, c.table.long()), (q, c.kv_len[:1], c.table),
+                 (q, c.kv_len, c.table.t().contiguous().t())):
+        with pytest.raises(ValueError):
+            lay.decode_step(*args)
+    with pytest.raises(ValueError):
+        lay.prefill(q, k, k[:1], cu)
+    with pytest.raises(ValueError):
+        lay.prefill(q, k, k, cu.long())
+    with pytest.raises(L.LolaError):
+        lay.prefill(q, k[:1], k[:1], cu)                       # other totals without offsets of their own
+    with pytest.raises(L.LolaError):
+        lay.append(k, k, c.kv_len, c.table, q=q)               # q without a rotation
+    with pytest.raises(L.LolaError):
+        lay.append(k[:1], k[:1], c.kv_len, c.table)            # one token for two sequences
+    with pytest.raises(KeyError):
+        lay.append(k, k, c.kv_len, c.table, pairs="both")
+    odd = torch.zeros(2 * 4 * 64 + 4, dtype=BF, device="cuda")[4:].view(2, 4, 64)     # 8-byte aligned
+    with pytest.raises(L.LolaError):
+        lay.decode_step(odd, c.kv_len, c.table)
+    big = L.ExactAttention(4, 2, 64, BF, torch.zeros(2, 2, 24, 64, dtype=BF, device="cuda"),
+                           torch.zeros(2, 2, 24, 64, dtype=BF, device="cuda"))
+    with pytest.raises(L.LolaError):
+        big.decode_step(q, c.kv_len, c.table)                  # pages of 24 tokens
+    quiet(L)
+    held = [sys.getrefcount(x) for x in (q, k, c.kv_len, c.table, cu, c.k_pool)]
+    for _ in range(50):
+        again = lay.decode_step(q, c.kv_len, c.table)
+        lay.prefill(q, k, k, cu)
+    assert held == [sys.getrefcount(x) for x in (q, k, c.kv_len, c.table, cu, c.k_pool)]
+    assert torch.equal(again, good) and sys.getrefcount(again) == sys.getrefcount(good)
+
+
 def test_kernel_timing_counts_the_new_kernels(L, gen):
     c = Paged(gen, [200], 1, 64, 16, BF)
     lay = L.ExactAttention(1, 1, 64, BF, c.k_pool, c.v_pool)
