@@ -1,196 +1,280 @@
-// K8 (CUDA cores): causal softmax attention over packed prompts.
+// K8 (float32): causal softmax attention over packed prompts.
 //
 // Row i of a sequence with Lq queries and Lk keys sees the keys j <= i + Lk - Lq.  One pass over
 // the keys with a running maximum m and sum l per row (log2 units, s = c log2(e) q . k):
 //   m' = max(m, max_j s_j),  l' = 2^{m - m'} l + sum_j 2^{s_j - m'},
 //   O' = 2^{m - m'} O + sum_j 2^{s_j - m'} v_j,        o = O / l,  lse = ln 2 (m + log2 l).
-// A CTA of 128 threads takes 32 queries of one head and 64 keys at a time; a thread holds a 4 x 4 tile of
-// the scores and 4 rows x d / 16 columns of O.  Q and K sit in shared memory with the channel
-// outermost, so that a channel's 4 + 4 operands of 16 products are two 16-byte reads.  V takes K's
-// place once the scores are formed, which lets four (d = 64) or three (d = 128) CTAs share an SM: with
-// 64 queries a CTA the longest one ran alone at the end (three prompts of 512-1024 tokens, 8 heads, d =
-// 64: 128 us against %%).  Bound by the FMA pipe for large batches, by the longest CTA for small ones.
+//
+// Both products run on the warps' tensor instructions in tf32, every operand split as x = hi + lo with hi
+// the nearest tf32 (2^-11 relative) and lo = x - hi exact: a b ~ hi hi + hi lo + lo hi.  Left out are
+// lo lo (2^-22 of a b) and lo's own bits behind tf32's (2^-21), so a product is good to about 2^-20 of
+// |a b|, averaged over its terms to well below the float32 sum's own rounding at these widths.  CUDA
+// cores need two shared-memory reads for 16 products here and were bound by those (31 TFLOP/s at
+// d = 128, half of the FMA rate at best); the tensor form reads an operand once for 16 rows.
+//
+// A CTA of four warps takes 32 queries of one head and 32 keys at a time, two tiles of K and V in flight
+// (cp.async): 16 queries and 16 keys of every tile a warp, the two halves of a query's keys joined at the
+// end (a warp that sees all keys of 16 queries is alone with the longest prompts: 78 us against 62 for
+// three prompts of 512-1024 tokens, 8 heads, d = 64).  Bound by the instruction's rate, about 256
+// multiply-adds a cycle and SM: 53 TFLOP/s of attention, 159 of products (4000 tokens, 16 heads).  Rows of 4 floats more than d keep every fragment read free of bank conflicts: K's
+// (key = lane / 4, channel = lane % 4) and V's (key = 2 (lane % 4), channel = lane / 4), where keys 2 t and
+// 2 t + 1 stand in for the instruction's rows t and t + 4, so that the scores' accumulators are the
+// weights' operand as they stand.
 #include "lola_attn.cuh"
+#include "lola_tc.cuh"
 
 namespace lola {
 namespace {
 
 __device__ int32_t g_status;
 
-constexpr int kTQ = 32;        // queries per tile
-constexpr int kT = 64;         // keys per tile
+constexpr int kTQ = 32;        // queries per CTA
+constexpr int kT = 32;         // keys per tile
+constexpr int kTW = kT / 2;    // ... of a warp
 constexpr int kNT = 128;
-constexpr int kLd = kT + 4;    // row strides of the transposed tiles (16-byte aligned rows)
-constexpr int kLdQ = kTQ + 4;
 
-// R rows of one head from src on (rows from `rows` on are zero) into shared memory, transposed: channel
-// c of row r at c * LD + r
-template <int D, int R, int LD>
-__device__ __forceinline__ void load_t(float* dst, const float* src, int64_t ld, int rows, float scale) {
-    const int r = threadIdx.x % R;
-#pragma unroll 4
-    for (int c = threadIdx.x / R; c < D / 4; c += kNT / R) {
-        const float4 v = r < rows ? *reinterpret_cast<const float4*>(src + r * ld + 4 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
-        dst[(4 * c) * LD + r] = v.x * scale;
-        dst[(4 * c + 1) * LD + r] = v.y * scale;
-        dst[(4 * c + 2) * LD + r] = v.z * scale;
-        dst[(4 * c + 3) * LD + r] = v.w * scale;
-    }
+__device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
+    // (an infinity or NaN leaves a NaN in lo: the callers look for them)
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
 }
-// row-major; returns whether some value is not finite
-template <int D>
-__device__ __forceinline__ bool load_rows(float* dst, const float* src, int64_t ld, int rows) {
-    float worst = 0.f;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < kT * (D / 4); i += kNT) {
-        const int r = i / (D / 4), c = i % (D / 4);
-        const float4 v = r < rows ? *reinterpret_cast<const float4*>(src + r * ld + 4 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
-        worst = fmaf(v.x, 0.f, fmaf(v.y, 0.f, fmaf(v.z, 0.f, fmaf(v.w, 0.f, worst))));   // 0 or NaN
-        *reinterpret_cast<float4*>(dst + r * D + 4 * c) = v;
-    }
-    return worst != 0.f;
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 template <int D>
-__global__ void __launch_bounds__(kNT, D == 64 ? 4 : 3) attn_prefill_kernel(const AttnArgs a) {
-    using T = float;
-    extern __shared__ __align__(16) float sm[];
-    float* Qs = sm;                   // [D][kLdQ]
-    float* Ks = Qs + D * kLdQ;        // [D][kLd], then
-    float* Vs = Ks;                   // [kT][D]
-    float* Ps = Ks + D * kLd;         // [key][kLdQ]
-    constexpr int CW = D / 16;        // O columns per thread
-
-    const int h = blockIdx.x % (unsigned)a.Hq;
+__global__ void __launch_bounds__(kNT, D == 64 ? 3 : 2) attn_f32_kernel(const AttnArgs a) {
+    constexpr int LD = D + 4, TILE = kT * LD;
+    extern __shared__ __align__(16) float sm[];       // [2][K, V][kT][LD]
+    const int h = blockIdx.x % (unsigned)a.Hq, hk = h / a.G;
     TilePos at;
     const bool live = find_tile<kNT, kTQ>(a, (int)(blockIdx.x / (unsigned)a.Hq), &at);
     if (at.bad) atomicOr(&g_status, (int)LOLA_ATTN_BAD_OFFSETS);
     if (!live) return;
-    const int q0 = at.q0, lq = at.lq, k0 = at.k0, lk = at.lk;
-    const int r0 = at.tile * kTQ, rows = min(kTQ, lq - r0), shift = lk - lq;
+    const int q0 = at.q0, lq = at.lq, k0 = at.k0, lk = at.lk, shift = lk - lq;
+    const int r0 = at.tile * kTQ, rows = min(kTQ, lq - r0);
     const int keys = max(0, min(lk, r0 + rows + shift));      // keys some row of the tile sees
+    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, g = lane >> 2, t = lane & 3;
+    const int row0 = r0 + 16 * (warp & 1) + g;                // this thread's rows: row0, row0 + 8
+    const int kw = (warp >> 1) * kTW;                         // this warp's keys of a tile
+    const int last[2] = {min(row0 + shift, lk - 1), min(row0 + 8 + shift, lk - 1)};   // their last keys
 
-    const T* Q = reinterpret_cast<const T*>(a.Q.data) + (int64_t)(q0 + r0) * a.Q.row + (int64_t)h * a.Q.head;
-    const T* K = reinterpret_cast<const T*>(a.K.data) + (int64_t)k0 * a.K.row + (int64_t)(h / a.G) * a.K.head;
-    const T* V = reinterpret_cast<const T*>(a.V.data) + (int64_t)k0 * a.V.row + (int64_t)(h / a.G) * a.V.head;
-    load_t<D, kTQ, kLdQ>(Qs, Q, a.Q.row, rows, a.scale_log2);
-
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;   // rows 4 ty .., keys 4 tx .., columns
-    float m[4], l[4], acc[4][CW];
+    const float* Q = reinterpret_cast<const float*>(a.Q.data) + (int64_t)q0 * a.Q.row + (int64_t)h * a.Q.head;
+    const float* K = reinterpret_cast<const float*>(a.K.data) + (int64_t)k0 * a.K.row + (int64_t)hk * a.K.head;
+    const float* V = reinterpret_cast<const float*>(a.V.data) + (int64_t)k0 * a.V.row + (int64_t)hk * a.V.head;
+    // tile j into its half of shared memory; rows behind the keys are zeros
+    auto load = [&](int j) {
+        float* dst = sm + (j & 1) * 2 * TILE;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        m[i] = -INFINITY;
-        l[i] = 0.f;
-#pragma unroll
-        for (int c = 0; c < CW; ++c) acc[i][c] = 0.f;
-    }
-    for (int j0 = 0; j0 < keys; j0 += kT) {
-        const int nk = min(kT, keys - j0);
-        __syncthreads();
-        load_t<D, kT, kLd>(Ks, K + (int64_t)j0 * a.K.row, a.K.row, nk, 1.f);
-        __syncthreads();
-        float s[4][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 8
-        for (int c = 0; c < D; ++c) {
-            const float4 q = *reinterpret_cast<const float4*>(Qs + c * kLdQ + 4 * ty);
-            const float4 k = *reinterpret_cast<const float4*>(Ks + c * kLd + 4 * tx);
-            const float qv[4] = {q.x, q.y, q.z, q.w}, kv[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[i][j] = fmaf(qv[i], kv[j], s[i][j]);
+        for (int x = 0; x < kT * D / 4 / kNT; ++x) {
+            const int e = threadIdx.x + x * kNT, r = e / (D / 4), c = e % (D / 4) * 4, key = j * kT + r;
+            const uint32_t n = key < keys ? 16u : 0u;
+            const int64_t src = n ? key : 0;
+            tc::cp_async16_z(tc::smem_u32(dst + r * LD + c), K + src * a.K.row + c, n);
+            tc::cp_async16_z(tc::smem_u32(dst + TILE + r * LD + c), V + src * a.V.row + c, n);
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    const int tiles = (keys + kT - 1) / kT;
+    if (tiles > 0) load(0);
+    float q[D / 8][4];                                        // this warp's rows as the A operand, scaled
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int last = r0 + 4 * ty + i + shift;         // the row's last key
+    for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = row0 + 8 * (e & 1);
+            q[x][e] = r < lq ? Q[(int64_t)r * a.Q.row + 8 * x + t + 4 * (e >> 1)] * a.scale_log2 : 0.f;
+        }
+    float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[x][e] = 0.f;
+    for (int j = 0; j < tiles; ++j) {
+        if (j + 1 < tiles) load(j + 1);
+        else asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads();
+        const float* Ks = sm + (j & 1) * 2 * TILE;
+        float* Vs = sm + (j & 1) * 2 * TILE + TILE;
+        // values that are not finite (x 0 is then not 0) would reach rows that do not see them
+        float worst = 0.f;
+#pragma unroll
+        for (int x = 0; x < kT * D / 4 / kNT; ++x) {
+            const int e = threadIdx.x + x * kNT;
+            const float4 v = *reinterpret_cast<const float4*>(Vs + e / (D / 4) * LD + e % (D / 4) * 4);
+            worst = fmaf(v.x, 0.f, fmaf(v.y, 0.f, fmaf(v.z, 0.f, fmaf(v.w, 0.f, worst))));
+        }
+        // ---- S: 16 rows x 16 keys ----
+        float s[kTW / 8][4] = {}, sl[kTW / 8][4] = {};
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x) {
+            uint32_t ah[4], al[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split(q[x][e], ah[e], al[e]);
+#pragma unroll
+            for (int n = 0; n < kTW / 8; ++n) {
+                const float* kp = Ks + (kw + 8 * n + g) * LD + 8 * x + t;
+                uint32_t h0, l0, h1, l1;
+                split(kp[0], h0, l0);
+                split(kp[4], h1, l1);
+                mma_tf32(sl[n], ah, l0, l1);
+                mma_tf32(sl[n], al, h0, h1);
+                mma_tf32(s[n], ah, h0, h1);
+            }
+        }
+        bool nan = false;
+#pragma unroll
+        for (int n = 0; n < kTW / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[n][e] += sl[n][e];
+                nan |= s[n][e] != s[n][e];
+            }
+        if (__any_sync(0xffffffffu, nan)) {
+            // a query or key is not finite: these scores once more, term by term
+#pragma unroll
+            for (int n = 0; n < kTW / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = row0 + 8 * (e >> 1);
+                    const float* kp = Ks + (kw + 8 * n + 2 * t + (e & 1)) * LD;
+                    float x = 0.f;
+                    if (r < lq)
+#pragma unroll 1
+                        for (int c = 0; c < D; ++c) x = fmaf(Q[(int64_t)r * a.Q.row + c] * a.scale_log2, kp[c], x);
+                    s[n][e] = x;
+                }
+        }
+        // ---- masks, running maximum, weights ----
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
             float mx = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int key = j0 + 4 * tx + j;
-                if (key > last || key >= keys) s[i][j] = -INFINITY;
-                mx = fmaxf(mx, s[i][j]);
-            }
+            for (int n = 0; n < kTW / 8; ++n)
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const float mn = fmaxf(m[i], mx), base = mn == -INFINITY ? 0.f : mn;
-            const float f = exp2f(m[i] - base);
+                for (int e = 0; e < 2; ++e) {
+                    if (j * kT + kw + 8 * n + 2 * t + e > last[r]) s[n][2 * r + e] = -INFINITY;
+                    mx = fmaxf(mx, s[n][2 * r + e]);
+                }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float mn = fmaxf(m[r], mx), base = mn == -INFINITY ? 0.f : mn, f = exp2f(m[r] - base);
+            m[r] = mn;
             float sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                s[i][j] = exp2f(s[i][j] - base);
-                sum += s[i][j];
-            }
+            for (int n = 0; n < kTW / 8; ++n)
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            l[i] = l[i] * f + sum;
-            m[i] = mn;
-#pragma unroll
-            for (int c = 0; c < CW; ++c) acc[i][c] *= f;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<float4*>(Ps + (4 * tx + j) * kLdQ + 4 * ty) =
-                make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
-        __syncthreads();                                      // (K is read)
-        const bool any_odd = __syncthreads_or(load_rows<D>(Vs, V + (int64_t)j0 * a.V.row, a.V.row, nk));
-        if (!any_odd) {
-#pragma unroll 4
-            for (int j = 0; j < kT; ++j) {
-                const float4 p = *reinterpret_cast<const float4*>(Ps + j * kLdQ + 4 * ty);
-                const float pv[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-                for (int c4 = 0; c4 < CW / 4; ++c4) {
-                    const float4 v = *reinterpret_cast<const float4*>(Vs + j * D + 64 * c4 + 4 * tx);
-                    const float vv[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[i][4 * c4 + e] = fmaf(pv[i], vv[e], acc[i][4 * c4 + e]);
+                for (int e = 0; e < 2; ++e) {
+                    s[n][2 * r + e] = exp2f(s[n][2 * r + e] - base);
+                    sum += s[n][2 * r + e];
                 }
+            l[r] = l[r] * f + sum;                            // (this thread's keys; joined at the end)
+            if (__any_sync(0xffffffffu, f != 1.f))
+#pragma unroll
+                for (int x = 0; x < D / 8; ++x) {
+                    o[x][2 * r] *= f;
+                    o[x][2 * r + 1] *= f;
+                }
+        }
+        const bool odd = __syncthreads_or(worst != 0.f);
+        if (odd) {
+            for (int e = threadIdx.x; e < kT * D; e += kNT) {
+                float* v = Vs + e / D * LD + e % D;
+                if (!(fabsf(*v) <= 3.402823466e38f)) *v = 0.f;
             }
-        } else {
-            // a value of the tile is not finite: only the keys a row sees may touch it
-            for (int j = 0; j < nk; ++j)
+            __syncthreads();
+        }
+        // ---- O += P V: keys 2 t and 2 t + 1 of eight as the instruction's t and t + 4 ----
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (j0 + j <= r0 + 4 * ty + i + shift) {
-                        const float p = Ps[j * kLdQ + 4 * ty + i];
+        for (int n = 0; n < kTW / 8; ++n) {
+            uint32_t ph[4], pl[4];
+            split(s[n][0], ph[0], pl[0]);
+            split(s[n][2], ph[1], pl[1]);
+            split(s[n][1], ph[2], pl[2]);
+            split(s[n][3], ph[3], pl[3]);
+            const float* vp = Vs + (kw + 8 * n + 2 * t) * LD + g;
 #pragma unroll
-                        for (int c = 0; c < CW; ++c)
-                            acc[i][c] = fmaf(p, Vs[j * D + 64 * (c / 4) + 4 * tx + (c & 3)], acc[i][c]);
+            for (int x = 0; x < D / 8; ++x) {
+                uint32_t h0, l0, h1, l1;
+                split(vp[8 * x], h0, l0);
+                split(vp[LD + 8 * x], h1, l1);
+                mma_tf32(o[x], ph, l0, l1);
+                mma_tf32(o[x], pl, h0, h1);
+                mma_tf32(o[x], ph, h0, h1);
+            }
+        }
+        if (odd) {
+            // what was zeroed, for the keys a row sees
+#pragma unroll 1
+            for (int k = kw; k < kw + kTW && j * kT + k < keys; ++k)
+#pragma unroll
+                for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float v = V[(int64_t)(j * kT + k) * a.V.row + 8 * x + 2 * t + (e & 1)];
+                        if (!(fabsf(v) <= 3.402823466e38f) && j * kT + k <= last[e >> 1]) o[x][e] += v;
                     }
         }
+        __syncthreads();                                      // (the tile is read)
     }
-    T* O = reinterpret_cast<T*>(a.O.data) + (int64_t)(q0 + r0) * a.O.row + (int64_t)h * a.O.head;
+    // ---- the two halves of the keys: warps 2, 3 hand theirs to warps 0, 1 ----
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 4 * ty + i;
-        if (r >= rows) continue;
-        const bool none = r0 + r + shift < 0;                 // the row sees no key
-        const float inv = 1.f / l[i];
+    for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    float* half = sm + (warp & 1) * 16 * (D + 2);             // o, m, l of 16 rows (lane by lane, not by row)
+    if (warp >= 2) {
 #pragma unroll
-        for (int c4 = 0; c4 < CW / 4; ++c4)
+        for (int x = 0; x < D / 8; ++x)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                IO<T>::st(O, r * a.O.row + 64 * c4 + 4 * tx + e, none ? 0.f : acc[i][4 * c4 + e] * inv);
-        if (a.lse && tx == 0)
-            a.lse[(int64_t)h * a.total_q + q0 + r0 + r] = none ? -INFINITY : (m[i] + log2f(l[i])) * kAttnLn2;
+            for (int e = 0; e < 4; ++e) half[(4 * x + e) * 32 + lane] = o[x][e];
+        if (t == 0)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                half[16 * D + 8 * r + g] = m[r];
+                half[16 * D + 16 + 8 * r + g] = l[r];
+            }
+    }
+    __syncthreads();
+    if (warp >= 2) return;
+    float* O = reinterpret_cast<float*>(a.O.data) + (int64_t)q0 * a.O.row + (int64_t)h * a.O.head;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int row = row0 + 8 * r;
+        const float m1 = half[16 * D + 8 * r + g], l1 = half[16 * D + 16 + 8 * r + g];
+        const float mn = fmaxf(m[r], m1), base = mn == -INFINITY ? 0.f : mn;
+        const float f0 = exp2f(m[r] - base), f1 = exp2f(m1 - base), ls = l[r] * f0 + l1 * f1;
+        if (row >= lq) continue;
+        const bool none = last[r] < 0;                        // the row sees no key
+        const float inv = 1.f / ls;
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x) {
+            float y[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                y[e] = none ? 0.f : (o[x][2 * r + e] * f0 + half[(4 * x + 2 * r + e) * 32 + lane] * f1) * inv;
+            *reinterpret_cast<float2*>(O + (int64_t)row * a.O.row + 8 * x + 2 * t) = make_float2(y[0], y[1]);
+        }
+        if (a.lse && t == 0)
+            a.lse[(int64_t)h * a.total_q + q0 + row] = none ? -INFINITY : (mn + log2f(ls)) * kAttnLn2;
     }
 }
 
 template <int D>
 cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
-    const size_t smem = sizeof(float) * (D * kLdQ + D * kLd + kT * kLdQ);
+    const size_t smem = sizeof(float) * 4 * kT * (D + 4);
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = opt_in_smem(attn_prefill_kernel<D>, (int)smem, done);
+    cudaError_t e = opt_in_smem(attn_f32_kernel<D>, (int)smem, done);
     if (e != cudaSuccess) return e;
     // at most this many tiles for any cut of total_q rows into n_seq sequences
     const int64_t tiles = ((int64_t)a.total_q + (int64_t)a.n_seq * (kTQ - 1)) / kTQ;
-    attn_prefill_kernel<D><<<(unsigned)(tiles * a.Hq), kNT, smem, st>>>(a);
+    attn_f32_kernel<D><<<(unsigned)(tiles * a.Hq), kNT, smem, st>>>(a);
     return cudaGetLastError();
 }
 
