@@ -24,14 +24,15 @@
 //     are zeroed in shared memory before the product (0 x NaN would reach rows that do not see
 //     them); the values taken out are added back in the epilogue, for the rows that see them.
 // What bounds it: for long sequences the tensor core and its power (16 heads of 32768 tokens, d = 128:
-// 2.73 ms, 1608 TFLOP/s, 87 % of the measured bf16 product; 4 x 4096 x 32 heads 417 us, 1318 TFLOP/s): a
+// 2.68 ms, 1640 TFLOP/s, 89 % of the measured bf16 product; 4 x 4096 x 32 heads 412 us, 1333 TFLOP/s): a
 // block pair's products take about 2300 cycles of the issuing thread's 2700, the rest is its wait for
 // the weights (a softmax is 1100 cycles, behind it the other tile's products).  At d = 64 the
-// exponentials weigh twice as much against the products (1037 TFLOP/s); short sequences are bound by an
+// exponentials weigh twice as much against the products (1060 TFLOP/s); short sequences are bound by an
 // item's own chain: scores, weights, product, epilogue.
 // Tried and slower: releasing P in halves, comparing S by column groups while it loads, one MMA thread
-// for each tile (their products interleave, 9 %), the next pair's waits between the products, and one
-// block per CTA without taking over others (4 x 4096 x 32 heads 457 us, ragged prompts 362 against 335).
+// for each tile (their products interleave, 9 %), the next pair's waits between the products, one block
+// per CTA without taking over others (4 x 4096 x 32 heads 457 us, ragged prompts 362 against 332), and
+// all sequences' longest tiles first (their K and V no longer fit L2 together: 427 us).
 // Every wait is bounded (1 s, those that may last a whole item 10 s, then LOLA_ATTN_TIMEOUT).
 #include <cuda.h>
 
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(sm);
     enum {
-        B_ITEM = 0, B_ITEMFREE = 2, B_STEAL = 4, B_Q = 5, B_QFREE = B_Q + NT, B_S = B_QFREE + NT, B_P = B_S + NT, B_O = B_P + NT,
+        B_ITEM = 0, B_ITEMFREE = 2, B_STEAL = 4, B_LOADED = 5, B_Q = 6, B_QFREE = B_Q + NT, B_S = B_QFREE + NT, B_P = B_S + NT, B_O = B_P + NT,
         B_DONE = B_O + NT, B_FULL, B_EMPTY = B_FULL + kCap, B_ARMED = B_EMPTY + kCap, B_CLEAN = B_ARMED + kClean,
         B_N = B_CLEAN + kClean
     };
@@ -242,6 +243,7 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
             mbar_init(bar(B_ITEMFREE + i), 4 * NT + 3);     // softmax warps, MMA, loader, cleaner
         }
         mbar_init(bar(B_STEAL), 1);
+        mbar_init(bar(B_LOADED), 1);
         for (int i = 0; i < NT; ++i) {
             mbar_init(bar(B_Q + i), 1);
             mbar_init(bar(B_QFREE + i), 1);
@@ -315,8 +317,7 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
         if (warp == C::kItemWarp) {
             // ================================ items ================================
             // This CTA's own block first, then blocks of the grid that have not started, one ahead of the
-            // work: no CTA has more than one item waiting, and none starts, looks tiles up or loads its
-            // first tiles while the tensor core waits.
+            // work: none looks tiles up or loads its first tiles while the tensor core waits.
             if (NT == 2) find.start(a, lane);
             bool ok = true, more = true;
             uint32_t block = blockIdx.x;
@@ -341,10 +342,11 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
                     }
                     __syncwarp();
                     ++n;
+                    // the next block is taken when this one's last load is under way, and not before: an
+                    // item that waits for a CTA busy with long ones would be missed elsewhere at the end
+                    ok = __all_sync(0xffffffffu, wait_for(B_LOADED, (uint32_t)(n - 1) & 1u, kItemNs));
+                    if (!ok) break;
                 }
-                // (a slot is free before the next block is taken)
-                if (n >= 2) ok = __all_sync(0xffffffffu, wait_for(B_ITEMFREE + (n & 1), (uint32_t)(n / 2 - 1) & 1u, kItemNs));
-                if (!ok) break;
                 if (lane == 0) {
                     mbar_expect(bar(B_STEAL), 16);
                     steal_block(smem_u32(&stolen), bar(B_STEAL));
@@ -356,6 +358,8 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
                 fence_async_smem();                                    // (read before the next answer lands there)
                 __syncwarp();
             }
+            // the end: an item that is none
+            if (ok && n >= 2) ok = __all_sync(0xffffffffu, wait_for(B_ITEMFREE + (n & 1), (uint32_t)(n / 2 - 1) & 1u, kItemNs));
             if (ok && lane == 0) {
                 items[n & 1].live = 0;
                 mbar_arrive1(bar(B_ITEM + (n & 1)));
@@ -394,7 +398,10 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
                             if (p == 0 && NT == 2) load_q(NT - 1);
                         }
                     }
-                    if (ok) mbar_arrive1(bar(B_ITEMFREE + (n & 1)));
+                    if (ok) {
+                        mbar_arrive1(bar(B_LOADED));
+                        mbar_arrive1(bar(B_ITEMFREE + (n & 1)));
+                    }
                 }
                 // leave no copy in flight
                 for (int x = max(0, P - kCap); x < P; ++x) mbar_wait(bar(full_of(x)), phase(x), kWaitNs);

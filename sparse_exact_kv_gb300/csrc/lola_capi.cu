@@ -685,7 +685,9 @@ int32_t lola_attn_prefill(const lola_attn_config* cfg, int32_t n_seq, int32_t to
     if (!rows_ok(cfg, Q, total_q, cfg->Hq, false) || !rows_ok(cfg, O, total_q, cfg->Hq, true)) return LOLA_ERR_INVALID_ARG;
     if (total_k > 0 && (!rows_ok(cfg, K, total_k, cfg->Hkv, false) || !rows_ok(cfg, V, total_k, cfg->Hkv, false)))
         return LOLA_ERR_INVALID_ARG;
-    if (((int64_t)total_q / 32 + n_seq) * cfg->Hq > 0x40000000) return LOLA_ERR_UNSUPPORTED;   // the grid
+    // row numbers a block behind the last stay inside 32 bits; the grid
+    if (total_q > 0x7fff0000 || total_k > 0x7fff0000) return LOLA_ERR_UNSUPPORTED;
+    if (((int64_t)total_q / 32 + n_seq) * cfg->Hq > 0x40000000) return LOLA_ERR_UNSUPPORTED;
     AttnArgs a;
     a.n_seq = n_seq;
     a.total_q = total_q;

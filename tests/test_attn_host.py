@@ -90,6 +90,7 @@ def test_prefill_refusals(L):
         assert prefill(L, **kw) == E, kw
     assert prefill(L, c=cfg(L, Hq=1 << 20, Hkv=1), tq=1 << 30, tk=1 << 30, o=rows(L, row=1 << 27)) in \
         (L.LOLA_ERR_UNSUPPORTED, E)
+    assert prefill(L, tk=0x7fffffff, k=rows(L, row=128), v=rows(L, row=128)) == L.LOLA_ERR_UNSUPPORTED
     # nothing to do is not an error, and touches nothing
     assert prefill(L, tq=0, tk=0, q=rows(L, data=0), o=rows(L, data=0)) == 0
 
