@@ -363,11 +363,17 @@ def _stream_of(stream, index):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _table_stride(table):
+    """The rows' stride (one row's is any; rows that overlap, as an expanded table's do, are refused by
+    the library)."""
+    n, width = table.shape
+    return width if n == 1 else table.stride(0)
+
+
 def _paged(k_pool, v_pool, kv_len, table):
     pages, _, page, _ = k_pool.shape
     n, width = table.shape
-    stride = table.stride(0)
-    return lola_paged_kv(k_pool.data_ptr(), v_pool.data_ptr(), pages, page, n, width, stride if stride > width else width,
+    return lola_paged_kv(k_pool.data_ptr(), v_pool.data_ptr(), pages, page, n, width, _table_stride(table),
                          table.data_ptr(), kv_len.data_ptr())
 
 
@@ -535,13 +541,13 @@ class ExactAttention:
         pool = self.k_pool
         if pool is None:
             raise ValueError("this layer has no key-value pools")
-        dev, (n, width), (stride, one) = pool.device, table.shape, table.stride()
+        dev, (n, width), one = pool.device, table.shape, table.stride(1)
         self._vector(kv_len, n, dev, "kv_len")
         if table.dtype != torch.int32 or table.device != dev or (one != 1 and width != 1):
             raise ValueError(f"table: want int32 [{n}, width] on {dev}, rows contiguous")
         pages, _, page, _ = pool.shape
         return lola_paged_kv(pool.data_ptr(), self.v_pool.data_ptr(), pages, page, n, width,
-                             stride if stride > width else width, table.data_ptr(), kv_len.data_ptr()), dev, n, _index_of(dev)
+                             _table_stride(table), table.data_ptr(), kv_len.data_ptr()), dev, n, _index_of(dev)
 
     def append(self, k, v, kv_len, table, cu_new=None, q=None, inv_freq=None, q_out=None, pairs="halves",
                positions=None, stream=None):

@@ -133,7 +133,7 @@ bool cache(PyObject* k_pool, PyObject* v_pool, PyObject* kv_len, PyObject* table
     kv->page = (int32_t)k.n[2];
     kv->n_seq = (int32_t)t.n[0];
     kv->width = (int32_t)t.n[1];
-    kv->table_stride = t.stride[0] > t.n[1] ? t.stride[0] : t.n[1];
+    kv->table_stride = t.n[0] == 1 ? t.n[1] : t.stride[0];
     kv->table = (const int32_t*)t.data;
     kv->kv_len = (const int32_t*)n.data;
     return true;

@@ -161,6 +161,21 @@ def test_positions_never_leave_the_pool(L):
             assert got == -1 or 0 <= got <= n_pages * Hkv * page * d - d
 
 
+def test_page_tables_whose_rows_overlap_are_refused(L, monkeypatch):
+    """An expanded table's rows have a stride of 0: the library gets it as it is, and refuses it."""
+    pool = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    row, lens = torch.zeros(1, 3, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    wide = torch.zeros(3, 5, dtype=torch.int32)
+    lay = L.ExactAttention(4, 2, 64, torch.bfloat16, pool, pool.clone())
+    monkeypatch.setattr(L, "_index_of", lambda dev: 0)
+    for table, stride in ((row.expand(2, 3), 0), (wide.as_strided((2, 3), (2, 1)), 2), (wide[:2, :3], 5)):
+        for kv in (L._paged(pool, pool, lens, table), lay._cache(lens, table)[0]):
+            assert kv.table_stride == stride
+            assert (L.lola_paged_slot(lay.cfg, kv, 1, 0, 0) >= 0) == (stride >= 3)
+    for table in (row, row.expand(1, 3), wide[:1, :3], wide.as_strided((1, 3), (1, 1))):      # one row: any stride
+        assert L.lola_paged_slot(lay.cfg, lay._cache(lens[:1], table)[0], 0, 0, 0) == 0
+
+
 def test_layer_refuses_other_tensors(L):
     """The class checks shapes, types and devices before the library is called."""
     bf, f32 = torch.bfloat16, torch.float32

@@ -665,6 +665,21 @@ def test_refused_calls_say_what_is_wrong(L, gen):
     assert torch.equal(again, good) and sys.getrefcount(again) == sys.getrefcount(good)
 
 
+def test_page_tables_whose_rows_overlap_are_refused(L, gen):
+    """One row of pages for every sequence, expanded: refused; a copy of it serves."""
+    c = Paged(gen, [30], 2, 64, 16, BF)
+    lay = L.ExactAttention(4, 2, 64, BF, c.k_pool, c.v_pool)
+    q, k, lens = randn(gen, 3, 4, 64, dtype=BF), randn(gen, 3, 2, 64, dtype=BF), ints([30, 30, 30])
+    shared = c.table[:1].expand(3, -1)
+    with pytest.raises(L.LolaError):
+        lay.decode_step(q, lens, shared)
+    with pytest.raises(L.LolaError):
+        lay.append(k, k, lens, shared)
+    got = lay.decode_step(q, lens, shared.contiguous())
+    quiet(L)
+    assert torch.equal(got[1], lay.decode_step(q[1:2], lens[:1], shared[:1])[0])
+
+
 def test_kernel_timing_counts_the_new_kernels(L, gen):
     c = Paged(gen, [200], 1, 64, 16, BF)
     lay = L.ExactAttention(1, 1, 64, BF, c.k_pool, c.v_pool)
