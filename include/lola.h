@@ -399,7 +399,8 @@ typedef struct {
  *   lse   nullable device float32 [Hq, total_q]
  * Rows of Q outside cu_q[0] .. cu_q[n_seq] are left as they were in O and lse.  Offsets that
  * decrease or pass total_q / total_k make their sequence empty and set LOLA_ATTN_BAD_OFFSETS.
- * total_q = 0 is a call that does nothing.  Stream-ordered; no workspace. */
+ * O may be Q itself (the same rows) and otherwise overlaps no input.  total_q = 0 is a call that does
+ * nothing.  Stream-ordered; no workspace. */
 int32_t lola_attn_prefill(const lola_attn_config* cfg, int32_t n_seq, int32_t total_q, int32_t total_k,
                           const int32_t* cu_q, const int32_t* cu_k, const lola_rows* Q, const lola_rows* K,
                           const lola_rows* V, const lola_rows* O, float* lse, void* stream);
@@ -455,7 +456,8 @@ int32_t lola_paged_append(const lola_attn_config* cfg, const lola_paged_kv* kv, 
 int64_t lola_paged_decode_workspace_bytes(const lola_attn_config* cfg);
 
 /* Attention of one query token per sequence over its kv_len cached tokens (the token's own key
- * included, when it was appended before).  Row b of Q and O is sequence b.
+ * included, when it was appended before).  Row b of Q and O is sequence b; O may be Q itself (the
+ * same rows) and otherwise overlaps no input.
  *   lse  nullable device float32 [n_seq, Hq]
  *   workspace  device, 16-byte aligned; its contents mean nothing before or after the call, and
  *        calls that may run at the same time need one each

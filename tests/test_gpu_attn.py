@@ -680,6 +680,23 @@ def test_page_tables_whose_rows_overlap_are_refused(L, gen):
     assert torch.equal(got[1], lay.decode_step(q[1:2], lens[:1], shared[:1])[0])
 
 
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 128), (F32, 64)])
+def test_outputs_in_place_of_the_queries(L, gen, dtype, d):
+    """The same bits as into other memory, for prompts of both forms and for single tokens."""
+    lay = L.ExactAttention(6, 2, d, dtype)
+    for lens in ([700, 130, 1, 391], [3000, 2500, 1200, 17] * 4):
+        q, k = randn(gen, sum(lens), 6, d, dtype=dtype), randn(gen, sum(lens), 2, d, dtype=dtype)
+        want = lay.prefill(q, k, k, offsets(lens))
+        assert lay.prefill(q, k, k, offsets(lens), out=q) is q and torch.equal(q, want)
+    lens = [4000, 3, 0, 777]
+    c = Paged(gen, lens, 2, d, 64, dtype)
+    lay = L.ExactAttention(6, 2, d, dtype, c.k_pool, c.v_pool)
+    q = randn(gen, 4, 6, d, dtype=dtype)
+    want = lay.decode_step(q, c.kv_len, c.table)
+    assert lay.decode_step(q, c.kv_len, c.table, out=q) is q and torch.equal(q, want)
+    quiet(L)
+
+
 def test_kernel_timing_counts_the_new_kernels(L, gen):
     c = Paged(gen, [200], 1, 64, 16, BF)
     lay = L.ExactAttention(1, 1, 64, BF, c.k_pool, c.v_pool)
