@@ -451,6 +451,18 @@ int32_t lola_paged_append(const lola_attn_config* cfg, const lola_paged_kv* kv, 
                           const lola_rows* QO, const float* inv_freq, int32_t rot, int32_t pairs,
                           const int32_t* positions, void* stream);
 
+/* Causal attention of packed prompts, or of later pieces of them, over the cache: sequence b has the
+ * query rows cu_q[b] .. cu_q[b+1] and its kv_len tokens in the cache as keys and values (the queries'
+ * own included, appended before); the last query sees all of them and each earlier query one less,
+ * as in lola_attn_prefill.
+ *   total_k  the sum of kv_len where the caller knows it, else 0: only the choice between two forms
+ *            of the kernel depends on it
+ *   lse, O and rows outside cu_q  as in lola_attn_prefill
+ * A page outside the cache counts as zero keys and values and sets LOLA_ATTN_BAD_PAGE; a kv_len
+ * beyond width * page sets it too and counts as width * page. */
+int32_t lola_paged_prefill(const lola_attn_config* cfg, const lola_paged_kv* kv, int32_t total_q, int32_t total_k,
+                           const int32_t* cu_q, const lola_rows* Q, const lola_rows* O, float* lse, void* stream);
+
 /* Bytes of device workspace a lola_paged_decode needs (negative: the lola_status of an invalid
  * cfg).  It does not depend on the cache's lengths. */
 int64_t lola_paged_decode_workspace_bytes(const lola_attn_config* cfg);

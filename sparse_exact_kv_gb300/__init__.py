@@ -49,7 +49,8 @@ EXPORTS = ("lola_version", "lola_status_string", "lola_last_cuda_error", "lola_c
            "lola_prefill", "lola_decode_step", "lola_read_status", "lola_kernel_timing", "lola_kernel_time",
            "lola_kernel_name", "lola_prefill_noalloc", "lola_selftest_bounded_wait", "lola_sre_map",
            "lola_sre_map_relative", "lola_hola_workspace_bytes", "lola_hola_prefill", "lola_hola_status",
-           "lola_attn_prefill", "lola_paged_slot", "lola_paged_append", "lola_paged_decode_workspace_bytes",
+           "lola_attn_prefill", "lola_paged_slot", "lola_paged_append", "lola_paged_prefill",
+           "lola_paged_decode_workspace_bytes",
            "lola_paged_decode", "lola_attn_status")
 # size of the fixed scratch array behind lola_prefill_noalloc (include/lola.h)
 LOLA_NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -136,6 +137,7 @@ def _load():
         "lola_hola_status": ([HC, ctypes.c_int32, P, P, P], ctypes.c_int32),
         "lola_attn_prefill": ([AC] + [ctypes.c_int32] * 3 + [P, P, R, R, R, R, P, P], ctypes.c_int32),
         "lola_paged_slot": ([AC, PK, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64], ctypes.c_int64),
+        "lola_paged_prefill": ([AC, PK, ctypes.c_int32, ctypes.c_int32, P, R, R, P, P], ctypes.c_int32),
         "lola_paged_append": ([AC, PK, ctypes.c_int32, P, R, R, R, R, P, ctypes.c_int32, ctypes.c_int32, P, P],
                               ctypes.c_int32),
         "lola_paged_decode_workspace_bytes": ([AC], ctypes.c_int64),
@@ -400,6 +402,14 @@ def lola_paged_append(cfg: lola_attn_config, kv: lola_paged_kv, K, V, cu_new=Non
         raise LolaError(st, "lola_paged_append")
 
 
+def lola_paged_prefill(cfg: lola_attn_config, kv: lola_paged_kv, Q, O, cu_q, total_k=0, lse=None, stream=None) -> None:
+    """Q, O: [total_q, Hq, d]; cu_q: int32 [n_seq + 1]; total_k: the tokens of all sequences, if known."""
+    st = _lib.lola_paged_prefill(cfg, kv, Q.shape[0], total_k, cu_q.data_ptr(), _rows(Q), _rows(O), _addr(lse),
+                                 _stream_of(stream, Q.get_device()))
+    if st:
+        raise LolaError(st, "lola_paged_prefill")
+
+
 def lola_paged_decode_workspace_bytes(cfg: lola_attn_config) -> int:
     b = _lib.lola_paged_decode_workspace_bytes(ctypes.byref(cfg))
     if b < 0:
@@ -589,6 +599,32 @@ class ExactAttention:
         if st:
             raise LolaError(st, "lola_paged_append")
         return q_out
+
+    def prefill_paged(self, q, cu_q, kv_len, table, total_k=0, out=None, lse=None, stream=None):
+        """Causal attention of packed prompts, or later pieces of them, over the cache: q [total_q, Hq, d]
+        with the rows cu_q int32 [n_seq + 1] of each sequence, whose kv_len tokens (the queries' own
+        included, appended before) are read from their pages.  ``total_k``: the sum of kv_len where it
+        is known (it only helps to choose the kernel's form).  Returns out [total_q, Hq, d]; ``lse`` as
+        in ``prefill``."""
+        if out is None and lse is None and stream is None:
+            out = _fast.prefill_paged(self._plan, self.k_pool, self.v_pool, q, cu_q, kv_len, table, total_k)
+            if out is not NotImplemented:
+                return out
+            out = None
+        kv, dev, n_seq, index = self._cache(kv_len, table)
+        n = q.shape[0]
+        rq = self._heads(q, self.Hq, n, dev, "q")
+        self._vector(cu_q, n_seq + 1, dev, "cu_q")
+        if lse is not None:
+            self._lse(lse, (self.Hq, n), dev)
+        if out is not None:
+            ro = self._heads(out, self.Hq, n, dev, "out")
+        else:
+            out, ro = self._like(q, stream)
+        st = _lib.lola_paged_prefill(self.cfg, kv, n, total_k, cu_q.data_ptr(), rq, ro, _addr(lse), _stream_of(stream, index))
+        if st:
+            raise LolaError(st, "lola_paged_prefill")
+        return out
 
     def decode_step(self, q, kv_len, table, out=None, lse=None, workspace=None, stream=None):
         """One query token per sequence, q [n_seq, Hq, d], over its kv_len cached tokens; returns out

@@ -1,4 +1,5 @@
-// K8 (float32): causal softmax attention over packed prompts.
+// K8 (float32): causal softmax attention over packed prompts, keys and values packed too or in the pages of
+// a cache.
 //
 // Row i of a sequence with Lq queries and Lk keys sees the keys j <= i + Lk - Lq.  One pass over
 // the keys with a running maximum m and sum l per row (log2 units, s = c log2(e) q . k):
@@ -45,14 +46,15 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D>
+// PG: keys and values in the pages of a cache
+template <int D, bool PG>
 __global__ void __launch_bounds__(kNT, D == 64 ? 3 : 2) attn_f32_kernel(const AttnArgs a) {
     constexpr int LD = D + 4, TILE = kT * LD;
     extern __shared__ __align__(16) float sm[];       // [2][K, V][kT][LD]
     const int h = blockIdx.x % (unsigned)a.Hq, hk = h / a.G;
     TilePos at;
-    const bool live = find_tile<kNT, kTQ>(a, (int)(blockIdx.x / (unsigned)a.Hq), &at);
-    if (at.bad) atomicOr(&g_status, (int)LOLA_ATTN_BAD_OFFSETS);
+    const bool live = find_tile<kNT, kTQ, PG>(a, (int)(blockIdx.x / (unsigned)a.Hq), &at);
+    if (at.bits) atomicOr(&g_status, at.bits);
     if (!live) return;
     const int q0 = at.q0, lq = at.lq, k0 = at.k0, lk = at.lk, shift = lk - lq;
     const int r0 = at.tile * kTQ, rows = min(kTQ, lq - r0);
@@ -63,22 +65,48 @@ __global__ void __launch_bounds__(kNT, D == 64 ? 3 : 2) attn_f32_kernel(const At
     const int last[2] = {min(row0 + shift, lk - 1), min(row0 + 8 + shift, lk - 1)};   // their last keys
 
     const float* Q = reinterpret_cast<const float*>(a.Q.data) + (int64_t)q0 * a.Q.row + (int64_t)h * a.Q.head;
-    const float* K = reinterpret_cast<const float*>(a.K.data) + (int64_t)k0 * a.K.row + (int64_t)hk * a.K.head;
-    const float* V = reinterpret_cast<const float*>(a.V.data) + (int64_t)k0 * a.V.row + (int64_t)hk * a.V.head;
-    // tile j into its half of shared memory; rows behind the keys are zeros
+    const float *K, *V;
+    if constexpr (PG) {
+        K = reinterpret_cast<const float*>(a.p.K);
+        V = reinterpret_cast<const float*>(a.p.V);
+    } else {
+        K = reinterpret_cast<const float*>(a.K.data) + (int64_t)k0 * a.K.row + (int64_t)hk * a.K.head;
+        V = reinterpret_cast<const float*>(a.V.data) + (int64_t)k0 * a.V.row + (int64_t)hk * a.V.head;
+    }
+    // the pages of a tile's halves, looked up one tile ahead; -1: none, or not in the cache
+    int pages[2] = {-1, -1};
+    auto look_up = [&](int j) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int pos = j * kT + x * 16;
+            pages[x] = pos < keys ? paged_page(a.p, at.b, pos) : -1;
+            if (pos < keys && pages[x] < 0) atomicOr(&g_status, (int)LOLA_ATTN_BAD_PAGE);
+        }
+    };
+    // tile j into its half of shared memory; rows behind the keys are zeros, and those without a page
     auto load = [&](int j) {
         float* dst = sm + (j & 1) * 2 * TILE;
 #pragma unroll
         for (int x = 0; x < kT * D / 4 / kNT; ++x) {
             const int e = threadIdx.x + x * kNT, r = e / (D / 4), c = e % (D / 4) * 4, key = j * kT + r;
-            const uint32_t n = key < keys ? 16u : 0u;
-            const int64_t src = n ? key : 0;
-            tc::cp_async16_z(tc::smem_u32(dst + r * LD + c), K + src * a.K.row + c, n);
-            tc::cp_async16_z(tc::smem_u32(dst + TILE + r * LD + c), V + src * a.V.row + c, n);
+            if constexpr (PG) {
+                const int page = r < 16 ? pages[0] : pages[1];
+                const uint32_t n = key < keys && page >= 0 ? 16u : 0u;
+                const int64_t src = n ? paged_offset(a.p, page, hk, key) + c : 0;
+                tc::cp_async16_z(tc::smem_u32(dst + r * LD + c), K + src, n);
+                tc::cp_async16_z(tc::smem_u32(dst + TILE + r * LD + c), V + src, n);
+            } else {
+                const uint32_t n = key < keys ? 16u : 0u;
+                const int64_t src = n ? key : 0;
+                tc::cp_async16_z(tc::smem_u32(dst + r * LD + c), K + src * a.K.row + c, n);
+                tc::cp_async16_z(tc::smem_u32(dst + TILE + r * LD + c), V + src * a.V.row + c, n);
+            }
         }
+        if constexpr (PG) look_up(j + 1);
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     const int tiles = (keys + kT - 1) / kT;
+    if constexpr (PG) look_up(0);
     if (tiles > 0) load(0);
     float q[D / 8][4];                                        // this warp's rows as the A operand, scaled
 #pragma unroll
@@ -210,14 +238,23 @@ __global__ void __launch_bounds__(kNT, D == 64 ? 3 : 2) attn_f32_kernel(const At
         if (odd) {
             // what was zeroed, for the keys a row sees
 #pragma unroll 1
-            for (int k = kw; k < kw + kTW && j * kT + k < keys; ++k)
+            for (int k = kw; k < kw + kTW && j * kT + k < keys; ++k) {
+                const float* row;
+                if constexpr (PG) {
+                    const int page = paged_page(a.p, at.b, j * kT + k);
+                    if (page < 0) continue;
+                    row = V + paged_offset(a.p, page, hk, j * kT + k);
+                } else {
+                    row = V + (int64_t)(j * kT + k) * a.V.row;
+                }
 #pragma unroll
                 for (int x = 0; x < D / 8; ++x)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float v = V[(int64_t)(j * kT + k) * a.V.row + 8 * x + 2 * t + (e & 1)];
+                        const float v = row[8 * x + 2 * t + (e & 1)];
                         if (!(fabsf(v) <= 3.402823466e38f) && j * kT + k <= last[e >> 1]) o[x][e] += v;
                     }
+            }
         }
         __syncthreads();                                      // (the tile is read)
     }
@@ -266,23 +303,24 @@ __global__ void __launch_bounds__(kNT, D == 64 ? 3 : 2) attn_f32_kernel(const At
     }
 }
 
-template <int D>
+template <int D, bool PG>
 cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
     const size_t smem = sizeof(float) * 4 * kT * (D + 4);
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = opt_in_smem(attn_f32_kernel<D>, (int)smem, done);
+    cudaError_t e = opt_in_smem(attn_f32_kernel<D, PG>, (int)smem, done);
     if (e != cudaSuccess) return e;
     // at most this many tiles for any cut of total_q rows into n_seq sequences
     const int64_t tiles = ((int64_t)a.total_q + (int64_t)a.n_seq * (kTQ - 1)) / kTQ;
-    attn_f32_kernel<D><<<(unsigned)(tiles * a.Hq), kNT, smem, st>>>(a);
+    attn_f32_kernel<D, PG><<<(unsigned)(tiles * a.Hq), kNT, smem, st>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t st) {
-    if (a.dtype == LOLA_F32) return a.d == 128 ? launch<128>(a, st) : launch<64>(a, st);
-    return launch_attn_tc(a, st);
+    if (a.dtype == LOLA_BF16) return launch_attn_tc(a, st);
+    if (a.p.table) return a.d == 128 ? launch<128, true>(a, st) : launch<64, true>(a, st);
+    return a.d == 128 ? launch<128, false>(a, st) : launch<64, false>(a, st);
 }
 
 cudaError_t attn_status_take(int32_t* bits, cudaStream_t st) { return take_word(g_status, bits, st); }

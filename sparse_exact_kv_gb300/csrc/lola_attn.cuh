@@ -16,17 +16,7 @@ struct Rows {
     int64_t row, head;   // elements
 };
 
-// one lola_attn_prefill
-struct AttnArgs {
-    int n_seq, total_q, total_k, Hq, G, dtype, d;
-    const int32_t* cu_q;
-    const int32_t* cu_k;
-    Rows Q, K, V, O;
-    float* lse;          // [Hq][total_q] or null
-    float scale_log2;    // c log2(e): scores are kept in log2 units
-};
-
-// a paged cache and one decode step over it
+// a paged cache
 struct PagedArgs {
     char* K;
     char* V;
@@ -37,12 +27,23 @@ struct PagedArgs {
     int Hq, Hkv, G, d, dtype;
 };
 
+// one lola_attn_prefill or lola_paged_prefill
+struct AttnArgs {
+    int n_seq, total_q, total_k, Hq, G, dtype, d;
+    const int32_t* cu_q;
+    const int32_t* cu_k;
+    Rows Q, K, V, O;
+    float* lse;          // [Hq][total_q] or null
+    float scale_log2;    // c log2(e): scores are kept in log2 units
+    PagedArgs p;         // lola_paged_prefill: the keys and values (p.table null otherwise)
+};
+
 // ---- packed sequences ----
-// Rows [begin, begin + len) of sequence b; malformed offsets make it empty (*bad set).
-__host__ __device__ inline void seq_rows(const int32_t* cu, int b, int total, int* begin, int* len, bool* bad) {
+// Rows [begin, begin + len) of sequence b; malformed offsets make it empty (and set a bit of *bits).
+__host__ __device__ inline void seq_rows(const int32_t* cu, int b, int total, int* begin, int* len, int* bits) {
     const int lo = cu[b], hi = cu[b + 1];
     if (lo < 0 || hi < lo || hi > total) {
-        *bad = true;
+        *bits |= LOLA_ATTN_BAD_OFFSETS;
         *begin = 0;
         *len = 0;
         return;
@@ -63,6 +64,19 @@ __host__ __device__ inline int paged_page(const PagedArgs& p, int b, int64_t pos
 }
 __host__ __device__ inline int64_t paged_offset(const PagedArgs& p, int page, int head, int64_t pos) {
     return (((int64_t)page * p.Hkv + head) * p.page + (pos & (p.page - 1))) * p.d;
+}
+
+// The keys of sequence b: packed rows [begin, begin + len), or its tokens in the cache (PG; begin = 0).
+template <bool PG>
+__device__ __forceinline__ void seq_keys(const AttnArgs& a, int b, int* begin, int* len, int* bits) {
+    if constexpr (PG) {
+        const int n = a.p.kv_len[b];
+        *begin = 0;
+        *len = (int)paged_tokens(a.p, n);
+        if (n > *len && n > 0) *bits |= LOLA_ATTN_BAD_PAGE;
+    } else {
+        seq_rows(a.cu_k, b, a.total_k, begin, len, bits);
+    }
 }
 
 // Piece c of n equal pieces of `total` units: [split_at(c), split_at(c + 1))
@@ -94,23 +108,22 @@ __device__ __forceinline__ I block_total(I x, I* sm) {
 // (shortest) tiles.  False if there is no such tile.  Each thread looks at one sequence of up to NT, all
 // four of its offsets at once: one round of loads, then a scan.
 struct TilePos {
-    int q0, lq, k0, lk, tile;
-    bool bad;            // some offsets are malformed (thread-local: what this thread has seen)
+    int b, q0, lq, k0, lk, tile;
+    int bits;            // what is wrong with offsets or lengths (thread-local: what this thread has seen)
 };
-template <int NT, int rows>
+template <int NT, int rows, bool PG>
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, int u, TilePos* pos) {
     __shared__ int sums[NT / kWarp];
     __shared__ TilePos found;
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
     TilePos own;
-    pos->bad = false;
+    pos->bits = 0;
     auto look = [&](int b) -> int {
+        own.b = b;
         own.q0 = own.lq = own.k0 = own.lk = 0;
         if (b >= a.n_seq) return 0;
-        bool bad = false, badk = false;
-        seq_rows(a.cu_q, b, a.total_q, &own.q0, &own.lq, &bad);
-        seq_rows(a.cu_k, b, a.total_k, &own.k0, &own.lk, &badk);
-        pos->bad |= bad | badk;
+        seq_rows(a.cu_q, b, a.total_q, &own.q0, &own.lq, &pos->bits);
+        seq_keys<PG>(a, b, &own.k0, &own.lk, &pos->bits);
         return (own.lq + rows - 1) / rows;
     };
     int n = 0;
@@ -146,9 +159,9 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int u, TilePos* pos
         before = all;
     }
     __syncthreads();
-    const bool bad = pos->bad;
+    const int bits = pos->bits;
     *pos = found;
-    pos->bad = bad;
+    pos->bits = bits;
     return true;
 }
 

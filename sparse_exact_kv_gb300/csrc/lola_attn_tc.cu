@@ -1,4 +1,5 @@
-// K8 (bf16, tensor cores): causal softmax attention over packed prompts.
+// K8 (bf16, tensor cores): causal softmax attention over packed prompts, keys and values packed too or in
+// the pages of a cache.
 //
 // Row i of a sequence with Lq queries and Lk keys sees the keys j <= i + Lk - Lq.  One pass over
 // the keys in blocks of 128 with a running maximum m and sum l per row (log2 units):
@@ -33,6 +34,9 @@
 // for each tile (their products interleave, 9 %), the next pair's waits between the products, one block
 // per CTA without taking over others (4 x 4096 x 32 heads 457 us, ragged prompts 362 against 332), and
 // all sequences' longest tiles first (their K and V no longer fit L2 together: 427 us).
+// Keys in pages: the loader's lanes look a block's pages up while its place in the ring is still being read and
+// load a box each.  Pages of 64 tokens and more cost next to nothing (512 queries behind 6000 keys, 4 times, 32/8
+// heads, d = 128: 205 us, packed rows 200); pages of 16 are 32 boxes of 2 KB a block (286 us).
 // Every wait is bounded (1 s, those that may last a whole item 10 s, then LOLA_ATTN_TIMEOUT).
 #include <cuda.h>
 
@@ -71,7 +75,8 @@ template <int D, int NT> struct Cfg {
 };
 
 struct Maps {
-    CUtensorMap q, k, v;   // [rows][heads][d], boxes of 128 rows x 1 head x 64 channels
+    CUtensorMap q, k, v;   // [rows][heads][d], boxes of 128 rows x 1 head x 64 channels; or k, v of the pools:
+                           // [pages x heads][64 channels][page], boxes of up to 128 rows of one page
 };
 
 
@@ -128,7 +133,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 
 // One item: a query tile (or two) of one head.
 struct Item {
-    int q0, lq, k0, lk, r0, h, live;
+    int b, q0, lq, k0, lk, r0, h, live;
 };
 // The blocks of 128 keys that its tiles read (nb, the most of them nmax) and those that all its rows see
 // whole (nf).
@@ -150,17 +155,17 @@ template <int NT> struct Span {
 // Query tiles of ROWS rows, found by one warp: the sequences' tiles are counted in order and taken
 // backwards (a sequence's longest tiles first, the first sequence's shortest ones at the very end), 32
 // sequences in the lanes at a time.
-template <int ROWS> struct Finder {
+template <int ROWS, bool PG> struct Finder {
     int q0, lq, k0, lk;      // this lane's sequence of the 32 from cb on
     int cb, own, inc;        // ... its tiles, and the tiles up to it in the lanes
     int before, total;       // tiles before cb, tiles of all
-    bool bad;
+    int bits;                // what is wrong with offsets and lengths
 
     __device__ __forceinline__ int look(const AttnArgs& a, int b) {
         q0 = lq = k0 = lk = 0;
         if (b < 0 || b >= a.n_seq) return 0;
-        seq_rows(a.cu_q, b, a.total_q, &q0, &lq, &bad);
-        seq_rows(a.cu_k, b, a.total_k, &k0, &lk, &bad);
+        seq_rows(a.cu_q, b, a.total_q, &q0, &lq, &bits);
+        seq_keys<PG>(a, b, &k0, &lk, &bits);
         return (lq + ROWS - 1) / ROWS;
     }
     __device__ __forceinline__ void chunk(const AttnArgs& a, int lane) {
@@ -172,14 +177,14 @@ template <int ROWS> struct Finder {
         }
     }
     __device__ __forceinline__ void start(const AttnArgs& a, int lane) {
-        bad = false;
+        bits = 0;
         before = 0;
         cb = (a.n_seq - 1) / kWarp * kWarp;
         for (int b = 0; b < cb; b += kWarp) before += look(a, b + lane);
         before = __reduce_add_sync(0xffffffffu, before);
         chunk(a, lane);
         total = before + __shfl_sync(0xffffffffu, inc, 31);
-        if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) atomicOr(&g_status, (int)LOLA_ATTN_BAD_OFFSETS);
+        if (blockIdx.x == 0 && bits) atomicOr(&g_status, bits);
     }
     // The number of tile `want` inside this lane's sequence, or -1 if another lane has it; no larger `want`
     // than the last one.
@@ -214,7 +219,8 @@ __device__ __forceinline__ bool stolen_block(uint32_t src, uint32_t* block) {
     return ok != 0;
 }
 
-template <int D, int NT>
+// PG: keys and values in the pages of a cache
+template <int D, int NT, bool PG>
 __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
     using C = Cfg<D, NT>;
     constexpr int kMmaWarp = C::kMmaWarp, kCap = C::kCap;
@@ -263,7 +269,7 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
         abort_sm = 0;
     }
     if (warp == kMmaWarp) tmem_alloc<C::kTmem>(smem_u32(&tmem_base));
-    Finder<C::kQ> find;
+    Finder<C::kQ, PG> find;
     // (before the barriers are there, as nothing of it needs them: five short prompts 11.2 -> 10.4 us; with two
     // tiles it costs the softmax registers, 4 x 4096 x 32 heads 415 -> 431 us)
     if (NT == 1 && warp == C::kItemWarp) find.start(a, lane);
@@ -330,6 +336,7 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
                     if (!ok) break;
                     if (at >= 0) {
                         Item& t = items[n & 1];
+                        t.b = find.cb + lane;
                         t.q0 = find.q0;
                         t.lq = find.lq;
                         t.k0 = find.k0;
@@ -366,17 +373,28 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
             }
         } else if (warp == C::kLoadWarp) {
             // ================================ loader ================================
-            if (lane == 0) {
+            // One thread; with pages the whole warp: a lane looks up and loads one box (of up to 128 rows of a
+            // page, 64 channels) of a pair.  Tokens behind the sequence and pages outside the cache are read
+            // behind the pool's end, as zeros.
+            if (PG || lane == 0) {
+                auto agree = [&](bool x) -> bool {
+                    if constexpr (PG) return __all_sync(0xffffffffu, x);
+                    else return x;
+                };
+                [[maybe_unused]] const int part = lane >> 4, bx = (lane >> 3) & 1;         // K or V, 64 channels
+                [[maybe_unused]] const int rows = PG ? min(a.p.page, kN) : kN, by = (lane & 7) * rows;
+                [[maybe_unused]] bool bad = false;
                 Item t;
                 bool ok = true;
                 int P = 0, cleans = 0, nq[NT] = {};
-                for (int n = 0; ok && get_item(n, &t); ++n) {
+                for (int n = 0; ok && agree(get_item(n, &t)); ++n) {
                     const Span<NT> sp(t);
                     const int hk = t.h / a.G;
                     auto load_q = [&](int i) {
                         if (sp.nb[i] == 0) return;
-                        if (nq[i] > 0 && !(ok = wait(B_QFREE + i, (uint32_t)(nq[i] - 1) & 1u))) return;
+                        if (nq[i] > 0 && !(ok = agree(wait(B_QFREE + i, (uint32_t)(nq[i] - 1) & 1u)))) return;
                         ++nq[i];
+                        if (PG && lane > 0) return;
                         mbar_expect(bar(B_Q + i), C::kTileBytes);
                         for (int x = 0; x < D / 64; ++x)
                             tma_load3(sb + (uint32_t)i * C::kTileBytes + 16384u * x, &maps.q, 64 * x, t.h, t.q0 + t.r0 + kM * i, bar(B_Q + i));
@@ -384,21 +402,41 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
                     if (sp.nmax > 0) {
                         load_q(0);
                         for (int p = 0; p <= sp.nmax && ok; ++p) {
-                            if (P >= kCap && !(ok = wait(empty_of(P), phase(P - kCap)))) break;
+                            [[maybe_unused]] int pos = 0, entry = 0;
+                            [[maybe_unused]] bool mine = false;
+                            if constexpr (PG) {
+                                // (looked up before the wait)
+                                mine = bx < D / 64 && by < kN && (part ? p > 0 : p < sp.nmax);
+                                pos = (p - part) * kN + by;
+                                const bool in = mine && pos < t.lk;
+                                const int page = in ? paged_page(a.p, t.b, pos) : -1;
+                                bad |= in && page < 0;
+                                entry = (page < 0 ? a.p.n_pages : page) * a.p.Hkv + (page < 0 ? 0 : hk);
+                            }
+                            if (P >= kCap && !(ok = agree(wait(empty_of(P), phase(P - kCap))))) break;
                             const int full = full_of(P);
-                            mbar_expect(bar(full), (uint32_t)((p > 0) + (p < sp.nmax)) * C::kTileBytes);
-                            if (p > 0)
-                                for (int x = 0; x < D / 64; ++x)
-                                    tma_load3(sb + v_of(P) + 16384u * x, &maps.v, 64 * x, hk, t.k0 + (p - 1) * kN, bar(full));
-                            if (p < sp.nmax)
-                                for (int x = 0; x < D / 64; ++x)
-                                    tma_load3(sb + k_of(P) + 16384u * x, &maps.k, 64 * x, hk, t.k0 + p * kN, bar(full));
-                            if (p > sp.nf) mbar_arrive1(bar(B_ARMED + cleans++ % kClean));
+                            if (!PG || lane == 0) mbar_expect(bar(full), (uint32_t)((p > 0) + (p < sp.nmax)) * C::kTileBytes);
+                            if constexpr (PG) {
+                                __syncwarp();
+                                if (mine)
+                                    tma_load4(sb + (part ? v_of(P) : k_of(P)) + 16384u * bx + 128u * by, part ? &maps.v : &maps.k, 0,
+                                              pos & (a.p.page - 1), bx, entry, bar(full));
+                            } else {
+                                if (p > 0)
+                                    for (int x = 0; x < D / 64; ++x)
+                                        tma_load3(sb + v_of(P) + 16384u * x, &maps.v, 64 * x, hk, t.k0 + (p - 1) * kN, bar(full));
+                                if (p < sp.nmax)
+                                    for (int x = 0; x < D / 64; ++x)
+                                        tma_load3(sb + k_of(P) + 16384u * x, &maps.k, 64 * x, hk, t.k0 + p * kN, bar(full));
+                            }
+                            if (p > sp.nf && (!PG || lane == 0)) mbar_arrive1(bar(B_ARMED + cleans % kClean));
+                            cleans += p > sp.nf;
                             ++P;
                             if (p == 0 && NT == 2) load_q(NT - 1);
                         }
                     }
-                    if (ok) {
+                    if (PG) __syncwarp();                              // (every lane has read the item)
+                    if (ok && (!PG || lane == 0)) {
                         mbar_arrive1(bar(B_LOADED));
                         mbar_arrive1(bar(B_ITEMFREE + (n & 1)));
                     }
@@ -407,6 +445,7 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
                 for (int x = max(0, P - kCap); x < P; ++x) mbar_wait(bar(full_of(x)), phase(x), kWaitNs);
                 for (int i = 0; i < NT; ++i)
                     if (nq[i] > 0) mbar_wait(bar(B_Q + i), (uint32_t)(nq[i] - 1) & 1u, kWaitNs);
+                if (PG && bad) atomicOr(&g_status, (int)LOLA_ATTN_BAD_PAGE);
             }
             __syncwarp();
         } else if (warp == kMmaWarp) {
@@ -637,14 +676,23 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
                 for (int y = 0; y < 32; ++y) o[y] = none ? 0.f : o[y] * inv;
                 if (odd && lane < rest) {
                     // values that are not finite and were kept out of the products: for the keys the row sees
-                    const __nv_bfloat16* V = reinterpret_cast<const __nv_bfloat16*>(a.V.data) + (int64_t)(t.h / a.G) * a.V.head + x;
 #pragma unroll 1
-                    for (int key = sp.nf * kN; key <= last; ++key)
+                    for (int key = sp.nf * kN; key <= last; ++key) {
+                        int64_t at;
+                        if constexpr (PG) {
+                            const int page = paged_page(a.p, t.b, key);
+                            if (page < 0) continue;
+                            at = paged_offset(a.p, page, t.h / a.G, key);
+                        } else {
+                            at = (int64_t)(t.k0 + key) * a.V.row + (int64_t)(t.h / a.G) * a.V.head;
+                        }
+                        const __nv_bfloat16* V = reinterpret_cast<const __nv_bfloat16*>(PG ? a.p.V : a.V.data) + at + x;
 #pragma unroll
                         for (int y = 0; y < 32; ++y) {
-                            const float v = __bfloat162float(V[(int64_t)(t.k0 + key) * a.V.row + y]);
+                            const float v = __bfloat162float(V[y]);
                             if (!(fabsf(v) <= 3.4e38f)) o[y] += v;
                         }
+                    }
                 }
                 uint32_t p[16];
 #pragma unroll
@@ -682,21 +730,24 @@ bool make_map(CUtensorMap* m, const Rows& r, int64_t rows, int heads, int d) {
     return make_tmap_rows(m, r.data, rows, heads, d, r.row, r.head, kM);
 }
 
-template <int D, int NT>
+template <int D, int NT, bool PG>
 cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
     using C = Cfg<D, NT>;
     Maps maps;
     const int Hkv = a.Hq / a.G;
     const int64_t rows_k = a.total_k > 0 ? a.total_k : 1;
-    if (!make_map(&maps.q, a.Q, a.total_q, a.Hq, D) || !make_map(&maps.k, a.K, rows_k, Hkv, D) ||
-        !make_map(&maps.v, a.V, rows_k, Hkv, D))
+    auto keys_map = [&](CUtensorMap* m, const Rows& r, const char* pool) {
+        if (!PG) return make_map(m, r, rows_k, Hkv, D);
+        return make_tmap_pages(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool, D, a.p.page, (int64_t)a.p.n_pages * Hkv, a.p.page < kN ? a.p.page : kN, 1);
+    };
+    if (!make_map(&maps.q, a.Q, a.total_q, a.Hq, D) || !keys_map(&maps.k, a.K, a.p.K) || !keys_map(&maps.v, a.V, a.p.V))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = opt_in_smem(attn_tc_kernel<D, NT>, C::kSmem, done);
+    cudaError_t e = opt_in_smem(attn_tc_kernel<D, NT, PG>, C::kSmem, done);
     if (e != cudaSuccess) return e;
     // at most this many tiles for any cut of total_q rows into n_seq sequences
     const int64_t tiles = ((int64_t)a.total_q + (int64_t)a.n_seq * (C::kQ - 1)) / C::kQ;
-    attn_tc_kernel<D, NT><<<(unsigned)(tiles * a.Hq), C::kThreads, C::kSmem, st>>>(maps, a);
+    attn_tc_kernel<D, NT, PG><<<(unsigned)(tiles * a.Hq), C::kThreads, C::kSmem, st>>>(maps, a);
     return cudaGetLastError();
 }
 
@@ -723,10 +774,14 @@ static bool one_tile(const AttnArgs& a) {
     return a.d == 128 ? cost(1, 6.8, 1.69) < cost(2, 8.6, 1.46) : cost(1, 5.0, 1.23) < cost(2, 6.4, 1.13);
 }
 
-cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t st) {
+template <bool PG> static cudaError_t launch_form(const AttnArgs& a, cudaStream_t st) {
     const bool one = one_tile(a);
-    if (a.d == 128) return one ? launch<128, 1>(a, st) : launch<128, 2>(a, st);
-    return one ? launch<64, 1>(a, st) : launch<64, 2>(a, st);
+    if (a.d == 128) return one ? launch<128, 1, PG>(a, st) : launch<128, 2, PG>(a, st);
+    return one ? launch<64, 1, PG>(a, st) : launch<64, 2, PG>(a, st);
+}
+
+cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t st) {
+    return a.p.table ? launch_form<true>(a, st) : launch_form<false>(a, st);
 }
 
 cudaError_t attn_tc_status_take(int32_t* bits, cudaStream_t st) { return take_word(g_status, bits, st); }

@@ -700,6 +700,7 @@ int32_t lola_attn_prefill(const lola_attn_config* cfg, int32_t n_seq, int32_t to
     a.cu_k = cu_k ? cu_k : cu_q;
     a.Q = to_rows(Q);
     a.O = to_rows(O);
+    a.p = PagedArgs{};
     a.K = total_k > 0 ? to_rows(K) : a.Q;      // (no key is read when there is none)
     a.V = total_k > 0 ? to_rows(V) : a.Q;
     a.lse = lse;
@@ -715,6 +716,35 @@ int64_t lola_paged_slot(const lola_attn_config* cfg, const lola_paged_kv* kv, in
     if (pos < 0 || pos >= paged_tokens(p, p.kv_len[seq])) return -1;
     const int page = paged_page(p, seq, pos);
     return page < 0 ? -1 : paged_offset(p, page, head, pos);
+}
+
+int32_t lola_paged_prefill(const lola_attn_config* cfg, const lola_paged_kv* kv, int32_t total_q, int32_t total_k,
+                           const int32_t* cu_q, const lola_rows* Q, const lola_rows* O, float* lse, void* stream) {
+    AttnArgs a;
+    const int32_t s = paged_check(cfg, kv, &a.p);
+    if (s != LOLA_OK) return s;
+    if (total_q < 0 || total_k < 0 || !cu_q || !aligned4(cu_q) || !aligned4(lse)) return LOLA_ERR_INVALID_ARG;
+    if (total_q == 0) return LOLA_OK;
+    if (!rows_ok(cfg, Q, total_q, cfg->Hq, false) || !rows_ok(cfg, O, total_q, cfg->Hq, true)) return LOLA_ERR_INVALID_ARG;
+    if (total_q > 0x7fff0000 || (int64_t)kv->width * kv->page > 0x7fff0000) return LOLA_ERR_UNSUPPORTED;
+    if (((int64_t)total_q / 32 + kv->n_seq) * cfg->Hq > 0x40000000) return LOLA_ERR_UNSUPPORTED;
+    a.n_seq = kv->n_seq;
+    a.total_q = total_q;
+    a.total_k = total_k > 0 ? total_k : total_q;
+    a.Hq = cfg->Hq;
+    a.G = cfg->Hq / cfg->Hkv;
+    a.dtype = cfg->dtype;
+    a.d = cfg->d;
+    a.cu_q = cu_q;
+    a.cu_k = nullptr;
+    a.Q = to_rows(Q);
+    a.O = to_rows(O);
+    a.K = a.V = Rows{nullptr, 0, 0};
+    a.lse = lse;
+    a.scale_log2 = attn_scale_log2(cfg);
+    cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = traced(LOLA_KERNEL_ATTN, st, [&]() { return launch_attn_prefill(a, st); });
+    return e == cudaSuccess ? LOLA_OK : cuda_fail(e, "paged prompt attention");
 }
 
 int32_t lola_paged_append(const lola_attn_config* cfg, const lola_paged_kv* kv, int32_t n_tokens,

@@ -645,14 +645,14 @@ bool make_tmap3(CUtensorMap* m, CUtensorMapDataType type, int elem_bytes, const 
 }
 
 bool make_tmap_pages(CUtensorMap* m, CUtensorMapDataType type, int elem_bytes, const void* base, int d, int page,
-                     int64_t depth, int box_rows) {
+                     int64_t depth, int box_rows, int box_cols) {
     auto enc = encoder();
     if (!enc) return false;
     const cuuint32_t inner = 128u / (cuuint32_t)elem_bytes, cols = (cuuint32_t)d / inner;
     const cuuint64_t row = (cuuint64_t)d * elem_bytes;
     const cuuint64_t dims[4] = {inner, (cuuint64_t)page, cols, (cuuint64_t)depth};
     const cuuint64_t strides[3] = {row, 128u, row * page};
-    const cuuint32_t box[4] = {inner, (cuuint32_t)box_rows, cols, 1u};
+    const cuuint32_t box[4] = {inner, (cuuint32_t)box_rows, (cuuint32_t)box_cols, 1u};
     const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
     return enc(m, type, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

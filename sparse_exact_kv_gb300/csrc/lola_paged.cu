@@ -145,14 +145,6 @@ __device__ __forceinline__ bool group_or(int id, bool x) {
         : "memory");
     return r != 0;
 }
-// box (x, y, z, w) into shared memory, completing on `bar`
-__device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
-            dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-        : "memory");
-}
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
@@ -831,8 +823,8 @@ cudaError_t launch_kernel(K kernel, std::atomic<uint64_t>& done, const DecodeArg
     const auto ty = sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const int64_t depth = (int64_t)d.p.n_pages * d.p.Hkv;
     const int rows = d.p.page < kTile ? d.p.page : kTile;
-    if (!make_tmap_pages(&maps.k, ty, sizeof(T), d.p.K, D, d.p.page, depth, rows) ||
-        !make_tmap_pages(&maps.v, ty, sizeof(T), d.p.V, D, d.p.page, depth, rows))
+    if (!make_tmap_pages(&maps.k, ty, sizeof(T), d.p.K, D, d.p.page, depth, rows, D * (int)sizeof(T) / 128) ||
+        !make_tmap_pages(&maps.v, ty, sizeof(T), d.p.V, D, d.p.page, depth, rows, D * (int)sizeof(T) / 128))
         return cudaErrorInvalidValue;
     const size_t smem = (size_t)C::kStages * 2 * C::kHalf + 1024;
     cudaError_t e = opt_in_smem(kernel, (int)smem, done);

@@ -165,6 +165,30 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return decline();
 }
 
+// prefill_paged(layer, k_pool, v_pool, q, cu_q, kv_len, table, total_k) -> out
+PyObject* prefill_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    Layer l;
+    int dev;
+    void* st;
+    Tensor q, cq;
+    lola_rows rq, ro;
+    lola_paged_kv kv;
+    if (n != 8 || !layer(a[0], &l) || !current(&dev, &st) || !cache(a[1], a[2], a[5], a[6], l, dev, &kv)) return decline();
+    const long long total_k = PyLong_Check(a[7]) ? PyLong_AsLongLong(a[7]) : -1;
+    if (total_k < 0 || total_k > INT32_MAX || !rows(a[3], &q, &rq, l.dtype, dev, -1, l.cfg->Hq, l.cfg->d) || q.n[0] > INT32_MAX ||
+        !vec(a[4], &cq, t_int32, dev, (int64_t)kv.n_seq + 1))
+        return decline();
+    PyObject* out = out_like(a[3], &ro, l, dev, q.n[0]);
+    if (!out) return decline();
+    int32_t s;
+    Py_BEGIN_ALLOW_THREADS
+    s = lola_paged_prefill(l.cfg, &kv, (int32_t)q.n[0], (int32_t)total_k, (const int32_t*)cq.data, &rq, &ro, nullptr, st);
+    Py_END_ALLOW_THREADS
+    if (s == LOLA_OK) return out;
+    Py_DECREF(out);
+    return decline();
+}
+
 // decode(layer, k_pool, v_pool, q, kv_len, table) -> out
 PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Layer l;
@@ -248,6 +272,7 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef methods[] = {
     {"setup", (PyCFunction)(void (*)(void))setup, METH_FASTCALL, nullptr},
     {"prefill", (PyCFunction)(void (*)(void))prefill, METH_FASTCALL, nullptr},
+    {"prefill_paged", (PyCFunction)(void (*)(void))prefill_paged, METH_FASTCALL, nullptr},
     {"decode", (PyCFunction)(void (*)(void))decode, METH_FASTCALL, nullptr},
     {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},

@@ -150,13 +150,21 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
-// ---- TMA (cp.async.bulk.tensor) on 3-D tensor maps ----
+// ---- TMA (cp.async.bulk.tensor) on 3-D and 4-D tensor maps ----
 // box (x, y, z) into shared memory, completing on `bar`
 __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
             dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+// box (x, y, z, w) into shared memory, completing on `bar`
+__device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
         : "memory");
 }
 // box (x, y, z) from shared memory to global memory (elements outside the tensor are not
@@ -184,10 +192,10 @@ bool make_tmap3(CUtensorMap* m, CUtensorMapDataType type, int elem_bytes, const 
 bool make_tmap_rows(CUtensorMap* m, const void* base, int64_t rows, int heads, int d, int64_t row, int64_t head,
                     int box_rows);
 // Host: a 4-D tensor map over a page pool [depth][page][d] of elem_bytes bytes, a row as d *
-// elem_bytes / 128 columns of 128 bytes: boxes of box_rows rows of one page and head, column by column,
-// 128-byte swizzle.
+// elem_bytes / 128 columns of 128 bytes: boxes of box_rows rows of one page and head, box_cols columns one
+// after the other, 128-byte swizzle; zeros for an entry outside the depth.
 bool make_tmap_pages(CUtensorMap* m, CUtensorMapDataType type, int elem_bytes, const void* base, int d, int page,
-                     int64_t depth, int box_rows);
+                     int64_t depth, int box_rows, int box_cols);
 
 __device__ __forceinline__ void cp_async16(uint32_t dst_smem, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src) : "memory");

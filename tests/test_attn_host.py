@@ -72,6 +72,12 @@ def append(L, c=None, kv=None, n=3, cu=None, k=None, v=None, q=None, qo=None, in
                                     r(k or rows(L)), r(v or rows(L)), r(q), r(qo), P(inv), rot, pairs, P(pos), None)
 
 
+def prefill_paged(L, c=None, kv=None, tq=10, tk=0, cu_q=256, q=None, o=None, lse=None):
+    r = lambda x: ctypes.byref(x if x is not None else rows(L))  # noqa: E731
+    return L._lib.lola_paged_prefill(ctypes.byref(c or cfg(L)), ctypes.byref(kv or paged(L)), tq, tk, P(cu_q), r(q), r(o),
+                                     P(lse), None)
+
+
 BAD_ROWS = [dict(data=0), dict(data=264), dict(row=0), dict(row=-1024), dict(head=0), dict(row=1028), dict(head=132),
             dict(row=1 << 41), dict(head=1 << 41)]
 
@@ -115,6 +121,24 @@ def test_decode_refusals(L):
     need = L.lola_paged_decode_workspace_bytes(cfg(L))
     assert need > 0
     assert decode(L, size=need - 1) == L.LOLA_ERR_WORKSPACE
+
+
+def test_paged_prefill_refusals(L):
+    E = L.LOLA_ERR_INVALID_ARG
+    for bad in BAD_ROWS:
+        assert prefill_paged(L, q=rows(L, **bad)) == E, bad
+        assert prefill_paged(L, o=rows(L, **bad)) == E, bad
+    assert prefill_paged(L, o=rows(L, row=128, head=128)) == E
+    for bad in (dict(K=0), dict(V=264), dict(n_pages=0), dict(n_seq=0), dict(width=0), dict(table_stride=3), dict(table=0),
+                dict(kv_len=258), dict(page=0)):
+        assert prefill_paged(L, kv=paged(L, **bad)) == E, bad
+    for page in (8, 24, 512):
+        assert prefill_paged(L, kv=paged(L, page=page)) == L.LOLA_ERR_UNSUPPORTED, page
+    for kw in (dict(tq=-1), dict(tk=-1), dict(cu_q=0), dict(cu_q=258), dict(lse=258)):
+        assert prefill_paged(L, **kw) == E, kw
+    assert prefill_paged(L, kv=paged(L, width=0x7fffff, table_stride=1 << 24, page=256)) == L.LOLA_ERR_UNSUPPORTED
+    assert prefill_paged(L, tq=0x7fffffff, q=rows(L, row=128), o=rows(L)) in (E, L.LOLA_ERR_UNSUPPORTED)
+    assert prefill_paged(L, tq=0, q=rows(L, data=0), o=rows(L, data=0)) == 0
 
 
 def test_append_refusals(L):

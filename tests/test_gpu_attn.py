@@ -439,6 +439,140 @@ def test_decode_strides_and_graphs(L, gen):
 
 
 # ---------------------------------------------------------------------------------------
+# prompts over the paged cache
+# ---------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,d,Hq,Hkv", [(BF, 128, 4, 2), (BF, 64, 5, 1), (F32, 64, 2, 2), (F32, 128, 3, 1)])
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("lens,keys", [([1], [1]), ([300, 1, 0, 63, 500], None), ([5, 130, 1, 17], [700, 130, 1300, 16]),
+                                       ([200, 3, 40], [60, 0, 33]), ([700] * 12, None), ([31] * 40, [257] * 40)])
+def test_paged_prefill_equals_packed(L, gen, dtype, d, Hq, Hkv, page, lens, keys):
+    """The same bits as over the gathered rows (the same form of the kernel: it depends on the totals),
+    those being checked against float64 for themselves; unused slots and pages hold NaN."""
+    keys = keys or lens
+    c = Paged(gen, keys, Hkv, d, page, dtype, junk=math.nan)
+    lay = L.ExactAttention(Hq, Hkv, d, dtype, c.k_pool, c.v_pool)
+    q = randn(gen, sum(lens), Hq, d, dtype=dtype)
+    k, v = torch.cat(c.k), torch.cat(c.v)
+    lse, want_lse = (torch.empty(Hq, sum(lens), device="cuda") for _ in range(2))
+    out = lay.prefill_paged(q, offsets(lens), c.kv_len, c.table, sum(keys), lse=lse)
+    want = lay.prefill(q, k, v, offsets(lens), offsets(keys), lse=want_lse)
+    quiet(L)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    if page == 32:
+        check_prefill(q, k, v, lens, keys, out)
+        unknown = lay.prefill_paged(q, offsets(lens), c.kv_len, c.table)     # (perhaps the other form)
+        quiet(L)
+        check_prefill(q, k, v, lens, keys, unknown)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
+def test_paged_prefill_longer(L, gen, dtype, d):
+    """Every place of the ring many times over, several items a CTA."""
+    lens, keys = [1500, 2048, 700, 130] * 5, [4000, 2048, 5003, 131] * 5
+    c = Paged(gen, keys, 2, d, 64, dtype)
+    lay = L.ExactAttention(8, 2, d, dtype, c.k_pool, c.v_pool)
+    q = randn(gen, sum(lens), 8, d, dtype=dtype)
+    for tk in (sum(keys), 0):
+        out = lay.prefill_paged(q, offsets(lens), c.kv_len, c.table, tk)
+        quiet(L)
+        k, v = torch.cat(c.k), torch.cat(c.v)
+        if tk:
+            assert torch.equal(out, lay.prefill(q, k, v, offsets(lens), offsets(keys)))
+        else:
+            check_prefill(q, k, v, lens, keys, out, heads=[0, 7], rows=[0, 1, 127, 128, 600, 1300, 1499, 2047])
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 128), (F32, 64)])
+def test_paged_prefill_values_that_are_not_finite(L, gen, dtype, d):
+    lens = [200, 300]
+    c = Paged(gen, lens, 1, d, 16, dtype, junk=math.inf)
+    for b, pos, x in ((0, 150, math.inf), (1, 131, math.nan), (1, 299, -math.inf)):
+        c.v[b][pos, 0, 3] = x
+        c.put(b, torch.tensor([pos], device="cuda"), c.k[b][pos:pos + 1], c.v[b][pos:pos + 1])
+    lay = L.ExactAttention(2, 1, d, dtype, c.k_pool, c.v_pool)
+    q = randn(gen, 500, 2, d, dtype=dtype)
+    out = lay.prefill_paged(q, offsets(lens), c.kv_len, c.table, 500)
+    want = lay.prefill(q, torch.cat(c.k), torch.cat(c.v), offsets(lens))
+    quiet(L)
+    assert torch.equal(out.nan_to_num(7.0, 8.0, 9.0), want.nan_to_num(7.0, 8.0, 9.0))
+    assert out[:150].isfinite().all() and out[150:200, :, 3].isinf().all() and out[200:331].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
+@pytest.mark.parametrize("page", [16, 64, 256])
+def test_paged_prefill_bad_pages_are_reported(L, gen, dtype, d, page):
+    """A page outside the cache stands for zeros; the other sequences do not notice.  A length beyond
+    the table counts as the table's."""
+    lens = [2 * page + 5, 300, 3 * page]
+    c = Paged(gen, lens, 2, d, page, dtype)
+    lay = L.ExactAttention(4, 2, d, dtype, c.k_pool, c.v_pool)
+    q = randn(gen, sum(lens), 4, d, dtype=dtype)
+    for bad in (-1, c.n_pages, 2 ** 31 - 1, -2 ** 31):
+        table = c.table.clone()
+        table[0, 1] = bad
+        out = lay.prefill_paged(q, offsets(lens), c.kv_len, table, sum(lens))
+        assert L.lola_attn_status()[1] == L.LOLA_ATTN_BAD_PAGE
+        k, v = c.k[0].clone(), c.v[0].clone()
+        k[page:2 * page] = 0
+        v[page:2 * page] = 0
+        want = lay.prefill(q, torch.cat([k, *c.k[1:]]), torch.cat([v, *c.v[1:]]), offsets(lens))
+        quiet(L)
+        assert torch.equal(out, want)
+    full = c.table.shape[1] * page
+    one = ints([full + 9])
+    i = max(range(3), key=lambda b: -(-lens[b] // page))
+    if lens[i] == full:
+        got = lay.prefill_paged(q[:7], offsets([7]), one, c.table[i:i + 1])
+        assert L.lola_attn_status()[1] == L.LOLA_ATTN_BAD_PAGE
+        assert torch.equal(got, lay.prefill_paged(q[:7], offsets([7]), ints([full]), c.table[i:i + 1]))
+        quiet(L)
+
+
+def test_paged_prefill_in_a_graph_with_other_lengths(L, gen):
+    """A server's step: pieces of prompts appended and attended, captured once, replayed as the lengths
+    grow; a table that is part of a wider one, queries a part of wider rows, rows behind the last
+    sequence left."""
+    Hq, Hkv, d, page, B, T = 8, 2, 128, 64, 3, 96
+    lay = L.ExactAttention.allocate(Hq, Hkv, d, 40, page)
+    table = ints([[13 * b + i for i in range(13)] + [-1] * 4 for b in range(B)])[:, :13]
+    rows = torch.empty(B * T, Hq + 2 * Hkv, d, dtype=BF, device="cuda")
+    cu, lens = ints([0] * (B + 1)), ints([0] * B)
+    out = torch.full((B * T, Hq, d), 5.0, dtype=BF, device="cuda")
+    inv = _freq(d)
+
+    def step():
+        q = lay.append(rows[:, Hq:Hq + Hkv], rows[:, Hq + Hkv:], lens, table, cu_new=cu, q=rows[:, :Hq], inv_freq=inv)
+        lay.prefill_paged(q, cu, lens, table, out=out)
+        return q
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q = step()
+    K, V = ([torch.empty(0, Hkv, d, dtype=BF, device="cuda") for _ in range(B)] for _ in range(2))
+    done = [0] * B
+    for new in ([96, 50, 1], [1, 96, 0], [90, 1, 96], [96, 96, 96]):
+        done = [x + n for x, n in zip(done, new)]
+        rows.copy_(randn(gen, B * T, Hq + 2 * Hkv, d, dtype=BF))
+        cu.copy_(offsets(new))
+        lens.copy_(ints(done))
+        out.fill_(5.0)
+        g.replay()
+        torch.cuda.synchronize()
+        quiet(L)
+        r = 0
+        for b, n in enumerate(new):
+            pos = torch.arange(done[b] - n, done[b], device="cuda")
+            K[b] = torch.cat([K[b], lay.k_pool[table[b].long()[pos // page], :, pos % page]])
+            V[b] = torch.cat([V[b], rows[r:r + n, Hq + Hkv:]])
+            r += n
+        check_prefill(q[:r], torch.cat(K), torch.cat(V), new, done, out[:r])
+        assert (out[r:] == 5.0).all()
+
+
+# ---------------------------------------------------------------------------------------
 # the paged cache: rotation and append
 # ---------------------------------------------------------------------------------------
 
@@ -590,6 +724,7 @@ def test_a_layer_serves_prompts_and_then_tokens(L, gen, dtype, d, Hq, Hkv, page)
         k, v = torch.cat(K), torch.cat(V)
         out = lay.prefill(qr, k, v, offsets(piece), offsets(done))
         check_prefill(qr, k, v, piece, done, out)
+        assert torch.equal(lay.prefill_paged(qr, offsets(piece), ints(done), table, sum(done)), out)
     for _ in range(steps):
         done = [x + 1 for x in done]
         qr = put([1] * B, done)
@@ -643,6 +778,12 @@ def test_refused_calls_say_what_is_wrong(L, gen):
         lay.prefill(q, k, k, cu.long())
     with pytest.raises(L.LolaError):
         lay.prefill(q, k[:1], k[:1], cu)                       # other totals without offsets of their own
+    for args in ((q.float(), cu, c.kv_len, c.table), (q, cu[:2], c.kv_len, c.table), (q, cu.long(), c.kv_len, c.table),
+                 (q, cu, c.kv_len.long(), c.table), (q, cu, c.kv_len, c.table.t().contiguous().t())):
+        with pytest.raises(ValueError):
+            lay.prefill_paged(*args)
+    with pytest.raises(L.LolaError):
+        lay.prefill_paged(q, cu, c.kv_len, c.table, total_k=-1)
     with pytest.raises(L.LolaError):
         lay.append(k, k, c.kv_len, c.table, q=q)               # q without a rotation
     with pytest.raises(L.LolaError):
@@ -661,6 +802,7 @@ def test_refused_calls_say_what_is_wrong(L, gen):
     for _ in range(50):
         again = lay.decode_step(q, c.kv_len, c.table)
         lay.prefill(q, k, k, cu)
+        lay.prefill_paged(q, cu, c.kv_len, c.table, 70)
     assert held == [sys.getrefcount(x) for x in (q, k, c.kv_len, c.table, cu, c.k_pool)]
     assert torch.equal(again, good) and sys.getrefcount(again) == sys.getrefcount(good)
 
