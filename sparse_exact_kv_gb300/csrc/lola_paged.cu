@@ -11,6 +11,11 @@
 // leaves (m, l, O) in the workspace, and the last of an item's pieces to arrive joins them:
 //   m = max_k m_k,  l = sum_k 2^{m_k - m} l_k,  o = sum_k 2^{m_k - m} O_k / l,
 // always in the order of the pieces, so that the result does not depend on who comes last.
+// Measured: 64 sequences of 1000-8000 tokens, 32/8 heads, d = 128, bf16: 139 us, 6.2 TB/s; 3 of 65536-131072, 8
+// heads: 177 us, 6.7 TB/s; float32, 64 x 4000, 32/8 heads, d = 128: 318 us, 6.6 TB/s; d = 64, 64 x 8000, 16/8 heads,
+// bf16: 171 us, 6.1 TB/s.  Short calls are bound by their chain of dependent accesses (lengths, pages, first
+// tile: 5 us; records, count, records read back where pieces are joined: 4 more: one sequence of 1000 tokens
+// 9.5 us).
 // Every wait is bounded (1 s, then LOLA_ATTN_TIMEOUT).
 #include <cuda.h>
 
@@ -30,6 +35,7 @@ constexpr int kThreads = kCons + kWarp;
 constexpr int kPieces = 152;              // one CTA per SM
 constexpr int kRows = 16;                 // query rows of a row group (at most)
 constexpr int kJoin = 16;                 // pieces joined at a time
+constexpr float kRaise = 8.0f;            // m is raised when a maximum passes it by this (log2)
 constexpr uint64_t kWaitNs = 1000000000ull;
 
 struct Maps {
@@ -215,7 +221,7 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
                                         uint32_t q_pitch, B& bars, Seg* segs, uint32_t* bad_sm, int* abort_sm, int lane) {
     using C = Cfg<T, D>;
     const PagedArgs& p = a.p;
-    const int box = min(p.page, kTile), nbox = kTile / box;       // tokens of a box, boxes of a tile
+    const int box = min(p.page, kTile), lb = 31 - __clz(box), nbox = kTile >> lb;   // tokens of a box, boxes of a tile
     int b = st.b;
     int lens_b = b;                                               // the lanes hold 32 sequences' lengths
     int lens = b + lane < p.n_seq ? p.kv_len[b + lane] : 0;
@@ -223,7 +229,7 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
     int tiles = tiles_of(tokens), item = (int)(st.rem / tiles), t0 = (int)(st.rem % tiles);
     int64_t u = st.u0;
     int n = 0, i = 0, held_b = -1, held = -1;
-    int64_t held_c = 0;                                           // ... and 32 page-table columns of held_b
+    int held_c = 0;                                           // ... and 32 page-table columns of held_b
     bool ok = true;
     while (u < st.u1 && ok) {
         const int t1 = (int)min((int64_t)tiles, t0 + (st.u1 - u));
@@ -264,24 +270,25 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
             const int s = n % C::kStages;
             if (n >= C::kStages) ok = __all_sync(0xffffffffu, ring_wait(smem_u32(&bars.empty[s]), (uint32_t)(n / C::kStages - 1) & 1, abort_sm));
             if (!ok) break;
-            const int64_t pos = (int64_t)t * kTile;
-            const int64_t col = pos >> p.page_log2;
-            const int used = (int)min((int64_t)nbox, (tokens - pos + box - 1) / box);       // boxes with tokens
+            // (positions fit 31 bits, but for the boxes behind the last token's)
+            const uint32_t pos = (uint32_t)t * kTile, have = (uint32_t)tokens;
+            const int col = (int)(pos >> p.page_log2);
+            const int used = have > pos ? min(nbox, (int)((have - pos + box - 1) >> lb)) : 0;     // boxes with tokens
             if (held_b != b || col < held_c || col + used > held_c + 32) {
                 held_b = b;
                 held_c = col;
-                const int64_t c = (col + lane) << p.page_log2;
+                const int64_t c = (int64_t)(col + lane) << p.page_log2;
                 held = c < tokens ? paged_page(p, b, c) : 0;
             }
             // lanes 0 .. used - 1: a box of K each; lanes 16 ..: of V
             const int x = lane & 15;
-            const int page = __shfl_sync(0xffffffffu, held, (int)(((pos + x * box) >> p.page_log2) - held_c) & 31);
+            const int page = __shfl_sync(0xffffffffu, held, ((int)((pos + x * box) >> p.page_log2) - held_c) & 31);
             const bool mine = x < used, bad = mine && page < 0;
             const uint32_t bad_mask = __ballot_sync(0xffffffffu, bad) & 0xffffu;
             if (lane == 0) {
                 if (bad_mask) atomicOr(&g_status, (int)LOLA_ATTN_BAD_PAGE);
                 bad_sm[s] = bad_mask;
-                mbar_expect(smem_u32(&bars.full[s]), (uint32_t)(2 * (max(used, 0) - __popc(bad_mask)) * box * C::kRowBytes));
+                mbar_expect(smem_u32(&bars.full[s]), (uint32_t)(2 * (used - __popc(bad_mask)) * box * C::kRowBytes));
                 *reinterpret_cast<volatile int*>(&bars.issued) = n + 1;
             }
             __syncwarp();
@@ -417,13 +424,20 @@ __device__ void join_pieces(const Args& a, const Seg& g, int t, int* go, F&& bar
     }
 }
 
-// ---- float32, CUDA cores: 256 threads take a tile together ----
-// Scores: a thread has one token and every fourth row; P V: a thread has one channel of every row over
-// its share of the tokens.  RM: rows compiled for (4 or 16).
+// ---- float32, CUDA cores ----
+// Eight warps, the two halves of them on alternate tiles of a segment.  A warp takes four query rows and
+// 64 / NP tokens of a tile (RM = 4, 8, 16 rows compiled for: NP = 4, 2, 1 parts of the tokens), 16 at a time,
+// with its own running maximum, sum and output, joined at the segment's end: no barrier inside a segment (with
+// all threads on one tile and two barriers in it, 64 sequences of 4000 tokens, 4 heads of 64, took 184 us, now 86).
+// Lanes 8 tg + j: chunk j (16 bytes) of every 128-byte column of the rows, tokens 4 i + tg, so that K and V are
+// read once, without bank conflicts, into products with q and the output in registers; the eight lanes' sums
+// of a score are added and dealt out by halves (14 shuffles for 16 tokens x 4 rows).  m is raised lazily, by
+// more than 2^8 at a time.
 template <int D, int RM>
 __global__ void __launch_bounds__(kThreads, 1) paged_decode_f32_kernel(const __grid_constant__ Maps maps, const Args a) {
     using C = Cfg<float, D>;
-    constexpr int KP = kCons / D, NW = kCons / kWarp;           // key parts of P V
+    constexpr int NC = RM / 4, NP = 4 / NC, KT = kTile / NP, X = D / 32, NW = kCons / kWarp;
+    constexpr bool kHold = D == 64;                             // q in registers (168 a thread: nine warps)
     extern __shared__ __align__(1024) uint8_t smraw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) Bars<C::kStages> bars;
@@ -431,17 +445,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_f32_kernel(const __g
     __shared__ int abort_sm, go;
     __shared__ Seg segs[1];
     __shared__ __align__(16) float Qs[kRows][D];
-    // the weights of two tiles, and at a segment's end its outputs by key part
-    __shared__ __align__(16) float shared_sr[KP * RM * D > 2 * RM * kTile ? KP * RM * D : 2 * RM * kTile];
-    auto Ss = reinterpret_cast<float(*)[RM][kTile]>(shared_sr);
-    auto red = reinterpret_cast<float(*)[RM][D]>(shared_sr);
-    __shared__ float fs[2][RM], ms[kRows], ls[kRows];
+    __shared__ __align__(16) float Ps[NW][16][4];               // a warp's weights, to be read by token
+    __shared__ __align__(16) float red[2 * NP][RM][D];          // the parts' outputs at a segment's end
+    __shared__ float ms[2 * NP][RM], ls[2 * NP][RM];
     const PagedArgs& p = a.p;
     const int tid = threadIdx.x, warp = tid / kWarp, lane = tid % kWarp;
     if (tid == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(smem_u32(&bars.full[s]), 1);
-            mbar_init(smem_u32(&bars.empty[s]), NW);
+            mbar_init(smem_u32(&bars.empty[s]), NW / 2);
         }
         mbar_init(smem_u32(&bars.seg_full[0]), 1);
         mbar_init(smem_u32(&bars.seg_empty[0]), NW);
@@ -455,8 +467,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_f32_kernel(const __g
         return;
     }
     auto bar = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
-    const int key = tid % kTile, hs = tid / kTile;
-    const int dim = tid % D, part = tid / D;
+    const int grp = warp >> 2, rc = (warp & 3) / NP, tp = (warp & 3) % NP, tg = lane >> 3, j = lane & 7;
+    const bool b2 = j & 4, b1 = j & 2, b0 = j & 1;
     const int box = min(p.page, kTile), lb = 31 - __clz(box);
     // byte offset of 16-byte chunk 0 of a token's row; column x (128 bytes) is x * box * 128 further
     auto row_at = [&](int k) { return (k >> lb) * box * C::kRowBytes + (k & (box - 1)) * 128; };
@@ -468,113 +480,189 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_f32_kernel(const __g
         const Seg g = segs[0];
         if (g.R < 0) break;
         if (!g.whole && tid == 64) open_cells<D>(a, g);
-        if (tid < RM) {
-            ms[tid] = -INFINITY;
-            ls[tid] = 0.f;
-        }
-        float acc[RM];
+        auto q_at = [&](int r, int x) { return *reinterpret_cast<const float4*>(&Qs[4 * rc + r][32 * x + 4 * j]); };
+        float4 q[4][kHold ? X : 1], acc[4][X];
 #pragma unroll
-        for (int r = 0; r < RM; ++r) acc[r] = 0.f;
-        bar();
-        bool ok = true;
-        for (int t = 0; t < g.tiles; ++t) {
-            const int n = g.n0 + t, s = n % C::kStages, e = n & 1;
-            ok = ok && ring_wait(smem_u32(&bars.full[s]), (uint32_t)(n / C::kStages) & 1, &abort_sm);
-            const uint8_t* Kt = sm + (size_t)s * 2 * C::kHalf;
-            const uint8_t* Vt = Kt + C::kHalf;
-            const int nk = max(0, min(kTile, g.len - t * kTile));
-            const uint32_t bad = ok ? bad_sm[s] : ~0u;
-            float sc[(RM + 3) / 4];
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int x = 0; x < (RM + 3) / 4; ++x) sc[x] = 0.f;
-            const bool seen = key < nk && !((bad >> (key >> lb)) & 1u);
-            const uint8_t* kr = Kt + row_at(key);
-#pragma unroll 4
-            for (int c = 0; c < D / 4; ++c) {
-                const float4 kv = *reinterpret_cast<const float4*>(kr + (c >> 3) * (box * 128) + (((c ^ key) & 7) << 4));
-#pragma unroll
-                for (int x = 0; x < (RM + 3) / 4; ++x) {
-                    const float4 q = *reinterpret_cast<const float4*>(&Qs[hs + 4 * x][4 * c]);
-                    sc[x] = fmaf(q.x, kv.x, sc[x]);
-                    sc[x] = fmaf(q.y, kv.y, sc[x]);
-                    sc[x] = fmaf(q.z, kv.z, sc[x]);
-                    sc[x] = fmaf(q.w, kv.w, sc[x]);
-                }
+            for (int x = 0; x < X; ++x) {
+                if (kHold) q[r][x] = q_at(r, x);
+                acc[r][x] = make_float4(0.f, 0.f, 0.f, 0.f);
             }
-#pragma unroll
-            for (int x = 0; x < (RM + 3) / 4; ++x) Ss[e][hs + 4 * x][key] = seen ? sc[x] * a.scale_log2 : -INFINITY;
-            bar();
-            // running maximum and sum: warp w takes rows w, w + 8
-            for (int r = warp; r < RM; r += NW) {
-                const float x = Ss[e][r][lane], y = Ss[e][r][lane + 32];
-                const float mo = ms[r], mn = fmaxf(mo, warp_max(fmaxf(x, y)));
-                const float bs = mn == -INFINITY ? 0.f : mn;
-                const float px = exp2f(x - bs), py = exp2f(y - bs);
-                const float f = exp2f(mo - bs), sum = warp_sum(px + py);
-                Ss[e][r][lane] = px;
-                Ss[e][r][lane + 32] = py;
-                __syncwarp();
-                if (lane == 0) {
-                    ms[r] = mn;
-                    ls[r] = ls[r] * f + sum;
-                    fs[e][r] = f;
-                }
-            }
-            bar();
-#pragma unroll
-            for (int r = 0; r < RM; ++r) acc[r] *= fs[e][r];
-            constexpr int KN = kTile / KP;
-            const int ch = dim / 4;
-            const uint8_t* vb = Vt + (ch >> 3) * (box * 128) + (dim & 3) * 4;
-            for (int k4 = part * KN; k4 < min(nk, (part + 1) * KN); k4 += 4) {
-                float v[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int kk = k4 + x;
-                    // (a token that is not seen has p = 0; its value row may be anything)
-                    const bool in = kk < nk && !((bad >> (kk >> lb)) & 1u);
-                    v[x] = in ? *reinterpret_cast<const float*>(vb + row_at(kk) + (((ch ^ kk) & 7) << 4)) : 0.f;
-                }
-#pragma unroll
-                for (int r = 0; r < RM; ++r) {
-                    const float4 pr = *reinterpret_cast<const float4*>(&Ss[e][r][k4]);
-                    acc[r] = fmaf(pr.x, v[0], acc[r]);
-                    acc[r] = fmaf(pr.y, v[1], acc[r]);
-                    acc[r] = fmaf(pr.z, v[2], acc[r]);
-                    acc[r] = fmaf(pr.w, v[3], acc[r]);
-                }
-            }
+        auto release = [&] {                                            // (g and the Q rows are in registers, or read)
             __syncwarp();
+            if (lane == 0) mbar_arrive1(smem_u32(&bars.seg_empty[0]));
+        };
+        if (kHold) release();
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};         // rows 2 b0 and 2 b0 + 1
+        bool ok = true;
+        for (int t = (g.n0 ^ grp) & 1; t < g.tiles; t += 2) {
+            const int n = g.n0 + t, s = n % C::kStages;
+            ok = issued_wait(&bars.issued, n, &abort_sm) &&
+                 ring_wait(smem_u32(&bars.full[s]), (uint32_t)(n / C::kStages) & 1, &abort_sm);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            uint8_t* Kt = sm + (size_t)s * 2 * C::kHalf;
+            uint8_t* Vt = Kt + C::kHalf;
+            const int nk = max(0, min(kTile, g.len - t * kTile));
+            const uint32_t bad = bad_sm[s];
+            auto hidden = [&](int k) { return k >= nk || ((bad >> (k >> lb)) & 1u); };
+            const bool some = nk < kTile || bad;
+            if (some) {
+                // tokens behind the sequence or on bad pages: their V rows (which may hold anything) become zero
+                for (int k = tp * KT; k < (tp + 1) * KT; ++k)
+                    if (hidden(k) && lane < D / 4)
+                        *reinterpret_cast<float4*>(Vt + row_at(k) + (lane >> 3) * (box * 128) + (lane & 7) * 16) = make_float4(0.f, 0.f, 0.f, 0.f);
+                fence_async_smem();            // (before the ring's next copy lands on these rows)
+                __syncwarp();
+            }
+#pragma unroll 1
+            for (int k0 = tp * KT; k0 < min((tp + 1) * KT, nk); k0 += 16) {
+                // ---- scores of 16 tokens: this lane's channels ----
+                const int at = row_at(k0) + tg * 128;
+                float sc[4][4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) sc[y][r] = 0.f;
+#pragma unroll
+                for (int x = 0; x < X; ++x) {
+                    float4 qx[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) qx[r] = kHold ? q[r][kHold ? x : 0] : q_at(r, x);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const float4 k = *reinterpret_cast<const float4*>(Kt + at + x * (box * 128) + y * 512 + (((j ^ (4 * y + tg)) & 7) << 4));
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            sc[y][r] = fmaf(qx[r].w, k.w, fmaf(qx[r].z, k.z, fmaf(qx[r].y, k.y, fmaf(qx[r].x, k.x, sc[y][r]))));
+                    }
+                }
+                // ---- added over the eight lanes: token 4 (j >> 1) + tg, rows 2 b0 and 2 b0 + 1 stay here ----
+                float u[2][4], w[4], z[2];
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        u[y][r] = (b2 ? sc[2 + y][r] : sc[y][r]) + __shfl_xor_sync(0xffffffffu, b2 ? sc[y][r] : sc[2 + y][r], 4);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) w[r] = (b1 ? u[1][r] : u[0][r]) + __shfl_xor_sync(0xffffffffu, b1 ? u[0][r] : u[1][r], 2);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    z[e] = ((b0 ? w[2 + e] : w[e]) + __shfl_xor_sync(0xffffffffu, b0 ? w[e] : w[2 + e], 1)) * a.scale_log2;
+                if (some && hidden(k0 + 4 * (j >> 1) + tg)) z[0] = z[1] = -INFINITY;
+                // ---- running maximum, weights ----
+                bool need[2];
+                float bm[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    bm[e] = z[e];
+#pragma unroll
+                    for (int o = 2; o < kWarp; o <<= 1) bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], o));
+                    need[e] = bm[e] > m[e] + kRaise || (m[e] == -INFINITY && bm[e] > m[e]);
+                }
+                if (__any_sync(0xffffffffu, need[0] || need[1])) {
+                    float f[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        f[e] = need[e] ? exp2f(m[e] - bm[e]) : 1.f;
+                        if (need[e]) m[e] = bm[e];
+                        l[e] *= f[e];
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float fr = __shfl_sync(0xffffffffu, f[r & 1], (lane & 30) | (r >> 1));
+#pragma unroll
+                        for (int x = 0; x < X; ++x) acc[r][x] = make_float4(acc[r][x].x * fr, acc[r][x].y * fr, acc[r][x].z * fr, acc[r][x].w * fr);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    z[e] = exp2f(z[e] - (m[e] == -INFINITY ? 0.f : m[e]));
+                    l[e] += z[e];
+                }
+                *reinterpret_cast<float2*>(&Ps[warp][4 * (j >> 1) + tg][2 * (j & 1)]) = make_float2(z[0], z[1]);
+                __syncwarp();
+                // ---- O += P V ----
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const float4 pr = *reinterpret_cast<const float4*>(&Ps[warp][4 * y + tg][0]);
+                    const float pv[4] = {pr.x, pr.y, pr.z, pr.w};
+#pragma unroll
+                    for (int x = 0; x < X; ++x) {
+                        const float4 v = *reinterpret_cast<const float4*>(Vt + at + x * (box * 128) + y * 512 + (((j ^ (4 * y + tg)) & 7) << 4));
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            acc[r][x].x = fmaf(pv[r], v.x, acc[r][x].x);
+                            acc[r][x].y = fmaf(pv[r], v.y, acc[r][x].y);
+                            acc[r][x].z = fmaf(pv[r], v.z, acc[r][x].z);
+                            acc[r][x].w = fmaf(pv[r], v.w, acc[r][x].w);
+                        }
+                    }
+                }
+                __syncwarp();                                           // (Ps is read)
+            }
             if (lane == 0) mbar_arrive1(smem_u32(&bars.empty[s]));
         }
-        // ---- the segment's end: add the key parts in order ----
+        // ---- the segment's end: the lanes' tokens (row tg stays here), then the parts in order ----
         if (group_or<kCons>(1, !ok)) {
             if (tid == 0) atomicOr(&g_status, (int)LOLA_ATTN_TIMEOUT);
             break;
         }
+        if (!kHold) release();
+        const int part = grp * NP + tp;
+        auto give = [](const float4& x, int o) {
+            return make_float4(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o),
+                               __shfl_xor_sync(0xffffffffu, x.z, o), __shfl_xor_sync(0xffffffffu, x.w, o));
+        };
+        auto plus = [](const float4& x, const float4& y) { return make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w); };
 #pragma unroll
-        for (int r = 0; r < RM; ++r) red[part][r][dim] = acc[r];
+        for (int x = 0; x < X; ++x) {
+            const bool t1 = tg & 2, t0 = tg & 1;
+            const float4 y0 = plus(t1 ? acc[2][x] : acc[0][x], give(t1 ? acc[0][x] : acc[2][x], 16));
+            const float4 y1 = plus(t1 ? acc[3][x] : acc[1][x], give(t1 ? acc[1][x] : acc[3][x], 16));
+            const float4 y = plus(t0 ? y1 : y0, give(t0 ? y0 : y1, 8));
+            *reinterpret_cast<float4*>(&red[part][4 * rc + tg][32 * x + 4 * j]) = y;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int o = 2; o < kWarp; o <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], o);
+            if (lane < 2) {
+                ms[part][4 * rc + 2 * lane + e] = m[e];
+                ls[part][4 * rc + 2 * lane + e] = l[e];
+            }
+        }
         bar();
         float* rec = record<D>(a, blockIdx.x, g.k == 0 ? g.s0 : 0);
         for (int e = tid; e < g.R * (D / 4); e += kCons) {
             const int r = e / (D / 4), c = e % (D / 4) * 4;
-            float y[4] = {0.f, 0.f, 0.f, 0.f};
+            float M = -INFINITY, ll = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < KP; ++k)
+            for (int k = 0; k < 2 * NP; ++k) M = fmaxf(M, ms[k][r]);
 #pragma unroll
-                for (int z = 0; z < 4; ++z) y[z] += red[k][r][c + z];
-            write_out<float, D>(a, g, g.whole, rec, r, c, y, ms[r], ls[r]);
+            for (int k = 0; k < 2 * NP; ++k) {
+                const float f = exp2f(ms[k][r] - (M == -INFINITY ? 0.f : M));
+                const float4 x = *reinterpret_cast<const float4*>(&red[k][r][c]);
+                ll = fmaf(f, ls[k][r], ll);
+                y[0] = fmaf(f, x.x, y[0]);
+                y[1] = fmaf(f, x.y, y[1]);
+                y[2] = fmaf(f, x.z, y[2]);
+                y[3] = fmaf(f, x.w, y[3]);
+            }
+            write_out<float, D>(a, g, g.whole, rec, r, c, y, M, ll);
         }
         if (!g.whole) join_pieces<float, D, kCons>(a, g, tid, &go, bar);
-        bar();                                                  // Qs, red, ms, ls are read
-        if (lane == 0) mbar_arrive1(smem_u32(&bars.seg_empty[0]));
+        bar();                                                  // red, ms, ls are read
     }
 }
 
 // ---- bf16: the tile products on the warps' matrix instructions ----
-// Two groups of four warps take the segments in turn, so that one group's epilogue runs beside the
-// other's tiles; a warp takes 16 of a tile's 64 tokens, with its own running maximum, sum and
-// output of the 16 query rows, joined at the segment's end.  S = Q K^T has the rows of Q as M, so
+// Two groups of four warps: at d = 128 they take the segments in turn, so that one group's epilogue runs beside
+// the other's tiles (64 sequences of 1000-8000 tokens, 32/8 heads: 142 us, 152 on tiles in turn); at d = 64, where a
+// tile's bytes come faster than four warps get through it, they take a segment's tiles in turn (64 x 8000 tokens,
+// 16/8 heads: 171 us, 214 on segments in turn).  A warp takes 16 of a tile's 64 tokens, with its own running
+// maximum, sum and output of the 16 query rows, joined at the segment's end.  S = Q K^T has the rows of Q as M, so
 // that its accumulators are the A operand of P V as they stand.  m is raised lazily (by more than
 // 2^8 at a time), which leaves the output alone for most tiles.
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -595,13 +683,14 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-constexpr float kRaise = 8.0f;
 
 template <int D, bool HALF> struct MmaSmem {
+    static constexpr bool kBoth = D == 64;
+    static constexpr int NW = kBoth ? 8 : 4;                                // warps of a segment
     static constexpr int HR = HALF ? 1 : 2, R8 = 8 * HR, CK = 512 / R8;     // rows kept; columns joined at a time
     static constexpr int kPitch = 2 * D + 16;                               // Q rows (16-byte shift against bank conflicts)
-    float red[2][4][R8][CK];
-    float ms[2][4][R8], ls[2][4][R8];
+    float red[8 / NW][NW][R8][CK];                                               // by group and warp
+    float ms[8 / NW][NW][R8], ls[8 / NW][NW][R8];
     uint8_t q[2][kRows * kPitch];
 };
 
@@ -612,6 +701,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_mma_kernel(const __g
     using C = Cfg<T, D>;
     using M = MmaSmem<D, HALF>;
     constexpr int HR = M::HR, CK = M::CK;
+    constexpr bool kBoth = M::kBoth;
+    constexpr int NW = M::NW, NT = NW * kWarp;
     extern __shared__ __align__(1024) uint8_t smraw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(sm);
@@ -629,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_mma_kernel(const __g
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&bars.seg_full[s]), 1);
-            mbar_init(smem_u32(&bars.seg_empty[s]), 4);
+            mbar_init(smem_u32(&bars.seg_empty[s]), NW);
         }
         abort_sm = 0;
         bars.issued = 0;
@@ -640,8 +731,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_mma_kernel(const __g
         produce<T, D, 2>(maps, a, st, sb, smem_u32(x.q[0]), M::kPitch, bars, segs, bad_sm, &abort_sm, lane);
         return;
     }
-    const int grp = warp >> 2, wg = warp & 3, gt = tid & 127, g8 = lane >> 2, q2 = (lane & 3) * 2;
-    auto bar = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + grp) : "memory"); };
+    const int grp = warp >> 2, wg = warp & 3, g8 = lane >> 2, q2 = (lane & 3) * 2;
+    const int own = kBoth ? 0 : grp, me = kBoth ? warp : wg, gt = kBoth ? tid : tid & 127;   // the segment's group, its warps and threads
+    auto bar = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + own), "n"(NT) : "memory"); };
     const int k0 = wg * 16;                                            // this warp's tokens of a tile
     const int box = min(p.page, kTile), lb = 31 - __clz(box);
     const uint32_t col = (uint32_t)box * 128;                          // from one 128-byte column to the next
@@ -649,27 +741,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_mma_kernel(const __g
     const int kkey = k0 + ((lane >> 4) << 3) + (lane & 7), kch = (lane >> 3) & 1;        // ldmatrix rows of K
     const int vkey = k0 + (((lane >> 3) & 1) << 3) + (lane & 7), vch = lane >> 4;        // ... of V
     const uint32_t krow = row_at(kkey), vrow = C::kHalf + row_at(vkey);
-    const uint32_t qrow = smem_u32(x.q[grp]) + ((lane & 7) + ((lane >> 3) & 1) * 8) * M::kPitch + (lane >> 4) * 16;
+    const uint32_t qrow = smem_u32(x.q[0]) + ((lane & 7) + ((lane >> 3) & 1) * 8) * M::kPitch + (lane >> 4) * 16;
     for (int i = 0;; ++i) {
-        if (group_or<128>(1 + grp, !ring_wait(smem_u32(&bars.seg_full[grp]), (uint32_t)i & 1, &abort_sm))) {
+        const int slot = kBoth ? i & 1 : grp;
+        if (group_or<NT>(1 + own, !ring_wait(smem_u32(&bars.seg_full[slot]), (uint32_t)(kBoth ? i >> 1 : i) & 1, &abort_sm))) {
             if (gt == 0) atomicOr(&g_status, (int)LOLA_ATTN_TIMEOUT);
             break;
         }
-        const Seg g = segs[grp];
+        const Seg g = segs[slot];
         if (g.R < 0) break;
         if (!g.whole && gt == 64) open_cells<D>(a, g);
         uint32_t qa[D / 16][4];
 #pragma unroll
-        for (int y = 0; y < D / 16; ++y) ldsm4(qrow + 32 * y, qa[y]);
+        for (int y = 0; y < D / 16; ++y) ldsm4(qrow + slot * kRows * M::kPitch + 32 * y, qa[y]);
         __syncwarp();
-        if (lane == 0) mbar_arrive1(smem_u32(&bars.seg_empty[grp]));   // (g and the Q rows are in registers)
+        if (lane == 0) mbar_arrive1(smem_u32(&bars.seg_empty[slot]));   // (g and the Q rows are in registers)
         float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
         for (int y = 0; y < D / 8; ++y)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[y][e] = 0.f;
         bool ok = true;
-        for (int t = 0; t < g.tiles; ++t) {
+        for (int t = kBoth ? (g.n0 ^ grp) & 1 : 0; t < g.tiles; t += kBoth ? 2 : 1) {
             const int n = g.n0 + t, s = n % C::kStages;
             ok = issued_wait(&bars.issued, n, &abort_sm) &&
                  ring_wait(smem_u32(&bars.full[s]), (uint32_t)(n / C::kStages) & 1, &abort_sm);
@@ -747,8 +840,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_mma_kernel(const __g
             __syncwarp();
             if (lane == 0) mbar_arrive1(smem_u32(&bars.empty[s]));
         }
-        // ---- the segment's end: add the four warps in order, then o or the piece's record ----
-        if (group_or<128>(1 + grp, !ok)) {
+        // ---- the segment's end: add the warps in order, then o or the piece's record ----
+        if (group_or<NT>(1 + own, !ok)) {
             if (gt == 0) atomicOr(&g_status, (int)LOLA_ATTN_TIMEOUT);
             break;
         }
@@ -757,8 +850,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_mma_kernel(const __g
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
             if ((lane & 3) == 0) {
-                x.ms[grp][wg][g8 + 8 * r] = m[r];
-                x.ls[grp][wg][g8 + 8 * r] = l[r];
+                x.ms[own][me][g8 + 8 * r] = m[r];
+                x.ls[own][me][g8 + 8 * r] = l[r];
             }
         }
         bar();
@@ -767,16 +860,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_mma_kernel(const __g
         for (int r = 0; r < HR; ++r) {
             float mm = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) mm = fmaxf(mm, x.ms[grp][w][g8 + 8 * r]);
+            for (int w = 0; w < NW; ++w) mm = fmaxf(mm, x.ms[own][w][g8 + 8 * r]);
             f[r] = ex2(m[r] - (mm == -INFINITY ? 0.f : mm));
         }
         float* rec = record<D>(a, blockIdx.x, g.k == 0 ? g.s0 : 0);
-        const int er = 4 * gt / CK, ec = 4 * gt % CK;          // 128 threads x 4 columns = R8 x CK
+        const int er = 4 * (gt & 127) / CK, ec = 4 * (gt & 127) % CK;        // 128 threads x 4 columns = R8 x CK
         float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) mm = fmaxf(mm, x.ms[grp][w][er]);
+        for (int w = 0; w < NW; ++w) mm = fmaxf(mm, x.ms[own][w][er]);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) ll = fmaf(x.ls[grp][w][er], ex2(x.ms[grp][w][er] - (mm == -INFINITY ? 0.f : mm)), ll);
+        for (int w = 0; w < NW; ++w) ll = fmaf(x.ls[own][w][er], ex2(x.ms[own][w][er] - (mm == -INFINITY ? 0.f : mm)), ll);
 #pragma unroll
         for (int c = 0; c < D; c += CK) {
             if (c > 0) bar();
@@ -784,21 +877,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_mma_kernel(const __g
             for (int y = 0; y < CK / 8; ++y)
 #pragma unroll
                 for (int r = 0; r < HR; ++r)
-                    *reinterpret_cast<float2*>(&x.red[grp][wg][g8 + 8 * r][8 * y + q2]) =
+                    *reinterpret_cast<float2*>(&x.red[own][me][g8 + 8 * r][8 * y + q2]) =
                         make_float2(o[c / 8 + y][2 * r] * f[r], o[c / 8 + y][2 * r + 1] * f[r]);
             bar();
-            float y[4] = {0.f, 0.f, 0.f, 0.f};
+            if (!kBoth || gt < 128) {
+                float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const float4 z = *reinterpret_cast<const float4*>(&x.red[grp][w][er][ec]);
-                y[0] += z.x;
-                y[1] += z.y;
-                y[2] += z.z;
-                y[3] += z.w;
+                for (int w = 0; w < NW; ++w) {
+                    const float4 z = *reinterpret_cast<const float4*>(&x.red[own][w][er][ec]);
+                    y[0] += z.x;
+                    y[1] += z.y;
+                    y[2] += z.z;
+                    y[3] += z.w;
+                }
+                if (er < g.R) write_out<T, D>(a, g, g.whole, rec, er, c + ec, y, mm, ll);
             }
-            if (er < g.R) write_out<T, D>(a, g, g.whole, rec, er, c + ec, y, mm, ll);
         }
-        if (!g.whole) join_pieces<T, D, 128>(a, g, gt, &go[grp], bar);
+        if (!g.whole) join_pieces<T, D, NT>(a, g, gt, &go[own], bar);
     }
 }
 
@@ -834,9 +929,10 @@ cudaError_t launch_kernel(K kernel, std::atomic<uint64_t>& done, const DecodeArg
 }
 template <int D>
 cudaError_t launch_f32(const DecodeArgs& d, cudaStream_t st) {
-    static std::atomic<uint64_t> done[2] = {};
-    return d.p.G <= 4 ? launch_kernel<float, D>(paged_decode_f32_kernel<D, 4>, done[0], d, st)
-                      : launch_kernel<float, D>(paged_decode_f32_kernel<D, kRows>, done[1], d, st);
+    static std::atomic<uint64_t> done[3] = {};
+    if (d.p.G <= 4) return launch_kernel<float, D>(paged_decode_f32_kernel<D, 4>, done[0], d, st);
+    if (d.p.G <= 8) return launch_kernel<float, D>(paged_decode_f32_kernel<D, 8>, done[1], d, st);
+    return launch_kernel<float, D>(paged_decode_f32_kernel<D, 16>, done[2], d, st);
 }
 template <int D>
 cudaError_t launch_bf16(const DecodeArgs& d, cudaStream_t st) {
