@@ -436,17 +436,13 @@ def lola_attn_status(stream=None):
 # Convenience: buffers allocated through torch, then the C ABI
 # ---------------------------------------------------------------------------------------
 
-_fast.setup(torch.empty_like, torch.empty, getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream),
-            getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device), torch.int32, torch.float32, torch.uint8)
-
-
 @functools.lru_cache(maxsize=256)
 def _attn_plan(Hq, Hkv, d, dtype, scale):
     """The config of a kind of layer, the decode step's workspace bytes (checks the config), and both as the
     marshalling module takes them (the config by its address: a layer holds on to it)."""
     cfg = make_attn_config(Hq, Hkv, d, dtype, scale)
     size = lola_paged_decode_workspace_bytes(cfg)
-    return cfg, size, (ctypes.addressof(cfg), dtype, size)
+    return cfg, size, (ctypes.addressof(cfg), size)
 
 
 def _need(ok, what):

@@ -19,7 +19,7 @@ SOURCES = ["lola_capi.cu", "lola_phi.cu", "lola_select.cu", "lola_chunk.cu", "lo
            "lola_decode.cu", "lola_noalloc.cu", "lola_relsre.cu",
            "lola_fixed.cu", "lola_hola.cu", "lola_hola_tc.cu", "lola_attn.cu",
            "lola_attn_tc.cu", "lola_append.cu", "lola_paged.cu"]
-PYMOD = os.path.join(PKG, "_lola_py.so")      # the binding's marshalling in C (csrc/lola_py.cpp)
+PYMOD = os.path.join(PKG, "_lola_py.so")      # the binding's marshalling (csrc/lola_py.cpp)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -61,8 +61,23 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with ThreadPoolExecutor(max_workers=jobs or len(SOURCES)) as ex:
+    def binding() -> list[str]:
+        import torch
+        lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+        inc = os.path.join(os.path.dirname(torch.__file__), "include")
+        obj = os.path.join(BUILD, "lola_py.o")
+        cmd = [cc, "-O2", "-std=c++17", "-w", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+               "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-c", os.path.join(CSRC, "lola_py.cpp"),
+               "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"compiling the binding's module failed:\n{r.stdout}\n{r.stderr}")
+        return [obj, "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Xlinker", f"-rpath,{lib}"]
+
+    with ThreadPoolExecutor(max_workers=jobs or len(SOURCES) + 1) as ex:
+        py = ex.submit(binding)
         results = list(ex.map(one, SOURCES))
+        py_link = py.result()
     if verbose_ptxas:
         for _, log in results:
             sys.stderr.write(log)
@@ -72,9 +87,8 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
     tmp = PYMOD + f".{os.getpid()}.tmp"
-    r = subprocess.run([cc, "-O2", "-std=c++17", "-shared", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I",
-                        sysconfig.get_paths()["include"], os.path.join(CSRC, "lola_py.cpp"), "-o", tmp, "-cudart", "none",
-                        "-L", PKG, "-l:liblola.so", "-Xlinker", "-rpath,$ORIGIN"], capture_output=True, text=True)
+    r = subprocess.run([cc, "-shared", "-o", tmp, *py_link, "-cudart", "none", "-L", PKG, "-l:liblola.so",
+                        "-Xlinker", "-rpath,$ORIGIN"], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"building the binding's module failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, PYMOD)
