@@ -127,6 +127,7 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendArgs a) {
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
     const PagedArgs& p = a.p;
 
+    wait_for_last_kernel();
     for (int i = warp; i < nt; i += NT / kWarp) {
         const int t = t0 + i;
         int b = t;
@@ -202,9 +203,8 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendArgs a) {
 // lie side by side in the page (512 tokens, 32/8 heads: 4.5 us one a CTA, 5.5 us four; 1024: 7.4 and 6.6).
 template <typename T, int D>
 cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
-    if (a.n_tokens <= kFew) paged_append_kernel<T, D, 1, 128, 3><<<a.n_tokens, 128, 0, st>>>(a);
-    else paged_append_kernel<T, D, 4, 256, 3><<<(a.n_tokens + 3) / 4, 256, 0, st>>>(a);
-    return cudaGetLastError();
+    if (a.n_tokens <= kFew) return launch_behind(paged_append_kernel<T, D, 1, 128, 3>, (unsigned)a.n_tokens, 128, 0, st, a);
+    return launch_behind(paged_append_kernel<T, D, 4, 256, 3>, (unsigned)(a.n_tokens + 3) / 4, 256, 0, st, a);
 }
 
 }  // namespace

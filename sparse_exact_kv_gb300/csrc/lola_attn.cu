@@ -51,6 +51,7 @@ template <int D, bool PG>
 __global__ void __launch_bounds__(kNT, D == 64 ? 3 : 2) attn_f32_kernel(const AttnArgs a) {
     constexpr int LD = D + 4, TILE = kT * LD;
     extern __shared__ __align__(16) float sm[];       // [2][K, V][kT][LD]
+    wait_for_last_kernel();
     const int h = blockIdx.x % (unsigned)a.Hq, hk = h / a.G;
     TilePos at;
     const bool live = find_tile<kNT, kTQ, PG>(a, (int)(blockIdx.x / (unsigned)a.Hq), &at);
@@ -311,8 +312,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     // at most this many tiles for any cut of total_q rows into n_seq sequences
     const int64_t tiles = ((int64_t)a.total_q + (int64_t)a.n_seq * (kTQ - 1)) / kTQ;
-    attn_f32_kernel<D, PG><<<(unsigned)(tiles * a.Hq), kNT, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_behind(attn_f32_kernel<D, PG>, (unsigned)(tiles * a.Hq), kNT, smem, st, a);
 }
 
 }  // namespace

@@ -179,6 +179,27 @@ cudaError_t opt_in_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
     return e;
 }
 
+// These kernels are launched behind the stream's last kernel without waiting for its end: a CTA may start when
+// that one's CTAs are done (or let it), sets up its barriers, and waits here before it touches global memory
+// -- every CTA, so that a kernel that is done says that all before it are.  In a stream, one sequence of 1000
+// tokens 12.2 -> 9.1 us a call, five short prompts 12.3 -> 9.9.  (They do not let the next kernel start before
+// their end: its first, longest CTAs would gather on the SMs that are free first; float32 prompts 63 -> 68 us.)
+__device__ __forceinline__ void wait_for_last_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t st, const A&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Reads a translation unit's anomaly word and clears it (after the stream's work).
 template <typename S>
 cudaError_t take_word(S& word, int32_t* bits, cudaStream_t st) {

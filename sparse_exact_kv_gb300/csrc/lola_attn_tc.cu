@@ -269,6 +269,7 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
         abort_sm = 0;
     }
     if (warp == kMmaWarp) tmem_alloc<C::kTmem>(smem_u32(&tmem_base));
+    wait_for_last_kernel();
     Finder<C::kQ, PG> find;
     // (before the barriers are there, as nothing of it needs them: five short prompts 11.2 -> 10.4 us; with two
     // tiles it costs the softmax registers, 4 x 4096 x 32 heads 415 -> 431 us)
@@ -747,8 +748,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     // at most this many tiles for any cut of total_q rows into n_seq sequences
     const int64_t tiles = ((int64_t)a.total_q + (int64_t)a.n_seq * (C::kQ - 1)) / C::kQ;
-    attn_tc_kernel<D, NT, PG><<<(unsigned)(tiles * a.Hq), C::kThreads, C::kSmem, st>>>(maps, a);
-    return cudaGetLastError();
+    return launch_behind(attn_tc_kernel<D, NT, PG>, (unsigned)(tiles * a.Hq), C::kThreads, C::kSmem, st, maps, a);
 }
 
 }  // namespace

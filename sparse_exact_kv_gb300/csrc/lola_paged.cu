@@ -460,6 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_f32_kernel(const __g
         abort_sm = 0;
         bars.issued = 0;
     }
+    wait_for_last_kernel();
     Start st;
     if (!find_start(p, a.I, &st)) return;
     if (warp == NW) {
@@ -725,6 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_mma_kernel(const __g
         abort_sm = 0;
         bars.issued = 0;
     }
+    wait_for_last_kernel();
     Start st;
     if (!find_start(p, a.I, &st)) return;
     if (warp == kCons / kWarp) {
@@ -924,8 +926,7 @@ cudaError_t launch_kernel(K kernel, std::atomic<uint64_t>& done, const DecodeArg
     const size_t smem = (size_t)C::kStages * 2 * C::kHalf + 1024;
     cudaError_t e = opt_in_smem(kernel, (int)smem, done);
     if (e != cudaSuccess) return e;
-    kernel<<<kPieces, kThreads, smem, st>>>(maps, make_args(d));
-    return cudaGetLastError();
+    return launch_behind(kernel, kPieces, kThreads, smem, st, maps, make_args(d));
 }
 template <int D>
 cudaError_t launch_f32(const DecodeArgs& d, cudaStream_t st) {
