@@ -28,12 +28,15 @@
 // 2.68 ms, 1640 TFLOP/s, 89 % of the measured bf16 product; 4 x 4096 x 32 heads 412 us, 1333 TFLOP/s): a
 // block pair's products take about 2300 cycles of the issuing thread's 2700, the rest is its wait for
 // the weights (a softmax is 1100 cycles, behind it the other tile's products).  At d = 64 the
-// exponentials weigh twice as much against the products (1060 TFLOP/s); short sequences are bound by an
-// item's own chain: scores, weights, product, epilogue.
+// exponentials weigh twice as much against the products, whose narrow half (N = 64) runs at half rate (1040
+// TFLOP/s); no unit is then above 60 % of its rate, the softmax warps' own dependences are the bound.  Short
+// sequences are bound by an item's own chain: scores, weights, product, epilogue.
 // Tried and slower: releasing P in halves, comparing S by column groups while it loads, one MMA thread
 // for each tile (their products interleave, 9 %), the next pair's waits between the products, one block
-// per CTA without taking over others (4 x 4096 x 32 heads 457 us, ragged prompts 362 against 332), and
-// all sequences' longest tiles first (their K and V no longer fit L2 together: 427 us).
+// per CTA without taking over others (4 x 4096 x 32 heads 457 us, ragged prompts 362 against 332),
+// all sequences' longest tiles first (their K and V no longer fit L2 together: 427 us), and at d = 64 three
+// places for the scores of both tiles, the next ones issued before the weights are there (one prompt of 32768,
+// 16 heads: 2.30 ms against 2.12).
 // Keys in pages: the loader's lanes look a block's pages up while its place in the ring is still being read and
 // load a box each.  Pages of 64 tokens and more cost next to nothing (512 queries behind 6000 keys, 4 times, 32/8
 // heads, d = 128: 205 us, packed rows 200); pages of 16 are 32 boxes of 2 KB a block (286 us).
