@@ -25,16 +25,16 @@
 //     are zeroed in shared memory before the product (0 x NaN would reach rows that do not see
 //     them); the values taken out are added back in the epilogue, for the rows that see them.
 // What bounds it: for long sequences the tensor core and its power (16 heads of 32768 tokens, d = 128:
-// 2.68 ms, 1640 TFLOP/s, 89 % of the measured bf16 product; 4 x 4096 x 32 heads 412 us, 1333 TFLOP/s): a
+// 2.53 ms, 1740 TFLOP/s, 94 % of the measured bf16 product; 4 x 4096 x 32 heads 386 us, 1424 TFLOP/s): a
 // block pair's products take about 2300 cycles of the issuing thread's 2700, the rest is its wait for
 // the weights (a softmax is 1100 cycles, behind it the other tile's products).  At d = 64 the
-// exponentials weigh twice as much against the products, whose narrow half (N = 64) runs at half rate (1040
+// exponentials weigh twice as much against the products, whose narrow half (N = 64) runs at half rate (1050
 // TFLOP/s); no unit is then above 60 % of its rate, the softmax warps' own dependences are the bound.  Short
 // sequences are bound by an item's own chain: scores, weights, product, epilogue.
 // Tried and slower: releasing P in halves, comparing S by column groups while it loads, one MMA thread
 // for each tile (their products interleave, 9 %), the next pair's waits between the products, one block
-// per CTA without taking over others (4 x 4096 x 32 heads 457 us, ragged prompts 362 against 332),
-// all sequences' longest tiles first (their K and V no longer fit L2 together: 427 us), and at d = 64 three
+// per CTA without taking over others (4 x 4096 x 32 heads 457 against 412 us, ragged prompts 362 against
+// 332), all sequences' longest tiles first (their K and V no longer fit L2 together: 427), and at d = 64 three
 // places for the scores of both tiles, the next ones issued before the weights are there (one prompt of 32768,
 // 16 heads: 2.30 ms against 2.12).
 // Keys in pages: the loader's lanes look a block's pages up while its place in the ring is still being read and
@@ -87,6 +87,13 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// two bfloat16 numbers of the larger magnitudes (signs of no meaning); NaN if either is one
+__device__ __forceinline__ uint32_t max_abs2(uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
 }
 
 // Products whose shared-memory descriptors come as a low word (address and leading offset in 16-byte
@@ -532,39 +539,58 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     const int valid = min(kN, t.lk - j * kN);
-                    // 16-byte chunks in memory order, eight in flight; a bfloat16 is not finite iff adding 1
-                    // to its exponent carries into the sign
-                    bool odd = false;
+                    // 16-byte chunks in memory order, eight (32 rows of 64 channels) in flight.  Nearly always all are
+                    // finite: the largest magnitude tells, one instruction a word (a test of every word's exponents, three,
+                    // took 4 x 4096 x 32 heads 412 us, now 382, and 16 prompts of 512 tokens 76, now 67).
                     uint4* p = reinterpret_cast<uint4*>(sm + v_of(pv)) + lane;
+                    uint32_t top[4] = {0u, 0u, 0u, 0u};
+                    auto look = [&](const uint4& y) {
+                        top[0] = max_abs2(top[0], y.x);
+                        top[1] = max_abs2(top[1], y.y);
+                        top[2] = max_abs2(top[2], y.z);
+                        top[3] = max_abs2(top[3], y.w);
+                    };
+                    if (valid == kN) {
 #pragma unroll 1
-                    for (int x0 = 0; x0 < kN * D / 8 / 32; x0 += 8) {
-                        uint4 y[8];
+                        for (int x0 = 0; x0 < kN * D / 8 / 32; x0 += 8) {
+                            uint4 y[8];
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) y[x] = p[32 * (x0 + x)];
-                        uint32_t hit = 0;
+                            for (int x = 0; x < 8; ++x) y[x] = p[32 * (x0 + x)];
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) {
-                            const int row = ((lane + 32 * (x0 + x)) >> 3) & (kN - 1);
-                            const uint32_t w = ((y[x].x & 0x7f807f80u) + 0x00800080u) | ((y[x].y & 0x7f807f80u) + 0x00800080u) |
-                                               ((y[x].z & 0x7f807f80u) + 0x00800080u) | ((y[x].w & 0x7f807f80u) + 0x00800080u);
-                            if (row < valid) hit |= w;
-                            else p[32 * (x0 + x)] = make_uint4(0, 0, 0, 0);
+                            for (int x = 0; x < 8; ++x) look(y[x]);
                         }
-                        if (!(hit & 0x80008000u)) continue;
-                        odd = true;
+                    } else {
 #pragma unroll 1
-                        for (int x = 0; x < 8; ++x) {
-                            const uint4 z = p[32 * (x0 + x)];
+                        for (int x0 = 0; x0 < kN * D / 8 / 32; x0 += 8) {
+                            const int left = valid - ((4 * x0) & (kN - 1)), row = lane >> 3;   // (4 x + lane / 8 of the 32)
+                            if (left > 0) {
+                                uint4 y[8];
+#pragma unroll
+                                for (int x = 0; x < 8; ++x) y[x] = p[32 * (x0 + x)];
+#pragma unroll
+                                for (int x = 0; x < 8; ++x)
+                                    if (4 * x + row < left) look(y[x]);
+                            }
+#pragma unroll
+                            for (int x = 0; x < 8; ++x)
+                                if (4 * x + row >= left) p[32 * (x0 + x)] = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    const uint32_t most = max_abs2(max_abs2(top[0], top[1]), max_abs2(top[2], top[3]));
+                    if (__any_sync(0xffffffffu, (most & 0x7f80u) == 0x7f80u || (most & 0x7f800000u) == 0x7f800000u)) {
+                        if (lane == 0) *reinterpret_cast<volatile int*>(&odd_sm[n & 1]) = 1;
+#pragma unroll 1
+                        for (int x = 0; x < kN * D / 8 / 32; ++x) {
+                            const uint4 z = p[32 * x];
                             uint32_t w[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const bool lo = (w[e] & 0x7f80u) == 0x7f80u, up = (w[e] & 0x7f800000u) == 0x7f800000u;
                                 w[e] &= (lo ? 0xffff0000u : ~0u) & (up ? 0xffffu : ~0u);
                             }
-                            p[32 * (x0 + x)] = make_uint4(w[0], w[1], w[2], w[3]);
+                            p[32 * x] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }
-                    if (odd) *reinterpret_cast<volatile int*>(&odd_sm[n & 1]) = 1;
                     fence_async_smem();
                     __threadfence_block();
                     __syncwarp();
@@ -759,22 +785,22 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
 // One or two tiles per CTA?  An item costs about o + s B microseconds, B the key blocks its tiles read on
 // average: measured on prompts of 128 to 8192 tokens, 8 heads (us; two tiles: a round of 152 CTAs, one
 // tile: a round of 304, two on an SM),
-//            d = 128, two: 8.6 + 1.46 B   one: 6.8 + 1.69 B      d = 64, two: 6.4 + 1.13 B   one: 5.0 + 1.23 B
-// so two tiles for long sequences (19 prompts of 4096 tokens, d = 128: 518 against 560 us), and one for short
-// ones (304 of 128 tokens: 69 against 89 us) and where its finer cut saves a round (10 tiles of ~50 blocks,
-// 16 heads, d = 64: 80 against 125 us).  The tiles of a ragged batch are not known here: half a tile is
-// added for each sequence, or what the grid may come to where the rounds are few and a tile more can
-// cost a whole one.
+//            d = 128, two: 6.8 + 1.39 B   one: 6.4 + 1.67 B      d = 64, two: 5.2 + 1.18 B   one: 5.0 + 1.30 B
+// so two tiles for long sequences (19 prompts of 4096 tokens, d = 128: 469 against 537 us), and one for short
+// ones (304 of 128 tokens: 61 against 79 us) and where its finer cut saves a round (10 tiles of ~50 blocks,
+// 16 heads, d = 64: 80 against 121 us).  The tiles of a ragged batch are not known here: for each sequence half a
+// tile is added, less with two (their last item has one tile half of the time), or, where the rounds are few and
+// a tile more can cost a whole one, what the grid may come to.
 static bool one_tile(const AttnArgs& a) {
     const double n = a.n_seq, lq = a.total_q / n, lk = a.total_k / n;
     const double blocks = (lk > lq ? lk - lq / 2 : lk / 2) / kN + 0.5;
     auto cost = [&](int nt, double o, double s) {
         const double q = nt * kM, slots = nt == 2 ? 152 : 304;
         const double most = (double)(((int64_t)a.total_q + (int64_t)a.n_seq * (int64_t)(q - 1)) / (int64_t)q) * a.Hq / slots;
-        const double mean = (a.total_q / q + 0.5 * n) * a.Hq / slots;
-        return (most <= 4 ? std::ceil(most) : std::ceil(mean)) * (o + s * blocks);
+        const double mean = (a.total_q / q + (nt == 2 ? 0.3 : 0.5) * n) * a.Hq / slots;
+        return (most <= 4 ? std::ceil(most) : mean) * (o + s * blocks);
     };
-    return a.d == 128 ? cost(1, 6.8, 1.69) < cost(2, 8.6, 1.46) : cost(1, 5.0, 1.23) < cost(2, 6.4, 1.13);
+    return a.d == 128 ? cost(1, 6.4, 1.67) < cost(2, 6.8, 1.39) : cost(1, 5.0, 1.30) < cost(2, 5.2, 1.18);
 }
 
 template <bool PG> static cudaError_t launch_form(const AttnArgs& a, cudaStream_t st) {
