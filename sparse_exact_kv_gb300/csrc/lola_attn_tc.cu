@@ -39,7 +39,7 @@
 // 16 heads: 2.30 ms against 2.12).
 // Keys in pages: the loader's lanes look a block's pages up while its place in the ring is still being read and
 // load a box each.  Pages of 64 tokens and more cost next to nothing (512 queries behind 6000 keys, 4 times, 32/8
-// heads, d = 128: 205 us, packed rows 200); pages of 16 are 32 boxes of 2 KB a block (286 us).
+// heads, d = 128: 199 us, packed rows 191); pages of 16 are 32 boxes of 2 KB a block (284 us).
 // Every wait is bounded (1 s, those that may last a whole item 10 s, then LOLA_ATTN_TIMEOUT).
 #include <cuda.h>
 

@@ -572,6 +572,66 @@ def test_paged_prefill_in_a_graph_with_other_lengths(L, gen):
         assert (out[r:] == 5.0).all()
 
 
+def test_kernels_behind_copies_sets_and_other_streams(L, gen):
+    """The kernels start behind whatever the stream did last: copies, memsets, kernels of another stream,
+    each other, in a stream and in a graph; every result is that of the same calls one by one."""
+    lens, page = [300, 77, 1], 16
+    c = Paged(gen, lens, 2, 64, page, BF)
+    lay = L.ExactAttention(4, 2, 64, BF, c.k_pool, c.v_pool)
+    src = [(randn(gen, 3, 4, 64, dtype=BF), randn(gen, 3, 2, 64, dtype=BF), randn(gen, 3, 2, 64, dtype=BF)) for _ in range(4)]
+    q, k, v = (torch.empty_like(x) for x in src[0])
+    cu, inv = offsets([1, 1, 1]), _freq(64)
+    out = [torch.empty_like(q) for _ in range(3)]
+    side = torch.cuda.Stream()
+
+    def step(wait=lambda: None):
+        out[0].zero_()                                         # a memset
+        q.copy_(src_now[0])                                    # copies
+        k.copy_(src_now[1])
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            v.copy_(src_now[2].mul(0.5))                       # another stream's kernels
+        torch.cuda.current_stream().wait_stream(side)
+        wait()
+        qr = lay.append(k, v, c.kv_len, c.table, q=q, inv_freq=inv)
+        wait()
+        lay.decode_step(qr, c.kv_len, c.table, out=out[0])
+        wait()
+        lay.prefill_paged(qr, cu, c.kv_len, c.table, out=out[1])
+        wait()
+        lay.decode_step(out[0], c.kv_len, c.table, out=out[2])
+        wait()
+        out[1].mul_(2.0)                                       # an ordinary kernel behind them
+
+    src_now = [torch.empty_like(x) for x in src[0]]
+    torch.cuda.synchronize()
+    want = []
+    for x in src:
+        for a, b in zip(src_now, x):
+            a.copy_(b)
+        step(torch.cuda.synchronize)
+        want.append([o.clone() for o in out])
+    main = torch.cuda.Stream()
+    with torch.cuda.stream(main):
+        for x, w in zip(src, want):
+            for a, b in zip(src_now, x):
+                a.copy_(b)
+            step()
+            assert all(torch.equal(a, b) for a, b in zip(out, w))
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=main):
+            step()
+            step()
+        for x, w in zip(src, want):
+            for a, b in zip(src_now, x):
+                a.copy_(b)
+            g.replay()
+            assert all(torch.equal(a, b) for a, b in zip(out, w))
+    torch.cuda.synchronize()
+    quiet(L)
+
+
 # ---------------------------------------------------------------------------------------
 # the paged cache: rotation and append
 # ---------------------------------------------------------------------------------------
