@@ -457,7 +457,7 @@ class ExactAttention:
     runs ``prefill`` needs none.  Outputs and the decode step's workspace are allocated through
     torch on the call's stream, so calls on several streams do not share any.  Shapes, types and
     devices are checked here, strides and alignment by the library; all tensors are on the current
-    CUDA device."""
+    CUDA device.  For serving: outputs carry no gradient."""
 
     __slots__ = ("cfg", "Hq", "Hkv", "d", "dtype", "k_pool", "v_pool", "_ws", "_plan")
 
