@@ -39,6 +39,15 @@ __device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
     hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
     lo = __float_as_uint(x - __uint_as_float(hi));
 }
+// ... of a value: hi stops at the largest finite tf32, so that the finite values above it (from 0x7f7ff000 on, which
+// round to infinity) keep finite parts.  Scores need no such stop: those that come out NaN are formed again.
+__device__ __forceinline__ void split_value(float x, uint32_t& hi, uint32_t& lo) {
+    const float r = __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u);
+    float h;
+    asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(h) : "f"(r), "f"(__uint_as_float(0x7f7fe000u)));   // the smaller magnitude, r's sign
+    hi = __float_as_uint(h);
+    lo = __float_as_uint(x - h);
+}
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -229,8 +238,8 @@ __global__ void __launch_bounds__(kNT, D == 64 ? 3 : 2) attn_f32_kernel(const At
 #pragma unroll
             for (int x = 0; x < D / 8; ++x) {
                 uint32_t h0, l0, h1, l1;
-                split(vp[8 * x], h0, l0);
-                split(vp[LD + 8 * x], h1, l1);
+                split_value(vp[8 * x], h0, l0);
+                split_value(vp[LD + 8 * x], h1, l1);
                 mma_tf32(o[x], ph, l0, l1);
                 mma_tf32(o[x], pl, h0, h1);
                 mma_tf32(o[x], ph, h0, h1);

@@ -1,0 +1,69 @@
+"""Exact attention on the GPU at the edges of its types and of its kernels' forms.  Bounds:
+tests/attn_parity.py, and beside the tests that need closer ones."""
+import math
+
+import pytest
+import torch
+
+from attn_parity import Paged, attend, check, check_decode, check_prefill, ints, offsets, randn
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+MAX = torch.finfo(F32).max
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import sparse_exact_kv_gb300 as lib
+    return lib
+
+
+@pytest.fixture
+def gen():
+    return torch.Generator(device="cuda").manual_seed(23)
+
+
+def quiet(L):
+    st, bits = L.lola_attn_status()
+    assert st == 0 and bits == 0, bits
+
+
+def prompt(L, q, k, v, paged, dtype=F32, lse=None):
+    """One prompt, its keys and values packed or in the pages of a cache."""
+    n, Hq, Hkv, d = q.shape[0], q.shape[1], k.shape[1], q.shape[2]
+    if not paged:
+        return L.ExactAttention(Hq, Hkv, d, dtype).prefill(q, k, v, offsets([n]), lse=lse)
+    page, need = 16, -(-n // 16)
+    pools = []
+    for x in (k, v):
+        pool = torch.zeros(need * page, Hkv, d, dtype=dtype, device="cuda")
+        pool[:n] = x
+        pools.append(pool.view(need, page, Hkv, d).transpose(1, 2).contiguous())
+    lay = L.ExactAttention(Hq, Hkv, d, dtype, *pools)
+    return lay.prefill_paged(q, offsets([n]), ints([n]), ints([list(range(need))]), n, lse=lse)
+
+
+# ---------------------------------------------------------------------------------------
+# float32 prompts: the operands' two parts
+# ---------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("paged", [False, True], ids=["packed", "paged"])
+def test_f32_prompt_values_next_to_the_largest(L, gen, d, paged):
+    """The largest finite values: rows before them are the same bits as without, rows from them on are
+    finite (one such value a channel, so that no sum of theirs passes the type)."""
+    n = 200
+    q, k, v = (randn(gen, n, 1, d, dtype=F32) for _ in range(3))
+    big = {(70, 3): MAX, (130, 9): -MAX, (131, 17): 3.4019938e38, (131, 18): -3.402e38, (199, 20): MAX}
+    for (at, ch), x in big.items():
+        v[at, 0, ch] = x
+    out = prompt(L, q, k, v, paged)
+    quiet(L)
+    for first in (70, 130, 131, 199):
+        v0 = v.clone()
+        v0[first:] = 0.0
+        assert torch.equal(out[:first], prompt(L, q, k, v0, paged)[:first])
+    assert bool(torch.isfinite(out).all())
+    check_prefill(q, k, v, [n], [n], out)
