@@ -173,13 +173,15 @@ __global__ void __launch_bounds__(kNT, D == 64 ? 3 : 2) attn_f32_kernel(const At
                 nan |= s[n][e] != s[n][e];
             }
         if (__any_sync(0xffffffffu, nan)) {
-            // a query or key is not finite: these scores once more, term by term
+            // a query or key is not finite, or its upper part is not: these scores, and no others (a row's bits are
+            // not to depend on keys that it does not see), once more, term by term
 #pragma unroll
             for (int n = 0; n < kTW / 8; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int r = row0 + 8 * (e >> 1);
                     const float* kp = Ks + (kw + 8 * n + 2 * t + (e & 1)) * LD;
+                    if (s[n][e] == s[n][e]) continue;
                     float x = 0.f;
                     if (r < lq)
 #pragma unroll 1

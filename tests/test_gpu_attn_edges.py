@@ -67,3 +67,28 @@ def test_f32_prompt_values_next_to_the_largest(L, gen, d, paged):
         assert torch.equal(out[:first], prompt(L, q, k, v0, paged)[:first])
     assert bool(torch.isfinite(out).all())
     check_prefill(q, k, v, [n], [n], out)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("paged", [False, True], ids=["packed", "paged"])
+def test_f32_prompt_unseen_keys_leave_the_bits(L, gen, d, bad, paged):
+    """A key that is not finite changes no bit of the rows before it.  Behind it a score of minus infinity
+    is a key of no weight; plus infinity or NaN makes the row NaN, as exp(inf - inf) is."""
+    n = 300
+    q, k, v = (randn(gen, n, 1, d, dtype=F32) for _ in range(3))
+    want = prompt(L, q, k, v, paged)
+    k[250, 0, 7] = bad
+    lse = torch.empty(1, n, device="cuda")
+    out = prompt(L, q, k, v, paged, lse=lse)
+    quiet(L)
+    assert torch.equal(out[:250], want[:250])
+    none = torch.zeros(n, dtype=torch.bool, device="cuda")
+    if not math.isnan(bad):                                    # the score is minus infinity: the key is not there
+        none[250:] = q[250:, 0, 7] * bad < 0
+    assert bool(torch.isnan(out[250:][~none[250:]]).all())
+    for r in torch.nonzero(none).flatten().tolist():
+        seen = torch.arange(r + 1, device="cuda") != 250
+        o, ls, to, tl = attend(q[r, 0][None], k[:r + 1, 0], v[:r + 1, 0], seen[None])
+        check(out[r, 0][None], o, to, f"row {r}")
+        check(lse[0, r][None], ls, tl, f"lse of row {r}")
