@@ -369,7 +369,8 @@ int32_t lola_hola_status(const lola_hola_config* cfg, int32_t n, const void* wor
  *   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(c q_i . k_j),  lse_i = log sum_j p_ij
  * over the keys j that the row sees.  A row that sees no key gets o = 0 and lse = -infinity;
  * keys a row does not see have no influence on it, whatever their bits (NaN included).
- * Scores, maxima, sums and the running output are float32; with bfloat16 io the weights p are
+ * Scores, maxima, sums and the running output are float32; prompts of float32 io form their products
+ * from two tf32 parts of each operand (good to 2^-21 of |a b| each); with bfloat16 io the weights p are
  * rounded to bfloat16 for the product with V (at most 2^-8 relative each, as the output's
  * own rounding, and averaged over the keys), the sum is taken over the unrounded weights,
  * and o is rounded once.  Device-side anomalies go to a word per device read with lola_attn_status(). */

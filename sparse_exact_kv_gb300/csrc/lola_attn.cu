@@ -7,20 +7,24 @@
 //   O' = 2^{m - m'} O + sum_j 2^{s_j - m'} v_j,        o = O / l,  lse = ln 2 (m + log2 l).
 //
 // Both products run on the warps' tensor instructions in tf32, every operand split as x = hi + lo with hi
-// the nearest tf32 (2^-11 relative) and lo = x - hi exact: a b ~ hi hi + hi lo + lo hi.  Left out are
-// lo lo (2^-22 of a b) and lo's own bits behind tf32's (2^-21), so a product is good to about 2^-20 of
-// |a b|, averaged over its terms to well below the float32 sum's own rounding at these widths.  CUDA
-// cores need two shared-memory reads for 16 products here and were bound by those (31 TFLOP/s at
-// d = 128, half of the FMA rate at best); the tensor form reads an operand once for 16 rows.
+// the nearest tf32 and lo = x - hi exact: a b ~ hi hi + hi lo + lo hi.  |lo| <= 2^-11 |x| has one bit more than
+// tf32 holds, so what is left out of a product is lo lo (2^-22 of |a b|) and that bit twice (2^-23 each):
+// 2^-21 of |a b| at most, about a float32 product's rounding in the mean.  The instruction cuts its sums off
+// instead of rounding them: a running output kept in its accumulators loses part of a last place every step,
+// always towards zero (16000 keys: 1e-5 of the output, float32 sums 3e-7).  So it only adds 16 keys of the
+// output, and half of the channels of a score, and those sums are added in float32, rounded (2e-7; 65 -> 67 us for
+// three prompts of 512-1024 tokens, 8/2 heads, d = 64, and 111 -> 123 us at d = 128).  CUDA cores need two
+// shared-memory reads for 16 products here and were bound by those (31 TFLOP/s at d = 128, half of the FMA rate
+// at best); the tensor form reads an operand once for 16 rows.
 //
 // A CTA of four warps takes 32 queries of one head and 32 keys at a time, two tiles of K and V in flight
 // (cp.async): 16 queries and 16 keys of every tile a warp, the two halves of a query's keys joined at the
 // end (a warp that sees all keys of 16 queries is alone with the longest prompts: 78 us against 62 for
-// three prompts of 512-1024 tokens, 8 heads, d = 64).  Bound by the instruction's rate, about 256
-// multiply-adds a cycle and SM: 53 TFLOP/s of attention, 159 of products (4000 tokens, 16 heads).  Rows of 4 floats more than d keep every fragment read free of bank conflicts: K's
-// (key = lane / 4, channel = lane % 4) and V's (key = 2 (lane % 4), channel = lane / 4), where keys 2 t and
-// 2 t + 1 stand in for the instruction's rows t and t + 4, so that the scores' accumulators are the
-// weights' operand as they stand.
+// three prompts of 512-1024 tokens, 8 heads, d = 64).  Bound by the instruction's rate, about 256 multiply-adds
+// a cycle and SM, and the splits beside it: 49 TFLOP/s of attention, 146 of products (4000 tokens, 16 heads, d = 64).
+// Rows of 4 floats more than d keep every fragment read free of bank conflicts: K's (key = lane / 4, channel =
+// lane % 4) and V's (key = 2 (lane % 4), channel = lane / 4), where keys 2 t and 2 t + 1 stand in for the
+// instruction's rows t and t + 4, so that the scores' accumulators are the weights' operand as they stand.
 #include "lola_attn.cuh"
 #include "lola_tc.cuh"
 
@@ -146,8 +150,8 @@ __global__ void __launch_bounds__(kNT, D == 64 ? 3 : 2) attn_f32_kernel(const At
             const float4 v = *reinterpret_cast<const float4*>(Vs + e / (D / 4) * LD + e % (D / 4) * 4);
             worst = fmaf(v.x, 0.f, fmaf(v.y, 0.f, fmaf(v.z, 0.f, fmaf(v.w, 0.f, worst))));
         }
-        // ---- S: 16 rows x 16 keys ----
-        float s[kTW / 8][4] = {}, sl[kTW / 8][4] = {};
+        // ---- S: 16 rows x 16 keys, the channels in two halves ----
+        float s[kTW / 8][4] = {}, s1[kTW / 8][4] = {}, sl[kTW / 8][4] = {};
 #pragma unroll
         for (int x = 0; x < D / 8; ++x) {
             uint32_t ah[4], al[4];
@@ -161,7 +165,7 @@ __global__ void __launch_bounds__(kNT, D == 64 ? 3 : 2) attn_f32_kernel(const At
                 split(kp[4], h1, l1);
                 mma_tf32(sl[n], ah, l0, l1);
                 mma_tf32(sl[n], al, h0, h1);
-                mma_tf32(s[n], ah, h0, h1);
+                mma_tf32(x < D / 16 ? s[n] : s1[n], ah, h0, h1);
             }
         }
         bool nan = false;
@@ -169,7 +173,7 @@ __global__ void __launch_bounds__(kNT, D == 64 ? 3 : 2) attn_f32_kernel(const At
         for (int n = 0; n < kTW / 8; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                s[n][e] += sl[n][e];
+                s[n][e] += s1[n][e] + sl[n][e];
                 nan |= s[n][e] != s[n][e];
             }
         if (__any_sync(0xffffffffu, nan)) {
@@ -229,23 +233,35 @@ __global__ void __launch_bounds__(kNT, D == 64 ? 3 : 2) attn_f32_kernel(const At
             __syncthreads();
         }
         // ---- O += P V: keys 2 t and 2 t + 1 of eight as the instruction's t and t + 4 ----
+        // (four channel groups side by side, so that their products do not wait for each other: one at a time 71 us)
+        uint32_t ph[kTW / 8][4], pl[kTW / 8][4];
 #pragma unroll
-        for (int n = 0; n < kTW / 8; ++n) {
-            uint32_t ph[4], pl[4];
-            split(s[n][0], ph[0], pl[0]);
-            split(s[n][2], ph[1], pl[1]);
-            split(s[n][1], ph[2], pl[2]);
-            split(s[n][3], ph[3], pl[3]);
-            const float* vp = Vs + (kw + 8 * n + 2 * t) * LD + g;
+        for (int n = 0; n < kTW / 8; ++n)
 #pragma unroll
-            for (int x = 0; x < D / 8; ++x) {
-                uint32_t h0, l0, h1, l1;
-                split_value(vp[8 * x], h0, l0);
-                split_value(vp[LD + 8 * x], h1, l1);
-                mma_tf32(o[x], ph, l0, l1);
-                mma_tf32(o[x], pl, h0, h1);
-                mma_tf32(o[x], ph, h0, h1);
+            for (int e = 0; e < 4; ++e) split(s[n][2 * (e & 1) + (e >> 1)], ph[n][e], pl[n][e]);
+#pragma unroll
+        for (int x = 0; x < D / 8; x += 4) {
+            float c[4][4] = {};
+#pragma unroll
+            for (int n = 0; n < kTW / 8; ++n) {
+                uint32_t h0[4], l0[4], h1[4], l1[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const float* vp = Vs + (kw + 8 * n + 2 * t) * LD + g + 8 * (x + y);
+                    split_value(vp[0], h0[y], l0[y]);
+                    split_value(vp[LD], h1[y], l1[y]);
+                }
+#pragma unroll
+                for (int y = 0; y < 4; ++y) mma_tf32(c[y], ph[n], l0[y], l1[y]);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) mma_tf32(c[y], pl[n], h0[y], h1[y]);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) mma_tf32(c[y], ph[n], h0[y], h1[y]);
             }
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[x + y][e] += c[y][e];
         }
         if (odd) {
             // what was zeroed, for the keys a row sees

@@ -92,3 +92,25 @@ def test_f32_prompt_unseen_keys_leave_the_bits(L, gen, d, bad, paged):
         o, ls, to, tl = attend(q[r, 0][None], k[:r + 1, 0], v[:r + 1, 0], seen[None])
         check(out[r, 0][None], o, to, f"row {r}")
         check(lse[0, r][None], ls, tl, f"lse of row {r}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("paged", [False, True], ids=["packed", "paged"])
+def test_f32_prompt_sums_are_rounded(L, gen, d, paged):
+    """One key with a weight near all and many with small ones, values of one: the output is one.
+
+    Bound: of the keys' tiles of 32 a warp takes 16 keys each, N tiles in all, and adds their sum to its
+    output and to its normaliser, which stay within [1, 2): half a step of 2^-23 each, N 2^-23 together.  The
+    small weights' own sums and parts (0.3 of the whole, (9 terms + 54) 2^-23 of it at most), the
+    joins and the division: 32 2^-23.  Sums cut off instead lose half a step on average for each of the four
+    instructions of a tile, 2 N 2^-23."""
+    n = 16000
+    q = torch.zeros(n, 1, d, device="cuda")
+    q[..., 0] = math.sqrt(d)
+    k = torch.zeros(n, 1, d, device="cuda")
+    k[1:, 0, 0] = -16 * math.log(2.0) + 0.3 * randn(gen, n - 1, dtype=F32)
+    out = prompt(L, q, k, torch.ones(n, 1, d, device="cuda"), paged)
+    quiet(L)
+    tol = (torch.arange(n, device="cuda").double() / 32 + 1 + 32) * 2.0 ** -23
+    over = (out[:, 0].double() - 1).abs().amax(-1) - tol
+    assert float(over.max()) <= 0, f"{float(((out - 1).abs().amax()) * 2 ** 23)} steps"
