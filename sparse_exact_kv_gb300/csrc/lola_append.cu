@@ -3,8 +3,10 @@
 // A pair (a, b) of channel pair i at position p becomes (a cos x - b sin x, b cos x + a sin x),
 // x = p w_i.  The angle only matters modulo one turn, so the kernel keeps W_i = frac(w_i / 2 pi)
 // as a 64-bit fixed-point fraction of a turn and takes p W_i modulo 2^64: the turn's fraction to
-// about 2^-56 p (from the double product w_i / 2 pi), exact in the reduction, whatever p.  Its top
-// 32 bits, read as a signed fraction, go to sincospif.
+// about 2^-56 p (from the double product w_i / 2 pi), exact in the reduction, whatever p.  Its top 32 bits
+// are taken to the nearest quarter turn as an integer, and only the rest, an eighth of a turn at most, becomes a
+// float32 number and goes to sincospif: it is then good to 2^-27 half turns (a whole turn in float32: 2^-25, cosines
+// 1.2e-7 off where their own rounding is 3e-8).
 //
 // Bound by HBM bytes for prompts (every element read once and written once, 16-byte accesses,
 // a pair's two halves in one thread, three such units in flight a thread; 18 k tokens of 32/8 heads:
@@ -162,7 +164,15 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendArgs a) {
         const int i = TOK == 1 ? 0 : e / (rot / 2), f = e - i * (rot / 2);
         const uint64_t x = turn_sm[f] * (uint64_t)(int64_t)pos_sm[i];    // modulo one turn
         float s, c;
-        sincospif((float)(int32_t)(uint32_t)(x >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns
+        // the nearest quarter turn and the rest, at most an eighth of a turn either way
+        const uint32_t z = (uint32_t)(x >> 32), quarter = (z + 0x20000000u) >> 30;
+        sincospif((float)(int32_t)(z - (quarter << 30)) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns
+        if (quarter & 1) {
+            const float y = c;
+            c = -s;
+            s = y;
+        }
+        if (quarter & 2) c = -c, s = -s;
         reinterpret_cast<float2*>(cs[i])[((f % VN / 2) * ru + f / VN) * 2 + (f & 1)] = make_float2(c, s);
     }
     __syncthreads();

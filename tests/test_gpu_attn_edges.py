@@ -114,3 +114,35 @@ def test_f32_prompt_sums_are_rounded(L, gen, d, paged):
     tol = (torch.arange(n, device="cuda").double() / 32 + 1 + 32) * 2.0 ** -23
     over = (out[:, 0].double() - 1).abs().amax(-1) - tol
     assert float(over.max()) <= 0, f"{float(((out - 1).abs().amax()) * 2 ** 23)} steps"
+
+
+# ---------------------------------------------------------------------------------------
+# the paged cache: rotation and append
+# ---------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("pairs", ["halves", "neighbours"])
+@pytest.mark.parametrize("n", [700, 9001])
+def test_append_cosines(L, gen, n, pairs):
+    """Pairs (1, 0) and (0, 1) show the cosines and sines themselves, all around the circle.
+
+    Bound: the rest of a quarter turn as float32, at most 2^-2 half turns: half a step 2^-27, times pi; what is cut
+    off the 64-bit turn, 2^-31 half turns; a step of the functions' own, 2^-24 below one."""
+    d, page = 128, 64
+    c = Paged(gen, [n], 1, d, page, F32)
+    x = torch.zeros(n, 2, d, device="cuda")
+    a = slice(0, d // 2) if pairs == "halves" else slice(0, d, 2)
+    b = slice(d // 2, d) if pairs == "halves" else slice(1, d, 2)
+    x[:, 0, a] = 1.0
+    x[:, 1, b] = 1.0
+    inv = (10000.0 ** (-torch.arange(0, d, 2, dtype=torch.float64) / d)).float().cuda()
+    lay = L.ExactAttention(2, 1, d, F32, c.k_pool, c.v_pool)
+    pos = torch.arange(n, device="cuda")
+    y = lay.append(x[:, :1], x[:, 1:], c.kv_len, c.table, cu_new=offsets([n]), q=x, inv_freq=inv, pairs=pairs)
+    quiet(L)
+    angle = pos[:, None].double() * inv.double()
+    tol = math.pi * (2.0 ** -27 + 2.0 ** -31) + 2.0 ** -24
+    stored = c.k_pool[c.table[0].long()[pos // page], 0, pos % page]
+    for got, want in ((y[:, 0, a], angle.cos()), (y[:, 0, b], angle.sin()), (y[:, 1, a], -angle.sin()),
+                      (y[:, 1, b], angle.cos()), (stored[:, a], angle.cos()), (stored[:, b], angle.sin())):
+        worst = float((got.double() - want).abs().max())
+        assert worst <= tol, worst
