@@ -4,8 +4,9 @@
 // Row i of a sequence with Lq queries and Lk keys sees the keys j <= i + Lk - Lq.  One pass over
 // the keys in blocks of 128 with a running maximum m and sum l per row (log2 units):
 //   S = Q K^T,  P = 2^{c S - m},  l += sum P,  O += P V,      o = O / l,
-// m is raised lazily: O and l are rescaled (in TMEM) only when a block's maximum passes m by more
-// than 2^8, so that P and l stay far inside float32 and bfloat16, and blocks rarely wait for O.
+// m is raised lazily: it is set 8 above a maximum (log2 units), and O and l are rescaled (in TMEM) only when a
+// later block's maximum passes it, so that blocks rarely wait for O.  No weight is above one, as with the maximum
+// itself, so that O does not pass float32 where the values do not.
 //
 // An item is 256 queries of one head, two tiles of 128 (MMA M = 128, TMEM lane = query) that share every
 // K and V block; while the tensor core works for one tile, the other tile's softmax runs.  Short
@@ -58,7 +59,7 @@ __device__ int32_t g_status;
 constexpr int kM = 128;                  // queries per tile
 constexpr int kN = 128;                  // keys per block
 constexpr int kClean = 4;                // barriers of the blocks to be cleaned
-constexpr float kRaise = 8.0f;           // m is raised when a block's maximum passes it by this (log2)
+constexpr float kRaise = 8.0f;           // m is set this far above a block's maximum (log2), and raised when one passes it
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint64_t kItemNs = 10000000000ull;   // ... of the waits that may last a whole item
 
@@ -639,13 +640,13 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
                 float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
                 for (int x = 4; x < kN; ++x) mx[x & 3] = fmaxf(mx[x & 3], s[x]);
-                const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                const bool need = bm > m + kRaise;
+                const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c, kRaise);
+                const bool need = top > m + kRaise;
                 if (j == 0) {
-                    m = bm;
+                    m = top;
                 } else if (__any_sync(0xffffffffu, need)) {
                     // (O_i is quiet: S of this block was issued behind the block before's P V, and is done)
-                    const float f = need ? ex2(m - bm) : 1.f;
+                    const float f = need ? ex2(m - top) : 1.f;
                     l *= f;
                     // (rare, and with S in registers: 16 columns at a time)
 #pragma unroll 1
@@ -657,7 +658,7 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
                         for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
                         tmem_st16(to + x, o);
                     }
-                    if (need) m = bm;
+                    if (need) m = top;
                 }
                 const float base = m == -INFINITY ? 0.f : m;
                 float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};

@@ -35,7 +35,7 @@ constexpr int kThreads = kCons + kWarp;
 constexpr int kPieces = 152;              // one CTA per SM
 constexpr int kRows = 16;                 // query rows of a row group (at most)
 constexpr int kJoin = 16;                 // pieces joined at a time
-constexpr float kRaise = 8.0f;            // m is raised when a maximum passes it by this (log2)
+constexpr float kRaise = 8.0f;            // bf16: m is set this far above a maximum (log2), and raised when one passes it
 constexpr uint64_t kWaitNs = 1000000000ull;
 
 struct Maps {
@@ -431,8 +431,8 @@ __device__ void join_pieces(const Args& a, const Seg& g, int t, int* go, F&& bar
 // all threads on one tile and two barriers in it, 64 sequences of 4000 tokens, 4 heads of 64, took 184 us, now 86).
 // Lanes 8 tg + j: chunk j (16 bytes) of every 128-byte column of the rows, tokens 4 i + tg, so that K and V are
 // read once, without bank conflicts, into products with q and the output in registers; the eight lanes' sums
-// of a score are added and dealt out by halves (14 shuffles for 16 tokens x 4 rows).  m is raised lazily, by
-// more than 2^8 at a time.
+// of a score are added and dealt out by halves (14 shuffles for 16 tokens x 4 rows).  m is the maximum so far:
+// the largest weights' exponents stay near zero, where they lose least.
 template <int D, int RM>
 __global__ void __launch_bounds__(kThreads, 1) paged_decode_f32_kernel(const __grid_constant__ Maps maps, const Args a) {
     using C = Cfg<float, D>;
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_f32_kernel(const __g
                     bm[e] = z[e];
 #pragma unroll
                     for (int o = 2; o < kWarp; o <<= 1) bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], o));
-                    need[e] = bm[e] > m[e] + kRaise || (m[e] == -INFINITY && bm[e] > m[e]);
+                    need[e] = bm[e] > m[e];
                 }
                 if (__any_sync(0xffffffffu, need[0] || need[1])) {
                     float f[2];
@@ -664,8 +664,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_f32_kernel(const __g
 // tile's bytes come faster than four warps get through it, they take a segment's tiles in turn (64 x 8000 tokens,
 // 16/8 heads: 171 us, 214 on segments in turn).  A warp takes 16 of a tile's 64 tokens, with its own running
 // maximum, sum and output of the 16 query rows, joined at the segment's end.  S = Q K^T has the rows of Q as M, so
-// that its accumulators are the A operand of P V as they stand.  m is raised lazily (by more than
-// 2^8 at a time), which leaves the output alone for most tiles.
+// that its accumulators are the A operand of P V as they stand.  m is raised lazily (it is set 8 above a
+// maximum, so that no weight is above one), which leaves the output alone for most tiles.
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -811,11 +811,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_mma_kernel(const __g
             for (int r = 0; r < HR; ++r) {
                 float bm = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
                 bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
-                bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2)) * a.scale_log2;
-                const bool need = bm > m[r] + kRaise || (m[r] == -INFINITY && bm > m[r]);
+                const float top = fmaf(fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2)), a.scale_log2, kRaise);
+                const bool need = top > m[r] + kRaise;
                 if (__any_sync(0xffffffffu, need)) {
-                    const float f = need ? ex2(m[r] - bm) : 1.f;
-                    if (need) m[r] = bm;
+                    const float f = need ? ex2(m[r] - top) : 1.f;
+                    if (need) m[r] = top;
                     l[r] *= f;
 #pragma unroll
                     for (int y = 0; y < D / 8; ++y) {

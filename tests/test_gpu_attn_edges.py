@@ -117,6 +117,60 @@ def test_f32_prompt_sums_are_rounded(L, gen, d, paged):
 
 
 # ---------------------------------------------------------------------------------------
+# large values under a rising maximum
+# ---------------------------------------------------------------------------------------
+
+def _rising(n, H, d, dtype):
+    """Scores that rise by 6.5 (log2) after the first block, and one value of 3e38 behind the rise."""
+    q, k, v = (torch.zeros(n, H, d, dtype=dtype, device="cuda") for _ in range(3))
+    q[..., 0] = 1.0
+    k[n // 2:, :, 0] = 4.5 * math.sqrt(d)
+    v[2 * n // 3, :, 5] = 3e38
+    v[..., 6] = 1.0
+    return q, k, v
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 128), (F32, 64)])
+@pytest.mark.parametrize("beside", [0, 20000], ids=["one-tile", "two-tiles"])
+def test_prompt_large_values_under_a_rising_maximum(L, gen, dtype, d, beside):
+    """Weights are at most one, so a finite value with a weight below one stays finite."""
+    if dtype == F32 and beside:
+        beside = 500
+    n, Hq, Hkv = 600, 16, 4
+    q, k, v = _rising(n, Hkv, d, dtype)
+    q = q.repeat_interleave(Hq // Hkv, 1)
+    lens = [n] + [beside] * (beside > 0)
+    if beside:
+        q, k, v = (torch.cat([x, randn(gen, beside, x.shape[1], d, dtype=dtype)]) for x in (q, k, v))
+    lse = torch.empty(Hq, sum(lens), device="cuda")
+    out = L.ExactAttention(Hq, Hkv, d, dtype).prefill(q, k, v, offsets(lens), lse=lse)
+    quiet(L)
+    assert bool(torch.isfinite(out[:n]).all())
+    check_prefill(q[:n], k[:n], v[:n], [n], [n], out[:n], lse[:, :n], heads=[0, 15])
+
+
+@pytest.mark.parametrize("dtype,d,Hq", [(BF, 128, 2), (BF, 128, 12), (BF, 64, 2), (BF, 64, 12), (F32, 128, 2), (F32, 64, 5),
+                                        (F32, 64, 12)])
+def test_decode_large_values_under_a_rising_maximum(L, gen, dtype, d, Hq):
+    """300 sequences, so that a warp sees several tiles of each."""
+    n, B = 600, 300
+    q, k, v = _rising(n, 1, d, dtype)
+    c = Paged(gen, [n] * B, 1, d, 64, dtype)
+    for b in range(B):
+        c.k[b], c.v[b] = k, v
+        c.put(b, torch.arange(n, device="cuda"), k, v)
+    q = q[:1].expand(B, Hq, d).contiguous()
+    lse = torch.empty(B, Hq, device="cuda")
+    out = L.ExactAttention(Hq, 1, d, dtype, c.k_pool, c.v_pool).decode_step(q, c.kv_len, c.table, lse=lse)
+    quiet(L)
+    assert bool(torch.isfinite(out).all())
+    o, ls, to, tl = attend(q[0], k[:, 0], v[:, 0], torch.ones(Hq, n, dtype=torch.bool, device="cuda"))
+    for b in range(B):
+        check(out[b], o, to, f"sequence {b}")
+        check(lse[b], ls, tl, f"lse of sequence {b}")
+
+
+# ---------------------------------------------------------------------------------------
 # the paged cache: rotation and append
 # ---------------------------------------------------------------------------------------
 
