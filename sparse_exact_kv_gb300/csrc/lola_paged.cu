@@ -327,11 +327,20 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
     }
 }
 
+// Whether sequence b has a token that can be seen (on a page of the cache).
+__device__ __noinline__ bool sees_token(const PagedArgs& p, int b) {
+    const int64_t tokens = paged_tokens(p, p.kv_len[b]);
+    for (int64_t pos = 0; pos < tokens; pos += p.page)
+        if (paged_page(p, b, pos) >= 0) return true;
+    return false;
+}
+
 // One row's 4 columns c .. c + 3: o, when all of the item's tokens are in, or a record
 template <typename T, int D>
 __device__ __forceinline__ void write_out(const Args& a, const Seg& g, bool whole, float* rec, int r, int c, float (&y)[4], float M, float L) {
     if (whole) {
-        const float inv = L == 0.f ? 0.f : 1.f / L;            // (no token seen: o = 0)
+        // (no token seen: o = 0; scores that are all minus infinity: 0 / 0)
+        const float inv = L == 0.f ? (sees_token(a.p, g.b) ? NAN : 0.f) : 1.f / L;
 #pragma unroll
         for (int z = 0; z < 4; ++z) y[z] *= inv;
         store4(reinterpret_cast<T*>(a.O.data) + (int64_t)g.b * a.O.row + (int64_t)(g.h0 + r) * a.O.head + c, y);

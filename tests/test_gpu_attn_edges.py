@@ -170,6 +170,34 @@ def test_decode_large_values_under_a_rising_maximum(L, gen, dtype, d, Hq):
         check(lse[b], ls, tl, f"lse of sequence {b}")
 
 
+@pytest.mark.parametrize("dtype,d,Hq", [(BF, 128, 2), (BF, 64, 12), (F32, 64, 2), (F32, 128, 5)])
+@pytest.mark.parametrize("n", [1, 300, 5000])
+def test_decode_scores_of_minus_infinity(L, gen, dtype, d, Hq, n):
+    """Where all scores are minus infinity the softmax is 0 / 0, as in the prompt form; where some are,
+    those tokens have no weight; a sequence without tokens is zero."""
+    c = Paged(gen, [n, n, 0], 1, d, 16, dtype)
+    q = randn(gen, 3, Hq, d, dtype=dtype)
+    q[..., 0] = 1.0
+    c.k[0][:, 0, 0] = -math.inf
+    c.k[1][:, 0, 0] = -math.inf
+    c.k[1][n // 2] = 1.0
+    for b in (0, 1):
+        c.put(b, torch.arange(n, device="cuda"), c.k[b], c.v[b])
+    lse = torch.empty(3, Hq, device="cuda")
+    lay = L.ExactAttention(Hq, 1, d, dtype, c.k_pool, c.v_pool)
+    out = lay.decode_step(q, c.kv_len, c.table, lse=lse)
+    lse2 = torch.empty(Hq, 3, device="cuda")
+    same = lay.prefill_paged(q, offsets([1, 1, 1]), c.kv_len, c.table, lse=lse2)
+    quiet(L)
+    for o, l in ((out, lse), (same, lse2.t())):
+        assert bool(torch.isnan(o[0]).all()) and bool((l[0] == -math.inf).all())
+        assert bool((o[2] == 0).all()) and bool((l[2] == -math.inf).all())
+    o, ls, to, tl = attend(q[1], c.k[1][n // 2:n // 2 + 1, 0], c.v[1][n // 2:n // 2 + 1, 0],
+                           torch.ones(Hq, 1, dtype=torch.bool, device="cuda"))
+    check(out[1], o, to, "one key of any weight")
+    check(lse[1], ls, tl, "its lse")
+
+
 # ---------------------------------------------------------------------------------------
 # the paged cache: rotation and append
 # ---------------------------------------------------------------------------------------
