@@ -165,7 +165,8 @@ template <int NT> struct Span {
 
 // Query tiles of ROWS rows, found by one warp: the sequences' tiles are counted in order and taken
 // backwards (a sequence's longest tiles first, the first sequence's shortest ones at the very end), 32
-// sequences in the lanes at a time.
+// sequences in the lanes at a time.  A CTA that takes blocks over finds them in order as a rule, but nothing
+// promises it: the lanes go on to other sequences in either direction.
 template <int ROWS, bool PG> struct Finder {
     int q0, lq, k0, lk;      // this lane's sequence of the 32 from cb on
     int cb, own, inc;        // ... its tiles, and the tiles up to it in the lanes
@@ -197,13 +198,17 @@ template <int ROWS, bool PG> struct Finder {
         total = before + __shfl_sync(0xffffffffu, inc, 31);
         if (blockIdx.x == 0 && bits) atomicOr(&g_status, bits);
     }
-    // The number of tile `want` inside this lane's sequence, or -1 if another lane has it; no larger `want`
-    // than the last one.
+    // The number of tile `want` (0 <= want < total) inside this lane's sequence, or -1 if another lane has it.
     __device__ __forceinline__ int tile(const AttnArgs& a, int want, int lane) {
         while (want < before) {
             cb -= kWarp;
             chunk(a, lane);
             before -= __shfl_sync(0xffffffffu, inc, 31);
+        }
+        for (int here; want - before >= (here = __shfl_sync(0xffffffffu, inc, 31));) {
+            cb += kWarp;
+            chunk(a, lane);
+            before += here;
         }
         const int at = want - before - (inc - own);
         return at >= 0 && at < own ? at : -1;

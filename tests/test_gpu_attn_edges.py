@@ -117,6 +117,35 @@ def test_f32_prompt_sums_are_rounded(L, gen, d, paged):
 
 
 # ---------------------------------------------------------------------------------------
+# many sequences: several rounds of items, which cross the 32 sequences looked at together
+# ---------------------------------------------------------------------------------------
+
+MANY = [([(53 * i) % 400 for i in range(300)], None),                   # short ones, some empty: one tile a CTA
+        ([2300 + 31 * (i % 40) for i in range(80)], None),             # long ones: two tiles
+        ([1 + i % 3 for i in range(1100)], [1 + (7 * i) % 300 for i in range(1100)]),     # a few queries of many
+        ([(5000 if i % 50 == 7 else i % 5) for i in range(130)], None)]
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
+@pytest.mark.parametrize("lens,keys", MANY, ids=["300-short", "80-long", "1100-pieces", "130-mixed"])
+@pytest.mark.parametrize("paged", [False, True], ids=["packed", "paged"])
+def test_prefill_many_sequences(L, gen, dtype, d, lens, keys, paged):
+    Hq, Hkv, keys = 8, 2, keys or lens
+    q = randn(gen, sum(lens), Hq, d, dtype=dtype)
+    if paged:
+        c = Paged(gen, keys, Hkv, d, 64, dtype, junk=math.nan)
+        k, v = torch.cat(c.k), torch.cat(c.v)
+        out = L.ExactAttention(Hq, Hkv, d, dtype, c.k_pool, c.v_pool).prefill_paged(q, offsets(lens), c.kv_len, c.table,
+                                                                                    sum(keys))
+    else:
+        k, v = (randn(gen, sum(keys), Hkv, d, dtype=dtype) for _ in range(2))
+        out = L.ExactAttention(Hq, Hkv, d, dtype).prefill(q, k, v, offsets(lens), offsets(keys))
+    quiet(L)
+    assert bool(torch.isfinite(out).all())
+    check_prefill(q, k, v, lens, keys, out, heads=[0, 7], rows=[0, 1, 127, 128, 255, 300, 2299, 4999])
+
+
+# ---------------------------------------------------------------------------------------
 # large values under a rising maximum
 # ---------------------------------------------------------------------------------------
 
