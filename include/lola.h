@@ -399,7 +399,8 @@ typedef struct {
  *   cu_q, cu_k  device int32 [n_seq + 1], non-decreasing; cu_k may be NULL: the same as cu_q
  *   lse   nullable device float32 [Hq, total_q]
  * Rows of Q outside cu_q[0] .. cu_q[n_seq] are left as they were in O and lse.  Offsets that
- * decrease or pass total_q / total_k make their sequence empty and set LOLA_ATTN_BAD_OFFSETS.
+ * decrease or pass total_q / total_k make their sequence empty and set LOLA_ATTN_BAD_OFFSETS; rows that then
+ * belong to several sequences hold the result of one of them, or none.
  * O may be Q itself (the same rows) and otherwise overlaps no input.  total_q = 0 is a call that does
  * nothing.  Stream-ordered; no workspace. */
 int32_t lola_attn_prefill(const lola_attn_config* cfg, int32_t n_seq, int32_t total_q, int32_t total_k,

@@ -190,13 +190,19 @@ template <int ROWS, bool PG> struct Finder {
     }
     __device__ __forceinline__ void start(const AttnArgs& a, int lane) {
         bits = 0;
-        before = 0;
         cb = (a.n_seq - 1) / kWarp * kWarp;
-        for (int b = 0; b < cb; b += kWarp) before += look(a, b + lane);
-        before = __reduce_add_sync(0xffffffffu, before);
+        int64_t sum = 0;
+        for (int b = 0; b < cb; b += kWarp) sum += look(a, b + lane);
+        if (cb > 0) {
+#pragma unroll
+            for (int o = kWarp / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        }
         chunk(a, lane);
-        total = before + __shfl_sync(0xffffffffu, inc, 31);
-        if (blockIdx.x == 0 && bits) atomicOr(&g_status, bits);
+        before = (int)sum;
+        // (more than 2^31 tiles: offsets that go back and forth over the same rows, and are reported; nothing is taken)
+        sum += __shfl_sync(0xffffffffu, inc, 31);
+        total = sum > 0x7fffffff ? 0 : (int)sum;
+        if (bits) atomicOr(&g_status, bits);
     }
     // The number of tile `want` (0 <= want < total) inside this lane's sequence, or -1 if another lane has it.
     __device__ __forceinline__ int tile(const AttnArgs& a, int want, int lane) {

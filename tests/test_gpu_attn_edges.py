@@ -145,6 +145,25 @@ def test_prefill_many_sequences(L, gen, dtype, d, lens, keys, paged):
     check_prefill(q, k, v, lens, keys, out, heads=[0, 7], rows=[0, 1, 127, 128, 255, 300, 2299, 4999])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_prefill_bad_offsets_behind_many_sequences(L, gen, dtype):
+    """The sequence that is wrong is not among the first 32 nor the last; its neighbours are whole.  The
+    rows 3993 .. 3999 belong to two sequences (99 and 102) and hold either's result: they are not looked at."""
+    n, d = 200 * 40, 64
+    q, k, v = (randn(gen, n, 2, d, dtype=dtype) for _ in range(3))
+    cu = [40 * i for i in range(201)]
+    cu[101] = cu[102] = cu[100] - 7                            # 100 decreases, 101 is empty, 102 begins early
+    out = torch.full((n, 2, d), 3.0, dtype=dtype, device="cuda")
+    L.ExactAttention(2, 2, d, dtype).prefill(q, k, v, ints(cu), out=out)
+    assert L.lola_attn_status()[1] == L.LOLA_ATTN_BAD_OFFSETS
+    quiet(L)
+    check_prefill(q, k, v, [40] * 99, [40] * 99, out, rows=[0, 39])
+    check_prefill(q[3960:4000], k[3960:4000], v[3960:4000], [40], [40], out[3960:4000], rows=[0, 32])
+    first = cu[102]                                            # sequence 102 reaches from there to its end
+    lens = [cu[103] - first] + [40] * 97
+    check_prefill(q[first:], k[first:], v[first:], lens, lens, out[first:], rows=[10, 39, 60, 86])
+
+
 # ---------------------------------------------------------------------------------------
 # large values under a rising maximum
 # ---------------------------------------------------------------------------------------
