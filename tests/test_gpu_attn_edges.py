@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from attn_parity import Paged, attend, check, check_decode, check_prefill, ints, offsets, randn
+from attn_parity import Paged, attend, check, check_prefill, ints, offsets, randn, rotated
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -23,6 +23,10 @@ def L():
 @pytest.fixture
 def gen():
     return torch.Generator(device="cuda").manual_seed(23)
+
+
+def _freq(rot):
+    return (10000.0 ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)).float().cuda()
 
 
 def quiet(L):
@@ -276,3 +280,147 @@ def test_append_cosines(L, gen, n, pairs):
                       (y[:, 1, b], angle.cos()), (stored[:, a], angle.cos()), (stored[:, b], angle.sin())):
         worst = float((got.double() - want).abs().max())
         assert worst <= tol, worst
+
+
+def _append_case(gen, lens_new, before, Hq, Hkv, d, page, dtype, lead=0, tail=0):
+    """A cache with room for the new tokens, their rows, and for each row its sequence and position (-1: not
+    in a sequence)."""
+    total = [a + b for a, b in zip(lens_new, before)]
+    c = Paged(gen, [0] * len(total), Hkv, d, page, dtype, extra=sum(-(-t // page) for t in total) + 3,
+              width=max(1, max(-(-t // page) for t in total)))
+    order = torch.randperm(c.n_pages, generator=torch.Generator().manual_seed(7)).tolist()
+    c.table = ints([[order.pop() if i * page < t else -1 for i in range(c.table.shape[1])] for t in total])
+    c.kv_len = ints(total)
+    n = lead + sum(lens_new) + tail
+    rows = randn(gen, n, Hq + 2 * Hkv, d, dtype=dtype)
+    seq = torch.full((n,), -1, dtype=torch.long, device="cuda")
+    pos = torch.full((n,), -1, dtype=torch.long, device="cuda")
+    new, at = torch.tensor(lens_new, device="cuda"), lead + sum(lens_new)
+    seq[lead:at] = torch.arange(len(total), device="cuda").repeat_interleave(new)
+    first = new.cumsum(0) - new
+    pos[lead:at] = torch.arange(at - lead, device="cuda") - first[seq[lead:at]] + torch.tensor(before, device="cuda")[seq[lead:at]]
+    return c, rows, seq, pos
+
+
+def _check_append(c, k0, v0, q, k, v, qr, seq, pos, inv, pairs, slot):
+    """Rows with a slot are in their pages, those without one have only their query; the rest of the pools is as
+    it was."""
+    live = torch.nonzero(seq >= 0).flatten()
+    y, tol = rotated(q[live], pos[live], inv, pairs)
+    check(qr[live], y, tol + 1e-30, "q")
+    live = torch.nonzero(slot).flatten()
+    p = pos[live]
+    pages, at = c.table.long()[seq[live], p // c.page], p % c.page
+    y, tol = rotated(k[live], p, inv, pairs)
+    check(c.k_pool[pages, :, at], y, tol + 1e-30, "k")
+    k0[pages, :, at], v0[pages, :, at] = c.k_pool[pages, :, at], v[live]
+    assert torch.equal(c.k_pool, k0) and torch.equal(c.v_pool, v0)
+
+
+@pytest.mark.parametrize("dtype,d,rot", [(BF, 128, 128), (BF, 64, 48), (F32, 128, 32), (F32, 64, 64)])
+@pytest.mark.parametrize("pairs", ["halves", "neighbours"])
+@pytest.mark.parametrize("n", [760, 761, 762, 763, 764, 3001])
+def test_append_prompts(L, gen, dtype, d, rot, pairs, n):
+    """The form for many tokens (from 761 on four of them a CTA, the last CTA with one to four), one
+    prompt behind earlier tokens."""
+    Hq, Hkv = 6, 2
+    c, rows, seq, pos = _append_case(gen, [n], [37], Hq, Hkv, d, 16, dtype)
+    k0, v0 = c.k_pool.clone(), c.v_pool.clone()
+    q, k, v = rows[:, :Hq], rows[:, Hq:Hq + Hkv], rows[:, Hq + Hkv:]
+    inv = _freq(rot)
+    qr = L.ExactAttention(Hq, Hkv, d, dtype, c.k_pool, c.v_pool).append(k, v, c.kv_len, c.table, cu_new=offsets([n]), q=q,
+                                                                        inv_freq=inv, pairs=pairs)
+    quiet(L)
+    _check_append(c, k0, v0, q, k, v, qr, seq, pos, inv, pairs, seq >= 0)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+@pytest.mark.parametrize("B,most", [(33, 1), (33, 90), (100, 60), (1100, 1), (1100, 9), (2100, 3)])
+def test_append_many_sequences(L, gen, dtype, d, B, most):
+    """The search for a row's sequence in one to three rounds, empty sequences, rows before the first and behind the
+    last one, which stay as they were; in place."""
+    Hq, Hkv, page, lead, tail = 3, 1, 32, 5, 6
+    new = [(i * 7919) % (most + 1) for i in range(B)]
+    before = [(i * 31) % 50 for i in range(B)]
+    c, rows, seq, pos = _append_case(gen, new, before, Hq, Hkv, d, page, dtype, lead, tail)
+    k0, v0 = c.k_pool.clone(), c.v_pool.clone()
+    q, k, v = rows[:, :Hq].clone(), rows[:, Hq:Hq + Hkv], rows[:, Hq + Hkv:]
+    inv, q0 = _freq(d), q.clone()
+    lay = L.ExactAttention(Hq, Hkv, d, dtype, c.k_pool, c.v_pool)
+    got = lay.append(k, v, c.kv_len, c.table, cu_new=offsets(new, lead), q=q, inv_freq=inv, q_out=q)
+    quiet(L)
+    assert got is q and torch.equal(q[:lead], q0[:lead]) and torch.equal(q[lead + sum(new):], q0[lead + sum(new):])
+    _check_append(c, k0, v0, q0, k, v, q, seq, pos, inv, "halves", seq >= 0)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n", [500, 2000])
+def test_append_bad_slots_among_many(L, gen, dtype, n):
+    """Tokens without a slot in the middle of a call: reported, their queries written, their neighbours whole;
+    positions of the caller's; no rotation."""
+    Hq, Hkv, d, page = 2, 2, 64, 16
+    c, rows, seq, pos = _append_case(gen, [n, 9], [0, 0], Hq, Hkv, d, page, dtype)
+    q, k, v = rows[:, :Hq], rows[:, Hq:Hq + Hkv], rows[:, Hq + Hkv:]
+    lay = L.ExactAttention(Hq, Hkv, d, dtype, c.k_pool, c.v_pool)
+    slot = seq >= 0
+    for col, bad in ((3, -1), (11, c.n_pages), (20, 2 ** 31 - 1)):
+        c.table[0, col] = bad
+        slot &= ~((seq == 0) & (pos // page == col))
+    k0, v0 = c.k_pool.clone(), c.v_pool.clone()
+    inv, turns = _freq(d), torch.flip(pos, (0,)) * 3
+    qr = lay.append(k, v, c.kv_len, c.table, cu_new=offsets([n, 9]), q=q, inv_freq=inv, positions=turns.int())
+    assert L.lola_attn_status() == (L.LOLA_ERR_DEVICE, L.LOLA_ATTN_BAD_PAGE)
+    y, tol = rotated(q, turns, inv, "halves")
+    check(qr, y, tol + 1e-30, "q")
+    live = torch.nonzero(slot).flatten()
+    pages, at = c.table.long()[seq[live], pos[live] // page], pos[live] % page
+    y, tol = rotated(k[live], turns[live], inv, "halves")
+    check(c.k_pool[pages, :, at], y, tol + 1e-30, "k")
+    k0[pages, :, at], v0[pages, :, at] = c.k_pool[pages, :, at], v[live]
+    assert torch.equal(c.k_pool, k0) and torch.equal(c.v_pool, v0)
+    assert lay.append(k, v, c.kv_len, c.table, cu_new=offsets([n, 9])) is None
+    assert L.lola_attn_status()[1] == L.LOLA_ATTN_BAD_PAGE
+    k0[pages, :, at] = k[live]
+    assert torch.equal(c.k_pool, k0) and torch.equal(c.v_pool, v0)
+    quiet(L)
+
+
+def test_append_at_the_ends_of_one_form(L, gen):
+    """The two forms, one token a CTA and four, give the same bits."""
+    Hq, Hkv, d = 4, 2, 128
+    c, rows, _, _ = _append_case(gen, [761], [0], Hq, Hkv, d, 64, BF)
+    q, k, v = rows[:, :Hq], rows[:, Hq:Hq + Hkv], rows[:, Hq + Hkv:]
+    lay, inv = L.ExactAttention(Hq, Hkv, d, BF, c.k_pool, c.v_pool), _freq(d)
+    many = lay.append(k, v, c.kv_len, c.table, cu_new=offsets([761]), q=q, inv_freq=inv)
+    pool = c.k_pool.clone()
+    few = [lay.append(k[a:b], v[a:b], ints([b]), c.table, cu_new=offsets([b - a]), q=q[a:b], inv_freq=inv)
+           for a, b in ((0, 400), (400, 761))]
+    quiet(L)
+    assert torch.equal(torch.cat(few), many) and torch.equal(c.k_pool, pool)
+
+
+# ---------------------------------------------------------------------------------------
+# single tokens: every group size of every form
+# ---------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 128), (F32, 64)])
+@pytest.mark.parametrize("G", [1, 3, 4, 5, 7, 8, 9, 15, 16, 17, 24, 33])
+def test_decode_group_sizes(L, gen, dtype, d, G):
+    """Lengths around the tiles and the pieces, junk of NaN in the pools and behind the lengths; a batch small enough
+    to be cut into pieces, and one whose segments hold several tiles and sequences."""
+    Hkv = 2
+    for lens in ([700, 1, 64, 0, 129], [(67 * i) % 300 for i in range(150)]):
+        c = Paged(gen, lens, Hkv, d, 32, dtype, junk=math.nan)
+        q = randn(gen, len(lens), G * Hkv, d, dtype=dtype)
+        lse = torch.empty(len(lens), G * Hkv, device="cuda")
+        lay = L.ExactAttention(G * Hkv, Hkv, d, dtype, c.k_pool, c.v_pool)
+        out = lay.decode_step(q, c.kv_len, c.table, lse=lse)
+        quiet(L)
+        for b in range(len(lens)) if len(lens) < 9 else (0, 1, 9, 76, 148, 149):
+            seen = torch.ones(G, lens[b], dtype=torch.bool, device="cuda")
+            for g in range(Hkv):
+                hs = slice(g * G, (g + 1) * G)
+                o, ls, to, tl = attend(q[b, hs], c.k[b][:, g], c.v[b][:, g], seen)
+                check(out[b, hs], o, to, f"sequence {b} group {g}")
+                check(lse[b, hs], ls, tl, f"lse of sequence {b} group {g}")
+        assert torch.equal(out, lay.decode_step(q, c.kv_len, c.table))
