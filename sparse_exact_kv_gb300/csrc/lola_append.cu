@@ -224,6 +224,6 @@ cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t st) {
     return a.p.d == 128 ? launch<__nv_bfloat16, 128>(a, st) : launch<__nv_bfloat16, 64>(a, st);
 }
 
-cudaError_t append_status_take(int32_t* bits, cudaStream_t st) { return take_word(g_status, bits, st); }
+cudaError_t append_status_word(int32_t** word) { return cudaGetSymbolAddress((void**)word, g_status); }
 
 }  // namespace lola

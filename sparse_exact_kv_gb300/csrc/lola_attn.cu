@@ -350,6 +350,6 @@ cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t st) {
     return a.d == 128 ? launch<128, false>(a, st) : launch<64, false>(a, st);
 }
 
-cudaError_t attn_status_take(int32_t* bits, cudaStream_t st) { return take_word(g_status, bits, st); }
+cudaError_t attn_status_word(int32_t** word) { return cudaGetSymbolAddress((void**)word, g_status); }
 
 }  // namespace lola

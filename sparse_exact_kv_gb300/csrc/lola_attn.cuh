@@ -200,17 +200,6 @@ cudaError_t launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads,
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Reads a translation unit's anomaly word and clears it (after the stream's work).
-template <typename S>
-cudaError_t take_word(S& word, int32_t* bits, cudaStream_t st) {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(bits, word, sizeof(int32_t), 0, cudaMemcpyDeviceToHost, st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e != cudaSuccess || *bits == 0) return e;
-    const int32_t zero = 0;
-    e = cudaMemcpyToSymbolAsync(word, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st);
-    return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
-}
-
 // ---- launchers ----
 cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t st);
 cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t st);       // bf16 (lola_attn_tc.cu)
@@ -233,10 +222,10 @@ struct DecodeArgs {
     float scale_log2;
 };
 cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t st);
-// reads and clears the anomaly words of a translation unit (after the stream's work)
-cudaError_t attn_status_take(int32_t* bits, cudaStream_t st);
-cudaError_t attn_tc_status_take(int32_t* bits, cudaStream_t st);
-cudaError_t append_status_take(int32_t* bits, cudaStream_t st);
-cudaError_t paged_status_take(int32_t* bits, cudaStream_t st);
+// the address of a translation unit's anomaly word on the current device
+cudaError_t attn_status_word(int32_t** word);
+cudaError_t attn_tc_status_word(int32_t** word);
+cudaError_t append_status_word(int32_t** word);
+cudaError_t paged_status_word(int32_t** word);
 
 }  // namespace lola

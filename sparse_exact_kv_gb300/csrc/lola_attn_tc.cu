@@ -825,6 +825,6 @@ cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t st) {
     return a.p.table ? launch_form<true>(a, st) : launch_form<false>(a, st);
 }
 
-cudaError_t attn_tc_status_take(int32_t* bits, cudaStream_t st) { return take_word(g_status, bits, st); }
+cudaError_t attn_tc_status_word(int32_t** word) { return cudaGetSymbolAddress((void**)word, g_status); }
 
 }  // namespace lola

@@ -301,6 +301,32 @@ bool rows_ok(const lola_attn_config* c, const lola_rows* r, int64_t rows, int64_
 }
 Rows to_rows(const lola_rows* r) { return r ? Rows{static_cast<char*>(r->data), r->row, r->head} : Rows{nullptr, 0, 0}; }
 
+// The anomaly words of the exact-attention kernels are read and cleared in one step, so that a bit that another
+// stream's kernel sets meanwhile is in this reading or left for the next one.
+struct StatusWords {
+    int32_t* word[4];
+};
+__device__ int32_t g_taken;
+__global__ void take_status_kernel(StatusWords w) {
+    int32_t bits = 0;
+    for (int i = 0; i < 4; ++i) bits |= atomicExch(w.word[i], 0);
+    g_taken = bits;
+}
+cudaError_t take_status(int32_t* bits, cudaStream_t st) {
+    static std::mutex m;                       // (one reading's bits are copied before the next one)
+    std::lock_guard<std::mutex> lock(m);
+    StatusWords w;
+    cudaError_t (*const find[])(int32_t**) = {attn_status_word, attn_tc_status_word, append_status_word, paged_status_word};
+    for (int i = 0; i < 4; ++i) {
+        const cudaError_t e = find[i](&w.word[i]);
+        if (e != cudaSuccess) return e;
+    }
+    take_status_kernel<<<1, 1, 0, st>>>(w);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(bits, g_taken, sizeof(*bits), 0, cudaMemcpyDeviceToHost, st);
+    return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
+}
+
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
 // A number of 56 bits that no other call of this process has, and that memory hardly holds by
@@ -813,13 +839,7 @@ int32_t lola_attn_status(int32_t* host_bits, void* stream) {
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e = cudaStreamSynchronize(st);
     int32_t bits = 0;
-    cudaError_t (*const take[])(int32_t*, cudaStream_t) = {attn_status_take, attn_tc_status_take, append_status_take,
-                                                        paged_status_take};
-    for (auto f : take) {
-        int32_t x = 0;
-        if (e == cudaSuccess) e = f(&x, st);
-        bits |= x;
-    }
+    if (e == cudaSuccess) e = take_status(&bits, st);
     if (e != cudaSuccess) return cuda_fail(e, "lola_attn_status");
     if (host_bits) *host_bits = bits;
     return bits ? LOLA_ERR_DEVICE : LOLA_OK;

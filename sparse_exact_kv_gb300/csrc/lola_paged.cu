@@ -960,6 +960,6 @@ cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t st) {
     return a.p.d == 128 ? launch_bf16<128>(a, st) : launch_bf16<64>(a, st);
 }
 
-cudaError_t paged_status_take(int32_t* bits, cudaStream_t st) { return take_word(g_status, bits, st); }
+cudaError_t paged_status_word(int32_t** word) { return cudaGetSymbolAddress((void**)word, g_status); }
 
 }  // namespace lola

@@ -424,3 +424,33 @@ def test_decode_group_sizes(L, gen, dtype, d, G):
                 check(out[b, hs], o, to, f"sequence {b} group {g}")
                 check(lse[b, hs], ls, tl, f"lse of sequence {b} group {g}")
         assert torch.equal(out, lay.decode_step(q, c.kv_len, c.table))
+
+
+# ---------------------------------------------------------------------------------------
+# anomalies
+# ---------------------------------------------------------------------------------------
+
+def test_status_bits_of_another_stream_are_not_lost(L, gen):
+    """One stream's calls set one bit and then another while the status is read all the time: every bit shows
+    in one of the readings."""
+    d = 64
+    c = Paged(gen, [100], 1, d, 16, BF)
+    lay = L.ExactAttention(1, 1, d, BF, c.k_pool, c.v_pool)
+    q = randn(gen, 100, 1, d, dtype=BF)
+    bad_cu, cu, bad_table = ints([5, 3]), offsets([100]), torch.full_like(c.table, -1)
+    out, side, here = torch.empty_like(q), torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    quiet(L)
+    both = L.LOLA_ATTN_BAD_OFFSETS | L.LOLA_ATTN_BAD_PAGE
+    for i in range(1500):
+        lay.prefill_paged(q, bad_cu, c.kv_len, c.table, out=out, stream=side)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(2000 + 977 * (i % 61))           # (a moment of GPU time between the two)
+        lay.prefill_paged(q, cu, c.kv_len, bad_table, out=out, stream=side)
+        done, bits = torch.cuda.Event(), 0
+        done.record(side)
+        while not done.query():
+            bits |= L.lola_attn_status(stream=here)[1]
+        bits |= L.lola_attn_status(stream=side)[1]
+        assert bits == both, i
+    quiet(L)
