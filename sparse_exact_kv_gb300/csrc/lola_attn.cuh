@@ -218,7 +218,7 @@ struct DecodeArgs {
     Rows Q, O;
     float* lse;
     float* part;             // workspace
-    uint64_t tag;            // a number no other call has
+    uint64_t tag;            // 56 bits that no other call has
     float scale_log2;
 };
 cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t st);
@@ -227,5 +227,6 @@ cudaError_t attn_status_word(int32_t** word);
 cudaError_t attn_tc_status_word(int32_t** word);
 cudaError_t append_status_word(int32_t** word);
 cudaError_t paged_status_word(int32_t** word);
+cudaError_t paged_give_up(int tile, cudaStream_t st);   // (lola_selftest_paged_wait)
 
 }  // namespace lola

@@ -37,6 +37,7 @@ constexpr int kRows = 16;                 // query rows of a row group (at most)
 constexpr int kJoin = 16;                 // pieces joined at a time
 constexpr float kRaise = 8.0f;            // bf16: m is set this far above a maximum (log2), and raised when one passes it
 constexpr uint64_t kWaitNs = 1000000000ull;
+__constant__ int c_give_up = -1;          // lola_selftest_paged_wait: a tile at which every third CTA gives up
 
 struct Maps {
     CUtensorMap k, v;   // [n_pages * Hkv][page][d] as 128-byte columns, boxes of min(page, 64) rows
@@ -161,6 +162,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 template <int S> struct Bars {
     uint64_t full[S], empty[S], seg_full[2], seg_empty[2];
     int issued;      // tiles whose stage is armed
+    int given;       // segment slots given to the consumers, when the producer is done
+    int arrived[2];  // this piece's record of that slot has been counted
 };
 
 // Which piece this CTA is and where it begins (all threads): false if there is none.
@@ -214,6 +217,14 @@ __device__ __forceinline__ bool find_start(const PagedArgs& p, int I, Start* st)
     return true;
 }
 
+// The segment [t0, t1) of an item of `tiles` tiles as one piece of it: the item's first unit is xs.
+__device__ __forceinline__ void place_piece(const Start& st, int64_t xs, int tiles, Seg* g) {
+    g->c0 = split_of(st.total, st.N, xs);
+    g->np = split_of(st.total, st.N, xs + tiles - 1) - g->c0 + 1;
+    g->k = (int)blockIdx.x - g->c0;
+    g->s0 = xs != split_at(st.total, st.N, g->c0);
+}
+
 // The producer warp: segments and their tiles, in order.  A tile's pages outside the cache are not
 // loaded; bit x of bad_sm marks the tile's x-th token box.  Segment i goes to slot i % NS.
 template <typename T, int D, int NS, typename B>
@@ -248,13 +259,7 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
             g.len = (int)max((int64_t)0, tokens - (int64_t)t0 * kTile);
             g.whole = t0 == 0 && t1 == tiles;
             g.k = g.np = g.c0 = g.s0 = 0;
-            if (!g.whole) {
-                const int64_t xs = u - t0;                        // the item's first unit
-                g.c0 = split_of(st.total, st.N, xs);
-                g.np = split_of(st.total, st.N, xs + tiles - 1) - g.c0 + 1;
-                g.k = (int)blockIdx.x - g.c0;
-                g.s0 = xs != split_at(st.total, st.N, g.c0);
-            }
+            if (!g.whole) place_piece(st, u - t0, tiles, &g);
             segs[slot] = g;
             if (p.kv_len[b] > tokens && tokens > 0) atomicOr(&g_status, (int)LOLA_ATTN_BAD_PAGE);
             mbar_expect(smem_u32(&bars.seg_full[slot]), (uint32_t)(R * C::kRowBytes));
@@ -269,6 +274,10 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
         for (int t = t0; t < t1; ++t, ++n) {
             const int s = n % C::kStages;
             if (n >= C::kStages) ok = __all_sync(0xffffffffu, ring_wait(smem_u32(&bars.empty[s]), (uint32_t)(n / C::kStages - 1) & 1, abort_sm));
+            if (n == c_give_up && blockIdx.x % 3 == (unsigned)n % 3) {
+                if (lane == 0) *reinterpret_cast<volatile int*>(abort_sm) = 1;
+                ok = false;
+            }
             if (!ok) break;
             // (positions fit 31 bits, but for the boxes behind the last token's)
             const uint32_t pos = (uint32_t)t * kTile, have = (uint32_t)tokens;
@@ -319,11 +328,9 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
             mbar_arrive1(smem_u32(&bars.seg_full[slot]));
         }
     }
-    // leave no copy in flight
-    if (!ok && lane == 0) {
-        atomicOr(&g_status, (int)LOLA_ATTN_TIMEOUT);
-        for (int x = max(0, n - C::kStages); x < n; ++x) mbar_wait(smem_u32(&bars.full[x % C::kStages]), (uint32_t)(x / C::kStages) & 1, kWaitNs);
-        for (int x = max(0, i - NS); x < i; ++x) mbar_wait(smem_u32(&bars.seg_full[x % NS]), (uint32_t)(x / NS) & 1, kWaitNs);
+    if (lane == 0) {
+        if (!ok) atomicOr(&g_status, (int)LOLA_ATTN_TIMEOUT);
+        bars.given = i;
     }
 }
 
@@ -359,7 +366,8 @@ __device__ __forceinline__ void write_out(const Args& a, const Seg& g, bool whol
 // second round over those joins.  A join counts its arrivals in a cell that holds the call's tag (56
 // bits) and the count (8): whoever takes part first swaps whatever the workspace held for the tag and a
 // count of 0 -- long before its own arrival, off the critical path -- and the last one leaves 0.  So a
-// workspace needs no clearing, and a replayed graph, whose tag stays the same, finds no old count.
+// workspace needs no clearing, and a replayed graph, whose tag stays the same, finds no old count: every
+// piece is counted, those of a CTA whose waits gave up too (settle).
 template <int D>
 __device__ __forceinline__ void open_cell(const Args& a, int piece, int slot) {
     unsigned long long* c = cell<D>(a, piece, slot);
@@ -373,24 +381,45 @@ __device__ __forceinline__ void open_cells(const Args& a, const Seg& g) {
     if (g.np > kJoin) open_cell<D>(a, g.c0, 2 + g.s0);
 }
 
+// A join that piece k of an item takes part in: pieces c0 + step (first + x), x < cnt, the very first one's record
+// in slot0.
+struct Join {
+    int k, np, step, slot0, slot;
+    __device__ __forceinline__ explicit Join(const Seg& g) : k(g.k), np(g.np), step(1), slot0(g.s0), slot(0) {}
+    __device__ __forceinline__ int first() const { return k / kJoin * kJoin; }
+    __device__ __forceinline__ int cnt() const { return min(kJoin, np - first()); }
+    __device__ __forceinline__ int head(const Seg& g) const { return g.c0 + step * first(); }
+    __device__ __forceinline__ int hslot() const { return first() == 0 ? slot0 : slot; }
+    // the second round: the joins, each in a record of its first piece
+    __device__ __forceinline__ void next() {
+        k /= kJoin;
+        np = (np + kJoin - 1) / kJoin;
+        step = kJoin;
+        slot0 = 2 + slot0;
+        slot = 2;
+    }
+};
+// One more arrival; whether it is the last one of `cnt`.
+template <int D>
+__device__ __forceinline__ bool arrive(const Args& a, int head, int hslot, int cnt) {
+    unsigned long long* c = cell<D>(a, head, hslot);
+    unsigned long long old;
+    asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], 1;" : "=l"(old) : "l"(reinterpret_cast<uint64_t>(c)) : "memory");
+    const bool last = (int)(old & 255) == cnt - 1;
+    if (last) *reinterpret_cast<volatile unsigned long long*>(c) = 0ull;
+    return last;
+}
+
 // Segment g's record is written by this group's NT threads (numbered t).  `bar` is their barrier.
 template <typename T, int D, int NT, typename F>
-__device__ void join_pieces(const Args& a, const Seg& g, int t, int* go, F&& bar) {
-    int k = g.k, np = g.np, step = 1, slot0 = g.s0, slot = 0;
-    for (;;) {
-        // members of this join: pieces c0 + step (first + x), x < cnt, the very first one's record in slot0
-        const int first = k / kJoin * kJoin, cnt = min(kJoin, np - first);
-        const int head = g.c0 + step * first, hslot = first == 0 ? slot0 : slot;
+__device__ void join_pieces(const Args& a, const Seg& g, int t, int* go, int* arrived, F&& bar) {
+    for (Join join(g);; join.next()) {
+        const int first = join.first(), cnt = join.cnt(), head = join.head(g), hslot = join.hslot(), slot = join.slot;
+        const int np = join.np, step = join.step;
         bar();
         if (t == 0) {
-            unsigned long long old;
-            asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], 1;"
-                         : "=l"(old)
-                         : "l"(reinterpret_cast<uint64_t>(cell<D>(a, head, hslot)))
-                         : "memory");
-            const bool last = (int)(old & 255) == cnt - 1;
-            if (last) *reinterpret_cast<volatile unsigned long long*>(cell<D>(a, head, hslot)) = 0ull;
-            *go = last;
+            *go = arrive<D>(a, head, hslot, cnt);
+            if (step == 1) arrived[g.k == 0 ? g.s0 : 0] = 1;
         }
         bar();
         if (!*go) return;
@@ -424,12 +453,39 @@ __device__ void join_pieces(const Args& a, const Seg& g, int t, int* go, F&& bar
             write_out<T, D>(a, g, cnt == np, record<D>(a, head, 2 + hslot), r, c, y, M, L);
         }
         if (cnt == np) return;
-        // the second round: the joins, each in a record of its first piece
-        k /= kJoin;
-        np = (np + kJoin - 1) / kJoin;
-        step = kJoin;
-        slot0 = 2 + slot0;
-        slot = 2;
+    }
+}
+
+// The end of a CTA whose waits gave up (all threads, after all roles): no copy is left in flight, and its pieces
+// that were not counted are, so that every cell of the call ends at 0 (what the joins then make of their records
+// is as invalid as the call).
+template <int D, int S, int NS, typename B>
+__device__ __noinline__ void settle(const Args& a, B& bars) {
+    if (threadIdx.x == 0) {
+        const int n = bars.issued, i = bars.given;
+        for (int x = max(0, n - S); x < n; ++x) mbar_wait(smem_u32(&bars.full[x % S]), (uint32_t)(x / S) & 1, kWaitNs);
+        for (int x = max(0, i - NS); x < i; ++x) mbar_wait(smem_u32(&bars.seg_full[x % NS]), (uint32_t)(x / NS) & 1, kWaitNs);
+    }
+    Start st;
+    if (!find_start(a.p, a.I, &st) || threadIdx.x != 0) return;
+    int b = st.b, tiles = tiles_of(paged_tokens(a.p, a.p.kv_len[b]));
+    int item = (int)(st.rem / tiles), t0 = (int)(st.rem % tiles);
+    for (int64_t u = st.u0; u < st.u1;) {
+        const int t1 = (int)min((int64_t)tiles, t0 + (st.u1 - u));
+        if (t0 > 0 || t1 < tiles) {
+            Seg g;
+            place_piece(st, u - t0, tiles, &g);
+            if (!bars.arrived[g.k == 0 ? g.s0 : 0]) {
+                open_cells<D>(a, g);
+                for (Join join(g); arrive<D>(a, join.head(g), join.hslot(), join.cnt()) && join.cnt() < join.np;) join.next();
+            }
+        }
+        u += t1 - t0;
+        t0 = 0;
+        if (++item == a.I && u < st.u1) {
+            item = 0;
+            tiles = tiles_of(paged_tokens(a.p, a.p.kv_len[++b]));
+        }
     }
 }
 
@@ -467,22 +523,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_f32_kernel(const __g
         mbar_init(smem_u32(&bars.seg_full[0]), 1);
         mbar_init(smem_u32(&bars.seg_empty[0]), NW);
         abort_sm = 0;
-        bars.issued = 0;
+        bars.issued = bars.given = bars.arrived[0] = bars.arrived[1] = 0;
     }
     wait_for_last_kernel();
     Start st;
     if (!find_start(p, a.I, &st)) return;
-    if (warp == NW) {
-        produce<float, D, 1>(maps, a, st, smem_u32(sm), smem_u32(Qs), D * 4, bars, segs, bad_sm, &abort_sm, lane);
-        return;
-    }
+    if (warp == NW) produce<float, D, 1>(maps, a, st, smem_u32(sm), smem_u32(Qs), D * 4, bars, segs, bad_sm, &abort_sm, lane);
     auto bar = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
     const int grp = warp >> 2, rc = (warp & 3) / NP, tp = (warp & 3) % NP, tg = lane >> 3, j = lane & 7;
     const bool b2 = j & 4, b1 = j & 2, b0 = j & 1;
     const int box = min(p.page, kTile), lb = 31 - __clz(box);
     // byte offset of 16-byte chunk 0 of a token's row; column x (128 bytes) is x * box * 128 further
     auto row_at = [&](int k) { return (k >> lb) * box * C::kRowBytes + (k & (box - 1)) * 128; };
-    for (int i = 0;; ++i) {
+    for (int i = 0; warp < NW; ++i) {
         if (group_or<kCons>(1, !ring_wait(smem_u32(&bars.seg_full[0]), (uint32_t)i & 1, &abort_sm))) {
             if (tid == 0) atomicOr(&g_status, (int)LOLA_ATTN_TIMEOUT);
             break;
@@ -662,9 +715,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_f32_kernel(const __g
             }
             write_out<float, D>(a, g, g.whole, rec, r, c, y, M, ll);
         }
-        if (!g.whole) join_pieces<float, D, kCons>(a, g, tid, &go, bar);
+        if (!g.whole) join_pieces<float, D, kCons>(a, g, tid, &go, bars.arrived, bar);
         bar();                                                  // red, ms, ls are read
     }
+    __syncthreads();
+    if (abort_sm) settle<D, C::kStages, 1>(a, bars);
 }
 
 // ---- bf16: the tile products on the warps' matrix instructions ----
@@ -733,15 +788,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_mma_kernel(const __g
             mbar_init(smem_u32(&bars.seg_empty[s]), NW);
         }
         abort_sm = 0;
-        bars.issued = 0;
+        bars.issued = bars.given = bars.arrived[0] = bars.arrived[1] = 0;
     }
     wait_for_last_kernel();
     Start st;
     if (!find_start(p, a.I, &st)) return;
-    if (warp == kCons / kWarp) {
-        produce<T, D, 2>(maps, a, st, sb, smem_u32(x.q[0]), M::kPitch, bars, segs, bad_sm, &abort_sm, lane);
-        return;
-    }
+    if (warp == kCons / kWarp) produce<T, D, 2>(maps, a, st, sb, smem_u32(x.q[0]), M::kPitch, bars, segs, bad_sm, &abort_sm, lane);
     const int grp = warp >> 2, wg = warp & 3, g8 = lane >> 2, q2 = (lane & 3) * 2;
     const int own = kBoth ? 0 : grp, me = kBoth ? warp : wg, gt = kBoth ? tid : tid & 127;   // the segment's group, its warps and threads
     auto bar = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + own), "n"(NT) : "memory"); };
@@ -753,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_mma_kernel(const __g
     const int vkey = k0 + (((lane >> 3) & 1) << 3) + (lane & 7), vch = lane >> 4;        // ... of V
     const uint32_t krow = row_at(kkey), vrow = C::kHalf + row_at(vkey);
     const uint32_t qrow = smem_u32(x.q[0]) + ((lane & 7) + ((lane >> 3) & 1) * 8) * M::kPitch + (lane >> 4) * 16;
-    for (int i = 0;; ++i) {
+    for (int i = 0; warp < kCons / kWarp; ++i) {
         const int slot = kBoth ? i & 1 : grp;
         if (group_or<NT>(1 + own, !ring_wait(smem_u32(&bars.seg_full[slot]), (uint32_t)(kBoth ? i >> 1 : i) & 1, &abort_sm))) {
             if (gt == 0) atomicOr(&g_status, (int)LOLA_ATTN_TIMEOUT);
@@ -904,8 +956,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_mma_kernel(const __g
                 if (er < g.R) write_out<T, D>(a, g, g.whole, rec, er, c + ec, y, mm, ll);
             }
         }
-        if (!g.whole) join_pieces<T, D, NT>(a, g, gt, &go[own], bar);
+        if (!g.whole) join_pieces<T, D, NT>(a, g, gt, &go[own], bars.arrived, bar);
     }
+    __syncthreads();
+    if (abort_sm) settle<D, C::kStages, 2>(a, bars);
 }
 
 Args make_args(const DecodeArgs& d) {
@@ -958,6 +1012,11 @@ int64_t paged_decode_workspace(int d) { return (int64_t)kPieces * kSlots * (reco
 cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t st) {
     if (a.p.dtype == LOLA_F32) return a.p.d == 128 ? launch_f32<128>(a, st) : launch_f32<64>(a, st);
     return a.p.d == 128 ? launch_bf16<128>(a, st) : launch_bf16<64>(a, st);
+}
+
+cudaError_t paged_give_up(int tile, cudaStream_t st) {
+    const cudaError_t e = cudaMemcpyToSymbolAsync(c_give_up, &tile, sizeof(tile), 0, cudaMemcpyHostToDevice, st);
+    return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
 }
 
 cudaError_t paged_status_word(int32_t** word) { return cudaGetSymbolAddress((void**)word, g_status); }
