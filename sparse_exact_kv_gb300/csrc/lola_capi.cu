@@ -329,16 +329,16 @@ cudaError_t take_status(int32_t* bits, cudaStream_t st) {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
-// A number of 56 bits that no other call of this process has, and that memory hardly holds by
-// chance (a mix of a counter and the process's start).
+// A number of 56 bits that none of the next 2^56 calls of this process has, and that memory hardly holds by
+// chance: a count from the process's start, mixed by steps that are one to one on 56 bits.
 uint64_t call_tag() {
+    constexpr uint64_t kBits = ((uint64_t)1 << 56) - 1;
     static const uint64_t seed = (uint64_t)std::chrono::steady_clock::now().time_since_epoch().count();
     static std::atomic<uint64_t> count{0};
-    uint64_t z = seed + (count.fetch_add(1, std::memory_order_relaxed) + 1) * 0x9e3779b97f4a7c15ull;   // SplitMix64
-    z = (z ^ (z >> 30)) * 0xbf58476d1ce4e5b9ull;
-    z = (z ^ (z >> 27)) * 0x94d049bb133111ebull;
-    z = (z ^ (z >> 31)) >> 8;
-    return z ? z : 1;
+    uint64_t z = (seed + (count.fetch_add(1, std::memory_order_relaxed) + 1) * 0x9e3779b97f4a7c15ull) & kBits;
+    z = ((z ^ (z >> 30)) * 0xbf58476d1ce4e5b9ull) & kBits;
+    z = ((z ^ (z >> 27)) * 0x94d049bb133111ebull) & kBits;
+    return z ^ (z >> 31);
 }
 
 int32_t paged_check(const lola_attn_config* c, const lola_paged_kv* kv, PagedArgs* p) {
