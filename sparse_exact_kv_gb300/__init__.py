@@ -51,7 +51,7 @@ EXPORTS = ("lola_version", "lola_status_string", "lola_last_cuda_error", "lola_c
            "lola_sre_map_relative", "lola_hola_workspace_bytes", "lola_hola_prefill", "lola_hola_status",
            "lola_attn_prefill", "lola_paged_slot", "lola_paged_append", "lola_paged_prefill",
            "lola_paged_decode_workspace_bytes",
-           "lola_paged_decode", "lola_attn_status", "lola_selftest_paged_wait")
+           "lola_paged_decode", "lola_attn_status", "lola_selftest_attn_wait")
 # size of the fixed scratch array behind lola_prefill_noalloc (include/lola.h)
 LOLA_NOALLOC_SCRATCH_BYTES = 32 << 20
 KERNELS = ("state_init", "phi", "select", "output", "decode", "phi_q", "hola_prep", "hola_state", "hola_cache",
@@ -142,7 +142,7 @@ def _load():
                               ctypes.c_int32),
         "lola_paged_decode_workspace_bytes": ([AC], ctypes.c_int64),
         "lola_paged_decode": ([AC, PK, R, R, P, P, ctypes.c_size_t, P], ctypes.c_int32),
-        "lola_selftest_paged_wait": ([ctypes.c_int32, P], ctypes.c_int32),
+        "lola_selftest_attn_wait": ([ctypes.c_int32, P], ctypes.c_int32),
         "lola_attn_status": ([ctypes.POINTER(ctypes.c_int32), P], ctypes.c_int32),
     }
     for name, (args, res) in sig.items():
@@ -426,9 +426,10 @@ def lola_paged_decode(cfg: lola_attn_config, kv: lola_paged_kv, Q, O, workspace,
         raise LolaError(st, "lola_paged_decode")
 
 
-def lola_selftest_paged_wait(tile: int, stream=None) -> None:
-    """The tile at which every third CTA of lola_paged_decode gives up on the current device; -1: none."""
-    _check(_lib.lola_selftest_paged_wait(int(tile), _stream(stream)), "lola_selftest_paged_wait")
+def lola_selftest_attn_wait(block: int, stream=None) -> None:
+    """The block of keys at which every third CTA of the exact-attention kernels gives up on the current
+    device; -1: none."""
+    _check(_lib.lola_selftest_attn_wait(int(block), _stream(stream)), "lola_selftest_attn_wait")
 
 
 def lola_attn_status(stream=None):

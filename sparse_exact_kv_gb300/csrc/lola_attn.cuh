@@ -227,6 +227,8 @@ cudaError_t attn_status_word(int32_t** word);
 cudaError_t attn_tc_status_word(int32_t** word);
 cudaError_t append_status_word(int32_t** word);
 cudaError_t paged_status_word(int32_t** word);
-cudaError_t paged_give_up(int tile, cudaStream_t st);   // (lola_selftest_paged_wait)
+// lola_selftest_attn_wait
+cudaError_t attn_tc_give_up(int pair, cudaStream_t st);
+cudaError_t paged_give_up(int tile, cudaStream_t st);
 
 }  // namespace lola

@@ -62,6 +62,7 @@ constexpr int kClean = 4;                // barriers of the blocks to be cleaned
 constexpr float kRaise = 8.0f;           // m is set this far above a block's maximum (log2), and raised when one passes it
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint64_t kItemNs = 10000000000ull;   // ... of the waits that may last a whole item
+__device__ int g_give_up = -1;           // lola_selftest_attn_wait: a pair of blocks at which every third CTA gives up
 
 // NT: query tiles of a CTA.  Two: one CTA per SM, K and V blocks shared by 256 queries.  One: two CTAs
 // per SM, each with its own ring (half the shared memory, half of TMEM).
@@ -290,6 +291,8 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
         }
         abort_sm = 0;
     }
+    int give_up = -1;
+    if (warp == C::kLoadWarp) give_up = *reinterpret_cast<const volatile int*>(&g_give_up);   // (long before it is looked at)
     if (warp == kMmaWarp) tmem_alloc<C::kTmem>(smem_u32(&tmem_base));
     wait_for_last_kernel();
     Finder<C::kQ, PG> find;
@@ -383,6 +386,7 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
                 }
                 __syncwarp();
                 ok = __all_sync(0xffffffffu, wait(B_STEAL, (uint32_t)steals & 1u));
+                if (!ok) mbar_wait(bar(B_STEAL), (uint32_t)steals & 1u, kWaitNs);   // (given up elsewhere: the answer is still to come)
                 ++steals;
                 if (ok) more = stolen_block(smem_u32(&stolen), &block);
                 fence_async_smem();                                    // (read before the next answer lands there)
@@ -437,6 +441,11 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
                                 entry = (page < 0 ? a.p.n_pages : page) * a.p.Hkv + (page < 0 ? 0 : hk);
                             }
                             if (P >= kCap && !(ok = agree(wait(empty_of(P), phase(P - kCap))))) break;
+                            if (P == give_up && blockIdx.x % 3 == (unsigned)P % 3) {
+                                abort_sm = 1;
+                                ok = false;
+                                break;
+                            }
                             const int full = full_of(P);
                             if (!PG || lane == 0) mbar_expect(bar(full), (uint32_t)((p > 0) + (p < sp.nmax)) * C::kTileBytes);
                             if constexpr (PG) {
@@ -823,6 +832,10 @@ template <bool PG> static cudaError_t launch_form(const AttnArgs& a, cudaStream_
 
 cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t st) {
     return a.p.table ? launch_form<true>(a, st) : launch_form<false>(a, st);
+}
+
+cudaError_t attn_tc_give_up(int pair, cudaStream_t st) {
+    return cudaMemcpyToSymbolAsync(g_give_up, &pair, sizeof(pair), 0, cudaMemcpyHostToDevice, st);
 }
 
 cudaError_t attn_tc_status_word(int32_t** word) { return cudaGetSymbolAddress((void**)word, g_status); }

@@ -810,10 +810,13 @@ int32_t lola_paged_append(const lola_attn_config* cfg, const lola_paged_kv* kv, 
     return e == cudaSuccess ? LOLA_OK : cuda_fail(e, "paged append");
 }
 
-int32_t lola_selftest_paged_wait(int32_t tile, void* stream) {
-    if (tile < -1) return LOLA_ERR_INVALID_ARG;
-    const cudaError_t e = paged_give_up(tile, (cudaStream_t)stream);
-    return e == cudaSuccess ? LOLA_OK : cuda_fail(e, "lola_selftest_paged_wait");
+int32_t lola_selftest_attn_wait(int32_t block, void* stream) {
+    if (block < -1) return LOLA_ERR_INVALID_ARG;
+    cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e = paged_give_up(block, st);
+    if (e == cudaSuccess) e = attn_tc_give_up(block, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    return e == cudaSuccess ? LOLA_OK : cuda_fail(e, "lola_selftest_attn_wait");
 }
 
 int64_t lola_paged_decode_workspace_bytes(const lola_attn_config* cfg) {

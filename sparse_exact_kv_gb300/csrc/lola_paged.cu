@@ -37,7 +37,7 @@ constexpr int kRows = 16;                 // query rows of a row group (at most)
 constexpr int kJoin = 16;                 // pieces joined at a time
 constexpr float kRaise = 8.0f;            // bf16: m is set this far above a maximum (log2), and raised when one passes it
 constexpr uint64_t kWaitNs = 1000000000ull;
-__constant__ int c_give_up = -1;          // lola_selftest_paged_wait: a tile at which every third CTA gives up
+__device__ int g_give_up = -1;            // lola_selftest_attn_wait: a tile at which every third CTA gives up
 
 struct Maps {
     CUtensorMap k, v;   // [n_pages * Hkv][page][d] as 128-byte columns, boxes of min(page, 64) rows
@@ -233,6 +233,7 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
     using C = Cfg<T, D>;
     const PagedArgs& p = a.p;
     const int box = min(p.page, kTile), lb = 31 - __clz(box), nbox = kTile >> lb;   // tokens of a box, boxes of a tile
+    const int give_up = *reinterpret_cast<const volatile int*>(&g_give_up);    // (beside the lengths)
     int b = st.b;
     int lens_b = b;                                               // the lanes hold 32 sequences' lengths
     int lens = b + lane < p.n_seq ? p.kv_len[b + lane] : 0;
@@ -274,7 +275,7 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
         for (int t = t0; t < t1; ++t, ++n) {
             const int s = n % C::kStages;
             if (n >= C::kStages) ok = __all_sync(0xffffffffu, ring_wait(smem_u32(&bars.empty[s]), (uint32_t)(n / C::kStages - 1) & 1, abort_sm));
-            if (n == c_give_up && blockIdx.x % 3 == (unsigned)n % 3) {
+            if (n == give_up && blockIdx.x % 3 == (unsigned)n % 3) {
                 if (lane == 0) *reinterpret_cast<volatile int*>(abort_sm) = 1;
                 ok = false;
             }
@@ -335,7 +336,7 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
 }
 
 // Whether sequence b has a token that can be seen (on a page of the cache).
-__device__ __noinline__ bool sees_token(const PagedArgs& p, int b) {
+__device__ __forceinline__ bool sees_token(const PagedArgs& p, int b) {
     const int64_t tokens = paged_tokens(p, p.kv_len[b]);
     for (int64_t pos = 0; pos < tokens; pos += p.page)
         if (paged_page(p, b, pos) >= 0) return true;
@@ -1015,8 +1016,7 @@ cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t st) {
 }
 
 cudaError_t paged_give_up(int tile, cudaStream_t st) {
-    const cudaError_t e = cudaMemcpyToSymbolAsync(c_give_up, &tile, sizeof(tile), 0, cudaMemcpyHostToDevice, st);
-    return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
+    return cudaMemcpyToSymbolAsync(g_give_up, &tile, sizeof(tile), 0, cudaMemcpyHostToDevice, st);
 }
 
 cudaError_t paged_status_word(int32_t** word) { return cudaGetSymbolAddress((void**)word, g_status); }

@@ -10,7 +10,7 @@ def L():
     return lib
 
 
-def test_selftest_tiles_outside_the_range_are_refused(L):
-    assert L._lib.lola_selftest_paged_wait(-2, None) == L.LOLA_ERR_INVALID_ARG
+def test_selftest_blocks_outside_the_range_are_refused(L):
+    assert L._lib.lola_selftest_attn_wait(-2, None) == L.LOLA_ERR_INVALID_ARG
     with pytest.raises(L.LolaError):
-        L.lola_selftest_paged_wait(-2, stream=0)
+        L.lola_selftest_attn_wait(-2, stream=0)

@@ -479,7 +479,7 @@ def test_decode_after_waits_that_gave_up(L, gen, dtype, d, lens):
     gave_up = 0
     try:
         for tile in [0, 1, 2, 3, 4, 5, 6, 8, 11, 15, 23, 1000]:
-            L.lola_selftest_paged_wait(tile)
+            L.lola_selftest_attn_wait(tile)
             for _ in range(3):
                 out.fill_(7.0)
                 g.replay()
@@ -488,11 +488,46 @@ def test_decode_after_waits_that_gave_up(L, gen, dtype, d, lens):
                 gave_up += bits != 0
                 assert bits or torch.equal(out, want), tile
                 assert not bool(cells.any()), tile
-            L.lola_selftest_paged_wait(-1)
+            L.lola_selftest_attn_wait(-1)
             out.fill_(7.0)
             g.replay()
             quiet(L)
             assert torch.equal(out, want), tile
     finally:
-        L.lola_selftest_paged_wait(-1)
+        L.lola_selftest_attn_wait(-1)
+    assert gave_up > 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens", [[4000, 100, 1, 2500], [200] * 400, [5000] * 16], ids=["few", "one-tile", "two-tiles"])
+@pytest.mark.parametrize("paged", [False, True], ids=["packed", "paged"])
+def test_prefill_after_waits_that_gave_up(L, gen, d, lens, paged):
+    """A prompt call whose waits gave up says so, ends, and leaves nothing behind for the next one."""
+    H, n = 4, sum(lens)
+    q = randn(gen, n, H, d, dtype=BF)
+    c = Paged(gen, lens, H, d, 64, BF)
+    k, v = torch.cat(c.k), torch.cat(c.v)
+    lay = L.ExactAttention(H, H, d, BF, c.k_pool, c.v_pool)
+    out, cu = torch.empty_like(q), offsets(lens)
+    call = (lambda: lay.prefill_paged(q, cu, c.kv_len, c.table, n, out=out)) if paged else (
+        lambda: lay.prefill(q, k, v, cu, out=out))
+    want, gave_up = call().clone(), 0
+    quiet(L)
+    try:
+        for block in (0, 1, 2, 3, 4, 7, 12, 25, 1000):
+            L.lola_selftest_attn_wait(block)
+            for _ in range(3):
+                out.fill_(7.0)
+                call()
+                st, bits = L.lola_attn_status()
+                assert bits in (0, L.LOLA_ATTN_TIMEOUT)
+                gave_up += bits != 0
+                assert bits or torch.equal(out, want), block
+            L.lola_selftest_attn_wait(-1)
+            out.fill_(7.0)
+            call()
+            quiet(L)
+            assert torch.equal(out, want), block
+    finally:
+        L.lola_selftest_attn_wait(-1)
     assert gave_up > 0
