@@ -480,6 +480,10 @@ class ExactAttention:
                   and v_pool.device == k_pool.device, "k_pool and v_pool differ in shape, type or device")
         self.k_pool, self.v_pool = k_pool, v_pool
 
+    def __reduce__(self):
+        # (``_plan`` is the address of this object's ``cfg``: a copy, or another process' object, is made anew)
+        return type(self), (self.Hq, self.Hkv, self.d, self.dtype, self.k_pool, self.v_pool, self.cfg.scale or None)
+
     @classmethod
     def allocate(cls, Hq, Hkv, d, n_pages, page=64, dtype=torch.bfloat16, device="cuda", scale=None):
         pool = lambda: torch.zeros(n_pages, Hkv, page, d, dtype=dtype, device=device)  # noqa: E731
