@@ -323,6 +323,8 @@ def lola_hola_status(cfg: lola_hola_config, n: int, workspace, stream=None):
 
 def make_attn_config(Hq, Hkv, d, dtype, scale=None) -> lola_attn_config:
     """``scale``: the logit scale, None for 1 / sqrt(d)."""
+    if scale is not None and ctypes.c_float(scale).value == 0:
+        raise ValueError("scale: want a positive number, or None for 1 / sqrt(d)")      # (0 is None's form in C)
     dt = dtype if isinstance(dtype, int) else {"f32": LOLA_F32, "bf16": LOLA_BF16,
                                                torch.float32: LOLA_F32, torch.bfloat16: LOLA_BF16}[dtype]
     return lola_attn_config(Hq, Hkv, d, dt, 0.0 if scale is None else scale)

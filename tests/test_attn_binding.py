@@ -31,3 +31,15 @@ def test_copies_of_a_layer_hold_their_own_description(L):
             if lay.k_pool is not None:
                 assert torch.equal(other.k_pool, lay.k_pool) and other.v_pool.shape == lay.v_pool.shape
         assert copy.copy(lay).k_pool is lay.k_pool             # a shallow copy shares the cache
+
+
+def test_a_scale_of_zero_is_refused(L):
+    """It stands for 1 / sqrt(d) in the C structure; from Python that is None, and 0 would be taken for it."""
+    import torch
+    for make in (lambda s: L.make_attn_config(4, 2, 64, "bf16", s), lambda s: L.ExactAttention(4, 2, 64, scale=s),
+                 lambda s: L.ExactAttention.allocate(4, 2, 64, 3, device="cpu", scale=s)):
+        for zero in (0.0, 0, -0.0, 1e-50):
+            with pytest.raises(ValueError):
+                make(zero)
+        make(None), make(0.25)
+    assert L.make_attn_config(4, 2, 64, torch.bfloat16).scale == 0.0
