@@ -473,14 +473,18 @@ class ExactAttention:
     def __init__(self, Hq, Hkv, d, dtype=torch.bfloat16, k_pool=None, v_pool=None, scale=None):
         self.cfg, self._ws, self._plan = _attn_plan(Hq, Hkv, d, dtype, scale)
         self.Hq, self.Hkv, self.d, self.dtype = Hq, Hkv, d, dtype
-        _need((k_pool is None) == (v_pool is None), "k_pool and v_pool come together")
-        if k_pool is not None:
-            shape = k_pool.shape
-            _need(len(shape) == 4 and shape[1] == Hkv and shape[3] == d and k_pool.dtype == dtype and k_pool.is_contiguous(),
-                  "pools are contiguous [n_pages, Hkv, page, d] of the layer's dtype")
-            _need(v_pool.shape == shape and v_pool.dtype == dtype and v_pool.is_contiguous()
-                  and v_pool.device == k_pool.device, "k_pool and v_pool differ in shape, type or device")
         self.k_pool, self.v_pool = k_pool, v_pool
+        if k_pool is not None or v_pool is not None:
+            self._check_pools()
+
+    def _check_pools(self):
+        k, v = self.k_pool, self.v_pool
+        _need(k is not None and v is not None, "k_pool and v_pool come together")
+        shape = k.shape
+        _need(len(shape) == 4 and shape[1] == self.Hkv and shape[3] == self.d and k.dtype == self.dtype and k.is_contiguous(),
+              "pools are contiguous [n_pages, Hkv, page, d] of the layer's dtype")
+        _need(v.shape == shape and v.dtype == self.dtype and v.is_contiguous() and v.device == k.device,
+              "k_pool and v_pool differ in shape, type or device")
 
     def __reduce__(self):
         # (``_plan`` is the address of this object's ``cfg``: a copy, or another process' object, is made anew)
@@ -560,6 +564,7 @@ class ExactAttention:
         pool = self.k_pool
         if pool is None:
             raise ValueError("this layer has no key-value pools")
+        self._check_pools()                        # (they may be others than the constructor saw)
         dev, (n, width), one = pool.device, table.shape, table.stride(1)
         self._vector(kv_len, n, dev, "kv_len")
         if table.dtype != torch.int32 or table.device != dev or (one != 1 and width != 1):

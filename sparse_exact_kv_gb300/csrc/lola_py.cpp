@@ -68,9 +68,11 @@ const Tensor* rows(PyObject* o, lola_rows* r, const Call& c, int64_t n, int64_t 
     return t && fill(*t, r, n, heads, c.cfg->d) ? t : nullptr;
 }
 
+// contiguous pools [n_pages, Hkv, page, d] of one shape, and what a call has for them
 bool cache(PyObject* k_pool, PyObject* v_pool, PyObject* kv_len, PyObject* table, const Call& c, lola_paged_kv* kv) {
     const Tensor *k = get(k_pool, c.dtype, c.device), *v = get(v_pool, c.dtype, c.device), *t = get(table, at::kInt, c.device);
-    if (!k || !v || !t || k->dim() != 4 || t->dim() != 2 || (t->stride(1) != 1 && t->size(1) != 1) ||
+    if (!k || !v || !t || k->dim() != 4 || k->size(1) != c.cfg->Hkv || k->size(3) != c.cfg->d || k->sizes() != v->sizes() ||
+        !k->is_contiguous() || !v->is_contiguous() || t->dim() != 2 || (t->stride(1) != 1 && t->size(1) != 1) ||
         k->size(0) > INT32_MAX || t->size(0) > INT32_MAX || t->size(1) > INT32_MAX)
         return false;
     const Tensor* n = vec(kv_len, at::kInt, c.device, t->size(0));

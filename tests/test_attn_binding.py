@@ -43,3 +43,27 @@ def test_a_scale_of_zero_is_refused(L):
                 make(zero)
         make(None), make(0.25)
     assert L.make_attn_config(4, 2, 64, torch.bfloat16).scale == 0.0
+
+
+def test_pools_that_do_not_fit_the_layer_are_refused(L, monkeypatch):
+    """Pools put in place of a layer's own are looked at in every call."""
+    import torch
+    bf = torch.bfloat16
+    monkeypatch.setattr(L, "_index_of", lambda dev: 0)
+    lay = L.ExactAttention(4, 2, 64, bf, torch.zeros(4, 2, 16, 64, dtype=bf), torch.zeros(4, 2, 16, 64, dtype=bf))
+    lens, table = torch.ones(1, dtype=torch.int32), torch.zeros(1, 1, dtype=torch.int32)
+    pool = torch.zeros(6, 2, 16, 64, dtype=bf)
+    lay.k_pool, lay.v_pool = pool, pool.clone()               # another cache of the same layer: taken
+    assert lay._cache(lens, table)[0].n_pages == 6
+    bad = [torch.zeros(4, 2, 16, 64, dtype=bf), torch.zeros(6, 1, 16, 64, dtype=bf), torch.zeros(6, 2, 16, 128, dtype=bf),
+           torch.zeros(6, 2, 32, 64, dtype=bf), torch.zeros(6, 2, 16, 64), torch.zeros(6, 16, 2, 64, dtype=bf).transpose(1, 2),
+           torch.zeros(12, 16, 64, dtype=bf), None]
+    for other in bad:
+        for k, v in ((pool, other), (other, pool)):
+            lay.k_pool, lay.v_pool = k, v
+            with pytest.raises(ValueError):
+                lay._cache(lens, table)
+    for other in bad[1:3] + bad[4:7]:
+        lay.k_pool = lay.v_pool = other
+        with pytest.raises(ValueError):
+            lay._cache(lens, table)

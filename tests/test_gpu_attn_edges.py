@@ -531,3 +531,42 @@ def test_prefill_after_waits_that_gave_up(L, gen, d, lens, paged):
     finally:
         L.lola_selftest_attn_wait(-1)
     assert gave_up > 0
+
+
+# ---------------------------------------------------------------------------------------
+# the binding
+# ---------------------------------------------------------------------------------------
+
+def test_pools_in_place_of_a_layers_own(L, gen):
+    """A layer's pools may be replaced by others that fit it; others are refused by every call."""
+    c, c2 = (Paged(gen, [70, 40], 2, 64, page, BF) for page in (16, 32))
+    lay = L.ExactAttention(4, 2, 64, BF, c.k_pool, c.v_pool)
+    q, k = randn(gen, 2, 4, 64, dtype=BF), randn(gen, 2, 2, 64, dtype=BF)
+    cu, inv = offsets([1, 1]), _freq(64)
+    lay.k_pool, lay.v_pool = c2.k_pool, c2.v_pool
+    out = lay.decode_step(q, c2.kv_len, c2.table)
+    quiet(L)
+    for b in range(2):
+        for h in range(4):
+            o, _, to, _ = attend(q[b, h][None], c2.k[b][:, h // 2], c2.v[b][:, h // 2],
+                                 torch.ones(1, c2.lens[b], dtype=torch.bool, device="cuda"))
+            check(out[b, h][None], o, to, f"sequence {b} head {h}")
+    for kp, vp in ((c.k_pool, c2.v_pool), (c2.k_pool, c.v_pool), (c.k_pool, None), (None, c.v_pool), (c.k_pool[:, :1], c.v_pool[:, :1]),
+                   (c.k_pool.float(), c.v_pool.float()), (c.k_pool.transpose(1, 2), c.v_pool.transpose(1, 2))):
+        lay.k_pool, lay.v_pool = kp, vp
+        for call in (lambda: lay.decode_step(q, c.kv_len, c.table), lambda: lay.append(k, k, c.kv_len, c.table, q=q, inv_freq=inv),
+                     lambda: lay.prefill_paged(q, cu, c.kv_len, c.table)):
+            with pytest.raises(ValueError):
+                call()
+    quiet(L)
+
+
+def test_copies_of_a_layer_serve(L, gen):
+    import copy
+    c = Paged(gen, [70, 40], 2, 64, 16, BF)
+    lay = L.ExactAttention(4, 2, 64, BF, c.k_pool, c.v_pool, scale=0.2)
+    q = randn(gen, 2, 4, 64, dtype=BF)
+    want = lay.decode_step(q, c.kv_len, c.table)
+    for other in (copy.copy(lay), copy.deepcopy(lay)):
+        assert torch.equal(other.decode_step(q, c.kv_len, c.table), want)
+    quiet(L)
