@@ -11,7 +11,10 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import os
+import warnings
 
 import torch
 
@@ -153,7 +156,25 @@ def _load():
 
 
 _lib = _load()
-from . import _lola_py as _fast  # noqa: E402  (links liblola.so: after it is loaded)
+
+
+class _Declines:
+    """In the marshalling module's place: every call takes its Python form."""
+    prefill = prefill_paged = decode = append = staticmethod(lambda *args: NotImplemented)
+
+
+def _marshalling(path):
+    """The marshalling module of that file, which links liblola.so and torch; _Declines if it is not there or does
+    not load (another torch than the one it was compiled against: nothing but speed depends on it)."""
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("_lola_py", path)
+        return importlib.util.module_from_spec(importlib.util.spec_from_file_location("_lola_py", path, loader=loader))
+    except (ImportError, OSError):
+        return _Declines
+
+
+_PYMOD = os.path.join(os.path.dirname(os.path.abspath(__file__)), f"_lola_py-{torch.__version__}.so")
+_fast = _marshalling(_PYMOD)
 
 
 def make_config(B, Hh, d_k, d_v, D, eta, lam, chunk, dtype, read_mask=0, alloc=LOLA_ALLOC_TOKEN,
@@ -471,6 +492,9 @@ class ExactAttention:
     __slots__ = ("cfg", "Hq", "Hkv", "d", "dtype", "k_pool", "v_pool", "_ws", "_plan")
 
     def __init__(self, Hq, Hkv, d, dtype=torch.bfloat16, k_pool=None, v_pool=None, scale=None):
+        if _fast is _Declines:
+            warnings.warn(f"{os.path.basename(_PYMOD)}, the marshalling module of ExactAttention for this torch, is missing or does "
+                          "not load: calls take their slower Python form (rebuild the package)", RuntimeWarning, stacklevel=2)
         self.cfg, self._ws, self._plan = _attn_plan(Hq, Hkv, d, dtype, scale)
         self.Hq, self.Hkv, self.d, self.dtype = Hq, Hkv, d, dtype
         self.k_pool, self.v_pool = k_pool, v_pool

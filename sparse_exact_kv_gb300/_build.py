@@ -19,7 +19,6 @@ SOURCES = ["lola_capi.cu", "lola_phi.cu", "lola_select.cu", "lola_chunk.cu", "lo
            "lola_decode.cu", "lola_noalloc.cu", "lola_relsre.cu",
            "lola_fixed.cu", "lola_hola.cu", "lola_hola_tc.cu", "lola_attn.cu",
            "lola_attn_tc.cu", "lola_append.cu", "lola_paged.cu"]
-PYMOD = os.path.join(PKG, "_lola_py.so")      # the binding's marshalling (csrc/lola_py.cpp)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -37,10 +36,21 @@ def _flags(verbose_ptxas: bool) -> list[str]:
     return f
 
 
+def pymod() -> str | None:
+    """The binding's marshalling module (csrc/lola_py.cpp) for this torch, whose C++ interface it is compiled
+    against; None without torch."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    return os.path.join(PKG, f"_lola_py-{torch.__version__}.so")
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(PYMOD):
+    built = [p for p in (LIB, pymod()) if p]
+    if not all(os.path.exists(p) for p in built):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(PYMOD))
+    t = min(os.path.getmtime(p) for p in built)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "lola.h"), __file__]
     return any(os.path.getmtime(p) > t for p in deps)
 
@@ -61,7 +71,9 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    def binding() -> list[str]:
+    def binding() -> list[str] | None:
+        if pymod() is None:
+            return None
         import torch
         lib = os.path.join(os.path.dirname(torch.__file__), "lib")
         inc = os.path.join(os.path.dirname(torch.__file__), "include")
@@ -86,12 +98,14 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    tmp = PYMOD + f".{os.getpid()}.tmp"
+    if py_link is None:
+        return LIB
+    tmp = pymod() + f".{os.getpid()}.tmp"
     r = subprocess.run([cc, "-shared", "-o", tmp, *py_link, "-cudart", "none", "-L", PKG, "-l:liblola.so",
                         "-Xlinker", "-rpath,$ORIGIN"], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"building the binding's module failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, PYMOD)
+    os.replace(tmp, pymod())
     return LIB
 
 

@@ -67,3 +67,47 @@ def test_pools_that_do_not_fit_the_layer_are_refused(L, monkeypatch):
         lay.k_pool = lay.v_pool = other
         with pytest.raises(ValueError):
             lay._cache(lens, table)
+
+
+def test_calls_decline_without_the_marshalling_module(L, tmp_path):
+    """A module that is not there, or does not load, leaves the Python form of every call."""
+    broken = tmp_path / "_lola_py-broken.so"
+    broken.write_bytes(b"no module")
+    for path in (str(tmp_path / "none.so"), str(broken)):
+        fast = L._marshalling(path)
+        for call in (fast.prefill, fast.prefill_paged, fast.decode, fast.append):
+            assert call(1, None, "anything") is NotImplemented
+    assert L._marshalling(L._PYMOD).decode() is NotImplemented         # the real one: wrong arguments, declined
+    assert type(L._fast).__name__ == "module"
+
+
+def test_the_package_does_not_need_the_marshalling_module(L):
+    """Under another torch than the module was compiled against the package loads, and says so where it matters."""
+    import subprocess
+    import sys
+    code = """
+import warnings, torch
+torch.__version__ = "0.0.0+other"
+import sparse_exact_kv_gb300 as L
+assert L.lola_check_config(L.make_config(1, 1, 64, 64, 64, 16, 16, 64, "bf16")) == 0
+with warnings.catch_warnings(record=True) as w:
+    warnings.simplefilter("always")
+    L.ExactAttention(4, 2, 64)
+assert any("marshalling" in str(x.message) for x in w), w
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=_root())
+    assert r.returncode == 0, r.stderr
+
+
+def test_another_torch_makes_the_build_stale(L, monkeypatch):
+    import __graft_entry__
+    import torch
+    build = __graft_entry__._build_module()
+    assert not build._stale()
+    monkeypatch.setattr(torch, "__version__", "0.0.0+other")
+    assert build._stale()
+
+
+def _root():
+    import os
+    return os.path.dirname(os.path.dirname(os.path.abspath(__file__)))

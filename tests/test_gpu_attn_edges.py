@@ -570,3 +570,29 @@ def test_copies_of_a_layer_serve(L, gen):
     for other in (copy.copy(lay), copy.deepcopy(lay)):
         assert torch.equal(other.decode_step(q, c.kv_len, c.table), want)
     quiet(L)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+def test_both_forms_of_the_binding_give_the_same_bits(L, gen, dtype, d, monkeypatch):
+    """The calls through the marshalling module, and their Python form, which serves without it."""
+    lens = [70, 300, 1]
+    n = sum(lens)
+
+    def run():
+        g = torch.Generator(device="cuda").manual_seed(3)
+        c = Paged(g, lens, 2, d, 16, dtype)
+        lay = L.ExactAttention(4, 2, d, dtype, c.k_pool, c.v_pool)
+        rows, cu = randn(g, n, 8, d, dtype=dtype), offsets(lens)
+        q, k, v = rows[:, :4], rows[:, 4:6], rows[:, 6:]
+        qr = lay.append(k, v, c.kv_len, c.table, cu_new=cu, q=q, inv_freq=_freq(d), pairs="neighbours")
+        assert lay.append(k[:3], v[:3], c.kv_len, c.table) is None
+        return [qr, lay.prefill(q, k, v, cu), lay.prefill_paged(qr, cu, c.kv_len, c.table),
+                lay.decode_step(q[:3], c.kv_len, c.table), c.k_pool, c.v_pool]
+
+    fast = run()
+    assert L._fast is not L._Declines
+    monkeypatch.setattr(L, "_fast", L._Declines)
+    with pytest.warns(RuntimeWarning):
+        slow = run()
+    quiet(L)
+    assert all(torch.equal(a, b) for a, b in zip(fast, slow))
