@@ -629,47 +629,51 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     });
     return fn;
 }
+// The driver's call with these arguments.  It wants a current context, which a host thread that has not used the
+// GPU yet does not have: the runtime then makes the device's own the thread's, and the call is made again.
+template <typename... A>
+bool encode(const A&... args) {
+    auto enc = encoder();
+    if (!enc) return false;
+    if (enc(args...) == CUDA_SUCCESS) return true;
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && enc(args...) == CUDA_SUCCESS;
+}
 }  // namespace
 
 bool make_tmap3(CUtensorMap* m, CUtensorMapDataType type, int elem_bytes, const void* base, int64_t inner,
                 int64_t rows, int64_t depth, int box_inner, int box_rows) {
-    auto enc = encoder();
-    if (!enc) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)depth};
     const cuuint64_t strides[2] = {(cuuint64_t)(inner * elem_bytes), (cuuint64_t)(inner * elem_bytes * rows)};
     const cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows, 1u};
     const cuuint32_t estr[3] = {1u, 1u, 1u};
-    return enc(m, type, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(m, type, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 bool make_tmap_pages(CUtensorMap* m, CUtensorMapDataType type, int elem_bytes, const void* base, int d, int page,
                      int64_t depth, int box_rows, int box_cols) {
-    auto enc = encoder();
-    if (!enc) return false;
     const cuuint32_t inner = 128u / (cuuint32_t)elem_bytes, cols = (cuuint32_t)d / inner;
     const cuuint64_t row = (cuuint64_t)d * elem_bytes;
     const cuuint64_t dims[4] = {inner, (cuuint64_t)page, cols, (cuuint64_t)depth};
     const cuuint64_t strides[3] = {row, 128u, row * page};
     const cuuint32_t box[4] = {inner, (cuuint32_t)box_rows, (cuuint32_t)box_cols, 1u};
     const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-    return enc(m, type, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(m, type, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 bool make_tmap_rows(CUtensorMap* m, const void* base, int64_t rows, int heads, int d, int64_t row, int64_t head,
                     int box_rows) {
-    auto enc = encoder();
-    if (!enc) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
     const cuuint64_t strides[2] = {(cuuint64_t)(head * 2), (cuuint64_t)(row * 2)};
     const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)box_rows};
     const cuuint32_t estr[3] = {1u, 1u, 1u};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 }  // namespace tc
 

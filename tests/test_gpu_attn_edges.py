@@ -596,3 +596,68 @@ def test_both_forms_of_the_binding_give_the_same_bits(L, gen, dtype, d, monkeypa
         slow = run()
     quiet(L)
     assert all(torch.equal(a, b) for a, b in zip(fast, slow))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("what", ["prefill", "prefill_paged", "decode_step", "append", "status"])
+def test_first_call_of_a_new_thread(L, gen, dtype, what):
+    """A host thread whose first use of the GPU is the call (a server's worker): nothing has made the device's
+    context the thread's own before."""
+    import threading
+    c = Paged(gen, [300, 40], 2, 64, 16, dtype)
+    lay = L.ExactAttention(4, 2, 64, dtype, c.k_pool, c.v_pool)
+    q, cu, inv = randn(gen, 340, 4, 64, dtype=dtype), offsets([300, 40]), _freq(64)
+    k, v = torch.cat(c.k), torch.cat(c.v)
+    out = [torch.empty_like(q), torch.empty_like(q)]
+    call = {"prefill": lambda i: lay.prefill(q, k, v, cu, out=out[i]),
+            "prefill_paged": lambda i: lay.prefill_paged(q, cu, c.kv_len, c.table, out=out[i]),
+            "decode_step": lambda i: lay.decode_step(q[:2], c.kv_len, c.table, out=out[i][:2]),
+            "append": lambda i: lay.append(k, v, c.kv_len, c.table, cu_new=cu, q=q, inv_freq=inv, q_out=out[i]),
+            "status": lambda i: L.lola_attn_status()}[what]
+    fast = {"prefill": lambda: lay.prefill(q, k, v, cu), "prefill_paged": lambda: lay.prefill_paged(q, cu, c.kv_len, c.table),
+            "decode_step": lambda: lay.decode_step(q[:2], c.kv_len, c.table),
+            "append": lambda: lay.append(k, v, c.kv_len, c.table, cu_new=cu, q=q, inv_freq=inv),
+            "status": lambda: L.lola_attn_status()}[what]
+    want = call(0)
+    torch.cuda.synchronize()
+    for f in (lambda: call(1), fast):
+        got = []
+
+        def run():
+            try:
+                got.append(f())
+            except Exception as e:
+                got.append(e)
+
+        t = threading.Thread(target=run)
+        t.start()
+        t.join()
+        assert not isinstance(got[0], Exception), got
+        torch.cuda.synchronize()
+        assert got[0] == (0, 0) if what == "status" else torch.equal(got[0], want)
+    quiet(L)
+
+
+def test_first_call_of_a_new_thread_lola(L, gen):
+    """... and the same for a LoLA layer's prefill on the tensor cores."""
+    import threading
+    lay = L.Lola(1, 2, 128, 128, 64, 64)
+    q, k, v = (randn(gen, 1, 2, 200, 128, dtype=BF) for _ in range(3))
+    W = torch.randn(64, 128, generator=gen, device="cuda") / 8
+    want = lay.prefill(q, k, v, W).clone()
+    L.lola_state_init(lay.cfg, lay.state)
+    Y, got = torch.empty_like(v), []
+    torch.cuda.synchronize()
+
+    def run():
+        try:
+            got.append(lay.prefill(q, k, v, W, Y=Y))
+        except Exception as e:
+            got.append(e)
+
+    t = threading.Thread(target=run)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not isinstance(got[0], Exception), got
+    assert torch.equal(Y, want)
