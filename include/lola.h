@@ -373,7 +373,8 @@ int32_t lola_hola_status(const lola_hola_config* cfg, int32_t n, const void* wor
  * from two tf32 parts of each operand (good to 2^-21 of |a b| each); with bfloat16 io the weights p are
  * rounded to bfloat16 for the product with V (at most 2^-8 relative each, as the output's
  * own rounding, and averaged over the keys), the sum is taken over the unrounded weights,
- * and o is rounded once.  Device-side anomalies go to a word per device read with lola_attn_status(). */
+ * and o is rounded once; the tensor cores cut those sums off, which leaves o low by up to 6e-4 of its size
+ * at 131072 keys (1e-5 at 4096).  Device-side anomalies go to a word per device read with lola_attn_status(). */
 typedef struct {
     int32_t Hq;      /* query heads */
     int32_t Hkv;     /* key/value heads; Hq is a multiple of Hkv */
@@ -414,7 +415,7 @@ typedef struct {
     void* V;
     int32_t n_pages;
     int32_t page;          /* tokens per page: 16, 32, 64, 128 or 256 */
-    int32_t n_seq;
+    int32_t n_seq;         /* at least 1: a call for no sequence is refused */
     int32_t width;         /* page-table columns */
     int64_t table_stride;  /* elements from one sequence's table row to the next, >= width */
     const int32_t* table;  /* device int32; entries behind a sequence's pages are not read */
@@ -438,7 +439,7 @@ typedef enum { LOLA_PAIRS_HALVES = 0, LOLA_PAIRS_NEIGHBOURS = 1 } lola_pairs;
  *           last tokens: row cu_new[b] + j is token kv_len[b] - (cu_new[b+1] - cu_new[b]) + j.
  *           NULL: one new token per sequence, row b for sequence b (n_tokens = n_seq)
  *   K, V    n_tokens rows of Hkv heads;  Q  nullable: n_tokens rows of Hq heads
- *   QO      the rotated queries (NULL with Q); may be Q itself
+ *   QO      the rotated queries (NULL with Q); may be Q itself (the same rows) and otherwise overlaps no input
  *   inv_freq  device float32 [rot / 2]; NULL: no rotation (Q must be NULL too)
  *   rot     rotated channels: a multiple of 16, at most d (not read without inv_freq)
  *   positions  nullable device int32 [n_tokens] >= 0: p of each row; NULL: the token's index in

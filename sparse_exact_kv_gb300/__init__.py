@@ -487,7 +487,8 @@ class ExactAttention:
     runs ``prefill`` needs none.  Outputs and the decode step's workspace are allocated through
     torch on the call's stream, so calls on several streams do not share any.  Shapes, types and
     devices are checked here, strides and alignment by the library; all tensors are on the current
-    CUDA device.  For serving: outputs carry no gradient."""
+    CUDA device.  A batch of no sequences is refused.  For serving: outputs carry no gradient, also
+    of inputs that require one."""
 
     __slots__ = ("cfg", "Hq", "Hkv", "d", "dtype", "k_pool", "v_pool", "_ws", "_plan")
 
@@ -605,7 +606,8 @@ class ExactAttention:
         int32 [n_seq + 1] the rows of each sequence's new tokens (None: one each); ``inv_freq``
         float32 [rot / 2] radians per position (None: no rotation); ``pairs`` the channel pairs of
         the rotation, "halves" or "neighbours"; ``positions`` int32 [n] in place of the tokens'
-        indexes.  ``q_out`` may be q itself."""
+        indexes.  ``q_out`` may be q itself; rows outside the sequences, and of sequences without
+        tokens, are left as they were in it (a fresh one is not initialised there)."""
         if q_out is None and positions is None and stream is None:
             r = _fast.append(self._plan, self.k_pool, self.v_pool, k, v, kv_len, table, cu_new, q, inv_freq, PAIRS[pairs])
             if r is not NotImplemented:

@@ -10,7 +10,7 @@
 //
 // Bound by HBM bytes for prompts (every element read once and written once, 16-byte accesses,
 // a pair's two halves in one thread, three such units in flight a thread; 18 k tokens of 32/8 heads:
-// 74 us, 6.0 TB/s, 88 % of the measured copy rate) and by latency for one token per sequence (3.4 us
+// 74.5 us, 5.9 TB/s, 88 % of the measured copy rate) and by latency for one token per sequence (3.4 us
 // for 64).  The cosines of a token are formed once and read side by side by the lanes (eight reads of
 // 8 bytes a unit, four ways into the same banks, took 24 us of 98 more).
 #include "lola_attn.cuh"

@@ -26,8 +26,8 @@
 //     are zeroed in shared memory before the product (0 x NaN would reach rows that do not see
 //     them); the values taken out are added back in the epilogue, for the rows that see them.
 // What bounds it: for long sequences the tensor core and its power (16 heads of 32768 tokens, d = 128:
-// 2.53 ms, 1740 TFLOP/s, 94 % of the measured bf16 product; 4 x 4096 x 32 heads 386 us, 1424 TFLOP/s): a
-// block pair's products take about 2300 cycles of the issuing thread's 2700, the rest is its wait for
+// 2.53 ms, 1740 TFLOP/s, 94 % of the measured bf16 product, and 2.66 ms in a row at 1.8 GHz and the power
+// limit; 4 x 4096 x 32 heads 389 us, 1413 TFLOP/s, and 403-420 us in a row): a block pair's products take about 2300 cycles of the issuing thread's 2700, the rest is its wait for
 // the weights (a softmax is 1100 cycles, behind it the other tile's products).  At d = 64 the
 // exponentials weigh twice as much against the products, whose narrow half (N = 64) runs at half rate (1050
 // TFLOP/s); no unit is then above 60 % of its rate, the softmax warps' own dependences are the bound.  Short
@@ -41,6 +41,8 @@
 // Keys in pages: the loader's lanes look a block's pages up while its place in the ring is still being read and
 // load a box each.  Pages of 64 tokens and more cost next to nothing (512 queries behind 6000 keys, 4 times, 32/8
 // heads, d = 128: 199 us, packed rows 191); pages of 16 are 32 boxes of 2 KB a block (284 us).
+// The tensor core cuts its float32 sums off instead of rounding them: outputs are low by up to 1e-5 of their
+// magnitude at 4096 keys, 1e-4 at 32768 and 5.5e-4 at 131072, where bfloat16 rounds by up to 2^-8.
 // Every wait is bounded (1 s, those that may last a whole item 10 s, then LOLA_ATTN_TIMEOUT).
 #include <cuda.h>
 

@@ -11,11 +11,12 @@
 // leaves (m, l, O) in the workspace, and the last of an item's pieces to arrive joins them:
 //   m = max_k m_k,  l = sum_k 2^{m_k - m} l_k,  o = sum_k 2^{m_k - m} O_k / l,
 // always in the order of the pieces, so that the result does not depend on who comes last.
-// Measured: 64 sequences of 1000-8000 tokens, 32/8 heads, d = 128, bf16: 139 us, 6.2 TB/s; 3 of 65536-131072, 8
-// heads: 177 us, 6.7 TB/s; float32, 64 x 4000, 32/8 heads, d = 128: 318 us, 6.6 TB/s; d = 64, 64 x 8000, 16/8 heads,
-// bf16: 171 us, 6.1 TB/s.  Short calls are bound by their chain of dependent accesses (lengths, pages, first
+// Measured: 64 sequences of 1000-8000 tokens, 32/8 heads, d = 128, bf16: 148 us, 6.0 TB/s; 3 of 65536-131072, 8
+// heads: 181 us, 6.5 TB/s; float32, 64 x 4000, 32/8 heads, d = 128: 319 us, 6.6 TB/s; d = 64, 64 x 8000, 16/8 heads,
+// bf16: 176 us, 6.0 TB/s.  The producer's warp holds all nine to 168 registers a thread, and the kernels for
+// d = 128 keep about 100 bytes of theirs in local memory (64 in float32, groups of up to 4).  Short calls are bound by their chain of dependent accesses (lengths, pages, first
 // tile: 5 us; records, count, records read back where pieces are joined: 4 more: one sequence of 1000 tokens
-// 9.5 us).
+// 9.3 us).
 // Every wait is bounded (1 s, then LOLA_ATTN_TIMEOUT).
 #include <cuda.h>
 
@@ -725,9 +726,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_f32_kernel(const __g
 
 // ---- bf16: the tile products on the warps' matrix instructions ----
 // Two groups of four warps: at d = 128 they take the segments in turn, so that one group's epilogue runs beside
-// the other's tiles (64 sequences of 1000-8000 tokens, 32/8 heads: 142 us, 152 on tiles in turn); at d = 64, where a
-// tile's bytes come faster than four warps get through it, they take a segment's tiles in turn (64 x 8000 tokens,
-// 16/8 heads: 171 us, 214 on segments in turn).  A warp takes 16 of a tile's 64 tokens, with its own running
+// the other's tiles (64 sequences of 1000-8000 tokens, 32/8 heads, when both were built: 142 us, 152 on tiles in
+// turn); at d = 64, where a tile's bytes come faster than four warps get through it, they take a segment's tiles in
+// turn (64 x 8000 tokens, 16/8 heads, likewise: 171 us, 214 on segments in turn).  A warp takes 16 of a tile's 64 tokens, with its own running
 // maximum, sum and output of the 16 query rows, joined at the segment's end.  S = Q K^T has the rows of Q as M, so
 // that its accumulators are the A operand of P V as they stand.  m is raised lazily (it is set 8 above a
 // maximum, so that no weight is above one), which leaves the output alone for most tiles.

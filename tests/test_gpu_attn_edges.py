@@ -661,3 +661,29 @@ def test_first_call_of_a_new_thread_lola(L, gen):
     torch.cuda.synchronize()
     assert not isinstance(got[0], Exception), got
     assert torch.equal(Y, want)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
+def test_calls_with_nothing_in_them(L, gen, dtype, d):
+    """No queries, no keys, no new tokens; a batch of no sequences is refused."""
+    lay = L.ExactAttention(4, 2, d, dtype, *(torch.zeros(3, 2, 16, d, dtype=dtype, device="cuda") for _ in range(2)))
+    rows = lambda n, h: randn(gen, n, h, d, dtype=dtype)  # noqa: E731
+    none, zeros, table, inv = ints([0, 0]), ints([0]), ints([[1]]), _freq(d)
+    lse = torch.zeros(4, 5, device="cuda")
+    assert lay.prefill(rows(0, 4), rows(0, 2), rows(0, 2), none).shape == (0, 4, d)
+    out = lay.prefill(rows(5, 4), rows(0, 2), rows(0, 2), offsets([5]), none, lse=lse)
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+    assert bool((lay.prefill(rows(5, 4), rows(0, 2), rows(0, 2), offsets([5]), none) == 0).all())
+    assert lay.prefill(rows(0, 4), rows(7, 2), rows(7, 2), none, offsets([7])).shape == (0, 4, d)
+    assert lay.prefill_paged(rows(0, 4), none, ints([9]), table).shape == (0, 4, d)
+    assert bool((lay.prefill_paged(rows(5, 4), offsets([5]), zeros, table) == 0).all())
+    assert bool((lay.decode_step(rows(1, 4), zeros, table) == 0).all())
+    assert lay.append(rows(0, 2), rows(0, 2), ints([9]), table, cu_new=none, q=rows(0, 4), inv_freq=inv).shape == (0, 4, d)
+    assert lay.append(rows(0, 2), rows(0, 2), ints([9]), table, cu_new=none) is None
+    assert not bool(lay.k_pool.any()) and not bool(lay.v_pool.any())
+    for call in (lambda: lay.decode_step(rows(0, 4), zeros[:0], table[:0]), lambda: lay.prefill(rows(0, 4), rows(0, 2), rows(0, 2), none[:1]),
+                 lambda: lay.prefill_paged(rows(0, 4), none[:1], zeros[:0], table[:0]),
+                 lambda: lay.append(rows(0, 2), rows(0, 2), zeros[:0], table[:0])):
+        with pytest.raises(L.LolaError):
+            call()
+    quiet(L)
