@@ -505,13 +505,12 @@ int32_t lola_attn_status(int32_t* host_bits, void* stream);
  * the range (before anything is enqueued), LOLA_ERR_CUDA on a CUDA failure. */
 int32_t lola_selftest_bounded_wait(int64_t limit_ns, int64_t* host_elapsed_ns, void* stream);
 
-/* For tests, with no exact-attention call under way on the current device: from now on every third CTA of
- * lola_paged_decode, and of the bfloat16 prompt attention, gives up at its block of keys number `block` (64
- * and 128 tokens, counted over all that the CTA does, from 0) as if a wait there had reached its limit; -1: none does.
- * Such a call sets LOLA_ATTN_TIMEOUT and its outputs are not valid, but it leaves its workspace as any other
- * call: a later call, or a replay of the same captured one, is right.  Synchronises `stream`;
- * LOLA_ERR_INVALID_ARG for a block below -1. */
-int32_t lola_selftest_attn_wait(int32_t block, void* stream);
+/* For tests: in the calls of lola_paged_decode and of the bfloat16 prompt attention that follow in this process, every
+ * third CTA gives up at its block of keys number `block` (64 and 128 tokens, counted over all that the CTA does, from
+ * 0) as if a wait there had reached its limit; -1: none does.  Such a call sets LOLA_ATTN_TIMEOUT and its outputs
+ * are not valid, but it leaves its workspace as any other call, so that a replay of a captured call is right whatever
+ * the one before met.  A captured call keeps what was set.  LOLA_ERR_INVALID_ARG for a block below -1. */
+int32_t lola_selftest_attn_wait(int32_t block);
 
 #ifdef __cplusplus
 }

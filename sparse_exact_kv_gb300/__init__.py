@@ -145,7 +145,7 @@ def _load():
                               ctypes.c_int32),
         "lola_paged_decode_workspace_bytes": ([AC], ctypes.c_int64),
         "lola_paged_decode": ([AC, PK, R, R, P, P, ctypes.c_size_t, P], ctypes.c_int32),
-        "lola_selftest_attn_wait": ([ctypes.c_int32, P], ctypes.c_int32),
+        "lola_selftest_attn_wait": ([ctypes.c_int32], ctypes.c_int32),
         "lola_attn_status": ([ctypes.POINTER(ctypes.c_int32), P], ctypes.c_int32),
     }
     for name, (args, res) in sig.items():
@@ -449,10 +449,9 @@ def lola_paged_decode(cfg: lola_attn_config, kv: lola_paged_kv, Q, O, workspace,
         raise LolaError(st, "lola_paged_decode")
 
 
-def lola_selftest_attn_wait(block: int, stream=None) -> None:
-    """The block of keys at which every third CTA of the exact-attention kernels gives up on the current
-    device; -1: none."""
-    _check(_lib.lola_selftest_attn_wait(int(block), _stream(stream)), "lola_selftest_attn_wait")
+def lola_selftest_attn_wait(block: int) -> None:
+    """The block of keys at which every third CTA of the exact-attention kernels gives up; -1: none."""
+    _check(_lib.lola_selftest_attn_wait(int(block)), "lola_selftest_attn_wait")
 
 
 def lola_attn_status(stream=None):

@@ -36,6 +36,7 @@ struct AttnArgs {
     float* lse;          // [Hq][total_q] or null
     float scale_log2;    // c log2(e): scores are kept in log2 units
     PagedArgs p;         // lola_paged_prefill: the keys and values (p.table null otherwise)
+    int give_up;         // lola_selftest_attn_wait: a pair of key blocks at which every third CTA gives up
 };
 
 // ---- packed sequences ----
@@ -165,6 +166,11 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int u, TilePos* pos
     return true;
 }
 
+// lola_selftest_attn_wait: whether this CTA is one that gives up at block `at`, and that is one of the n from `first` on.
+__device__ __forceinline__ bool gives_up(int at, int first, int n) {
+    return at >= first && at - first < n && blockIdx.x % 3 == (unsigned)at % 3;
+}
+
 // Opts a kernel in to `bytes` of dynamic shared memory, once per device (`done`: the kernel's own,
 // one bit per device; the call costs about a microsecond).
 template <typename K>
@@ -181,7 +187,7 @@ cudaError_t opt_in_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
 
 // These kernels are launched behind the stream's last kernel without waiting for its end: a CTA may start when
 // that one's CTAs are done (or let it), sets up its barriers, and waits here before it touches global memory
-// (but for the self-test's word, which no kernel writes) -- every CTA, so that a kernel that is done says that all before it are.  In a stream, one sequence of 1000
+// -- every CTA, so that a kernel that is done says that all before it are.  In a stream, one sequence of 1000
 // tokens 12.2 -> 9.1 us a call, five short prompts 12.3 -> 9.9.  (They do not let the next kernel start before
 // their end: its first, longest CTAs would gather on the SMs that are free first; float32 prompts 63 -> 68 us.)
 __device__ __forceinline__ void wait_for_last_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -219,6 +225,7 @@ struct DecodeArgs {
     float* lse;
     float* part;             // workspace
     uint64_t tag;            // 56 bits that no other call has
+    int give_up;             // lola_selftest_attn_wait
     float scale_log2;
 };
 cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t st);
@@ -227,8 +234,5 @@ cudaError_t attn_status_word(int32_t** word);
 cudaError_t attn_tc_status_word(int32_t** word);
 cudaError_t append_status_word(int32_t** word);
 cudaError_t paged_status_word(int32_t** word);
-// lola_selftest_attn_wait
-cudaError_t attn_tc_give_up(int pair, cudaStream_t st);
-cudaError_t paged_give_up(int tile, cudaStream_t st);
 
 }  // namespace lola

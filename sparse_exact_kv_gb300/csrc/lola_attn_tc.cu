@@ -40,7 +40,7 @@
 // 16 heads: 2.30 ms against 2.12).
 // Keys in pages: the loader's lanes look a block's pages up while its place in the ring is still being read and
 // load a box each.  Pages of 64 tokens and more cost next to nothing (512 queries behind 6000 keys, 4 times, 32/8
-// heads, d = 128: 199 us, packed rows 191); pages of 16 are 32 boxes of 2 KB a block (284 us).
+// heads, d = 128: 198 us, packed rows 192); pages of 16 are 32 boxes of 2 KB a block (280 us).
 // The tensor core cuts its float32 sums off instead of rounding them: outputs are low by up to 1e-5 of their
 // magnitude at 4096 keys, 1e-4 at 32768 and 5.5e-4 at 131072, where bfloat16 rounds by up to 2^-8.
 // Every wait is bounded (1 s, those that may last a whole item 10 s, then LOLA_ATTN_TIMEOUT).
@@ -64,7 +64,6 @@ constexpr int kClean = 4;                // barriers of the blocks to be cleaned
 constexpr float kRaise = 8.0f;           // m is set this far above a block's maximum (log2), and raised when one passes it
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint64_t kItemNs = 10000000000ull;   // ... of the waits that may last a whole item
-__device__ int g_give_up = -1;           // lola_selftest_attn_wait: a pair of blocks at which every third CTA gives up
 
 // NT: query tiles of a CTA.  Two: one CTA per SM, K and V blocks shared by 256 queries.  One: two CTAs
 // per SM, each with its own ring (half the shared memory, half of TMEM).
@@ -293,8 +292,6 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
         }
         abort_sm = 0;
     }
-    int give_up = -1;
-    if (warp == C::kLoadWarp) give_up = *reinterpret_cast<const volatile int*>(&g_give_up);   // (long before it is looked at)
     if (warp == kMmaWarp) tmem_alloc<C::kTmem>(smem_u32(&tmem_base));
     wait_for_last_kernel();
     Finder<C::kQ, PG> find;
@@ -430,7 +427,9 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
                     };
                     if (sp.nmax > 0) {
                         load_q(0);
-                        for (int p = 0; p <= sp.nmax && ok; ++p) {
+                        const bool give_up = gives_up(a.give_up, P, sp.nmax + 1);
+                        const int stop = give_up ? a.give_up - P : sp.nmax + 1;
+                        for (int p = 0; p < stop && ok; ++p) {
                             [[maybe_unused]] int pos = 0, entry = 0;
                             [[maybe_unused]] bool mine = false;
                             if constexpr (PG) {
@@ -443,11 +442,6 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
                                 entry = (page < 0 ? a.p.n_pages : page) * a.p.Hkv + (page < 0 ? 0 : hk);
                             }
                             if (P >= kCap && !(ok = agree(wait(empty_of(P), phase(P - kCap))))) break;
-                            if (P == give_up && blockIdx.x % 3 == (unsigned)P % 3) {
-                                abort_sm = 1;
-                                ok = false;
-                                break;
-                            }
                             const int full = full_of(P);
                             if (!PG || lane == 0) mbar_expect(bar(full), (uint32_t)((p > 0) + (p < sp.nmax)) * C::kTileBytes);
                             if constexpr (PG) {
@@ -467,6 +461,10 @@ __global__ void __launch_bounds__((NT + 1) * 128, 3 - NT) attn_tc_kernel(const _
                             cleans += p > sp.nf;
                             ++P;
                             if (p == 0 && NT == 2) load_q(NT - 1);
+                        }
+                        if (give_up) {
+                            abort_sm = 1;
+                            ok = false;
                         }
                     }
                     if (PG) __syncwarp();                              // (every lane has read the item)
@@ -834,10 +832,6 @@ template <bool PG> static cudaError_t launch_form(const AttnArgs& a, cudaStream_
 
 cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t st) {
     return a.p.table ? launch_form<true>(a, st) : launch_form<false>(a, st);
-}
-
-cudaError_t attn_tc_give_up(int pair, cudaStream_t st) {
-    return cudaMemcpyToSymbolAsync(g_give_up, &pair, sizeof(pair), 0, cudaMemcpyHostToDevice, st);
 }
 
 cudaError_t attn_tc_status_word(int32_t** word) { return cudaGetSymbolAddress((void**)word, g_status); }

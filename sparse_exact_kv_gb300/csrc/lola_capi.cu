@@ -329,6 +329,8 @@ cudaError_t take_status(int32_t* bits, cudaStream_t st) {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
+std::atomic<int> g_give_up{-1};     // lola_selftest_attn_wait
+
 // A number of 56 bits that none of the next 2^56 calls of this process has, and that memory hardly holds by
 // chance: a count from the process's start, mixed by steps that are one to one on 56 bits.
 uint64_t call_tag() {
@@ -731,6 +733,7 @@ int32_t lola_attn_prefill(const lola_attn_config* cfg, int32_t n_seq, int32_t to
     a.V = total_k > 0 ? to_rows(V) : a.Q;
     a.lse = lse;
     a.scale_log2 = attn_scale_log2(cfg);
+    a.give_up = g_give_up.load(std::memory_order_relaxed);
     cudaStream_t st = (cudaStream_t)stream;
     const cudaError_t e = traced(LOLA_KERNEL_ATTN, st, [&]() { return launch_attn_prefill(a, st); });
     return e == cudaSuccess ? LOLA_OK : cuda_fail(e, "prompt attention");
@@ -768,6 +771,7 @@ int32_t lola_paged_prefill(const lola_attn_config* cfg, const lola_paged_kv* kv,
     a.K = a.V = Rows{nullptr, 0, 0};
     a.lse = lse;
     a.scale_log2 = attn_scale_log2(cfg);
+    a.give_up = g_give_up.load(std::memory_order_relaxed);
     cudaStream_t st = (cudaStream_t)stream;
     const cudaError_t e = traced(LOLA_KERNEL_ATTN, st, [&]() { return launch_attn_prefill(a, st); });
     return e == cudaSuccess ? LOLA_OK : cuda_fail(e, "paged prompt attention");
@@ -810,13 +814,10 @@ int32_t lola_paged_append(const lola_attn_config* cfg, const lola_paged_kv* kv, 
     return e == cudaSuccess ? LOLA_OK : cuda_fail(e, "paged append");
 }
 
-int32_t lola_selftest_attn_wait(int32_t block, void* stream) {
+int32_t lola_selftest_attn_wait(int32_t block) {
     if (block < -1) return LOLA_ERR_INVALID_ARG;
-    cudaStream_t st = (cudaStream_t)stream;
-    cudaError_t e = paged_give_up(block, st);
-    if (e == cudaSuccess) e = attn_tc_give_up(block, st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    return e == cudaSuccess ? LOLA_OK : cuda_fail(e, "lola_selftest_attn_wait");
+    g_give_up.store(block, std::memory_order_relaxed);
+    return LOLA_OK;
 }
 
 int64_t lola_paged_decode_workspace_bytes(const lola_attn_config* cfg) {
@@ -838,6 +839,7 @@ int32_t lola_paged_decode(const lola_attn_config* cfg, const lola_paged_kv* kv, 
     a.lse = lse;
     a.part = static_cast<float*>(workspace);
     a.scale_log2 = attn_scale_log2(cfg);
+    a.give_up = g_give_up.load(std::memory_order_relaxed);
     cudaStream_t st = (cudaStream_t)stream;
     a.tag = call_tag();
     const cudaError_t e = traced(LOLA_KERNEL_PAGED, st, [&]() { return launch_paged_decode(a, st); });

@@ -13,7 +13,7 @@
 // always in the order of the pieces, so that the result does not depend on who comes last.
 // Measured: 64 sequences of 1000-8000 tokens, 32/8 heads, d = 128, bf16: 148 us, 6.0 TB/s; 3 of 65536-131072, 8
 // heads: 181 us, 6.5 TB/s; float32, 64 x 4000, 32/8 heads, d = 128: 319 us, 6.6 TB/s; d = 64, 64 x 8000, 16/8 heads,
-// bf16: 176 us, 6.0 TB/s.  The producer's warp holds all nine to 168 registers a thread, and the kernels for
+// bf16: 172 us, 6.1 TB/s.  The producer's warp holds all nine to 168 registers a thread, and the kernels for
 // d = 128 keep about 100 bytes of theirs in local memory (64 in float32, groups of up to 4).  Short calls are bound by their chain of dependent accesses (lengths, pages, first
 // tile: 5 us; records, count, records read back where pieces are joined: 4 more: one sequence of 1000 tokens
 // 9.3 us).
@@ -38,7 +38,6 @@ constexpr int kRows = 16;                 // query rows of a row group (at most)
 constexpr int kJoin = 16;                 // pieces joined at a time
 constexpr float kRaise = 8.0f;            // bf16: m is set this far above a maximum (log2), and raised when one passes it
 constexpr uint64_t kWaitNs = 1000000000ull;
-__device__ int g_give_up = -1;            // lola_selftest_attn_wait: a tile at which every third CTA gives up
 
 struct Maps {
     CUtensorMap k, v;   // [n_pages * Hkv][page][d] as 128-byte columns, boxes of min(page, 64) rows
@@ -51,6 +50,7 @@ struct Args {
     float* part;        // workspace: records, then the joins' cells
     uint64_t tag;       // this call's mark in the cells (the low 8 bits are 0)
     float scale_log2;
+    int give_up;        // lola_selftest_attn_wait: a tile at which every third CTA gives up
     int RG, I;          // row groups per key/value head; items (row groups) per sequence
 };
 
@@ -234,7 +234,6 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
     using C = Cfg<T, D>;
     const PagedArgs& p = a.p;
     const int box = min(p.page, kTile), lb = 31 - __clz(box), nbox = kTile >> lb;   // tokens of a box, boxes of a tile
-    const int give_up = *reinterpret_cast<const volatile int*>(&g_give_up);    // (beside the lengths)
     int b = st.b;
     int lens_b = b;                                               // the lanes hold 32 sequences' lengths
     int lens = b + lane < p.n_seq ? p.kv_len[b + lane] : 0;
@@ -273,13 +272,11 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
                       smem_u32(&bars.seg_full[slot]));
         ++i;
         // ---- its tiles ----
-        for (int t = t0; t < t1; ++t, ++n) {
+        const bool give_up = gives_up(a.give_up, n, t1 - t0);
+        const int stop = give_up ? t0 + a.give_up - n : t1;
+        for (int t = t0; t < stop; ++t, ++n) {
             const int s = n % C::kStages;
             if (n >= C::kStages) ok = __all_sync(0xffffffffu, ring_wait(smem_u32(&bars.empty[s]), (uint32_t)(n / C::kStages - 1) & 1, abort_sm));
-            if (n == give_up && blockIdx.x % 3 == (unsigned)n % 3) {
-                if (lane == 0) *reinterpret_cast<volatile int*>(abort_sm) = 1;
-                ok = false;
-            }
             if (!ok) break;
             // (positions fit 31 bits, but for the boxes behind the last token's)
             const uint32_t pos = (uint32_t)t * kTile, have = (uint32_t)tokens;
@@ -307,6 +304,10 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
                 tma_load4(ring + (uint32_t)s * 2 * C::kHalf + (lane >> 4) * C::kHalf + x * (uint32_t)(box * C::kRowBytes),
                           lane >> 4 ? &maps.v : &maps.k, 0, (int)((pos + x * box) & (p.page - 1)), 0, page * p.Hkv + hk,
                           smem_u32(&bars.full[s]));
+        }
+        if (give_up) {
+            if (lane == 0) *reinterpret_cast<volatile int*>(abort_sm) = 1;
+            ok = false;
         }
         u += t1 - t0;
         t0 = 0;
@@ -973,6 +974,7 @@ Args make_args(const DecodeArgs& d) {
     a.part = d.part;
     a.tag = d.tag << 8;
     a.scale_log2 = d.scale_log2;
+    a.give_up = d.give_up;
     a.RG = (d.p.G + kRows - 1) / kRows;
     a.I = d.p.Hkv * a.RG;
     return a;
@@ -1014,10 +1016,6 @@ int64_t paged_decode_workspace(int d) { return (int64_t)kPieces * kSlots * (reco
 cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t st) {
     if (a.p.dtype == LOLA_F32) return a.p.d == 128 ? launch_f32<128>(a, st) : launch_f32<64>(a, st);
     return a.p.d == 128 ? launch_bf16<128>(a, st) : launch_bf16<64>(a, st);
-}
-
-cudaError_t paged_give_up(int tile, cudaStream_t st) {
-    return cudaMemcpyToSymbolAsync(g_give_up, &tile, sizeof(tile), 0, cudaMemcpyHostToDevice, st);
 }
 
 cudaError_t paged_status_word(int32_t** word) { return cudaGetSymbolAddress((void**)word, g_status); }

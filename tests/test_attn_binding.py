@@ -11,9 +11,9 @@ def L():
 
 
 def test_selftest_blocks_outside_the_range_are_refused(L):
-    assert L._lib.lola_selftest_attn_wait(-2, None) == L.LOLA_ERR_INVALID_ARG
+    assert L._lib.lola_selftest_attn_wait(-2) == L.LOLA_ERR_INVALID_ARG
     with pytest.raises(L.LolaError):
-        L.lola_selftest_attn_wait(-2, stream=0)
+        L.lola_selftest_attn_wait(-2)
 
 
 def test_copies_of_a_layer_hold_their_own_description(L):
