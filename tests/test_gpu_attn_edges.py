@@ -687,3 +687,32 @@ def test_calls_with_nothing_in_them(L, gen, dtype, d):
         with pytest.raises(L.LolaError):
             call()
     quiet(L)
+
+
+def test_beside_a_lola_layer_on_another_stream(L, gen):
+    """A stack's two kinds of layers on two streams at once, which share the SMs' tensor memory: the bits of each are
+    those of its calls alone."""
+    lola = [L.Lola(1, 8, 128, 128, 64, 64, alloc=L.LOLA_ALLOC_CHUNK) for _ in range(6)]
+    q, k, v = (randn(gen, 1, 8, 1500, 128, dtype=BF) for _ in range(3))
+    W = torch.randn(64, 128, generator=gen, device="cuda") / 8
+    lens = [700, 130, 2000, 1]
+    c = Paged(gen, lens, 2, 128, 64, BF)
+    lay = L.ExactAttention(8, 2, 128, BF, c.k_pool, c.v_pool)
+    qe, cu, out = randn(gen, sum(lens), 8, 128, dtype=BF), offsets(lens), []
+    one = lola[0].prefill(q, k, v, W).clone()
+    two, three = lay.prefill_paged(qe, cu, c.kv_len, c.table), lay.decode_step(qe[:4], c.kv_len, c.table)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for other in lola[1:]:
+        other.workspace_for(1500)
+        Y = torch.empty_like(v)
+        with torch.cuda.stream(a):
+            other.prefill(q, k, v, W, Y=Y)
+        with torch.cuda.stream(b):
+            for _ in range(20):
+                out.append((lay.prefill_paged(qe, cu, c.kv_len, c.table), lay.decode_step(qe[:4], c.kv_len, c.table)))
+        torch.cuda.synchronize()
+        assert torch.equal(Y, one)
+        assert all(torch.equal(x, two) and torch.equal(y, three) for x, y in out)
+        out.clear()
+    quiet(L)
