@@ -629,7 +629,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     });
     return fn;
 }
-// The driver's call with these arguments.  It wants a current context, which a host thread that has not used the
+// cuTensorMapEncodeTiled with these arguments.  It wants a current context, which a host thread that has not used the
 // GPU yet does not have: the runtime then makes the device's own the thread's, and the call is made again.
 template <typename... A>
 bool encode(const A&... args) {
