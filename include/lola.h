@@ -263,7 +263,9 @@ typedef enum {
     LOLA_KERNEL_ATTN = 10,       /* exact attention over packed prompts */
     LOLA_KERNEL_APPEND = 11,     /* rotation and append to the paged cache */
     LOLA_KERNEL_PAGED = 12,      /* exact attention of one token over the paged cache */
-    LOLA_KERNEL_COUNT = 13
+    LOLA_KERNEL_QUANT_READ = 13, /* the quantised cache read back as rows */
+    LOLA_KERNEL_PREFIX = 14,     /* shared prefixes, for all sequences that begin with them */
+    LOLA_KERNEL_COUNT = 15
 } lola_kernel_id;
 
 /* enable != 0: clear the totals and start recording (process-wide); 0: stop recording. */
@@ -482,6 +484,73 @@ int64_t lola_paged_decode_workspace_bytes(const lola_attn_config* cfg);
  * width * page sets it too and counts as width * page. */
 int32_t lola_paged_decode(const lola_attn_config* cfg, const lola_paged_kv* kv, const lola_rows* Q,
                           const lola_rows* O, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- the paged cache, quantised ------------------------------------------------------------
+ * K and V of a lola_paged_kv hold e4m3 numbers (device [n_pages, Hkv, page, d], one byte each), and every row
+ * (one token's key or value of one head) has a power of two: x_i = code_i * 2^(byte - 127).  d + 1 bytes a row
+ * in place of 2 d (bfloat16) or 4 d.
+ * lola_quant_append takes for a row the smallest power with max |x_i| <= 448 * 2^e, kept in [-100, 119], and rounds
+ * x_i 2^-e to the nearest code (ties to even; numbers that are larger than 448 at the highest power saturate): an error
+ * of at most 2^-4 |x_i| or 2^(e - 10), whichever is larger.  Numbers that are not finite become the code for NaN, one
+ * by one, and do not count for the power.  A rotated key is rounded this once only.
+ * code_i * 2^e is exact in bfloat16 and in float32.  Powers that a caller writes: byte 1 .. 254 are 2^-126 .. 2^127
+ * (a product that leaves float32's range is infinite), 0 makes a key's row zero, and with 255 the results that see the
+ * row mean nothing. */
+typedef struct {
+    void* K;               /* device uint8 [n_pages, Hkv, page], 16-byte aligned: of the pools' rows */
+    void* V;
+} lola_kv_scales;
+
+/* lola_paged_append into a quantised cache: the same arguments and rules; K, V and Q are rows of cfg's dtype. */
+int32_t lola_quant_append(const lola_attn_config* cfg, const lola_paged_kv* kv, const lola_kv_scales* scales, int32_t n_tokens,
+                          const int32_t* cu_new, const lola_rows* K, const lola_rows* V, const lola_rows* Q,
+                          const lola_rows* QO, const float* inv_freq, int32_t rot, int32_t pairs,
+                          const int32_t* positions, void* stream);
+
+/* The cached tokens of all sequences as packed rows of cfg's dtype, for lola_attn_prefill: sequence b's kv_len
+ * tokens are the rows cu[b] .. cu[b+1].
+ *   total  rows of K and V, at least the sum of kv_len (lengths that pass it set LOLA_ATTN_BAD_OFFSETS; what is behind
+ *          the last row is not written).  Rows behind the sum are left as they were
+ *   cu     device int32 [n_seq + 1], written
+ * A token on a page outside the cache is read as zeros and sets LOLA_ATTN_BAD_PAGE; a kv_len beyond width * page sets
+ * it too and counts as width * page.  K and V must not overlap each other or the cache. */
+int32_t lola_quant_read(const lola_attn_config* cfg, const lola_paged_kv* kv, const lola_kv_scales* scales, int32_t total,
+                        const lola_rows* K, const lola_rows* V, int32_t* cu, void* stream);
+
+/* lola_paged_decode over a quantised cache: the same arguments, workspace and rules.  Codes and powers enter the
+ * products exactly.  With bfloat16 io q keeps all its bits down to 2^-28 of its row's largest number, and the weights
+ * are rounded to 11 bits; with float32 io both are good to float32's own rounding of the row's largest.  |q_i| is at
+ * most 2^100. */
+int32_t lola_quant_decode(const lola_attn_config* cfg, const lola_paged_kv* kv, const lola_kv_scales* scales, const lola_rows* Q,
+                          const lola_rows* O, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- sequences that begin with the same tokens -----------------------------------------------
+ * Prefixes of a cache, each held once: prefix g's tokens are in the pages of its own table row, and the sequences
+ * cu[g] .. cu[g+1] - 1 see them before their own tokens. */
+typedef struct {
+    int32_t n;             /* prefixes, at least 1 */
+    int32_t width;         /* page-table columns */
+    int64_t table_stride;  /* elements from one prefix' table row to the next, >= width */
+    const int32_t* table;  /* device int32; entries behind a prefix' pages are not read */
+    const int32_t* len;    /* device int32 [n]: tokens of each prefix; <= 0 means none */
+    const int32_t* cu;     /* device int32 [n + 1], non-decreasing; NULL with n = 1: all sequences share the prefix */
+} lola_prefixes;
+
+/* Bytes of device workspace a lola_shared_decode of n_seq sequences needs (negative: the lola_status of invalid
+ * arguments). */
+int64_t lola_shared_decode_workspace_bytes(const lola_attn_config* cfg, int32_t n_seq);
+
+/* Attention of one query token per sequence over its prefix' tokens and its own kv_len cached tokens: lola_paged_decode
+ * (scales NULL) or lola_quant_decode of the two one behind the other, with a prefix' keys and values read once for all
+ * sequences that share it.
+ * kv describes the pools and the sequences' own tokens (kv_len 0: none; the tokens are counted from 0 behind the
+ * prefix, so that an append of them takes explicit positions).  A sequence outside cu[0] .. cu[n] - 1 has no prefix.
+ * Offsets that decrease or pass n_seq leave their prefix without sequences and set LOLA_ATTN_BAD_OFFSETS; sequences
+ * that then belong to several see one of them, or none.  Pages outside the cache and lengths beyond the tables are
+ * treated as in lola_paged_decode.  The same inputs give the same bits. */
+int32_t lola_shared_decode(const lola_attn_config* cfg, const lola_paged_kv* kv, const lola_kv_scales* scales,
+                           const lola_prefixes* prefixes, const lola_rows* Q, const lola_rows* O, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream);
 
 /* Anomalies of the exact-attention calls since the last lola_attn_status on this device. */
 typedef enum {

@@ -54,11 +54,12 @@ EXPORTS = ("lola_version", "lola_status_string", "lola_last_cuda_error", "lola_c
            "lola_sre_map_relative", "lola_hola_workspace_bytes", "lola_hola_prefill", "lola_hola_status",
            "lola_attn_prefill", "lola_paged_slot", "lola_paged_append", "lola_paged_prefill",
            "lola_paged_decode_workspace_bytes",
-           "lola_paged_decode", "lola_attn_status", "lola_selftest_attn_wait")
+           "lola_paged_decode", "lola_quant_append", "lola_quant_read", "lola_quant_decode",
+           "lola_shared_decode_workspace_bytes", "lola_shared_decode", "lola_attn_status", "lola_selftest_attn_wait")
 # size of the fixed scratch array behind lola_prefill_noalloc (include/lola.h)
 LOLA_NOALLOC_SCRATCH_BYTES = 32 << 20
 KERNELS = ("state_init", "phi", "select", "output", "decode", "phi_q", "hola_prep", "hola_state", "hola_cache",
-           "hola_read", "attn", "append", "paged")
+           "hola_read", "attn", "append", "paged", "quant_read", "prefix")
 
 
 class lola_config(ctypes.Structure):
@@ -88,6 +89,15 @@ class lola_paged_kv(ctypes.Structure):
                 ("table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p)]
 
 
+class lola_kv_scales(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p)]
+
+
+class lola_prefixes(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("width", ctypes.c_int32), ("table_stride", ctypes.c_int64),
+                ("table", ctypes.c_void_p), ("len", ctypes.c_void_p), ("cu", ctypes.c_void_p)]
+
+
 class lola_state_layout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in
                 ("head_bytes", "H", "s", "win_pos", "win_k", "win_v", "win_phi", "c_pos", "c_k", "c_v", "c_phi",
@@ -114,6 +124,8 @@ def _load():
     AC = ctypes.POINTER(lola_attn_config)
     PK = ctypes.POINTER(lola_paged_kv)
     R = ctypes.POINTER(lola_rows)
+    SC = ctypes.POINTER(lola_kv_scales)
+    PX = ctypes.POINTER(lola_prefixes)
     sig = {
         "lola_version": ([], ctypes.c_int32),
         "lola_status_string": ([ctypes.c_int32], ctypes.c_char_p),
@@ -145,6 +157,12 @@ def _load():
                               ctypes.c_int32),
         "lola_paged_decode_workspace_bytes": ([AC], ctypes.c_int64),
         "lola_paged_decode": ([AC, PK, R, R, P, P, ctypes.c_size_t, P], ctypes.c_int32),
+        "lola_quant_append": ([AC, PK, SC, ctypes.c_int32, P, R, R, R, R, P, ctypes.c_int32, ctypes.c_int32, P, P],
+                              ctypes.c_int32),
+        "lola_quant_read": ([AC, PK, SC, ctypes.c_int32, R, R, P, P], ctypes.c_int32),
+        "lola_quant_decode": ([AC, PK, SC, R, R, P, P, ctypes.c_size_t, P], ctypes.c_int32),
+        "lola_shared_decode_workspace_bytes": ([AC, ctypes.c_int32], ctypes.c_int64),
+        "lola_shared_decode": ([AC, PK, SC, PX, R, R, P, P, ctypes.c_size_t, P], ctypes.c_int32),
         "lola_selftest_attn_wait": ([ctypes.c_int32], ctypes.c_int32),
         "lola_attn_status": ([ctypes.POINTER(ctypes.c_int32), P], ctypes.c_int32),
     }
@@ -161,6 +179,7 @@ _lib = _load()
 class _Declines:
     """In the marshalling module's place: every call takes its Python form."""
     prefill = prefill_paged = decode = append = staticmethod(lambda *args: NotImplemented)
+    quant_append = quant_decode = quant_read = shared = staticmethod(lambda *args: NotImplemented)
 
 
 def _marshalling(path):
@@ -449,6 +468,49 @@ def lola_paged_decode(cfg: lola_attn_config, kv: lola_paged_kv, Q, O, workspace,
         raise LolaError(st, "lola_paged_decode")
 
 
+def lola_quant_append(cfg: lola_attn_config, kv: lola_paged_kv, scales: lola_kv_scales, K, V, cu_new=None, Q=None, QO=None,
+                      inv_freq=None, pairs=LOLA_PAIRS_HALVES, positions=None, stream=None) -> None:
+    """lola_paged_append into a quantised cache."""
+    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
+    st = _lib.lola_quant_append(cfg, kv, scales, K.shape[0], _addr(cu_new), _rows(K), _rows(V), _rows(Q), _rows(QO),
+                                _addr(inv_freq), rot, pairs, _addr(positions), _stream_of(stream, K.get_device()))
+    if st:
+        raise LolaError(st, "lola_quant_append")
+
+
+def lola_quant_read(cfg: lola_attn_config, kv: lola_paged_kv, scales: lola_kv_scales, K, V, cu, stream=None) -> None:
+    """K, V: [total, Hkv, d], written; cu: int32 [n_seq + 1], written."""
+    st = _lib.lola_quant_read(cfg, kv, scales, K.shape[0], _rows(K), _rows(V), cu.data_ptr(),
+                              _stream_of(stream, K.get_device()))
+    if st:
+        raise LolaError(st, "lola_quant_read")
+
+
+def lola_quant_decode(cfg: lola_attn_config, kv: lola_paged_kv, scales: lola_kv_scales, Q, O, workspace, lse=None,
+                      stream=None) -> None:
+    """lola_paged_decode over a quantised cache."""
+    st = _lib.lola_quant_decode(cfg, kv, scales, _rows(Q), _rows(O), _addr(lse), workspace.data_ptr(), workspace.nbytes,
+                                _stream_of(stream, Q.get_device()))
+    if st:
+        raise LolaError(st, "lola_quant_decode")
+
+
+def lola_shared_decode_workspace_bytes(cfg: lola_attn_config, n_seq: int) -> int:
+    b = _lib.lola_shared_decode_workspace_bytes(ctypes.byref(cfg), n_seq)
+    if b < 0:
+        raise LolaError(int(b), "lola_shared_decode_workspace_bytes")
+    return int(b)
+
+
+def lola_shared_decode(cfg: lola_attn_config, kv: lola_paged_kv, scales, prefixes: lola_prefixes, Q, O, workspace, lse=None,
+                       stream=None) -> None:
+    """Q, O: [n_seq, Hq, d]; ``scales``: a quantised cache's, or None."""
+    st = _lib.lola_shared_decode(cfg, kv, scales, prefixes, _rows(Q), _rows(O), _addr(lse), workspace.data_ptr(),
+                                 workspace.nbytes, _stream_of(stream, Q.get_device()))
+    if st:
+        raise LolaError(st, "lola_shared_decode")
+
+
 def lola_selftest_attn_wait(block: int) -> None:
     """The block of keys at which every third CTA of the exact-attention kernels gives up; -1: none."""
     _check(_lib.lola_selftest_attn_wait(int(block)), "lola_selftest_attn_wait")
@@ -490,6 +552,7 @@ class ExactAttention:
     of inputs that require one."""
 
     __slots__ = ("cfg", "Hq", "Hkv", "d", "dtype", "k_pool", "v_pool", "_ws", "_plan")
+    _APPEND, _DECODE = "lola_paged_append", "lola_paged_decode"
 
     def __init__(self, Hq, Hkv, d, dtype=torch.bfloat16, k_pool=None, v_pool=None, scale=None):
         if _fast is _Declines:
@@ -513,6 +576,14 @@ class ExactAttention:
     def __reduce__(self):
         # (``_plan`` is the address of this object's ``cfg``: a copy, or another process' object, is made anew)
         return type(self), (self.Hq, self.Hkv, self.d, self.dtype, self.k_pool, self.v_pool, self.cfg.scale or None)
+
+    def _powers(self):
+        """A quantised cache's powers of two."""
+        return None, None
+
+    def _scales(self):
+        """... as the library's calls take them."""
+        return ()
 
     @classmethod
     def allocate(cls, Hq, Hkv, d, n_pages, page=64, dtype=torch.bfloat16, device="cuda", scale=None):
@@ -611,6 +682,9 @@ class ExactAttention:
             r = _fast.append(self._plan, self.k_pool, self.v_pool, k, v, kv_len, table, cu_new, q, inv_freq, PAIRS[pairs])
             if r is not NotImplemented:
                 return r
+        return self._append(k, v, kv_len, table, cu_new, q, inv_freq, q_out, pairs, positions, stream)
+
+    def _append(self, k, v, kv_len, table, cu_new, q, inv_freq, q_out, pairs, positions, stream):
         kv, dev, n_seq, index = self._cache(kv_len, table)
         n = k.shape[0]
         rk = self._heads(k, self.Hkv, n, dev, "k")
@@ -633,10 +707,10 @@ class ExactAttention:
                 q_out, ro = self._like(q, stream)
         elif q_out is not None:
             raise ValueError("q_out without q")
-        st = _lib.lola_paged_append(self.cfg, kv, n, _addr(cu_new), rk, rv, rq, ro, freq, rot, PAIRS[pairs],
-                                    _addr(positions), _stream_of(stream, index))
+        st = getattr(_lib, self._APPEND)(self.cfg, kv, *self._scales(), n, _addr(cu_new), rk, rv, rq, ro, freq, rot, PAIRS[pairs],
+                                         _addr(positions), _stream_of(stream, index))
         if st:
-            raise LolaError(st, "lola_paged_append")
+            raise LolaError(st, self._APPEND)
         return q_out
 
     def prefill_paged(self, q, cu_q, kv_len, table, total_k=0, out=None, lse=None, stream=None):
@@ -674,6 +748,35 @@ class ExactAttention:
             if out is not NotImplemented:
                 return out
             out = None
+        return self._decode(self._DECODE, self._scales(), q, kv_len, table, out, lse, workspace, stream)
+
+    def decode_shared(self, q, kv_len, table, prefix_len, prefix_table, cu_prefix=None, out=None, lse=None, workspace=None,
+                      stream=None):
+        """``decode_step`` for sequences that begin with common tokens, which are in the cache once: prefix g's
+        prefix_len[g] tokens (int32 [n_prefix]) are in the pages of ``prefix_table``'s row g (int32 [n_prefix,
+        width]), and the sequences cu_prefix[g] .. cu_prefix[g + 1] - 1 see them before their own ``kv_len`` tokens
+        (int32 [n_prefix + 1]; None with one prefix: all sequences do).  Own tokens are appended like any other
+        sequence's, with ``positions`` behind the prefix where they are rotated.  ``workspace``: a buffer of
+        lola_shared_decode_workspace_bytes."""
+        if out is None and lse is None and workspace is None and stream is None:
+            out = _fast.shared(self._plan, self.k_pool, self.v_pool, *self._powers(), q, kv_len, table, prefix_len,
+                               prefix_table, cu_prefix)
+            if out is not NotImplemented:
+                return out
+            out = None
+        dev, (n, width) = table.device, prefix_table.shape
+        self._vector(prefix_len, n, dev, "prefix_len")
+        if prefix_table.dtype != torch.int32 or prefix_table.device != dev or (prefix_table.stride(1) != 1 and width != 1):
+            raise ValueError(f"prefix_table: want int32 [{n}, width] on {dev}, rows contiguous")
+        if cu_prefix is not None:
+            self._vector(cu_prefix, n + 1, dev, "cu_prefix")
+        elif n != 1:
+            raise ValueError("cu_prefix: needed with several prefixes")
+        px = lola_prefixes(n, width, _table_stride(prefix_table), prefix_table.data_ptr(), prefix_len.data_ptr(), _addr(cu_prefix))
+        scales = self._scales() or (None,)
+        return self._decode("lola_shared_decode", (*scales, px), q, kv_len, table, out, lse, workspace, stream)
+
+    def _decode(self, name, more, q, kv_len, table, out, lse, workspace, stream):
         kv, dev, n, index = self._cache(kv_len, table)
         rq = self._heads(q, self.Hq, n, dev, "q")
         if lse is not None:
@@ -682,18 +785,124 @@ class ExactAttention:
             ro = self._heads(out, self.Hq, n, dev, "out")
         else:
             out, ro = self._like(q, stream)
-        size = self._ws
+        size = self._ws if name != "lola_shared_decode" else lola_shared_decode_workspace_bytes(self.cfg, n)
         if workspace is None:
             workspace = self._empty(size, torch.uint8, dev, stream)
         else:
             size = workspace.nbytes
             if workspace.device != dev or not workspace.is_contiguous():
                 raise ValueError(f"workspace: want a contiguous buffer on {dev}")
-        st = _lib.lola_paged_decode(self.cfg, kv, rq, ro, _addr(lse), workspace.data_ptr(), size,
-                                    _stream_of(stream, index))
+        st = getattr(_lib, name)(self.cfg, kv, *more, rq, ro, _addr(lse), workspace.data_ptr(), size,
+                                 _stream_of(stream, index))
         if st:
-            raise LolaError(st, "lola_paged_decode")
+            raise LolaError(st, name)
         return out
+
+
+def _quantized(cls, *a):
+    """A QuantizedAttention of what its __reduce__ gives."""
+    kinds = (torch.float8_e4m3fn,) * 2 + (torch.float8_e8m0fnu,) * 2
+    return cls(*a[:4], *(None if x is None else x.view(t) for x, t in zip(a[4:8], kinds)), *a[8:])
+
+
+class QuantizedAttention(ExactAttention):
+    """ExactAttention over a quantised cache: e4m3 numbers and a power of two for every token's key and value of
+    a head, d + 1 bytes in place of 2 d.
+
+    ``k_pool``, ``v_pool``: float8_e4m3fn [n_pages, Hkv, page, d]; ``k_scale``, ``v_scale``: float8_e8m0fnu
+    [n_pages, Hkv, page].  ``dtype`` is that of queries, outputs and appended rows.  ``append``, ``decode_step`` and
+    ``decode_shared`` take what ExactAttention's take; ``read`` gives the cached rows back, and ``prefill_paged``
+    attends to them.  ``prefill`` attends to the rows that it is given, which are not quantised."""
+
+    __slots__ = ("k_scale", "v_scale")
+    _APPEND, _DECODE = "lola_quant_append", "lola_quant_decode"
+
+    def __init__(self, Hq, Hkv, d, dtype=torch.bfloat16, k_pool=None, v_pool=None, k_scale=None, v_scale=None, scale=None):
+        self.k_scale, self.v_scale = k_scale, v_scale
+        super().__init__(Hq, Hkv, d, dtype, k_pool, v_pool, scale)
+
+    def _check_pools(self):
+        k, v, ks, vs = self.k_pool, self.v_pool, self.k_scale, self.v_scale
+        _need(not any(x is None for x in (k, v, ks, vs)), "k_pool, v_pool, k_scale and v_scale come together")
+        shape = k.shape
+        _need(len(shape) == 4 and shape[1] == self.Hkv and shape[3] == self.d, "pools are [n_pages, Hkv, page, d]")
+        for x, want, dt in ((k, shape, torch.float8_e4m3fn), (v, shape, torch.float8_e4m3fn),
+                            (ks, shape[:3], torch.float8_e8m0fnu), (vs, shape[:3], torch.float8_e8m0fnu)):
+            _need(x.shape == want and x.dtype == dt and x.is_contiguous() and x.device == k.device,
+                  "pools are contiguous float8_e4m3fn [n_pages, Hkv, page, d] and float8_e8m0fnu [n_pages, Hkv, page] on one device")
+
+    def _made_of(self):
+        return self.Hq, self.Hkv, self.d, self.dtype, self.k_pool, self.v_pool, self.k_scale, self.v_scale, self.cfg.scale or None
+
+    def __copy__(self):
+        return type(self)(*self._made_of())
+
+    def __reduce__(self):
+        # (torch does not serialise all of its 8-bit types: as bytes)
+        a = list(self._made_of())
+        a[4:8] = [None if x is None else x.view(torch.uint8) for x in a[4:8]]
+        return _quantized, (type(self), *a)
+
+    def _powers(self):
+        return self.k_scale, self.v_scale
+
+    def _scales(self):
+        if self.k_pool is None:
+            raise ValueError("this layer has no key-value pools")
+        self._check_pools()
+        return (lola_kv_scales(self.k_scale.data_ptr(), self.v_scale.data_ptr()),)
+
+    @classmethod
+    def allocate(cls, Hq, Hkv, d, n_pages, page=64, dtype=torch.bfloat16, device="cuda", scale=None):
+        def pool(dt, *shape):
+            return torch.zeros(n_pages, Hkv, page, *shape, dtype=torch.uint8, device=device).view(dt)
+        e4, e8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+        return cls(Hq, Hkv, d, dtype, pool(e4, d), pool(e4, d), pool(e8), pool(e8), scale)
+
+    def append(self, k, v, kv_len, table, cu_new=None, q=None, inv_freq=None, q_out=None, pairs="halves",
+               positions=None, stream=None):
+        """ExactAttention.append; a rotated key is rounded once, to its codes."""
+        if q_out is None and positions is None and stream is None:
+            r = _fast.quant_append(self._plan, self.k_pool, self.v_pool, self.k_scale, self.v_scale, k, v, kv_len, table, cu_new,
+                                   q, inv_freq, PAIRS[pairs])
+            if r is not NotImplemented:
+                return r
+        return self._append(k, v, kv_len, table, cu_new, q, inv_freq, q_out, pairs, positions, stream)
+
+    def decode_step(self, q, kv_len, table, out=None, lse=None, workspace=None, stream=None):
+        """ExactAttention.decode_step."""
+        if out is None and lse is None and workspace is None and stream is None:
+            out = _fast.quant_decode(self._plan, self.k_pool, self.v_pool, self.k_scale, self.v_scale, q, kv_len, table)
+            if out is not NotImplemented:
+                return out
+            out = None
+        return self._decode(self._DECODE, self._scales(), q, kv_len, table, out, lse, workspace, stream)
+
+    def read(self, kv_len, table, total, stream=None):
+        """The cached tokens of all sequences as packed rows of the layer's type: (k, v) [total, Hkv, d] and
+        cu int32 [n_seq + 1], sequence b's rows being cu[b] .. cu[b + 1] - 1.  ``total``: the sum of ``kv_len``
+        (rows behind the sum of a larger one are not initialised)."""
+        if stream is None:
+            r = _fast.quant_read(self._plan, self.k_pool, self.v_pool, self.k_scale, self.v_scale, kv_len, table, total)
+            if r is not NotImplemented:
+                return r
+        kv, dev, n, index = self._cache(kv_len, table)
+        if not isinstance(total, int) or not 0 <= total < 1 << 31:
+            raise ValueError("total: want the sum of kv_len")
+        k, v = (self._empty((total, self.Hkv, self.d), self.dtype, dev, stream) for _ in range(2))
+        cu = self._empty(n + 1, torch.int32, dev, stream)
+        st = _lib.lola_quant_read(self.cfg, kv, *self._scales(), total, _rows(k), _rows(v), cu.data_ptr(), _stream_of(stream, index))
+        if st:
+            raise LolaError(st, "lola_quant_read")
+        return k, v, cu
+
+    def prefill_paged(self, q, cu_q, kv_len, table, total_k=0, out=None, lse=None, stream=None):
+        """ExactAttention.prefill_paged: the cached rows are read back and attended to.  ``total_k``, the sum of
+        kv_len, has to be given."""
+        if total_k < 1:
+            raise ValueError("total_k: want the sum of kv_len")
+        k, v, cu_k = self.read(kv_len, table, total_k, stream)
+        return self.prefill(q, k, v, cu_q, cu_k, out, lse, stream)
 
 
 class Lola:

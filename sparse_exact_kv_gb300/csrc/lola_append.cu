@@ -20,22 +20,8 @@ namespace {
 
 __device__ int32_t g_status;
 
+constexpr int kLowPower = 27, kTopPower = 246;   // a quantised row's power of two, biased by 127: 2^-100 .. 2^119
 constexpr int kFew = 760;   // tokens up to which a CTA takes one (five CTAs per SM)
-
-// the sequence that row t belongs to, one warp: the last b with cu[b] <= t, found 32 offsets at a
-// time; -1 if none
-__device__ __forceinline__ int warp_find_seq(const int32_t* cu, int n_seq, int t, int lane) {
-    int lo = 0, hi = n_seq + 1;            // cu[lo] <= t < cu[hi] (hi may be one past the end)
-    if (cu[0] > t || cu[n_seq] <= t) return -1;
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-        const bool le = at < hi && cu[at] <= t;
-        const int k = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
-        lo = lo + k * step;
-        hi = min(hi, lo + step);
-    }
-    return lo;
-}
 
 template <typename T> __device__ __forceinline__ void unpack(const uint4& x, float (&v)[16 / sizeof(T)]);
 template <> __device__ __forceinline__ void unpack<float>(const uint4& x, float (&v)[4]) {
@@ -70,6 +56,7 @@ template <typename T> struct Unit {
     T* dst;              // null: nothing to do
     int c0, c1;          // channels of the two chunks
     uint4 x, y;
+    uint8_t* power;      // a row to be quantised (dst: its bytes): where its power of two goes; else null
 };
 // cs: float4 (i, u) at i * units + u holds pairs 2 i and 2 i + 1 of unit u, so that the lanes of a warp,
 // whose units follow each other, read side by side
@@ -82,8 +69,30 @@ __device__ __forceinline__ void load_unit(Unit<T>& n, const T* src, T* dst, int 
     n.c1 = turn && !neighbours ? n.c0 + rot / 2 : n.c0 + VN;
     n.cs = turn ? cs + u : nullptr;
     n.dst = dst;
+    n.power = nullptr;
     n.x = *reinterpret_cast<const uint4*>(src + n.c0);
     n.y = *reinterpret_cast<const uint4*>(src + n.c1);
+}
+template <int VN>
+__device__ __forceinline__ void turn_unit(float (&a)[VN], float (&b)[VN], const float4* cs, bool neighbours, int step) {
+#pragma unroll
+    for (int i = 0; i < VN / 2; ++i) {
+        const float4 c = cs[i * step];
+        // pairs 2 i and 2 i + 1: neighbours in the 2 VN channels, or element 2 i (+ 1) of either chunk
+        auto turn = [](float& x, float& y, float co, float si) {
+            const float x0 = x;
+            x = x0 * co - y * si;
+            y = y * co + x0 * si;
+        };
+        if (neighbours) {
+            float(&z)[VN] = 4 * i < VN ? a : b;
+            turn(z[4 * i % VN], z[4 * i % VN + 1], c.x, c.y);
+            turn(z[4 * i % VN + 2], z[4 * i % VN + 3], c.z, c.w);
+        } else {
+            turn(a[2 * i], b[2 * i], c.x, c.y);
+            turn(a[2 * i + 1], b[2 * i + 1], c.z, c.w);
+        }
+    }
 }
 template <typename T>
 __device__ __forceinline__ void finish_unit(Unit<T>& n, bool neighbours, int step) {
@@ -92,24 +101,7 @@ __device__ __forceinline__ void finish_unit(Unit<T>& n, bool neighbours, int ste
         float a[VN], b[VN];
         unpack<T>(n.x, a);
         unpack<T>(n.y, b);
-#pragma unroll
-        for (int i = 0; i < VN / 2; ++i) {
-            const float4 c = n.cs[i * step];
-            // pairs 2 i and 2 i + 1: neighbours in the 2 VN channels, or element 2 i (+ 1) of either chunk
-            auto turn = [](float& x, float& y, float co, float si) {
-                const float x0 = x;
-                x = x0 * co - y * si;
-                y = y * co + x0 * si;
-            };
-            if (neighbours) {
-                float(&z)[VN] = 4 * i < VN ? a : b;
-                turn(z[4 * i % VN], z[4 * i % VN + 1], c.x, c.y);
-                turn(z[4 * i % VN + 2], z[4 * i % VN + 3], c.z, c.w);
-            } else {
-                turn(a[2 * i], b[2 * i], c.x, c.y);
-                turn(a[2 * i + 1], b[2 * i + 1], c.z, c.w);
-            }
-        }
+        turn_unit<VN>(a, b, n.cs, neighbours, step);
         n.x = pack<T>(a);
         n.y = pack<T>(b);
     }
@@ -117,8 +109,54 @@ __device__ __forceinline__ void finish_unit(Unit<T>& n, bool neighbours, int ste
     *reinterpret_cast<uint4*>(n.dst + n.c1) = n.y;
 }
 
-// TOK tokens a CTA of NT threads; a thread has IN units in flight.
-template <typename T, int D, int TOK, int NT, int IN>
+// The same for a row that is quantised: its UH units are in as many neighbouring lanes (all lanes of the warp come
+// here, those of other rows without effect).  The row's power of two is the smallest 2^e whose 448-fold reaches its
+// largest magnitude: 448 = 1.75 2^8, so that e is the magnitude's own exponent - 8, and one more behind 1.75; it is
+// kept in [-100, 119], where code 2^e is exact in bfloat16 and float32 and sums of 2^-e stay in float32.  A
+// rotated key is not rounded before that.  Numbers that are not finite become the code for NaN, and do not count for e.
+template <typename T, int UH>
+__device__ __forceinline__ void quantise_unit(Unit<T>& n, bool neighbours, int step, bool first) {
+    constexpr int VN = 16 / sizeof(T);
+    float a[VN], b[VN];
+    uint32_t top = 0u;
+    if (n.power) {
+        unpack<T>(n.x, a);
+        unpack<T>(n.y, b);
+        if (n.cs) turn_unit<VN>(a, b, n.cs, neighbours, step);
+#pragma unroll
+        for (int i = 0; i < VN; ++i) {
+            const uint32_t x = __float_as_uint(a[i]) & 0x7fffffffu, y = __float_as_uint(b[i]) & 0x7fffffffu;
+            if (x < 0x7f800000u) top = max(top, x);
+            if (y < 0x7f800000u) top = max(top, y);
+        }
+    }
+#pragma unroll
+    for (int o = UH / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (!n.power) return;
+    const int power = min(max((int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u), kLowPower), kTopPower);
+    const float down = __uint_as_float((uint32_t)(254 - power) << 23);
+    auto codes = [&](const float(&v)[VN], uint8_t* dst) {
+        uint32_t w[VN / 4];
+#pragma unroll
+        for (int i = 0; i < VN / 4; ++i) {
+            // (saturating, but infinities are no number of this type's)
+            auto num = [&](float x) { return fabsf(x) < INFINITY ? x * down : NAN; };
+            uint16_t lo, hi;
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(num(v[4 * i + 1])), "f"(num(v[4 * i])));
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(num(v[4 * i + 3])), "f"(num(v[4 * i + 2])));
+            w[i] = (uint32_t)lo | ((uint32_t)hi << 16);
+        }
+        if constexpr (VN == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t*>(dst) = w[0];
+    };
+    uint8_t* dst = reinterpret_cast<uint8_t*>(n.dst);
+    codes(a, dst + n.c0);
+    codes(b, dst + n.c1);
+    if (first) *n.power = (uint8_t)power;
+}
+
+// TOK tokens a CTA of NT threads; a thread has IN units in flight.  QZ: into a quantised cache.
+template <typename T, int D, int TOK, int NT, int IN, bool QZ>
 __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendArgs a) {
     __shared__ __align__(16) float4 cs[TOK][D / 4];
     __shared__ uint64_t turn_sm[D / 2];
@@ -178,12 +216,13 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendArgs a) {
     __syncthreads();
     const int hq = a.Q.data ? p.Hq : 0, heads = hq + 2 * p.Hkv, units = nt * heads * UH;
     const bool nb = a.pairs == LOLA_PAIRS_NEIGHBOURS;
-    for (int e0 = threadIdx.x; e0 < units; e0 += NT * IN) {
+    for (int e0 = threadIdx.x; (QZ ? e0 - lane : e0) < units; e0 += NT * IN) {
         Unit<T> n[IN];
 #pragma unroll
         for (int x = 0; x < IN; ++x) {
             const int e = e0 + x * NT;
             n[x].dst = nullptr;
+            n[x].power = nullptr;
             if (e >= units) continue;
             const int u = e % UH, th = e / UH;
             int i = 0;                           // th / heads
@@ -199,29 +238,38 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendArgs a) {
                 const bool v = h >= hq + p.Hkv;
                 const int hk = h - hq - (v ? p.Hkv : 0);
                 const Rows& r = v ? a.V : a.K;
+                const int64_t at = s + (int64_t)hk * p.page * D;
                 load_unit<T>(n[x], reinterpret_cast<const T*>(r.data) + t * r.row + hk * r.head,
-                             reinterpret_cast<T*>(v ? p.V : p.K) + s + (int64_t)hk * p.page * D, u, v ? 0 : rot, nb, cs[i]);
+                             QZ ? reinterpret_cast<T*>((v ? p.V : p.K) + at) : reinterpret_cast<T*>(v ? p.V : p.K) + at, u, v ? 0 : rot, nb,
+                             cs[i]);
+                if (QZ) n[x].power = (v ? p.Vs : p.Ks) + at / D;
             }
         }
 #pragma unroll
-        for (int x = 0; x < IN; ++x)
-            if (n[x].dst) finish_unit<T>(n[x], nb, ru);
+        for (int x = 0; x < IN; ++x) {
+            if (QZ) quantise_unit<T, UH>(n[x], nb, ru, (e0 + x * NT) % UH == 0);
+            if (n[x].dst && !n[x].power) finish_unit<T>(n[x], nb, ru);
+        }
     }
 }
 
 // Few tokens: one a CTA, so that none waits for another's page lookup; many: four, whose rows of a head
 // lie side by side in the page (512 tokens, 32/8 heads: 4.5 us one a CTA, 5.5 us four; 1024: 7.4 and 6.6).
-template <typename T, int D>
+template <typename T, int D, bool QZ>
 cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
-    if (a.n_tokens <= kFew) return launch_behind(paged_append_kernel<T, D, 1, 128, 3>, (unsigned)a.n_tokens, 128, 0, st, a);
-    return launch_behind(paged_append_kernel<T, D, 4, 256, 3>, (unsigned)(a.n_tokens + 3) / 4, 256, 0, st, a);
+    if (a.n_tokens <= kFew) return launch_behind(paged_append_kernel<T, D, 1, 128, 3, QZ>, (unsigned)a.n_tokens, 128, 0, st, a);
+    return launch_behind(paged_append_kernel<T, D, 4, 256, 3, QZ>, (unsigned)(a.n_tokens + 3) / 4, 256, 0, st, a);
+}
+template <typename T>
+cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
+    if (a.p.Ks) return a.p.d == 128 ? launch<T, 128, true>(a, st) : launch<T, 64, true>(a, st);
+    return a.p.d == 128 ? launch<T, 128, false>(a, st) : launch<T, 64, false>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t st) {
-    if (a.p.dtype == LOLA_F32) return a.p.d == 128 ? launch<float, 128>(a, st) : launch<float, 64>(a, st);
-    return a.p.d == 128 ? launch<__nv_bfloat16, 128>(a, st) : launch<__nv_bfloat16, 64>(a, st);
+    return a.p.dtype == LOLA_F32 ? launch<float>(a, st) : launch<__nv_bfloat16>(a, st);
 }
 
 cudaError_t append_status_word(int32_t** word) { return cudaGetSymbolAddress((void**)word, g_status); }

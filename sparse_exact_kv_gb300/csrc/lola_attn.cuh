@@ -25,7 +25,26 @@ struct PagedArgs {
     const int32_t* table;
     const int32_t* kv_len;
     int Hq, Hkv, G, d, dtype;
+    uint8_t* Ks;         // a quantised cache's powers of two [n_pages, Hkv, page] (K and V are e4m3 numbers then),
+    uint8_t* Vs;         // or null
 };
+
+// Prefixes that several sequences share: sequences cu[g] .. cu[g + 1] - 1 see the tokens of prefix g before their
+// own.  A kernel over the prefixes leaves, for every row (sequence, query head) i of a prefix with tokens, the parts
+// of its softmax (largest score m in log2 units, sum l and output z against m): one part in whole[i], ml[i], or the
+// parts of the prefix' pieces in records, piece after piece, the first of them at desc[i].y, row desc[i].z; desc[i].x
+// says how many.  The kernel over the sequences' own tokens joins them with its own part.
+struct Prior {
+    PagedArgs p;           // tables and lengths of the prefixes (p.n_seq of them); p.table null: there are none
+    const int32_t* cu;     // null: one prefix for all sequences
+    int n_seq;             // sequences
+    int4* desc;
+    float* whole;          // [n_seq * Hq][d]
+    float2* ml;
+    float* rec;            // records of `rows` rows: z, where row r's columns 4 x .. 4 x + 3 are at r row_step + x chunk_step,
+    int rows, row_step, chunk_step;      // then m [rows], l [rows]
+};
+__host__ __device__ constexpr int64_t prior_record(int rows, int d) { return (int64_t)rows * (d + 2); }
 
 // one lola_attn_prefill or lola_paged_prefill
 struct AttnArgs {
@@ -78,6 +97,33 @@ __device__ __forceinline__ void seq_keys(const AttnArgs& a, int b, int* begin, i
     } else {
         seq_rows(a.cu_k, b, a.total_k, begin, len, bits);
     }
+}
+
+// The sequence that row t belongs to, one warp: the last b with cu[b] <= t, found 32 offsets at a time; -1 if none.
+__device__ __forceinline__ int warp_find_seq(const int32_t* cu, int n_seq, int t, int lane) {
+    int lo = 0, hi = n_seq + 1;            // cu[lo] <= t < cu[hi] (hi may be one past the end)
+    if (cu[0] > t || cu[n_seq] <= t) return -1;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const bool le = at < hi && cu[at] <= t;
+        const int k = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
+        lo = lo + k * step;
+        hi = min(hi, lo + step);
+    }
+    return lo;
+}
+// The prefix of sequence b (one warp), if it has one with tokens, or -1: where offsets are malformed, only one whose
+// kernel has worked for b too.
+__device__ __forceinline__ int prior_of(const Prior& q, int b, int lane) {
+    if (!q.p.table) return -1;
+    int g = 0, lo, n, bad = 0;
+    if (q.cu) {
+        g = warp_find_seq(q.cu, q.p.n_seq, b, lane);
+        if (g < 0 || g >= q.p.n_seq) return -1;
+        seq_rows(q.cu, g, q.n_seq, &lo, &n, &bad);
+        if (b < lo || b >= lo + n) return -1;
+    }
+    return paged_tokens(q.p, q.p.kv_len[g]) > 0 ? g : -1;
 }
 
 // Piece c of n equal pieces of `total` units: [split_at(c), split_at(c + 1))
@@ -220,7 +266,8 @@ struct AppendArgs {
 cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t st);
 int64_t paged_decode_workspace(int d);
 struct DecodeArgs {
-    PagedArgs p;
+    PagedArgs p;             // launch_*_prefix: of the prefixes
+    Prior sh;
     Rows Q, O;
     float* lse;
     float* part;             // workspace
@@ -229,10 +276,23 @@ struct DecodeArgs {
     float scale_log2;
 };
 cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t st);
+// Bytes of the workspace of `q`'s arrays; lays them out from `base` on, where q is given.
+int64_t prior_workspace(int n_seq, int Hq, int d, int dtype, char* base, Prior* q);
+cudaError_t launch_paged_prefix(const DecodeArgs& a, cudaStream_t st);
+cudaError_t launch_quant_decode(const DecodeArgs& a, cudaStream_t st);
+cudaError_t launch_quant_prefix(const DecodeArgs& a, cudaStream_t st);
+struct ReadArgs {
+    PagedArgs p;
+    int total;               // rows
+    Rows K, V;
+    int32_t* cu;             // [n_seq + 1], written
+};
+cudaError_t launch_quant_read(const ReadArgs& a, cudaStream_t st);
 // the address of a translation unit's anomaly word on the current device
 cudaError_t attn_status_word(int32_t** word);
 cudaError_t attn_tc_status_word(int32_t** word);
 cudaError_t append_status_word(int32_t** word);
 cudaError_t paged_status_word(int32_t** word);
+cudaError_t quant_status_word(int32_t** word);
 
 }  // namespace lola

@@ -304,20 +304,20 @@ Rows to_rows(const lola_rows* r) { return r ? Rows{static_cast<char*>(r->data), 
 // The anomaly words of the exact-attention kernels are read and cleared in one step, so that a bit that another
 // stream's kernel sets meanwhile is in this reading or left for the next one.
 struct StatusWords {
-    int32_t* word[4];
+    int32_t* word[5];
 };
 __device__ int32_t g_taken;
 __global__ void take_status_kernel(StatusWords w) {
     int32_t bits = 0;
-    for (int i = 0; i < 4; ++i) bits |= atomicExch(w.word[i], 0);
+    for (int i = 0; i < 5; ++i) bits |= atomicExch(w.word[i], 0);
     g_taken = bits;
 }
 cudaError_t take_status(int32_t* bits, cudaStream_t st) {
     static std::mutex m;                       // (one reading's bits are copied before the next one)
     std::lock_guard<std::mutex> lock(m);
     StatusWords w;
-    cudaError_t (*const find[])(int32_t**) = {attn_status_word, attn_tc_status_word, append_status_word, paged_status_word};
-    for (int i = 0; i < 4; ++i) {
+    cudaError_t (*const find[])(int32_t**) = {attn_status_word, attn_tc_status_word, append_status_word, paged_status_word, quant_status_word};
+    for (int i = 0; i < 5; ++i) {
         const cudaError_t e = find[i](&w.word[i]);
         if (e != cudaSuccess) return e;
     }
@@ -366,6 +366,7 @@ int32_t paged_check(const lola_attn_config* c, const lola_paged_kv* kv, PagedArg
     p->table_stride = kv->table_stride;
     p->table = kv->table;
     p->kv_len = kv->kv_len;
+    p->Ks = p->Vs = nullptr;
     p->Hq = c->Hq;
     p->Hkv = c->Hkv;
     p->G = c->Hq / c->Hkv;
@@ -373,6 +374,16 @@ int32_t paged_check(const lola_attn_config* c, const lola_paged_kv* kv, PagedArg
     p->dtype = c->dtype;
     return LOLA_OK;
 }
+// a quantised cache: the pools' powers of two beside them
+int32_t quant_check(const lola_attn_config* c, const lola_paged_kv* kv, const lola_kv_scales* scales, PagedArgs* p) {
+    const int32_t s = paged_check(c, kv, p);
+    if (s != LOLA_OK) return s;
+    if (!scales || !scales->K || !scales->V || !aligned16(scales->K) || !aligned16(scales->V)) return LOLA_ERR_INVALID_ARG;
+    p->Ks = static_cast<uint8_t*>(scales->K);
+    p->Vs = static_cast<uint8_t*>(scales->V);
+    return LOLA_OK;
+}
+constexpr int64_t kMostRows = (int64_t)1 << 28;     // (sequence, query head) rows of a lola_shared_decode
 }  // namespace
 
 }  // namespace lola
@@ -589,7 +600,7 @@ int32_t lola_kernel_time(int32_t id, double* total_ms, int64_t* launches) {
 const char* lola_kernel_name(int32_t id) {
     static const char* names[LOLA_KERNEL_COUNT] = {"state_init", "phi",        "select",     "output",     "decode",
                                                         "phi_q",      "hola_prep",  "hola_state", "hola_cache", "hola_read",
-                                                        "attn",       "append",     "paged"};
+                                                        "attn",       "append",     "paged",      "quant_read", "prefix"};
     return (id >= 0 && id < LOLA_KERNEL_COUNT) ? names[id] : "";
 }
 
@@ -777,13 +788,10 @@ int32_t lola_paged_prefill(const lola_attn_config* cfg, const lola_paged_kv* kv,
     return e == cudaSuccess ? LOLA_OK : cuda_fail(e, "paged prompt attention");
 }
 
-int32_t lola_paged_append(const lola_attn_config* cfg, const lola_paged_kv* kv, int32_t n_tokens,
-                          const int32_t* cu_new, const lola_rows* K, const lola_rows* V, const lola_rows* Q,
-                          const lola_rows* QO, const float* inv_freq, int32_t rot, int32_t pairs,
-                          const int32_t* positions, void* stream) {
-    AppendArgs a;
-    const int32_t s = paged_check(cfg, kv, &a.p);
-    if (s != LOLA_OK) return s;
+static int32_t append(const lola_attn_config* cfg, const lola_paged_kv* kv, AppendArgs a, int32_t n_tokens,
+                      const int32_t* cu_new, const lola_rows* K, const lola_rows* V, const lola_rows* Q,
+                      const lola_rows* QO, const float* inv_freq, int32_t rot, int32_t pairs,
+                      const int32_t* positions, void* stream) {
     if (n_tokens < 0 || !aligned4(cu_new) || !aligned4(inv_freq) || !aligned4(positions)) return LOLA_ERR_INVALID_ARG;
     if (!cu_new && n_tokens != kv->n_seq) return LOLA_ERR_INVALID_ARG;
     if (!Q != !QO || (Q && !inv_freq)) return LOLA_ERR_INVALID_ARG;
@@ -814,6 +822,42 @@ int32_t lola_paged_append(const lola_attn_config* cfg, const lola_paged_kv* kv, 
     return e == cudaSuccess ? LOLA_OK : cuda_fail(e, "paged append");
 }
 
+int32_t lola_paged_append(const lola_attn_config* cfg, const lola_paged_kv* kv, int32_t n_tokens,
+                          const int32_t* cu_new, const lola_rows* K, const lola_rows* V, const lola_rows* Q,
+                          const lola_rows* QO, const float* inv_freq, int32_t rot, int32_t pairs,
+                          const int32_t* positions, void* stream) {
+    AppendArgs a;
+    const int32_t s = paged_check(cfg, kv, &a.p);
+    if (s != LOLA_OK) return s;
+    return append(cfg, kv, a, n_tokens, cu_new, K, V, Q, QO, inv_freq, rot, pairs, positions, stream);
+}
+
+int32_t lola_quant_append(const lola_attn_config* cfg, const lola_paged_kv* kv, const lola_kv_scales* scales, int32_t n_tokens,
+                          const int32_t* cu_new, const lola_rows* K, const lola_rows* V, const lola_rows* Q,
+                          const lola_rows* QO, const float* inv_freq, int32_t rot, int32_t pairs,
+                          const int32_t* positions, void* stream) {
+    AppendArgs a;
+    const int32_t s = quant_check(cfg, kv, scales, &a.p);
+    if (s != LOLA_OK) return s;
+    return append(cfg, kv, a, n_tokens, cu_new, K, V, Q, QO, inv_freq, rot, pairs, positions, stream);
+}
+
+int32_t lola_quant_read(const lola_attn_config* cfg, const lola_paged_kv* kv, const lola_kv_scales* scales, int32_t total,
+                        const lola_rows* K, const lola_rows* V, int32_t* cu, void* stream) {
+    ReadArgs a;
+    const int32_t s = quant_check(cfg, kv, scales, &a.p);
+    if (s != LOLA_OK) return s;
+    if (total < 0 || !cu || !aligned4(cu)) return LOLA_ERR_INVALID_ARG;
+    if (total > 0 && (!rows_ok(cfg, K, total, cfg->Hkv, true) || !rows_ok(cfg, V, total, cfg->Hkv, true))) return LOLA_ERR_INVALID_ARG;
+    a.total = total;
+    a.K = total > 0 ? to_rows(K) : Rows{nullptr, 0, 0};
+    a.V = total > 0 ? to_rows(V) : Rows{nullptr, 0, 0};
+    a.cu = cu;
+    cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = traced(LOLA_KERNEL_QUANT_READ, st, [&]() { return launch_quant_read(a, st); });
+    return e == cudaSuccess ? LOLA_OK : cuda_fail(e, "quantised read");
+}
+
 int32_t lola_selftest_attn_wait(int32_t block) {
     if (block < -1) return LOLA_ERR_INVALID_ARG;
     g_give_up.store(block, std::memory_order_relaxed);
@@ -825,25 +869,85 @@ int64_t lola_paged_decode_workspace_bytes(const lola_attn_config* cfg) {
     return s == LOLA_OK ? paged_decode_workspace(cfg->d) : s;
 }
 
-int32_t lola_paged_decode(const lola_attn_config* cfg, const lola_paged_kv* kv, const lola_rows* Q,
-                          const lola_rows* O, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
-    DecodeArgs a;
-    const int32_t s = paged_check(cfg, kv, &a.p);
-    if (s != LOLA_OK) return s;
+// Checks and arguments that single-token attention has in all its forms.
+static int32_t decode_args(const lola_attn_config* cfg, const lola_paged_kv* kv, const lola_rows* Q, const lola_rows* O, float* lse,
+                           void* workspace, size_t workspace_bytes, int64_t need, DecodeArgs* a) {
     if (!rows_ok(cfg, Q, kv->n_seq, cfg->Hq, false) || !rows_ok(cfg, O, kv->n_seq, cfg->Hq, true) || !aligned4(lse))
         return LOLA_ERR_INVALID_ARG;
     if (!workspace || !aligned16(workspace)) return LOLA_ERR_INVALID_ARG;
-    if ((int64_t)workspace_bytes < paged_decode_workspace(cfg->d)) return LOLA_ERR_WORKSPACE;
-    a.Q = to_rows(Q);
-    a.O = to_rows(O);
-    a.lse = lse;
-    a.part = static_cast<float*>(workspace);
-    a.scale_log2 = attn_scale_log2(cfg);
-    a.give_up = g_give_up.load(std::memory_order_relaxed);
+    if ((int64_t)workspace_bytes < need) return LOLA_ERR_WORKSPACE;
+    a->sh = Prior{};
+    a->Q = to_rows(Q);
+    a->O = to_rows(O);
+    a->lse = lse;
+    a->part = static_cast<float*>(workspace);
+    a->scale_log2 = attn_scale_log2(cfg);
+    a->give_up = g_give_up.load(std::memory_order_relaxed);
+    a->tag = call_tag();
+    return LOLA_OK;
+}
+
+int32_t lola_paged_decode(const lola_attn_config* cfg, const lola_paged_kv* kv, const lola_rows* Q,
+                          const lola_rows* O, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    DecodeArgs a;
+    int32_t s = paged_check(cfg, kv, &a.p);
+    if (s == LOLA_OK) s = decode_args(cfg, kv, Q, O, lse, workspace, workspace_bytes, paged_decode_workspace(cfg->d), &a);
+    if (s != LOLA_OK) return s;
     cudaStream_t st = (cudaStream_t)stream;
-    a.tag = call_tag();
     const cudaError_t e = traced(LOLA_KERNEL_PAGED, st, [&]() { return launch_paged_decode(a, st); });
     return e == cudaSuccess ? LOLA_OK : cuda_fail(e, "paged decode");
+}
+
+int32_t lola_quant_decode(const lola_attn_config* cfg, const lola_paged_kv* kv, const lola_kv_scales* scales, const lola_rows* Q,
+                          const lola_rows* O, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    DecodeArgs a;
+    int32_t s = quant_check(cfg, kv, scales, &a.p);
+    if (s == LOLA_OK) s = decode_args(cfg, kv, Q, O, lse, workspace, workspace_bytes, paged_decode_workspace(cfg->d), &a);
+    if (s != LOLA_OK) return s;
+    cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = traced(LOLA_KERNEL_PAGED, st, [&]() { return launch_quant_decode(a, st); });
+    return e == cudaSuccess ? LOLA_OK : cuda_fail(e, "quantised decode");
+}
+
+int64_t lola_shared_decode_workspace_bytes(const lola_attn_config* cfg, int32_t n_seq) {
+    const int32_t s = attn_check(cfg);
+    if (s != LOLA_OK) return s;
+    if (n_seq < 1) return LOLA_ERR_INVALID_ARG;
+    if ((int64_t)n_seq * cfg->Hq > kMostRows) return LOLA_ERR_UNSUPPORTED;
+    return paged_decode_workspace(cfg->d) + prior_workspace(n_seq, cfg->Hq, cfg->d, cfg->dtype, nullptr, nullptr);
+}
+
+int32_t lola_shared_decode(const lola_attn_config* cfg, const lola_paged_kv* kv, const lola_kv_scales* scales,
+                           const lola_prefixes* prefixes, const lola_rows* Q, const lola_rows* O, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+    DecodeArgs a;
+    int32_t s = scales ? quant_check(cfg, kv, scales, &a.p) : paged_check(cfg, kv, &a.p);
+    if (s != LOLA_OK) return s;
+    const lola_prefixes* x = prefixes;
+    if (!x || !x->table || !x->len || !aligned4(x->table) || !aligned4(x->len) || !aligned4(x->cu) || x->n < 1 || x->width < 1 ||
+        x->table_stride < x->width || (!x->cu && x->n != 1))
+        return LOLA_ERR_INVALID_ARG;
+    if ((int64_t)kv->n_seq * cfg->Hq > kMostRows || (int64_t)x->width * kv->page > 0x7fff0000) return LOLA_ERR_UNSUPPORTED;
+    const int64_t own = paged_decode_workspace(cfg->d);
+    s = decode_args(cfg, kv, Q, O, lse, workspace, workspace_bytes, own + prior_workspace(kv->n_seq, cfg->Hq, cfg->d, cfg->dtype, nullptr, nullptr), &a);
+    if (s != LOLA_OK) return s;
+    Prior& q = a.sh;
+    q.p = a.p;
+    q.p.n_seq = x->n;
+    q.p.width = x->width;
+    q.p.table_stride = x->table_stride;
+    q.p.table = x->table;
+    q.p.kv_len = x->len;
+    q.cu = x->cu;
+    q.n_seq = kv->n_seq;
+    prior_workspace(kv->n_seq, cfg->Hq, cfg->d, cfg->dtype, static_cast<char*>(workspace) + own, &q);
+    DecodeArgs first = a;
+    first.p = q.p;
+    cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e = traced(LOLA_KERNEL_PREFIX, st, [&]() { return scales ? launch_quant_prefix(first, st) : launch_paged_prefix(first, st); });
+    if (e != cudaSuccess) return cuda_fail(e, "shared prefix");
+    e = traced(LOLA_KERNEL_PAGED, st, [&]() { return scales ? launch_quant_decode(a, st) : launch_paged_decode(a, st); });
+    return e == cudaSuccess ? LOLA_OK : cuda_fail(e, "shared decode");
 }
 
 int32_t lola_attn_status(int32_t* host_bits, void* stream) {

@@ -69,8 +69,9 @@ const Tensor* rows(PyObject* o, lola_rows* r, const Call& c, int64_t n, int64_t 
 }
 
 // contiguous pools [n_pages, Hkv, page, d] of one shape, and what a call has for them
-bool cache(PyObject* k_pool, PyObject* v_pool, PyObject* kv_len, PyObject* table, const Call& c, lola_paged_kv* kv) {
-    const Tensor *k = get(k_pool, c.dtype, c.device), *v = get(v_pool, c.dtype, c.device), *t = get(table, at::kInt, c.device);
+bool cache(PyObject* k_pool, PyObject* v_pool, PyObject* kv_len, PyObject* table, const Call& c, lola_paged_kv* kv,
+           at::ScalarType type) {
+    const Tensor *k = get(k_pool, type, c.device), *v = get(v_pool, type, c.device), *t = get(table, at::kInt, c.device);
     if (!k || !v || !t || k->dim() != 4 || k->size(1) != c.cfg->Hkv || k->size(3) != c.cfg->d || k->sizes() != v->sizes() ||
         !k->is_contiguous() || !v->is_contiguous() || t->dim() != 2 || (t->stride(1) != 1 && t->size(1) != 1) ||
         k->size(0) > INT32_MAX || t->size(0) > INT32_MAX || t->size(1) > INT32_MAX)
@@ -86,6 +87,22 @@ bool cache(PyObject* k_pool, PyObject* v_pool, PyObject* kv_len, PyObject* table
     kv->table_stride = t->size(0) == 1 ? t->size(1) : t->stride(0);
     kv->table = (const int32_t*)t->data_ptr();
     kv->kv_len = (const int32_t*)n->data_ptr();
+    return true;
+}
+
+bool cache(PyObject* k_pool, PyObject* v_pool, PyObject* kv_len, PyObject* table, const Call& c, lola_paged_kv* kv) {
+    return cache(k_pool, v_pool, kv_len, table, c, kv, c.dtype);
+}
+// ... quantised: contiguous powers of two [n_pages, Hkv, page] beside them
+bool cache(PyObject* k_pool, PyObject* v_pool, PyObject* k_scale, PyObject* v_scale, PyObject* kv_len, PyObject* table, const Call& c,
+           lola_paged_kv* kv, lola_kv_scales* sc) {
+    if (!cache(k_pool, v_pool, kv_len, table, c, kv, at::kFloat8_e4m3fn)) return false;
+    const Tensor *k = get(k_scale, at::kFloat8_e8m0fnu, c.device), *v = get(v_scale, at::kFloat8_e8m0fnu, c.device);
+    for (const Tensor* t : {k, v})
+        if (!t || t->dim() != 3 || t->size(0) != kv->n_pages || t->size(1) != c.cfg->Hkv || t->size(2) != kv->page || !t->is_contiguous())
+            return false;
+    sc->K = k->data_ptr();
+    sc->V = v->data_ptr();
     return true;
 }
 
@@ -166,12 +183,100 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// append(layer, k_pool, v_pool, k, v, kv_len, table, cu_new | None, q | None, inv_freq | None, pairs) -> q_out
-PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+// quant_decode(layer, k_pool, v_pool, k_scale, v_scale, q, kv_len, table) -> out
+PyObject* quant_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        const auto c = n == 8 ? begin(a[0]) : std::nullopt;
+        lola_paged_kv kv;
+        lola_kv_scales sc;
+        if (!c || !cache(a[1], a[2], a[3], a[4], a[6], a[7], *c, &kv, &sc)) return decline();
+        lola_rows rq, ro;
+        const Tensor* q = rows(a[5], &rq, *c, kv.n_seq, c->cfg->Hq);
+        if (!q) return decline();
+        Tensor out = at::empty_like(*q);
+        if (!fill(out, &ro, q->size(0), c->cfg->Hq, c->cfg->d)) return decline();
+        const Tensor ws = at::empty({c->ws}, q->options().dtype(at::kByte));
+        int32_t s;
+        Py_BEGIN_ALLOW_THREADS
+        s = lola_quant_decode(c->cfg, &kv, &sc, &rq, &ro, nullptr, ws.data_ptr(), (size_t)c->ws, c->stream.stream());
+        Py_END_ALLOW_THREADS
+        return s == LOLA_OK ? THPVariable_Wrap(std::move(out)) : decline();
+    });
+}
+
+// shared(layer, k_pool, v_pool, k_scale | None, v_scale | None, q, kv_len, table, prefix_len, prefix_table, cu | None) -> out
+PyObject* shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
         const auto c = n == 11 ? begin(a[0]) : std::nullopt;
+        if (!c) return decline();
         lola_paged_kv kv;
-        if (!c || !cache(a[1], a[2], a[5], a[6], *c, &kv)) return decline();
+        lola_kv_scales sc;
+        const bool quant = a[3] != Py_None;
+        if (!(quant ? cache(a[1], a[2], a[3], a[4], a[6], a[7], *c, &kv, &sc) : cache(a[1], a[2], a[6], a[7], *c, &kv))) return decline();
+        const Tensor *t = get(a[9], at::kInt, c->device), *cu = nullptr;
+        if (!t || t->dim() != 2 || (t->stride(1) != 1 && t->size(1) != 1) || t->size(0) >= INT32_MAX || t->size(1) > INT32_MAX) return decline();
+        const Tensor* len = vec(a[8], at::kInt, c->device, t->size(0));
+        if (!len || (a[10] != Py_None && !(cu = vec(a[10], at::kInt, c->device, t->size(0) + 1)))) return decline();
+        const lola_prefixes px{(int32_t)t->size(0), (int32_t)t->size(1), t->size(0) == 1 ? t->size(1) : t->stride(0), (const int32_t*)t->data_ptr(),
+                               (const int32_t*)len->data_ptr(), cu ? (const int32_t*)cu->data_ptr() : nullptr};
+        lola_rows rq, ro;
+        const Tensor* q = rows(a[5], &rq, *c, kv.n_seq, c->cfg->Hq);
+        if (!q) return decline();
+        const int64_t size = lola_shared_decode_workspace_bytes(c->cfg, kv.n_seq);
+        if (size < 0) return decline();
+        Tensor out = at::empty_like(*q);
+        if (!fill(out, &ro, q->size(0), c->cfg->Hq, c->cfg->d)) return decline();
+        const Tensor ws = at::empty({size}, q->options().dtype(at::kByte));
+        int32_t s;
+        Py_BEGIN_ALLOW_THREADS
+        s = lola_shared_decode(c->cfg, &kv, quant ? &sc : nullptr, &px, &rq, &ro, nullptr, ws.data_ptr(), (size_t)size, c->stream.stream());
+        Py_END_ALLOW_THREADS
+        return s == LOLA_OK ? THPVariable_Wrap(std::move(out)) : decline();
+    });
+}
+
+// quant_read(layer, k_pool, v_pool, k_scale, v_scale, kv_len, table, total) -> (k, v, cu)
+PyObject* quant_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        const auto c = n == 8 ? begin(a[0]) : std::nullopt;
+        lola_paged_kv kv;
+        lola_kv_scales sc;
+        if (!c || !cache(a[1], a[2], a[3], a[4], a[5], a[6], *c, &kv, &sc)) return decline();
+        const long long total = PyLong_Check(a[7]) ? PyLong_AsLongLong(a[7]) : -1;
+        if (total < 0 || total > INT32_MAX) return decline();
+        const auto options = THPVariable_Unpack(a[1]).options();
+        Tensor k = at::empty({total, c->cfg->Hkv, c->cfg->d}, options.dtype(c->dtype)), v = at::empty_like(k);
+        Tensor cu = at::empty({(int64_t)kv.n_seq + 1}, options.dtype(at::kInt));
+        lola_rows rk, rv;
+        if (!fill(k, &rk, total, c->cfg->Hkv, c->cfg->d) || !fill(v, &rv, total, c->cfg->Hkv, c->cfg->d)) return decline();
+        int32_t s;
+        Py_BEGIN_ALLOW_THREADS
+        s = lola_quant_read(c->cfg, &kv, &sc, (int32_t)total, &rk, &rv, (int32_t*)cu.data_ptr(), c->stream.stream());
+        Py_END_ALLOW_THREADS
+        if (s != LOLA_OK) return decline();
+        PyObject* r = PyTuple_New(3);
+        if (!r) return decline();
+        PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(k)));
+        PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(std::move(v)));
+        PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(std::move(cu)));
+        return r;
+    });
+}
+
+// append(layer, k_pool, v_pool, k, v, kv_len, table, cu_new | None, q | None, inv_freq | None, pairs) -> q_out, and
+// quant_append(layer, k_pool, v_pool, k_scale, v_scale, k, ...)
+template <bool QZ> PyObject* append_to(PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        const auto c = n == (QZ ? 13 : 11) ? begin(a[0]) : std::nullopt;
+        lola_paged_kv kv;
+        [[maybe_unused]] lola_kv_scales sc;
+        if (!c) return decline();
+        if constexpr (QZ) {
+            if (!cache(a[1], a[2], a[3], a[4], a[7], a[8], *c, &kv, &sc)) return decline();
+            a += 2;                                        // (k and what follows it, by the other's numbers)
+        } else if (!cache(a[1], a[2], a[5], a[6], *c, &kv)) {
+            return decline();
+        }
         const long pairs = PyLong_AsLong(a[10]);
         if (pairs == -1 && PyErr_Occurred()) return decline();
         lola_rows rk, rv, rq, ro;
@@ -188,9 +293,13 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         }
         int32_t s;
         Py_BEGIN_ALLOW_THREADS
-        s = lola_paged_append(c->cfg, &kv, (int32_t)k->size(0), cu ? (const int32_t*)cu->data_ptr() : nullptr, &rk, &rv, q ? &rq : nullptr,
-                              q ? &ro : nullptr, freq ? (const float*)freq->data_ptr() : nullptr, freq ? (int32_t)(2 * freq->size(0)) : 0,
-                              (int32_t)pairs, nullptr, c->stream.stream());
+        auto call = [&](auto f, auto... more) {
+            return f(c->cfg, &kv, more..., (int32_t)k->size(0), cu ? (const int32_t*)cu->data_ptr() : nullptr, &rk, &rv, q ? &rq : nullptr,
+                     q ? &ro : nullptr, freq ? (const float*)freq->data_ptr() : nullptr, freq ? (int32_t)(2 * freq->size(0)) : 0,
+                     (int32_t)pairs, nullptr, c->stream.stream());
+        };
+        if constexpr (QZ) s = call(lola_quant_append, &sc);
+        else s = call(lola_paged_append);
         Py_END_ALLOW_THREADS
         if (s != LOLA_OK) return decline();
         if (q) return THPVariable_Wrap(std::move(out));
@@ -198,11 +307,18 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) { return append_to<false>(a, n); }
+PyObject* quant_append(PyObject*, PyObject* const* a, Py_ssize_t n) { return append_to<true>(a, n); }
+
 PyMethodDef methods[] = {
     {"prefill", (PyCFunction)(void (*)(void))prefill, METH_FASTCALL, nullptr},
     {"prefill_paged", (PyCFunction)(void (*)(void))prefill_paged, METH_FASTCALL, nullptr},
     {"decode", (PyCFunction)(void (*)(void))decode, METH_FASTCALL, nullptr},
     {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, nullptr},
+    {"quant_append", (PyCFunction)(void (*)(void))quant_append, METH_FASTCALL, nullptr},
+    {"quant_decode", (PyCFunction)(void (*)(void))quant_decode, METH_FASTCALL, nullptr},
+    {"quant_read", (PyCFunction)(void (*)(void))quant_read, METH_FASTCALL, nullptr},
+    {"shared", (PyCFunction)(void (*)(void))shared, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lola_py", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
