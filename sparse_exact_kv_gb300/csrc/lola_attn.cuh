@@ -278,6 +278,8 @@ struct DecodeArgs {
 cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t st);
 // Bytes of the workspace of `q`'s arrays; lays them out from `base` on, where q is given.
 int64_t prior_workspace(int n_seq, int Hq, int d, int dtype, char* base, Prior* q);
+constexpr int kPrefixRows = 256;         // rows of a record of launch_prefix_tc, column chunks one behind the other
+cudaError_t launch_prefix_tc(const DecodeArgs& a, cudaStream_t st);       // bf16 io
 cudaError_t launch_paged_prefix(const DecodeArgs& a, cudaStream_t st);
 cudaError_t launch_quant_decode(const DecodeArgs& a, cudaStream_t st);
 cudaError_t launch_quant_prefix(const DecodeArgs& a, cudaStream_t st);
@@ -294,5 +296,6 @@ cudaError_t attn_tc_status_word(int32_t** word);
 cudaError_t append_status_word(int32_t** word);
 cudaError_t paged_status_word(int32_t** word);
 cudaError_t quant_status_word(int32_t** word);
+cudaError_t prefix_status_word(int32_t** word);
 
 }  // namespace lola

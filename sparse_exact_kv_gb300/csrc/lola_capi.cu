@@ -304,20 +304,21 @@ Rows to_rows(const lola_rows* r) { return r ? Rows{static_cast<char*>(r->data), 
 // The anomaly words of the exact-attention kernels are read and cleared in one step, so that a bit that another
 // stream's kernel sets meanwhile is in this reading or left for the next one.
 struct StatusWords {
-    int32_t* word[5];
+    int32_t* word[6];
 };
 __device__ int32_t g_taken;
 __global__ void take_status_kernel(StatusWords w) {
     int32_t bits = 0;
-    for (int i = 0; i < 5; ++i) bits |= atomicExch(w.word[i], 0);
+    for (int i = 0; i < 6; ++i) bits |= atomicExch(w.word[i], 0);
     g_taken = bits;
 }
 cudaError_t take_status(int32_t* bits, cudaStream_t st) {
     static std::mutex m;                       // (one reading's bits are copied before the next one)
     std::lock_guard<std::mutex> lock(m);
     StatusWords w;
-    cudaError_t (*const find[])(int32_t**) = {attn_status_word, attn_tc_status_word, append_status_word, paged_status_word, quant_status_word};
-    for (int i = 0; i < 5; ++i) {
+    cudaError_t (*const find[])(int32_t**) = {attn_status_word, attn_tc_status_word, append_status_word, paged_status_word,
+                                                  quant_status_word, prefix_status_word};
+    for (int i = 0; i < 6; ++i) {
         const cudaError_t e = find[i](&w.word[i]);
         if (e != cudaSuccess) return e;
     }
@@ -944,7 +945,10 @@ int32_t lola_shared_decode(const lola_attn_config* cfg, const lola_paged_kv* kv,
     DecodeArgs first = a;
     first.p = q.p;
     cudaStream_t st = (cudaStream_t)stream;
-    cudaError_t e = traced(LOLA_KERNEL_PREFIX, st, [&]() { return scales ? launch_quant_prefix(first, st) : launch_paged_prefix(first, st); });
+    cudaError_t e = traced(LOLA_KERNEL_PREFIX, st, [&]() { 
+        if (cfg->dtype == LOLA_BF16) return launch_prefix_tc(first, st);
+        return scales ? launch_quant_prefix(first, st) : launch_paged_prefix(first, st);
+    });
     if (e != cudaSuccess) return cuda_fail(e, "shared prefix");
     e = traced(LOLA_KERNEL_PAGED, st, [&]() { return scales ? launch_quant_decode(a, st) : launch_paged_decode(a, st); });
     return e == cudaSuccess ? LOLA_OK : cuda_fail(e, "shared decode");

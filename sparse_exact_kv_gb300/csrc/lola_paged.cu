@@ -500,7 +500,8 @@ template <bool SH> cudaError_t launch(const DecodeArgs& a, cudaStream_t st) {
 int64_t paged_decode_workspace(int d) { return (int64_t)kPieces * kSlots * (record_floats(d) * sizeof(float) + sizeof(uint64_t)); }
 
 int64_t prior_workspace(int n_seq, int Hq, int d, int dtype, char* base, Prior* q) {
-    const int64_t n = (int64_t)n_seq * Hq, rows = kRows;
+    const bool tc = dtype == LOLA_BF16;                     // (lola_prefix.cu)
+    const int64_t n = (int64_t)n_seq * Hq, rows = tc ? kPrefixRows : kRows;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         char* x = base ? base + at : nullptr;
@@ -517,8 +518,8 @@ int64_t prior_workspace(int n_seq, int Hq, int d, int dtype, char* base, Prior* 
         q->whole = reinterpret_cast<float*>(whole);
         q->rec = reinterpret_cast<float*>(rec);
         q->rows = (int)rows;
-        q->row_step = d;
-        q->chunk_step = 4;
+        q->row_step = tc ? 4 : d;
+        q->chunk_step = tc ? 4 * kPrefixRows : 4;
     }
     return at;
 }

@@ -69,7 +69,7 @@ struct Group {
     int m0, rows;          // first sequence
     int RG, I;             // row groups per key/value head; items
 };
-template <bool SH> __device__ __forceinline__ Group group_of(const Args& a, int b, int* bits = nullptr) {
+template <bool SH, int ROWS = kRows> __device__ __forceinline__ Group group_of(const Args& a, int b, int* bits = nullptr) {
     Group g;
     if constexpr (SH) {
         int n = a.sh.n_seq, bad = 0;
@@ -77,7 +77,7 @@ template <bool SH> __device__ __forceinline__ Group group_of(const Args& a, int 
         if (a.sh.cu) seq_rows(a.sh.cu, b, a.sh.n_seq, &g.m0, &n, &bad);
         if (bits) *bits |= bad;
         g.rows = n * a.p.G;
-        g.RG = (g.rows + kRows - 1) / kRows;
+        g.RG = (g.rows + ROWS - 1) / ROWS;
         g.I = a.p.Hkv * g.RG;
     } else {
         g.m0 = b;
@@ -90,13 +90,15 @@ template <bool SH> __device__ __forceinline__ Group group_of(const Args& a, int 
 
 // Tiles of sequence b, for each of its items: at least one, so that an empty sequence's output
 // is written too.
-__device__ __forceinline__ int tiles_of(int64_t tokens) { return tokens <= 0 ? 1 : (int)((tokens + kTile - 1) / kTile); }
+template <int TILE = kTile>
+__device__ __forceinline__ int tiles_of(int64_t tokens) { return tokens <= 0 ? 1 : (int)((tokens + TILE - 1) / TILE); }
 
 // Units of sequence (or prefix) b: a prefix without tokens or sequences has none.
-template <bool SH> __device__ __forceinline__ int64_t units_of(const Args& a, int b, int* bits = nullptr) {
+template <bool SH, int TILE = kTile, int ROWS = kRows>
+__device__ __forceinline__ int64_t units_of(const Args& a, int b, int* bits = nullptr) {
     const int64_t tokens = paged_tokens(a.p, a.p.kv_len[b]);
     if (SH && tokens == 0) return 0;
-    return (int64_t)tiles_of(tokens) * group_of<SH>(a, b, bits).I;
+    return (int64_t)tiles_of<TILE>(tokens) * group_of<SH, ROWS>(a, b, bits).I;
 }
 
 // Pieces of `total` units: none is empty.
@@ -195,25 +197,26 @@ struct Start {
     int64_t total, u0, u1, rem;   // units; rem: the first unit's number inside its sequence
     int N, b;
 };
-template <bool SH> __device__ __forceinline__ bool find_start(const Args& a, Start* st) {
+template <bool SH, int NT = kThreads, int TILE = kTile, int ROWS = kRows>
+__device__ __forceinline__ bool find_start(const Args& a, Start* st) {
     const PagedArgs& p = a.p;
-    __shared__ int64_t sums[kThreads / kWarp];
+    __shared__ int64_t sums[NT / kWarp];
     __shared__ int found_b;
     __shared__ int64_t found_r;
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
     int bits = 0;
-    auto count = [&](int b) -> int64_t { return b < p.n_seq ? units_of<SH>(a, b, &bits) : 0; };
+    auto count = [&](int b) -> int64_t { return b < p.n_seq ? units_of<SH, TILE, ROWS>(a, b, &bits) : 0; };
     const int64_t own = count(threadIdx.x);            // (the whole of it up to 288 sequences)
     int64_t rest = 0;
-    for (int b = threadIdx.x + kThreads; b < p.n_seq; b += kThreads) rest += count(b);
-    st->total = block_total<kThreads>(own + rest, sums);
+    for (int b = threadIdx.x + NT; b < p.n_seq; b += NT) rest += count(b);
+    st->total = block_total<NT>(own + rest, sums);
     st->N = pieces_of(st->total);
     if (SH && bits) atomicOr(&g_status, bits);
     if ((int)blockIdx.x >= st->N) return false;
     st->u0 = split_at(st->total, st->N, blockIdx.x);
     st->u1 = split_at(st->total, st->N, blockIdx.x + 1);
     int64_t before = 0;
-    for (int base = 0; base < p.n_seq; base += kThreads) {
+    for (int base = 0; base < p.n_seq; base += NT) {
         const int64_t x = base == 0 ? own : count(base + threadIdx.x);
         int64_t inc = x;
 #pragma unroll
@@ -226,7 +229,7 @@ template <bool SH> __device__ __forceinline__ bool find_start(const Args& a, Sta
         __syncthreads();
         int64_t pre = before, all = before;
 #pragma unroll
-        for (int w = 0; w < kThreads / kWarp; ++w) {
+        for (int w = 0; w < NT / kWarp; ++w) {
             if (w < warp) pre += sums[w];
             all += sums[w];
         }

@@ -1,0 +1,602 @@
+// K12: attention of many sequences' query tokens over the prefixes that they share (bfloat16 io, tensor cores).
+//
+// The rows of a prefix and key head are the query heads of all sequences that share it: up to 256 of them are an item,
+// two tiles of 128 (MMA M = 128, TMEM lane = row), which read every block of 128 keys once:
+//   S = Q K^T,  P = 2^{c S - m},  l += sum P,  O += P V.
+// No row is masked but by the prefix' length.  The (prefix, key head, 256 rows, block) units are counted in that order
+// and cut into as many equal pieces as there are SMs, so that one prefix alone fills the GPU; a piece leaves (m, l, O) of
+// each of its segments for the kernel over the sequences' own tokens, which joins them (lola_paged.cuh).
+// An item of up to 128 rows has one tile of them: then its two halves are the even and the odd blocks, so that one half's
+// softmax runs beside the other's products, and the halves are added at the segment's end.
+// Warps: 0-3, 4-7 softmax of tile 0, 1 (one thread per row: Q rows to shared memory, S into registers, maximum, weights, P
+// into TMEM over S, at the end O out of TMEM); 8 products (one thread); 9 pages and loads, a ring of K and V blocks.
+// QZ, a quantised cache: the ring's blocks are written by warps 12-15, from e4m3 numbers and powers of two that a second
+// ring brings.  code 2^e is exact in bfloat16: an e4m3 number's exponent and fraction, shifted into place, are the
+// bfloat16 number code 2^-120, which is multiplied by 2^(e + 120).
+// m is raised lazily, as in lola_attn_tc.cu: it is set 8 above a maximum, so that no weight is above one.
+// Every wait is bounded (1 s, then LOLA_ATTN_TIMEOUT).
+#include "lola_attn_mma.cuh"
+#include "lola_paged.cuh"
+
+namespace lola {
+namespace {
+
+constexpr int kM = 128;                  // rows of a tile
+constexpr int kN = 128;                  // keys of a block
+constexpr int kItem = kPrefixRows;       // rows of an item: two tiles
+static_assert(kItem == 2 * kM, "");
+constexpr int kBad = 8;                  // blocks whose pages are remembered: more than the loader is ahead
+
+template <int D, bool QZ> struct PCfg {
+    static constexpr int kThreads = QZ ? 512 : 384;
+    static constexpr int kMmaWarp = 8, kLoadWarp = 9, kConvWarp = 12;
+    static constexpr int kTileBytes = kM * D * 2;                       // a Q tile, a K or V block
+    static constexpr int kRing = D == 128 ? (QZ ? 3 : 5) : (QZ ? 4 : 8);
+    static constexpr int kRaw = QZ ? (D == 128 ? 4 : 8) : 1;            // blocks of codes (K or V)
+    static constexpr int kRawBytes = QZ ? kN * D + kN : 0;
+    static constexpr int kSmem = (2 + kRing) * kTileBytes + kRaw * kRawBytes + 1024;
+    __device__ static constexpr uint32_t TS(int i) { return 128u * i; }  // S (P over its first half)
+    __device__ static constexpr uint32_t TO(int i) { return 256u + (uint32_t)D * i; }
+};
+
+// A segment: blocks of one item.  nb < 0: there are no more.
+struct PSeg {
+    int m0, r0, R, hk;         // first sequence of the prefix; first row of the item among the prefix' rows, rows
+    int nb, len;               // blocks; tokens from the first one on
+    int n0, blk0;              // numbers of the first stage and block, over all segments
+    int whole, k, np, rec;     // as in Seg; rec: the item's first record
+};
+
+template <int D, bool QZ>
+__global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(const __grid_constant__ Maps maps, const Args a) {
+    using C = PCfg<D, QZ>;
+    constexpr int kRing = C::kRing, kRaw = C::kRaw;
+    extern __shared__ __align__(1024) uint8_t smraw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(sm);
+    enum {
+        B_SEG = 0, B_SEGFREE = 2, B_Q = 4, B_S = 6, B_P = 8, B_O = 10, B_ML = 12, B_READ, B_DONE, B_FULL,
+        B_EMPTY = B_FULL + kRing, B_RFULL = B_EMPTY + kRing, B_REMPTY = B_RFULL + kRaw, B_N = B_REMPTY + kRaw
+    };
+    __shared__ __align__(8) uint64_t bars[B_N];
+    __shared__ PSeg segs[2];
+    __shared__ uint32_t tmem_base, bad_sm[kBad];
+    __shared__ int2 raw_sm[kRaw];            // tokens of a raw block (< 0: no more blocks), its bad boxes
+    __shared__ int abort_sm;
+    const PagedArgs& p = a.p;
+    const int tid = threadIdx.x, warp = tid / kWarp, lane = tid % kWarp;
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(B_SEG + i), 1);
+            mbar_init(bar(B_SEGFREE + i), 9);            // softmax warps, products
+            mbar_init(bar(B_Q + i), 4);
+            mbar_init(bar(B_S + i), 1);
+            mbar_init(bar(B_P + i), 4);
+            mbar_init(bar(B_O + i), 1);
+        }
+        mbar_init(bar(B_ML), 8);
+        mbar_init(bar(B_READ), 8);
+        mbar_init(bar(B_DONE), 1);
+        for (int s = 0; s < kRing; ++s) {
+            mbar_init(bar(B_FULL + s), QZ ? 4 : 1);
+            mbar_init(bar(B_EMPTY + s), 1);
+        }
+        for (int s = 0; s < kRaw; ++s) {
+            mbar_init(bar(B_RFULL + s), 1);
+            mbar_init(bar(B_REMPTY + s), 4);
+        }
+        abort_sm = 0;
+    }
+    wait_for_last_kernel();
+    Start st;
+    if (!find_start<true, C::kThreads, kN, kItem>(a, &st)) return;
+    if (warp == C::kMmaWarp) tmem_alloc<512>(smem_u32(&tmem_base));
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tb = tmem_base;
+
+    auto wait = [&](int i, uint32_t parity) -> bool { return ring_wait(bar(i), parity & 1u, &abort_sm); };
+    auto wait_all = [&](int i, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(i, parity)); };
+    auto get_seg = [&](int n, PSeg* g) -> bool {
+        if (!wait(B_SEG + (n & 1), (uint32_t)(n >> 1))) return false;
+        *g = segs[n & 1];
+        return g->nb >= 0;
+    };
+    // Blocks are loaded, and read by the products, in one order: `look` blocks of K, then by turns V of a block and K of
+    // the one `look` further on.  Stage n is the n-th of them over all segments.
+    auto stage_at = [&](int n) { return (uint32_t)(2 + n % kRing) * C::kTileBytes; };
+    auto look_of = [](const PSeg& g) { return g.R > kM ? 1 : 2; };
+
+    if (warp >= C::kMmaWarp) {
+        // (what the block was launched with, 168 a thread, given out anew; QZ: 128, which do for all)
+        if constexpr (!QZ) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == C::kLoadWarp) {
+            // ================================ pages and loads ================================
+            const int box = min(p.page, kN), lb = 31 - __clz(box), nbox = kN >> lb;     // tokens of a box, boxes of a block
+            const int half = lane >> 3, by = (lane & 7) << lb;                         // this lane's box (half: 64 channels)
+            int b = st.b, tokens = (int)paged_tokens(p, p.kv_len[b]);
+            Group gr = group_of<true, kItem>(a, b);
+            int tiles = tiles_of<kN>(tokens), item = (int)(st.rem / tiles), t0 = (int)(st.rem % tiles);
+            int64_t u = st.u0;
+            int seg = 0, n = 0, blk = 0;
+            bool ok = true;
+            uint32_t wrong = 0;
+            while (u < st.u1 && ok) {
+                const int t1 = (int)min((int64_t)tiles, t0 + (st.u1 - u)), nb = t1 - t0;
+                const int hk = item / gr.RG, r0 = (item % gr.RG) * kItem;
+                if (seg >= 2 && !(ok = wait_all(B_SEGFREE + (seg & 1), (uint32_t)(seg / 2 - 1)))) break;
+                const int look = gr.rows - r0 > kM ? 1 : 2;
+                if (lane == 0) {
+                    PSeg g;
+                    g.m0 = gr.m0;
+                    g.r0 = r0;
+                    g.R = min(kItem, gr.rows - r0);
+                    g.hk = hk;
+                    g.nb = nb;
+                    g.len = tokens - t0 * kN;
+                    g.n0 = n;
+                    g.blk0 = blk;
+                    g.whole = nb == tiles;
+                    g.k = g.np = g.rec = 0;
+                    if (!g.whole) {
+                        Seg x;
+                        place_piece(st, u - t0, tiles, &x);
+                        g.k = x.k;
+                        g.np = x.np;
+                        g.rec = 2 * x.c0 + x.s0;
+                    }
+                    segs[seg & 1] = g;
+                    if (p.kv_len[b] > tokens) wrong = 1;
+                    mbar_arrive1(bar(B_SEG + (seg & 1)));
+                }
+                ++seg;
+                // the page of this lane's box of block t, and of those that wait for their V
+                auto page_of = [&](int t) {
+                    const int pos = t * kN + by;
+                    return t < t1 && (lane & 7) < nbox && pos < tokens ? paged_page(p, b, pos) : -1;
+                };
+                int next = page_of(t0), now = -1, held[2] = {-1, -1};
+                const bool give_up = gives_up(a.give_up, blk, nb);
+                const int stop = give_up ? a.give_up - blk : nb + look;
+                for (int x = 0; x < stop && ok; ++x) {
+                    held[1] = held[0];
+                    held[0] = now;
+                    now = next;
+                    next = page_of(t0 + x + 1);
+#pragma unroll
+                    for (int kv = 1; kv >= 0; --kv) {
+                        const int t = t0 + (kv ? x - look : x);
+                        if (kv ? x < look : x >= nb) continue;
+                        const int page = kv ? (look == 1 ? held[0] : held[1]) : now, pos = t * kN + by, at = pos & (p.page - 1);
+                        const bool used = (lane & 7) < nbox && pos < tokens, bad = used && page < 0;
+                        const uint32_t bad_mask = __ballot_sync(0xffffffffu, bad) & 0xffu;
+                        if (bad_mask) wrong = 1;
+                        if constexpr (QZ) {
+                            const int r = n % kRaw, good = __popc(__ballot_sync(0xffffffffu, used) & 0xffu) - __popc(bad_mask);
+                            if (n >= kRaw && !(ok = wait_all(B_REMPTY + r, (uint32_t)(n / kRaw - 1)))) break;
+                            if (lane == 0) {
+                                if (!kv) bad_sm[blk % kBad] = bad_mask;
+                                raw_sm[r] = make_int2(min(kN, tokens - t * kN), (int)bad_mask);
+                                mbar_expect(bar(B_RFULL + r), (uint32_t)(good * box * (D + 1)));
+                            }
+                            __syncwarp();
+                            if (used && !bad && half < 2) {
+                                const int64_t row = ((int64_t)page * p.Hkv + hk) * p.page + at;
+                                const uint32_t dst = sb + (2 + kRing) * C::kTileBytes + r * C::kRawBytes;
+                                if (half == 0) bulk_load(dst + by * D, (kv ? p.V : p.K) + row * D, (uint32_t)(box * D), bar(B_RFULL + r));
+                                else bulk_load(dst + kN * D + by, (kv ? p.Vs : p.Ks) + row, (uint32_t)box, bar(B_RFULL + r));
+                            }
+                        } else {
+                            // (a box behind the prefix' tokens or on a bad page is read behind the pool's end, as zeros)
+                            const int s = n % kRing;
+                            if (n >= kRing && !(ok = wait_all(B_EMPTY + s, (uint32_t)(n / kRing - 1)))) break;
+                            if (lane == 0) {
+                                if (!kv) bad_sm[blk % kBad] = bad_mask;
+                                mbar_expect(bar(B_FULL + s), C::kTileBytes);
+                            }
+                            __syncwarp();
+                            if ((lane & 7) < nbox && half < D / 64)
+                                tma_load4(sb + stage_at(n) + 16384u * half + 128u * by, kv ? &maps.v : &maps.k, 0, at, half,
+                                          page < 0 ? p.n_pages * p.Hkv : page * p.Hkv + hk, bar(B_FULL + s));
+                        }
+                        ++n;
+                        blk += !kv;
+                    }
+                }
+                if (give_up) {
+                    if (lane == 0) *reinterpret_cast<volatile int*>(&abort_sm) = 1;
+                    ok = false;
+                }
+                u += nb;
+                t0 = 0;
+                if (++item == gr.I && u < st.u1) {
+                    item = 0;
+                    do {                                               // (units are left: there is such a prefix)
+                        ++b;
+                        tokens = (int)paged_tokens(p, p.kv_len[b]);
+                        gr = group_of<true, kItem>(a, b);
+                    } while (tokens == 0 || gr.I == 0);
+                    tiles = tiles_of<kN>(tokens);
+                }
+            }
+            // the others' end
+            if (ok && seg >= 2) ok = wait_all(B_SEGFREE + (seg & 1), (uint32_t)(seg / 2 - 1));
+            if (ok && QZ && n >= kRaw) ok = wait_all(B_REMPTY + n % kRaw, (uint32_t)(n / kRaw - 1));
+            if (lane == 0) {
+                if (ok) {
+                    segs[seg & 1].nb = -1;
+                    mbar_arrive1(bar(B_SEG + (seg & 1)));
+                }
+                // leave no copy in flight (before the end of the codes, which is one more phase of its barrier)
+                constexpr int kLast = QZ ? kRaw : kRing, kFirst = QZ ? (int)B_RFULL : (int)B_FULL;
+                for (int x = max(0, n - kLast); x < n; ++x) mbar_wait(bar(kFirst + x % kLast), (uint32_t)(x / kLast) & 1u, kWaitNs);
+                if (QZ && ok) {
+                    raw_sm[n % kRaw] = make_int2(-1, 0);
+                    mbar_arrive1(bar(B_RFULL + n % kRaw));
+                }
+                if (wrong) atomicOr(&g_status, (int)LOLA_ATTN_BAD_PAGE);
+            }
+            __syncwarp();
+        } else if (warp == C::kMmaWarp) {
+            // ================================ products ================================
+            if (lane == 0) {
+                constexpr uint32_t id_s = idesc_bf16(kM, kN, 0), id_o = idesc_bf16(kM, D, 1);
+                constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+                PSeg g;
+                bool ok = true;
+                int n = 0, np[2] = {0, 0}, nq[2] = {0, 0};             // stages; weights and Q tiles that were waited for
+                auto full = [&](int x) { return wait(B_FULL + x % kRing, (uint32_t)(x / kRing)); };
+                auto s_mma = [&](int i, int x) {
+                    const uint32_t q = desc_lo(sb + (uint32_t)i * C::kTileBytes, 16), k = desc_lo(sb + stage_at(x), 16);
+#pragma unroll
+                    for (int y = 0; y < D / 16; ++y) {
+                        const uint32_t o = (uint32_t)(y >> 2) * 1024u + (uint32_t)(y & 3) * 2u;   // 16-byte units
+                        mma_ss(tb + C::TS(i), q + o, k + o, hi, id_s, y > 0);
+                    }
+                    mma_commit(bar(B_S + i));
+                };
+                for (int seg = 0; ok && get_seg(seg, &g); ++seg) {
+                    mbar_arrive1(bar(B_SEGFREE + (seg & 1)));
+                    const bool two = g.R > kM;
+                    const int look = look_of(g);
+                    for (int x = 0; x < min(look, g.nb) && ok; ++x, ++n) {
+                        ok = full(n);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            if (ok && (two || i == x)) {
+                                ok = wait(B_Q + i, (uint32_t)nq[i]++);
+                                fence_after();
+                                if (ok) s_mma(i, n);
+                            }
+                        mma_commit(bar(B_EMPTY + n % kRing));
+                    }
+                    for (int j = 0; j < g.nb && ok; ++j) {
+                        const bool more = j + look < g.nb;
+                        ok = full(n) && (!more || full(n + 1));
+                        const uint32_t v = desc_lo(sb + stage_at(n), 16384);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            if (ok && (two || i == (j & 1))) {
+                                if (!(ok = wait(B_P + i, (uint32_t)np[i]++))) break;
+                                fence_after();
+#pragma unroll
+                                for (int y = 0; y < kN / 16; ++y)
+                                    mma_ts(tb + C::TO(i), tb + C::TS(i) + 8 * y, v + 128u * y, hi, id_o, y > 0 ? 1u : (uint32_t)(j >= look));
+                                if (more) s_mma(i, n + 1);
+                                else mma_commit(bar(B_O + i));
+                            }
+                        mma_commit(bar(B_EMPTY + n % kRing));
+                        if (more) mma_commit(bar(B_EMPTY + (n + 1) % kRing));
+                        n += 1 + more;
+                    }
+                }
+                // leave no product in flight
+                mma_commit(bar(B_DONE));
+                if (!mbar_wait(bar(B_DONE), 0, kWaitNs)) abort_sm = 1;
+            }
+            __syncwarp();
+        } else if (QZ && warp >= C::kConvWarp) {
+            // ================================ codes to bfloat16 ================================
+            const int t = tid & 127;
+            for (int n = 0;; ++n) {
+                const int r = n % kRaw, s = n % kRing;
+                if (!wait_all(B_RFULL + r, (uint32_t)(n / kRaw))) break;
+                const int2 info = raw_sm[r];
+                if (info.x < 0) break;
+                if (n >= kRing && !wait_all(B_EMPTY + s, (uint32_t)(n / kRing - 1))) break;
+                const uint8_t* raw = sm + (size_t)(2 + kRing) * C::kTileBytes + (size_t)r * C::kRawBytes;
+                uint8_t* out = sm + stage_at(n);
+                const int lb = 31 - __clz(min(p.page, kN));
+                const bool some = info.x < kN || info.y;
+                constexpr int CH = D / 16;                             // 16-byte chunks of a token's codes
+#pragma unroll 2
+                for (int x = 0; x < CH; ++x) {
+                    const int e = t + 128 * x, k = e / CH, c = e % CH;
+                    uint4 w = *reinterpret_cast<const uint4*>(raw + (size_t)e * 16);
+                    const uint32_t power = raw[kN * D + k];
+                    if (some && (k >= info.x || (info.y >> (k >> lb)) & 1)) w = make_uint4(0, 0, 0, 0);
+                    // 2^(e + 120), in two factors where it is above 2^127
+                    const uint32_t f1 = min(power + 120u, 254u) * 0x00800080u;
+                    uint32_t z[8];
+                    uint32_t nan = 0u;
+                    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        // codes 1, 3 and 0, 2 of the word: sign, exponent and fraction in a bfloat16 number's place
+                        const uint32_t lo = in[i] << 8;
+                        const uint32_t odd = ((in[i] >> 4) & 0x07f007f0u) | (in[i] & 0x80008000u);
+                        const uint32_t even = ((lo >> 4) & 0x07f007f0u) | (lo & 0x80008000u);
+                        nan |= (in[i] & 0x7f7f7f7fu) + 0x01010101u;
+                        uint32_t ye, yo;
+                        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(ye) : "r"(even), "r"(f1));
+                        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(yo) : "r"(odd), "r"(f1));
+                        z[2 * i] = ye;
+                        z[2 * i + 1] = yo;
+                    }
+                    if (power > 134u) {
+                        const uint32_t f2 = (power - 7u) * 0x00800080u;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(z[i]) : "r"(f2));
+                    }
+                    if (nan & 0x80808080u) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t m = (((in[i] & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u;   // codes that are NaN
+                            if (m & 1u) z[2 * i] |= 0x7fffu;
+                            if (m & 0x10000u) z[2 * i] |= 0x7fff0000u;
+                            if (m & 0x100u) z[2 * i + 1] |= 0x7fffu;
+                            if (m & 0x1000000u) z[2 * i + 1] |= 0x7fff0000u;
+                        }
+                    }
+                    // (codes 0, 2 and 1, 3 of a word: into order)
+                    uint4 y[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        y[i] = make_uint4(__byte_perm(z[4 * i], z[4 * i + 1], 0x5410), __byte_perm(z[4 * i], z[4 * i + 1], 0x7632),
+                                          __byte_perm(z[4 * i + 2], z[4 * i + 3], 0x5410), __byte_perm(z[4 * i + 2], z[4 * i + 3], 0x7632));
+                    uint8_t* row = out + 16384 * (c >> 2) + k * 128;
+                    const int c16 = 2 * (c & 3);
+                    const bool swap = D == 128 && (c & 4);             // (so that eight lanes' 16 bytes lie in different banks)
+                    *reinterpret_cast<uint4*>(row + (((c16 + swap) ^ k) & 7) * 16) = swap ? y[1] : y[0];
+                    *reinterpret_cast<uint4*>(row + (((c16 + !swap) ^ k) & 7) * 16) = swap ? y[0] : y[1];
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive1(bar(B_FULL + s));
+                    mbar_arrive1(bar(B_REMPTY + r));
+                }
+            }
+        }
+    } else {
+        // ================================ softmax ================================
+        if constexpr (!QZ) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int i = warp >> 2, r = (warp & 3) * 32 + lane;                    // tile, row of the tile
+        const uint32_t lo = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tb + lo + C::TS(i), to = tb + lo + C::TO(i);
+        const float c = a.scale_log2;
+        uint8_t* Qt = sm + (size_t)i * C::kTileBytes;
+        int ns = 0, no = 0, pairs = 0;                                          // blocks, segments with blocks, and with two halves
+        for (int it = 0;; ++it) {
+            PSeg g;
+            if (!__all_sync(0xffffffffu, get_seg(it, &g))) break;
+            if (lane == 0) mbar_arrive1(bar(B_SEGFREE + (it & 1)));
+            const bool two = g.R > kM, pair = !two && g.nb > 1;
+            const int n = two ? g.nb : (g.nb + 1 - i) / 2, look = look_of(g);
+            const int tile_row = two ? kM * i : 0;
+            if (n > 0) {
+                // ---- Q rows of the tile, 16 bytes a lane, into the layout that the products read ----
+                constexpr int CH = D / 8, PER = 32 / CH;                        // chunks of a row; rows at a time
+                const int ch = lane % CH;
+#pragma unroll 8
+                for (int x = 0; x < 32; x += PER) {
+                    const int rr = (warp & 3) * 32 + x + lane / CH, row = tile_row + rr;
+                    uint4 z = make_uint4(0, 0, 0, 0);
+                    if (row < g.R) {
+                        const int flat = g.r0 + row, seq = flat / p.G;
+                        z = *reinterpret_cast<const uint4*>(a.Q.data + ((int64_t)(g.m0 + seq) * a.Q.row +
+                                                                        (int64_t)(g.hk * p.G + flat - seq * p.G) * a.Q.head + 8 * ch) * 2);
+                    }
+                    *reinterpret_cast<uint4*>(Qt + 16384 * (ch >> 3) + kmaj_chunk(rr, ch & 7)) = z;
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(bar(B_Q + i));
+            }
+            float m = -INFINITY, l = 0.f;
+            bool ok = true;
+            for (int jj = 0; jj < n && ok; ++jj) {
+                const int j = two ? jj : 2 * jj + i;
+                if (!(ok = wait_all(B_S + i, (uint32_t)(ns + jj)))) break;
+                fence_after();
+                // (QZ: read twice, 32 columns at a time, as 128 registers a thread do not hold them all)
+                float s[QZ ? 32 : kN];
+                const int valid = g.len - j * kN;
+                const uint32_t bad = bad_sm[(g.blk0 + j) % kBad];
+                const bool some = valid < kN || bad;
+                const int lb = 31 - __clz(min(p.page, kN));
+                auto hide = [&](float(&z)[QZ ? 32 : kN], int x0) {
+#pragma unroll
+                    for (int x = 0; x < (QZ ? 32 : kN); ++x)
+                        if (x0 + x >= valid || (bad >> ((x0 + x) >> lb)) & 1u) z[x] = -INFINITY;
+                };
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                if constexpr (QZ) {
+#pragma unroll 1
+                    for (int x = 0; x < kN; x += 32) {
+                        tmem_ld32(ts + x, s);
+                        tmem_wait_ld();
+                        if (some) hide(s, x);
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) mx[y & 3] = fmaxf(mx[y & 3], s[y]);
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < kN; x += 32) tmem_ld32(ts + x, s + x);
+                    tmem_wait_ld();
+                    if (some) hide(s, 0);
+                    if (valid < kN) {
+                        // values behind the prefix, which may be anything, become zero (both tiles see to it)
+                        const int vs = g.n0 + j + min(g.nb, j + look);
+                        if (!(ok = wait_all(B_FULL + vs % kRing, (uint32_t)(vs / kRing)))) break;
+                        for (int x = max(valid, 0) * 8 + r; x < kN * 8; x += kM)
+#pragma unroll
+                            for (int y = 0; y < D / 64; ++y) *reinterpret_cast<uint4*>(sm + stage_at(vs) + 16384 * y + 16 * x) = make_uint4(0, 0, 0, 0);
+                        fence_async_smem();
+                    }
+#pragma unroll
+                    for (int x = 0; x < kN; ++x) mx[x & 3] = fmaxf(mx[x & 3], s[x]);
+                }
+                const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c, kRaise);
+                const bool need = top > m + kRaise;
+                if (jj == 0) {
+                    m = top;
+                } else if (__any_sync(0xffffffffu, need)) {
+                    // (O is quiet: S of this block was issued behind the tile's last P V, and is done)
+                    const float f = need ? ex2(m - top) : 1.f;
+                    l *= f;
+#pragma unroll 1
+                    for (int x = 0; x < D; x += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(to + x, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                        tmem_st16(to + x, o);
+                    }
+                    if (need) m = top;
+                }
+                const float base = m == -INFINITY ? 0.f : m;
+                float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
+#pragma unroll
+                for (int x = 0; x < kN; x += 32) {
+                    uint32_t pw[16];
+                    if constexpr (QZ) {
+                        tmem_ld32(ts + x, s);
+                        tmem_wait_ld();
+                        if (some) hide(s, x);
+                    }
+                    constexpr int kAt = QZ ? 0 : 1;
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) {
+                        float2 e = fma2(make_float2(s[kAt * x + 2 * y], s[kAt * x + 2 * y + 1]), c2, b2);
+                        e.x = ex2(e.x);
+                        e.y = ex2(e.y);
+                        ls[y & 1] = add2(ls[y & 1], e);
+                        pw[y] = pack2(e.x, e.y);
+                    }
+                    tmem_st16(ts + x / 2, pw);
+                }
+                l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+                tmem_wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(bar(B_P + i));
+            }
+            // ---- the segment's part: for the row, m, l and O ----
+            if (n > 0 && ok) ok = wait_all(B_O + i, (uint32_t)no);
+            if (!ok) break;
+            fence_after();
+            ns += n;
+            no += n > 0;
+            float f0 = 1.f, f1 = 0.f;
+            if (pair) {
+                // both halves' m and l, in the place of their Q rows
+                reinterpret_cast<float2*>(Qt)[r] = make_float2(m, l);
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(bar(B_ML));
+                if (!wait_all(B_ML, (uint32_t)pairs)) break;
+                fence_after();                                                  // (the other half's O is read here too)
+                const float2 x = reinterpret_cast<const float2*>(sm)[r], y = reinterpret_cast<const float2*>(sm + C::kTileBytes)[r];
+                m = fmaxf(x.x, y.x);
+                const float base = m == -INFINITY ? 0.f : m;
+                f0 = ex2(x.x - base);
+                f1 = ex2(y.x - base);
+                l = f0 * x.y + f1 * y.y;
+            }
+            const int row = tile_row + r, flat = g.r0 + row, seq = flat / p.G;
+            const bool mine = row < g.R && n > 0;
+            const Prior& q = a.sh;
+            const int64_t at = (int64_t)(g.m0 + seq) * p.Hq + g.hk * p.G + flat - seq * p.G;
+            float* rec = q.rec + ((int64_t)blockIdx.x * 2 + (g.k == 0 ? g.rec & 1 : 0)) * prior_record(kItem, D);
+            // (two halves: half of the columns each)
+            const int c0 = pair ? i * (D / 2) : 0, c1 = pair ? c0 + D / 2 : D;
+            if (n > 0) {
+#pragma unroll 1
+                for (int x = c0; x < c1; x += 32) {
+                    float o[32];
+                    if (pair) {
+                        float z[32];
+                        tmem_ld32(tb + lo + C::TO(0) + x, o);
+                        tmem_ld32(tb + lo + C::TO(1) + x, z);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) o[y] = fmaf(f0, o[y], f1 * z[y]);
+                    } else {
+                        tmem_ld32(to + x, o);
+                        tmem_wait_ld();
+                    }
+                    if (mine) {
+#pragma unroll
+                        for (int y = 0; y < 32; y += 4) {
+                            float* dst = g.whole ? q.whole + at * D + x + y : rec + ((x + y) / 4 * kItem + row) * 4;
+                            *reinterpret_cast<float4*>(dst) = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+                        }
+                    }
+                }
+            }
+            if (mine && c0 == 0) {
+                if (g.whole) {
+                    q.ml[at] = make_float2(m, l);
+                } else {
+                    rec[kItem * D + row] = m;
+                    rec[kItem * D + kItem + row] = l;
+                }
+                if (g.whole || g.k == 0) q.desc[at] = g.whole ? make_int4(1, 0, 0, 0) : make_int4(g.np, g.rec, row, 0);
+            }
+            fence_before();
+            if (pair) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(bar(B_READ));
+                if (!wait_all(B_READ, (uint32_t)pairs)) break;
+                ++pairs;
+            }
+        }
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (abort_sm && tid == 0) atomicOr(&g_status, (int)LOLA_ATTN_TIMEOUT);
+    if (warp == C::kMmaWarp) tmem_dealloc<512>(tb);
+}
+
+template <int D, bool QZ> cudaError_t launch_tc(const DecodeArgs& d, cudaStream_t st) {
+    using C = PCfg<D, QZ>;
+    static std::atomic<uint64_t> done{0};
+    Maps maps{};
+    if constexpr (!QZ) {
+        const int64_t depth = (int64_t)d.p.n_pages * d.p.Hkv;
+        const int rows = d.p.page < kN ? d.p.page : kN;
+        if (!make_tmap_pages(&maps.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d.p.K, D, d.p.page, depth, rows, 1) ||
+            !make_tmap_pages(&maps.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d.p.V, D, d.p.page, depth, rows, 1))
+            return cudaErrorInvalidValue;
+    }
+    cudaError_t e = opt_in_smem(prefix_tc_kernel<D, QZ>, C::kSmem, done);
+    if (e != cudaSuccess) return e;
+    return launch_behind(prefix_tc_kernel<D, QZ>, kPieces, C::kThreads, C::kSmem, st, maps, make_args(d));
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_tc(const DecodeArgs& a, cudaStream_t st) {
+    if (a.p.Ks) return a.p.d == 128 ? launch_tc<128, true>(a, st) : launch_tc<64, true>(a, st);
+    return a.p.d == 128 ? launch_tc<128, false>(a, st) : launch_tc<64, false>(a, st);
+}
+
+cudaError_t prefix_status_word(int32_t** word) { return cudaGetSymbolAddress((void**)word, g_status); }
+
+}  // namespace lola

@@ -419,7 +419,7 @@ def test_shared_lengths(L, gen, dtype, quant, d, Hq, Hkv, page, prefixes, member
 
 @pytest.mark.parametrize("dtype,quant,d,Hq,Hkv,n,members", [
     (BF, False, 128, 8, 2, 20001, 33), (BF, False, 64, 12, 2, 9000, 21), (BF, True, 128, 8, 1, 30000, 17), (BF, True, 64, 24, 4, 7000, 40),
-    (F32, False, 64, 4, 1, 6001, 9), (F32, True, 128, 4, 1, 5000, 9), (BF, False, 128, 7, 1, 3000, 150), (BF, True, 128, 20, 1, 2500, 30)])
+    (BF, True, 128, 8, 8, 30000, 34), (BF, True, 64, 32, 8, 40001, 10), (F32, False, 64, 4, 1, 6001, 9), (F32, True, 128, 4, 1, 5000, 9), (BF, False, 128, 7, 1, 3000, 150), (BF, True, 128, 20, 1, 2500, 30)])
 def test_shared_longer(L, gen, dtype, quant, d, Hq, Hkv, n, members):
     """Long prefixes, whose length is cut; rows that are no multiple of a tile's; own parts of many lengths."""
     lens = [(i * 83) % 300 for i in range(members + 3)]
