@@ -946,8 +946,11 @@ int32_t lola_shared_decode(const lola_attn_config* cfg, const lola_paged_kv* kv,
     first.p = q.p;
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e = traced(LOLA_KERNEL_PREFIX, st, [&]() { 
-        if (cfg->dtype == LOLA_BF16) return launch_prefix_tc(first, st);
-        return scales ? launch_quant_prefix(first, st) : launch_paged_prefix(first, st);
+
+        const cudaError_t r = cfg->dtype == LOLA_BF16 ? launch_prefix_tc(first, st)
+                              : scales                ? launch_quant_prefix(first, st)
+                                                      : launch_paged_prefix(first, st);
+        return r == cudaSuccess ? launch_prior_join(first, st) : r;
     });
     if (e != cudaSuccess) return cuda_fail(e, "shared prefix");
     e = traced(LOLA_KERNEL_PAGED, st, [&]() { return scales ? launch_quant_decode(a, st) : launch_paged_decode(a, st); });

@@ -490,6 +490,66 @@ cudaError_t launch_bf16(const DecodeArgs& d, cudaStream_t st) {
     return !SH && d.p.G <= 8 ? launch_kernel<__nv_bfloat16, D>(paged_decode_mma_kernel<D, true, false>, done[0], d, st)
                              : launch_kernel<__nv_bfloat16, D>(paged_decode_mma_kernel<D, false, SH>, done[1], d, st);
 }
+// ---- one part of the parts that the pieces of a prefix have left ----
+// Two rows a warp: its lanes take the rows in turn, as neighbouring rows' 16 bytes often share a sector, and first the
+// largest scores and sums of 16 pieces each, whose weights they deal out.
+template <int D>
+__global__ void __launch_bounds__(256) prior_join_kernel(const Prior q, int64_t rows) {
+    constexpr int kCols = D / 64;                                        // float4 of a lane
+    const int lane = threadIdx.x % kWarp, own = lane >> 1;
+    const int64_t i = ((int64_t)blockIdx.x * (256 / kWarp) + threadIdx.x / kWarp) * 2 + (lane & 1);
+    wait_for_last_kernel();
+    const int4 at = i < rows ? __ldcg(q.desc + i) : make_int4(0, 0, 0, 0);
+    // (rows without a prefix, or behind a kernel whose waits gave up, may hold anything)
+    const bool mine = at.x >= 2 && at.x <= kPieces && at.y >= 0 && at.y / 2 <= kPieces - at.x && at.z >= 0 && at.z < q.rows;
+    const int n = mine ? at.x : 0, most = max(n, __shfl_xor_sync(0xffffffffu, n, 1));
+    const int64_t size = prior_record(q.rows, D);
+    auto record_of = [&](int k) { return q.rec + (k == 0 ? at.y : (at.y / 2 + k) * 2) * size; };
+    float M = -INFINITY, L = 0.f;
+    float4 y[kCols];
+#pragma unroll
+    for (int x = 0; x < kCols; ++x) y[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < most; k0 += 16) {
+        float m = -INFINITY, l = 0.f;
+        if (k0 + own < n) {
+            const float* rec = record_of(k0 + own) + q.rows * D + at.z;
+            m = __ldcg(rec);
+            l = __ldcg(rec + q.rows);
+        }
+        float top = m;
+#pragma unroll
+        for (int o = 2; o < kWarp; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = fmaxf(top, M);
+        const float base = top == -INFINITY ? 0.f : top, f = ex2(M - base), w = ex2(m - base);
+        float sum = w * l;
+#pragma unroll
+        for (int o = 2; o < kWarp; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        L = fmaf(f, L, sum);
+        M = top;
+#pragma unroll
+        for (int x = 0; x < kCols; ++x) y[x] = make_float4(y[x].x * f, y[x].y * f, y[x].z * f, y[x].w * f);
+#pragma unroll 8
+        for (int k = 0; k < 16; ++k) {
+            const float wk = __shfl_sync(0xffffffffu, w, 2 * k + (lane & 1));
+            if (k0 + k < n) {
+                const float* rec = record_of(k0 + k) + at.z * q.row_step;
+#pragma unroll
+                for (int x = 0; x < kCols; ++x) {
+                    const float4 z = __ldcg(reinterpret_cast<const float4*>(rec + (own + 16 * x) * q.chunk_step));
+                    y[x].x = fmaf(wk, z.x, y[x].x);
+                    y[x].y = fmaf(wk, z.y, y[x].y);
+                    y[x].z = fmaf(wk, z.z, y[x].z);
+                    y[x].w = fmaf(wk, z.w, y[x].w);
+                }
+            }
+        }
+    }
+    if (!mine) return;
+#pragma unroll
+    for (int x = 0; x < kCols; ++x) *reinterpret_cast<float4*>(q.whole + i * D + 4 * (own + 16 * x)) = y[x];
+    if (own == 0) q.ml[i] = make_float2(M, L);
+}
+
 template <bool SH> cudaError_t launch(const DecodeArgs& a, cudaStream_t st) {
     if (a.p.dtype == LOLA_F32) return a.p.d == 128 ? launch_f32<128, SH>(a, st) : launch_f32<64, SH>(a, st);
     return a.p.d == 128 ? launch_bf16<128, SH>(a, st) : launch_bf16<64, SH>(a, st);
@@ -526,6 +586,12 @@ int64_t prior_workspace(int n_seq, int Hq, int d, int dtype, char* base, Prior* 
 
 cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t st) { return launch<false>(a, st); }
 cudaError_t launch_paged_prefix(const DecodeArgs& a, cudaStream_t st) { return launch<true>(a, st); }
+cudaError_t launch_prior_join(const DecodeArgs& a, cudaStream_t st) {
+    const int64_t rows = (int64_t)a.sh.n_seq * a.p.Hq;
+    const unsigned grid = (unsigned)((rows + 15) / 16);
+    return a.p.d == 128 ? launch_behind(prior_join_kernel<128>, grid, 256, 0, st, a.sh, rows)
+                        : launch_behind(prior_join_kernel<64>, grid, 256, 0, st, a.sh, rows);
+}
 
 cudaError_t paged_status_word(int32_t** word) { return cudaGetSymbolAddress((void**)word, g_status); }
 

@@ -399,34 +399,11 @@ __device__ __forceinline__ void add_part(float m, float l, const float4& z, floa
     y[3] = fmaf(f, y[3], f1 * z.w);
     M = top;
 }
-// The prefix' parts of row (seq, head), columns c .. c + 3, in the pieces' order.
+// The prefix' part of row i, columns c .. c + 3.
 template <int D>
 __device__ __forceinline__ void add_prior(const Prior& q, int64_t i, int c, float (&y)[4], float& M, float& L) {
-    constexpr int kBatch = 4;                                    // loads in flight
-    const int4 at = __ldcg(q.desc + i);
-    const int64_t size = prior_record(q.rows, D);
-    if (at.x == 1) {
-        const float2 ml = __ldcg(q.ml + i);
-        add_part(ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(q.whole + i * D + c)), y, M, L);
-        return;
-    }
-    // (a prefix kernel whose waits gave up may have left anything there)
-    if (at.x < 2 || at.y < 0 || at.z < 0 || at.z >= q.rows || at.x > kPieces || at.y / 2 > kPieces - at.x) return;
-    for (int x0 = 0; x0 < at.x; x0 += kBatch) {
-        float m[kBatch], l[kBatch];
-        float4 z[kBatch];
-#pragma unroll
-        for (int x = 0; x < kBatch; ++x) {
-            const int k = min(x0 + x, at.x - 1);
-            const float* rec = q.rec + (k == 0 ? at.y : (at.y / 2 + k) * 2) * size;
-            m[x] = x0 + x < at.x ? __ldcg(rec + q.rows * D + at.z) : -INFINITY;
-            l[x] = __ldcg(rec + q.rows * D + q.rows + at.z);
-            z[x] = __ldcg(reinterpret_cast<const float4*>(rec + at.z * q.row_step + c / 4 * q.chunk_step));
-        }
-#pragma unroll
-        for (int x = 0; x < kBatch; ++x) 
-            if (x0 + x < at.x) add_part(m[x], l[x], z[x], y, M, L);
-    }
+    const float2 ml = __ldcg(q.ml + i);
+    add_part(ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(q.whole + i * D + c)), y, M, L);
 }
 
 // Where a segment that is a piece of its item leaves its part.

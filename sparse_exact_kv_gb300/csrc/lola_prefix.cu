@@ -10,12 +10,17 @@
 // softmax runs beside the other's products, and the halves are added at the segment's end.
 // Warps: 0-3, 4-7 softmax of tile 0, 1 (one thread per row: Q rows to shared memory, S into registers, maximum, weights, P
 // into TMEM over S, at the end O out of TMEM); 8 products (one thread); 9 pages and loads, a ring of K and V blocks.
-// QZ, a quantised cache: the ring's blocks are written by warps 12-15, from e4m3 numbers and powers of two that a second
-// ring brings.  code 2^e is exact in bfloat16: an e4m3 number's exponent and fraction, shifted into place, are the
-// bfloat16 number code 2^-120, which is multiplied by 2^(e + 120).
+// QZ, a quantised cache: the ring's blocks are written by warps 12-15, as float16 numbers code 2^(e - E), from e4m3 numbers
+// and powers of two that a second ring brings; E is the block's largest power, of its keys or of its values (numbers 2^-33
+// and less of the largest one that these may hold round or vanish: as small against the block's scores, or outputs, as
+// float32's own rounding).  A key's 2^E is a factor of the scores, a value's joins the weights' exponent, as in
+// lola_quant.cu, from where the rows of Q with powers of two of their own and the weights times 2^15 come too.
+// (Blocks of bfloat16 numbers code 2^e, by shifts, two products a pair and a look for NaN, took the four warps 3.4 us for
+// K and V.)
 // m is raised lazily, as in lola_attn_tc.cu: it is set 8 above a maximum, so that no weight is above one.
 // Every wait is bounded (1 s, then LOLA_ATTN_TIMEOUT).
 #include "lola_attn_mma.cuh"
+#include "lola_codes.cuh"
 #include "lola_paged.cuh"
 
 namespace lola {
@@ -25,7 +30,8 @@ constexpr int kM = 128;                  // rows of a tile
 constexpr int kN = 128;                  // keys of a block
 constexpr int kItem = kPrefixRows;       // rows of an item: two tiles
 static_assert(kItem == 2 * kM, "");
-constexpr int kBad = 8;                  // blocks whose pages are remembered: more than the loader is ahead
+constexpr int kBad = 8;                  // blocks whose pages and powers are remembered: more than the loader is ahead
+constexpr float kWeightBits = 15.f;      // QZ: weights are kept times kUp
 
 template <int D, bool QZ> struct PCfg {
     static constexpr int kThreads = QZ ? 512 : 384;
@@ -33,7 +39,7 @@ template <int D, bool QZ> struct PCfg {
     static constexpr int kTileBytes = kM * D * 2;                       // a Q tile, a K or V block
     static constexpr int kRing = D == 128 ? (QZ ? 3 : 5) : (QZ ? 4 : 8);
     static constexpr int kRaw = QZ ? (D == 128 ? 4 : 8) : 1;            // blocks of codes (K or V)
-    static constexpr int kRawBytes = QZ ? kN * D + kN : 0;
+    static constexpr int kRawBytes = QZ ? kN * D + 2 * kN : 0;         // codes, their powers, behind keys the values' powers too
     static constexpr int kSmem = (2 + kRing) * kTileBytes + kRaw * kRawBytes + 1024;
     __device__ static constexpr uint32_t TS(int i) { return 128u * i; }  // S (P over its first half)
     __device__ static constexpr uint32_t TO(int i) { return 256u + (uint32_t)D * i; }
@@ -61,7 +67,8 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
     __shared__ __align__(8) uint64_t bars[B_N];
     __shared__ PSeg segs[2];
     __shared__ uint32_t tmem_base, bad_sm[kBad];
-    __shared__ int2 raw_sm[kRaw];            // tokens of a raw block (< 0: no more blocks), its bad boxes
+    __shared__ uint32_t power_sm[kBad];      // QZ: the largest powers of a block's keys and values (biased; in the second byte)
+    __shared__ int4 raw_sm[kRaw];            // of a raw block: tokens (< 0: no more blocks), bad boxes, the block's number (>= 0: keys)
     __shared__ int abort_sm;
     const PagedArgs& p = a.p;
     const int tid = threadIdx.x, warp = tid / kWarp, lane = tid % kWarp;
@@ -178,15 +185,15 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
                             if (n >= kRaw && !(ok = wait_all(B_REMPTY + r, (uint32_t)(n / kRaw - 1)))) break;
                             if (lane == 0) {
                                 if (!kv) bad_sm[blk % kBad] = bad_mask;
-                                raw_sm[r] = make_int2(min(kN, tokens - t * kN), (int)bad_mask);
-                                mbar_expect(bar(B_RFULL + r), (uint32_t)(good * box * (D + 1)));
+                                raw_sm[r] = make_int4(min(kN, tokens - t * kN), (int)bad_mask, (kv ? t - t0 : blk), kv);
+                                mbar_expect(bar(B_RFULL + r), (uint32_t)(good * box * (D + 1 + !kv)));
                             }
                             __syncwarp();
-                            if (used && !bad && half < 2) {
+                            if (used && !bad && half < 3 - kv) {
                                 const int64_t row = ((int64_t)page * p.Hkv + hk) * p.page + at;
                                 const uint32_t dst = sb + (2 + kRing) * C::kTileBytes + r * C::kRawBytes;
                                 if (half == 0) bulk_load(dst + by * D, (kv ? p.V : p.K) + row * D, (uint32_t)(box * D), bar(B_RFULL + r));
-                                else bulk_load(dst + kN * D + by, (kv ? p.Vs : p.Ks) + row, (uint32_t)box, bar(B_RFULL + r));
+                                else bulk_load(dst + kN * (D + half - 1) + by, (kv || half == 2 ? p.Vs : p.Ks) + row, (uint32_t)box, bar(B_RFULL + r));
                             }
                         } else {
                             // (a box behind the prefix' tokens or on a bad page is read behind the pool's end, as zeros)
@@ -233,7 +240,7 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
                 constexpr int kLast = QZ ? kRaw : kRing, kFirst = QZ ? (int)B_RFULL : (int)B_FULL;
                 for (int x = max(0, n - kLast); x < n; ++x) mbar_wait(bar(kFirst + x % kLast), (uint32_t)(x / kLast) & 1u, kWaitNs);
                 if (QZ && ok) {
-                    raw_sm[n % kRaw] = make_int2(-1, 0);
+                    raw_sm[n % kRaw] = make_int4(-1, 0, 0, 0);
                     mbar_arrive1(bar(B_RFULL + n % kRaw));
                 }
                 if (wrong) atomicOr(&g_status, (int)LOLA_ATTN_BAD_PAGE);
@@ -242,7 +249,9 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
         } else if (warp == C::kMmaWarp) {
             // ================================ products ================================
             if (lane == 0) {
-                constexpr uint32_t id_s = idesc_bf16(kM, kN, 0), id_o = idesc_bf16(kM, D, 1);
+                // (QZ: float16 operands)
+                constexpr uint32_t kind = QZ ? ~((1u << 7) | (1u << 10)) : ~0u;
+                constexpr uint32_t id_s = idesc_bf16(kM, kN, 0) & kind, id_o = idesc_bf16(kM, D, 1) & kind;
                 constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
                 PSeg g;
                 bool ok = true;
@@ -303,59 +312,51 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
             for (int n = 0;; ++n) {
                 const int r = n % kRaw, s = n % kRing;
                 if (!wait_all(B_RFULL + r, (uint32_t)(n / kRaw))) break;
-                const int2 info = raw_sm[r];
+                const int4 info = raw_sm[r];
                 if (info.x < 0) break;
                 if (n >= kRing && !wait_all(B_EMPTY + s, (uint32_t)(n / kRing - 1))) break;
                 const uint8_t* raw = sm + (size_t)(2 + kRing) * C::kTileBytes + (size_t)r * C::kRawBytes;
                 uint8_t* out = sm + stage_at(n);
                 const int lb = 31 - __clz(min(p.page, kN));
                 const bool some = info.x < kN || info.y;
+                auto hidden = [&](int k) { return some && (k >= info.x || (info.y >> (k >> lb)) & 1); };
+                // the largest of 128 powers, of tokens that are seen
+                auto largest = [&](const uint8_t* powers) {
+                    uint32_t w = *reinterpret_cast<const uint32_t*>(powers + 4 * lane);
+                    if (some) {
+                        const int left = info.x - 4 * lane;
+                        if (hidden(4 * lane)) w = 0;
+                        else if (left < 4) w &= (1u << (8 * left)) - 1u;
+                    }
+                    return __reduce_max_sync(0xffffffffu, max(max(w & 255u, (w >> 8) & 255u), max((w >> 16) & 255u, w >> 24)));
+                };
+                const uint32_t E = largest(raw + kN * D);
+                if (!info.w) {
+                    const uint32_t F = largest(raw + kN * (D + 1));
+                    if (t == 0) power_sm[info.z % kBad] = E | F << 8;
+                }
                 constexpr int CH = D / 16;                             // 16-byte chunks of a token's codes
-#pragma unroll 2
+#pragma unroll 4
                 for (int x = 0; x < CH; ++x) {
                     const int e = t + 128 * x, k = e / CH, c = e % CH;
                     uint4 w = *reinterpret_cast<const uint4*>(raw + (size_t)e * 16);
-                    const uint32_t power = raw[kN * D + k];
-                    if (some && (k >= info.x || (info.y >> (k >> lb)) & 1)) w = make_uint4(0, 0, 0, 0);
-                    // 2^(e + 120), in two factors where it is above 2^127
-                    const uint32_t f1 = min(power + 120u, 254u) * 0x00800080u;
-                    uint32_t z[8];
-                    uint32_t nan = 0u;
+                    if (hidden(k)) w = make_uint4(0, 0, 0, 0);
+                    // 2^(e - E) in float16: down to 2^-14, then to 2^-24, then none
+                    const int down = max(0, (int)E - (int)raw[kN * D + k]);
+                    const uint32_t f = (down < 15 ? (15u - down) << 10 : down < 25 ? 1u << (24 - down) : 0u) * 0x10001u;
+                    uint4 y[2];
                     const uint32_t in[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        // codes 1, 3 and 0, 2 of the word: sign, exponent and fraction in a bfloat16 number's place
-                        const uint32_t lo = in[i] << 8;
-                        const uint32_t odd = ((in[i] >> 4) & 0x07f007f0u) | (in[i] & 0x80008000u);
-                        const uint32_t even = ((lo >> 4) & 0x07f007f0u) | (lo & 0x80008000u);
-                        nan |= (in[i] & 0x7f7f7f7fu) + 0x01010101u;
-                        uint32_t ye, yo;
-                        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(ye) : "r"(even), "r"(f1));
-                        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(yo) : "r"(odd), "r"(f1));
-                        z[2 * i] = ye;
-                        z[2 * i + 1] = yo;
+                        uint32_t lo, hi;
+                        widen(in[i], lo, hi);
+                        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(lo), "r"(f));
+                        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(hi), "r"(f));
+                        if (i == 0) y[0].x = lo, y[0].y = hi;
+                        if (i == 1) y[0].z = lo, y[0].w = hi;
+                        if (i == 2) y[1].x = lo, y[1].y = hi;
+                        if (i == 3) y[1].z = lo, y[1].w = hi;
                     }
-                    if (power > 134u) {
-                        const uint32_t f2 = (power - 7u) * 0x00800080u;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(z[i]) : "r"(f2));
-                    }
-                    if (nan & 0x80808080u) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t m = (((in[i] & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u;   // codes that are NaN
-                            if (m & 1u) z[2 * i] |= 0x7fffu;
-                            if (m & 0x10000u) z[2 * i] |= 0x7fff0000u;
-                            if (m & 0x100u) z[2 * i + 1] |= 0x7fffu;
-                            if (m & 0x1000000u) z[2 * i + 1] |= 0x7fff0000u;
-                        }
-                    }
-                    // (codes 0, 2 and 1, 3 of a word: into order)
-                    uint4 y[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        y[i] = make_uint4(__byte_perm(z[4 * i], z[4 * i + 1], 0x5410), __byte_perm(z[4 * i], z[4 * i + 1], 0x7632),
-                                          __byte_perm(z[4 * i + 2], z[4 * i + 3], 0x5410), __byte_perm(z[4 * i + 2], z[4 * i + 3], 0x7632));
                     uint8_t* row = out + 16384 * (c >> 2) + k * 128;
                     const int c16 = 2 * (c & 3);
                     const bool swap = D == 128 && (c & 4);             // (so that eight lanes' 16 bytes lie in different banks)
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
         const int i = warp >> 2, r = (warp & 3) * 32 + lane;                    // tile, row of the tile
         const uint32_t lo = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tb + lo + C::TS(i), to = tb + lo + C::TO(i);
-        const float c = a.scale_log2;
+        float c = a.scale_log2;                                                 // (QZ: with the power of two of the row of Q)
         uint8_t* Qt = sm + (size_t)i * C::kTileBytes;
         int ns = 0, no = 0, pairs = 0;                                          // blocks, segments with blocks, and with two halves
         for (int it = 0;; ++it) {
@@ -388,18 +389,41 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
             const int tile_row = two ? kM * i : 0;
             if (n > 0) {
                 // ---- Q rows of the tile, 16 bytes a lane, into the layout that the products read ----
-                constexpr int CH = D / 8, PER = 32 / CH;                        // chunks of a row; rows at a time
+                constexpr int CH = D / 8, PER = 32 / CH, kBatch = 8;            // chunks of a row; rows at a time; times in flight
                 const int ch = lane % CH;
-#pragma unroll 8
-                for (int x = 0; x < 32; x += PER) {
-                    const int rr = (warp & 3) * 32 + x + lane / CH, row = tile_row + rr;
-                    uint4 z = make_uint4(0, 0, 0, 0);
-                    if (row < g.R) {
-                        const int flat = g.r0 + row, seq = flat / p.G;
-                        z = *reinterpret_cast<const uint4*>(a.Q.data + ((int64_t)(g.m0 + seq) * a.Q.row +
-                                                                        (int64_t)(g.hk * p.G + flat - seq * p.G) * a.Q.head + 8 * ch) * 2);
+                for (int x0 = 0; x0 < 32; x0 += PER * kBatch) {
+                    uint4 z[kBatch];
+#pragma unroll
+                    for (int x = 0; x < kBatch; ++x) {
+                        const int row = tile_row + (warp & 3) * 32 + x0 + x * PER + lane / CH;
+                        z[x] = make_uint4(0, 0, 0, 0);
+                        if (row < g.R) {
+                            const int flat = g.r0 + row, seq = flat / p.G;
+                            z[x] = *reinterpret_cast<const uint4*>(a.Q.data + ((int64_t)(g.m0 + seq) * a.Q.row +
+                                                                               (int64_t)(g.hk * p.G + flat - seq * p.G) * a.Q.head + 8 * ch) * 2);
+                        }
                     }
-                    *reinterpret_cast<uint4*>(Qt + 16384 * (ch >> 3) + kmaj_chunk(rr, ch & 7)) = z;
+#pragma unroll
+                    for (int x = 0; x < kBatch; ++x) {
+                        const int rr = (warp & 3) * 32 + x0 + x * PER + lane / CH;
+                        if constexpr (QZ) {
+                            // float16 numbers, the row's largest magnitude in [2^14, 2^15)
+                            uint32_t w[4] = {z[x].x, z[x].y, z[x].z, z[x].w}, big = 0u;
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) big = max(big, max((w[y] << 16) & 0x7fff0000u, w[y] & 0x7fff0000u));
+#pragma unroll
+                            for (int o = 1; o < CH; o <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+                            const uint32_t up = min(268u - (big >> 23), 240u);
+                            const float f = __uint_as_float(up << 23);
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) w[y] = half2_of(__uint_as_float(w[y] << 16) * f, __uint_as_float(w[y] & 0xffff0000u) * f);
+                            z[x] = make_uint4(w[0], w[1], w[2], w[3]);
+                            const int at = x0 + x * PER;                        // this time's first row of the warp's 32
+                            const uint32_t mine = __shfl_sync(0xffffffffu, up, ((lane - at) * CH) & 31);
+                            if (lane >= at && lane < at + PER) c = a.scale_log2 * __uint_as_float((254u - mine) << 23);
+                        }
+                        *reinterpret_cast<uint4*>(Qt + 16384 * (ch >> 3) + kmaj_chunk(rr, ch & 7)) = z[x];
+                    }
                 }
                 fence_async_smem();
                 __syncwarp();
@@ -449,7 +473,16 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
 #pragma unroll
                     for (int x = 0; x < kN; ++x) mx[x & 3] = fmaxf(mx[x & 3], s[x]);
                 }
-                const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c, kRaise);
+                // the scores' factor, and what their weights' exponents have besides
+                float cb = c, add = 0.f;
+                [[maybe_unused]] uint32_t F = 127u;
+                if constexpr (QZ) {
+                    const uint32_t powers = power_sm[(g.blk0 + j) % kBad];
+                    F = powers >> 8;
+                    cb = fmaxf(c * __uint_as_float((powers & 255u) << 23), 1.2e-38f);     // (0 would make NaN of hidden scores)
+                    add = (float)(int)F - 127.f;
+                }
+                const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), cb, add + kRaise);
                 const bool need = top > m + kRaise;
                 if (jj == 0) {
                     m = top;
@@ -470,7 +503,8 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
                 }
                 const float base = m == -INFINITY ? 0.f : m;
                 float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
+                const float off = QZ ? add + kWeightBits - base : -base;
+                const float2 c2 = make_float2(cb, cb), b2 = make_float2(off, off);
 #pragma unroll
                 for (int x = 0; x < kN; x += 32) {
                     uint32_t pw[16];
@@ -486,11 +520,12 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
                         e.x = ex2(e.x);
                         e.y = ex2(e.y);
                         ls[y & 1] = add2(ls[y & 1], e);
-                        pw[y] = pack2(e.x, e.y);
+                        pw[y] = QZ ? half2_of(e.x, e.y) : pack2(e.x, e.y);
                     }
                     tmem_st16(ts + x / 2, pw);
                 }
-                l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+                const float sum = (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+                l = QZ ? fmaf(sum, power_down(F) * (1.f / kUp), l) : l + sum;
                 tmem_wait_st();
                 fence_before();
                 __syncwarp();
@@ -502,7 +537,8 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
             fence_after();
             ns += n;
             no += n > 0;
-            float f0 = 1.f, f1 = 0.f;
+            constexpr float kDown = QZ ? 1.f / kUp : 1.f;
+            float f0 = kDown, f1 = 0.f;
             if (pair) {
                 // both halves' m and l, in the place of their Q rows
                 reinterpret_cast<float2*>(Qt)[r] = make_float2(m, l);
@@ -517,6 +553,8 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
                 f0 = ex2(x.x - base);
                 f1 = ex2(y.x - base);
                 l = f0 * x.y + f1 * y.y;
+                f0 *= kDown;
+                f1 *= kDown;
             }
             const int row = tile_row + r, flat = g.r0 + row, seq = flat / p.G;
             const bool mine = row < g.R && n > 0;
@@ -539,6 +577,10 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
                     } else {
                         tmem_ld32(to + x, o);
                         tmem_wait_ld();
+                        if (QZ) {
+#pragma unroll
+                            for (int y = 0; y < 32; ++y) o[y] *= f0;
+                        }
                     }
                     if (mine) {
 #pragma unroll

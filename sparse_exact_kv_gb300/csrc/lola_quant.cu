@@ -14,39 +14,23 @@
 // float16 numbers of 2^15 w_j (rounded by 2^-12 of themselves, or by 2^-40 where they are small; float32 io: two parts).
 // The contraction's channels may come in any order: a lane's four neighbouring codes of K, one word, are its four
 // channels of a product, and the same four of q.  A word of V holds two channels of two tokens and is permuted first.
+#include "lola_codes.cuh"
 #include "lola_paged.cuh"
-
-#include <cuda_fp16.h>
 
 namespace lola {
 namespace {
 
-// four e4m3 numbers as float16 numbers
-__device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}\n"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-}
 __device__ __forceinline__ void mma16816_h(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t half2_of(float x, float y) {
-    const __half2 h = __floats2half2_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
 // what the float16 numbers of x and y leave
 __device__ __forceinline__ uint32_t half2_rest(float x, float y, uint32_t h) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
     return half2_of(x - f.x, y - f.y);
 }
-// 2^(127 - b) for a byte b < 255 (2^-127, of b = 254, is no normal number)
-__device__ __forceinline__ float power_down(uint32_t b) { return __uint_as_float(b < 254u ? (254u - b) << 23 : 0x400000u); }
-
-constexpr float kUp = 32768.f;            // the weights' factor
-
 template <typename TO, int D, bool HALF> struct QSmem {
     static constexpr int NW = kCons / kWarp;
     static constexpr int HR = HALF ? 1 : 2, R8 = 8 * HR, CK = 512 / R8;     // rows kept; columns joined at a time
