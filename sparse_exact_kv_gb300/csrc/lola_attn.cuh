@@ -127,11 +127,21 @@ __device__ __forceinline__ int prior_of(const Prior& q, int b, int lane) {
     return paged_tokens(q.p, q.p.kv_len[g]) > 0 ? g : -1;
 }
 
-// Piece c of n equal pieces of `total` units: [split_at(c), split_at(c + 1))
-__host__ __device__ inline int64_t split_at(int64_t total, int n, int c) { return total * c / n; }
+// Piece c of n equal pieces of `total` units: [split_at(c), split_at(c + 1)).  (Divisions of 64 bits take hundreds of
+// clocks, and a kernel begins with half a dozen of them: 32 bits where they do.)
+__host__ __device__ inline int64_t split_at(int64_t total, int n, int c) {
+    const int64_t x = total * c;
+    return x >> 32 ? x / n : (int64_t)((uint32_t)x / (uint32_t)n);
+}
+__host__ __device__ inline int divide(int64_t x, int by, int* rest) {
+    const int q = x >> 32 ? (int)(x / by) : (int)((uint32_t)x / (uint32_t)by);
+    *rest = (int)(x - (int64_t)q * by);
+    return q;
+}
 // the piece that holds unit u < total
 __host__ __device__ inline int split_of(int64_t total, int n, int64_t u) {
-    int c = (int)(u * n / total);
+    const int64_t x = u * n;
+    int c = (x | total) >> 32 ? (int)(x / total) : (int)((uint32_t)x / (uint32_t)total);
     while (c + 1 < n && split_at(total, n, c + 1) <= u) ++c;
     while (c > 0 && split_at(total, n, c) > u) --c;
     return c;

@@ -271,7 +271,7 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
     int lens_b = b;                                               // the lanes hold 32 sequences' lengths
     int lens = b + lane < p.n_seq ? p.kv_len[b + lane] : 0;
     int64_t tokens = paged_tokens(p, __shfl_sync(0xffffffffu, lens, 0));
-    int tiles = tiles_of(tokens), item = (int)(st.rem / tiles), t0 = (int)(st.rem % tiles);
+    int tiles = tiles_of(tokens), t0, item = divide(st.rem, tiles, &t0);
     int64_t u = st.u0;
     int n = 0, i = 0, held_b = -1, held = -1;
     int held_c = 0;                                           // ... and 32 page-table columns of held_b
@@ -546,7 +546,7 @@ __device__ void join_pieces(const Args& a, const Seg& g, int t, int* go, int* ar
 // The end of a CTA whose waits gave up (all threads, after all roles): no copy is left in flight, and its pieces
 // that were not counted are, so that every cell of the call ends at 0 (what the joins then make of their records
 // is as invalid as the call).
-template <int D, int S, int NS, bool SH, typename B>
+template <int D, int S, int NS, bool SH, int NT = kThreads, typename B>
 __device__ __noinline__ void settle(const Args& a, B& bars) {
     if (threadIdx.x == 0) {
         const int n = bars.issued, i = bars.given;
@@ -555,7 +555,7 @@ __device__ __noinline__ void settle(const Args& a, B& bars) {
     }
     if constexpr (SH) return;                                      // (nothing is counted)
     Start st;
-    if (!find_start<false>(a, &st) || threadIdx.x != 0) return;
+    if (!find_start<false, NT>(a, &st) || threadIdx.x != 0) return;
     int b = st.b, tiles = tiles_of(paged_tokens(a.p, a.p.kv_len[b]));
     int item = (int)(st.rem / tiles), t0 = (int)(st.rem % tiles);
     for (int64_t u = st.u0; u < st.u1;) {
@@ -613,7 +613,7 @@ inline Args make_args(const DecodeArgs& d) {
 }
 
 template <typename T, int D, typename K>
-cudaError_t launch_kernel(K kernel, std::atomic<uint64_t>& done, const DecodeArgs& d, cudaStream_t st) {
+cudaError_t launch_kernel(K kernel, int consumers, std::atomic<uint64_t>& done, const DecodeArgs& d, cudaStream_t st) {
     using C = Cfg<T, D>;
     Maps maps;
     const auto ty = sizeof(T) == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
@@ -628,7 +628,7 @@ cudaError_t launch_kernel(K kernel, std::atomic<uint64_t>& done, const DecodeArg
         return cudaErrorInvalidValue;
     cudaError_t e = opt_in_smem(kernel, C::kSmem, done);
     if (e != cudaSuccess) return e;
-    return launch_behind(kernel, kPieces, kThreads, C::kSmem, st, maps, make_args(d));
+    return launch_behind(kernel, kPieces, (consumers + 1) * kWarp, C::kSmem, st, maps, make_args(d));
 }
 
 }  // namespace

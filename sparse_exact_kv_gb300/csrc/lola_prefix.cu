@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
             const int half = lane >> 3, by = (lane & 7) << lb;                         // this lane's box (half: 64 channels)
             int b = st.b, tokens = (int)paged_tokens(p, p.kv_len[b]);
             Group gr = group_of<true, kItem>(a, b);
-            int tiles = tiles_of<kN>(tokens), item = (int)(st.rem / tiles), t0 = (int)(st.rem % tiles);
+            int tiles = tiles_of<kN>(tokens), t0, item = divide(st.rem, tiles, &t0);
             int64_t u = st.u0;
             int seg = 0, n = 0, blk = 0;
             bool ok = true;
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
                 uint8_t* out = sm + stage_at(n);
                 const int lb = 31 - __clz(min(p.page, kN));
                 const bool some = info.x < kN || info.y;
-                auto hidden = [&](int k) { return some && (k >= info.x || (info.y >> (k >> lb)) & 1); };
+                auto hidden = [&](int k) { return k >= info.x || (info.y >> (k >> lb)) & 1; };
                 // the largest of 128 powers, of tokens that are seen
                 auto largest = [&](const uint8_t* powers) {
                     uint32_t w = *reinterpret_cast<const uint32_t*>(powers + 4 * lane);
@@ -335,33 +335,40 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
                     const uint32_t F = largest(raw + kN * (D + 1));
                     if (t == 0) power_sm[info.z % kBad] = E | F << 8;
                 }
-                constexpr int CH = D / 16;                             // 16-byte chunks of a token's codes
-#pragma unroll 4
-                for (int x = 0; x < CH; ++x) {
-                    const int e = t + 128 * x, k = e / CH, c = e % CH;
-                    uint4 w = *reinterpret_cast<const uint4*>(raw + (size_t)e * 16);
-                    if (hidden(k)) w = make_uint4(0, 0, 0, 0);
-                    // 2^(e - E) in float16: down to 2^-14, then to 2^-24, then none
-                    const int down = max(0, (int)E - (int)raw[kN * D + k]);
-                    const uint32_t f = (down < 15 ? (15u - down) << 10 : down < 25 ? 1u << (24 - down) : 0u) * 0x10001u;
-                    uint4 y[2];
-                    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+                // 16 codes a thread: CH such chunks a token, a warp takes PT tokens of every 128 / CH.  Each lane finds one
+                // token's factor, 2^(e - E) in float16: down to 2^-14, then to 2^-24, then none.  (Loads before stores, which
+                // might be the same place for all the compiler knows: a block took one warp a scheduler 1190 clocks, now 560.)
+                constexpr int CH = D / 16, PT = 32 / CH, kBatch = 4;
+                const int own = 128 / CH * (lane / PT) + PT * (warp & 3) + lane % PT;
+                const int down = max(0, (int)E - (int)raw[kN * D + own]);
+                const uint32_t factor = (down < 15 ? (15u - down) << 10 : down < 25 ? 1u << (24 - down) : 0u) * 0x10001u;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t lo, hi;
-                        widen(in[i], lo, hi);
-                        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(lo), "r"(f));
-                        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(hi), "r"(f));
-                        if (i == 0) y[0].x = lo, y[0].y = hi;
-                        if (i == 1) y[0].z = lo, y[0].w = hi;
-                        if (i == 2) y[1].x = lo, y[1].y = hi;
-                        if (i == 3) y[1].z = lo, y[1].w = hi;
+                for (int x0 = 0; x0 < CH; x0 += kBatch) {
+                    uint4 w[kBatch];
+#pragma unroll
+                    for (int x = 0; x < kBatch; ++x) {
+                        w[x] = *reinterpret_cast<const uint4*>(raw + (size_t)(t + 128 * (x0 + x)) * 16);
+                        if (some && hidden((t + 128 * (x0 + x)) / CH)) w[x] = make_uint4(0, 0, 0, 0);
                     }
-                    uint8_t* row = out + 16384 * (c >> 2) + k * 128;
-                    const int c16 = 2 * (c & 3);
-                    const bool swap = D == 128 && (c & 4);             // (so that eight lanes' 16 bytes lie in different banks)
-                    *reinterpret_cast<uint4*>(row + (((c16 + swap) ^ k) & 7) * 16) = swap ? y[1] : y[0];
-                    *reinterpret_cast<uint4*>(row + (((c16 + !swap) ^ k) & 7) * 16) = swap ? y[0] : y[1];
+#pragma unroll
+                    for (int x = 0; x < kBatch; ++x) {
+                        const int e = t + 128 * (x0 + x), k = e / CH, c = e % CH;
+                        const uint32_t f = __shfl_sync(0xffffffffu, factor, PT * (x0 + x) + lane / CH);
+                        const uint32_t in[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+                        uint32_t z[8];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            widen(in[i], z[2 * i], z[2 * i + 1]);
+                            asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(z[2 * i]) : "r"(f));
+                            asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(z[2 * i + 1]) : "r"(f));
+                        }
+                        const uint4 y0 = make_uint4(z[0], z[1], z[2], z[3]), y1 = make_uint4(z[4], z[5], z[6], z[7]);
+                        uint8_t* row = out + 16384 * (c >> 2) + k * 128;
+                        const int c16 = 2 * (c & 3);
+                        const bool swap = D == 128 && (c & 4);         // (so that eight lanes' 16 bytes lie in different banks)
+                        *reinterpret_cast<uint4*>(row + (((c16 + swap) ^ k) & 7) * 16) = swap ? y1 : y0;
+                        *reinterpret_cast<uint4*>(row + (((c16 + !swap) ^ k) & 7) * 16) = swap ? y0 : y1;
+                    }
                 }
                 fence_async_smem();
                 __syncwarp();
@@ -435,43 +442,39 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
                 const int j = two ? jj : 2 * jj + i;
                 if (!(ok = wait_all(B_S + i, (uint32_t)(ns + jj)))) break;
                 fence_after();
-                // (QZ: read twice, 32 columns at a time, as 128 registers a thread do not hold them all)
-                float s[QZ ? 32 : kN];
+                // (QZ: columns 64 .. 127 are read twice, as 128 registers a thread do not hold all)
+                constexpr int kHeld = QZ ? 64 : kN;
+                float s[kHeld];
                 const int valid = g.len - j * kN;
                 const uint32_t bad = bad_sm[(g.blk0 + j) % kBad];
                 const bool some = valid < kN || bad;
                 const int lb = 31 - __clz(min(p.page, kN));
-                auto hide = [&](float(&z)[QZ ? 32 : kN], int x0) {
+                // columns x0 .. x0 + 31 in s[at ..]
+                auto hide = [&](int at, int x0) {
+                    if (!some) return;
 #pragma unroll
-                    for (int x = 0; x < (QZ ? 32 : kN); ++x)
-                        if (x0 + x >= valid || (bad >> ((x0 + x) >> lb)) & 1u) z[x] = -INFINITY;
+                    for (int x = 0; x < 32; ++x)
+                        if (x0 + x >= valid || (bad >> ((x0 + x) >> lb)) & 1u) s[at + x] = -INFINITY;
                 };
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                if constexpr (QZ) {
-#pragma unroll 1
-                    for (int x = 0; x < kN; x += 32) {
-                        tmem_ld32(ts + x, s);
-                        tmem_wait_ld();
-                        if (some) hide(s, x);
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) mx[y & 3] = fmaxf(mx[y & 3], s[y]);
-                    }
-                } else {
+                for (int x0 = kN - kHeld; x0 >= 0; x0 -= kHeld) {
 #pragma unroll
-                    for (int x = 0; x < kN; x += 32) tmem_ld32(ts + x, s + x);
+                    for (int x = 0; x < kHeld; x += 32) tmem_ld32(ts + x0 + x, s + x);
                     tmem_wait_ld();
-                    if (some) hide(s, 0);
-                    if (valid < kN) {
-                        // values behind the prefix, which may be anything, become zero (both tiles see to it)
-                        const int vs = g.n0 + j + min(g.nb, j + look);
-                        if (!(ok = wait_all(B_FULL + vs % kRing, (uint32_t)(vs / kRing)))) break;
-                        for (int x = max(valid, 0) * 8 + r; x < kN * 8; x += kM)
 #pragma unroll
-                            for (int y = 0; y < D / 64; ++y) *reinterpret_cast<uint4*>(sm + stage_at(vs) + 16384 * y + 16 * x) = make_uint4(0, 0, 0, 0);
-                        fence_async_smem();
-                    }
+                    for (int x = 0; x < kHeld; x += 32) hide(x, x0 + x);
 #pragma unroll
-                    for (int x = 0; x < kN; ++x) mx[x & 3] = fmaxf(mx[x & 3], s[x]);
+                    for (int x = 0; x < kHeld; ++x) mx[x & 3] = fmaxf(mx[x & 3], s[x]);
+                }
+                if (!QZ && valid < kN) {
+                    // values behind the prefix, which may be anything, become zero (both tiles see to it)
+                    const int vs = g.n0 + j + min(g.nb, j + look);
+                    if (!(ok = wait_all(B_FULL + vs % kRing, (uint32_t)(vs / kRing)))) break;
+                    for (int x = max(valid, 0) * 8 + r; x < kN * 8; x += kM)
+#pragma unroll
+                        for (int y = 0; y < D / 64; ++y) *reinterpret_cast<uint4*>(sm + stage_at(vs) + 16384 * y + 16 * x) = make_uint4(0, 0, 0, 0);
+                    fence_async_smem();
                 }
                 // the scores' factor, and what their weights' exponents have besides
                 float cb = c, add = 0.f;
@@ -505,24 +508,38 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
                 float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 const float off = QZ ? add + kWeightBits - base : -base;
                 const float2 c2 = make_float2(cb, cb), b2 = make_float2(off, off);
-#pragma unroll
-                for (int x = 0; x < kN; x += 32) {
+                // weights of the 32 scores in s[at ..], columns x on, over the scores
+                auto weigh = [&](int at, int x) {
                     uint32_t pw[16];
-                    if constexpr (QZ) {
-                        tmem_ld32(ts + x, s);
-                        tmem_wait_ld();
-                        if (some) hide(s, x);
-                    }
-                    constexpr int kAt = QZ ? 0 : 1;
 #pragma unroll
                     for (int y = 0; y < 16; ++y) {
-                        float2 e = fma2(make_float2(s[kAt * x + 2 * y], s[kAt * x + 2 * y + 1]), c2, b2);
+                        float2 e = fma2(make_float2(s[at + 2 * y], s[at + 2 * y + 1]), c2, b2);
                         e.x = ex2(e.x);
                         e.y = ex2(e.y);
                         ls[y & 1] = add2(ls[y & 1], e);
                         pw[y] = QZ ? half2_of(e.x, e.y) : pack2(e.x, e.y);
                     }
                     tmem_st16(ts + x / 2, pw);
+                };
+                if constexpr (QZ) {
+                    // (a place's next columns are under way while the other's are weighed)
+                    auto arrived = [&](int at, int x) {
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) asm volatile("" : "+f"(s[at + y]));
+                        hide(at, x);
+                    };
+                    weigh(0, 0);
+                    tmem_ld32(ts + 64, s);
+                    weigh(32, 32);
+                    arrived(0, 64);
+                    tmem_ld32(ts + 96, s + 32);
+                    weigh(0, 64);
+                    arrived(32, 96);
+                    weigh(32, 96);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < kN; x += 32) weigh(x, x);
                 }
                 const float sum = (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
                 l = QZ ? fmaf(sum, power_down(F) * (1.f / kUp), l) : l + sum;

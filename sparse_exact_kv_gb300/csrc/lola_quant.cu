@@ -12,6 +12,9 @@
 // q comes as float16 numbers of its row's own power of two (its largest number in [2^14, 2^15): a bfloat16 number
 // loses nothing down to 2^-28 of that; a float32 number is kept in two parts, to 2^-39 of it), the weights as
 // float16 numbers of 2^15 w_j (rounded by 2^-12 of themselves, or by 2^-40 where they are small; float32 io: two parts).
+// The products have tokens, then channels, as M and the query rows as N, eight at a time: S^T = K Q^T, O^T = V^T P^T, the
+// weights turned by movmatrix in between.  Groups of up to eight query heads then cost half the products and registers
+// of the other way round (M = 16 rows), which leaves room for twelve warps in place of eight.
 // The contraction's channels may come in any order: a lane's four neighbouring codes of K, one word, are its four
 // channels of a product, and the same four of q.  A word of V holds two channels of two tokens and is permuted first.
 #include "lola_codes.cuh"
@@ -31,23 +34,31 @@ __device__ __forceinline__ uint32_t half2_rest(float x, float y, uint32_t h) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
     return half2_of(x - f.x, y - f.y);
 }
-template <typename TO, int D, bool HALF> struct QSmem {
-    static constexpr int NW = kCons / kWarp;
-    static constexpr int HR = HALF ? 1 : 2, R8 = 8 * HR, CK = 512 / R8;     // rows kept; columns joined at a time
+// the 8 x 8 numbers of a warp's lanes (row lane / 4, columns 2 (lane % 4) and + 1), transposed
+__device__ __forceinline__ uint32_t turned(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// NB: query rows in eights
+template <typename TO, int D, int NB> struct QSmem {
+    static constexpr int NW = NB == 1 ? 12 : 8;                             // consumer warps
+    static constexpr int kCk = NB == 1 ? 64 : 32;                           // columns joined at a time
     static constexpr int kPitch = D * (int)sizeof(TO) + 16;                 // Q rows
-    float red[NW][R8][CK];
-    float ms[NW][R8], ls[NW][R8];
+    float red[NW][8 * NB][kCk + 8];                                         // (rows 32 bytes apart: 8-byte stores of four rows)
+    float ms[NW][8 * NB], ls[NW][8 * NB];
     uint8_t q[2][kRows * kPitch];
 };
 
-// All eight warps on a segment, in two groups that take its tiles in turn; a warp has 16 of a tile's 64 tokens.
-// HALF: at most 8 query rows (rows 8-15 of the products hold anything and are left alone).  TO: q and o.
-template <typename TO, int D, bool HALF, bool SH>
-__global__ void __launch_bounds__(kThreads, 1) quant_decode_kernel(const __grid_constant__ Maps maps, const Args a) {
+// All warps on a segment, in groups of four that take its tiles in turn; a warp has 16 of a tile's 64 tokens.
+// TO: q and o.
+template <typename TO, int D, int NB, bool SH>
+__global__ void __launch_bounds__((QSmem<TO, D, NB>::NW + 1) * kWarp, 1) quant_decode_kernel(const __grid_constant__ Maps maps, const Args a) {
     using T = uint8_t;
     using C = Cfg<T, D>;
-    using M = QSmem<TO, D, HALF>;
-    constexpr int HR = M::HR, CK = M::CK, NW = M::NW, NT = kCons;
+    using M = QSmem<TO, D, NB>;
+    constexpr int NW = M::NW, NT = NW * kWarp, kGroups = NW / 4, CK = M::kCk;
     constexpr bool kTwo = sizeof(TO) == 4;                             // q and the weights in two parts
     extern __shared__ __align__(1024) uint8_t smraw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
@@ -73,10 +84,10 @@ __global__ void __launch_bounds__(kThreads, 1) quant_decode_kernel(const __grid_
     }
     wait_for_last_kernel();
     Start st;
-    if (!find_start<SH>(a, &st)) return;
+    if (!find_start<SH, NT + kWarp>(a, &st)) return;
     if (warp == NW) produce<T, TO, D, 2, SH>(maps, a, st, sb, smem_u32(x.q[0]), M::kPitch, bars, segs, bad_sm, &abort_sm, lane);
     const int grp = warp >> 2, k0 = (warp & 3) * 16, g8 = lane >> 2, q4 = lane & 3, q2 = q4 * 2;
-    auto bar = [&] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+    auto bar = [&] { asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory"); };
     const int box = min(p.page, kTile), lb = 31 - __clz(box);
     // 16-byte chunk ch of token k's row: rows of 128 bytes (two tokens at d = 64), chunks swizzled
     auto chunk_at = [](int k, int ch) {
@@ -93,86 +104,106 @@ __global__ void __launch_bounds__(kThreads, 1) quant_decode_kernel(const __grid_
         const Seg g = segs[slot];
         if (g.R < 0) break;
         if (!SH && !g.whole && tid == 64) open_cells<D>(a, g);
-        // ---- q: rows g8 and g8 + 8, channels 16 y + 4 q4 .. + 3, with a power of two of the row's own ----
-        uint32_t qa[D / 16][4], qr[kTwo ? D / 16 : 1][4];
-        float qs[2];
+        // ---- q: row 8 b + g8, channels 16 y + 4 q4 .. + 3, with a power of two of the row's own; the lanes' rows of the
+        // scores are 8 b + q2 and + 1 ----
+        uint32_t qa[NB][D / 16][2], qr[kTwo ? NB : 1][kTwo ? D / 16 : 1][2];
+        float qs[NB][2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const uint8_t* row = x.q[slot] + (g8 + 8 * r) * M::kPitch;
-            float v[D / 16][4];
+        for (int b = 0; b < NB; ++b) {
+            const uint8_t* row = x.q[slot] + (g8 + 8 * b) * M::kPitch;
             uint32_t top = 0u;
-#pragma unroll
-            for (int y = 0; y < D / 16; ++y) {
+            auto channels = [&](int y, float(&v)[4]) {
                 if constexpr (kTwo) {
                     const float4 z = *reinterpret_cast<const float4*>(row + (16 * y + 4 * q4) * 4);
-                    v[y][0] = z.x, v[y][1] = z.y, v[y][2] = z.z, v[y][3] = z.w;
+                    v[0] = z.x, v[1] = z.y, v[2] = z.z, v[3] = z.w;
                 } else {
                     const uint2 z = *reinterpret_cast<const uint2*>(row + (16 * y + 4 * q4) * 2);
-                    v[y][0] = __uint_as_float(z.x << 16), v[y][1] = __uint_as_float(z.x & 0xffff0000u);
-                    v[y][2] = __uint_as_float(z.y << 16), v[y][3] = __uint_as_float(z.y & 0xffff0000u);
+                    v[0] = __uint_as_float(z.x << 16), v[1] = __uint_as_float(z.x & 0xffff0000u);
+                    v[2] = __uint_as_float(z.y << 16), v[3] = __uint_as_float(z.y & 0xffff0000u);
                 }
+            };
 #pragma unroll
-                for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(v[y][e]) & 0x7fffffffu);
+            for (int y = 0; y < D / 16; ++y) {
+                float v[4];
+                channels(y, v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
             }
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const uint32_t up = min(268u - (top >> 23), 240u);         // the largest magnitude goes to [2^14, 2^15)
             const float f = __uint_as_float(up << 23);
-            qs[r] = a.scale_log2 * __uint_as_float((254u - up) << 23);
 #pragma unroll
-            for (int y = 0; y < D / 16; ++y)
+            for (int e = 0; e < 2; ++e)
+                qs[b][e] = a.scale_log2 * __uint_as_float((254u - __shfl_sync(0xffffffffu, up, 4 * (q2 + e))) << 23);
+#pragma unroll
+            for (int y = 0; y < D / 16; ++y) {
+                float v[4];
+                channels(y, v);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float u = v[y][2 * e] * f, w = v[y][2 * e + 1] * f;
-                    qa[y][2 * e + r] = half2_of(u, w);
-                    if constexpr (kTwo) qr[y][2 * e + r] = half2_rest(u, w, qa[y][2 * e + r]);
+                    const float u = v[2 * e] * f, w = v[2 * e + 1] * f;
+                    qa[b][y][e] = half2_of(u, w);
+                    if constexpr (kTwo) qr[b][y][e] = half2_rest(u, w, qa[b][y][e]);
                 }
+            }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive1(smem_u32(&bars.seg_empty[slot]));   // (g and the Q rows are in registers)
-        float o[D / 16][2][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        // o: channels 16 y + 2 g8 (0, 1) and + 1 (2, 3), rows 8 b + q2 and + 1
+        float o[D / 16][NB][4], m[NB][2], l[NB][2];
 #pragma unroll
-        for (int y = 0; y < D / 16; ++y)
+        for (int b = 0; b < NB; ++b) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[y][e >> 2][e & 3] = 0.f;
+            for (int e = 0; e < 2; ++e) {
+                m[b][e] = -INFINITY;
+                l[b][e] = 0.f;
+            }
+#pragma unroll
+            for (int y = 0; y < D / 16; ++y)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[y][b][e] = 0.f;
+        }
         bool ok = true;
-        for (int t = (g.n0 ^ grp) & 1; t < g.tiles; t += 2) {
+        for (int t = (grp + kGroups - g.n0 % kGroups) % kGroups; t < g.tiles; t += kGroups) {
             const int n = g.n0 + t, s = n % C::kStages;
             ok = issued_wait(&bars.issued, n, &abort_sm) &&
                  ring_wait(smem_u32(&bars.full[s]), (uint32_t)(n / C::kStages) & 1, &abort_sm);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const uint32_t kt = sb + (uint32_t)s * 2 * C::kHalf, vt = kt + C::kHalf;
-            const uint8_t* powers = sm + (size_t)C::kStages * 2 * C::kHalf + (size_t)s * C::kScales + k0 + q2;
+            const uint8_t* powers = sm + (size_t)C::kStages * 2 * C::kHalf + (size_t)s * C::kScales + k0 + g8;
             const int left = g.len - t * kTile;
             const uint32_t bad = bad_sm[s];
-            // ---- S: 16 rows x 16 tokens, two chains a token half ----
-            float c0[2][4] = {}, c1[2][4] = {};
+            // ---- S^T: 16 tokens x 8 rows, two chains ----
+            float c0[NB][4] = {}, c1[NB][4] = {};
 #pragma unroll
             for (int y = 0; y < D / 32; ++y) {
                 uint32_t kb[4];
                 ldsm4(kt + chunk_at(token, 2 * y + ch0), kb);
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    uint32_t lo, hi;
-                    widen(kb[z], lo, hi);
-                    mma16816_h(z >> 1 ? c1[z & 1] : c0[z & 1], qa[2 * y + (z >> 1)], lo, hi);
-                    if constexpr (kTwo) mma16816_h(z >> 1 ? c1[z & 1] : c0[z & 1], qr[2 * y + (z >> 1)], lo, hi);
+                for (int z = 0; z < 2; ++z) {
+                    uint32_t ka[4];                                    // tokens g8, g8 + 8: channels 4 q4, + 1; then + 2, + 3
+                    widen(kb[2 * z], ka[0], ka[2]);
+                    widen(kb[2 * z + 1], ka[1], ka[3]);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        mma16816_h(z ? c1[b] : c0[b], ka, qa[b][2 * y + z][0], qa[b][2 * y + z][1]);
+                        if constexpr (kTwo) mma16816_h(z ? c1[b] : c0[b], ka, qr[b][2 * y + z][0], qr[b][2 * y + z][1]);
+                    }
                 }
             }
-            // ---- scores and exponents of the weights: tokens k0 + q2, + 1, + 8, + 9 ----
-            float sc[2][4], down[2][2];
+            // ---- scores and exponents of the weights: tokens k0 + g8 (0, 1), + 8 (2, 3) ----
+            float sc[NB][4], down[2];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-                const uint32_t kp = *reinterpret_cast<const uint16_t*>(powers + 8 * y), vp = *reinterpret_cast<const uint16_t*>(powers + kTile + 8 * y);
+                const uint32_t kp = powers[8 * y], vp = powers[kTile + 8 * y];
+                const float fk = __uint_as_float(kp << 23), fv = (float)(int)vp - 127.f;
+                down[y] = power_down(vp);
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const uint32_t kb = z ? kp >> 8 : kp & 255u, vb = z ? vp >> 8 : vp & 255u;
-                    const float fk = __uint_as_float(kb << 23), fv = (float)(int)vb - 127.f;
-                    down[y][z] = power_down(vb);
+                for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int r = 0; r < HR; ++r) sc[y][2 * r + z] = fmaf((c0[y][2 * r + z] + c1[y][2 * r + z]) * qs[r], fk, fv);
-                }
+                    for (int e = 0; e < 2; ++e) sc[b][2 * y + e] = fmaf((c0[b][2 * y + e] + c1[b][2 * y + e]) * qs[b][e], fk, fv);
             }
             if (left < k0 + 16 || bad) {
                 // tokens behind the sequence or on bad pages: no score, and their V rows (which may
@@ -181,9 +212,9 @@ __global__ void __launch_bounds__(kThreads, 1) quant_decode_kernel(const __grid_
                 auto hidden = [&](int k) { return k >= nk || ((bad >> (k >> lb)) & 1u); };
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
+                    if (hidden(k0 + 8 * y + g8))
 #pragma unroll
-                    for (int e = 0; e < 2 * HR; ++e)
-                        if (hidden(k0 + 8 * y + q2 + (e & 1))) sc[y][e] = -INFINITY;
+                        for (int b = 0; b < NB; ++b) sc[b][2 * y] = sc[b][2 * y + 1] = -INFINITY;
                 for (int k = k0; k < k0 + 16; ++k)
                     if (hidden(k) && lane < D / 16)
                         *reinterpret_cast<uint4*>(sm + (size_t)s * 2 * C::kHalf + C::kHalf + chunk_at(k, lane)) = make_uint4(0, 0, 0, 0);
@@ -191,56 +222,60 @@ __global__ void __launch_bounds__(kThreads, 1) quant_decode_kernel(const __grid_
                 __syncwarp();
             }
             // ---- running maximum, weights ----
-            uint32_t pa[4] = {0u, 0u, 0u, 0u}, pr[4] = {0u, 0u, 0u, 0u};
+            uint32_t pb[NB][2], pr[kTwo ? NB : 1][2];                  // tokens 2 q4, + 1 (+ 8) of row 8 b + g8
 #pragma unroll
-            for (int r = 0; r < HR; ++r) {
-                float bm = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
-                bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
-                const float top = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2)) + kRaise;
-                const bool need = top > m[r] + kRaise;
-                if (__any_sync(0xffffffffu, need)) {
-                    const float f = need ? ex2(m[r] - top) : 1.f;
-                    if (need) m[r] = top;
-                    l[r] *= f;
+            for (int b = 0; b < NB; ++b) {
+                float top[2];
 #pragma unroll
-                    for (int y = 0; y < D / 16; ++y)
+                for (int e = 0; e < 2; ++e) {
+                    top[e] = fmaxf(sc[b][e], sc[b][2 + e]);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            o[y][e][2 * r] *= f;
-                            o[y][e][2 * r + 1] *= f;
-                        }
+                    for (int z = 4; z < kWarp; z <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], z));
+                    top[e] += kRaise;
                 }
-                const float base = m[r] == -INFINITY ? 0.f : m[r];
-                float w[2][2];
+                const bool need[2] = {top[0] > m[b][0] + kRaise, top[1] > m[b][1] + kRaise};
+                if (__any_sync(0xffffffffu, need[0] || need[1])) {
 #pragma unroll
-                for (int y = 0; y < 2; ++y)
+                    for (int e = 0; e < 2; ++e) {
+                        const float f = need[e] ? ex2(m[b][e] - top[e]) : 1.f;
+                        if (need[e]) m[b][e] = top[e];
+                        l[b][e] *= f;
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        w[y][z] = ex2(sc[y][2 * r + z] - base);
-                        l[r] = fmaf(w[y][z], down[y][z], l[r]);
-                        w[y][z] *= kUp;
+                        for (int y = 0; y < D / 16; ++y) {
+                            o[y][b][e] *= f;
+                            o[y][b][2 + e] *= f;
+                        }
                     }
+                }
+                float w[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const int e = z & 1;
+                    w[z] = ex2(sc[b][z] - (m[b][e] == -INFINITY ? 0.f : m[b][e]));
+                    l[b][e] = fmaf(w[z], down[z >> 1], l[b][e]);
+                    w[z] *= kUp;
+                }
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    pa[2 * y + r] = half2_of(w[y][0], w[y][1]);
-                    if constexpr (kTwo) pr[2 * y + r] = half2_rest(w[y][0], w[y][1], pa[2 * y + r]);
+                    const uint32_t h = half2_of(w[2 * y], w[2 * y + 1]);
+                    pb[b][y] = turned(h);
+                    if constexpr (kTwo) pr[b][y] = turned(half2_rest(w[2 * y], w[2 * y + 1], h));
                 }
             }
-            // ---- O += P V ----
+            // ---- O^T += V^T P^T ----
 #pragma unroll
             for (int y = 0; y < D / 32; ++y) {
                 uint32_t vb[4];
                 ldsm4_t(vt + chunk_at(token, 2 * y + ch0), vb);
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
-                    uint32_t e0, o0, e1, o1;
-                    widen(__byte_perm(vb[2 * z], 0u, 0x3120), e0, o0);
-                    widen(__byte_perm(vb[2 * z + 1], 0u, 0x3120), e1, o1);
-                    mma16816_h(o[2 * y + z][0], pa, e0, e1);
-                    mma16816_h(o[2 * y + z][1], pa, o0, o1);
-                    if constexpr (kTwo) {
-                        mma16816_h(o[2 * y + z][0], pr, e0, e1);
-                        mma16816_h(o[2 * y + z][1], pr, o0, o1);
+                    uint32_t va[4];                                    // channels 2 g8, 2 g8 + 1: tokens 2 q4, + 1; then + 8, + 9
+                    widen(__byte_perm(vb[2 * z], 0u, 0x3120), va[0], va[1]);
+                    widen(__byte_perm(vb[2 * z + 1], 0u, 0x3120), va[2], va[3]);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        mma16816_h(o[2 * y + z][b], va, pb[b][0], pb[b][1]);
+                        if constexpr (kTwo) mma16816_h(o[2 * y + z][b], va, pr[b][0], pr[b][1]);
                     }
                 }
             }
@@ -253,41 +288,47 @@ __global__ void __launch_bounds__(kThreads, 1) quant_decode_kernel(const __grid_
             break;
         }
 #pragma unroll
-        for (int r = 0; r < HR; ++r) {
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-            if (q4 == 0) {
-                x.ms[warp][g8 + 8 * r] = m[r];
-                x.ls[warp][g8 + 8 * r] = l[r];
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int z = 4; z < kWarp; z <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], z);
+                if (g8 == 0) {
+                    x.ms[warp][8 * b + q2 + e] = m[b][e];
+                    x.ls[warp][8 * b + q2 + e] = l[b][e];
+                }
             }
-        }
         bar();
-        float f[2];
+        float f[NB][2];
 #pragma unroll
-        for (int r = 0; r < HR; ++r) {
-            float mm = -INFINITY;
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int w = 0; w < NW; ++w) mm = fmaxf(mm, x.ms[w][g8 + 8 * r]);
-            f[r] = ex2(m[r] - (mm == -INFINITY ? 0.f : mm)) * (1.f / kUp);
-        }
+            for (int e = 0; e < 2; ++e) {
+                float mm = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) mm = fmaxf(mm, x.ms[w][8 * b + q2 + e]);
+                f[b][e] = ex2(m[b][e] - (mm == -INFINITY ? 0.f : mm)) * (1.f / kUp);
+            }
         float* rec = segment_record<D, SH>(a, g);
-        const int er = 4 * (tid & 127) / CK, ec = 4 * (tid & 127) % CK;        // 128 threads x 4 columns = R8 x CK
+        const int er = 4 * (tid & 127) / CK, ec = 4 * (tid & 127) % CK;        // 128 threads x 4 columns = 8 NB x CK
         float mm = -INFINITY, ll = 0.f;
+        if (tid < 128) {
 #pragma unroll
-        for (int w = 0; w < NW; ++w) mm = fmaxf(mm, x.ms[w][er]);
+            for (int w = 0; w < NW; ++w) mm = fmaxf(mm, x.ms[w][er]);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) ll = fmaf(x.ls[w][er], ex2(x.ms[w][er] - (mm == -INFINITY ? 0.f : mm)), ll);
+            for (int w = 0; w < NW; ++w) ll = fmaf(x.ls[w][er], ex2(x.ms[w][er] - (mm == -INFINITY ? 0.f : mm)), ll);
+        }
 #pragma unroll
         for (int c = 0; c < D; c += CK) {
             if (c > 0) bar();
 #pragma unroll
             for (int y = 0; y < CK / 16; ++y)
 #pragma unroll
-                for (int r = 0; r < HR; ++r) {
-                    const float(&z)[2][4] = o[c / 16 + y];
-                    *reinterpret_cast<float4*>(&x.red[warp][g8 + 8 * r][16 * y + 4 * q4]) =
-                        make_float4(z[0][2 * r] * f[r], z[1][2 * r] * f[r], z[0][2 * r + 1] * f[r], z[1][2 * r + 1] * f[r]);
-                }
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        *reinterpret_cast<float2*>(&x.red[warp][8 * b + q2 + e][16 * y + 2 * g8]) =
+                            make_float2(o[c / 16 + y][b][e] * f[b][e], o[c / 16 + y][b][2 + e] * f[b][e]);
             bar();
             if (tid < 128) {
                 float y[4] = {0.f, 0.f, 0.f, 0.f};
@@ -305,15 +346,16 @@ __global__ void __launch_bounds__(kThreads, 1) quant_decode_kernel(const __grid_
         if (!SH && !g.whole) join_pieces<TO, D, NT>(a, g, tid, &go, bars.arrived, bar);
     }
     __syncthreads();
-    if (abort_sm) settle<D, C::kStages, 2, SH>(a, bars);
+    if (abort_sm) settle<D, C::kStages, 2, SH, NT + kWarp>(a, bars);
 }
 
 template <typename TO, int D, bool SH>
 cudaError_t launch_quant(const DecodeArgs& d, cudaStream_t st) {
     static std::atomic<uint64_t> done[2] = {};
-    return !SH && d.p.G <= 8 ? launch_kernel<uint8_t, D>(quant_decode_kernel<TO, D, true, false>, done[0], d, st)
-                             : launch_kernel<uint8_t, D>(quant_decode_kernel<TO, D, false, SH>, done[1], d, st);
+    return !SH && d.p.G <= 8 ? launch_kernel<uint8_t, D>(quant_decode_kernel<TO, D, 1, false>, QSmem<TO, D, 1>::NW, done[0], d, st)
+                             : launch_kernel<uint8_t, D>(quant_decode_kernel<TO, D, 2, SH>, QSmem<TO, D, 2>::NW, done[1], d, st);
 }
+
 template <bool SH> cudaError_t launch_quant(const DecodeArgs& a, cudaStream_t st) {
     if (a.p.dtype == LOLA_F32) return a.p.d == 128 ? launch_quant<float, 128, SH>(a, st) : launch_quant<float, 64, SH>(a, st);
     return a.p.d == 128 ? launch_quant<__nv_bfloat16, 128, SH>(a, st) : launch_quant<__nv_bfloat16, 64, SH>(a, st);
@@ -325,34 +367,32 @@ template <bool SH> cudaError_t launch_quant(const DecodeArgs& a, cudaStream_t st
 // output in flight a thread.  Bound by bytes: each code read once, each number written once.
 constexpr int kReadRows = 32, kReadThreads = 256;
 
-template <typename T> __device__ __forceinline__ uint4 read_unit(const uint8_t* src, float f);
-template <> __device__ __forceinline__ uint4 read_unit<float>(const uint8_t* src, float f) {
-    uint32_t lo, hi;
-    widen(*reinterpret_cast<const uint32_t*>(src), lo, hi);
-    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo)), y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-    return make_uint4(__float_as_uint(x.x * f), __float_as_uint(x.y * f), __float_as_uint(y.x * f), __float_as_uint(y.y * f));
-}
-template <> __device__ __forceinline__ uint4 read_unit<__nv_bfloat16>(const uint8_t* src, float f) {
-    const uint2 w = *reinterpret_cast<const uint2*>(src);
-    uint32_t r[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = 0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
+// 16 / sizeof(T) codes (4 or 8 bytes) times f
+template <typename T> struct ReadUnit;
+template <> struct ReadUnit<float> {
+    using Codes = uint32_t;
+    static __device__ __forceinline__ uint4 of(uint32_t w, float f) {
         uint32_t lo, hi;
-        widen(i ? w.y : w.x, lo, hi);
+        widen(w, lo, hi);
         const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo)), y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-        r[2 * i] = pack2(x.x * f, x.y * f);
-        r[2 * i + 1] = pack2(y.x * f, y.y * f);
+        return make_uint4(__float_as_uint(x.x * f), __float_as_uint(x.y * f), __float_as_uint(y.x * f), __float_as_uint(y.y * f));
     }
-    return make_uint4(r[0], r[1], r[2], r[3]);
-}
+};
+template <> struct ReadUnit<__nv_bfloat16> {
+    using Codes = uint2;
+    static __device__ __forceinline__ uint4 of(uint2 w, float f) {
+        const uint4 x = ReadUnit<float>::of(w.x, f), y = ReadUnit<float>::of(w.y, f);
+        auto pair = [](uint32_t a, uint32_t b) { return pack2(__uint_as_float(a), __uint_as_float(b)); };
+        return make_uint4(pair(x.x, x.y), pair(x.z, x.w), pair(y.x, y.y), pair(y.z, y.w));
+    }
+};
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kReadThreads) quant_read_kernel(const ReadArgs a) {
     constexpr int VN = 16 / sizeof(T), UH = D / VN;                    // numbers of a unit, units of a head
     __shared__ int64_t sums[kReadThreads / kWarp];
-    __shared__ int64_t from[kReadRows];                                // (page, slot) of a row: -1 zeros, -2 no row
+    __shared__ int64_t from[kReadRows];                                // token, then (page, slot) of a row: -1 zeros, -2 no row
+    __shared__ int seq[kReadRows];
     const PagedArgs& p = a.p;
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
     const int64_t r0 = (int64_t)blockIdx.x * kReadRows, r1 = min(r0 + kReadRows, (int64_t)a.total);
@@ -387,13 +427,19 @@ __global__ void __launch_bounds__(kReadThreads) quant_read_kernel(const ReadArgs
             if (hi > a.total) bits |= LOLA_ATTN_BAD_OFFSETS;
         }
         for (int64_t r = max(lo, r0); r < min(hi, r1); ++r) {
-            const int64_t pos = r - lo;
-            const int page = paged_page(p, b, pos);
-            if (page < 0) bits |= LOLA_ATTN_BAD_PAGE;
-            from[r - r0] = page < 0 ? -1 : (int64_t)page * p.Hkv * p.page + (pos & (p.page - 1));
+            seq[r - r0] = b;
+            from[r - r0] = r - lo;
         }
         before = all;
         if (blockIdx.x > 0 && before >= r1) break;
+    }
+    __syncthreads();
+    // (a lookup a thread, of all rows at once)
+    if (threadIdx.x < kReadRows && from[threadIdx.x] >= 0) {
+        const int64_t pos = from[threadIdx.x];
+        const int page = paged_page(p, seq[threadIdx.x], pos);
+        if (page < 0) bits |= LOLA_ATTN_BAD_PAGE;
+        from[threadIdx.x] = page < 0 ? -1 : (int64_t)page * p.Hkv * p.page + (pos & (p.page - 1));
     }
     if (bits) atomicOr(&g_status, bits);
     __syncthreads();
@@ -404,22 +450,26 @@ __global__ void __launch_bounds__(kReadThreads) quant_read_kernel(const ReadArgs
         const uint8_t* powers = kv ? p.Vs : p.Ks;
         const Rows& out = kv ? a.V : a.K;
         for (int e0 = threadIdx.x; e0 < units; e0 += NU * kReadThreads) {
-            uint4 y[NU];
+            // (loads without conditions, from the pool's first row where there is nothing to read: all are under way at once)
+            typename ReadUnit<T>::Codes w[NU];
+            uint8_t power[NU];
             T* dst[NU];
+            uint32_t zero = 0u;
 #pragma unroll
             for (int x = 0; x < NU; ++x) {
-                const int e = e0 + x * kReadThreads, u = e % UH, rh = e / UH, i = rh / p.Hkv, h = rh - i * p.Hkv;
-                dst[x] = nullptr;
-                if (e >= units || from[i] == -2) continue;
-                dst[x] = reinterpret_cast<T*>(out.data) + (r0 + i) * out.row + (int64_t)h * out.head + u * VN;
-                y[x] = make_uint4(0, 0, 0, 0);
-                if (from[i] < 0) continue;
-                const int64_t row = from[i] + (int64_t)h * p.page;
-                y[x] = read_unit<T>(pool + row * D + u * VN, __uint_as_float((uint32_t)powers[row] << 23));
+                const int e = min(e0 + x * kReadThreads, units - 1), u = e % UH, rh = e / UH, i = rh / p.Hkv, h = rh - i * p.Hkv;
+                const int64_t at = from[i], row = at < 0 ? 0 : at + (int64_t)h * p.page;
+                w[x] = *reinterpret_cast<const typename ReadUnit<T>::Codes*>(pool + row * D + u * VN);
+                power[x] = powers[row];
+                if (at < 0) zero |= 1u << x;
+                const bool none = e0 + x * kReadThreads >= units || at == -2;
+                dst[x] = none ? nullptr : reinterpret_cast<T*>(out.data) + (r0 + i) * out.row + (int64_t)h * out.head + u * VN;
             }
 #pragma unroll
-            for (int x = 0; x < NU; ++x)
-                if (dst[x]) *reinterpret_cast<uint4*>(dst[x]) = y[x];
+            for (int x = 0; x < NU; ++x) {
+                const uint4 y = ReadUnit<T>::of(w[x], __uint_as_float((uint32_t)power[x] << 23));
+                if (dst[x]) *reinterpret_cast<uint4*>(dst[x]) = (zero >> x) & 1u ? make_uint4(0, 0, 0, 0) : y;
+            }
         }
     }
 }
