@@ -480,15 +480,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_mma_kernel(const __g
 template <int D, bool SH>
 cudaError_t launch_f32(const DecodeArgs& d, cudaStream_t st) {
     static std::atomic<uint64_t> done[3] = {};
-    if (!SH && d.p.G <= 4) return launch_kernel<float, D>(paged_decode_f32_kernel<D, 4, false>, kCons / kWarp, done[0], d, st);
-    if (!SH && d.p.G <= 8) return launch_kernel<float, D>(paged_decode_f32_kernel<D, 8, false>, kCons / kWarp, done[1], d, st);
-    return launch_kernel<float, D>(paged_decode_f32_kernel<D, 16, SH>, kCons / kWarp, done[2], d, st);
+    if (!SH && d.p.G <= 4) return launch_kernel<float, D>(paged_decode_f32_kernel<D, 4, false>, kThreads / kWarp, done[0], d, st);
+    if (!SH && d.p.G <= 8) return launch_kernel<float, D>(paged_decode_f32_kernel<D, 8, false>, kThreads / kWarp, done[1], d, st);
+    return launch_kernel<float, D>(paged_decode_f32_kernel<D, 16, SH>, kThreads / kWarp, done[2], d, st);
 }
 template <int D, bool SH>
 cudaError_t launch_bf16(const DecodeArgs& d, cudaStream_t st) {
     static std::atomic<uint64_t> done[2] = {};
-    return !SH && d.p.G <= 8 ? launch_kernel<__nv_bfloat16, D>(paged_decode_mma_kernel<D, true, false>, kCons / kWarp, done[0], d, st)
-                             : launch_kernel<__nv_bfloat16, D>(paged_decode_mma_kernel<D, false, SH>, kCons / kWarp, done[1], d, st);
+    return !SH && d.p.G <= 8 ? launch_kernel<__nv_bfloat16, D>(paged_decode_mma_kernel<D, true, false>, kThreads / kWarp, done[0], d, st)
+                             : launch_kernel<__nv_bfloat16, D>(paged_decode_mma_kernel<D, false, SH>, kThreads / kWarp, done[1], d, st);
 }
 // ---- one part of the parts that the pieces of a prefix have left ----
 // Two rows a warp: its lanes take the rows in turn, as neighbouring rows' 16 bytes often share a sector, and first the

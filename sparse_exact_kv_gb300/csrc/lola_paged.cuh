@@ -22,6 +22,7 @@ constexpr int kRows = 16;                 // query rows of a row group (at most)
 constexpr int kJoin = 16;                 // pieces joined at a time
 constexpr float kRaise = 8.0f;            // bf16: m is set this far above a maximum (log2), and raised when one passes it
 constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr uint64_t kDrainNs = 50000000ull;   // ... for copies in flight, when a wait has given up
 
 struct Maps {
     CUtensorMap k, v;   // [n_pages * Hkv][page][d] as 128-byte columns, boxes of min(page, 64) rows (e4m3: of 128
@@ -40,12 +41,14 @@ struct Args {
     int RG, I;          // row groups per key/value head; items (row groups) per sequence
 };
 
-// T: the cache's numbers (uint8_t: e4m3, whose powers of two, a byte a token, follow the ring)
+// T: the cache's numbers (uint8_t: e4m3, whose powers of two, a byte a token, follow the ring; a tile has twice the
+// tokens, as the producers take some 600 clocks for one, whatever its bytes)
 template <typename T, int D> struct Cfg {
+    static constexpr int kTokens = sizeof(T) == 1 ? 128 : kTile;   // of a tile
     static constexpr int kRowBytes = D * (int)sizeof(T);
-    static constexpr int kHalf = kTile * kRowBytes;                // K or V of a tile
-    static constexpr int kScales = sizeof(T) == 1 ? 2 * kTile : 0; // bytes of powers of a tile
-    static constexpr int kMost = sizeof(T) == 1 ? 16 : 12;
+    static constexpr int kHalf = kTokens * kRowBytes;              // K or V of a tile
+    static constexpr int kScales = sizeof(T) == 1 ? 2 * kTokens : 0;   // bytes of powers of a tile
+    static constexpr int kMost = 12;
     static constexpr int kStages = 196608 / (2 * kHalf + kScales) > kMost ? kMost : 196608 / (2 * kHalf + kScales);
     static constexpr int kSmem = kStages * (2 * kHalf + kScales) + 1024;
 };
@@ -257,21 +260,25 @@ __device__ __forceinline__ void place_piece(const Start& st, int64_t xs, int til
 
 // The producer warp: segments and their tiles, in order.  A tile's pages outside the cache are not
 // loaded; bit x of bad_sm marks the tile's x-th token box.  Segment i goes to slot i % NS.
-// TQ: the queries' numbers.
+// TQ: the queries' numbers.  e4m3: four warps (`part` 0-3: codes of K, of V, powers of K, of V) that walk the segments
+// side by side, as each copy takes its thread some 180 clocks to issue, and a tile of codes half a tile's time at most
+// (all four copies by one warp: 64 sequences of 1000-8000 tokens, 32/8 heads, d = 128, 117 us).  The first of them does the rest.
 template <typename T, typename TQ, int D, int NS, bool SH, typename B>
 __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const Start& st, uint32_t ring, uint32_t qs,
-                                        uint32_t q_pitch, B& bars, Seg* segs, uint32_t* bad_sm, int* abort_sm, int lane) {
+                                        uint32_t q_pitch, B& bars, Seg* segs, uint32_t* bad_sm, int* abort_sm, int lane, int part = 0) {
     using C = Cfg<T, D>;
+    constexpr bool kParts = C::kScales > 0;
+    const bool first = !kParts || part == 0;
     const PagedArgs& p = a.p;
     constexpr uint32_t kQBytes = D * (uint32_t)sizeof(TQ);
-    const int box = min(p.page, kTile), lb = 31 - __clz(box), nbox = kTile >> lb;   // tokens of a box, boxes of a tile
+    const int box = min(p.page, C::kTokens), lb = 31 - __clz(box), nbox = C::kTokens >> lb;   // tokens of a box, boxes of a tile
     int b = st.b;
     Group gr = group_of<SH>(a, b);
     int prior = SH ? 0 : prior_of(a.sh, b, lane) + 1;
     int lens_b = b;                                               // the lanes hold 32 sequences' lengths
     int lens = b + lane < p.n_seq ? p.kv_len[b + lane] : 0;
     int64_t tokens = paged_tokens(p, __shfl_sync(0xffffffffu, lens, 0));
-    int tiles = tiles_of(tokens), t0, item = divide(st.rem, tiles, &t0);
+    int tiles = tiles_of<C::kTokens>(tokens), t0, item = divide(st.rem, tiles, &t0);
     int64_t u = st.u0;
     int n = 0, i = 0, held_b = -1, held = -1;
     int held_c = 0;                                           // ... and 32 page-table columns of held_b
@@ -281,9 +288,9 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
         const int hk = item / gr.RG, r0 = (item % gr.RG) * kRows, h0 = hk * p.G + (SH ? 0 : r0), R = min(kRows, gr.rows - r0);
         // ---- the segment's descriptor and Q rows ----
         const int slot = i % NS;
-        if (i >= NS) ok = __all_sync(0xffffffffu, ring_wait(smem_u32(&bars.seg_empty[slot]), (uint32_t)(i / NS - 1) & 1, abort_sm));
+        if (first && i >= NS) ok = __all_sync(0xffffffffu, ring_wait(smem_u32(&bars.seg_empty[slot]), (uint32_t)(i / NS - 1) & 1, abort_sm));
         if (!ok) break;
-        if (lane == 0) {
+        if (first && lane == 0) {
             Seg g;
             g.b = gr.m0;
             g.h0 = h0;
@@ -292,7 +299,7 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
             g.R = R;
             g.tiles = t1 - t0;
             g.n0 = n;
-            g.len = (int)max((int64_t)0, tokens - (int64_t)t0 * kTile);
+            g.len = (int)max((int64_t)0, tokens - (int64_t)t0 * C::kTokens);
             g.whole = t0 == 0 && t1 == tiles;
             g.k = g.np = g.c0 = g.s0 = 0;
             if (!g.whole) place_piece(st, u - t0, tiles, &g);
@@ -301,7 +308,7 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
             mbar_expect(smem_u32(&bars.seg_full[slot]), (uint32_t)R * kQBytes);
         }
         __syncwarp();
-        if (lane < R) {
+        if (first && lane < R) {
             const int seq = SH ? gr.m0 + (r0 + lane) / p.G : b, h = SH ? h0 + (r0 + lane) % p.G : h0 + lane;
             bulk_load(qs + (uint32_t)slot * kRows * q_pitch + lane * q_pitch,
                       a.Q.data + ((int64_t)seq * a.Q.row + (int64_t)h * a.Q.head) * (int)sizeof(TQ), kQBytes, smem_u32(&bars.seg_full[slot]));
@@ -315,7 +322,7 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
             if (n >= C::kStages) ok = __all_sync(0xffffffffu, ring_wait(smem_u32(&bars.empty[s]), (uint32_t)(n / C::kStages - 1) & 1, abort_sm));
             if (!ok) break;
             // (positions fit 31 bits, but for the boxes behind the last token's)
-            const uint32_t pos = (uint32_t)t * kTile, have = (uint32_t)tokens;
+            const uint32_t pos = (uint32_t)t * C::kTokens, have = (uint32_t)tokens;
             const int col = (int)(pos >> p.page_log2);
             const int used = have > pos ? min(nbox, (int)((have - pos + box - 1) >> lb)) : 0;     // boxes with tokens
             if (held_b != b || col < held_c || col + used > held_c + 32) {
@@ -324,29 +331,30 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
                 const int64_t c = (int64_t)(col + lane) << p.page_log2;
                 held = c < tokens ? paged_page(p, b, c) : 0;
             }
-            // lanes 0 .. used - 1: a box of K each; lanes 16 ..: of V
+            // lanes 0 .. used - 1: a box of K each; lanes 16 ..: of V (e4m3: this warp's part)
             const int x = lane & 15;
             const int page = __shfl_sync(0xffffffffu, held, ((int)((pos + x * box) >> p.page_log2) - held_c) & 31);
             const bool mine = x < used, bad = mine && page < 0;
             const uint32_t bad_mask = __ballot_sync(0xffffffffu, bad) & 0xffffu;
-            if (lane == 0) {
+            if (first && lane == 0) {
                 if (bad_mask) atomicOr(&g_status, (int)LOLA_ATTN_BAD_PAGE);
                 bad_sm[s] = bad_mask;
                 mbar_expect(smem_u32(&bars.full[s]), (uint32_t)(2 * (used - __popc(bad_mask)) * box * (C::kRowBytes + (C::kScales ? 1 : 0))));
                 *reinterpret_cast<volatile int*>(&bars.issued) = n + 1;
             }
             __syncwarp();
-            if (mine && !bad) {
-                const int at = (int)((pos + x * box) & (p.page - 1));
-                tma_load4(ring + (uint32_t)s * 2 * C::kHalf + (lane >> 4) * C::kHalf + x * (uint32_t)(box * C::kRowBytes),
-                          lane >> 4 ? &maps.v : &maps.k, 0, C::kScales ? at * D / 128 : at, 0, page * p.Hkv + hk, smem_u32(&bars.full[s]));
-                if constexpr (C::kScales > 0)
-                    bulk_load(ring + (uint32_t)C::kStages * 2 * C::kHalf + (uint32_t)s * C::kScales + (lane >> 4) * kTile + x * box,
-                              (lane >> 4 ? p.Vs : p.Ks) + ((int64_t)page * p.Hkv + hk) * p.page + at, (uint32_t)box, smem_u32(&bars.full[s]));
+            if (mine && !bad && (!kParts || lane < 16)) {
+                const int at = (int)((pos + x * box) & (p.page - 1)), v = kParts ? part & 1 : lane >> 4;
+                if (!kParts || part < 2)
+                    tma_load4(ring + (uint32_t)s * 2 * C::kHalf + v * C::kHalf + x * (uint32_t)(box * C::kRowBytes), v ? &maps.v : &maps.k, 0,
+                              kParts ? at * D / 128 : at, 0, page * p.Hkv + hk, smem_u32(&bars.full[s]));
+                else if constexpr (kParts)
+                    bulk_load(ring + (uint32_t)C::kStages * 2 * C::kHalf + (uint32_t)s * C::kScales + v * C::kTokens + x * box,
+                              (v ? p.Vs : p.Ks) + ((int64_t)page * p.Hkv + hk) * p.page + at, (uint32_t)box, smem_u32(&bars.full[s]));
             }
         }
         if (give_up) {
-            if (lane == 0) *reinterpret_cast<volatile int*>(abort_sm) = 1;
+            if (first && lane == 0) *reinterpret_cast<volatile int*>(abort_sm) = 1;
             ok = false;
         }
         u += t1 - t0;
@@ -363,9 +371,10 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
                 gr = group_of<SH>(a, b);
             } while (SH && (tokens == 0 || gr.I == 0));               // (units are left: there is such a prefix)
             if (!SH) prior = prior_of(a.sh, b, lane) + 1;
-            tiles = tiles_of(tokens);
+            tiles = tiles_of<C::kTokens>(tokens);
         }
     }
+    if (!first) return;
     // the consumers' end
     for (int e = 0; e < NS && ok; ++e, ++i) {
         const int slot = i % NS;
@@ -546,17 +555,18 @@ __device__ void join_pieces(const Args& a, const Seg& g, int t, int* go, int* ar
 // The end of a CTA whose waits gave up (all threads, after all roles): no copy is left in flight, and its pieces
 // that were not counted are, so that every cell of the call ends at 0 (what the joins then make of their records
 // is as invalid as the call).
-template <int D, int S, int NS, bool SH, int NT = kThreads, typename B>
+template <int D, int S, int NS, bool SH, int NT = kThreads, int TILE = kTile, typename B>
 __device__ __noinline__ void settle(const Args& a, B& bars) {
     if (threadIdx.x == 0) {
         const int n = bars.issued, i = bars.given;
-        for (int x = max(0, n - S); x < n; ++x) mbar_wait(smem_u32(&bars.full[x % S]), (uint32_t)(x / S) & 1, kWaitNs);
+        // (of a tile's copies, those of a warp that met the end sooner are missing: then the others are waited for for long enough)
+        for (int x = max(0, n - S); x < n; ++x) mbar_wait(smem_u32(&bars.full[x % S]), (uint32_t)(x / S) & 1, kDrainNs);
         for (int x = max(0, i - NS); x < i; ++x) mbar_wait(smem_u32(&bars.seg_full[x % NS]), (uint32_t)(x / NS) & 1, kWaitNs);
     }
     if constexpr (SH) return;                                      // (nothing is counted)
     Start st;
-    if (!find_start<false, NT>(a, &st) || threadIdx.x != 0) return;
-    int b = st.b, tiles = tiles_of(paged_tokens(a.p, a.p.kv_len[b]));
+    if (!find_start<false, NT, TILE>(a, &st) || threadIdx.x != 0) return;
+    int b = st.b, tiles = tiles_of<TILE>(paged_tokens(a.p, a.p.kv_len[b]));
     int item = (int)(st.rem / tiles), t0 = (int)(st.rem % tiles);
     for (int64_t u = st.u0; u < st.u1;) {
         const int t1 = (int)min((int64_t)tiles, t0 + (st.u1 - u));
@@ -572,7 +582,7 @@ __device__ __noinline__ void settle(const Args& a, B& bars) {
         t0 = 0;
         if (++item == a.I && u < st.u1) {
             item = 0;
-            tiles = tiles_of(paged_tokens(a.p, a.p.kv_len[++b]));
+            tiles = tiles_of<TILE>(paged_tokens(a.p, a.p.kv_len[++b]));
         }
     }
 }
@@ -613,14 +623,14 @@ inline Args make_args(const DecodeArgs& d) {
 }
 
 template <typename T, int D, typename K>
-cudaError_t launch_kernel(K kernel, int consumers, std::atomic<uint64_t>& done, const DecodeArgs& d, cudaStream_t st) {
+cudaError_t launch_kernel(K kernel, int warps, std::atomic<uint64_t>& done, const DecodeArgs& d, cudaStream_t st) {
     using C = Cfg<T, D>;
     Maps maps;
     const auto ty = sizeof(T) == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                     : sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                      : CU_TENSOR_MAP_DATA_TYPE_UINT8;
     const int64_t depth = (int64_t)d.p.n_pages * d.p.Hkv;
-    const int rows = d.p.page < kTile ? d.p.page : kTile;
+    const int rows = d.p.page < C::kTokens ? d.p.page : C::kTokens;
     // (e4m3: rows of 128 bytes)
     const int wide = sizeof(T) == 1 ? 128 : D, fold = wide / D;
     if (!make_tmap_pages(&maps.k, ty, sizeof(T), d.p.K, wide, d.p.page / fold, depth, rows / fold, wide * (int)sizeof(T) / 128) ||
@@ -628,7 +638,7 @@ cudaError_t launch_kernel(K kernel, int consumers, std::atomic<uint64_t>& done, 
         return cudaErrorInvalidValue;
     cudaError_t e = opt_in_smem(kernel, C::kSmem, done);
     if (e != cudaSuccess) return e;
-    return launch_behind(kernel, kPieces, (consumers + 1) * kWarp, C::kSmem, st, maps, make_args(d));
+    return launch_behind(kernel, kPieces, warps * kWarp, C::kSmem, st, maps, make_args(d));
 }
 
 }  // namespace

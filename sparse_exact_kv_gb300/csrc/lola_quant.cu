@@ -43,7 +43,8 @@ __device__ __forceinline__ uint32_t turned(uint32_t x) {
 
 // NB: query rows in eights
 template <typename TO, int D, int NB> struct QSmem {
-    static constexpr int NW = NB == 1 ? 12 : 8;                             // consumer warps
+    static constexpr int NW = NB == 1 ? 12 : 8;                             // consumer warps, and all
+    static constexpr int kAll = NW + 4;
     static constexpr int kCk = NB == 1 ? 64 : 32;                           // columns joined at a time
     static constexpr int kPitch = D * (int)sizeof(TO) + 16;                 // Q rows
     float red[NW][8 * NB][kCk + 8];                                         // (rows 32 bytes apart: 8-byte stores of four rows)
@@ -51,10 +52,10 @@ template <typename TO, int D, int NB> struct QSmem {
     uint8_t q[2][kRows * kPitch];
 };
 
-// All warps on a segment, in groups of four that take its tiles in turn; a warp has 16 of a tile's 64 tokens.
+// All warps on a segment, in groups of four that take its tiles in turn; a warp has 32 of a tile's 128 tokens, 16 at a time.
 // TO: q and o.
 template <typename TO, int D, int NB, bool SH>
-__global__ void __launch_bounds__((QSmem<TO, D, NB>::NW + 1) * kWarp, 1) quant_decode_kernel(const __grid_constant__ Maps maps, const Args a) {
+__global__ void __launch_bounds__(QSmem<TO, D, NB>::kAll * kWarp, 1) quant_decode_kernel(const __grid_constant__ Maps maps, const Args a) {
     using T = uint8_t;
     using C = Cfg<T, D>;
     using M = QSmem<TO, D, NB>;
@@ -84,17 +85,17 @@ __global__ void __launch_bounds__((QSmem<TO, D, NB>::NW + 1) * kWarp, 1) quant_d
     }
     wait_for_last_kernel();
     Start st;
-    if (!find_start<SH, NT + kWarp>(a, &st)) return;
-    if (warp == NW) produce<T, TO, D, 2, SH>(maps, a, st, sb, smem_u32(x.q[0]), M::kPitch, bars, segs, bad_sm, &abort_sm, lane);
-    const int grp = warp >> 2, k0 = (warp & 3) * 16, g8 = lane >> 2, q4 = lane & 3, q2 = q4 * 2;
+    if (!find_start<SH, M::kAll * kWarp, C::kTokens>(a, &st)) return;
+    if (warp >= NW) produce<T, TO, D, 2, SH>(maps, a, st, sb, smem_u32(x.q[0]), M::kPitch, bars, segs, bad_sm, &abort_sm, lane, warp - NW);
+    const int grp = warp >> 2, g8 = lane >> 2, q4 = lane & 3, q2 = q4 * 2;
     auto bar = [&] { asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory"); };
-    const int box = min(p.page, kTile), lb = 31 - __clz(box);
+    const int box = min(p.page, C::kTokens), lb = 31 - __clz(box);
     // 16-byte chunk ch of token k's row: rows of 128 bytes (two tokens at d = 64), chunks swizzled
     auto chunk_at = [](int k, int ch) {
         const int row = k * D / 128, c = D == 128 ? ch : (k & 1) * 4 + ch;
         return (uint32_t)(row * 128 + (((c ^ row) & 7) << 4));
     };
-    const int token = k0 + ((lane >> 3) & 1) * 8 + (lane & 7), ch0 = lane >> 4;     // this lane's ldmatrix row
+    const int row0 = ((lane >> 3) & 1) * 8 + (lane & 7), ch0 = lane >> 4;           // this lane's ldmatrix row
     for (int i = 0; warp < NW; ++i) {
         const int slot = i & 1;
         if (group_or<NT>(1, !ring_wait(smem_u32(&bars.seg_full[slot]), (uint32_t)(i >> 1) & 1, &abort_sm))) {
@@ -172,110 +173,114 @@ __global__ void __launch_bounds__((QSmem<TO, D, NB>::NW + 1) * kWarp, 1) quant_d
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const uint32_t kt = sb + (uint32_t)s * 2 * C::kHalf, vt = kt + C::kHalf;
-            const uint8_t* powers = sm + (size_t)C::kStages * 2 * C::kHalf + (size_t)s * C::kScales + k0 + g8;
-            const int left = g.len - t * kTile;
+            const uint8_t* powers = sm + (size_t)C::kStages * 2 * C::kHalf + (size_t)s * C::kScales + g8;
+            const int left = g.len - t * C::kTokens;
             const uint32_t bad = bad_sm[s];
-            // ---- S^T: 16 tokens x 8 rows, two chains ----
-            float c0[NB][4] = {}, c1[NB][4] = {};
+#pragma unroll 1
+            for (int k0 = (warp & 3) * 32, half = 0; half < 2; ++half, k0 += 16) {
+                const int token = k0 + row0;
+                // ---- S^T: 16 tokens x 8 rows, two chains ----
+                float c0[NB][4] = {}, c1[NB][4] = {};
 #pragma unroll
-            for (int y = 0; y < D / 32; ++y) {
-                uint32_t kb[4];
-                ldsm4(kt + chunk_at(token, 2 * y + ch0), kb);
+                for (int y = 0; y < D / 32; ++y) {
+                    uint32_t kb[4];
+                    ldsm4(kt + chunk_at(token, 2 * y + ch0), kb);
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    uint32_t ka[4];                                    // tokens g8, g8 + 8: channels 4 q4, + 1; then + 2, + 3
-                    widen(kb[2 * z], ka[0], ka[2]);
-                    widen(kb[2 * z + 1], ka[1], ka[3]);
+                    for (int z = 0; z < 2; ++z) {
+                        uint32_t ka[4];                                    // tokens g8, g8 + 8: channels 4 q4, + 1; then + 2, + 3
+                        widen(kb[2 * z], ka[0], ka[2]);
+                        widen(kb[2 * z + 1], ka[1], ka[3]);
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        mma16816_h(z ? c1[b] : c0[b], ka, qa[b][2 * y + z][0], qa[b][2 * y + z][1]);
-                        if constexpr (kTwo) mma16816_h(z ? c1[b] : c0[b], ka, qr[b][2 * y + z][0], qr[b][2 * y + z][1]);
-                    }
-                }
-            }
-            // ---- scores and exponents of the weights: tokens k0 + g8 (0, 1), + 8 (2, 3) ----
-            float sc[NB][4], down[2];
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const uint32_t kp = powers[8 * y], vp = powers[kTile + 8 * y];
-                const float fk = __uint_as_float(kp << 23), fv = (float)(int)vp - 127.f;
-                down[y] = power_down(vp);
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) sc[b][2 * y + e] = fmaf((c0[b][2 * y + e] + c1[b][2 * y + e]) * qs[b][e], fk, fv);
-            }
-            if (left < k0 + 16 || bad) {
-                // tokens behind the sequence or on bad pages: no score, and their V rows (which may
-                // hold anything) become zero
-                const int nk = max(0, min(kTile, left));
-                auto hidden = [&](int k) { return k >= nk || ((bad >> (k >> lb)) & 1u); };
-#pragma unroll
-                for (int y = 0; y < 2; ++y)
-                    if (hidden(k0 + 8 * y + g8))
-#pragma unroll
-                        for (int b = 0; b < NB; ++b) sc[b][2 * y] = sc[b][2 * y + 1] = -INFINITY;
-                for (int k = k0; k < k0 + 16; ++k)
-                    if (hidden(k) && lane < D / 16)
-                        *reinterpret_cast<uint4*>(sm + (size_t)s * 2 * C::kHalf + C::kHalf + chunk_at(k, lane)) = make_uint4(0, 0, 0, 0);
-                fence_async_smem();            // (before the ring's next copy lands on these rows)
-                __syncwarp();
-            }
-            // ---- running maximum, weights ----
-            uint32_t pb[NB][2], pr[kTwo ? NB : 1][2];                  // tokens 2 q4, + 1 (+ 8) of row 8 b + g8
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                float top[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    top[e] = fmaxf(sc[b][e], sc[b][2 + e]);
-#pragma unroll
-                    for (int z = 4; z < kWarp; z <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], z));
-                    top[e] += kRaise;
-                }
-                const bool need[2] = {top[0] > m[b][0] + kRaise, top[1] > m[b][1] + kRaise};
-                if (__any_sync(0xffffffffu, need[0] || need[1])) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float f = need[e] ? ex2(m[b][e] - top[e]) : 1.f;
-                        if (need[e]) m[b][e] = top[e];
-                        l[b][e] *= f;
-#pragma unroll
-                        for (int y = 0; y < D / 16; ++y) {
-                            o[y][b][e] *= f;
-                            o[y][b][2 + e] *= f;
+                        for (int b = 0; b < NB; ++b) {
+                            mma16816_h(z ? c1[b] : c0[b], ka, qa[b][2 * y + z][0], qa[b][2 * y + z][1]);
+                            if constexpr (kTwo) mma16816_h(z ? c1[b] : c0[b], ka, qr[b][2 * y + z][0], qr[b][2 * y + z][1]);
                         }
                     }
                 }
-                float w[4];
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    const int e = z & 1;
-                    w[z] = ex2(sc[b][z] - (m[b][e] == -INFINITY ? 0.f : m[b][e]));
-                    l[b][e] = fmaf(w[z], down[z >> 1], l[b][e]);
-                    w[z] *= kUp;
-                }
+                // ---- scores and exponents of the weights: tokens k0 + g8 (0, 1), + 8 (2, 3) ----
+                float sc[NB][4], down[2];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const uint32_t h = half2_of(w[2 * y], w[2 * y + 1]);
-                    pb[b][y] = turned(h);
-                    if constexpr (kTwo) pr[b][y] = turned(half2_rest(w[2 * y], w[2 * y + 1], h));
+                    const uint32_t kp = powers[k0 + 8 * y], vp = powers[C::kTokens + k0 + 8 * y];
+                    const float fk = __uint_as_float(kp << 23), fv = (float)(int)vp - 127.f;
+                    down[y] = power_down(vp);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) sc[b][2 * y + e] = fmaf((c0[b][2 * y + e] + c1[b][2 * y + e]) * qs[b][e], fk, fv);
                 }
-            }
-            // ---- O^T += V^T P^T ----
+                if (left < k0 + 16 || bad) {
+                    // tokens behind the sequence or on bad pages: no score, and their V rows (which may
+                    // hold anything) become zero
+                    const int nk = max(0, min(C::kTokens, left));
+                    auto hidden = [&](int k) { return k >= nk || ((bad >> (k >> lb)) & 1u); };
 #pragma unroll
-            for (int y = 0; y < D / 32; ++y) {
-                uint32_t vb[4];
-                ldsm4_t(vt + chunk_at(token, 2 * y + ch0), vb);
+                    for (int y = 0; y < 2; ++y)
+                        if (hidden(k0 + 8 * y + g8))
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    uint32_t va[4];                                    // channels 2 g8, 2 g8 + 1: tokens 2 q4, + 1; then + 8, + 9
-                    widen(__byte_perm(vb[2 * z], 0u, 0x3120), va[0], va[1]);
-                    widen(__byte_perm(vb[2 * z + 1], 0u, 0x3120), va[2], va[3]);
+                            for (int b = 0; b < NB; ++b) sc[b][2 * y] = sc[b][2 * y + 1] = -INFINITY;
+                    for (int k = k0; k < k0 + 16; ++k)
+                        if (hidden(k) && lane < D / 16)
+                            *reinterpret_cast<uint4*>(sm + (size_t)s * 2 * C::kHalf + C::kHalf + chunk_at(k, lane)) = make_uint4(0, 0, 0, 0);
+                    fence_async_smem();            // (before the ring's next copy lands on these rows)
+                    __syncwarp();
+                }
+                // ---- running maximum, weights ----
+                uint32_t pb[NB][2], pr[kTwo ? NB : 1][2];                  // tokens 2 q4, + 1 (+ 8) of row 8 b + g8
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        mma16816_h(o[2 * y + z][b], va, pb[b][0], pb[b][1]);
-                        if constexpr (kTwo) mma16816_h(o[2 * y + z][b], va, pr[b][0], pr[b][1]);
+                for (int b = 0; b < NB; ++b) {
+                    float top[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        top[e] = fmaxf(sc[b][e], sc[b][2 + e]);
+#pragma unroll
+                        for (int z = 4; z < kWarp; z <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], z));
+                        top[e] += kRaise;
+                    }
+                    const bool need[2] = {top[0] > m[b][0] + kRaise, top[1] > m[b][1] + kRaise};
+                    if (__any_sync(0xffffffffu, need[0] || need[1])) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float f = need[e] ? ex2(m[b][e] - top[e]) : 1.f;
+                            if (need[e]) m[b][e] = top[e];
+                            l[b][e] *= f;
+#pragma unroll
+                            for (int y = 0; y < D / 16; ++y) {
+                                o[y][b][e] *= f;
+                                o[y][b][2 + e] *= f;
+                            }
+                        }
+                    }
+                    float w[4];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const int e = z & 1;
+                        w[z] = ex2(sc[b][z] - (m[b][e] == -INFINITY ? 0.f : m[b][e]));
+                        l[b][e] = fmaf(w[z], down[z >> 1], l[b][e]);
+                        w[z] *= kUp;
+                    }
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const uint32_t h = half2_of(w[2 * y], w[2 * y + 1]);
+                        pb[b][y] = turned(h);
+                        if constexpr (kTwo) pr[b][y] = turned(half2_rest(w[2 * y], w[2 * y + 1], h));
+                    }
+                }
+                // ---- O^T += V^T P^T ----
+#pragma unroll
+                for (int y = 0; y < D / 32; ++y) {
+                    uint32_t vb[4];
+                    ldsm4_t(vt + chunk_at(token, 2 * y + ch0), vb);
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        uint32_t va[4];                                    // channels 2 g8, 2 g8 + 1: tokens 2 q4, + 1; then + 8, + 9
+                        widen(__byte_perm(vb[2 * z], 0u, 0x3120), va[0], va[1]);
+                        widen(__byte_perm(vb[2 * z + 1], 0u, 0x3120), va[2], va[3]);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            mma16816_h(o[2 * y + z][b], va, pb[b][0], pb[b][1]);
+                            if constexpr (kTwo) mma16816_h(o[2 * y + z][b], va, pr[b][0], pr[b][1]);
+                        }
                     }
                 }
             }
@@ -346,14 +351,14 @@ __global__ void __launch_bounds__((QSmem<TO, D, NB>::NW + 1) * kWarp, 1) quant_d
         if (!SH && !g.whole) join_pieces<TO, D, NT>(a, g, tid, &go, bars.arrived, bar);
     }
     __syncthreads();
-    if (abort_sm) settle<D, C::kStages, 2, SH, NT + kWarp>(a, bars);
+    if (abort_sm) settle<D, C::kStages, 2, SH, M::kAll * kWarp, C::kTokens>(a, bars);
 }
 
 template <typename TO, int D, bool SH>
 cudaError_t launch_quant(const DecodeArgs& d, cudaStream_t st) {
     static std::atomic<uint64_t> done[2] = {};
-    return !SH && d.p.G <= 8 ? launch_kernel<uint8_t, D>(quant_decode_kernel<TO, D, 1, false>, QSmem<TO, D, 1>::NW, done[0], d, st)
-                             : launch_kernel<uint8_t, D>(quant_decode_kernel<TO, D, 2, SH>, QSmem<TO, D, 2>::NW, done[1], d, st);
+    return !SH && d.p.G <= 8 ? launch_kernel<uint8_t, D>(quant_decode_kernel<TO, D, 1, false>, QSmem<TO, D, 1>::kAll, done[0], d, st)
+                             : launch_kernel<uint8_t, D>(quant_decode_kernel<TO, D, 2, SH>, QSmem<TO, D, 2>::kAll, done[1], d, st);
 }
 
 template <bool SH> cudaError_t launch_quant(const DecodeArgs& a, cudaStream_t st) {
