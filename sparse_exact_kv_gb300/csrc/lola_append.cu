@@ -13,6 +13,8 @@
 // 74.5 us, 5.9 TB/s, 88 % of the measured copy rate) and by latency for one token per sequence (3.4 us
 // for 64).  The cosines of a token are formed once and read side by side by the lanes (eight reads of
 // 8 bytes a unit, four ways into the same banks, took 24 us of 98 more).
+#include <type_traits>
+
 #include "lola_attn.cuh"
 
 namespace lola {
@@ -117,47 +119,64 @@ __device__ __forceinline__ void finish_unit(Unit<T>& n, bool neighbours, int ste
 template <typename T, int UH>
 __device__ __forceinline__ void quantise_unit(Unit<T>& n, bool neighbours, int step, bool first) {
     constexpr int VN = 16 / sizeof(T);
-    float a[VN], b[VN];
-    uint32_t top = 0u;
+    float a[VN], b[VN], top = 0.f;
     if (n.power) {
         unpack<T>(n.x, a);
         unpack<T>(n.y, b);
         if (n.cs) turn_unit<VN>(a, b, n.cs, neighbours, step);
 #pragma unroll
-        for (int i = 0; i < VN; ++i) {
-            const uint32_t x = __float_as_uint(a[i]) & 0x7fffffffu, y = __float_as_uint(b[i]) & 0x7fffffffu;
-            if (x < 0x7f800000u) top = max(top, x);
-            if (y < 0x7f800000u) top = max(top, y);
-        }
+        for (int i = 0; i < VN; ++i) top = fmaxf(fmaxf(top, fabsf(a[i])), fabsf(b[i]));      // (NaN does not count)
     }
 #pragma unroll
-    for (int o = UH / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int o = UH / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (__any_sync(0xffffffffu, top == INFINITY)) {
+        // infinities somewhere: they become NaN, which the conversion keeps
+        top = 0.f;
+        if (n.power) {
+#pragma unroll
+            for (int i = 0; i < VN; ++i) {
+                a[i] = fabsf(a[i]) < INFINITY ? a[i] : NAN;
+                b[i] = fabsf(b[i]) < INFINITY ? b[i] : NAN;
+                top = fmaxf(fmaxf(top, fabsf(a[i])), fabsf(b[i]));
+            }
+        }
+#pragma unroll
+        for (int o = UH / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    }
     if (!n.power) return;
-    const int power = min(max((int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u), kLowPower), kTopPower);
+    const uint32_t bits = __float_as_uint(top);
+    const int power = min(max((int)(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u), kLowPower), kTopPower);
     const float down = __uint_as_float((uint32_t)(254 - power) << 23);
-    auto codes = [&](const float(&v)[VN], uint8_t* dst) {
-        uint32_t w[VN / 4];
+    auto codes = [&](const float(&v)[VN], uint32_t(&w)[VN / 4]) {
 #pragma unroll
         for (int i = 0; i < VN / 4; ++i) {
-            // (saturating, but infinities are no number of this type's)
-            auto num = [&](float x) { return fabsf(x) < INFINITY ? x * down : NAN; };
             uint16_t lo, hi;
-            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(num(v[4 * i + 1])), "f"(num(v[4 * i])));
-            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(num(v[4 * i + 3])), "f"(num(v[4 * i + 2])));
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[4 * i + 1] * down), "f"(v[4 * i] * down));
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[4 * i + 3] * down), "f"(v[4 * i + 2] * down));
             w[i] = (uint32_t)lo | ((uint32_t)hi << 16);
         }
-        if constexpr (VN == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-        else *reinterpret_cast<uint32_t*>(dst) = w[0];
     };
     uint8_t* dst = reinterpret_cast<uint8_t*>(n.dst);
-    codes(a, dst + n.c0);
-    codes(b, dst + n.c1);
+    uint32_t x[VN / 4], y[VN / 4];
+    codes(a, x);
+    codes(b, y);
+    if constexpr (VN == 8) {
+        if (n.c1 == n.c0 + VN) {
+            *reinterpret_cast<uint4*>(dst + n.c0) = make_uint4(x[0], x[1], y[0], y[1]);
+        } else {
+            *reinterpret_cast<uint2*>(dst + n.c0) = make_uint2(x[0], x[1]);
+            *reinterpret_cast<uint2*>(dst + n.c1) = make_uint2(y[0], y[1]);
+        }
+    } else {
+        *reinterpret_cast<uint32_t*>(dst + n.c0) = x[0];
+        *reinterpret_cast<uint32_t*>(dst + n.c1) = y[0];
+    }
     if (first) *n.power = (uint8_t)power;
 }
 
 // TOK tokens a CTA of NT threads; a thread has IN units in flight.  QZ: into a quantised cache.
 template <typename T, int D, int TOK, int NT, int IN, bool QZ>
-__global__ void __launch_bounds__(NT) paged_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(NT, QZ && TOK > 1 ? 8 : 1) paged_append_kernel(const AppendArgs a) {
     __shared__ __align__(16) float4 cs[TOK][D / 4];
     __shared__ uint64_t turn_sm[D / 2];
     __shared__ int64_t slot[TOK];      // element offset of (page, head 0, slot), -1: no slot, -2: skip the row
@@ -168,6 +187,18 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendArgs a) {
     const PagedArgs& p = a.p;
 
     wait_for_last_kernel();
+    if constexpr (QZ) {
+        // (the rows are on their way while positions, pages and cosines are found)
+        constexpr int LN = D * sizeof(T) / 128;                              // 128-byte lines of a head
+        const int hq = a.Q.data ? p.Hq : 0, heads = hq + 2 * p.Hkv;
+        for (int e = threadIdx.x; e < nt * heads * LN; e += NT) {
+            const int l = e % LN, th = e / LN, i = th / heads, h = th - i * heads;
+            const bool q = h < hq, v = h >= hq + p.Hkv;
+            const Rows& r = q ? a.Q : v ? a.V : a.K;
+            const char* at = r.data + ((int64_t)(t0 + i) * r.row + (int64_t)(q ? h : h - hq - (v ? p.Hkv : 0)) * r.head) * (int)sizeof(T) + 128 * l;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+        }
+    }
     for (int i = warp; i < nt; i += NT / kWarp) {
         const int t = t0 + i;
         int b = t;
@@ -214,50 +245,66 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(const AppendArgs a) {
         reinterpret_cast<float2*>(cs[i])[((f % VN / 2) * ru + f / VN) * 2 + (f & 1)] = make_float2(c, s);
     }
     __syncthreads();
-    const int hq = a.Q.data ? p.Hq : 0, heads = hq + 2 * p.Hkv, units = nt * heads * UH;
+    const int hq = a.Q.data ? p.Hq : 0;
     const bool nb = a.pairs == LOLA_PAIRS_NEIGHBOURS;
-    for (int e0 = threadIdx.x; (QZ ? e0 - lane : e0) < units; e0 += NT * IN) {
-        Unit<T> n[IN];
+    // heads h0 .. h0 + heads - 1 of the CTA's tokens (queries, keys, values, in this order); `some` of them are quantised
+    auto copy = [&](int h0, int heads, auto some) {
+        constexpr bool kSome = decltype(some)::value;
+        const int units = nt * heads * UH;
+        for (int e0 = threadIdx.x; (kSome ? e0 - lane : e0) < units; e0 += NT * IN) {
+            Unit<T> n[IN];
 #pragma unroll
-        for (int x = 0; x < IN; ++x) {
-            const int e = e0 + x * NT;
-            n[x].dst = nullptr;
-            n[x].power = nullptr;
-            if (e >= units) continue;
-            const int u = e % UH, th = e / UH;
-            int i = 0;                           // th / heads
+            for (int x = 0; x < IN; ++x) {
+                const int e = e0 + x * NT;
+                n[x].dst = nullptr;
+                n[x].power = nullptr;
+                if (e >= units) continue;
+                const int u = e % UH, th = e / UH;
+                int i = 0;                           // th / heads
 #pragma unroll
-            for (int z = 1; z < TOK; ++z) i += th >= z * heads;
-            const int h = th - i * heads;
-            const int64_t t = t0 + i, s = slot[i];
-            if (s == -2 || (s < 0 && h >= hq)) continue;
-            if (h < hq) {
-                load_unit<T>(n[x], reinterpret_cast<const T*>(a.Q.data) + t * a.Q.row + h * a.Q.head,
-                             reinterpret_cast<T*>(a.QO.data) + t * a.QO.row + h * a.QO.head, u, rot, nb, cs[i]);
-            } else {
-                const bool v = h >= hq + p.Hkv;
-                const int hk = h - hq - (v ? p.Hkv : 0);
-                const Rows& r = v ? a.V : a.K;
-                const int64_t at = s + (int64_t)hk * p.page * D;
-                load_unit<T>(n[x], reinterpret_cast<const T*>(r.data) + t * r.row + hk * r.head,
-                             QZ ? reinterpret_cast<T*>((v ? p.V : p.K) + at) : reinterpret_cast<T*>(v ? p.V : p.K) + at, u, v ? 0 : rot, nb,
-                             cs[i]);
-                if (QZ) n[x].power = (v ? p.Vs : p.Ks) + at / D;
+                for (int z = 1; z < TOK; ++z) i += th >= z * heads;
+                const int h = h0 + th - i * heads;
+                const int64_t t = t0 + i, s = slot[i];
+                if (s == -2 || (s < 0 && h >= hq)) continue;
+                if (h < hq) {
+                    load_unit<T>(n[x], reinterpret_cast<const T*>(a.Q.data) + t * a.Q.row + h * a.Q.head,
+                                 reinterpret_cast<T*>(a.QO.data) + t * a.QO.row + h * a.QO.head, u, rot, nb, cs[i]);
+                } else {
+                    const bool v = h >= hq + p.Hkv;
+                    const int hk = h - hq - (v ? p.Hkv : 0);
+                    const Rows& r = v ? a.V : a.K;
+                    const int64_t at = s + (int64_t)hk * p.page * D;
+                    load_unit<T>(n[x], reinterpret_cast<const T*>(r.data) + t * r.row + hk * r.head,
+                                 QZ ? reinterpret_cast<T*>((v ? p.V : p.K) + at) : reinterpret_cast<T*>(v ? p.V : p.K) + at, u, v ? 0 : rot,
+                                 nb, cs[i]);
+                    if (QZ) n[x].power = (v ? p.Vs : p.Ks) + at / D;
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < IN; ++x) {
+                if (kSome) quantise_unit<T, UH>(n[x], nb, ru, (e0 + x * NT) % UH == 0);
+                if (n[x].dst && !n[x].power) finish_unit<T>(n[x], nb, ru);
             }
         }
-#pragma unroll
-        for (int x = 0; x < IN; ++x) {
-            if (QZ) quantise_unit<T, UH>(n[x], nb, ru, (e0 + x * NT) % UH == 0);
-            if (n[x].dst && !n[x].power) finish_unit<T>(n[x], nb, ru);
-        }
+    };
+    if constexpr (QZ && TOK > 1) {
+        // (one behind the other: each loop's code and registers are its own)
+        copy(0, hq, std::false_type{});
+        copy(hq, 2 * p.Hkv, std::true_type{});
+    } else {
+        copy(0, hq + 2 * p.Hkv, std::bool_constant<QZ>{});
     }
 }
 
 // Few tokens: one a CTA, so that none waits for another's page lookup; many: four, whose rows of a head
 // lie side by side in the page (512 tokens, 32/8 heads: 4.5 us one a CTA, 5.5 us four; 1024: 7.4 and 6.6).
+// Into a quantised cache two, by CTAs of 128 threads, eight on an SM: more threads hide the longer way from a row's loads
+// to its stores (18 k tokens, 32/8 heads, page 16: 79 us, 5.1 TB/s, 76 % of the measured copy rate; four tokens by 256
+// threads, three units each, 96 us, two units 81; one token by 128 threads 117).
 template <typename T, int D, bool QZ>
 cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
     if (a.n_tokens <= kFew) return launch_behind(paged_append_kernel<T, D, 1, 128, 3, QZ>, (unsigned)a.n_tokens, 128, 0, st, a);
+    if (QZ) return launch_behind(paged_append_kernel<T, D, 2, 128, 2, QZ>, (unsigned)(a.n_tokens + 1) / 2, 128, 0, st, a);
     return launch_behind(paged_append_kernel<T, D, 4, 256, 3, QZ>, (unsigned)(a.n_tokens + 3) / 4, 256, 0, st, a);
 }
 template <typename T>

@@ -32,8 +32,8 @@ struct PagedArgs {
 // Prefixes that several sequences share: sequences cu[g] .. cu[g + 1] - 1 see the tokens of prefix g before their
 // own.  A kernel over the prefixes leaves, for every row (sequence, query head) i of a prefix with tokens, the parts
 // of its softmax (largest score m in log2 units, sum l and output z against m): one part in whole[i], ml[i], or the
-// parts of the prefix' pieces in records, piece after piece, the first of them at desc[i].y, row desc[i].z; desc[i].x
-// says how many.  A second kernel makes one part of those, and the kernel over the sequences' own tokens joins it with
+// parts of the prefix' pieces in records, the first of them number desc[i].y, the others in the first of two of every
+// desc[i].w-th CTA from there on, row desc[i].z; desc[i].x says how many.  A second kernel makes one part of those, and the kernel over the sequences' own tokens joins it with
 // its own.  (When the latter read all parts itself, row after row, 64 sequences behind 16001 tokens took it 92 us.)
 struct Prior {
     PagedArgs p;           // tables and lengths of the prefixes (p.n_seq of them); p.table null: there are none

@@ -501,10 +501,11 @@ __global__ void __launch_bounds__(256) prior_join_kernel(const Prior q, int64_t 
     wait_for_last_kernel();
     const int4 at = i < rows ? __ldcg(q.desc + i) : make_int4(0, 0, 0, 0);
     // (rows without a prefix, or behind a kernel whose waits gave up, may hold anything)
-    const bool mine = at.x >= 2 && at.x <= kPieces && at.y >= 0 && at.y / 2 <= kPieces - at.x && at.z >= 0 && at.z < q.rows;
+    const bool mine = at.x >= 2 && at.x <= kPieces && at.y >= 0 && at.w >= 1 && at.w <= kPieces && at.y / 2 + (at.x - 1) * at.w < kPieces &&
+                      at.z >= 0 && at.z < q.rows;
     const int n = mine ? at.x : 0, most = max(n, __shfl_xor_sync(0xffffffffu, n, 1));
     const int64_t size = prior_record(q.rows, D);
-    auto record_of = [&](int k) { return q.rec + (k == 0 ? at.y : (at.y / 2 + k) * 2) * size; };
+    auto record_of = [&](int k) { return q.rec + (k == 0 ? at.y : (at.y / 2 + k * at.w) * 2) * size; };
     float M = -INFINITY, L = 0.f;
     float4 y[kCols];
 #pragma unroll

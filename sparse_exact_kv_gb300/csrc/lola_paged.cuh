@@ -198,7 +198,8 @@ template <int S> struct Bars {
 // Which piece this CTA is and where it begins (all threads): false if there is none.
 struct Start {
     int64_t total, u0, u1, rem;   // units; rem: the first unit's number inside its sequence
-    int N, b;
+    int N, b;                     // pieces; the first unit's sequence
+    int piece;
 };
 template <bool SH, int NT = kThreads, int TILE = kTile, int ROWS = kRows>
 __device__ __forceinline__ bool find_start(const Args& a, Start* st) {
@@ -214,6 +215,7 @@ __device__ __forceinline__ bool find_start(const Args& a, Start* st) {
     for (int b = threadIdx.x + NT; b < p.n_seq; b += NT) rest += count(b);
     st->total = block_total<NT>(own + rest, sums);
     st->N = pieces_of(st->total);
+    st->piece = (int)blockIdx.x;
     if (SH && bits) atomicOr(&g_status, bits);
     if ((int)blockIdx.x >= st->N) return false;
     st->u0 = split_at(st->total, st->N, blockIdx.x);
@@ -254,7 +256,7 @@ __device__ __forceinline__ bool find_start(const Args& a, Start* st) {
 __device__ __forceinline__ void place_piece(const Start& st, int64_t xs, int tiles, Seg* g) {
     g->c0 = split_of(st.total, st.N, xs);
     g->np = split_of(st.total, st.N, xs + tiles - 1) - g->c0 + 1;
-    g->k = (int)blockIdx.x - g->c0;
+    g->k = st.piece - g->c0;
     g->s0 = xs != split_at(st.total, st.N, g->c0);
 }
 
@@ -439,7 +441,7 @@ __device__ __forceinline__ void write_out(const Args& a, const Seg& g, bool whol
                 rec[kRows * D + kRows + r] = L;
             }
         }
-        if (c == 0 && (whole || g.k == 0)) q.desc[i] = whole ? make_int4(1, 0, 0, 0) : make_int4(g.np, 2 * g.c0 + g.s0, r, 0);
+        if (c == 0 && (whole || g.k == 0)) q.desc[i] = whole ? make_int4(1, 0, 0, 0) : make_int4(g.np, 2 * g.c0 + g.s0, r, 1);
     } else if (whole) {
         if (g.prior) add_prior<D>(a.sh, (int64_t)g.b * a.p.Hq + g.h0 + r, c, y, M, L);
         // (no token seen: o = 0; scores that are all minus infinity: 0 / 0)

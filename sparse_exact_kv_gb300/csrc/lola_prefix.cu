@@ -5,7 +5,10 @@
 //   S = Q K^T,  P = 2^{c S - m},  l += sum P,  O += P V.
 // No row is masked but by the prefix' length.  The (prefix, key head, 256 rows, block) units are counted in that order
 // and cut into as many equal pieces as there are SMs, so that one prefix alone fills the GPU; a piece leaves (m, l, O) of
-// each of its segments for the kernel over the sequences' own tokens, which joins them (lola_paged.cuh).
+// each of its segments for the kernel that joins them (lola_paged.cu).  With one prefix of more than 256 rows, the row
+// items of the same keys are side by side in time: the units are (key head, block), and as many CTAs as there are row
+// items take a piece, so that keys and values come from HBM once (counted one item behind the other, 512 rows of
+// 128000 tokens read them twice: 8 heads, d = 128, 218 us).
 // An item of up to 128 rows has one tile of them: then its two halves are the even and the odd blocks, so that one half's
 // softmax runs beside the other's products, and the halves are added at the segment's end.
 // Warps: 0-3, 4-7 softmax of tile 0, 1 (one thread per row: Q rows to shared memory, S into registers, maximum, weights, P
@@ -97,8 +100,64 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
     }
     wait_for_last_kernel();
     Start st;
-    if (!find_start<true, C::kThreads, kN, kItem>(a, &st)) return;
+    int share = 1;                           // CTAs of a piece, one for each row item
+    if (p.n_seq == 1) {
+        int bits = 0;
+        const Group gr = group_of<true, kItem>(a, 0, &bits);
+        const int64_t tokens = paged_tokens(p, p.kv_len[0]);
+        if (bits && tid == 0) atomicOr(&g_status, bits);
+        share = gr.RG > 1 && gr.RG <= kPieces / 2 ? gr.RG : 1;
+        st.total = tokens == 0 ? 0 : (int64_t)tiles_of<kN>(tokens) * (share > 1 ? p.Hkv : gr.I);
+        st.N = (int)min((int64_t)(kPieces / share), st.total);
+        st.piece = (int)blockIdx.x / share;
+        st.b = 0;
+        if (st.piece >= st.N) return;
+        st.rem = st.u0 = split_at(st.total, st.N, st.piece);
+        st.u1 = split_at(st.total, st.N, st.piece + 1);
+    } else if (!find_start<true, C::kThreads, kN, kItem>(a, &st)) {
+        return;
+    }
     if (warp == C::kMmaWarp) tmem_alloc<512>(smem_u32(&tmem_base));
+    // ---- the loader's place: its item and block, and the segment that begins there ----
+    int w_b = st.b, w_tokens = 0, w_tiles = 1, w_item = 0, w_t0 = 0, w_page = -1;
+    Group w_gr{};
+    const int w_box = min(p.page, kN);
+    // the page of this lane's box of block t (up to t1)
+    auto page_of = [&](int t, int t1) {
+        const int pos = t * kN + (lane & 7) * w_box;
+        return t < t1 && (lane & 7) * w_box < kN && pos < w_tokens ? paged_page(p, w_b, pos) : -1;
+    };
+    // the segment from unit u on, as number `seg`, its first stage and block n and blk
+    auto make_seg = [&](int64_t u, int seg, int n, int blk) {
+        const int t1 = (int)min((int64_t)w_tiles, w_t0 + (st.u1 - u));
+        PSeg g;
+        g.m0 = w_gr.m0;
+        g.r0 = share > 1 ? (int)blockIdx.x % share * kItem : (w_item % w_gr.RG) * kItem;
+        g.R = min(kItem, w_gr.rows - g.r0);
+        g.hk = share > 1 ? w_item : w_item / w_gr.RG;
+        g.nb = t1 - w_t0;
+        g.len = w_tokens - w_t0 * kN;
+        g.n0 = n;
+        g.blk0 = blk;
+        g.whole = g.nb == w_tiles;
+        g.k = g.np = g.rec = 0;
+        if (!g.whole) {
+            Seg x;
+            place_piece(st, u - w_t0, w_tiles, &x);
+            g.k = x.k;
+            g.np = x.np;
+            g.rec = 2 * (x.c0 * share + (int)blockIdx.x % share) + x.s0;
+        }
+        segs[seg & 1] = g;
+    };
+    if (warp == C::kLoadWarp) {
+        w_tokens = (int)paged_tokens(p, p.kv_len[w_b]);
+        w_gr = group_of<true, kItem>(a, w_b);
+        w_tiles = tiles_of<kN>(w_tokens);
+        w_item = divide(st.rem, w_tiles, &w_t0);
+        w_page = page_of(w_t0, w_tiles);
+        if (lane == 0) make_seg(st.u0, 0, 0, 0);
+    }
     fence_before();
     __syncthreads();
     fence_after();
@@ -121,57 +180,32 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
         if constexpr (!QZ) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == C::kLoadWarp) {
             // ================================ pages and loads ================================
-            const int box = min(p.page, kN), lb = 31 - __clz(box), nbox = kN >> lb;     // tokens of a box, boxes of a block
+            const int box = w_box, lb = 31 - __clz(box), nbox = kN >> lb;               // tokens of a box, boxes of a block
             const int half = lane >> 3, by = (lane & 7) << lb;                         // this lane's box (half: 64 channels)
-            int b = st.b, tokens = (int)paged_tokens(p, p.kv_len[b]);
-            Group gr = group_of<true, kItem>(a, b);
-            int tiles = tiles_of<kN>(tokens), t0, item = divide(st.rem, tiles, &t0);
             int64_t u = st.u0;
             int seg = 0, n = 0, blk = 0;
             bool ok = true;
             uint32_t wrong = 0;
             while (u < st.u1 && ok) {
-                const int t1 = (int)min((int64_t)tiles, t0 + (st.u1 - u)), nb = t1 - t0;
-                const int hk = item / gr.RG, r0 = (item % gr.RG) * kItem;
                 if (seg >= 2 && !(ok = wait_all(B_SEGFREE + (seg & 1), (uint32_t)(seg / 2 - 1)))) break;
-                const int look = gr.rows - r0 > kM ? 1 : 2;
+                if (seg > 0 && lane == 0) make_seg(u, seg, n, blk);
+                const int t0 = w_t0, t1 = (int)min((int64_t)w_tiles, t0 + (st.u1 - u)), nb = t1 - t0, tokens = w_tokens;
+                const int r0 = share > 1 ? (int)blockIdx.x % share * kItem : (w_item % w_gr.RG) * kItem;
+                const int hk = share > 1 ? w_item : w_item / w_gr.RG, look = w_gr.rows - r0 > kM ? 1 : 2;
                 if (lane == 0) {
-                    PSeg g;
-                    g.m0 = gr.m0;
-                    g.r0 = r0;
-                    g.R = min(kItem, gr.rows - r0);
-                    g.hk = hk;
-                    g.nb = nb;
-                    g.len = tokens - t0 * kN;
-                    g.n0 = n;
-                    g.blk0 = blk;
-                    g.whole = nb == tiles;
-                    g.k = g.np = g.rec = 0;
-                    if (!g.whole) {
-                        Seg x;
-                        place_piece(st, u - t0, tiles, &x);
-                        g.k = x.k;
-                        g.np = x.np;
-                        g.rec = 2 * x.c0 + x.s0;
-                    }
-                    segs[seg & 1] = g;
-                    if (p.kv_len[b] > tokens) wrong = 1;
+                    if (p.kv_len[w_b] > tokens) wrong = 1;
                     mbar_arrive1(bar(B_SEG + (seg & 1)));
                 }
+                // the page of this lane's box of the next block, and of those that wait for their V
+                int next = seg == 0 ? (t0 < t1 ? w_page : -1) : page_of(t0, t1), now = -1, held[2] = {-1, -1};
                 ++seg;
-                // the page of this lane's box of block t, and of those that wait for their V
-                auto page_of = [&](int t) {
-                    const int pos = t * kN + by;
-                    return t < t1 && (lane & 7) < nbox && pos < tokens ? paged_page(p, b, pos) : -1;
-                };
-                int next = page_of(t0), now = -1, held[2] = {-1, -1};
                 const bool give_up = gives_up(a.give_up, blk, nb);
                 const int stop = give_up ? a.give_up - blk : nb + look;
                 for (int x = 0; x < stop && ok; ++x) {
                     held[1] = held[0];
                     held[0] = now;
                     now = next;
-                    next = page_of(t0 + x + 1);
+                    next = page_of(t0 + x + 1, t1);
 #pragma unroll
                     for (int kv = 1; kv >= 0; --kv) {
                         const int t = t0 + (kv ? x - look : x);
@@ -217,15 +251,15 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
                     ok = false;
                 }
                 u += nb;
-                t0 = 0;
-                if (++item == gr.I && u < st.u1) {
-                    item = 0;
+                w_t0 = 0;
+                if (++w_item == (share > 1 ? p.Hkv : w_gr.I) && u < st.u1) {
+                    w_item = 0;
                     do {                                               // (units are left: there is such a prefix)
-                        ++b;
-                        tokens = (int)paged_tokens(p, p.kv_len[b]);
-                        gr = group_of<true, kItem>(a, b);
-                    } while (tokens == 0 || gr.I == 0);
-                    tiles = tiles_of<kN>(tokens);
+                        ++w_b;
+                        w_tokens = (int)paged_tokens(p, p.kv_len[w_b]);
+                        w_gr = group_of<true, kItem>(a, w_b);
+                    } while (w_tokens == 0 || w_gr.I == 0);
+                    w_tiles = tiles_of<kN>(w_tokens);
                 }
             }
             // the others' end
@@ -283,7 +317,7 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
                     }
                     for (int j = 0; j < g.nb && ok; ++j) {
                         const bool more = j + look < g.nb;
-                        ok = full(n) && (!more || full(n + 1));
+                        ok = full(n);
                         const uint32_t v = desc_lo(sb + stage_at(n), 16384);
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
@@ -293,11 +327,16 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
 #pragma unroll
                                 for (int y = 0; y < kN / 16; ++y)
                                     mma_ts(tb + C::TO(i), tb + C::TS(i) + 8 * y, v + 128u * y, hi, id_o, y > 0 ? 1u : (uint32_t)(j >= look));
-                                if (more) s_mma(i, n + 1);
-                                else mma_commit(bar(B_O + i));
+                                const bool last = !two || i == 1;                  // (tile of the block)
+                                if (last) mma_commit(bar(B_EMPTY + n % kRing));
+                                if (!more) {
+                                    mma_commit(bar(B_O + i));
+                                } else {
+                                    if (!(ok = full(n + 1))) break;
+                                    s_mma(i, n + 1);
+                                    if (last) mma_commit(bar(B_EMPTY + (n + 1) % kRing));
+                                }
                             }
-                        mma_commit(bar(B_EMPTY + n % kRing));
-                        if (more) mma_commit(bar(B_EMPTY + (n + 1) % kRing));
                         n += 1 + more;
                     }
                 }
@@ -396,40 +435,38 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
             const int tile_row = two ? kM * i : 0;
             if (n > 0) {
                 // ---- Q rows of the tile, 16 bytes a lane, into the layout that the products read ----
-                constexpr int CH = D / 8, PER = 32 / CH, kBatch = 8;            // chunks of a row; rows at a time; times in flight
-                const int ch = lane % CH;
-                for (int x0 = 0; x0 < 32; x0 += PER * kBatch) {
-                    uint4 z[kBatch];
+                constexpr int CH = D / 8, PER = 32 / CH;                        // chunks of a row; rows at a time
+                const int ch = lane % CH, row0 = (warp & 3) * 32 + lane / CH;
+                const uint32_t q_at = smem_u32(Qt) + 16384u * (ch >> 3);
+                int flat = g.r0 + tile_row + row0, seq = flat / p.G, h = flat - seq * p.G;
+                const char* src = a.Q.data + ((int64_t)(g.m0 + seq) * a.Q.row + (int64_t)(g.hk * p.G + h) * a.Q.head + 8 * ch) * 2;
+#pragma unroll 1
+                for (int x = 0; x < 32; x += PER) {
+                    const bool in = tile_row + row0 + x < g.R;
+                    cp_async16_z(q_at + kmaj_chunk(row0 + x, ch & 7), in ? src : a.Q.data, in ? 16u : 0u);
+                    src += (int64_t)PER * a.Q.head * 2;
+                    for (h += PER; h >= p.G; h -= p.G) src += (a.Q.row - (int64_t)p.G * a.Q.head) * 2;
+                }
+                cp_async_wait_all();
+                if constexpr (QZ) {
+                    // float16 numbers, the row's largest magnitude in [2^14, 2^15)
+#pragma unroll 4
+                    for (int x = 0; x < 32; x += PER) {
+                        uint4* at = reinterpret_cast<uint4*>(Qt + 16384 * (ch >> 3) + kmaj_chunk(row0 + x, ch & 7));
+                        const uint4 z = *at;
+                        uint32_t w[4] = {z.x, z.y, z.z, z.w}, big = 0u;
 #pragma unroll
-                    for (int x = 0; x < kBatch; ++x) {
-                        const int row = tile_row + (warp & 3) * 32 + x0 + x * PER + lane / CH;
-                        z[x] = make_uint4(0, 0, 0, 0);
-                        if (row < g.R) {
-                            const int flat = g.r0 + row, seq = flat / p.G;
-                            z[x] = *reinterpret_cast<const uint4*>(a.Q.data + ((int64_t)(g.m0 + seq) * a.Q.row +
-                                                                               (int64_t)(g.hk * p.G + flat - seq * p.G) * a.Q.head + 8 * ch) * 2);
-                        }
-                    }
+                        for (int y = 0; y < 4; ++y) big = max(big, max((w[y] << 16) & 0x7fff0000u, w[y] & 0x7fff0000u));
 #pragma unroll
-                    for (int x = 0; x < kBatch; ++x) {
-                        const int rr = (warp & 3) * 32 + x0 + x * PER + lane / CH;
-                        if constexpr (QZ) {
-                            // float16 numbers, the row's largest magnitude in [2^14, 2^15)
-                            uint32_t w[4] = {z[x].x, z[x].y, z[x].z, z[x].w}, big = 0u;
+                        for (int o = 1; o < CH; o <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+                        const uint32_t up = min(268u - (big >> 23), 240u);
+                        const float f = __uint_as_float(up << 23);
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) big = max(big, max((w[y] << 16) & 0x7fff0000u, w[y] & 0x7fff0000u));
-#pragma unroll
-                            for (int o = 1; o < CH; o <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
-                            const uint32_t up = min(268u - (big >> 23), 240u);
-                            const float f = __uint_as_float(up << 23);
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) w[y] = half2_of(__uint_as_float(w[y] << 16) * f, __uint_as_float(w[y] & 0xffff0000u) * f);
-                            z[x] = make_uint4(w[0], w[1], w[2], w[3]);
-                            const int at = x0 + x * PER;                        // this time's first row of the warp's 32
-                            const uint32_t mine = __shfl_sync(0xffffffffu, up, ((lane - at) * CH) & 31);
-                            if (lane >= at && lane < at + PER) c = a.scale_log2 * __uint_as_float((254u - mine) << 23);
-                        }
-                        *reinterpret_cast<uint4*>(Qt + 16384 * (ch >> 3) + kmaj_chunk(rr, ch & 7)) = z[x];
+                        for (int y = 0; y < 4; ++y) w[y] = half2_of(__uint_as_float(w[y] << 16) * f, __uint_as_float(w[y] & 0xffff0000u) * f);
+                        *at = make_uint4(w[0], w[1], w[2], w[3]);
+                        // (rows x .. x + PER - 1 of the warp's 32 are those of lanes x ..)
+                        const uint32_t mine = __shfl_sync(0xffffffffu, up, ((lane - x) * CH) & 31);
+                        if (lane >= x && lane < x + PER) c = a.scale_log2 * __uint_as_float((254u - mine) << 23);
                     }
                 }
                 fence_async_smem();
@@ -615,7 +652,7 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
                     rec[kItem * D + row] = m;
                     rec[kItem * D + kItem + row] = l;
                 }
-                if (g.whole || g.k == 0) q.desc[at] = g.whole ? make_int4(1, 0, 0, 0) : make_int4(g.np, g.rec, row, 0);
+                if (g.whole || g.k == 0) q.desc[at] = g.whole ? make_int4(1, 0, 0, 0) : make_int4(g.np, g.rec, row, share);
             }
             fence_before();
             if (pair) {
