@@ -29,23 +29,24 @@ struct PagedArgs {
     uint8_t* Vs;         // or null
 };
 
-// Prefixes that several sequences share: sequences cu[g] .. cu[g + 1] - 1 see the tokens of prefix g before their
-// own.  A kernel over the prefixes leaves, for every row (sequence, query head) i of a prefix with tokens, the parts
-// of its softmax (largest score m in log2 units, sum l and output z against m): one part in whole[i], ml[i], or the
-// parts of the prefix' pieces in records, the first of them number desc[i].y, the others in the first of two of every
-// desc[i].w-th CTA from there on, row desc[i].z; desc[i].x says how many.  A second kernel makes one part of those, and the kernel over the sequences' own tokens joins it with
-// its own.  (When the latter read all parts itself, row after row, 64 sequences behind 16001 tokens took it 92 us.)
-struct Prior {
-    PagedArgs p;           // tables and lengths of the prefixes (p.n_seq of them); p.table null: there are none
-    const int32_t* cu;     // null: one prefix for all sequences
-    int n_seq;             // sequences
+// Parts of softmaxes, left for a kernel that joins them (lola_shared.cu): of row (sequence, query head) i, largest score m in
+// log2 units, sum l and output z against m.  One part in whole[i], ml[i], or the parts of several pieces in records, the first
+// of them number desc[i].y, the others in the first of two of every desc[i].w-th CTA from there on, row desc[i].z; desc[i].x
+// says how many.  Nothing is there for a row without tokens.
+struct Parts {
     int4* desc;
     float* whole;          // [n_seq * Hq][d]
     float2* ml;
     float* rec;            // records of `rows` rows: z, where row r's columns 4 x .. 4 x + 3 are at r row_step + x chunk_step,
     int rows, row_step, chunk_step;      // then m [rows], l [rows]
 };
-__host__ __device__ constexpr int64_t prior_record(int rows, int d) { return (int64_t)rows * (d + 2); }
+__host__ __device__ constexpr int64_t part_record(int rows, int d) { return (int64_t)rows * (d + 2); }
+
+// Which sequences see the tokens of entry g of a page table: g itself (each), or cu[g] .. cu[g + 1] - 1 (all, where cu is null).
+struct Sharing {
+    const int32_t* cu;
+    int n_seq, each;
+};
 
 // one lola_attn_prefill or lola_paged_prefill
 struct AttnArgs {
@@ -113,20 +114,6 @@ __device__ __forceinline__ int warp_find_seq(const int32_t* cu, int n_seq, int t
     }
     return lo;
 }
-// The prefix of sequence b (one warp), if it has one with tokens, or -1: where offsets are malformed, only one whose
-// kernel has worked for b too.
-__device__ __forceinline__ int prior_of(const Prior& q, int b, int lane) {
-    if (!q.p.table) return -1;
-    int g = 0, lo, n, bad = 0;
-    if (q.cu) {
-        g = warp_find_seq(q.cu, q.p.n_seq, b, lane);
-        if (g < 0 || g >= q.p.n_seq) return -1;
-        seq_rows(q.cu, g, q.n_seq, &lo, &n, &bad);
-        if (b < lo || b >= lo + n) return -1;
-    }
-    return paged_tokens(q.p, q.p.kv_len[g]) > 0 ? g : -1;
-}
-
 // Piece c of n equal pieces of `total` units: [split_at(c), split_at(c + 1)).  (Divisions of 64 bits take hundreds of
 // clocks, and a kernel begins with half a dozen of them: 32 bits where they do.)
 __host__ __device__ inline int64_t split_at(int64_t total, int n, int c) {
@@ -277,8 +264,9 @@ struct AppendArgs {
 cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t st);
 int64_t paged_decode_workspace(int d);
 struct DecodeArgs {
-    PagedArgs p;             // launch_*_prefix: of the prefixes
-    Prior sh;
+    PagedArgs p;             // launch_*_parts: of the prefixes, or of the sequences' own tokens
+    Sharing sh;
+    Parts parts;             // launch_*_parts: what they leave
     Rows Q, O;
     float* lse;
     float* part;             // workspace
@@ -287,14 +275,23 @@ struct DecodeArgs {
     float scale_log2;
 };
 cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t st);
-// Bytes of the workspace of `q`'s arrays; lays them out from `base` on, where q is given.
-int64_t prior_workspace(int n_seq, int Hq, int d, int dtype, char* base, Prior* q);
+cudaError_t launch_paged_parts(const DecodeArgs& a, cudaStream_t st);
+cudaError_t launch_quant_parts(const DecodeArgs& a, cudaStream_t st);
 constexpr int kPrefixRows = 256;         // rows of a record of launch_prefix_tc, column chunks one behind the other
-cudaError_t launch_prefix_tc(const DecodeArgs& a, cudaStream_t st);       // bf16 io
-cudaError_t launch_paged_prefix(const DecodeArgs& a, cudaStream_t st);
-cudaError_t launch_prior_join(const DecodeArgs& a, cudaStream_t st);
+cudaError_t launch_prefix_tc(const DecodeArgs& a, cudaStream_t st);       // bf16 io: prefixes
+struct SharedArgs {
+    PagedArgs p, prefix;     // the sequences' own tokens; the prefixes
+    const int32_t* cu;
+    Rows Q, O;
+    float* lse;
+    char* workspace;
+    int give_up;
+    float scale_log2;
+};
+int64_t shared_workspace(int n_seq, int Hq, int d, int dtype);
+cudaError_t launch_shared_prefix(const SharedArgs& a, cudaStream_t st);
+cudaError_t launch_shared_own(const SharedArgs& a, cudaStream_t st);
 cudaError_t launch_quant_decode(const DecodeArgs& a, cudaStream_t st);
-cudaError_t launch_quant_prefix(const DecodeArgs& a, cudaStream_t st);
 struct ReadArgs {
     PagedArgs p;
     int total;               // rows

@@ -877,7 +877,8 @@ static int32_t decode_args(const lola_attn_config* cfg, const lola_paged_kv* kv,
         return LOLA_ERR_INVALID_ARG;
     if (!workspace || !aligned16(workspace)) return LOLA_ERR_INVALID_ARG;
     if ((int64_t)workspace_bytes < need) return LOLA_ERR_WORKSPACE;
-    a->sh = Prior{};
+    a->sh = Sharing{};
+    a->parts = Parts{};
     a->Q = to_rows(Q);
     a->O = to_rows(O);
     a->lse = lse;
@@ -915,7 +916,7 @@ int64_t lola_shared_decode_workspace_bytes(const lola_attn_config* cfg, int32_t 
     if (s != LOLA_OK) return s;
     if (n_seq < 1) return LOLA_ERR_INVALID_ARG;
     if ((int64_t)n_seq * cfg->Hq > kMostRows) return LOLA_ERR_UNSUPPORTED;
-    return paged_decode_workspace(cfg->d) + prior_workspace(n_seq, cfg->Hq, cfg->d, cfg->dtype, nullptr, nullptr);
+    return shared_workspace(n_seq, cfg->Hq, cfg->d, cfg->dtype);
 }
 
 int32_t lola_shared_decode(const lola_attn_config* cfg, const lola_paged_kv* kv, const lola_kv_scales* scales,
@@ -929,31 +930,26 @@ int32_t lola_shared_decode(const lola_attn_config* cfg, const lola_paged_kv* kv,
         x->table_stride < x->width || (!x->cu && x->n != 1))
         return LOLA_ERR_INVALID_ARG;
     if ((int64_t)kv->n_seq * cfg->Hq > kMostRows || (int64_t)x->width * kv->page > 0x7fff0000) return LOLA_ERR_UNSUPPORTED;
-    const int64_t own = paged_decode_workspace(cfg->d);
-    s = decode_args(cfg, kv, Q, O, lse, workspace, workspace_bytes, own + prior_workspace(kv->n_seq, cfg->Hq, cfg->d, cfg->dtype, nullptr, nullptr), &a);
+    s = decode_args(cfg, kv, Q, O, lse, workspace, workspace_bytes, shared_workspace(kv->n_seq, cfg->Hq, cfg->d, cfg->dtype), &a);
     if (s != LOLA_OK) return s;
-    Prior& q = a.sh;
-    q.p = a.p;
-    q.p.n_seq = x->n;
-    q.p.width = x->width;
-    q.p.table_stride = x->table_stride;
-    q.p.table = x->table;
-    q.p.kv_len = x->len;
-    q.cu = x->cu;
-    q.n_seq = kv->n_seq;
-    prior_workspace(kv->n_seq, cfg->Hq, cfg->d, cfg->dtype, static_cast<char*>(workspace) + own, &q);
-    DecodeArgs first = a;
-    first.p = q.p;
+    SharedArgs b;
+    b.p = b.prefix = a.p;
+    b.prefix.n_seq = x->n;
+    b.prefix.width = x->width;
+    b.prefix.table_stride = x->table_stride;
+    b.prefix.table = x->table;
+    b.prefix.kv_len = x->len;
+    b.cu = x->cu;
+    b.Q = a.Q;
+    b.O = a.O;
+    b.lse = lse;
+    b.workspace = static_cast<char*>(workspace);
+    b.give_up = a.give_up;
+    b.scale_log2 = a.scale_log2;
     cudaStream_t st = (cudaStream_t)stream;
-    cudaError_t e = traced(LOLA_KERNEL_PREFIX, st, [&]() { 
-
-        const cudaError_t r = cfg->dtype == LOLA_BF16 ? launch_prefix_tc(first, st)
-                              : scales                ? launch_quant_prefix(first, st)
-                                                      : launch_paged_prefix(first, st);
-        return r == cudaSuccess ? launch_prior_join(first, st) : r;
-    });
+    cudaError_t e = traced(LOLA_KERNEL_PREFIX, st, [&]() { return launch_shared_prefix(b, st); });
     if (e != cudaSuccess) return cuda_fail(e, "shared prefix");
-    e = traced(LOLA_KERNEL_PAGED, st, [&]() { return scales ? launch_quant_decode(a, st) : launch_paged_decode(a, st); });
+    e = traced(LOLA_KERNEL_PAGED, st, [&]() { return launch_shared_own(b, st); });
     return e == cudaSuccess ? LOLA_OK : cuda_fail(e, "shared decode");
 }
 

@@ -477,80 +477,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_mma_kernel(const __g
     if (abort_sm) settle<D, C::kStages, 2, SH>(a, bars);
 }
 
+// (rows of a prefix: as many as its sequences have)
 template <int D, bool SH>
 cudaError_t launch_f32(const DecodeArgs& d, cudaStream_t st) {
     static std::atomic<uint64_t> done[3] = {};
-    if (!SH && d.p.G <= 4) return launch_kernel<float, D>(paged_decode_f32_kernel<D, 4, false>, kThreads / kWarp, done[0], d, st);
-    if (!SH && d.p.G <= 8) return launch_kernel<float, D>(paged_decode_f32_kernel<D, 8, false>, kThreads / kWarp, done[1], d, st);
+    const int rows = !SH || d.sh.each ? d.p.G : kRows;
+    if (rows <= 4) return launch_kernel<float, D>(paged_decode_f32_kernel<D, 4, SH>, kThreads / kWarp, done[0], d, st);
+    if (rows <= 8) return launch_kernel<float, D>(paged_decode_f32_kernel<D, 8, SH>, kThreads / kWarp, done[1], d, st);
     return launch_kernel<float, D>(paged_decode_f32_kernel<D, 16, SH>, kThreads / kWarp, done[2], d, st);
 }
 template <int D, bool SH>
 cudaError_t launch_bf16(const DecodeArgs& d, cudaStream_t st) {
     static std::atomic<uint64_t> done[2] = {};
-    return !SH && d.p.G <= 8 ? launch_kernel<__nv_bfloat16, D>(paged_decode_mma_kernel<D, true, false>, kThreads / kWarp, done[0], d, st)
-                             : launch_kernel<__nv_bfloat16, D>(paged_decode_mma_kernel<D, false, SH>, kThreads / kWarp, done[1], d, st);
+    return d.p.G <= 8 ? launch_kernel<__nv_bfloat16, D>(paged_decode_mma_kernel<D, true, SH>, kThreads / kWarp, done[0], d, st)
+                      : launch_kernel<__nv_bfloat16, D>(paged_decode_mma_kernel<D, false, SH>, kThreads / kWarp, done[1], d, st);
 }
-// ---- one part of the parts that the pieces of a prefix have left ----
-// Two rows a warp: its lanes take the rows in turn, as neighbouring rows' 16 bytes often share a sector, and first the
-// largest scores and sums of 16 pieces each, whose weights they deal out.
-template <int D>
-__global__ void __launch_bounds__(256) prior_join_kernel(const Prior q, int64_t rows) {
-    constexpr int kCols = D / 64;                                        // float4 of a lane
-    const int lane = threadIdx.x % kWarp, own = lane >> 1;
-    const int64_t i = ((int64_t)blockIdx.x * (256 / kWarp) + threadIdx.x / kWarp) * 2 + (lane & 1);
-    wait_for_last_kernel();
-    const int4 at = i < rows ? __ldcg(q.desc + i) : make_int4(0, 0, 0, 0);
-    // (rows without a prefix, or behind a kernel whose waits gave up, may hold anything)
-    const bool mine = at.x >= 2 && at.x <= kPieces && at.y >= 0 && at.w >= 1 && at.w <= kPieces && at.y / 2 + (at.x - 1) * at.w < kPieces &&
-                      at.z >= 0 && at.z < q.rows;
-    const int n = mine ? at.x : 0, most = max(n, __shfl_xor_sync(0xffffffffu, n, 1));
-    const int64_t size = prior_record(q.rows, D);
-    auto record_of = [&](int k) { return q.rec + (k == 0 ? at.y : (at.y / 2 + k * at.w) * 2) * size; };
-    float M = -INFINITY, L = 0.f;
-    float4 y[kCols];
-#pragma unroll
-    for (int x = 0; x < kCols; ++x) y[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < most; k0 += 16) {
-        float m = -INFINITY, l = 0.f;
-        if (k0 + own < n) {
-            const float* rec = record_of(k0 + own) + q.rows * D + at.z;
-            m = __ldcg(rec);
-            l = __ldcg(rec + q.rows);
-        }
-        float top = m;
-#pragma unroll
-        for (int o = 2; o < kWarp; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        top = fmaxf(top, M);
-        const float base = top == -INFINITY ? 0.f : top, f = ex2(M - base), w = ex2(m - base);
-        float sum = w * l;
-#pragma unroll
-        for (int o = 2; o < kWarp; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        L = fmaf(f, L, sum);
-        M = top;
-#pragma unroll
-        for (int x = 0; x < kCols; ++x) y[x] = make_float4(y[x].x * f, y[x].y * f, y[x].z * f, y[x].w * f);
-#pragma unroll 8
-        for (int k = 0; k < 16; ++k) {
-            const float wk = __shfl_sync(0xffffffffu, w, 2 * k + (lane & 1));
-            if (k0 + k < n) {
-                const float* rec = record_of(k0 + k) + at.z * q.row_step;
-#pragma unroll
-                for (int x = 0; x < kCols; ++x) {
-                    const float4 z = __ldcg(reinterpret_cast<const float4*>(rec + (own + 16 * x) * q.chunk_step));
-                    y[x].x = fmaf(wk, z.x, y[x].x);
-                    y[x].y = fmaf(wk, z.y, y[x].y);
-                    y[x].z = fmaf(wk, z.z, y[x].z);
-                    y[x].w = fmaf(wk, z.w, y[x].w);
-                }
-            }
-        }
-    }
-    if (!mine) return;
-#pragma unroll
-    for (int x = 0; x < kCols; ++x) *reinterpret_cast<float4*>(q.whole + i * D + 4 * (own + 16 * x)) = y[x];
-    if (own == 0) q.ml[i] = make_float2(M, L);
-}
-
 template <bool SH> cudaError_t launch(const DecodeArgs& a, cudaStream_t st) {
     if (a.p.dtype == LOLA_F32) return a.p.d == 128 ? launch_f32<128, SH>(a, st) : launch_f32<64, SH>(a, st);
     return a.p.d == 128 ? launch_bf16<128, SH>(a, st) : launch_bf16<64, SH>(a, st);
@@ -560,39 +501,8 @@ template <bool SH> cudaError_t launch(const DecodeArgs& a, cudaStream_t st) {
 
 int64_t paged_decode_workspace(int d) { return (int64_t)kPieces * kSlots * (record_floats(d) * sizeof(float) + sizeof(uint64_t)); }
 
-int64_t prior_workspace(int n_seq, int Hq, int d, int dtype, char* base, Prior* q) {
-    const bool tc = dtype == LOLA_BF16;                     // (lola_prefix.cu)
-    const int64_t n = (int64_t)n_seq * Hq, rows = tc ? kPrefixRows : kRows;
-    int64_t at = 0;
-    auto take = [&](int64_t bytes) {
-        char* x = base ? base + at : nullptr;
-        at += (bytes + 15) / 16 * 16;
-        return x;
-    };
-    char* desc = take(n * sizeof(int4));
-    char* ml = take(n * sizeof(float2));
-    char* whole = take(n * d * sizeof(float));
-    char* rec = take(kPieces * 2 * prior_record((int)rows, d) * sizeof(float));
-    if (q) {
-        q->desc = reinterpret_cast<int4*>(desc);
-        q->ml = reinterpret_cast<float2*>(ml);
-        q->whole = reinterpret_cast<float*>(whole);
-        q->rec = reinterpret_cast<float*>(rec);
-        q->rows = (int)rows;
-        q->row_step = tc ? 4 : d;
-        q->chunk_step = tc ? 4 * kPrefixRows : 4;
-    }
-    return at;
-}
-
 cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t st) { return launch<false>(a, st); }
-cudaError_t launch_paged_prefix(const DecodeArgs& a, cudaStream_t st) { return launch<true>(a, st); }
-cudaError_t launch_prior_join(const DecodeArgs& a, cudaStream_t st) {
-    const int64_t rows = (int64_t)a.sh.n_seq * a.p.Hq;
-    const unsigned grid = (unsigned)((rows + 15) / 16);
-    return a.p.d == 128 ? launch_behind(prior_join_kernel<128>, grid, 256, 0, st, a.sh, rows)
-                        : launch_behind(prior_join_kernel<64>, grid, 256, 0, st, a.sh, rows);
-}
+cudaError_t launch_paged_parts(const DecodeArgs& a, cudaStream_t st) { return launch<true>(a, st); }
 
 cudaError_t paged_status_word(int32_t** word) { return cudaGetSymbolAddress((void**)word, g_status); }
 

@@ -30,8 +30,9 @@ struct Maps {
 };
 
 struct Args {
-    PagedArgs p;        // SH: of the prefixes, which take the sequences' place
-    Prior sh;           // shared prefixes (sh.p.table null: none)
+    PagedArgs p;        // SH: of the prefixes, or of the sequences
+    Sharing sh;         // SH: whose rows see them
+    Parts parts;        // SH: what is left of them
     Rows Q, O;
     float* lse;
     float* part;        // workspace: records, then the joins' cells
@@ -67,7 +68,8 @@ __device__ __forceinline__ unsigned long long* cell(const Args& a, int piece, in
     return reinterpret_cast<unsigned long long*>(a.part + (int64_t)kPieces * kSlots * record_floats(D)) + piece * kSlots + slot;
 }
 
-// ---- query rows: G of a sequence, or (SH) those of all sequences that share a prefix, sequence by sequence ----
+// ---- query rows: G of a sequence, or (SH) those of all sequences that share a prefix, sequence by sequence.  SH: the
+// segments' parts are left for another kernel, none of them is joined here ----
 struct Group {
     int m0, rows;          // first sequence
     int RG, I;             // row groups per key/value head; items
@@ -75,8 +77,8 @@ struct Group {
 template <bool SH, int ROWS = kRows> __device__ __forceinline__ Group group_of(const Args& a, int b, int* bits = nullptr) {
     Group g;
     if constexpr (SH) {
-        int n = a.sh.n_seq, bad = 0;
-        g.m0 = 0;
+        int n = a.sh.each ? 1 : a.sh.n_seq, bad = 0;
+        g.m0 = a.sh.each ? b : 0;
         if (a.sh.cu) seq_rows(a.sh.cu, b, a.sh.n_seq, &g.m0, &n, &bad);
         if (bits) *bits |= bad;
         g.rows = n * a.p.G;
@@ -111,7 +113,6 @@ __device__ __forceinline__ int pieces_of(int64_t total) { return (int)min((int64
 struct Seg {
     int b, h0, R;          // (first) sequence, first query head, query rows
     int r0;                // SH: the first row's number among the prefix' rows of this key head
-    int prior;             // the sequence's prefix + 1, where it has one with tokens
     int tiles, n0;         // tiles of the segment, number of its first one in the ring's order
     int len;               // tokens of the sequence from the segment's first tile on
     int whole;             // it covers the whole item
@@ -276,7 +277,6 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
     const int box = min(p.page, C::kTokens), lb = 31 - __clz(box), nbox = C::kTokens >> lb;   // tokens of a box, boxes of a tile
     int b = st.b;
     Group gr = group_of<SH>(a, b);
-    int prior = SH ? 0 : prior_of(a.sh, b, lane) + 1;
     int lens_b = b;                                               // the lanes hold 32 sequences' lengths
     int lens = b + lane < p.n_seq ? p.kv_len[b + lane] : 0;
     int64_t tokens = paged_tokens(p, __shfl_sync(0xffffffffu, lens, 0));
@@ -297,7 +297,6 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
             g.b = gr.m0;
             g.h0 = h0;
             g.r0 = SH ? r0 : 0;
-            g.prior = prior;
             g.R = R;
             g.tiles = t1 - t0;
             g.n0 = n;
@@ -372,7 +371,6 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
                 tokens = paged_tokens(p, __shfl_sync(0xffffffffu, lens, b - lens_b));
                 gr = group_of<SH>(a, b);
             } while (SH && (tokens == 0 || gr.I == 0));               // (units are left: there is such a prefix)
-            if (!SH) prior = prior_of(a.sh, b, lane) + 1;
             tiles = tiles_of<C::kTokens>(tokens);
         }
     }
@@ -400,36 +398,19 @@ __device__ __forceinline__ bool sees_token(const PagedArgs& p, int b) {
     return false;
 }
 
-// One more part of a row's softmax: largest score m, sum l, output z (four columns), all against m.
-__device__ __forceinline__ void add_part(float m, float l, const float4& z, float (&y)[4], float& M, float& L) {
-    const float top = fmaxf(M, m), base = top == -INFINITY ? 0.f : top, f = ex2(M - base), f1 = ex2(m - base);
-    L = fmaf(f, L, f1 * l);
-    y[0] = fmaf(f, y[0], f1 * z.x);
-    y[1] = fmaf(f, y[1], f1 * z.y);
-    y[2] = fmaf(f, y[2], f1 * z.z);
-    y[3] = fmaf(f, y[3], f1 * z.w);
-    M = top;
-}
-// The prefix' part of row i, columns c .. c + 3.
-template <int D>
-__device__ __forceinline__ void add_prior(const Prior& q, int64_t i, int c, float (&y)[4], float& M, float& L) {
-    const float2 ml = __ldcg(q.ml + i);
-    add_part(ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(q.whole + i * D + c)), y, M, L);
-}
-
 // Where a segment that is a piece of its item leaves its part.
 template <int D, bool SH> __device__ __forceinline__ float* segment_record(const Args& a, const Seg& g) {
     const int slot = g.k == 0 ? g.s0 : 0;
-    if constexpr (SH) return a.sh.rec + ((int64_t)blockIdx.x * 2 + slot) * prior_record(kRows, D);
+    if constexpr (SH) return a.parts.rec + ((int64_t)blockIdx.x * 2 + slot) * part_record(kRows, D);
     else return record<D>(a, blockIdx.x, slot);
 }
 
-// One row's 4 columns c .. c + 3: o, when all of the item's tokens are in, or a record.  SH: left for the sequences'
-// own kernel.
+// One row's 4 columns c .. c + 3: o, when all of the item's tokens are in, or a record.  SH: left for the
+// kernel that joins them.
 template <typename T, int D, bool SH>
 __device__ __forceinline__ void write_out(const Args& a, const Seg& g, bool whole, float* rec, int r, int c, float (&y)[4], float M, float L) {
     if constexpr (SH) {
-        const Prior& q = a.sh;
+        const Parts& q = a.parts;
         const int64_t i = (int64_t)(g.b + (g.r0 + r) / a.p.G) * a.p.Hq + g.h0 + (g.r0 + r) % a.p.G;
         if (whole) {
             store4(q.whole + i * D + c, y);
@@ -443,9 +424,8 @@ __device__ __forceinline__ void write_out(const Args& a, const Seg& g, bool whol
         }
         if (c == 0 && (whole || g.k == 0)) q.desc[i] = whole ? make_int4(1, 0, 0, 0) : make_int4(g.np, 2 * g.c0 + g.s0, r, 1);
     } else if (whole) {
-        if (g.prior) add_prior<D>(a.sh, (int64_t)g.b * a.p.Hq + g.h0 + r, c, y, M, L);
         // (no token seen: o = 0; scores that are all minus infinity: 0 / 0)
-        const float inv = L == 0.f ? (sees_token(a.p, g.b) || (g.prior && sees_token(a.sh.p, g.prior - 1)) ? NAN : 0.f) : 1.f / L;
+        const float inv = L == 0.f ? (sees_token(a.p, g.b) ? NAN : 0.f) : 1.f / L;
 #pragma unroll
         for (int z = 0; z < 4; ++z) y[z] *= inv;
         store4(reinterpret_cast<T*>(a.O.data) + (int64_t)g.b * a.O.row + (int64_t)(g.h0 + r) * a.O.head + c, y);
@@ -612,6 +592,7 @@ inline Args make_args(const DecodeArgs& d) {
     Args a;
     a.p = d.p;
     a.sh = d.sh;
+    a.parts = d.parts;
     a.Q = d.Q;
     a.O = d.O;
     a.lse = d.lse;

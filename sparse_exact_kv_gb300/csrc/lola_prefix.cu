@@ -5,7 +5,7 @@
 //   S = Q K^T,  P = 2^{c S - m},  l += sum P,  O += P V.
 // No row is masked but by the prefix' length.  The (prefix, key head, 256 rows, block) units are counted in that order
 // and cut into as many equal pieces as there are SMs, so that one prefix alone fills the GPU; a piece leaves (m, l, O) of
-// each of its segments for the kernel that joins them (lola_paged.cu).  With one prefix of more than 256 rows, the row
+// each of its segments for the kernel that joins them (lola_shared.cu).  With one prefix of more than 256 rows, the row
 // items of the same keys are side by side in time: the units are (key head, block), and as many CTAs as there are row
 // items take a piece, so that keys and values come from HBM once (counted one item behind the other, 512 rows of
 // 128000 tokens read them twice: 8 heads, d = 128, 218 us).
@@ -612,9 +612,9 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
             }
             const int row = tile_row + r, flat = g.r0 + row, seq = flat / p.G;
             const bool mine = row < g.R && n > 0;
-            const Prior& q = a.sh;
+            const Parts& q = a.parts;
             const int64_t at = (int64_t)(g.m0 + seq) * p.Hq + g.hk * p.G + flat - seq * p.G;
-            float* rec = q.rec + ((int64_t)blockIdx.x * 2 + (g.k == 0 ? g.rec & 1 : 0)) * prior_record(kItem, D);
+            float* rec = q.rec + ((int64_t)blockIdx.x * 2 + (g.k == 0 ? g.rec & 1 : 0)) * part_record(kItem, D);
             // (two halves: half of the columns each)
             const int c0 = pair ? i * (D / 2) : 0, c1 = pair ? c0 + D / 2 : D;
             if (n > 0) {

@@ -357,8 +357,9 @@ __global__ void __launch_bounds__(QSmem<TO, D, NB>::kAll * kWarp, 1) quant_decod
 template <typename TO, int D, bool SH>
 cudaError_t launch_quant(const DecodeArgs& d, cudaStream_t st) {
     static std::atomic<uint64_t> done[2] = {};
-    return !SH && d.p.G <= 8 ? launch_kernel<uint8_t, D>(quant_decode_kernel<TO, D, 1, false>, QSmem<TO, D, 1>::kAll, done[0], d, st)
-                             : launch_kernel<uint8_t, D>(quant_decode_kernel<TO, D, 2, SH>, QSmem<TO, D, 2>::kAll, done[1], d, st);
+    return (!SH || d.sh.each) && d.p.G <= 8
+               ? launch_kernel<uint8_t, D>(quant_decode_kernel<TO, D, 1, SH>, QSmem<TO, D, 1>::kAll, done[0], d, st)
+               : launch_kernel<uint8_t, D>(quant_decode_kernel<TO, D, 2, SH>, QSmem<TO, D, 2>::kAll, done[1], d, st);
 }
 
 template <bool SH> cudaError_t launch_quant(const DecodeArgs& a, cudaStream_t st) {
@@ -486,7 +487,7 @@ template <typename T, int D> cudaError_t launch_read(const ReadArgs& a, cudaStre
 }  // namespace
 
 cudaError_t launch_quant_decode(const DecodeArgs& a, cudaStream_t st) { return launch_quant<false>(a, st); }
-cudaError_t launch_quant_prefix(const DecodeArgs& a, cudaStream_t st) { return launch_quant<true>(a, st); }
+cudaError_t launch_quant_parts(const DecodeArgs& a, cudaStream_t st) { return launch_quant<true>(a, st); }
 
 cudaError_t launch_quant_read(const ReadArgs& a, cudaStream_t st) {
     if (a.p.dtype == LOLA_F32) return a.p.d == 128 ? launch_read<float, 128>(a, st) : launch_read<float, 64>(a, st);
