@@ -179,7 +179,7 @@ _lib = _load()
 class _Declines:
     """In the marshalling module's place: every call takes its Python form."""
     prefill = prefill_paged = decode = append = staticmethod(lambda *args: NotImplemented)
-    quant_append = quant_decode = quant_read = shared = staticmethod(lambda *args: NotImplemented)
+    quant_pools = quant_append = quant_decode = quant_read = shared = staticmethod(lambda *args: NotImplemented)
 
 
 def _marshalling(path):
@@ -823,6 +823,8 @@ class QuantizedAttention(ExactAttention):
 
     def _check_pools(self):
         k, v, ks, vs = self.k_pool, self.v_pool, self.k_scale, self.v_scale
+        if _fast.quant_pools(self._plan[0], k, v, ks, vs) is True:
+            return
         _need(not any(x is None for x in (k, v, ks, vs)), "k_pool, v_pool, k_scale and v_scale come together")
         shape = k.shape
         _need(len(shape) == 4 and shape[1] == self.Hkv and shape[3] == self.d, "pools are [n_pages, Hkv, page, d]")

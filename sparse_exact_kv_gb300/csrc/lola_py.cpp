@@ -69,19 +69,35 @@ const Tensor* rows(PyObject* o, lola_rows* r, const Call& c, int64_t n, int64_t 
 }
 
 // contiguous pools [n_pages, Hkv, page, d] of one shape, and what a call has for them
-bool cache(PyObject* k_pool, PyObject* v_pool, PyObject* kv_len, PyObject* table, const Call& c, lola_paged_kv* kv,
-           at::ScalarType type) {
-    const Tensor *k = get(k_pool, type, c.device), *v = get(v_pool, type, c.device), *t = get(table, at::kInt, c.device);
-    if (!k || !v || !t || k->dim() != 4 || k->size(1) != c.cfg->Hkv || k->size(3) != c.cfg->d || k->sizes() != v->sizes() ||
-        !k->is_contiguous() || !v->is_contiguous() || t->dim() != 2 || (t->stride(1) != 1 && t->size(1) != 1) ||
-        k->size(0) > INT32_MAX || t->size(0) > INT32_MAX || t->size(1) > INT32_MAX)
+bool pools(PyObject* k_pool, PyObject* v_pool, int device, const lola_attn_config* cfg, lola_paged_kv* kv, at::ScalarType type) {
+    const Tensor *k = get(k_pool, type, device), *v = get(v_pool, type, device);
+    if (!k || !v || k->dim() != 4 || k->size(1) != cfg->Hkv || k->size(3) != cfg->d || k->sizes() != v->sizes() || !k->is_contiguous() ||
+        !v->is_contiguous() || k->size(0) > INT32_MAX || k->size(2) > INT32_MAX)
         return false;
-    const Tensor* n = vec(kv_len, at::kInt, c.device, t->size(0));
-    if (!n) return false;
     kv->K = k->data_ptr();
     kv->V = v->data_ptr();
     kv->n_pages = (int32_t)k->size(0);
     kv->page = (int32_t)k->size(2);
+    return true;
+}
+// ... and a quantised cache's powers of two [n_pages, Hkv, page], contiguous
+bool powers(PyObject* k_scale, PyObject* v_scale, int device, const lola_attn_config* cfg, const lola_paged_kv& kv, lola_kv_scales* sc) {
+    const Tensor *k = get(k_scale, at::kFloat8_e8m0fnu, device), *v = get(v_scale, at::kFloat8_e8m0fnu, device);
+    for (const Tensor* t : {k, v})
+        if (!t || t->dim() != 3 || t->size(0) != kv.n_pages || t->size(1) != cfg->Hkv || t->size(2) != kv.page || !t->is_contiguous())
+            return false;
+    sc->K = k->data_ptr();
+    sc->V = v->data_ptr();
+    return true;
+}
+bool cache(PyObject* k_pool, PyObject* v_pool, PyObject* kv_len, PyObject* table, const Call& c, lola_paged_kv* kv,
+           at::ScalarType type) {
+    const Tensor* t = get(table, at::kInt, c.device);
+    if (!pools(k_pool, v_pool, c.device, c.cfg, kv, type) || !t || t->dim() != 2 || (t->stride(1) != 1 && t->size(1) != 1) ||
+        t->size(0) > INT32_MAX || t->size(1) > INT32_MAX)
+        return false;
+    const Tensor* n = vec(kv_len, at::kInt, c.device, t->size(0));
+    if (!n) return false;
     kv->n_seq = (int32_t)t->size(0);
     kv->width = (int32_t)t->size(1);
     kv->table_stride = t->size(0) == 1 ? t->size(1) : t->stride(0);
@@ -93,17 +109,10 @@ bool cache(PyObject* k_pool, PyObject* v_pool, PyObject* kv_len, PyObject* table
 bool cache(PyObject* k_pool, PyObject* v_pool, PyObject* kv_len, PyObject* table, const Call& c, lola_paged_kv* kv) {
     return cache(k_pool, v_pool, kv_len, table, c, kv, c.dtype);
 }
-// ... quantised: contiguous powers of two [n_pages, Hkv, page] beside them
+// ... quantised
 bool cache(PyObject* k_pool, PyObject* v_pool, PyObject* k_scale, PyObject* v_scale, PyObject* kv_len, PyObject* table, const Call& c,
            lola_paged_kv* kv, lola_kv_scales* sc) {
-    if (!cache(k_pool, v_pool, kv_len, table, c, kv, at::kFloat8_e4m3fn)) return false;
-    const Tensor *k = get(k_scale, at::kFloat8_e8m0fnu, c.device), *v = get(v_scale, at::kFloat8_e8m0fnu, c.device);
-    for (const Tensor* t : {k, v})
-        if (!t || t->dim() != 3 || t->size(0) != kv->n_pages || t->size(1) != c.cfg->Hkv || t->size(2) != kv->page || !t->is_contiguous())
-            return false;
-    sc->K = k->data_ptr();
-    sc->V = v->data_ptr();
-    return true;
+    return cache(k_pool, v_pool, kv_len, table, c, kv, at::kFloat8_e4m3fn) && powers(k_scale, v_scale, c.device, c.cfg, *kv, sc);
 }
 
 PyObject* decline() {
@@ -180,6 +189,20 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
         s = lola_paged_decode(c->cfg, &kv, &rq, &ro, nullptr, ws.data_ptr(), (size_t)c->ws, c->stream.stream());
         Py_END_ALLOW_THREADS
         return s == LOLA_OK ? THPVariable_Wrap(std::move(out)) : decline();
+    });
+}
+
+// quant_pools(address of the layer's lola_attn_config, k_pool, v_pool, k_scale, v_scale) -> True where they fit the layer (and are
+// on the current device)
+PyObject* quant_pools(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        const auto* cfg = n == 5 ? (const lola_attn_config*)(uintptr_t)PyLong_AsUnsignedLongLong(a[0]) : nullptr;
+        if (PyErr_Occurred() || !cfg || c10::cuda::device_count() == 0) return decline();
+        const int device = c10::cuda::current_device();
+        lola_paged_kv kv;
+        lola_kv_scales sc;
+        if (!pools(a[1], a[2], device, cfg, &kv, at::kFloat8_e4m3fn) || !powers(a[3], a[4], device, cfg, kv, &sc)) return decline();
+        Py_RETURN_TRUE;
     });
 }
 
@@ -315,6 +338,7 @@ PyMethodDef methods[] = {
     {"prefill_paged", (PyCFunction)(void (*)(void))prefill_paged, METH_FASTCALL, nullptr},
     {"decode", (PyCFunction)(void (*)(void))decode, METH_FASTCALL, nullptr},
     {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, nullptr},
+    {"quant_pools", (PyCFunction)(void (*)(void))quant_pools, METH_FASTCALL, nullptr},
     {"quant_append", (PyCFunction)(void (*)(void))quant_append, METH_FASTCALL, nullptr},
     {"quant_decode", (PyCFunction)(void (*)(void))quant_decode, METH_FASTCALL, nullptr},
     {"quant_read", (PyCFunction)(void (*)(void))quant_read, METH_FASTCALL, nullptr},
