@@ -275,7 +275,8 @@ struct DecodeArgs {
     float scale_log2;
 };
 cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t st);
-cudaError_t launch_paged_parts(const DecodeArgs& a, cudaStream_t st);
+cudaError_t launch_f32_parts(const DecodeArgs& a, cudaStream_t st);
+cudaError_t launch_bf16_parts(const DecodeArgs& a, cudaStream_t st);
 cudaError_t launch_quant_parts(const DecodeArgs& a, cudaStream_t st);
 constexpr int kPrefixRows = 256;         // rows of a record of launch_prefix_tc, column chunks one behind the other
 cudaError_t launch_prefix_tc(const DecodeArgs& a, cudaStream_t st);       // bf16 io: prefixes

@@ -275,7 +275,7 @@ template <int D, bool HALF> struct MmaSmem {
 };
 
 // HALF: at most 8 query rows (rows 8-15 of the products hold anything and are left alone)
-template <int D, bool HALF, bool SH>
+template <int D, bool HALF>
 __global__ void __launch_bounds__(kThreads, 1) paged_decode_mma_kernel(const __grid_constant__ Maps maps, const Args a) {
     using T = __nv_bfloat16;
     using C = Cfg<T, D>;
@@ -307,8 +307,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_mma_kernel(const __g
     }
     wait_for_last_kernel();
     Start st;
-    if (!find_start<SH>(a, &st)) return;
-    if (warp == kCons / kWarp) produce<T, T, D, 2, SH>(maps, a, st, sb, smem_u32(x.q[0]), M::kPitch, bars, segs, bad_sm, &abort_sm, lane);
+    if (!find_start<false>(a, &st)) return;
+    if (warp == kCons / kWarp) produce<T, T, D, 2, false>(maps, a, st, sb, smem_u32(x.q[0]), M::kPitch, bars, segs, bad_sm, &abort_sm, lane);
     const int grp = warp >> 2, wg = warp & 3, g8 = lane >> 2, q2 = (lane & 3) * 2;
     const int own = kBoth ? 0 : grp, me = kBoth ? warp : wg, gt = kBoth ? tid : tid & 127;   // the segment's group, its warps and threads
     auto bar = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + own), "n"(NT) : "memory"); };
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_mma_kernel(const __g
         }
         const Seg g = segs[slot];
         if (g.R < 0) break;
-        if (!SH && !g.whole && gt == 64) open_cells<D>(a, g);
+        if (!g.whole && gt == 64) open_cells<D>(a, g);
         uint32_t qa[D / 16][4];
 #pragma unroll
         for (int y = 0; y < D / 16; ++y) ldsm4(qrow + slot * kRows * M::kPitch + 32 * y, qa[y]);
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_mma_kernel(const __g
             for (int w = 0; w < NW; ++w) mm = fmaxf(mm, x.ms[own][w][g8 + 8 * r]);
             f[r] = ex2(m[r] - (mm == -INFINITY ? 0.f : mm));
         }
-        float* rec = segment_record<D, SH>(a, g);
+        float* rec = segment_record<D, false>(a, g);
         const int er = 4 * (gt & 127) / CK, ec = 4 * (gt & 127) % CK;        // 128 threads x 4 columns = R8 x CK
         float mm = -INFINITY, ll = 0.f;
 #pragma unroll
@@ -468,13 +468,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_mma_kernel(const __g
                     y[2] += z.z;
                     y[3] += z.w;
                 }
-                if (er < g.R) write_out<T, D, SH>(a, g, g.whole, rec, er, c + ec, y, mm, ll);
+                if (er < g.R) write_out<T, D, false>(a, g, g.whole, rec, er, c + ec, y, mm, ll);
             }
         }
-        if (!SH && !g.whole) join_pieces<T, D, NT>(a, g, gt, &go[own], bars.arrived, bar);
+        if (!g.whole) join_pieces<T, D, NT>(a, g, gt, &go[own], bars.arrived, bar);
     }
     __syncthreads();
-    if (abort_sm) settle<D, C::kStages, 2, SH>(a, bars);
+    if (abort_sm) settle<D, C::kStages, 2, false>(a, bars);
 }
 
 // (rows of a prefix: as many as its sequences have)
@@ -486,23 +486,24 @@ cudaError_t launch_f32(const DecodeArgs& d, cudaStream_t st) {
     if (rows <= 8) return launch_kernel<float, D>(paged_decode_f32_kernel<D, 8, SH>, kThreads / kWarp, done[1], d, st);
     return launch_kernel<float, D>(paged_decode_f32_kernel<D, 16, SH>, kThreads / kWarp, done[2], d, st);
 }
-template <int D, bool SH>
+template <int D>
 cudaError_t launch_bf16(const DecodeArgs& d, cudaStream_t st) {
     static std::atomic<uint64_t> done[2] = {};
-    return d.p.G <= 8 ? launch_kernel<__nv_bfloat16, D>(paged_decode_mma_kernel<D, true, SH>, kThreads / kWarp, done[0], d, st)
-                      : launch_kernel<__nv_bfloat16, D>(paged_decode_mma_kernel<D, false, SH>, kThreads / kWarp, done[1], d, st);
-}
-template <bool SH> cudaError_t launch(const DecodeArgs& a, cudaStream_t st) {
-    if (a.p.dtype == LOLA_F32) return a.p.d == 128 ? launch_f32<128, SH>(a, st) : launch_f32<64, SH>(a, st);
-    return a.p.d == 128 ? launch_bf16<128, SH>(a, st) : launch_bf16<64, SH>(a, st);
+    return d.p.G <= 8 ? launch_kernel<__nv_bfloat16, D>(paged_decode_mma_kernel<D, true>, kThreads / kWarp, done[0], d, st)
+                      : launch_kernel<__nv_bfloat16, D>(paged_decode_mma_kernel<D, false>, kThreads / kWarp, done[1], d, st);
 }
 
 }  // namespace
 
 int64_t paged_decode_workspace(int d) { return (int64_t)kPieces * kSlots * (record_floats(d) * sizeof(float) + sizeof(uint64_t)); }
 
-cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t st) { return launch<false>(a, st); }
-cudaError_t launch_paged_parts(const DecodeArgs& a, cudaStream_t st) { return launch<true>(a, st); }
+cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t st) {
+    if (a.p.dtype == LOLA_F32) return a.p.d == 128 ? launch_f32<128, false>(a, st) : launch_f32<64, false>(a, st);
+    return a.p.d == 128 ? launch_bf16<128>(a, st) : launch_bf16<64>(a, st);
+}
+cudaError_t launch_f32_parts(const DecodeArgs& a, cudaStream_t st) {
+    return a.p.d == 128 ? launch_f32<128, true>(a, st) : launch_f32<64, true>(a, st);
+}
 
 cudaError_t paged_status_word(int32_t** word) { return cudaGetSymbolAddress((void**)word, g_status); }
 

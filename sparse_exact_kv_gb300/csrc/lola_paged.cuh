@@ -53,6 +53,10 @@ template <typename T, int D> struct Cfg {
     static constexpr int kStages = 196608 / (2 * kHalf + kScales) > kMost ? kMost : 196608 / (2 * kHalf + kScales);
     static constexpr int kSmem = kStages * (2 * kHalf + kScales) + 1024;
 };
+// ... with a ring of S stages
+template <typename B, int S> struct Ring : B {
+    static constexpr int kStages = S, kSmem = S * (2 * B::kHalf + B::kScales) + 1024;
+};
 
 // ---- the workspace: per piece four records of (O [16][d], m [16], l [16]) -- its first segment's (slot
 // 0), its last one's (1), and the joins of up to 16 pieces that begin with one of them (2, 3) -- and as
@@ -169,6 +173,18 @@ __device__ __forceinline__ bool issued_wait(const int* issued, int n, int* abort
     }
     return true;
 }
+// `turns` segments' groups have been added up in a buffer (the upper half of *joined)
+__device__ __forceinline__ bool joined_wait(const int* joined, int turns, int* abort_sm) {
+    const uint64_t start = globaltimer_ns();
+    while ((*reinterpret_cast<const volatile int*>(joined) >> 16) < turns) {
+        if (*reinterpret_cast<volatile int*>(abort_sm)) return false;
+        if (globaltimer_ns() - start > kWaitNs) {
+            *abort_sm = 1;
+            return false;
+        }
+    }
+    return true;
+}
 // barrier `id` of a group of NT threads that also tells all of them whether one had x (so that a
 // wait that gave up ends the whole group, and no barrier is left waiting)
 template <int NT>
@@ -189,8 +205,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 // Barriers: a ring stage is full / empty; a segment slot (descriptor and Q rows) is full / empty.
-template <int S> struct Bars {
-    uint64_t full[S], empty[S], seg_full[2], seg_empty[2];
+template <int S, int NS = 2> struct Bars {
+    uint64_t full[S], empty[S], seg_full[NS], seg_empty[NS];
     int issued;      // tiles whose stage is armed
     int given;       // segment slots given to the consumers, when the producer is done
     int arrived[2];  // this piece's record of that slot has been counted
@@ -266,10 +282,9 @@ __device__ __forceinline__ void place_piece(const Start& st, int64_t xs, int til
 // TQ: the queries' numbers.  e4m3: four warps (`part` 0-3: codes of K, of V, powers of K, of V) that walk the segments
 // side by side, as each copy takes its thread some 180 clocks to issue, and a tile of codes half a tile's time at most
 // (all four copies by one warp: 64 sequences of 1000-8000 tokens, 32/8 heads, d = 128, 117 us).  The first of them does the rest.
-template <typename T, typename TQ, int D, int NS, bool SH, typename B>
+template <typename T, typename TQ, int D, int NS, bool SH, typename C = Cfg<T, D>, int ROWS = kRows, typename B>
 __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const Start& st, uint32_t ring, uint32_t qs,
                                         uint32_t q_pitch, B& bars, Seg* segs, uint32_t* bad_sm, int* abort_sm, int lane, int part = 0) {
-    using C = Cfg<T, D>;
     constexpr bool kParts = C::kScales > 0;
     const bool first = !kParts || part == 0;
     const PagedArgs& p = a.p;
@@ -311,7 +326,7 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
         __syncwarp();
         if (first && lane < R) {
             const int seq = SH ? gr.m0 + (r0 + lane) / p.G : b, h = SH ? h0 + (r0 + lane) % p.G : h0 + lane;
-            bulk_load(qs + (uint32_t)slot * kRows * q_pitch + lane * q_pitch,
+            bulk_load(qs + (uint32_t)slot * ROWS * q_pitch + lane * q_pitch,
                       a.Q.data + ((int64_t)seq * a.Q.row + (int64_t)h * a.Q.head) * (int)sizeof(TQ), kQBytes, smem_u32(&bars.seg_full[slot]));
         }
         ++i;
@@ -606,7 +621,8 @@ inline Args make_args(const DecodeArgs& d) {
 }
 
 template <typename T, int D, typename K>
-cudaError_t launch_kernel(K kernel, int warps, std::atomic<uint64_t>& done, const DecodeArgs& d, cudaStream_t st) {
+cudaError_t launch_kernel(K kernel, int warps, std::atomic<uint64_t>& done, const DecodeArgs& d, cudaStream_t st,
+                          int smem = Cfg<T, D>::kSmem) {
     using C = Cfg<T, D>;
     Maps maps;
     const auto ty = sizeof(T) == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
@@ -619,9 +635,9 @@ cudaError_t launch_kernel(K kernel, int warps, std::atomic<uint64_t>& done, cons
     if (!make_tmap_pages(&maps.k, ty, sizeof(T), d.p.K, wide, d.p.page / fold, depth, rows / fold, wide * (int)sizeof(T) / 128) ||
         !make_tmap_pages(&maps.v, ty, sizeof(T), d.p.V, wide, d.p.page / fold, depth, rows / fold, wide * (int)sizeof(T) / 128))
         return cudaErrorInvalidValue;
-    cudaError_t e = opt_in_smem(kernel, C::kSmem, done);
+    cudaError_t e = opt_in_smem(kernel, smem, done);
     if (e != cudaSuccess) return e;
-    return launch_behind(kernel, kPieces, warps * kWarp, C::kSmem, st, maps, make_args(d));
+    return launch_behind(kernel, kPieces, warps * kWarp, smem, st, maps, make_args(d));
 }
 
 }  // namespace

@@ -41,34 +41,39 @@ __device__ __forceinline__ uint32_t turned(uint32_t x) {
     return y;
 }
 
-// NB: query rows in eights
-template <typename TO, int D, int NB> struct QSmem {
-    static constexpr int NW = NB == 1 ? 12 : 8;                             // consumer warps, and all
-    static constexpr int kAll = NW + 4;
+// T: the cache's numbers (bfloat16, or uint8_t: e4m3).  NB: query rows in eights.
+template <typename T, typename TO, int D, int NB> struct TSmem {
+    static constexpr int kGroups = NB == 1 ? 3 : 2;                         // groups of four consumer warps
+    static constexpr int NW = 4 * kGroups, kAll = NW + (sizeof(T) == 1 ? 4 : 1);    // consumer warps, and all
+    static constexpr int NS = sizeof(TO) == 4 ? 2 : 4;                      // segments under way
+    static constexpr int kRing = (D == 128 ? 5 : 10) - (NB == 1 ? 0 : D == 128 ? 1 : 2);   // tiles
     static constexpr int kCk = NB == 1 ? 64 : 32;                           // columns joined at a time
     static constexpr int kPitch = D * (int)sizeof(TO) + 16;                 // Q rows
-    float red[NW][8 * NB][kCk + 8];                                         // (rows 32 bytes apart: 8-byte stores of four rows)
-    float ms[NW][8 * NB], ls[NW][8 * NB];
-    uint8_t q[2][kRows * kPitch];
+    float red[kGroups][4][8 * NB][kCk + 8];                                 // (rows 32 bytes apart: 8-byte stores of four rows)
+    float part[2][kGroups][8 * NB][D];                                      // the groups' parts of a segment
+    float part_ml[2][kGroups][2][8 * NB];
+    float ms[kGroups][4][8 * NB], ls[kGroups][4][8 * NB];
+    uint8_t q[NS][8 * NB * kPitch];
 };
 
-// All warps on a segment, in groups of four that take its tiles in turn; a warp has 32 of a tile's 128 tokens, 16 at a time.
-// TO: q and o.
-template <typename TO, int D, int NB, bool SH>
-__global__ void __launch_bounds__(QSmem<TO, D, NB>::kAll * kWarp, 1) quant_decode_kernel(const __grid_constant__ Maps maps, const Args a) {
-    using T = uint8_t;
-    using C = Cfg<T, D>;
-    using M = QSmem<TO, D, NB>;
-    constexpr int NW = M::NW, NT = NW * kWarp, kGroups = NW / 4, CK = M::kCk;
-    constexpr bool kTwo = sizeof(TO) == 4;                             // q and the weights in two parts
+// Tile n is group n % kGroups', a warp has a quarter of its tokens, 16 at a time.  A group that is done with its tiles of a
+// segment adds its warps up and goes on to the next segment; the last of a segment's groups to be done adds the groups up, in
+// their order.  So a sequence of one tile takes one group, and the others' tiles run beside its end (all warps at the segment's
+// end together: 64 sequences of 1000-8000 tokens, 32/8 heads, d = 128, e4m3, 94 us; 1024 items of 64 tokens 37 us).
+template <typename T, typename TO, int D, int NB, bool SH>
+__global__ void __launch_bounds__(TSmem<T, TO, D, NB>::kAll * kWarp, 1) decode_t_kernel(const __grid_constant__ Maps maps, const Args a) {
+    using M = TSmem<T, TO, D, NB>;
+    using C = Ring<Cfg<T, D>, M::kRing>;
+    constexpr int NW = M::NW, NT = 128, kGroups = M::kGroups, NS = M::NS, CK = M::kCk;
+    constexpr bool QZ = sizeof(T) == 1, kTwo = sizeof(TO) == 4;        // kTwo: q and the weights in two parts
     extern __shared__ __align__(1024) uint8_t smraw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(sm);
-    __shared__ __align__(16) M x;
-    __shared__ __align__(8) Bars<C::kStages> bars;
+    M& x = *reinterpret_cast<M*>(sm + C::kSmem - 1024);
+    __shared__ __align__(8) Bars<C::kStages, NS> bars;
     __shared__ uint32_t bad_sm[C::kStages];
-    __shared__ int abort_sm, go;
-    __shared__ Seg segs[2];
+    __shared__ int abort_sm, go[kGroups], joined[2];       // joined: the groups that are done with part[]; in the upper half: how
+    __shared__ Seg segs[NS];                               // many segments' groups have been added up there
     const PagedArgs& p = a.p;
     const int tid = threadIdx.x, warp = tid / kWarp, lane = tid % kWarp;
     if (tid == 0) {
@@ -76,82 +81,105 @@ __global__ void __launch_bounds__(QSmem<TO, D, NB>::kAll * kWarp, 1) quant_decod
             mbar_init(smem_u32(&bars.full[s]), 1);
             mbar_init(smem_u32(&bars.empty[s]), 4);
         }
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < NS; ++s) {
             mbar_init(smem_u32(&bars.seg_full[s]), 1);
             mbar_init(smem_u32(&bars.seg_empty[s]), NW);
         }
-        abort_sm = 0;
+        abort_sm = joined[0] = joined[1] = 0;
         bars.issued = bars.given = bars.arrived[0] = bars.arrived[1] = 0;
     }
     wait_for_last_kernel();
     Start st;
     if (!find_start<SH, M::kAll * kWarp, C::kTokens>(a, &st)) return;
-    if (warp >= NW) produce<T, TO, D, 2, SH>(maps, a, st, sb, smem_u32(x.q[0]), M::kPitch, bars, segs, bad_sm, &abort_sm, lane, warp - NW);
-    const int grp = warp >> 2, g8 = lane >> 2, q4 = lane & 3, q2 = q4 * 2;
-    auto bar = [&] { asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory"); };
+    if (warp >= NW) produce<T, TO, D, NS, SH, C, 8 * NB>(maps, a, st, sb, smem_u32(x.q[0]), M::kPitch, bars, segs, bad_sm, &abort_sm, lane, warp - NW);
+    const int grp = warp >> 2, w4 = warp & 3, gt = tid & 127, g8 = lane >> 2, q4 = lane & 3, q2 = q4 * 2;
+    auto bar = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(NT) : "memory"); };
     const int box = min(p.page, C::kTokens), lb = 31 - __clz(box);
-    // 16-byte chunk ch of token k's row: rows of 128 bytes (two tokens at d = 64), chunks swizzled
-    auto chunk_at = [](int k, int ch) {
-        const int row = k * D / 128, c = D == 128 ? ch : (k & 1) * 4 + ch;
-        return (uint32_t)(row * 128 + (((c ^ row) & 7) << 4));
+    // 16-byte chunk ch of token k's row: rows of 128 bytes, chunks swizzled; bfloat16: a box of 128-byte columns, e4m3: one
+    // column, whose rows are two tokens at d = 64
+    auto chunk_at = [&](int k, int ch) {
+        if constexpr (QZ) {
+            const int row = k * D / 128, c = D == 128 ? ch : (k & 1) * 4 + ch;
+            return (uint32_t)(row * 128 + (((c ^ row) & 7) << 4));
+        } else {
+            return (uint32_t)((k >> lb) * box * C::kRowBytes + (k & (box - 1)) * 128 + (ch >> 3) * box * 128 + (((ch ^ k) & 7) << 4));
+        }
     };
-    const int row0 = ((lane >> 3) & 1) * 8 + (lane & 7), ch0 = lane >> 4;           // this lane's ldmatrix row
+    // this lane's ldmatrix rows: of K, and of V (e4m3: the same)
+    const int krow = ((lane >> 3) & 1) * 8 + (lane & 7), kch = lane >> 4;
+    const int vrow = QZ ? krow : (lane >> 4) * 8 + (lane & 7), vch = QZ ? kch : (lane >> 3) & 1;
+    int multi = 0;                                          // segments of several groups so far
     for (int i = 0; warp < NW; ++i) {
-        const int slot = i & 1;
-        if (group_or<NT>(1, !ring_wait(smem_u32(&bars.seg_full[slot]), (uint32_t)(i >> 1) & 1, &abort_sm))) {
-            if (tid == 0) atomicOr(&g_status, (int)LOLA_ATTN_TIMEOUT);
+        const int slot = i % NS;
+        if (group_or<NT>(1 + grp, !ring_wait(smem_u32(&bars.seg_full[slot]), (uint32_t)(i / NS) & 1, &abort_sm))) {
+            if (gt == 0) atomicOr(&g_status, (int)LOLA_ATTN_TIMEOUT);
             break;
         }
         const Seg g = segs[slot];
         if (g.R < 0) break;
-        if (!SH && !g.whole && tid == 64) open_cells<D>(a, g);
-        // ---- q: row 8 b + g8, channels 16 y + 4 q4 .. + 3, with a power of two of the row's own; the lanes' rows of the
-        // scores are 8 b + q2 and + 1 ----
+        const int t0 = (grp + kGroups - g.n0 % kGroups) % kGroups, groups = min(kGroups, g.tiles), turn = multi;
+        multi += groups > 1;
+        if (t0 >= g.tiles) {                                            // (none of its tiles)
+            __syncwarp();
+            if (lane == 0) mbar_arrive1(smem_u32(&bars.seg_empty[slot]));
+            continue;
+        }
+        if (!SH && !g.whole && t0 == 0 && gt == 64) open_cells<D>(a, g);
+        // ---- q: row 8 b + g8.  e4m3: channels 16 y + 4 q4 .. + 3, with a power of two of the row's own; the lanes' rows of the
+        // scores are 8 b + q2 and + 1.  bfloat16: channels 16 y + q2, + 1, + 8, + 9 ----
         uint32_t qa[NB][D / 16][2], qr[kTwo ? NB : 1][kTwo ? D / 16 : 1][2];
         float qs[NB][2];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const uint8_t* row = x.q[slot] + (g8 + 8 * b) * M::kPitch;
-            uint32_t top = 0u;
-            auto channels = [&](int y, float(&v)[4]) {
-                if constexpr (kTwo) {
-                    const float4 z = *reinterpret_cast<const float4*>(row + (16 * y + 4 * q4) * 4);
-                    v[0] = z.x, v[1] = z.y, v[2] = z.z, v[3] = z.w;
-                } else {
-                    const uint2 z = *reinterpret_cast<const uint2*>(row + (16 * y + 4 * q4) * 2);
-                    v[0] = __uint_as_float(z.x << 16), v[1] = __uint_as_float(z.x & 0xffff0000u);
-                    v[2] = __uint_as_float(z.y << 16), v[3] = __uint_as_float(z.y & 0xffff0000u);
+            if constexpr (QZ) {
+                uint32_t top = 0u;
+                auto channels = [&](int y, float(&v)[4]) {
+                    if constexpr (kTwo) {
+                        const float4 z = *reinterpret_cast<const float4*>(row + (16 * y + 4 * q4) * 4);
+                        v[0] = z.x, v[1] = z.y, v[2] = z.z, v[3] = z.w;
+                    } else {
+                        const uint2 z = *reinterpret_cast<const uint2*>(row + (16 * y + 4 * q4) * 2);
+                        v[0] = __uint_as_float(z.x << 16), v[1] = __uint_as_float(z.x & 0xffff0000u);
+                        v[2] = __uint_as_float(z.y << 16), v[3] = __uint_as_float(z.y & 0xffff0000u);
+                    }
+                };
+#pragma unroll
+                for (int y = 0; y < D / 16; ++y) {
+                    float v[4];
+                    channels(y, v);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
                 }
-            };
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const uint32_t up = min(268u - (top >> 23), 240u);     // the largest magnitude goes to [2^14, 2^15)
+                const float f = __uint_as_float(up << 23);
 #pragma unroll
-            for (int y = 0; y < D / 16; ++y) {
-                float v[4];
-                channels(y, v);
+                for (int e = 0; e < 2; ++e)
+                    qs[b][e] = a.scale_log2 * __uint_as_float((254u - __shfl_sync(0xffffffffu, up, 4 * (q2 + e))) << 23);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
-            }
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const uint32_t up = min(268u - (top >> 23), 240u);         // the largest magnitude goes to [2^14, 2^15)
-            const float f = __uint_as_float(up << 23);
+                for (int y = 0; y < D / 16; ++y) {
+                    float v[4];
+                    channels(y, v);
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                qs[b][e] = a.scale_log2 * __uint_as_float((254u - __shfl_sync(0xffffffffu, up, 4 * (q2 + e))) << 23);
-#pragma unroll
-            for (int y = 0; y < D / 16; ++y) {
-                float v[4];
-                channels(y, v);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float u = v[2 * e] * f, w = v[2 * e + 1] * f;
-                    qa[b][y][e] = half2_of(u, w);
-                    if constexpr (kTwo) qr[b][y][e] = half2_rest(u, w, qa[b][y][e]);
+                    for (int e = 0; e < 2; ++e) {
+                        const float u = v[2 * e] * f, w = v[2 * e + 1] * f;
+                        qa[b][y][e] = half2_of(u, w);
+                        if constexpr (kTwo) qr[b][y][e] = half2_rest(u, w, qa[b][y][e]);
+                    }
                 }
+            } else {
+#pragma unroll
+                for (int y = 0; y < D / 16; ++y)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) qa[b][y][e] = *reinterpret_cast<const uint32_t*>(row + (16 * y + 8 * e + q2) * 2);
+                qs[b][0] = qs[b][1] = a.scale_log2;
             }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive1(smem_u32(&bars.seg_empty[slot]));   // (g and the Q rows are in registers)
-        // o: channels 16 y + 2 g8 (0, 1) and + 1 (2, 3), rows 8 b + q2 and + 1
+        // o: channels 16 y + 2 g8 (0, 1) and + 1 (2, 3), or (bfloat16) + g8 and + 8 + g8; rows 8 b + q2 and + 1
         float o[D / 16][NB][4], m[NB][2], l[NB][2];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -166,48 +194,65 @@ __global__ void __launch_bounds__(QSmem<TO, D, NB>::kAll * kWarp, 1) quant_decod
                 for (int e = 0; e < 4; ++e) o[y][b][e] = 0.f;
         }
         bool ok = true;
-        for (int t = (grp + kGroups - g.n0 % kGroups) % kGroups; t < g.tiles; t += kGroups) {
+        for (int t = t0; t < g.tiles; t += kGroups) {
             const int n = g.n0 + t, s = n % C::kStages;
             ok = issued_wait(&bars.issued, n, &abort_sm) &&
                  ring_wait(smem_u32(&bars.full[s]), (uint32_t)(n / C::kStages) & 1, &abort_sm);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const uint32_t kt = sb + (uint32_t)s * 2 * C::kHalf, vt = kt + C::kHalf;
-            const uint8_t* powers = sm + (size_t)C::kStages * 2 * C::kHalf + (size_t)s * C::kScales + g8;
+            [[maybe_unused]] const uint8_t* powers = sm + (size_t)C::kStages * 2 * C::kHalf + (size_t)s * C::kScales + g8;
             const int left = g.len - t * C::kTokens;
             const uint32_t bad = bad_sm[s];
 #pragma unroll 1
-            for (int k0 = (warp & 3) * 32, half = 0; half < 2; ++half, k0 += 16) {
-                const int token = k0 + row0;
+            for (int k0 = w4 * (C::kTokens / 4), end = k0 + C::kTokens / 4; k0 < end; k0 += 16) {
                 // ---- S^T: 16 tokens x 8 rows, two chains ----
                 float c0[NB][4] = {}, c1[NB][4] = {};
+                if constexpr (QZ) {
 #pragma unroll
-                for (int y = 0; y < D / 32; ++y) {
-                    uint32_t kb[4];
-                    ldsm4(kt + chunk_at(token, 2 * y + ch0), kb);
+                    for (int y = 0; y < D / 32; ++y) {
+                        uint32_t kb[4];
+                        ldsm4(kt + chunk_at(k0 + krow, 2 * y + kch), kb);
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        uint32_t ka[4];                                    // tokens g8, g8 + 8: channels 4 q4, + 1; then + 2, + 3
-                        widen(kb[2 * z], ka[0], ka[2]);
-                        widen(kb[2 * z + 1], ka[1], ka[3]);
+                        for (int z = 0; z < 2; ++z) {
+                            uint32_t ka[4];                            // tokens g8, g8 + 8: channels 4 q4, + 1; then + 2, + 3
+                            widen(kb[2 * z], ka[0], ka[2]);
+                            widen(kb[2 * z + 1], ka[1], ka[3]);
 #pragma unroll
-                        for (int b = 0; b < NB; ++b) {
-                            mma16816_h(z ? c1[b] : c0[b], ka, qa[b][2 * y + z][0], qa[b][2 * y + z][1]);
-                            if constexpr (kTwo) mma16816_h(z ? c1[b] : c0[b], ka, qr[b][2 * y + z][0], qr[b][2 * y + z][1]);
+                            for (int b = 0; b < NB; ++b) {
+                                mma16816_h(z ? c1[b] : c0[b], ka, qa[b][2 * y + z][0], qa[b][2 * y + z][1]);
+                                if constexpr (kTwo) mma16816_h(z ? c1[b] : c0[b], ka, qr[b][2 * y + z][0], qr[b][2 * y + z][1]);
+                            }
                         }
                     }
+                } else {
+#pragma unroll
+                    for (int y = 0; y < D / 16; ++y) {
+                        uint32_t ka[4];
+                        ldsm4(kt + chunk_at(k0 + krow, 2 * y + kch), ka);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) mma16816(y & 1 ? c1[b] : c0[b], ka, qa[b][y][0], qa[b][y][1]);
+                    }
                 }
-                // ---- scores and exponents of the weights: tokens k0 + g8 (0, 1), + 8 (2, 3) ----
-                float sc[NB][4], down[2];
+                // ---- scores and (e4m3) exponents of the weights: tokens k0 + g8 (0, 1), + 8 (2, 3) ----
+                float sc[NB][4];
+                [[maybe_unused]] float down[2];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const uint32_t kp = powers[k0 + 8 * y], vp = powers[C::kTokens + k0 + 8 * y];
-                    const float fk = __uint_as_float(kp << 23), fv = (float)(int)vp - 127.f;
-                    down[y] = power_down(vp);
+                    float fk = 1.f, fv = 0.f;
+                    if constexpr (QZ) {
+                        const uint32_t kp = powers[k0 + 8 * y], vp = powers[C::kTokens + k0 + 8 * y];
+                        fk = __uint_as_float(kp << 23);
+                        fv = (float)(int)vp - 127.f;
+                        down[y] = power_down(vp);
+                    }
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) sc[b][2 * y + e] = fmaf((c0[b][2 * y + e] + c1[b][2 * y + e]) * qs[b][e], fk, fv);
+                        for (int e = 0; e < 2; ++e) {
+                            const float z = (c0[b][2 * y + e] + c1[b][2 * y + e]) * qs[b][e];
+                            sc[b][2 * y + e] = QZ ? fmaf(z, fk, fv) : z;
+                        }
                 }
                 if (left < k0 + 16 || bad) {
                     // tokens behind the sequence or on bad pages: no score, and their V rows (which may
@@ -220,13 +265,13 @@ __global__ void __launch_bounds__(QSmem<TO, D, NB>::kAll * kWarp, 1) quant_decod
 #pragma unroll
                             for (int b = 0; b < NB; ++b) sc[b][2 * y] = sc[b][2 * y + 1] = -INFINITY;
                     for (int k = k0; k < k0 + 16; ++k)
-                        if (hidden(k) && lane < D / 16)
+                        if (hidden(k) && lane < C::kRowBytes / 16)
                             *reinterpret_cast<uint4*>(sm + (size_t)s * 2 * C::kHalf + C::kHalf + chunk_at(k, lane)) = make_uint4(0, 0, 0, 0);
-                    fence_async_smem();            // (before the ring's next copy lands on these rows)
+                    fence_async_smem();        // (before the ring's next copy lands on these rows)
                     __syncwarp();
                 }
                 // ---- running maximum, weights ----
-                uint32_t pb[NB][2], pr[kTwo ? NB : 1][2];                  // tokens 2 q4, + 1 (+ 8) of row 8 b + g8
+                uint32_t pb[NB][2], pr[kTwo ? NB : 1][2];              // tokens 2 q4, + 1 (+ 8) of row 8 b + g8
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                     float top[2];
@@ -256,40 +301,56 @@ __global__ void __launch_bounds__(QSmem<TO, D, NB>::kAll * kWarp, 1) quant_decod
                     for (int z = 0; z < 4; ++z) {
                         const int e = z & 1;
                         w[z] = ex2(sc[b][z] - (m[b][e] == -INFINITY ? 0.f : m[b][e]));
-                        l[b][e] = fmaf(w[z], down[z >> 1], l[b][e]);
-                        w[z] *= kUp;
+                        if constexpr (QZ) {
+                            l[b][e] = fmaf(w[z], down[z >> 1], l[b][e]);
+                            w[z] *= kUp;
+                        } else {
+                            l[b][e] += w[z];
+                        }
                     }
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const uint32_t h = half2_of(w[2 * y], w[2 * y + 1]);
+                        const uint32_t h = QZ ? half2_of(w[2 * y], w[2 * y + 1]) : pack2(w[2 * y], w[2 * y + 1]);
                         pb[b][y] = turned(h);
                         if constexpr (kTwo) pr[b][y] = turned(half2_rest(w[2 * y], w[2 * y + 1], h));
                     }
                 }
                 // ---- O^T += V^T P^T ----
+                if constexpr (QZ) {
 #pragma unroll
-                for (int y = 0; y < D / 32; ++y) {
-                    uint32_t vb[4];
-                    ldsm4_t(vt + chunk_at(token, 2 * y + ch0), vb);
+                    for (int y = 0; y < D / 32; ++y) {
+                        uint32_t vb[4];
+                        ldsm4_t(vt + chunk_at(k0 + vrow, 2 * y + vch), vb);
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        uint32_t va[4];                                    // channels 2 g8, 2 g8 + 1: tokens 2 q4, + 1; then + 8, + 9
-                        widen(__byte_perm(vb[2 * z], 0u, 0x3120), va[0], va[1]);
-                        widen(__byte_perm(vb[2 * z + 1], 0u, 0x3120), va[2], va[3]);
+                        for (int z = 0; z < 2; ++z) {
+                            uint32_t va[4];                            // channels 2 g8, 2 g8 + 1: tokens 2 q4, + 1; then + 8, + 9
+                            widen(__byte_perm(vb[2 * z], 0u, 0x3120), va[0], va[1]);
+                            widen(__byte_perm(vb[2 * z + 1], 0u, 0x3120), va[2], va[3]);
 #pragma unroll
-                        for (int b = 0; b < NB; ++b) {
-                            mma16816_h(o[2 * y + z][b], va, pb[b][0], pb[b][1]);
-                            if constexpr (kTwo) mma16816_h(o[2 * y + z][b], va, pr[b][0], pr[b][1]);
+                            for (int b = 0; b < NB; ++b) {
+                                mma16816_h(o[2 * y + z][b], va, pb[b][0], pb[b][1]);
+                                if constexpr (kTwo) mma16816_h(o[2 * y + z][b], va, pr[b][0], pr[b][1]);
+                            }
                         }
+                    }
+                } else {
+#pragma unroll
+                    for (int y = 0; y < D / 16; ++y) {
+                        uint32_t va[4];
+                        ldsm4_t(vt + chunk_at(k0 + vrow, 2 * y + vch), va);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) mma16816(o[y][b], va, pb[b][0], pb[b][1]);
                     }
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive1(smem_u32(&bars.empty[s]));
         }
-        // ---- the segment's end: add the warps in order, then o or the piece's record ----
-        if (group_or<NT>(1, !ok)) {
-            if (tid == 0) atomicOr(&g_status, (int)LOLA_ATTN_TIMEOUT);
+        // ---- the group's end: its warps in order ----
+        const int buf = turn & 1;
+        if (groups > 1 && ok) ok = joined_wait(&joined[buf], turn >> 1, &abort_sm);    // (the parts before are read)
+        if (group_or<NT>(1 + grp, !ok)) {
+            if (gt == 0) atomicOr(&g_status, (int)LOLA_ATTN_TIMEOUT);
             break;
         }
 #pragma unroll
@@ -299,8 +360,8 @@ __global__ void __launch_bounds__(QSmem<TO, D, NB>::kAll * kWarp, 1) quant_decod
 #pragma unroll
                 for (int z = 4; z < kWarp; z <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], z);
                 if (g8 == 0) {
-                    x.ms[warp][8 * b + q2 + e] = m[b][e];
-                    x.ls[warp][8 * b + q2 + e] = l[b][e];
+                    x.ms[grp][w4][8 * b + q2 + e] = m[b][e];
+                    x.ls[grp][w4][8 * b + q2 + e] = l[b][e];
                 }
             }
         bar();
@@ -311,18 +372,16 @@ __global__ void __launch_bounds__(QSmem<TO, D, NB>::kAll * kWarp, 1) quant_decod
             for (int e = 0; e < 2; ++e) {
                 float mm = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < NW; ++w) mm = fmaxf(mm, x.ms[w][8 * b + q2 + e]);
-                f[b][e] = ex2(m[b][e] - (mm == -INFINITY ? 0.f : mm)) * (1.f / kUp);
+                for (int w = 0; w < 4; ++w) mm = fmaxf(mm, x.ms[grp][w][8 * b + q2 + e]);
+                f[b][e] = ex2(m[b][e] - (mm == -INFINITY ? 0.f : mm)) * (QZ ? 1.f / kUp : 1.f);
             }
         float* rec = segment_record<D, SH>(a, g);
-        const int er = 4 * (tid & 127) / CK, ec = 4 * (tid & 127) % CK;        // 128 threads x 4 columns = 8 NB x CK
+        const int er = 4 * gt / CK, ec = 4 * gt % CK;                          // 128 threads x 4 columns = 8 NB x CK
         float mm = -INFINITY, ll = 0.f;
-        if (tid < 128) {
 #pragma unroll
-            for (int w = 0; w < NW; ++w) mm = fmaxf(mm, x.ms[w][er]);
+        for (int w = 0; w < 4; ++w) mm = fmaxf(mm, x.ms[grp][w][er]);
 #pragma unroll
-            for (int w = 0; w < NW; ++w) ll = fmaf(x.ls[w][er], ex2(x.ms[w][er] - (mm == -INFINITY ? 0.f : mm)), ll);
-        }
+        for (int w = 0; w < 4; ++w) ll = fmaf(x.ls[grp][w][er], ex2(x.ms[grp][w][er] - (mm == -INFINITY ? 0.f : mm)), ll);
 #pragma unroll
         for (int c = 0; c < D; c += CK) {
             if (c > 0) bar();
@@ -331,40 +390,88 @@ __global__ void __launch_bounds__(QSmem<TO, D, NB>::kAll * kWarp, 1) quant_decod
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        *reinterpret_cast<float2*>(&x.red[warp][8 * b + q2 + e][16 * y + 2 * g8]) =
-                            make_float2(o[c / 16 + y][b][e] * f[b][e], o[c / 16 + y][b][2 + e] * f[b][e]);
+                    for (int e = 0; e < 2; ++e) {
+                        const float(&z)[4] = o[c / 16 + y][b];
+                        float* to = &x.red[grp][w4][8 * b + q2 + e][16 * y];
+                        if constexpr (QZ) {
+                            *reinterpret_cast<float2*>(to + 2 * g8) = make_float2(z[e] * f[b][e], z[2 + e] * f[b][e]);
+                        } else {
+                            to[g8] = z[e] * f[b][e];
+                            to[8 + g8] = z[2 + e] * f[b][e];
+                        }
+                    }
             bar();
-            if (tid < 128) {
-                float y[4] = {0.f, 0.f, 0.f, 0.f};
+            float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int w = 0; w < NW; ++w) {
-                    const float4 z = *reinterpret_cast<const float4*>(&x.red[w][er][ec]);
-                    y[0] += z.x;
-                    y[1] += z.y;
-                    y[2] += z.z;
-                    y[3] += z.w;
+            for (int w = 0; w < 4; ++w) {
+                const float4 z = *reinterpret_cast<const float4*>(&x.red[grp][w][er][ec]);
+                y[0] += z.x;
+                y[1] += z.y;
+                y[2] += z.z;
+                y[3] += z.w;
+            }
+            if (groups > 1) store4(&x.part[buf][grp][er][c + ec], y);
+            else if (er < g.R) write_out<TO, D, SH>(a, g, g.whole, rec, er, c + ec, y, mm, ll);
+        }
+        if (groups > 1) {
+            // ---- the groups in order, by the last of them ----
+            if (ec == 0) {
+                x.part_ml[buf][grp][0][er] = mm;
+                x.part_ml[buf][grp][1][er] = ll;
+            }
+            __threadfence_block();
+            bar();
+            if (gt == 0) go[grp] = (atomicAdd(&joined[buf], 1) & 0xffff) == groups - 1;
+            bar();
+            if (!go[grp]) continue;
+            __threadfence_block();
+            for (int e = gt; e < g.R * (D / 4); e += NT) {
+                const int r = e / (D / 4), c = e % (D / 4) * 4;
+                float top = -INFINITY, sum = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+                auto has = [&](int k) { return (k + kGroups - g.n0 % kGroups) % kGroups < g.tiles; };
+#pragma unroll
+                for (int k = 0; k < kGroups; ++k)
+                    if (has(k)) top = fmaxf(top, x.part_ml[buf][k][0][r]);
+#pragma unroll
+                for (int k = 0; k < kGroups; ++k) {
+                    if (!has(k)) continue;
+                    const float w = ex2(x.part_ml[buf][k][0][r] - (top == -INFINITY ? 0.f : top));
+                    const float4 z = *reinterpret_cast<const float4*>(&x.part[buf][k][r][c]);
+                    sum = fmaf(w, x.part_ml[buf][k][1][r], sum);
+                    y[0] = fmaf(w, z.x, y[0]);
+                    y[1] = fmaf(w, z.y, y[1]);
+                    y[2] = fmaf(w, z.z, y[2]);
+                    y[3] = fmaf(w, z.w, y[3]);
                 }
-                if (er < g.R) write_out<TO, D, SH>(a, g, g.whole, rec, er, c + ec, y, mm, ll);
+                write_out<TO, D, SH>(a, g, g.whole, rec, r, c, y, top, sum);
+            }
+            bar();
+            if (gt == 0) {
+                __threadfence_block();
+                atomicAdd(&joined[buf], 0x10000 - groups);                     // (one more segment, no group of the next one yet)
             }
         }
-        if (!SH && !g.whole) join_pieces<TO, D, NT>(a, g, tid, &go, bars.arrived, bar);
+        if (!SH && !g.whole) join_pieces<TO, D, NT>(a, g, gt, &go[grp], bars.arrived, bar);
     }
     __syncthreads();
-    if (abort_sm) settle<D, C::kStages, 2, SH, M::kAll * kWarp, C::kTokens>(a, bars);
+    if (abort_sm) settle<D, C::kStages, NS, SH, M::kAll * kWarp, C::kTokens>(a, bars);
 }
 
-template <typename TO, int D, bool SH>
-cudaError_t launch_quant(const DecodeArgs& d, cudaStream_t st) {
-    static std::atomic<uint64_t> done[2] = {};
-    return (!SH || d.sh.each) && d.p.G <= 8
-               ? launch_kernel<uint8_t, D>(quant_decode_kernel<TO, D, 1, SH>, QSmem<TO, D, 1>::kAll, done[0], d, st)
-               : launch_kernel<uint8_t, D>(quant_decode_kernel<TO, D, 2, SH>, QSmem<TO, D, 2>::kAll, done[1], d, st);
+template <typename T, typename TO, int D, int NB, bool SH>
+cudaError_t launch_t(const DecodeArgs& d, cudaStream_t st) {
+    using M = TSmem<T, TO, D, NB>;
+    using C = Ring<Cfg<T, D>, M::kRing>;
+    static_assert(C::kSmem + sizeof(M) + 2048 <= 232448, "");
+    static std::atomic<uint64_t> done{0};
+    return launch_kernel<T, D>(decode_t_kernel<T, TO, D, NB, SH>, M::kAll, done, d, st, C::kSmem + (int)sizeof(M));
 }
-
+// (rows of a prefix: as many as its sequences have)
+template <typename T, typename TO, int D, bool SH> cudaError_t launch_t(const DecodeArgs& d, cudaStream_t st) {
+    return (!SH || d.sh.each) && d.p.G <= 8 ? launch_t<T, TO, D, 1, SH>(d, st) : launch_t<T, TO, D, 2, SH>(d, st);
+}
 template <bool SH> cudaError_t launch_quant(const DecodeArgs& a, cudaStream_t st) {
-    if (a.p.dtype == LOLA_F32) return a.p.d == 128 ? launch_quant<float, 128, SH>(a, st) : launch_quant<float, 64, SH>(a, st);
-    return a.p.d == 128 ? launch_quant<__nv_bfloat16, 128, SH>(a, st) : launch_quant<__nv_bfloat16, 64, SH>(a, st);
+    if (a.p.dtype == LOLA_F32) return a.p.d == 128 ? launch_t<uint8_t, float, 128, SH>(a, st) : launch_t<uint8_t, float, 64, SH>(a, st);
+    return a.p.d == 128 ? launch_t<uint8_t, __nv_bfloat16, 128, SH>(a, st) : launch_t<uint8_t, __nv_bfloat16, 64, SH>(a, st);
 }
 
 // ---- the cached rows as rows ----
@@ -488,6 +595,9 @@ template <typename T, int D> cudaError_t launch_read(const ReadArgs& a, cudaStre
 
 cudaError_t launch_quant_decode(const DecodeArgs& a, cudaStream_t st) { return launch_quant<false>(a, st); }
 cudaError_t launch_quant_parts(const DecodeArgs& a, cudaStream_t st) { return launch_quant<true>(a, st); }
+cudaError_t launch_bf16_parts(const DecodeArgs& a, cudaStream_t st) {
+    return a.p.d == 128 ? launch_t<__nv_bfloat16, __nv_bfloat16, 128, true>(a, st) : launch_t<__nv_bfloat16, __nv_bfloat16, 64, true>(a, st);
+}
 
 cudaError_t launch_quant_read(const ReadArgs& a, cudaStream_t st) {
     if (a.p.dtype == LOLA_F32) return a.p.d == 128 ? launch_read<float, 128>(a, st) : launch_read<float, 64>(a, st);

@@ -182,12 +182,12 @@ int64_t shared_workspace(int n_seq, int Hq, int d, int dtype) {
 cudaError_t launch_shared_prefix(const SharedArgs& a, cudaStream_t st) {
     const DecodeArgs d = parts_args(a, false);
     if (a.p.dtype == LOLA_BF16) return launch_prefix_tc(d, st);
-    return a.p.Ks ? launch_quant_parts(d, st) : launch_paged_parts(d, st);
+    return a.p.Ks ? launch_quant_parts(d, st) : launch_f32_parts(d, st);
 }
 
 cudaError_t launch_shared_own(const SharedArgs& a, cudaStream_t st) {
     const DecodeArgs d = parts_args(a, true);
-    const cudaError_t e = a.p.Ks ? launch_quant_parts(d, st) : launch_paged_parts(d, st);
+    const cudaError_t e = a.p.Ks ? launch_quant_parts(d, st) : a.p.dtype == LOLA_BF16 ? launch_bf16_parts(d, st) : launch_f32_parts(d, st);
     if (e != cudaSuccess) return e;
     JoinArgs j;
     j.p = a.p;
