@@ -49,6 +49,7 @@ template <typename T, int D> struct Cfg {
     static constexpr int kRowBytes = D * (int)sizeof(T);
     static constexpr int kHalf = kTokens * kRowBytes;              // K or V of a tile
     static constexpr int kScales = sizeof(T) == 1 ? 2 * kTokens : 0;   // bytes of powers of a tile
+    static constexpr int kFull = sizeof(T) == 1 ? 1 + kWarp : 1;   // arrivals that a loaded tile takes
     static constexpr int kMost = 12;
     static constexpr int kStages = 196608 / (2 * kHalf + kScales) > kMost ? kMost : 196608 / (2 * kHalf + kScales);
     static constexpr int kSmem = kStages * (2 * kHalf + kScales) + 1024;
@@ -158,6 +159,10 @@ __device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, int* ab
             return false;
         }
     }
+}
+// 4 bytes, asynchronously
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 // the producer has armed tile n's stage: only then does the parity of n's phase tell it from the one
 // before (a group that has not waited for that one, which was another group's, would pass at once)
@@ -279,9 +284,10 @@ __device__ __forceinline__ void place_piece(const Start& st, int64_t xs, int til
 
 // The producer warp: segments and their tiles, in order.  A tile's pages outside the cache are not
 // loaded; bit x of bad_sm marks the tile's x-th token box.  Segment i goes to slot i % NS.
-// TQ: the queries' numbers.  e4m3: four warps (`part` 0-3: codes of K, of V, powers of K, of V) that walk the segments
-// side by side, as each copy takes its thread some 180 clocks to issue, and a tile of codes half a tile's time at most
-// (all four copies by one warp: 64 sequences of 1000-8000 tokens, 32/8 heads, d = 128, 117 us).  The first of them does the rest.
+// TQ: the queries' numbers.  e4m3: three warps (`part` 0-2: codes of K, of V, powers of both) that walk the segments side
+// by side, as each copy takes its thread some 180 clocks to issue, and a tile of codes half a tile's time at most (all
+// copies by one warp: 64 sequences of 1000-8000 tokens, 32/8 heads, d = 128, 117 us).  The first of them does the rest.
+// The powers come four bytes a lane, past the tensor unit, whose small copies take as long as its large ones.
 template <typename T, typename TQ, int D, int NS, bool SH, typename C = Cfg<T, D>, int ROWS = kRows, typename B>
 __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const Start& st, uint32_t ring, uint32_t qs,
                                         uint32_t q_pitch, B& bars, Seg* segs, uint32_t* bad_sm, int* abort_sm, int lane, int part = 0) {
@@ -355,18 +361,27 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
             if (first && lane == 0) {
                 if (bad_mask) atomicOr(&g_status, (int)LOLA_ATTN_BAD_PAGE);
                 bad_sm[s] = bad_mask;
-                mbar_expect(smem_u32(&bars.full[s]), (uint32_t)(2 * (used - __popc(bad_mask)) * box * (C::kRowBytes + (C::kScales ? 1 : 0))));
+                mbar_expect(smem_u32(&bars.full[s]), (uint32_t)(2 * (used - __popc(bad_mask)) * box * C::kRowBytes));
                 *reinterpret_cast<volatile int*>(&bars.issued) = n + 1;
             }
             __syncwarp();
+            if constexpr (kParts) {
+                if (part == 2) {
+                    const int k = 4 * lane, of = __shfl_sync(0xffffffffu, held, ((int)((pos + k) >> p.page_log2) - held_c) & 31);
+                    if ((k >> lb) < used && of >= 0) {
+                        const int64_t at = ((int64_t)of * p.Hkv + hk) * p.page + ((pos + k) & (p.page - 1));
+                        const uint32_t to = ring + (uint32_t)C::kStages * 2 * C::kHalf + (uint32_t)s * C::kScales + k;
+                        cp_async4(to, p.Ks + at);
+                        cp_async4(to + C::kTokens, p.Vs + at);
+                    }
+                    cp_async_arrive_noinc(smem_u32(&bars.full[s]));
+                    continue;
+                }
+            }
             if (mine && !bad && (!kParts || lane < 16)) {
-                const int at = (int)((pos + x * box) & (p.page - 1)), v = kParts ? part & 1 : lane >> 4;
-                if (!kParts || part < 2)
-                    tma_load4(ring + (uint32_t)s * 2 * C::kHalf + v * C::kHalf + x * (uint32_t)(box * C::kRowBytes), v ? &maps.v : &maps.k, 0,
-                              kParts ? at * D / 128 : at, 0, page * p.Hkv + hk, smem_u32(&bars.full[s]));
-                else if constexpr (kParts)
-                    bulk_load(ring + (uint32_t)C::kStages * 2 * C::kHalf + (uint32_t)s * C::kScales + v * C::kTokens + x * box,
-                              (v ? p.Vs : p.Ks) + ((int64_t)page * p.Hkv + hk) * p.page + at, (uint32_t)box, smem_u32(&bars.full[s]));
+                const int at = (int)((pos + x * box) & (p.page - 1)), v = kParts ? part : lane >> 4;
+                tma_load4(ring + (uint32_t)s * 2 * C::kHalf + v * C::kHalf + x * (uint32_t)(box * C::kRowBytes), v ? &maps.v : &maps.k, 0,
+                          kParts ? at * D / 128 : at, 0, page * p.Hkv + hk, smem_u32(&bars.full[s]));
             }
         }
         if (give_up) {

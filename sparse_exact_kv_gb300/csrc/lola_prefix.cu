@@ -44,6 +44,12 @@ template <int D, bool QZ> struct PCfg {
     static constexpr int kRaw = QZ ? (D == 128 ? 4 : 8) : 1;            // blocks of codes (K or V)
     static constexpr int kRawBytes = QZ ? kN * D + 2 * kN : 0;         // codes, their powers, behind keys the values' powers too
     static constexpr int kSmem = (2 + kRing) * kTileBytes + kRaw * kRawBytes + 1024;
+    // Registers of a softmax thread and of the others: what the block was launched with, 168 or 128 a thread, given out
+    // anew, so that a row's 128 scores fit.  QZ at d = 128 is bound by the conversion, whose warps need theirs (128
+    // sequences behind 131072 tokens: 300 us, 334 with 192 and 64), and reads half of the scores twice; at d = 64 the
+    // scores come first (64 behind 64000 tokens, 32/8 heads: 60 us, 68 the other way).
+    static constexpr int kSoftmaxRegs = QZ ? (D == 128 ? 128 : 192) : 208, kOtherRegs = QZ ? (D == 128 ? 128 : 64) : 88;
+    static constexpr int kHeld = QZ && D == 128 ? 64 : kN;             // scores in registers
     __device__ static constexpr uint32_t TS(int i) { return 128u * i; }  // S (P over its first half)
     __device__ static constexpr uint32_t TO(int i) { return 256u + (uint32_t)D * i; }
 };
@@ -77,6 +83,7 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
     const int tid = threadIdx.x, warp = tid / kWarp, lane = tid % kWarp;
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     if (tid == 0) {
+        auto mbar_init = [](uint32_t at, int count) { asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(at), "r"(count)); };
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(B_SEG + i), 1);
             mbar_init(bar(B_SEGFREE + i), 9);            // softmax warps, products
@@ -96,6 +103,7 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
             mbar_init(bar(B_RFULL + s), 1);
             mbar_init(bar(B_REMPTY + s), 4);
         }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         abort_sm = 0;
     }
     wait_for_last_kernel();
@@ -150,13 +158,34 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
         }
         segs[seg & 1] = g;
     };
+    w_tokens = (int)paged_tokens(p, p.kv_len[w_b]);
+    w_gr = group_of<true, kItem>(a, w_b);
+    w_tiles = tiles_of<kN>(w_tokens);
+    w_item = divide(st.rem, w_tiles, &w_t0);
+    // ---- Q rows of tile i, 16 bytes a lane, into the layout that the products read: on their way (those of the first
+    // segment while the pages are looked up and TMEM is allocated, before K and V fill the memory's queues) ----
+    constexpr int QCH = D / 8, QPER = 32 / QCH;                          // chunks of a row; rows at a time
+    const int q_ch = lane % QCH, q_row = (warp & 3) * 32 + lane / QCH;
+    auto load_q = [&](int i, int m0, int r0, int R, int hk) {
+        const int tile_row = R > kM ? kM * i : 0;
+        const uint32_t at = sb + (uint32_t)i * C::kTileBytes + 16384u * (q_ch >> 3);
+        const int flat = r0 + tile_row + q_row, seq = flat / p.G;
+        int h = flat - seq * p.G;
+        const char* src = a.Q.data + ((int64_t)(m0 + seq) * a.Q.row + (int64_t)(hk * p.G + h) * a.Q.head + 8 * q_ch) * 2;
+#pragma unroll 1
+        for (int x = 0; x < 32; x += QPER) {
+            const bool in = tile_row + q_row + x < R;
+            cp_async16_z(at + kmaj_chunk(q_row + x, q_ch & 7), in ? src : a.Q.data, in ? 16u : 0u);
+            src += (int64_t)QPER * a.Q.head * 2;
+            for (h += QPER; h >= p.G; h -= p.G) src += (a.Q.row - (int64_t)p.G * a.Q.head) * 2;
+        }
+    };
     if (warp == C::kLoadWarp) {
-        w_tokens = (int)paged_tokens(p, p.kv_len[w_b]);
-        w_gr = group_of<true, kItem>(a, w_b);
-        w_tiles = tiles_of<kN>(w_tokens);
-        w_item = divide(st.rem, w_tiles, &w_t0);
         w_page = page_of(w_t0, w_tiles);
         if (lane == 0) make_seg(st.u0, 0, 0, 0);
+    } else if (warp < C::kMmaWarp) {
+        const int r0 = share > 1 ? (int)blockIdx.x % share * kItem : (w_item % w_gr.RG) * kItem;
+        load_q(warp >> 2, w_gr.m0, r0, min(kItem, w_gr.rows - r0), share > 1 ? w_item : w_item / w_gr.RG);
     }
     fence_before();
     __syncthreads();
@@ -176,8 +205,7 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
     auto look_of = [](const PSeg& g) { return g.R > kM ? 1 : 2; };
 
     if (warp >= C::kMmaWarp) {
-        // (what the block was launched with, 168 a thread, given out anew; QZ: 128, which do for all)
-        if constexpr (!QZ) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if constexpr (C::kOtherRegs < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
         if (warp == C::kLoadWarp) {
             // ================================ pages and loads ================================
             const int box = w_box, lb = 31 - __clz(box), nbox = kN >> lb;               // tokens of a box, boxes of a block
@@ -192,10 +220,8 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
                 const int t0 = w_t0, t1 = (int)min((int64_t)w_tiles, t0 + (st.u1 - u)), nb = t1 - t0, tokens = w_tokens;
                 const int r0 = share > 1 ? (int)blockIdx.x % share * kItem : (w_item % w_gr.RG) * kItem;
                 const int hk = share > 1 ? w_item : w_item / w_gr.RG, look = w_gr.rows - r0 > kM ? 1 : 2;
-                if (lane == 0) {
-                    if (p.kv_len[w_b] > tokens) wrong = 1;
-                    mbar_arrive1(bar(B_SEG + (seg & 1)));
-                }
+                if (lane == 0) mbar_arrive1(bar(B_SEG + (seg & 1)));
+                if (p.kv_len[w_b] > tokens) wrong = 1;
                 // the page of this lane's box of the next block, and of those that wait for their V
                 int next = seg == 0 ? (t0 < t1 ? w_page : -1) : page_of(t0, t1), now = -1, held[2] = {-1, -1};
                 ++seg;
@@ -419,7 +445,7 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
         }
     } else {
         // ================================ softmax ================================
-        if constexpr (!QZ) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        if constexpr (C::kSoftmaxRegs > 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
         const int i = warp >> 2, r = (warp & 3) * 32 + lane;                    // tile, row of the tile
         const uint32_t lo = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tb + lo + C::TS(i), to = tb + lo + C::TO(i);
@@ -434,39 +460,28 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
             const int n = two ? g.nb : (g.nb + 1 - i) / 2, look = look_of(g);
             const int tile_row = two ? kM * i : 0;
             if (n > 0) {
-                // ---- Q rows of the tile, 16 bytes a lane, into the layout that the products read ----
-                constexpr int CH = D / 8, PER = 32 / CH;                        // chunks of a row; rows at a time
-                const int ch = lane % CH, row0 = (warp & 3) * 32 + lane / CH;
-                const uint32_t q_at = smem_u32(Qt) + 16384u * (ch >> 3);
-                int flat = g.r0 + tile_row + row0, seq = flat / p.G, h = flat - seq * p.G;
-                const char* src = a.Q.data + ((int64_t)(g.m0 + seq) * a.Q.row + (int64_t)(g.hk * p.G + h) * a.Q.head + 8 * ch) * 2;
-#pragma unroll 1
-                for (int x = 0; x < 32; x += PER) {
-                    const bool in = tile_row + row0 + x < g.R;
-                    cp_async16_z(q_at + kmaj_chunk(row0 + x, ch & 7), in ? src : a.Q.data, in ? 16u : 0u);
-                    src += (int64_t)PER * a.Q.head * 2;
-                    for (h += PER; h >= p.G; h -= p.G) src += (a.Q.row - (int64_t)p.G * a.Q.head) * 2;
-                }
+                // ---- Q rows of the tile ----
+                if (it > 0) load_q(i, g.m0, g.r0, g.R, g.hk);
                 cp_async_wait_all();
                 if constexpr (QZ) {
                     // float16 numbers, the row's largest magnitude in [2^14, 2^15)
 #pragma unroll 4
-                    for (int x = 0; x < 32; x += PER) {
-                        uint4* at = reinterpret_cast<uint4*>(Qt + 16384 * (ch >> 3) + kmaj_chunk(row0 + x, ch & 7));
+                    for (int x = 0; x < 32; x += QPER) {
+                        uint4* at = reinterpret_cast<uint4*>(Qt + 16384 * (q_ch >> 3) + kmaj_chunk(q_row + x, q_ch & 7));
                         const uint4 z = *at;
                         uint32_t w[4] = {z.x, z.y, z.z, z.w}, big = 0u;
 #pragma unroll
                         for (int y = 0; y < 4; ++y) big = max(big, max((w[y] << 16) & 0x7fff0000u, w[y] & 0x7fff0000u));
 #pragma unroll
-                        for (int o = 1; o < CH; o <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+                        for (int o = 1; o < QCH; o <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
                         const uint32_t up = min(268u - (big >> 23), 240u);
                         const float f = __uint_as_float(up << 23);
 #pragma unroll
                         for (int y = 0; y < 4; ++y) w[y] = half2_of(__uint_as_float(w[y] << 16) * f, __uint_as_float(w[y] & 0xffff0000u) * f);
                         *at = make_uint4(w[0], w[1], w[2], w[3]);
-                        // (rows x .. x + PER - 1 of the warp's 32 are those of lanes x ..)
-                        const uint32_t mine = __shfl_sync(0xffffffffu, up, ((lane - x) * CH) & 31);
-                        if (lane >= x && lane < x + PER) c = a.scale_log2 * __uint_as_float((254u - mine) << 23);
+                        // (rows x .. x + QPER - 1 of the warp's 32 are those of lanes x ..)
+                        const uint32_t mine = __shfl_sync(0xffffffffu, up, ((lane - x) * QCH) & 31);
+                        if (lane >= x && lane < x + QPER) c = a.scale_log2 * __uint_as_float((254u - mine) << 23);
                     }
                 }
                 fence_async_smem();
@@ -479,19 +494,22 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
                 const int j = two ? jj : 2 * jj + i;
                 if (!(ok = wait_all(B_S + i, (uint32_t)(ns + jj)))) break;
                 fence_after();
-                // (QZ: columns 64 .. 127 are read twice, as 128 registers a thread do not hold all)
-                constexpr int kHeld = QZ ? 64 : kN;
+                // (QZ, d = 128: columns 64 .. 127 are read twice, as 128 registers a thread do not hold all)
+                constexpr int kHeld = C::kHeld;
                 float s[kHeld];
                 const int valid = g.len - j * kN;
                 const uint32_t bad = bad_sm[(g.blk0 + j) % kBad];
                 const bool some = valid < kN || bad;
                 const int lb = 31 - __clz(min(p.page, kN));
-                // columns x0 .. x0 + 31 in s[at ..]
+                // columns x0 .. x0 + 31 in s[at ..] (rare: a branch, and not conditions in every block's path)
                 auto hide = [&](int at, int x0) {
                     if (!some) return;
+                    asm volatile("" ::: "memory");
+                    uint32_t seen = valid >= x0 + 32 ? ~0u : valid <= x0 ? 0u : (1u << (valid - x0)) - 1u;
+                    for (int x = 0; x < 32; x += 1 << min(lb, 5))
+                        if ((bad >> ((x0 + x) >> lb)) & 1u) seen &= lb >= 5 ? 0u : ~(((1u << (1 << lb)) - 1u) << x);
 #pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        if (x0 + x >= valid || (bad >> ((x0 + x) >> lb)) & 1u) s[at + x] = -INFINITY;
+                    for (int x = 0; x < 32; ++x) s[at + x] = (seen >> x) & 1u ? s[at + x] : -INFINITY;
                 };
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -558,7 +576,7 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
                     }
                     tmem_st16(ts + x / 2, pw);
                 };
-                if constexpr (QZ) {
+                if constexpr (kHeld < kN) {
                     // (a place's next columns are under way while the other's are weighed)
                     auto arrived = [&](int at, int x) {
                         tmem_wait_ld();

@@ -44,7 +44,7 @@ __device__ __forceinline__ uint32_t turned(uint32_t x) {
 // T: the cache's numbers (bfloat16, or uint8_t: e4m3).  NB: query rows in eights.
 template <typename T, typename TO, int D, int NB> struct TSmem {
     static constexpr int kGroups = NB == 1 ? 3 : 2;                         // groups of four consumer warps
-    static constexpr int NW = 4 * kGroups, kAll = NW + (sizeof(T) == 1 ? 4 : 1);    // consumer warps, and all
+    static constexpr int NW = 4 * kGroups, kAll = NW + (sizeof(T) == 1 ? 3 : 1);    // consumer warps, and all
     static constexpr int NS = sizeof(TO) == 4 ? 2 : 4;                      // segments under way
     static constexpr int kRing = (D == 128 ? 5 : 10) - (NB == 1 ? 0 : D == 128 ? 1 : 2);   // tiles
     static constexpr int kCk = NB == 1 ? 64 : 32;                           // columns joined at a time
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(TSmem<T, TO, D, NB>::kAll * kWarp, 1) decode_t
     const int tid = threadIdx.x, warp = tid / kWarp, lane = tid % kWarp;
     if (tid == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(smem_u32(&bars.full[s]), 1);
+            mbar_init(smem_u32(&bars.full[s]), C::kFull);
             mbar_init(smem_u32(&bars.empty[s]), 4);
         }
         for (int s = 0; s < NS; ++s) {
