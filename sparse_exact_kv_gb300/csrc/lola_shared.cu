@@ -5,8 +5,8 @@
 // kernel here joins them:
 //   m = max_k m_k,  l = sum_k 2^{m_k - m} l_k,  o = sum_k 2^{m_k - m} z_k / l,
 // the prefix' parts first, in the order of the pieces: the same inputs give the same bits.
-// Bound by its chain of accesses (which parts, the parts): four rows a CTA, a row's parts dealt out to four warps,
-// which have eight of them in flight each.  (When the kernel over the own tokens read the prefix' parts itself, row
+// Bound by its chain of accesses (which parts, the parts): two rows a CTA, their parts dealt out to eight warps,
+// which have three of them in flight each.  (When the kernel over the own tokens read the prefix' parts itself, row
 // after row, 64 sequences behind 16001 tokens took it 92 us, 8 heads, d = 128.)
 #include "lola_paged.cuh"
 
@@ -25,6 +25,14 @@ struct JoinArgs {
 // kernel has worked for b too.
 __device__ __forceinline__ int prefix_of(const JoinArgs& a, int b, int lane) {
     int g = 0, lo, n, bad = 0;
+    if (a.cu && a.prefix.n_seq < kWarp) {
+        // (few prefixes: all offsets and lengths at once)
+        const int c = lane <= a.prefix.n_seq ? a.cu[lane] : 0x7fffffff, len = lane < a.prefix.n_seq ? a.prefix.kv_len[lane] : 0;
+        g = 31 - __clz(__ballot_sync(0xffffffffu, c <= b));
+        const int begin = __shfl_sync(0xffffffffu, c, max(g, 0)), end = __shfl_sync(0xffffffffu, c, min(g + 1, kWarp - 1));
+        const int tokens = __shfl_sync(0xffffffffu, len, max(g, 0));
+        return g >= 0 && g < a.prefix.n_seq && begin >= 0 && end > b && end <= a.p.n_seq && paged_tokens(a.prefix, tokens) > 0 ? g : -1;
+    }
     if (a.cu) {
         g = warp_find_seq(a.cu, a.prefix.n_seq, b, lane);
         if (g < 0 || g >= a.prefix.n_seq) return -1;
@@ -62,12 +70,12 @@ template <int N> __device__ __forceinline__ void add_part(float m, float l, cons
 
 // Two rows a warp, in the lanes by turns (neighbouring rows' 16 bytes of a record share a sector).
 template <typename T, int D>
-__global__ void __launch_bounds__(256) shared_join_kernel(const JoinArgs a) {
-    constexpr int N = D / 64, kWarps = 4, kBatch = 4;                    // float4 of a lane; warps of a row; parts in flight
-    __shared__ float4 y_sm[2][kWarps][N][kWarp];
-    __shared__ float2 ml_sm[2][kWarps][2];
-    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, pair = warp / kWarps, w = warp % kWarps, own = lane >> 1;
-    const int64_t rows = (int64_t)a.p.n_seq * a.p.Hq, i0 = ((int64_t)blockIdx.x * 2 + pair) * 2, i = i0 + (lane & 1);
+__global__ void __launch_bounds__(256, 4) shared_join_kernel(const JoinArgs a) {
+    constexpr int N = D / 64, kWarps = 8, kBatch = 3;                    // float4 of a lane; warps; parts in flight
+    __shared__ float4 y_sm[kWarps][N][kWarp];
+    __shared__ float2 ml_sm[kWarps][2];
+    const int w = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, own = lane >> 1;
+    const int64_t rows = (int64_t)a.p.n_seq * a.p.Hq, i0 = (int64_t)blockIdx.x * 2, i = i0 + (lane & 1);
     wait_for_last_kernel();
     const int b0 = (int)(min(i0, rows - 1) / a.p.Hq), b1 = (int)(min(i0 + 1, rows - 1) / a.p.Hq), b = lane & 1 ? b1 : b0;
     int4 at_a = make_int4(0, 0, 0, 0), at_b = at_a;
@@ -107,16 +115,16 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const JoinArgs a) {
             if (k0 + kWarps * e < n) add_part<N>(m[e], l[e], z[e], y, M, L);
     }
 #pragma unroll
-    for (int x = 0; x < N; ++x) y_sm[pair][w][x][lane] = y[x];
-    if (own == 0) ml_sm[pair][w][lane & 1] = make_float2(M, L);
+    for (int x = 0; x < N; ++x) y_sm[w][x][lane] = y[x];
+    if (own == 0) ml_sm[w][lane & 1] = make_float2(M, L);
     __syncthreads();
     if (w > 0 || i >= rows) return;
 #pragma unroll
     for (int e = 1; e < kWarps; ++e) {
         float4 z[N];
 #pragma unroll
-        for (int x = 0; x < N; ++x) z[x] = y_sm[pair][e][x][lane];
-        const float2 ml = ml_sm[pair][e][lane & 1];
+        for (int x = 0; x < N; ++x) z[x] = y_sm[e][x][lane];
+        const float2 ml = ml_sm[e][lane & 1];
         add_part<N>(ml.x, ml.y, z, y, M, L);
     }
     // (no token seen: o = 0; scores that are all minus infinity: 0 / 0)
@@ -196,7 +204,7 @@ cudaError_t launch_shared_own(const SharedArgs& a, cudaStream_t st) {
     carve(&j.a, &j.b, a.workspace, a.p.n_seq, a.p.Hq, a.p.d, a.p.dtype);
     j.O = a.O;
     j.lse = a.lse;
-    const unsigned grid = (unsigned)(((int64_t)a.p.n_seq * a.p.Hq + 3) / 4);
+    const unsigned grid = (unsigned)(((int64_t)a.p.n_seq * a.p.Hq + 1) / 2);
     if (a.p.dtype == LOLA_F32)
         return a.p.d == 128 ? launch_behind(shared_join_kernel<float, 128>, grid, 256, 0, st, j)
                             : launch_behind(shared_join_kernel<float, 64>, grid, 256, 0, st, j);
