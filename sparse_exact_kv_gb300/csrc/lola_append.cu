@@ -174,31 +174,14 @@ __device__ __forceinline__ void quantise_unit(Unit<T>& n, bool neighbours, int s
     if (first) *n.power = (uint8_t)power;
 }
 
-// TOK tokens a CTA of NT threads; a thread has IN units in flight.  QZ: into a quantised cache.
-template <typename T, int D, int TOK, int NT, int IN, bool QZ>
-__global__ void __launch_bounds__(NT, QZ && TOK > 1 ? 8 : 1) paged_append_kernel(const AppendArgs a) {
-    __shared__ __align__(16) float4 cs[TOK][D / 4];
-    __shared__ uint64_t turn_sm[D / 2];
-    __shared__ int64_t slot[TOK];      // element offset of (page, head 0, slot), -1: no slot, -2: skip the row
-    __shared__ int pos_sm[TOK];
-    constexpr int VN = 16 / sizeof(T), UH = D / (2 * VN);   // units per head
-    const int t0 = blockIdx.x * TOK, nt = min(TOK, a.n_tokens - t0);
+// Slots, positions and cosines of the CTA's tokens t0 .. t0 + nt - 1 (all threads).
+template <typename T, int D, int TOK, int NT>
+__device__ __forceinline__ void place_tokens(const AppendArgs& a, int t0, int nt, float4 (&cs)[TOK][D / 4], uint64_t (&turn_sm)[D / 2],
+                                             int64_t (&slot)[TOK], int (&pos_sm)[TOK], int rot) {
+    constexpr int VN = 16 / sizeof(T);
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
     const PagedArgs& p = a.p;
 
-    wait_for_last_kernel();
-    if constexpr (QZ) {
-        // (the rows are on their way while positions, pages and cosines are found)
-        constexpr int LN = D * sizeof(T) / 128;                              // 128-byte lines of a head
-        const int hq = a.Q.data ? p.Hq : 0, heads = hq + 2 * p.Hkv;
-        for (int e = threadIdx.x; e < nt * heads * LN; e += NT) {
-            const int l = e % LN, th = e / LN, i = th / heads, h = th - i * heads;
-            const bool q = h < hq, v = h >= hq + p.Hkv;
-            const Rows& r = q ? a.Q : v ? a.V : a.K;
-            const char* at = r.data + ((int64_t)(t0 + i) * r.row + (int64_t)(q ? h : h - hq - (v ? p.Hkv : 0)) * r.head) * (int)sizeof(T) + 128 * l;
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
-        }
-    }
     for (int i = warp; i < nt; i += NT / kWarp) {
         const int t = t0 + i;
         int b = t;
@@ -220,7 +203,6 @@ __global__ void __launch_bounds__(NT, QZ && TOK > 1 ? 8 : 1) paged_append_kernel
             pos_sm[i] = a.positions ? a.positions[t] : (int)pos;
         }
     }
-    const int rot = a.inv_freq ? a.rot : 0;
     // the turn of one position, by the last warps (the first ones look the tokens up)
     for (int f = NT - 1 - (int)threadIdx.x; f < rot / 2; f += NT) {
         double turns = (double)a.inv_freq[f] * 0.15915494309189535;    // w / 2 pi
@@ -245,7 +227,77 @@ __global__ void __launch_bounds__(NT, QZ && TOK > 1 ? 8 : 1) paged_append_kernel
         reinterpret_cast<float2*>(cs[i])[((f % VN / 2) * ru + f / VN) * 2 + (f & 1)] = make_float2(c, s);
     }
     __syncthreads();
-    const int hq = a.Q.data ? p.Hq : 0;
+}
+
+// TOK tokens a CTA of NT threads; a thread has IN units in flight.
+template <typename T, int D, int TOK, int NT, int IN>
+__global__ void __launch_bounds__(NT) paged_append_kernel(const AppendArgs a) {
+    __shared__ __align__(16) float4 cs[TOK][D / 4];
+    __shared__ uint64_t turn_sm[D / 2];
+    __shared__ int64_t slot[TOK];      // element offset of (page, head 0, slot), -1: no slot, -2: skip the row
+    __shared__ int pos_sm[TOK];
+    constexpr int VN = 16 / sizeof(T), UH = D / (2 * VN);   // units per head
+    const int t0 = blockIdx.x * TOK, nt = min(TOK, a.n_tokens - t0);
+    const PagedArgs& p = a.p;
+    wait_for_last_kernel();
+    const int rot = a.inv_freq ? a.rot : 0, ru = rot / (2 * VN);
+    place_tokens<T, D, TOK, NT>(a, t0, nt, cs, turn_sm, slot, pos_sm, rot);
+    const int hq = a.Q.data ? p.Hq : 0, heads = hq + 2 * p.Hkv, units = nt * heads * UH;
+    const bool nb = a.pairs == LOLA_PAIRS_NEIGHBOURS;
+    for (int e0 = threadIdx.x; e0 < units; e0 += NT * IN) {
+        Unit<T> n[IN];
+#pragma unroll
+        for (int x = 0; x < IN; ++x) {
+            const int e = e0 + x * NT;
+            n[x].dst = nullptr;
+            if (e >= units) continue;
+            const int u = e % UH, th = e / UH;
+            int i = 0;                           // th / heads
+#pragma unroll
+            for (int z = 1; z < TOK; ++z) i += th >= z * heads;
+            const int h = th - i * heads;
+            const int64_t t = t0 + i, s = slot[i];
+            if (s == -2 || (s < 0 && h >= hq)) continue;
+            if (h < hq) {
+                load_unit<T>(n[x], reinterpret_cast<const T*>(a.Q.data) + t * a.Q.row + h * a.Q.head,
+                             reinterpret_cast<T*>(a.QO.data) + t * a.QO.row + h * a.QO.head, u, rot, nb, cs[i]);
+            } else {
+                const bool v = h >= hq + p.Hkv;
+                const int hk = h - hq - (v ? p.Hkv : 0);
+                const Rows& r = v ? a.V : a.K;
+                load_unit<T>(n[x], reinterpret_cast<const T*>(r.data) + t * r.row + hk * r.head,
+                             reinterpret_cast<T*>(v ? p.V : p.K) + s + (int64_t)hk * p.page * D, u, v ? 0 : rot, nb, cs[i]);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < IN; ++x)
+            if (n[x].dst) finish_unit<T>(n[x], nb, ru);
+    }
+}
+
+// The same into a quantised cache.
+template <typename T, int D, int TOK, int NT, int IN>
+__global__ void __launch_bounds__(NT, TOK > 1 ? 8 : 1) quant_append_kernel(const AppendArgs a) {
+    __shared__ __align__(16) float4 cs[TOK][D / 4];
+    __shared__ uint64_t turn_sm[D / 2];
+    __shared__ int64_t slot[TOK];
+    __shared__ int pos_sm[TOK];
+    constexpr int VN = 16 / sizeof(T), UH = D / (2 * VN);   // units per head
+    const int t0 = blockIdx.x * TOK, nt = min(TOK, a.n_tokens - t0), lane = threadIdx.x % kWarp;
+    const PagedArgs& p = a.p;
+    wait_for_last_kernel();
+    const int hq = a.Q.data ? p.Hq : 0, rot = a.inv_freq ? a.rot : 0, ru = rot / (2 * VN);
+    // (the rows are on their way while positions, pages and cosines are found)
+    constexpr int LN = D * sizeof(T) / 128;                              // 128-byte lines of a head
+    const int heads = hq + 2 * p.Hkv;
+    for (int e = threadIdx.x; e < nt * heads * LN; e += NT) {
+        const int l = e % LN, th = e / LN, i = th / heads, h = th - i * heads;
+        const bool q = h < hq, v = h >= hq + p.Hkv;
+        const Rows& r = q ? a.Q : v ? a.V : a.K;
+        const char* at = r.data + ((int64_t)(t0 + i) * r.row + (int64_t)(q ? h : h - hq - (v ? p.Hkv : 0)) * r.head) * (int)sizeof(T) + 128 * l;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+    }
+    place_tokens<T, D, TOK, NT>(a, t0, nt, cs, turn_sm, slot, pos_sm, rot);
     const bool nb = a.pairs == LOLA_PAIRS_NEIGHBOURS;
     // heads h0 .. h0 + heads - 1 of the CTA's tokens (queries, keys, values, in this order); `some` of them are quantised
     auto copy = [&](int h0, int heads, auto some) {
@@ -275,9 +327,8 @@ __global__ void __launch_bounds__(NT, QZ && TOK > 1 ? 8 : 1) paged_append_kernel
                     const Rows& r = v ? a.V : a.K;
                     const int64_t at = s + (int64_t)hk * p.page * D;
                     load_unit<T>(n[x], reinterpret_cast<const T*>(r.data) + t * r.row + hk * r.head,
-                                 QZ ? reinterpret_cast<T*>((v ? p.V : p.K) + at) : reinterpret_cast<T*>(v ? p.V : p.K) + at, u, v ? 0 : rot,
-                                 nb, cs[i]);
-                    if (QZ) n[x].power = (v ? p.Vs : p.Ks) + at / D;
+                                 reinterpret_cast<T*>((v ? p.V : p.K) + at), u, v ? 0 : rot, nb, cs[i]);
+                    n[x].power = (v ? p.Vs : p.Ks) + at / D;
                 }
             }
 #pragma unroll
@@ -287,12 +338,12 @@ __global__ void __launch_bounds__(NT, QZ && TOK > 1 ? 8 : 1) paged_append_kernel
             }
         }
     };
-    if constexpr (QZ && TOK > 1) {
+    if constexpr (TOK > 1) {
         // (one behind the other: each loop's code and registers are its own)
         copy(0, hq, std::false_type{});
         copy(hq, 2 * p.Hkv, std::true_type{});
     } else {
-        copy(0, hq + 2 * p.Hkv, std::bool_constant<QZ>{});
+        copy(0, hq + 2 * p.Hkv, std::true_type{});
     }
 }
 
@@ -303,9 +354,13 @@ __global__ void __launch_bounds__(NT, QZ && TOK > 1 ? 8 : 1) paged_append_kernel
 // threads, three units each, 96 us, two units 81; one token by 128 threads 117).
 template <typename T, int D, bool QZ>
 cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
-    if (a.n_tokens <= kFew) return launch_behind(paged_append_kernel<T, D, 1, 128, 3, QZ>, (unsigned)a.n_tokens, 128, 0, st, a);
-    if (QZ) return launch_behind(paged_append_kernel<T, D, 2, 128, 2, QZ>, (unsigned)(a.n_tokens + 1) / 2, 128, 0, st, a);
-    return launch_behind(paged_append_kernel<T, D, 4, 256, 3, QZ>, (unsigned)(a.n_tokens + 3) / 4, 256, 0, st, a);
+    if constexpr (QZ) {
+        if (a.n_tokens <= kFew) return launch_behind(quant_append_kernel<T, D, 1, 128, 3>, (unsigned)a.n_tokens, 128, 0, st, a);
+        return launch_behind(quant_append_kernel<T, D, 2, 128, 2>, (unsigned)(a.n_tokens + 1) / 2, 128, 0, st, a);
+    } else {
+        if (a.n_tokens <= kFew) return launch_behind(paged_append_kernel<T, D, 1, 128, 3>, (unsigned)a.n_tokens, 128, 0, st, a);
+        return launch_behind(paged_append_kernel<T, D, 4, 256, 3>, (unsigned)(a.n_tokens + 3) / 4, 256, 0, st, a);
+    }
 }
 template <typename T>
 cudaError_t launch(const AppendArgs& a, cudaStream_t st) {
