@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_f32_kernel(const __g
         mbar_init(smem_u32(&bars.seg_full[0]), 1);
         mbar_init(smem_u32(&bars.seg_empty[0]), NW);
         abort_sm = 0;
-        bars.issued = bars.given = bars.arrived[0] = bars.arrived[1] = 0;
+        bars.issued = bars.ahead = bars.given = bars.arrived[0] = bars.arrived[1] = 0;
     }
     wait_for_last_kernel();
     Start st;
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_mma_kernel(const __g
             mbar_init(smem_u32(&bars.seg_empty[s]), NW);
         }
         abort_sm = 0;
-        bars.issued = bars.given = bars.arrived[0] = bars.arrived[1] = 0;
+        bars.issued = bars.ahead = bars.given = bars.arrived[0] = bars.arrived[1] = 0;
     }
     wait_for_last_kernel();
     Start st;

@@ -178,10 +178,10 @@ __device__ __forceinline__ bool issued_wait(const int* issued, int n, int* abort
     }
     return true;
 }
-// `turns` segments' groups have been added up in a buffer (the upper half of *joined)
-__device__ __forceinline__ bool joined_wait(const int* joined, int turns, int* abort_sm) {
+// *count has come to `want`
+__device__ __forceinline__ bool count_wait(const int* count, int want, int* abort_sm) {
     const uint64_t start = globaltimer_ns();
-    while ((*reinterpret_cast<const volatile int*>(joined) >> 16) < turns) {
+    while (*reinterpret_cast<const volatile int*>(count) < want) {
         if (*reinterpret_cast<volatile int*>(abort_sm)) return false;
         if (globaltimer_ns() - start > kWaitNs) {
             *abort_sm = 1;
@@ -213,6 +213,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 template <int S, int NS = 2> struct Bars {
     uint64_t full[S], empty[S], seg_full[NS], seg_empty[NS];
     int issued;      // tiles whose stage is armed
+    int ahead;       // tiles whose V codes' copies are on their way (e4m3: by a warp of their own, which may be ahead)
     int given;       // segment slots given to the consumers, when the producer is done
     int arrived[2];  // this piece's record of that slot has been counted
 };
@@ -364,6 +365,7 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
                 mbar_expect(smem_u32(&bars.full[s]), (uint32_t)(2 * (used - __popc(bad_mask)) * box * C::kRowBytes));
                 *reinterpret_cast<volatile int*>(&bars.issued) = n + 1;
             }
+            if (kParts && part == 1 && lane == 0) *reinterpret_cast<volatile int*>(&bars.ahead) = n + 1;
             __syncwarp();
             if constexpr (kParts) {
                 if (part == 2) {
@@ -404,7 +406,10 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
             tiles = tiles_of<C::kTokens>(tokens);
         }
     }
-    if (!first) return;
+    if (!first) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        return;
+    }
     // the consumers' end
     for (int e = 0; e < NS && ok; ++e, ++i) {
         const int slot = i % NS;
@@ -570,8 +575,9 @@ __device__ void join_pieces(const Args& a, const Seg& g, int t, int* go, int* ar
 template <int D, int S, int NS, bool SH, int NT = kThreads, int TILE = kTile, typename B>
 __device__ __noinline__ void settle(const Args& a, B& bars) {
     if (threadIdx.x == 0) {
-        const int n = bars.issued, i = bars.given;
-        // (of a tile's copies, those of a warp that met the end sooner are missing: then the others are waited for for long enough)
+        const int n = max(bars.issued, bars.ahead), i = bars.given;
+        // (of a tile's copies, those of a warp that met the end sooner are missing, or the tile is not armed: then the others are
+        // waited for for long enough)
         for (int x = max(0, n - S); x < n; ++x) mbar_wait(smem_u32(&bars.full[x % S]), (uint32_t)(x / S) & 1, kDrainNs);
         for (int x = max(0, i - NS); x < i; ++x) mbar_wait(smem_u32(&bars.seg_full[x % NS]), (uint32_t)(x / NS) & 1, kWaitNs);
     }

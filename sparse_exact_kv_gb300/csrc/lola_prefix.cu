@@ -680,6 +680,7 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
                 ++pairs;
             }
         }
+        cp_async_wait_all();                 // (the first Q rows, where a wait gave up before them)
     }
     fence_before();
     __syncthreads();

@@ -72,8 +72,9 @@ __global__ void __launch_bounds__(TSmem<T, TO, D, NB>::kAll * kWarp, 1) decode_t
     M& x = *reinterpret_cast<M*>(sm + C::kSmem - 1024);
     __shared__ __align__(8) Bars<C::kStages, NS> bars;
     __shared__ uint32_t bad_sm[C::kStages];
-    __shared__ int abort_sm, go[kGroups], joined[2];       // joined: the groups that are done with part[]; in the upper half: how
-    __shared__ Seg segs[NS];                               // many segments' groups have been added up there
+    __shared__ int abort_sm, go[kGroups];
+    __shared__ int here[2], joined[2];                     // groups whose parts are in part[]; segments that were added up there
+    __shared__ Seg segs[NS];
     const PagedArgs& p = a.p;
     const int tid = threadIdx.x, warp = tid / kWarp, lane = tid % kWarp;
     if (tid == 0) {
@@ -85,8 +86,8 @@ __global__ void __launch_bounds__(TSmem<T, TO, D, NB>::kAll * kWarp, 1) decode_t
             mbar_init(smem_u32(&bars.seg_full[s]), 1);
             mbar_init(smem_u32(&bars.seg_empty[s]), NW);
         }
-        abort_sm = joined[0] = joined[1] = 0;
-        bars.issued = bars.given = bars.arrived[0] = bars.arrived[1] = 0;
+        abort_sm = here[0] = here[1] = joined[0] = joined[1] = 0;
+        bars.issued = bars.ahead = bars.given = bars.arrived[0] = bars.arrived[1] = 0;
     }
     wait_for_last_kernel();
     Start st;
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(TSmem<T, TO, D, NB>::kAll * kWarp, 1) decode_t
         }
         // ---- the group's end: its warps in order ----
         const int buf = turn & 1;
-        if (groups > 1 && ok) ok = joined_wait(&joined[buf], turn >> 1, &abort_sm);    // (the parts before are read)
+        if (groups > 1 && ok) ok = count_wait(&joined[buf], turn >> 1, &abort_sm);    // (the parts before are read)
         if (group_or<NT>(1 + grp, !ok)) {
             if (gt == 0) atomicOr(&g_status, (int)LOLA_ATTN_TIMEOUT);
             break;
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(TSmem<T, TO, D, NB>::kAll * kWarp, 1) decode_t
             }
             __threadfence_block();
             bar();
-            if (gt == 0) go[grp] = (atomicAdd(&joined[buf], 1) & 0xffff) == groups - 1;
+            if (gt == 0) go[grp] = atomicAdd(&here[buf], 1) == groups - 1;
             bar();
             if (!go[grp]) continue;
             __threadfence_block();
@@ -447,8 +448,9 @@ __global__ void __launch_bounds__(TSmem<T, TO, D, NB>::kAll * kWarp, 1) decode_t
             }
             bar();
             if (gt == 0) {
+                here[buf] = 0;
                 __threadfence_block();
-                atomicAdd(&joined[buf], 0x10000 - groups);                     // (one more segment, no group of the next one yet)
+                *reinterpret_cast<volatile int*>(&joined[buf]) = (turn >> 1) + 1;
             }
         }
         if (!SH && !g.whole) join_pieces<TO, D, NT>(a, g, gt, &go[grp], bars.arrived, bar);

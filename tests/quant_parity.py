@@ -3,8 +3,10 @@
 A row x becomes e4m3 codes of x 2^-e, 2^e the smallest power with max |x| <= 448 2^e in [2^-100, 2^119]; e4m3 numbers are
 2^-9 apart below 2^-6 and round by at most 2^-4 of themselves above, so that |code 2^e - x| <= max(2^-4 |x|, 2^(e - 10)).
 Attention over codes: as attn_parity's bounds, over the numbers that the codes stand for, which enter the products
-exactly.  Two terms more: q is kept to 2^-39 of its row's largest number (|ds| <= c 2^-38 max|q| sum |k|), and a weight
-that is small against its row's largest one, to 2^-33 of that: 2^-31 (keys + 8) of the largest column's sum of p |v|."""
+exactly.  Three terms more: q is kept to 2^-39 of its row's largest number (|ds| <= c 2^-38 max|q| sum |k|); behind a shared
+prefix, keys and values are kept to half of 2^-24 of their block's largest power, which is at most 1 / 224 of its largest
+number (|ds| <= c 2^-32 max|k| sum |q|, and 2^-32 max|v| in o); and a weight that is small against its row's largest one,
+to 2^-33 of that: 2^-31 (keys + 8) of the largest column's sum of p |v|, which has room for the values' term too."""
 import math
 
 import torch
@@ -79,7 +81,8 @@ def check_attention(q, parts, out, lse=None, scale=None, what=""):
         g = h * k.shape[1] // Hq
         o, ls, to, tl = attend(q[h][None], k[:, g], v[:, g], ~hidden[None], scale)
         fk, fv = (torch.nan_to_num(x[~hidden][:, g]) for x in (k, v))
-        ds = c * 2.0 ** -38 * float(q[h].abs().max()) * float(fk.abs().sum(-1).max()) if n else 0.0
+        fq = torch.nan_to_num(q[h].double()).abs()
+        ds = c * (2.0 ** -38 * float(fq.max() * fk.abs().sum(-1).max()) + 2.0 ** -32 * float(fq.sum() * fk.abs().max())) if n else 0.0
         A = fv.abs().amax() if n else 0.0
         check(out[h][None], o, to + (2 * ds + 2.0 ** -31 * (n + 8)) * A, f"{what} head {h}")
         if lse is not None:

@@ -557,6 +557,72 @@ def test_shared_strides_streams_and_graphs(L, gen, dtype, quant):
             s.check(qs, o)
 
 
+@pytest.mark.parametrize("dtype,quant,d", [(BF, True, 128), (BF, True, 64), (F32, True, 128)])
+@pytest.mark.parametrize("up", [-60, -20, 15, 60])
+def test_shared_powers_of_many_sizes(L, gen, dtype, quant, d, up):
+    """Keys and values of magnitudes far from one, of many different ones in a block, and queries that make up for it."""
+    s = Shared(gen, quant, [700], [5], [40, 3, 0, 130, 17], 1, d, 32, dtype)
+    c = s.c
+    for b, n in enumerate(c.lens):
+        pos = torch.arange(n, device="cuda")
+        f, g = (2.0 ** torch.randint(-m, m, (n, 1, 1), generator=gen, device="cuda").double() for m in (3, 12))
+        c.k[b] = c.store("k", b, pos, (c.k[b] * f * 2.0 ** -up).float())
+        c.v[b] = c.store("v", b, pos, (c.v[b] * g * 2.0 ** up).float())
+    q = (0.3 * randn(gen, 5, 3, d, dtype=F32) * 2.0 ** up).to(dtype)
+    lse = torch.empty(5, 3, dtype=F32, device="cuda")
+    out = s.layer(L, 3, 1, d, dtype).decode_shared(q, s.kv_len, s.table, s.prefix_len, s.prefix_table, lse=lse)
+    quiet(L)
+    s.check(q, out, lse)
+
+
+@pytest.mark.parametrize("dtype,quant", [(BF, False), (BF, True), (F32, False), (F32, True)])
+@pytest.mark.parametrize("what", ["step", "shared"])
+@pytest.mark.parametrize("prefix,lens", [(6000, [4000, 100, 1, 2500]), (40000, [7] * 30), (130, [200] * 400)], ids=["few", "long", "many"])
+def test_calls_after_waits_that_gave_up(L, gen, dtype, quant, what, prefix, lens):
+    """A call whose waits gave up says so, ends, and leaves nothing behind: neither in a replay of a captured call nor
+    in the next call in its workspace."""
+    if what == "step" and not quant:
+        pytest.skip("the plain cache's own test")
+    s = Shared(gen, quant, [prefix], [len(lens)], lens, 1, 128, 64, dtype)
+    lay = s.layer(L, 4, 1, 128, dtype)
+    q = randn(gen, len(lens), 4, 128, dtype=dtype)
+    out = torch.zeros_like(q)
+    size = L.lola_shared_decode_workspace_bytes(lay.cfg, len(lens)) if what == "shared" else L.lola_paged_decode_workspace_bytes(lay.cfg)
+    ws = torch.randint(0, 255, (size,), dtype=torch.uint8, device="cuda", generator=gen)
+
+    def call():
+        if what == "shared":
+            lay.decode_shared(q, s.kv_len, s.table, s.prefix_len, s.prefix_table, out=out, workspace=ws)
+        else:
+            lay.decode_step(q, s.kv_len, s.table, out=out, workspace=ws)
+
+    call()
+    quiet(L)
+    want, gave_up = out.clone(), 0
+    try:
+        for block in (0, 1, 2, 3, 5, 8, 1000):
+            L.lola_selftest_attn_wait(block)
+            g = torch.cuda.CUDAGraph()
+            torch.cuda.synchronize()
+            with torch.cuda.graph(g):
+                call()
+            for _ in range(2):
+                out.fill_(7.0)
+                g.replay()
+                st, bits = L.lola_attn_status()
+                assert bits in (0, L.LOLA_ATTN_TIMEOUT)
+                gave_up += bits != 0
+                assert bits or torch.equal(out, want), block
+            L.lola_selftest_attn_wait(-1)
+            out.fill_(7.0)
+            call()
+            quiet(L)
+            assert torch.equal(out, want), block
+    finally:
+        L.lola_selftest_attn_wait(-1)
+    assert gave_up > 0
+
+
 # ---------------------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------------------
@@ -623,3 +689,59 @@ def test_two_calls_at_once_do_not_share(L, gen):
     for i in range(2):
         for a, b in got[i]:
             assert torch.equal(a, want[i][0]) and torch.equal(b, want[i][1])
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+def test_both_forms_of_the_binding_give_the_same_bits(L, dtype, d, monkeypatch):
+    """The calls through the marshalling module, and their Python form, which serves without it."""
+    def run():
+        g = torch.Generator(device="cuda").manual_seed(3)
+        s = Shared(g, True, [90, 40], [2, 1], [70, 300, 1], 2, d, 16, dtype)
+        lay = s.layer(L, 4, 2, d, dtype)
+        n = 371
+        rows, cu = randn(g, n, 8, d, dtype=dtype), offsets(s.lens)
+        q, k, v = rows[:, :4], rows[:, 4:6], rows[:, 6:]
+        inv = torch.rand(d // 2, generator=g, device="cuda")
+        qr = lay.append(k, v, s.kv_len, s.table, cu_new=cu, q=q, inv_freq=inv, pairs="neighbours")
+        assert lay.append(k[:3], v[:3], s.kv_len, s.table) is None
+        out = [qr, *lay.read(s.kv_len, s.table, n), lay.prefill_paged(qr, cu, s.kv_len, s.table, n), lay.decode_step(q[:3], s.kv_len, s.table),
+               lay.decode_shared(q[:3], s.kv_len, s.table, s.prefix_len, s.prefix_table, s.cu)]
+        io = Shared(g, False, [90, 40], [2, 1], [70, 300, 1], 2, d, 16, dtype)
+        out.append(io.layer(L, 4, 2, d, dtype).decode_shared(q[:3], io.kv_len, io.table, io.prefix_len, io.prefix_table, io.cu))
+        return out + [x.view(torch.uint8) for x in (lay.k_pool, lay.v_pool, lay.k_scale, lay.v_scale)]
+
+    fast = run()
+    assert L._fast is not L._Declines
+    monkeypatch.setattr(L, "_fast", L._Declines)
+    with pytest.warns(RuntimeWarning):
+        slow = run()
+    quiet(L)
+    assert all(torch.equal(a, b) for a, b in zip(fast, slow)) and len(fast) == len(slow)
+
+
+def test_refused_calls_say_what_is_wrong(L, gen):
+    """Arguments that do not fit are refused by both forms, with nothing enqueued."""
+    s = Shared(gen, True, [90, 40], [2, 1], [70, 30, 1], 2, 64, 16, BF)
+    lay = s.layer(L, 4, 2, 64, BF)
+    q, k = randn(gen, 3, 4, 64, dtype=BF), randn(gen, 3, 2, 64, dtype=BF)
+    bad = [lambda: lay.decode_step(q[:2], s.kv_len, s.table), lambda: lay.decode_step(q.float(), s.kv_len, s.table),
+           lambda: lay.decode_step(q, s.kv_len.long(), s.table), lambda: lay.decode_step(q, s.kv_len, s.table[:, ::2]),
+           lambda: lay.append(k, k.float(), s.kv_len, s.table), lambda: lay.append(k, k, s.kv_len, s.table, q=q[:, :3]),
+           lambda: lay.read(s.kv_len[:2], s.table, 5), lambda: lay.read(s.kv_len, s.table.cpu(), 5), lambda: lay.read(s.kv_len, s.table, -1),
+           lambda: lay.prefill_paged(q, offsets([1, 1, 1]), s.kv_len, s.table),
+           lambda: lay.decode_shared(q, s.kv_len, s.table, s.prefix_len, s.prefix_table),
+           lambda: lay.decode_shared(q, s.kv_len, s.table, s.prefix_len[:1], s.prefix_table, s.cu),
+           lambda: lay.decode_shared(q, s.kv_len, s.table, s.prefix_len, s.prefix_table, s.cu[:2]),
+           lambda: lay.decode_shared(q, s.kv_len, s.table, s.prefix_len, s.prefix_table.cpu(), s.cu),
+           lambda: lay.decode_shared(q, s.kv_len, s.table, s.prefix_len, s.prefix_table, s.cu, workspace=torch.empty(0, dtype=torch.uint8)),
+           lambda: L.ExactAttention(4, 2, 64, BF, lay.k_pool, lay.v_pool)]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
+    for f in (lambda: lay.append(k, k, s.kv_len, s.table, q=q),                      # queries without a rotation
+              lambda: lay.decode_shared(q, s.kv_len, s.table, s.prefix_len, s.prefix_table[:1].expand(2, -1), s.cu),
+              lambda: lay.decode_shared(q, s.kv_len, s.table, s.prefix_len, s.prefix_table, s.cu,
+                                        workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(L.LolaError):
+            f()
+    quiet(L)
