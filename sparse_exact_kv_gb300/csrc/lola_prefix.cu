@@ -45,11 +45,14 @@ template <int D, bool QZ> struct PCfg {
     static constexpr int kRawBytes = QZ ? kN * D + 2 * kN : 0;         // codes, their powers, behind keys the values' powers too
     static constexpr int kSmem = (2 + kRing) * kTileBytes + kRaw * kRawBytes + 1024;
     // Registers of a softmax thread and of the others: what the block was launched with, 168 or 128 a thread, given out
-    // anew, so that a row's 128 scores fit.  QZ at d = 128 is bound by the conversion, whose warps need theirs (128
-    // sequences behind 131072 tokens: 300 us, 334 with 192 and 64), and reads half of the scores twice; at d = 64 the
-    // scores come first (64 behind 64000 tokens, 32/8 heads: 60 us, 68 the other way).
+    // anew, so that a row's 128 scores fit.  QZ at d = 64: the scores come first here too (64 sequences behind 64000 tokens,
+    // 32/8 heads: 60 us, 68 with 128 and 128).
     static constexpr int kSoftmaxRegs = QZ ? (D == 128 ? 128 : 192) : 208, kOtherRegs = QZ ? (D == 128 ? 128 : 64) : 88;
-    static constexpr int kHeld = QZ && D == 128 ? 64 : kN;             // scores in registers
+    // Scores in registers.  QZ at d = 128 is bound by the conversion, whose warps need their 128 registers and the schedulers'
+    // time: the softmax goes over S twice there, 32 columns at a time (128 sequences behind 131072 tokens, 32/8 heads: 256 us;
+    // half of the scores held 300, all of them, with 192 and 64 registers, 334; eight converting warps 276).  Elsewhere S is
+    // read once (bfloat16, the same size: 198 us, 221 in the loop; QZ, d = 64, 24/4 heads: 162 and 171).
+    static constexpr int kHeld = QZ && D == 128 ? 32 : kN;
     __device__ static constexpr uint32_t TS(int i) { return 128u * i; }  // S (P over its first half)
     __device__ static constexpr uint32_t TO(int i) { return 256u + (uint32_t)D * i; }
 };
@@ -494,7 +497,6 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
                 const int j = two ? jj : 2 * jj + i;
                 if (!(ok = wait_all(B_S + i, (uint32_t)(ns + jj)))) break;
                 fence_after();
-                // (QZ, d = 128: columns 64 .. 127 are read twice, as 128 registers a thread do not hold all)
                 constexpr int kHeld = C::kHeld;
                 float s[kHeld];
                 const int valid = g.len - j * kN;
@@ -512,7 +514,7 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
                     for (int x = 0; x < 32; ++x) s[at + x] = (seen >> x) & 1u ? s[at + x] : -INFINITY;
                 };
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
+#pragma unroll 1
                 for (int x0 = kN - kHeld; x0 >= 0; x0 -= kHeld) {
 #pragma unroll
                     for (int x = 0; x < kHeld; x += 32) tmem_ld32(ts + x0 + x, s + x);
@@ -577,21 +579,15 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
                     tmem_st16(ts + x / 2, pw);
                 };
                 if constexpr (kHeld < kN) {
-                    // (a place's next columns are under way while the other's are weighed)
-                    auto arrived = [&](int at, int x) {
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int y = 0; y < 32; ++y) asm volatile("" : "+f"(s[at + y]));
-                        hide(at, x);
-                    };
-                    weigh(0, 0);
-                    tmem_ld32(ts + 64, s);
-                    weigh(32, 32);
-                    arrived(0, 64);
-                    tmem_ld32(ts + 96, s + 32);
-                    weigh(0, 64);
-                    arrived(32, 96);
-                    weigh(32, 96);
+#pragma unroll 1
+                    for (int x = 0; x < kN; x += 32) {
+                        weigh(0, x);
+                        if (x + 32 < kN) {
+                            tmem_ld32(ts + x + 32, s);
+                            tmem_wait_ld();
+                            hide(0, x + 32);
+                        }
+                    }
                 } else {
 #pragma unroll
                     for (int x = 0; x < kN; x += 32) weigh(x, x);
