@@ -558,34 +558,47 @@ __global__ void __launch_bounds__(kReadThreads) quant_read_kernel(const ReadArgs
     }
     if (bits) atomicOr(&g_status, bits);
     __syncthreads();
-    constexpr int NU = 8;
-    const int units = kReadRows * p.Hkv * UH;
-    for (int kv = 0; kv < 2; ++kv) {
-        const uint8_t* pool = reinterpret_cast<const uint8_t*>(kv ? p.V : p.K);
-        const uint8_t* powers = kv ? p.Vs : p.Ks;
-        const Rows& out = kv ? a.V : a.K;
-        for (int e0 = threadIdx.x; e0 < units; e0 += NU * kReadThreads) {
-            // (loads without conditions, from the pool's first row where there is nothing to read: all are under way at once)
-            typename ReadUnit<T>::Codes w[NU];
-            uint8_t power[NU];
-            T* dst[NU];
-            uint32_t zero = 0u;
+    // K and V of NU units a thread are under way at once.  Unit e is part w of row i; from unit to unit the next one is
+    // found without a division.
+    constexpr int NU = 4;
+    const int per = p.Hkv * UH, step_i = kReadThreads / per, step_w = kReadThreads - step_i * per;
+    int i = (int)threadIdx.x / per, w = (int)threadIdx.x - i * per;
+    while (i < kReadRows) {
+        // (loads without conditions, from the pool's first row where there is nothing to read)
+        typename ReadUnit<T>::Codes c[2][NU];
+        uint8_t power[2][NU];
+        int row_of[NU], part_of[NU];
+        uint32_t zero = 0u, none = 0u;
 #pragma unroll
-            for (int x = 0; x < NU; ++x) {
-                const int e = min(e0 + x * kReadThreads, units - 1), u = e % UH, rh = e / UH, i = rh / p.Hkv, h = rh - i * p.Hkv;
-                const int64_t at = from[i], row = at < 0 ? 0 : at + (int64_t)h * p.page;
-                w[x] = *reinterpret_cast<const typename ReadUnit<T>::Codes*>(pool + row * D + u * VN);
-                power[x] = powers[row];
-                if (at < 0) zero |= 1u << x;
-                const bool none = e0 + x * kReadThreads >= units || at == -2;
-                dst[x] = none ? nullptr : reinterpret_cast<T*>(out.data) + (r0 + i) * out.row + (int64_t)h * out.head + u * VN;
+        for (int x = 0; x < NU; ++x) {
+            const int64_t at = i < kReadRows ? from[i] : -2;
+            const int64_t row = at < 0 ? 0 : at + (int64_t)(w / UH) * p.page;
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                c[kv][x] = *reinterpret_cast<const typename ReadUnit<T>::Codes*>((kv ? p.V : p.K) + row * D + w % UH * VN);
+                power[kv][x] = (kv ? p.Vs : p.Ks)[row];
             }
-#pragma unroll
-            for (int x = 0; x < NU; ++x) {
-                const uint4 y = ReadUnit<T>::of(w[x], __uint_as_float((uint32_t)power[x] << 23));
-                if (dst[x]) *reinterpret_cast<uint4*>(dst[x]) = (zero >> x) & 1u ? make_uint4(0, 0, 0, 0) : y;
+            if (at < 0) zero |= 1u << x;
+            if (at == -2) none |= 1u << x;
+            row_of[x] = i;
+            part_of[x] = w;
+            i += step_i;
+            w += step_w;
+            if (w >= per) {
+                w -= per;
+                ++i;
             }
         }
+#pragma unroll
+        for (int x = 0; x < NU; ++x)
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                const Rows& out = kv ? a.V : a.K;
+                const uint4 y = ReadUnit<T>::of(c[kv][x], __uint_as_float((uint32_t)power[kv][x] << 23));
+                if (!((none >> x) & 1u))
+                    *reinterpret_cast<uint4*>(reinterpret_cast<T*>(out.data) + (r0 + row_of[x]) * out.row + (int64_t)(part_of[x] / UH) * out.head +
+                                              part_of[x] % UH * VN) = (zero >> x) & 1u ? make_uint4(0, 0, 0, 0) : y;
+            }
     }
 }
 template <typename T, int D> cudaError_t launch_read(const ReadArgs& a, cudaStream_t st) {
