@@ -75,9 +75,10 @@ __global__ void __launch_bounds__(256, 4) shared_join_kernel(const JoinArgs a) {
     __shared__ float4 y_sm[kWarps][N][kWarp];
     __shared__ float2 ml_sm[kWarps][2];
     const int w = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, own = lane >> 1;
-    const int64_t rows = (int64_t)a.p.n_seq * a.p.Hq, i0 = (int64_t)blockIdx.x * 2, i = i0 + (lane & 1);
+    // (2^28 rows at most)
+    const int rows = a.p.n_seq * a.p.Hq, i0 = (int)blockIdx.x * 2, i = i0 + (lane & 1);
+    const int b0 = i0 / a.p.Hq, b1 = i0 + 1 < rows && i0 + 1 == (b0 + 1) * a.p.Hq ? b0 + 1 : b0, b = lane & 1 ? b1 : b0;
     wait_for_last_kernel();
-    const int b0 = (int)(min(i0, rows - 1) / a.p.Hq), b1 = (int)(min(i0 + 1, rows - 1) / a.p.Hq), b = lane & 1 ? b1 : b0;
     int4 at_a = make_int4(0, 0, 0, 0), at_b = at_a;
     if (i < rows) {
         at_a = __ldcg(a.a.desc + i);
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(256, 4) shared_join_kernel(const JoinArgs a) {
     }
     // (no token seen: o = 0; scores that are all minus infinity: 0 / 0)
     const float inv = L == 0.f ? (sees_token(a.p, b) || (g >= 0 && sees_token(a.prefix, g)) ? NAN : 0.f) : 1.f / L;
-    const int h = (int)(i - (int64_t)b * a.p.Hq);
+    const int h = i - b * a.p.Hq;
     T* o = reinterpret_cast<T*>(a.O.data) + (int64_t)b * a.O.row + (int64_t)h * a.O.head;
 #pragma unroll
     for (int x = 0; x < N; ++x) {
