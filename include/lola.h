@@ -576,9 +576,9 @@ int32_t lola_selftest_bounded_wait(int64_t limit_ns, int64_t* host_elapsed_ns, v
 
 /* For tests: in the calls of lola_paged_decode, lola_quant_decode, lola_shared_decode and of the bfloat16 prompt attention
  * that follow in this process, every third CTA gives up at its block of keys number `block` (64 or 128 tokens, counted over
- * all that the CTA does, from 0) as if a wait there had reached its limit; -1: none does.  Such a call sets LOLA_ATTN_TIMEOUT and its outputs
- * are not valid, but it leaves its workspace as any other call, so that a replay of a captured call is right whatever
- * the one before met.  A captured call keeps what was set.  LOLA_ERR_INVALID_ARG for a block below -1. */
+ * all that the CTA does, from 0) as if a wait there had reached its limit; -1: none does.  Such a call sets
+ * LOLA_ATTN_TIMEOUT and its outputs are not valid, but it leaves its workspace as any other call, so that a replay of a
+ * captured call is right whatever the one before met.  A captured call keeps what was set.  LOLA_ERR_INVALID_ARG for a block below -1. */
 int32_t lola_selftest_attn_wait(int32_t block);
 
 #ifdef __cplusplus

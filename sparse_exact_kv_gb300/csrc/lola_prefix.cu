@@ -21,6 +21,12 @@
 // (Blocks of bfloat16 numbers code 2^e, by shifts, two products a pair and a look for NaN, took the four warps 3.4 us for
 // K and V.)
 // m is raised lazily, as in lola_attn_tc.cu: it is set 8 above a maximum, so that no weight is above one.
+// Long prefixes: bfloat16, 128 sequences behind 131072 tokens, 32/8 heads, d = 128, 198 us, 1390 TFLOP/s, bound by the way from
+// scores to weights beside the products; a quantised cache 256 us, 1070 TFLOP/s, bound by the conversion beside that (a block
+// of K or V takes its four warps 560 clocks alone, 1300 there).  Short ones by their start: 64 sequences behind 16001
+// tokens take 33 us, of which lookups, TMEM and the first block are 6 and the first pass through the softmax's code, which
+// comes into the instruction caches meanwhile, another 5 (a pass over an empty block ahead of the first one, less code, and
+// fewer loads at the start were each built and measured: no gain).
 // Every wait is bounded (1 s, then LOLA_ATTN_TIMEOUT).
 #include "lola_attn_mma.cuh"
 #include "lola_codes.cuh"
@@ -32,7 +38,7 @@ namespace {
 constexpr int kM = 128;                  // rows of a tile
 constexpr int kN = 128;                  // keys of a block
 constexpr int kItem = kPrefixRows;       // rows of an item: two tiles
-static_assert(kItem == 2 * kM, "");
+static_assert(kItem == 2 * kM, "two tiles");
 constexpr int kBad = 8;                  // blocks whose pages and powers are remembered: more than the loader is ahead
 constexpr float kWeightBits = 15.f;      // QZ: weights are kept times kUp
 
@@ -375,7 +381,7 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
             }
             __syncwarp();
         } else if (QZ && warp >= C::kConvWarp) {
-            // ================================ codes to bfloat16 ================================
+            // ================================ codes to float16 ================================
             const int t = tid & 127;
             for (int n = 0;; ++n) {
                 const int r = n % kRaw, s = n % kRing;

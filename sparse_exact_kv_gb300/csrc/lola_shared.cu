@@ -6,7 +6,7 @@
 //   m = max_k m_k,  l = sum_k 2^{m_k - m} l_k,  o = sum_k 2^{m_k - m} z_k / l,
 // the prefix' parts first, in the order of the pieces: the same inputs give the same bits.
 // Bound by its chain of accesses (which parts, the parts): two rows a CTA, their parts dealt out to eight warps,
-// which have three of them in flight each.  (When the kernel over the own tokens read the prefix' parts itself, row
+// which have three of them in flight each (64 sequences behind 16001 tokens, 32 heads, 19 prefix parts a row: 10 us).  (When the kernel over the own tokens read the prefix' parts itself, row
 // after row, 64 sequences behind 16001 tokens took it 92 us, 8 heads, d = 128.)
 #include "lola_paged.cuh"
 
