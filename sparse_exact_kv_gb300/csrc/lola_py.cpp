@@ -9,8 +9,9 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty_like.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -30,6 +31,14 @@ const Tensor* get(PyObject* o, at::ScalarType dtype, int device) {
     if (!t.defined() || t.layout() != at::kStrided || !t.is_cuda() || t.get_device() != device || t.scalar_type() != dtype) return nullptr;
     return &t;
 }
+
+// New memory of torch's, without its dispatch of operators (which takes as long as the allocation): a tensor, one like q,
+// and a workspace on the current device and stream.
+Tensor empty(at::IntArrayRef size, at::ScalarType dtype, int device) {
+    return at::detail::empty_cuda(size, dtype, at::Device(at::kCUDA, (c10::DeviceIndex)device), std::nullopt);
+}
+Tensor like(const Tensor& q) { return q.is_contiguous() ? empty(q.sizes(), q.scalar_type(), q.get_device()) : at::empty_like(q); }
+at::DataPtr scratch(int64_t bytes) { return c10::cuda::CUDACachingAllocator::get()->allocate((size_t)bytes); }
 
 // a contiguous vector of n entries (n < 0: any number)
 const Tensor* vec(PyObject* o, at::ScalarType dtype, int device, int64_t n) {
@@ -139,7 +148,7 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (!q || !k || !rows(a[3], &rv, *c, k->size(0), c->cfg->Hkv)) return decline();
         const Tensor *cq = vec(a[4], at::kInt, c->device, -1), *ck = nullptr;
         if (!cq || (a[5] != Py_None && !(ck = vec(a[5], at::kInt, c->device, cq->size(0))))) return decline();
-        Tensor out = at::empty_like(*q);
+        Tensor out = like(*q);
         if (!fill(out, &ro, q->size(0), c->cfg->Hq, c->cfg->d)) return decline();
         int32_t s;
         Py_BEGIN_ALLOW_THREADS
@@ -160,7 +169,7 @@ PyObject* prefill_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
         lola_rows rq, ro;
         const Tensor *q = rows(a[3], &rq, *c, -1, c->cfg->Hq), *cq = vec(a[4], at::kInt, c->device, (int64_t)kv.n_seq + 1);
         if (!q || !cq || total_k < 0 || total_k > INT32_MAX) return decline();
-        Tensor out = at::empty_like(*q);
+        Tensor out = like(*q);
         if (!fill(out, &ro, q->size(0), c->cfg->Hq, c->cfg->d)) return decline();
         int32_t s;
         Py_BEGIN_ALLOW_THREADS
@@ -180,13 +189,13 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
         lola_rows rq, ro;
         const Tensor* q = rows(a[3], &rq, *c, kv.n_seq, c->cfg->Hq);
         if (!q) return decline();
-        Tensor out = at::empty_like(*q);
+        Tensor out = like(*q);
         if (!fill(out, &ro, q->size(0), c->cfg->Hq, c->cfg->d)) return decline();
         // the workspace, released to torch behind the call
-        const Tensor ws = at::empty({c->ws}, q->options().dtype(at::kByte));
+        const at::DataPtr ws = scratch(c->ws);
         int32_t s;
         Py_BEGIN_ALLOW_THREADS
-        s = lola_paged_decode(c->cfg, &kv, &rq, &ro, nullptr, ws.data_ptr(), (size_t)c->ws, c->stream.stream());
+        s = lola_paged_decode(c->cfg, &kv, &rq, &ro, nullptr, ws.get(), (size_t)c->ws, c->stream.stream());
         Py_END_ALLOW_THREADS
         return s == LOLA_OK ? THPVariable_Wrap(std::move(out)) : decline();
     });
@@ -216,12 +225,12 @@ PyObject* quant_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
         lola_rows rq, ro;
         const Tensor* q = rows(a[5], &rq, *c, kv.n_seq, c->cfg->Hq);
         if (!q) return decline();
-        Tensor out = at::empty_like(*q);
+        Tensor out = like(*q);
         if (!fill(out, &ro, q->size(0), c->cfg->Hq, c->cfg->d)) return decline();
-        const Tensor ws = at::empty({c->ws}, q->options().dtype(at::kByte));
+        const at::DataPtr ws = scratch(c->ws);
         int32_t s;
         Py_BEGIN_ALLOW_THREADS
-        s = lola_quant_decode(c->cfg, &kv, &sc, &rq, &ro, nullptr, ws.data_ptr(), (size_t)c->ws, c->stream.stream());
+        s = lola_quant_decode(c->cfg, &kv, &sc, &rq, &ro, nullptr, ws.get(), (size_t)c->ws, c->stream.stream());
         Py_END_ALLOW_THREADS
         return s == LOLA_OK ? THPVariable_Wrap(std::move(out)) : decline();
     });
@@ -247,12 +256,12 @@ PyObject* shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (!q) return decline();
         const int64_t size = lola_shared_decode_workspace_bytes(c->cfg, kv.n_seq);
         if (size < 0) return decline();
-        Tensor out = at::empty_like(*q);
+        Tensor out = like(*q);
         if (!fill(out, &ro, q->size(0), c->cfg->Hq, c->cfg->d)) return decline();
-        const Tensor ws = at::empty({size}, q->options().dtype(at::kByte));
+        const at::DataPtr ws = scratch(size);
         int32_t s;
         Py_BEGIN_ALLOW_THREADS
-        s = lola_shared_decode(c->cfg, &kv, quant ? &sc : nullptr, &px, &rq, &ro, nullptr, ws.data_ptr(), (size_t)size, c->stream.stream());
+        s = lola_shared_decode(c->cfg, &kv, quant ? &sc : nullptr, &px, &rq, &ro, nullptr, ws.get(), (size_t)size, c->stream.stream());
         Py_END_ALLOW_THREADS
         return s == LOLA_OK ? THPVariable_Wrap(std::move(out)) : decline();
     });
@@ -267,9 +276,8 @@ PyObject* quant_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (!c || !cache(a[1], a[2], a[3], a[4], a[5], a[6], *c, &kv, &sc)) return decline();
         const long long total = PyLong_Check(a[7]) ? PyLong_AsLongLong(a[7]) : -1;
         if (total < 0 || total > INT32_MAX) return decline();
-        const auto options = THPVariable_Unpack(a[1]).options();
-        Tensor k = at::empty({total, c->cfg->Hkv, c->cfg->d}, options.dtype(c->dtype)), v = at::empty_like(k);
-        Tensor cu = at::empty({(int64_t)kv.n_seq + 1}, options.dtype(at::kInt));
+        Tensor k = empty({total, c->cfg->Hkv, c->cfg->d}, c->dtype, c->device), v = empty(k.sizes(), c->dtype, c->device);
+        Tensor cu = empty({(int64_t)kv.n_seq + 1}, at::kInt, c->device);
         lola_rows rk, rv;
         if (!fill(k, &rk, total, c->cfg->Hkv, c->cfg->d) || !fill(v, &rv, total, c->cfg->Hkv, c->cfg->d)) return decline();
         int32_t s;
@@ -311,7 +319,7 @@ template <bool QZ> PyObject* append_to(PyObject* const* a, Py_ssize_t n) {
             return decline();
         Tensor out;
         if (q) {
-            out = at::empty_like(*q);
+            out = like(*q);
             if (!fill(out, &ro, q->size(0), c->cfg->Hq, c->cfg->d)) return decline();
         }
         int32_t s;
