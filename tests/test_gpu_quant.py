@@ -141,6 +141,52 @@ def test_append_padded_batches_and_bad_pages(L, gen):
     assert torch.equal(before[1], c.v_pool.view(torch.uint8))
 
 
+@pytest.mark.parametrize("dtype,d,Hq,Hkv", [(BF, 128, 6, 3), (BF, 64, 12, 1), (F32, 128, 3, 3), (F32, 64, 9, 1)])
+def test_append_many_rows_padded_bad_pages_and_numbers_that_are_not_finite(L, gen, dtype, d, Hq, Hkv):
+    """As above, in calls of more tokens than a CTA each is given."""
+    page, n, cu = 16, 1003, [2, 700, 700, 990]
+    c = QPaged(gen, [750, 5, 290], Hkv, d, page, dtype)
+    lay = c.layer(L, Hq, Hkv, d, dtype)
+    q, k, v = (randn(gen, n, h, d, dtype=dtype) for h in (Hq, Hkv, Hkv))
+    k *= torch.exp2(torch.randint(-90, 90, (n, Hkv, 1), generator=gen, device="cuda").float()).to(dtype)
+    k[torch.rand(k.shape, generator=gen, device="cuda") < 0.01] = math.nan
+    v[torch.rand(v.shape, generator=gen, device="cuda") < 0.01] = -math.inf
+    table = c.table.clone()
+    table[0, 30], table[2, 0] = c.n_pages, -5                # positions 480 .. 495 of sequence 0, 0 .. 15 of 2
+    before = {w: (getattr(c, w + "_pool").view(torch.uint8).clone(), getattr(c, w + "_scale").view(torch.uint8).clone()) for w in "kv"}
+    lay.append(k, v, c.kv_len, table, cu_new=ints(cu))
+    assert L.lola_attn_status()[1] == L.LOLA_ATTN_BAD_PAGE
+    rows = [(b, cu[b] + i, len_ - (cu[b + 1] - cu[b]) + i) for b, len_ in enumerate(c.lens) for i in range(cu[b + 1] - cu[b])]
+    rows = [r for r in rows if not (r[0] == 0 and 480 <= r[2] < 496) and not (r[0] == 2 and r[2] < 16)]
+    b, r, pos = (torch.tensor(x, device="cuda") for x in zip(*rows))
+    at = c.table.long()[b, pos // page], pos % page
+    for w, x in (("k", k), ("v", v)):
+        codes, power = encode(x[r])
+        pool, scale = before[w]
+        pool[at[0], :, at[1]], scale[at[0], :, at[1]] = codes.view(torch.uint8), power
+        now = getattr(c, w + "_pool").view(torch.uint8)
+        nan = (pool & 0x7f) == 0x7f                          # (NaN has two codes)
+        assert torch.equal(nan, (now & 0x7f) == 0x7f) and torch.equal(pool[~nan], now[~nan])
+        assert torch.equal(scale, getattr(c, w + "_scale").view(torch.uint8))
+    # queries are written for tokens without a slot too, and for no row outside the sequences; positions of the caller's
+    freq = torch.rand(d // 2, generator=gen, device="cuda")
+    where = torch.randint(0, 1 << 24, (n,), generator=gen, device="cuda", dtype=torch.int64).int()
+    out = torch.full_like(q, 7.0)
+    lay.append(k, v, c.kv_len, table, cu_new=ints(cu), q=q, inv_freq=freq, q_out=out, positions=where, pairs="neighbours")
+    assert L.lola_attn_status()[1] == L.LOLA_ATTN_BAD_PAGE
+    want, tol = rotated(q, where.long(), freq, "neighbours")
+    inside = torch.zeros(n, dtype=torch.bool, device="cuda")
+    inside[2:990] = True
+    check(out[inside], want[inside], tol[inside], "q")
+    assert bool((out[~inside] == 7).all())
+    # in place, and in rows of one projection
+    both = torch.cat([q, k, v], 1)
+    lay.append(both[:, Hq:Hq + Hkv], both[:, Hq + Hkv:], c.kv_len, table, cu_new=ints(cu), q=both[:, :Hq], inv_freq=freq,
+               q_out=both[:, :Hq], positions=where, pairs="neighbours")
+    L.lola_attn_status()
+    assert torch.equal(both[inside, :Hq], out[inside]) and torch.equal(both[~inside, :Hq], q[~inside])
+
+
 # ---------------------------------------------------------------------------------------
 # read
 # ---------------------------------------------------------------------------------------
