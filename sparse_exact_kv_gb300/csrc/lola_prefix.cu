@@ -13,7 +13,7 @@
 // softmax runs beside the other's products, and the halves are added at the segment's end.
 // Warps: 0-3, 4-7 softmax of tile 0, 1 (one thread per row: Q rows to shared memory, S into registers, maximum, weights, P
 // into TMEM over S, at the end O out of TMEM); 8 products (one thread); 9 pages and loads, a ring of K and V blocks.
-// QZ, a quantised cache: the ring's blocks are written by warps 12-15, as float16 numbers code 2^(e - E), from e4m3 numbers
+// QZ, a quantised cache: the ring's blocks are written by warps 12-15 (or, by turns, 12-15 and 16-19), as float16 numbers code 2^(e - E), from e4m3 numbers
 // and powers of two that a second ring brings; E is the block's largest power, of its keys or of its values (numbers 2^-33
 // and less of the largest one that these may hold round or vanish: as small against the block's scores, or outputs, as
 // float32's own rounding).  A key's 2^E is a factor of the scores, a value's joins the weights' exponent, as in
@@ -42,8 +42,9 @@ static_assert(kItem == 2 * kM, "two tiles");
 constexpr int kBad = 8;                  // blocks whose pages and powers are remembered: more than the loader is ahead
 constexpr float kWeightBits = 15.f;      // QZ: weights are kept times kUp
 
-template <int D, bool QZ> struct PCfg {
-    static constexpr int kThreads = QZ ? 512 : 384;
+// CV: groups of four converting warps.
+template <int D, bool QZ, int CV> struct PCfg {
+    static constexpr int kThreads = 384 + 128 * CV;
     static constexpr int kMmaWarp = 8, kLoadWarp = 9, kConvWarp = 12;
     static constexpr int kTileBytes = kM * D * 2;                       // a Q tile, a K or V block
     static constexpr int kRing = D == 128 ? (QZ ? 3 : 5) : (QZ ? 4 : 8);
@@ -53,10 +54,12 @@ template <int D, bool QZ> struct PCfg {
     // Registers of a softmax thread and of the others: what the block was launched with, 168 or 128 a thread, given out
     // anew, so that a row's 128 scores fit.  QZ at d = 64: the scores come first here too (64 sequences behind 64000 tokens,
     // 32/8 heads: 60 us, 68 with 128 and 128).
-    static constexpr int kSoftmaxRegs = QZ ? (D == 128 ? 128 : 192) : 208, kOtherRegs = QZ ? (D == 128 ? 128 : 64) : 88;
+    static constexpr int kSoftmaxRegs = QZ ? (D == 128 ? 128 : 192) : 208, kOtherRegs = QZ ? (D == 64 ? 64 : CV == 2 ? 72 : 128) : 88;
+    static constexpr int kLaunchRegs = QZ ? (CV == 2 ? 96 : 128) : 168;
+    static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs, "more than the block has");
     // Scores in registers.  QZ at d = 128 is bound by the conversion, whose warps need their 128 registers and the schedulers'
     // time: the softmax goes over S twice there, 32 columns at a time (128 sequences behind 131072 tokens, 32/8 heads: 256 us;
-    // half of the scores held 300, all of them, with 192 and 64 registers, 334; eight converting warps 276).  Elsewhere S is
+    // half of the scores held 300, all of them, with 192 and 64 registers, 334).  Elsewhere S is
     // read once (bfloat16, the same size: 198 us, 221 in the loop; QZ, d = 64, 24/4 heads: 162 and 171).
     static constexpr int kHeld = QZ && D == 128 ? 32 : kN;
     __device__ static constexpr uint32_t TS(int i) { return 128u * i; }  // S (P over its first half)
@@ -71,9 +74,9 @@ struct PSeg {
     int whole, k, np, rec;     // as in Seg; rec: the item's first record
 };
 
-template <int D, bool QZ>
-__global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(const __grid_constant__ Maps maps, const Args a) {
-    using C = PCfg<D, QZ>;
+template <int D, bool QZ, int CV>
+__global__ void __launch_bounds__(PCfg<D, QZ, CV>::kThreads, 1) prefix_tc_kernel(const __grid_constant__ Maps maps, const Args a) {
+    using C = PCfg<D, QZ, CV>;
     constexpr int kRing = C::kRing, kRaw = C::kRaw;
     extern __shared__ __align__(1024) uint8_t smraw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
@@ -299,7 +302,8 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
             }
             // the others' end
             if (ok && seg >= 2) ok = wait_all(B_SEGFREE + (seg & 1), (uint32_t)(seg / 2 - 1));
-            if (ok && QZ && n >= kRaw) ok = wait_all(B_REMPTY + n % kRaw, (uint32_t)(n / kRaw - 1));
+            for (int x = n; x < n + CV && ok; ++x)
+                if (x >= kRaw) ok = wait_all(B_REMPTY + x % kRaw, (uint32_t)(x / kRaw - 1));
             if (lane == 0) {
                 if (ok) {
                     segs[seg & 1].nb = -1;
@@ -308,9 +312,9 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
                 // leave no copy in flight (before the end of the codes, which is one more phase of its barrier)
                 constexpr int kLast = QZ ? kRaw : kRing, kFirst = QZ ? (int)B_RFULL : (int)B_FULL;
                 for (int x = max(0, n - kLast); x < n; ++x) mbar_wait(bar(kFirst + x % kLast), (uint32_t)(x / kLast) & 1u, kWaitNs);
-                if (QZ && ok) {
-                    raw_sm[n % kRaw] = make_int4(-1, 0, 0, 0);
-                    mbar_arrive1(bar(B_RFULL + n % kRaw));
+                for (int x = n; x < n + CV && ok; ++x) {
+                    raw_sm[x % kRaw] = make_int4(-1, 0, 0, 0);
+                    mbar_arrive1(bar(B_RFULL + x % kRaw));
                 }
                 if (wrong) atomicOr(&g_status, (int)LOLA_ATTN_BAD_PAGE);
             }
@@ -383,7 +387,7 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
         } else if (QZ && warp >= C::kConvWarp) {
             // ================================ codes to float16 ================================
             const int t = tid & 127;
-            for (int n = 0;; ++n) {
+            for (int n = CV == 1 ? 0 : (warp - C::kConvWarp) >> 2;; n += CV) {
                 const int r = n % kRaw, s = n % kRing;
                 if (!wait_all(B_RFULL + r, (uint32_t)(n / kRaw))) break;
                 const int4 info = raw_sm[r];
@@ -454,7 +458,7 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
         }
     } else {
         // ================================ softmax ================================
-        if constexpr (C::kSoftmaxRegs > 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
+        if constexpr (C::kSoftmaxRegs > C::kLaunchRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
         const int i = warp >> 2, r = (warp & 3) * 32 + lane;                    // tile, row of the tile
         const uint32_t lo = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tb + lo + C::TS(i), to = tb + lo + C::TO(i);
@@ -691,8 +695,8 @@ __global__ void __launch_bounds__(PCfg<D, QZ>::kThreads, 1) prefix_tc_kernel(con
     if (warp == C::kMmaWarp) tmem_dealloc<512>(tb);
 }
 
-template <int D, bool QZ> cudaError_t launch_tc(const DecodeArgs& d, cudaStream_t st) {
-    using C = PCfg<D, QZ>;
+template <int D, bool QZ, int CV> cudaError_t launch_tc(const DecodeArgs& d, cudaStream_t st) {
+    using C = PCfg<D, QZ, CV>;
     static std::atomic<uint64_t> done{0};
     Maps maps{};
     if constexpr (!QZ) {
@@ -702,16 +706,19 @@ template <int D, bool QZ> cudaError_t launch_tc(const DecodeArgs& d, cudaStream_
             !make_tmap_pages(&maps.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d.p.V, D, d.p.page, depth, rows, 1))
             return cudaErrorInvalidValue;
     }
-    cudaError_t e = opt_in_smem(prefix_tc_kernel<D, QZ>, C::kSmem, done);
+    cudaError_t e = opt_in_smem(prefix_tc_kernel<D, QZ, CV>, C::kSmem, done);
     if (e != cudaSuccess) return e;
-    return launch_behind(prefix_tc_kernel<D, QZ>, kPieces, C::kThreads, C::kSmem, st, maps, make_args(d));
+    return launch_behind(prefix_tc_kernel<D, QZ, CV>, kPieces, C::kThreads, C::kSmem, st, maps, make_args(d));
 }
 
 }  // namespace
 
 cudaError_t launch_prefix_tc(const DecodeArgs& a, cudaStream_t st) {
-    if (a.p.Ks) return a.p.d == 128 ? launch_tc<128, true>(a, st) : launch_tc<64, true>(a, st);
-    return a.p.d == 128 ? launch_tc<128, false>(a, st) : launch_tc<64, false>(a, st);
+    if (!a.p.Ks) return a.p.d == 128 ? launch_tc<128, false, 0>(a, st) : launch_tc<64, false, 0>(a, st);
+    if (a.p.d == 64) return launch_tc<64, true, 1>(a, st);
+    // One tile of rows whatever the prefixes' sequences are: half of the softmax, and the conversion is what counts (32
+    // sequences behind 131072 tokens, 32/8 heads: 101 us, 116 with four converting warps; 64: 142 and 131).
+    return (int64_t)a.sh.n_seq * a.p.G <= kM ? launch_tc<128, true, 2>(a, st) : launch_tc<128, true, 1>(a, st);
 }
 
 cudaError_t prefix_status_word(int32_t** word) { return cudaGetSymbolAddress((void**)word, g_status); }
