@@ -265,6 +265,7 @@ cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t st);
 int64_t paged_decode_workspace(int d);
 struct DecodeArgs {
     PagedArgs p;             // launch_*_parts: of the prefixes, or of the sequences' own tokens
+    PagedArgs pre;           // launch_*_behind: the prefixes (sh says whose)
     Sharing sh;
     Parts parts;             // launch_*_parts: what they leave
     Rows Q, O;
@@ -278,6 +279,9 @@ cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t st);
 cudaError_t launch_f32_parts(const DecodeArgs& a, cudaStream_t st);
 cudaError_t launch_bf16_parts(const DecodeArgs& a, cudaStream_t st);
 cudaError_t launch_quant_parts(const DecodeArgs& a, cudaStream_t st);
+cudaError_t launch_f32_behind(const DecodeArgs& a, cudaStream_t st);
+cudaError_t launch_tiles_behind(const DecodeArgs& a, cudaStream_t st);      // bfloat16 and quantised caches
+constexpr int kFewPrefixes = 8;                                            // ... for that many prefixes at most
 constexpr int kPrefixRows = 256;         // rows of a record of launch_prefix_tc, column chunks one behind the other
 cudaError_t launch_prefix_tc(const DecodeArgs& a, cudaStream_t st);       // bf16 io: prefixes
 struct SharedArgs {

@@ -385,6 +385,11 @@ int32_t quant_check(const lola_attn_config* c, const lola_paged_kv* kv, const lo
     return LOLA_OK;
 }
 constexpr int64_t kMostRows = (int64_t)1 << 28;     // (sequence, query head) rows of a lola_shared_decode
+// Bytes of prefixes, counted for each sequence that might see them, up to which lola_shared_decode reads them so, from L2
+// for the most part (a call, one kernel and three, d = 128: 4 sequences behind 900 tokens, 32/8 heads, bfloat16, 15 MB, 14.5
+// and 20.9 us; 8 behind two of up to 2049, 8/4 heads, d = 64, float32, 34 MB, 15.6 and 20.5; a third of a microsecond more
+// for a MB).
+constexpr double kReadAgain = 36e6;
 }  // namespace
 
 }  // namespace lola
@@ -877,6 +882,7 @@ static int32_t decode_args(const lola_attn_config* cfg, const lola_paged_kv* kv,
         return LOLA_ERR_INVALID_ARG;
     if (!workspace || !aligned16(workspace)) return LOLA_ERR_INVALID_ARG;
     if ((int64_t)workspace_bytes < need) return LOLA_ERR_WORKSPACE;
+    a->pre = PagedArgs{};
     a->sh = Sharing{};
     a->parts = Parts{};
     a->Q = to_rows(Q);
@@ -932,6 +938,7 @@ int32_t lola_shared_decode(const lola_attn_config* cfg, const lola_paged_kv* kv,
     if ((int64_t)kv->n_seq * cfg->Hq > kMostRows || (int64_t)x->width * kv->page > 0x7fff0000) return LOLA_ERR_UNSUPPORTED;
     s = decode_args(cfg, kv, Q, O, lse, workspace, workspace_bytes, shared_workspace(kv->n_seq, cfg->Hq, cfg->d, cfg->dtype), &a);
     if (s != LOLA_OK) return s;
+    cudaStream_t st = (cudaStream_t)stream;
     SharedArgs b;
     b.p = b.prefix = a.p;
     b.prefix.n_seq = x->n;
@@ -939,6 +946,16 @@ int32_t lola_shared_decode(const lola_attn_config* cfg, const lola_paged_kv* kv,
     b.prefix.table_stride = x->table_stride;
     b.prefix.table = x->table;
     b.prefix.kv_len = x->len;
+    // Few tokens altogether: one kernel that reads a prefix again for each of its sequences.
+    const int64_t row = cfg->d * (int64_t)(scales ? 1 : cfg->dtype == LOLA_BF16 ? 2 : 4);
+    if (x->n <= kFewPrefixes && (double)kv->n_seq * x->width * kv->page * cfg->Hkv * 2 * row <= kReadAgain) {
+        a.pre = b.prefix;
+        a.sh = Sharing{x->cu, kv->n_seq, 0};
+        const cudaError_t e = traced(LOLA_KERNEL_PAGED, st, [&]() {
+            return !scales && cfg->dtype == LOLA_F32 ? launch_f32_behind(a, st) : launch_tiles_behind(a, st);
+        });
+        return e == cudaSuccess ? LOLA_OK : cuda_fail(e, "shared decode");
+    }
     b.cu = x->cu;
     b.Q = a.Q;
     b.O = a.O;
@@ -946,7 +963,6 @@ int32_t lola_shared_decode(const lola_attn_config* cfg, const lola_paged_kv* kv,
     b.workspace = static_cast<char*>(workspace);
     b.give_up = a.give_up;
     b.scale_log2 = a.scale_log2;
-    cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e = traced(LOLA_KERNEL_PREFIX, st, [&]() { return launch_shared_prefix(b, st); });
     if (e != cudaSuccess) return cuda_fail(e, "shared prefix");
     e = traced(LOLA_KERNEL_PAGED, st, [&]() { return launch_shared_own(b, st); });

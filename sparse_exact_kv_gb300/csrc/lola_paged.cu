@@ -32,7 +32,7 @@ namespace {
 // read once, without bank conflicts, into products with q and the output in registers; the eight lanes' sums
 // of a score are added and dealt out by halves (14 shuffles for 16 tokens x 4 rows).  m is the maximum so far:
 // the largest weights' exponents stay near zero, where they lose least.
-template <int D, int RM, bool SH>
+template <int D, int RM, bool SH, bool PRE>
 __global__ void __launch_bounds__(kThreads, 1) paged_decode_f32_kernel(const __grid_constant__ Maps maps, const Args a) {
     using C = Cfg<float, D>;
     constexpr int NC = RM / 4, NP = 4 / NC, KT = kTile / NP, X = D / 32, NW = kCons / kWarp;
@@ -61,8 +61,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_f32_kernel(const __g
     }
     wait_for_last_kernel();
     Start st;
-    if (!find_start<SH>(a, &st)) return;
-    if (warp == NW) produce<float, float, D, 1, SH>(maps, a, st, smem_u32(sm), smem_u32(Qs), D * 4, bars, segs, bad_sm, &abort_sm, lane);
+    if (!find_start<SH, kThreads, kTile, kRows, PRE>(a, &st)) return;
+    if (warp == NW) produce<float, float, D, 1, SH, C, kRows, PRE>(maps, a, st, smem_u32(sm), smem_u32(Qs), D * 4, bars, segs, bad_sm, &abort_sm, lane);
     auto bar = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
     const int grp = warp >> 2, rc = (warp & 3) / NP, tp = (warp & 3) % NP, tg = lane >> 3, j = lane & 7;
     const bool b2 = j & 4, b1 = j & 2, b0 = j & 1;
@@ -101,8 +101,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_f32_kernel(const __g
             if (!ok) break;
             uint8_t* Kt = sm + (size_t)s * 2 * C::kHalf;
             uint8_t* Vt = Kt + C::kHalf;
-            const int nk = max(0, min(kTile, g.len - t * kTile));
-            const uint32_t bad = bad_sm[s];
+            const uint32_t info = bad_sm[s], bad = PRE ? info & 0xffffu : info;
+            const int nk = PRE ? (int)(info >> 16) : max(0, min(kTile, g.len - t * kTile));
             auto hidden = [&](int k) { return k >= nk || ((bad >> (k >> lb)) & 1u); };
             const bool some = nk < kTile || bad;
             if (some) {
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_f32_kernel(const __g
         bar();                                                  // red, ms, ls are read
     }
     __syncthreads();
-    if (abort_sm) settle<D, C::kStages, 1, SH>(a, bars);
+    if (abort_sm) settle<D, C::kStages, 1, SH, kThreads, kTile, PRE>(a, bars);
 }
 
 // ---- bf16: the tile products on the warps' matrix instructions ----
@@ -478,13 +478,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_mma_kernel(const __g
 }
 
 // (rows of a prefix: as many as its sequences have)
-template <int D, bool SH>
+template <int D, bool SH, bool PRE = false>
 cudaError_t launch_f32(const DecodeArgs& d, cudaStream_t st) {
     static std::atomic<uint64_t> done[3] = {};
     const int rows = !SH || d.sh.each ? d.p.G : kRows;
-    if (rows <= 4) return launch_kernel<float, D>(paged_decode_f32_kernel<D, 4, SH>, kThreads / kWarp, done[0], d, st);
-    if (rows <= 8) return launch_kernel<float, D>(paged_decode_f32_kernel<D, 8, SH>, kThreads / kWarp, done[1], d, st);
-    return launch_kernel<float, D>(paged_decode_f32_kernel<D, 16, SH>, kThreads / kWarp, done[2], d, st);
+    if (rows <= 4) return launch_kernel<float, D>(paged_decode_f32_kernel<D, 4, SH, PRE>, kThreads / kWarp, done[0], d, st);
+    if (rows <= 8) return launch_kernel<float, D>(paged_decode_f32_kernel<D, 8, SH, PRE>, kThreads / kWarp, done[1], d, st);
+    return launch_kernel<float, D>(paged_decode_f32_kernel<D, 16, SH, PRE>, kThreads / kWarp, done[2], d, st);
 }
 template <int D>
 cudaError_t launch_bf16(const DecodeArgs& d, cudaStream_t st) {
@@ -503,6 +503,9 @@ cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t st) {
 }
 cudaError_t launch_f32_parts(const DecodeArgs& a, cudaStream_t st) {
     return a.p.d == 128 ? launch_f32<128, true>(a, st) : launch_f32<64, true>(a, st);
+}
+cudaError_t launch_f32_behind(const DecodeArgs& a, cudaStream_t st) {
+    return a.p.d == 128 ? launch_f32<128, false, true>(a, st) : launch_f32<64, false, true>(a, st);
 }
 
 cudaError_t paged_status_word(int32_t** word) { return cudaGetSymbolAddress((void**)word, g_status); }

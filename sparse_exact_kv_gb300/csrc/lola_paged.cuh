@@ -31,7 +31,8 @@ struct Maps {
 
 struct Args {
     PagedArgs p;        // SH: of the prefixes, or of the sequences
-    Sharing sh;         // SH: whose rows see them
+    PagedArgs pre;      // PRE: the prefixes
+    Sharing sh;         // SH, PRE: whose rows see them
     Parts parts;        // SH: what is left of them
     Rows Q, O;
     float* lse;
@@ -103,9 +104,32 @@ template <bool SH, int ROWS = kRows> __device__ __forceinline__ Group group_of(c
 template <int TILE = kTile>
 __device__ __forceinline__ int tiles_of(int64_t tokens) { return tokens <= 0 ? 1 : (int)((tokens + TILE - 1) / TILE); }
 
+// ---- PRE: the tiles of a sequence are those of its prefix, then its own ----
+struct View {
+    int g, tokens, tiles;      // the prefix (-1: none), its tokens and tiles
+};
+template <int TILE> __device__ __forceinline__ View view_of(const Args& a, int b, int* bits) {
+    View v{-1, 0, 0};
+    for (int x = 0; x < a.pre.n_seq; ++x) {
+        int lo = 0, n = a.p.n_seq;
+        if (a.sh.cu) seq_rows(a.sh.cu, x, a.p.n_seq, &lo, &n, bits);
+        if (b >= lo && b < lo + n) v.g = x;
+    }
+    if (v.g >= 0) v.tokens = (int)paged_tokens(a.pre, a.pre.kv_len[v.g]);
+    v.tiles = (v.tokens + TILE - 1) / TILE;
+    return v;
+}
+// tiles of sequence b, which has so many tokens of its own
+template <int TILE, bool PRE> __device__ __forceinline__ int item_tiles(const Args& a, int b, int64_t tokens, int* bits) {
+    if constexpr (!PRE) return tiles_of<TILE>(tokens);
+    const int pre = view_of<TILE>(a, b, bits).tiles;
+    return pre + (pre > 0 && tokens <= 0 ? 0 : tiles_of<TILE>(tokens));
+}
+
 // Units of sequence (or prefix) b: a prefix without tokens or sequences has none.
-template <bool SH, int TILE = kTile, int ROWS = kRows>
-__device__ __forceinline__ int64_t units_of(const Args& a, int b, int* bits = nullptr) {
+template <bool SH, int TILE = kTile, int ROWS = kRows, bool PRE = false>
+__device__ __forceinline__ int64_t units_of(const Args& a, int b, int* bits) {
+    if constexpr (PRE) return (int64_t)item_tiles<TILE, true>(a, b, paged_tokens(a.p, a.p.kv_len[b]), bits) * a.I;
     const int64_t tokens = paged_tokens(a.p, a.p.kv_len[b]);
     if (SH && tokens == 0) return 0;
     return (int64_t)tiles_of<TILE>(tokens) * group_of<SH, ROWS>(a, b, bits).I;
@@ -224,7 +248,7 @@ struct Start {
     int N, b;                     // pieces; the first unit's sequence
     int piece;
 };
-template <bool SH, int NT = kThreads, int TILE = kTile, int ROWS = kRows>
+template <bool SH, int NT = kThreads, int TILE = kTile, int ROWS = kRows, bool PRE = false>
 __device__ __forceinline__ bool find_start(const Args& a, Start* st) {
     const PagedArgs& p = a.p;
     __shared__ int64_t sums[NT / kWarp];
@@ -232,14 +256,14 @@ __device__ __forceinline__ bool find_start(const Args& a, Start* st) {
     __shared__ int64_t found_r;
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
     int bits = 0;
-    auto count = [&](int b) -> int64_t { return b < p.n_seq ? units_of<SH, TILE, ROWS>(a, b, &bits) : 0; };
+    auto count = [&](int b) -> int64_t { return b < p.n_seq ? units_of<SH, TILE, ROWS, PRE>(a, b, &bits) : 0; };
     const int64_t own = count(threadIdx.x);            // (the whole of it up to 288 sequences)
     int64_t rest = 0;
     for (int b = threadIdx.x + NT; b < p.n_seq; b += NT) rest += count(b);
     st->total = block_total<NT>(own + rest, sums);
     st->N = pieces_of(st->total);
     st->piece = (int)blockIdx.x;
-    if (SH && bits) atomicOr(&g_status, bits);
+    if ((SH || PRE) && bits) atomicOr(&g_status, bits);
     if ((int)blockIdx.x >= st->N) return false;
     st->u0 = split_at(st->total, st->N, blockIdx.x);
     st->u1 = split_at(st->total, st->N, blockIdx.x + 1);
@@ -289,7 +313,7 @@ __device__ __forceinline__ void place_piece(const Start& st, int64_t xs, int til
 // by side, as each copy takes its thread some 180 clocks to issue, and a tile of codes half a tile's time at most (all
 // copies by one warp: 64 sequences of 1000-8000 tokens, 32/8 heads, d = 128, 117 us).  The first of them does the rest.
 // The powers come four bytes a lane, past the tensor unit, whose small copies take as long as its large ones.
-template <typename T, typename TQ, int D, int NS, bool SH, typename C = Cfg<T, D>, int ROWS = kRows, typename B>
+template <typename T, typename TQ, int D, int NS, bool SH, typename C = Cfg<T, D>, int ROWS = kRows, bool PRE = false, typename B>
 __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const Start& st, uint32_t ring, uint32_t qs,
                                         uint32_t q_pitch, B& bars, Seg* segs, uint32_t* bad_sm, int* abort_sm, int lane, int part = 0) {
     constexpr bool kParts = C::kScales > 0;
@@ -302,7 +326,10 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
     int lens_b = b;                                               // the lanes hold 32 sequences' lengths
     int lens = b + lane < p.n_seq ? p.kv_len[b + lane] : 0;
     int64_t tokens = paged_tokens(p, __shfl_sync(0xffffffffu, lens, 0));
-    int tiles = tiles_of<C::kTokens>(tokens), t0, item = divide(st.rem, tiles, &t0);
+    int ignored = 0;
+    [[maybe_unused]] View view{-1, 0, 0};
+    if constexpr (PRE) view = view_of<C::kTokens>(a, b, &ignored);
+    int tiles = item_tiles<C::kTokens, PRE>(a, b, tokens, &ignored), t0, item = divide(st.rem, tiles, &t0);
     int64_t u = st.u0;
     int n = 0, i = 0, held_b = -1, held = -1;
     int held_c = 0;                                           // ... and 32 page-table columns of held_b
@@ -328,6 +355,7 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
             if (!g.whole) place_piece(st, u - t0, tiles, &g);
             segs[slot] = g;
             if (p.kv_len[b] > tokens && tokens > 0) atomicOr(&g_status, (int)LOLA_ATTN_BAD_PAGE);
+            if (PRE && view.g >= 0 && a.pre.kv_len[view.g] > view.tokens) atomicOr(&g_status, (int)LOLA_ATTN_BAD_PAGE);
             mbar_expect(smem_u32(&bars.seg_full[slot]), (uint32_t)R * kQBytes);
         }
         __syncwarp();
@@ -345,14 +373,16 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
             if (n >= C::kStages) ok = __all_sync(0xffffffffu, ring_wait(smem_u32(&bars.empty[s]), (uint32_t)(n / C::kStages - 1) & 1, abort_sm));
             if (!ok) break;
             // (positions fit 31 bits, but for the boxes behind the last token's)
-            const uint32_t pos = (uint32_t)t * C::kTokens, have = (uint32_t)tokens;
+            const bool pre = PRE && t < view.tiles;
+            const uint32_t pos = (uint32_t)(PRE && !pre ? t - view.tiles : t) * C::kTokens, have = (uint32_t)(pre ? view.tokens : tokens);
+            const int entry = PRE ? 2 * b + pre : b;              // (whose columns are held)
             const int col = (int)(pos >> p.page_log2);
             const int used = have > pos ? min(nbox, (int)((have - pos + box - 1) >> lb)) : 0;     // boxes with tokens
-            if (held_b != b || col < held_c || col + used > held_c + 32) {
-                held_b = b;
+            if (held_b != entry || col < held_c || col + used > held_c + 32) {
+                held_b = entry;
                 held_c = col;
                 const int64_t c = (int64_t)(col + lane) << p.page_log2;
-                held = c < tokens ? paged_page(p, b, c) : 0;
+                held = c >= (int64_t)have ? 0 : pre ? paged_page(a.pre, view.g, c) : paged_page(p, b, c);
             }
             // lanes 0 .. used - 1: a box of K each; lanes 16 ..: of V (e4m3: this warp's part)
             const int x = lane & 15;
@@ -361,7 +391,7 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
             const uint32_t bad_mask = __ballot_sync(0xffffffffu, bad) & 0xffffu;
             if (first && lane == 0) {
                 if (bad_mask) atomicOr(&g_status, (int)LOLA_ATTN_BAD_PAGE);
-                bad_sm[s] = bad_mask;
+                bad_sm[s] = PRE ? bad_mask | (have > pos ? min(have - pos, (uint32_t)C::kTokens) : 0u) << 16 : bad_mask;
                 mbar_expect(smem_u32(&bars.full[s]), (uint32_t)(2 * (used - __popc(bad_mask)) * box * C::kRowBytes));
                 *reinterpret_cast<volatile int*>(&bars.issued) = n + 1;
             }
@@ -403,7 +433,8 @@ __device__ __forceinline__ void produce(const Maps& maps, const Args& a, const S
                 tokens = paged_tokens(p, __shfl_sync(0xffffffffu, lens, b - lens_b));
                 gr = group_of<SH>(a, b);
             } while (SH && (tokens == 0 || gr.I == 0));               // (units are left: there is such a prefix)
-            tiles = tiles_of<C::kTokens>(tokens);
+            if constexpr (PRE) view = view_of<C::kTokens>(a, b, &ignored);
+            tiles = item_tiles<C::kTokens, PRE>(a, b, tokens, &ignored);
         }
     }
     if (!first) {
@@ -433,6 +464,14 @@ __device__ __forceinline__ bool sees_token(const PagedArgs& p, int b) {
     return false;
 }
 
+// ... or its prefix has
+__device__ __forceinline__ bool sees_any(const Args& a, int b) {
+    if (sees_token(a.p, b)) return true;
+    int ignored = 0;
+    const int g = a.pre.n_seq > 0 ? view_of<kTile>(a, b, &ignored).g : -1;
+    return g >= 0 && sees_token(a.pre, g);
+}
+
 // Where a segment that is a piece of its item leaves its part.
 template <int D, bool SH> __device__ __forceinline__ float* segment_record(const Args& a, const Seg& g) {
     const int slot = g.k == 0 ? g.s0 : 0;
@@ -460,7 +499,7 @@ __device__ __forceinline__ void write_out(const Args& a, const Seg& g, bool whol
         if (c == 0 && (whole || g.k == 0)) q.desc[i] = whole ? make_int4(1, 0, 0, 0) : make_int4(g.np, 2 * g.c0 + g.s0, r, 1);
     } else if (whole) {
         // (no token seen: o = 0; scores that are all minus infinity: 0 / 0)
-        const float inv = L == 0.f ? (sees_token(a.p, g.b) ? NAN : 0.f) : 1.f / L;
+        const float inv = L == 0.f ? (sees_any(a, g.b) ? NAN : 0.f) : 1.f / L;
 #pragma unroll
         for (int z = 0; z < 4; ++z) y[z] *= inv;
         store4(reinterpret_cast<T*>(a.O.data) + (int64_t)g.b * a.O.row + (int64_t)(g.h0 + r) * a.O.head + c, y);
@@ -572,7 +611,7 @@ __device__ void join_pieces(const Args& a, const Seg& g, int t, int* go, int* ar
 // The end of a CTA whose waits gave up (all threads, after all roles): no copy is left in flight, and its pieces
 // that were not counted are, so that every cell of the call ends at 0 (what the joins then make of their records
 // is as invalid as the call).
-template <int D, int S, int NS, bool SH, int NT = kThreads, int TILE = kTile, typename B>
+template <int D, int S, int NS, bool SH, int NT = kThreads, int TILE = kTile, bool PRE = false, typename B>
 __device__ __noinline__ void settle(const Args& a, B& bars) {
     if (threadIdx.x == 0) {
         const int n = max(bars.issued, bars.ahead), i = bars.given;
@@ -583,8 +622,10 @@ __device__ __noinline__ void settle(const Args& a, B& bars) {
     }
     if constexpr (SH) return;                                      // (nothing is counted)
     Start st;
-    if (!find_start<false, NT, TILE>(a, &st) || threadIdx.x != 0) return;
-    int b = st.b, tiles = tiles_of<TILE>(paged_tokens(a.p, a.p.kv_len[b]));
+    if (!find_start<false, NT, TILE, kRows, PRE>(a, &st) || threadIdx.x != 0) return;
+    int ignored = 0;
+    auto count = [&](int b) { return item_tiles<TILE, PRE>(a, b, paged_tokens(a.p, a.p.kv_len[b]), &ignored); };
+    int b = st.b, tiles = count(b);
     int item = (int)(st.rem / tiles), t0 = (int)(st.rem % tiles);
     for (int64_t u = st.u0; u < st.u1;) {
         const int t1 = (int)min((int64_t)tiles, t0 + (st.u1 - u));
@@ -600,7 +641,7 @@ __device__ __noinline__ void settle(const Args& a, B& bars) {
         t0 = 0;
         if (++item == a.I && u < st.u1) {
             item = 0;
-            tiles = tiles_of<TILE>(paged_tokens(a.p, a.p.kv_len[++b]));
+            tiles = count(++b);
         }
     }
 }
@@ -627,6 +668,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 inline Args make_args(const DecodeArgs& d) {
     Args a;
     a.p = d.p;
+    a.pre = d.pre;
     a.sh = d.sh;
     a.parts = d.parts;
     a.Q = d.Q;

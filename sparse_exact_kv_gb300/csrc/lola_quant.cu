@@ -63,7 +63,7 @@ template <typename T, typename TO, int D, int NB> struct TSmem {
 // segment adds its warps up and goes on to the next segment; the last of a segment's groups to be done adds the groups up, in
 // their order.  So a sequence of one tile takes one group, and the others' tiles run beside its end (all warps at the segment's
 // end together: 64 sequences of 1000-8000 tokens, 32/8 heads, d = 128, e4m3, 94 us; 1024 items of 64 tokens 37 us).
-template <typename T, typename TO, int D, int NB, bool SH>
+template <typename T, typename TO, int D, int NB, bool SH, bool PRE>
 __global__ void __launch_bounds__(TSmem<T, TO, D, NB>::kAll * kWarp, 1) decode_t_kernel(const __grid_constant__ Maps maps, const Args a) {
     using M = TSmem<T, TO, D, NB>;
     using C = Ring<Cfg<T, D>, M::kRing>;
@@ -94,8 +94,8 @@ __global__ void __launch_bounds__(TSmem<T, TO, D, NB>::kAll * kWarp, 1) decode_t
     }
     wait_for_last_kernel();
     Start st;
-    if (!find_start<SH, M::kAll * kWarp, C::kTokens>(a, &st)) return;
-    if (warp >= NW) produce<T, TO, D, NS, SH, C, 8 * NB>(maps, a, st, sb, smem_u32(x.q[0]), M::kPitch, bars, segs, bad_sm, &abort_sm, lane, warp - NW);
+    if (!find_start<SH, M::kAll * kWarp, C::kTokens, kRows, PRE>(a, &st)) return;
+    if (warp >= NW) produce<T, TO, D, NS, SH, C, 8 * NB, PRE>(maps, a, st, sb, smem_u32(x.q[0]), M::kPitch, bars, segs, bad_sm, &abort_sm, lane, warp - NW);
     const int grp = warp >> 2, w4 = warp & 3, gt = tid & 127, g8 = lane >> 2, q4 = lane & 3, q2 = q4 * 2;
     auto bar = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(NT) : "memory"); };
     const int box = min(p.page, C::kTokens), lb = 31 - __clz(box);
@@ -206,8 +206,8 @@ __global__ void __launch_bounds__(TSmem<T, TO, D, NB>::kAll * kWarp, 1) decode_t
             if (!ok) break;
             const uint32_t kt = sb + (uint32_t)s * 2 * C::kHalf, vt = kt + C::kHalf;
             [[maybe_unused]] const uint8_t* powers = sm + (size_t)C::kStages * 2 * C::kHalf + (size_t)s * C::kScales + g8;
-            const int left = g.len - t * C::kTokens;
-            const uint32_t bad = bad_sm[s];
+            const uint32_t info = bad_sm[s], bad = PRE ? info & 0xffffu : info;
+            const int left = PRE ? (int)(info >> 16) : g.len - t * C::kTokens;
 #pragma unroll 1
             for (int k0 = w4 * (C::kTokens / 4), end = k0 + C::kTokens / 4; k0 < end; k0 += 16) {
                 // ---- S^T: 16 tokens x 8 rows, two chains ----
@@ -459,24 +459,24 @@ __global__ void __launch_bounds__(TSmem<T, TO, D, NB>::kAll * kWarp, 1) decode_t
         if (!SH && !g.whole) join_pieces<TO, D, NT>(a, g, gt, &go[grp], bars.arrived, bar);
     }
     __syncthreads();
-    if (abort_sm) settle<D, C::kStages, NS, SH, M::kAll * kWarp, C::kTokens>(a, bars);
+    if (abort_sm) settle<D, C::kStages, NS, SH, M::kAll * kWarp, C::kTokens, PRE>(a, bars);
 }
 
-template <typename T, typename TO, int D, int NB, bool SH>
+template <typename T, typename TO, int D, int NB, bool SH, bool PRE>
 cudaError_t launch_t(const DecodeArgs& d, cudaStream_t st) {
     using M = TSmem<T, TO, D, NB>;
     using C = Ring<Cfg<T, D>, M::kRing>;
     static_assert(C::kSmem + sizeof(M) + 2048 <= 232448, "ring, joins and the barriers beside them");
     static std::atomic<uint64_t> done{0};
-    return launch_kernel<T, D>(decode_t_kernel<T, TO, D, NB, SH>, M::kAll, done, d, st, C::kSmem + (int)sizeof(M));
+    return launch_kernel<T, D>(decode_t_kernel<T, TO, D, NB, SH, PRE>, M::kAll, done, d, st, C::kSmem + (int)sizeof(M));
 }
 // (rows of a prefix: as many as its sequences have)
-template <typename T, typename TO, int D, bool SH> cudaError_t launch_t(const DecodeArgs& d, cudaStream_t st) {
-    return (!SH || d.sh.each) && d.p.G <= 8 ? launch_t<T, TO, D, 1, SH>(d, st) : launch_t<T, TO, D, 2, SH>(d, st);
+template <typename T, typename TO, int D, bool SH, bool PRE = false> cudaError_t launch_t(const DecodeArgs& d, cudaStream_t st) {
+    return (!SH || d.sh.each) && d.p.G <= 8 ? launch_t<T, TO, D, 1, SH, PRE>(d, st) : launch_t<T, TO, D, 2, SH, PRE>(d, st);
 }
-template <bool SH> cudaError_t launch_quant(const DecodeArgs& a, cudaStream_t st) {
-    if (a.p.dtype == LOLA_F32) return a.p.d == 128 ? launch_t<uint8_t, float, 128, SH>(a, st) : launch_t<uint8_t, float, 64, SH>(a, st);
-    return a.p.d == 128 ? launch_t<uint8_t, __nv_bfloat16, 128, SH>(a, st) : launch_t<uint8_t, __nv_bfloat16, 64, SH>(a, st);
+template <bool SH, bool PRE = false> cudaError_t launch_quant(const DecodeArgs& a, cudaStream_t st) {
+    if (a.p.dtype == LOLA_F32) return a.p.d == 128 ? launch_t<uint8_t, float, 128, SH, PRE>(a, st) : launch_t<uint8_t, float, 64, SH, PRE>(a, st);
+    return a.p.d == 128 ? launch_t<uint8_t, __nv_bfloat16, 128, SH, PRE>(a, st) : launch_t<uint8_t, __nv_bfloat16, 64, SH, PRE>(a, st);
 }
 
 // ---- the cached rows as rows ----
@@ -616,6 +616,11 @@ cudaError_t launch_quant_decode(const DecodeArgs& a, cudaStream_t st) { return l
 cudaError_t launch_quant_parts(const DecodeArgs& a, cudaStream_t st) { return launch_quant<true>(a, st); }
 cudaError_t launch_bf16_parts(const DecodeArgs& a, cudaStream_t st) {
     return a.p.d == 128 ? launch_t<__nv_bfloat16, __nv_bfloat16, 128, true>(a, st) : launch_t<__nv_bfloat16, __nv_bfloat16, 64, true>(a, st);
+}
+cudaError_t launch_tiles_behind(const DecodeArgs& a, cudaStream_t st) {
+    if (a.p.Ks) return launch_quant<false, true>(a, st);
+    return a.p.d == 128 ? launch_t<__nv_bfloat16, __nv_bfloat16, 128, false, true>(a, st)
+                        : launch_t<__nv_bfloat16, __nv_bfloat16, 64, false, true>(a, st);
 }
 
 cudaError_t launch_quant_read(const ReadArgs& a, cudaStream_t st) {

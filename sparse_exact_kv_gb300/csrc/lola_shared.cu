@@ -8,6 +8,10 @@
 // Bound by its chain of accesses (which parts, the parts): two rows a CTA, their parts dealt out to eight warps,
 // which have three of them in flight each (64 sequences behind 16001 tokens, 32 heads, 19 prefix parts a row: 10 us).  (When the kernel over the own tokens read the prefix' parts itself, row
 // after row, 64 sequences behind 16001 tokens took it 92 us, 8 heads, d = 128.)
+// Three kernels take 20 us whatever there is to do; few tokens altogether go to K10's and K11's kernels in a form whose
+// sequences' tiles are those of the prefix, then their own (PRE).
+#include <algorithm>
+
 #include "lola_paged.cuh"
 
 namespace lola {
@@ -169,6 +173,7 @@ DecodeArgs parts_args(const SharedArgs& a, bool own) {
     Parts x[2];
     carve(&x[0], &x[1], a.workspace, a.p.n_seq, a.p.Hq, a.p.d, a.p.dtype);
     d.p = own ? a.p : a.prefix;
+    d.pre = PagedArgs{};
     d.sh = Sharing{own ? nullptr : a.cu, a.p.n_seq, own};
     d.parts = x[own];
     d.Q = a.Q;
@@ -185,7 +190,7 @@ DecodeArgs parts_args(const SharedArgs& a, bool own) {
 
 int64_t shared_workspace(int n_seq, int Hq, int d, int dtype) {
     Parts x, y;
-    return carve(&x, &y, nullptr, n_seq, Hq, d, dtype);
+    return std::max(carve(&x, &y, nullptr, n_seq, Hq, d, dtype), paged_decode_workspace(d));
 }
 
 cudaError_t launch_shared_prefix(const SharedArgs& a, cudaStream_t st) {

@@ -412,6 +412,25 @@ def test_decode_strides_and_graphs(L, gen):
 # shared prefixes
 # ---------------------------------------------------------------------------------------
 
+WIDE = False
+
+
+@pytest.fixture
+def wide(request):
+    """Prefix tables so wide that a call reads every prefix once, for all sequences, however short it is; otherwise
+    short ones are read for each sequence."""
+    global WIDE
+    WIDE = request.param
+    yield
+    WIDE = False
+
+
+def pytest_generate_tests(metafunc):
+    if "Shared" in metafunc.function.__code__.co_names:
+        metafunc.fixturenames.insert(0, "wide")
+        metafunc.parametrize("wide", [False, True], ids=["narrow", "wide"], indirect=True)
+
+
 class Shared:
     """A cache of prefixes and sequences: sequence b sees prefix of[b] (-1: none) before its own tokens."""
 
@@ -420,6 +439,10 @@ class Shared:
         c, k = self.c, len(prefixes)
         self.prefix_len, self.kv_len = c.kv_len[:k].clone(), c.kv_len[k:].clone()
         self.prefix_table, self.table = c.table[:k], c.table[k:]
+        if WIDE:
+            row = 2 * Hkv * d * (1 if quant else torch.finfo(dtype).bits // 8)
+            junk = torch.randint(-9, 1 << 30, (k, 36_000_000 // (len(lens) * page * row) + 2), generator=gen, device="cuda").int()
+            self.prefix_table = torch.cat([self.prefix_table, junk], 1)
         self.cu = offsets(members, start)
         self.of = [-1] * start
         for g, m in enumerate(members):
