@@ -542,7 +542,7 @@ int64_t lola_shared_decode_workspace_bytes(const lola_attn_config* cfg, int32_t 
 
 /* Attention of one query token per sequence over its prefix' tokens and its own kv_len cached tokens: lola_paged_decode
  * (scales NULL) or lola_quant_decode of the two one behind the other, with a prefix' keys and values read once for all
- * sequences that share it.  (Up to 8 prefixes whose tables hold few tokens, n_seq width page Hkv rows of up to 36 MB, are
+ * sequences that share it.  (Up to 8 prefixes whose tables hold few tokens, n_seq width page Hkv rows of up to 64 MB, are
  * read for each sequence, by one kernel.)
  * kv describes the pools and the sequences' own tokens (kv_len 0: none; the tokens are counted from 0 behind the
  * prefix, so that an append of them takes explicit positions).  A sequence outside cu[0] .. cu[n] - 1 has no prefix.

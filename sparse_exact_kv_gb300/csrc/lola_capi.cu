@@ -386,10 +386,10 @@ int32_t quant_check(const lola_attn_config* c, const lola_paged_kv* kv, const lo
 }
 constexpr int64_t kMostRows = (int64_t)1 << 28;     // (sequence, query head) rows of a lola_shared_decode
 // Bytes of prefixes, counted for each sequence that might see them, up to which lola_shared_decode reads them so, from L2
-// for the most part (a call, one kernel and three, d = 128: 4 sequences behind 900 tokens, 32/8 heads, bfloat16, 15 MB, 14.5
-// and 20.9 us; 8 behind two of up to 2049, 8/4 heads, d = 64, float32, 34 MB, 15.6 and 20.5; a third of a microsecond more
-// for a MB).
-constexpr double kReadAgain = 36e6;
+// for the most part (one kernel and three, us a call: d = 128, 32/8 heads, 4 sequences behind 300 tokens, bfloat16, 5 MB, 11
+// and 19; 16 behind 1000, 67 MB, 18.1 and 19.3; behind 2000, 134 MB, 23.8 and 20.2; 16 behind 2000, e4m3, 67 MB, 21 and 24;
+// d = 64, 8/4 heads, float32, 66 MB, 18.8 and 18.6).
+constexpr double kReadAgain = 64e6;
 }  // namespace
 
 }  // namespace lola

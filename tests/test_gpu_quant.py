@@ -441,7 +441,7 @@ class Shared:
         self.prefix_table, self.table = c.table[:k], c.table[k:]
         if WIDE:
             row = 2 * Hkv * d * (1 if quant else torch.finfo(dtype).bits // 8)
-            junk = torch.randint(-9, 1 << 30, (k, 36_000_000 // (len(lens) * page * row) + 2), generator=gen, device="cuda").int()
+            junk = torch.randint(-9, 1 << 30, (k, 64_000_000 // (len(lens) * page * row) + 2), generator=gen, device="cuda").int()
             self.prefix_table = torch.cat([self.prefix_table, junk], 1)
         self.cu = offsets(members, start)
         self.of = [-1] * start
