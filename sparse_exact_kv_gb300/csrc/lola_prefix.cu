@@ -474,7 +474,12 @@ __global__ void __launch_bounds__(PCfg<D, QZ, CV>::kThreads, 1) prefix_tc_kernel
             const int tile_row = two ? kM * i : 0;
             if (n > 0) {
                 // ---- Q rows of the tile ----
-                if (it > 0) load_q(i, g.m0, g.r0, g.R, g.hk);
+                if (it > 0) {
+                    // (a tile without blocks in the first segment has not waited for its rows' copies there, and copies of one
+                    // thread land in any order)
+                    cp_async_wait_all();
+                    load_q(i, g.m0, g.r0, g.R, g.hk);
+                }
                 cp_async_wait_all();
                 if constexpr (QZ) {
                     // float16 numbers, the row's largest magnitude in [2^14, 2^15)
