@@ -19,6 +19,6 @@ __device__ __forceinline__ uint32_t half2_of(float x, float y) {
 // 2^(127 - b) for a byte b < 255 (2^-127, of b = 254, is no normal number)
 __device__ __forceinline__ float power_down(uint32_t b) { return __uint_as_float(b < 254u ? (254u - b) << 23 : 0x400000u); }
 
-constexpr float kUp = 32768.f;            // the weights' factor
+constexpr float kUpBits = 15.f, kUp = 32768.f;            // the weights' factor 2^15
 
 }  // namespace lola

@@ -7,8 +7,11 @@
 // whole batch for every SM, a producer warp with a ring of tiles, a running softmax per warp, the pieces' join.
 // Here the codes become float16 numbers (exact) in the registers and go to the warps' float16 products; the
 // powers of two of the keys scale the scores, those of the values join the weights in the exponent:
-//   s_j = c 2^{e_j} q . code_j,   w_j = 2^{s_j + f_j - m},   O = sum_j w_j code'_j,   l = sum_j w_j 2^{-f_j},
-// m set above the largest s_j + f_j: everything but the exponentials, the weights' rounding and the sums is exact.
+//   s_j = c 2^{e_j} q . code_j,   w_j = 2^{s_j + f_j - m},   O = sum_j w_j code'_j,   l = sum_j 2^{s_j - r},
+// m set above the largest s_j + f_j, r, a lane's own, above its largest s_j: everything but the exponentials, the weights'
+// rounding and the sums is exact, however far the powers lie apart (l as a sum of w_j 2^{-f_j} lost rows whose power is
+// 2^-110 of another's: of zeros, which have 2^-100, beside numbers of 2^20).  At a segment's end O comes to 2^{m - r}, and
+// from there on m and l are the scores'.
 // q comes as float16 numbers of its row's own power of two (its largest number in [2^14, 2^15): a bfloat16 number
 // loses nothing down to 2^-28 of that; a float32 number is kept in two parts, to 2^-39 of it), the weights as
 // float16 numbers of 2^15 w_j (rounded by 2^-12 of themselves, or by 2^-40 where they are small; float32 io: two parts).
@@ -18,8 +21,8 @@
 // The contraction's channels may come in any order: a lane's four neighbouring codes of K, one word, are its four
 // channels of a product, and the same four of q.  A word of V holds two channels of two tokens and is permuted first.
 // Bound by reading codes and powers once.  Measured (bfloat16 io, d = 128): 64 sequences of 1000-8000 tokens, 32/8 heads,
-// 88 us, 5.1 TB/s (loads alone, without products: 75 us; the rest is the segments' ends); 3 of 65536-131072 tokens, 40/8
-// heads, 97 us, 6.1 TB/s; one of 1000 tokens 9.6 us, a chain of dependent accesses as in K10.
+// 90 us, 5.0 TB/s (loads alone, without products: 75 us; the rest is the segments' ends; l out of the weights: 88 us); 3 of
+// 65536-131072 tokens, 40/8 heads, 98 us, 6.1 TB/s; one of 1000 tokens 9.3 us, a chain of dependent accesses as in K10.
 #include "lola_codes.cuh"
 #include "lola_paged.cuh"
 
@@ -43,6 +46,8 @@ __device__ __forceinline__ uint32_t turned(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
+
+constexpr float kNone = -3.0e38f;       // below any score (QZ: in place of an infinity, which differences would have to avoid)
 
 // T: the cache's numbers (bfloat16, or uint8_t: e4m3).  NB: query rows in eights.
 template <typename T, typename TO, int D, int NB> struct TSmem {
@@ -184,12 +189,14 @@ __global__ void __launch_bounds__(TSmem<T, TO, D, NB>::kAll * kWarp, 1) decode_t
         __syncwarp();
         if (lane == 0) mbar_arrive1(smem_u32(&bars.seg_empty[slot]));   // (g and the Q rows are in registers)
         // o: channels 16 y + 2 g8 (0, 1) and + 1 (2, 3), or (bfloat16) + g8 and + 8 + g8; rows 8 b + q2 and + 1
+        // ml: what l is kept against (QZ)
         float o[D / 16][NB][4], m[NB][2], l[NB][2];
+        [[maybe_unused]] float ml[NB][2];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                m[b][e] = -INFINITY;
+                m[b][e] = ml[b][e] = QZ ? kNone : -INFINITY;
                 l[b][e] = 0.f;
             }
 #pragma unroll
@@ -238,24 +245,21 @@ __global__ void __launch_bounds__(TSmem<T, TO, D, NB>::kAll * kWarp, 1) decode_t
                         for (int b = 0; b < NB; ++b) mma16816(y & 1 ? c1[b] : c0[b], ka, qa[b][y][0], qa[b][y][1]);
                     }
                 }
-                // ---- scores and (e4m3) exponents of the weights: tokens k0 + g8 (0, 1), + 8 (2, 3) ----
-                float sc[NB][4];
-                [[maybe_unused]] float down[2];
+                // ---- scores, and (e4m3) what the weights' exponents have besides: tokens k0 + g8 (0, 1), + 8 (2, 3) ----
+                float sc[NB][4], fv[2] = {0.f, 0.f};
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    float fk = 1.f, fv = 0.f;
+                    float fk = 1.f;
                     if constexpr (QZ) {
-                        const uint32_t kp = powers[k0 + 8 * y], vp = powers[C::kTokens + k0 + 8 * y];
-                        fk = __uint_as_float(kp << 23);
-                        fv = (float)(int)vp - 127.f;
-                        down[y] = power_down(vp);
+                        fk = __uint_as_float((uint32_t)powers[k0 + 8 * y] << 23);
+                        fv[y] = (float)(int)powers[C::kTokens + k0 + 8 * y] - 127.f;
                     }
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const float z = (c0[b][2 * y + e] + c1[b][2 * y + e]) * qs[b][e];
-                            sc[b][2 * y + e] = QZ ? fmaf(z, fk, fv) : z;
+                            sc[b][2 * y + e] = QZ ? z * fk : z;
                         }
                 }
                 if (left < k0 + 16 || bad) {
@@ -281,18 +285,27 @@ __global__ void __launch_bounds__(TSmem<T, TO, D, NB>::kAll * kWarp, 1) decode_t
                     float top[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        top[e] = fmaxf(sc[b][e], sc[b][2 + e]);
+                        top[e] = QZ ? fmaxf(sc[b][e] + fv[0], sc[b][2 + e] + fv[1]) : fmaxf(sc[b][e], sc[b][2 + e]);
 #pragma unroll
                         for (int z = 4; z < kWarp; z <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], z));
                         top[e] += kRaise;
                     }
                     const bool need[2] = {top[0] > m[b][0] + kRaise, top[1] > m[b][1] + kRaise};
-                    if (__any_sync(0xffffffffu, need[0] || need[1])) {
+                    // (QZ: the lane's own scores)
+                    const float own[2] = {fmaxf(sc[b][0], sc[b][2]), fmaxf(sc[b][1], sc[b][3])};
+                    const bool more = QZ && (own[0] > ml[b][0] || own[1] > ml[b][1]);
+                    if (__any_sync(0xffffffffu, need[0] || need[1] || more)) {
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const float f = need[e] ? ex2(m[b][e] - top[e]) : 1.f;
                             if (need[e]) m[b][e] = top[e];
-                            l[b][e] *= f;
+                            if constexpr (QZ) {
+                                const float now = own[e] > ml[b][e] ? own[e] + kRaise : ml[b][e];
+                                l[b][e] *= ex2(ml[b][e] - now);
+                                ml[b][e] = now;
+                            } else {
+                                l[b][e] *= f;
+                            }
 #pragma unroll
                             for (int y = 0; y < D / 16; ++y) {
                                 o[y][b][e] *= f;
@@ -304,11 +317,11 @@ __global__ void __launch_bounds__(TSmem<T, TO, D, NB>::kAll * kWarp, 1) decode_t
 #pragma unroll
                     for (int z = 0; z < 4; ++z) {
                         const int e = z & 1;
-                        w[z] = ex2(sc[b][z] - (m[b][e] == -INFINITY ? 0.f : m[b][e]));
                         if constexpr (QZ) {
-                            l[b][e] = fmaf(w[z], down[z >> 1], l[b][e]);
-                            w[z] *= kUp;
+                            w[z] = ex2(sc[b][z] + fv[z >> 1] + (kUpBits - m[b][e]));
+                            l[b][e] += ex2(sc[b][z] - ml[b][e]);
                         } else {
+                            w[z] = ex2(sc[b][z] - (m[b][e] == -INFINITY ? 0.f : m[b][e]));
                             l[b][e] += w[z];
                         }
                     }
@@ -361,10 +374,18 @@ __global__ void __launch_bounds__(TSmem<T, TO, D, NB>::kAll * kWarp, 1) decode_t
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+                float top = m[b][e];
+                if constexpr (QZ) {
+                    top = ml[b][e];
+#pragma unroll
+                    for (int z = 4; z < kWarp; z <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, z));
+                    l[b][e] *= ex2(ml[b][e] - top);
+                    top = top == kNone ? -INFINITY : top;
+                }
 #pragma unroll
                 for (int z = 4; z < kWarp; z <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], z);
                 if (g8 == 0) {
-                    x.ms[grp][w4][8 * b + q2 + e] = m[b][e];
+                    x.ms[grp][w4][8 * b + q2 + e] = top;
                     x.ls[grp][w4][8 * b + q2 + e] = l[b][e];
                 }
             }
@@ -377,7 +398,9 @@ __global__ void __launch_bounds__(TSmem<T, TO, D, NB>::kAll * kWarp, 1) decode_t
                 float mm = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < 4; ++w) mm = fmaxf(mm, x.ms[grp][w][8 * b + q2 + e]);
-                f[b][e] = ex2(m[b][e] - (mm == -INFINITY ? 0.f : mm)) * (QZ ? 1.f / kUp : 1.f);
+                // (QZ: 2^{m - mm} / kUp, which may be far from one, by its square root)
+                const float to = m[b][e] - (mm == -INFINITY ? 0.f : mm);
+                f[b][e] = QZ ? ex2(0.5f * (to - kUpBits)) : ex2(to);
             }
         float* rec = segment_record<D, SH>(a, g);
         const int er = 4 * gt / CK, ec = 4 * gt % CK;                          // 128 threads x 4 columns = 8 NB x CK
@@ -398,7 +421,7 @@ __global__ void __launch_bounds__(TSmem<T, TO, D, NB>::kAll * kWarp, 1) decode_t
                         const float(&z)[4] = o[c / 16 + y][b];
                         float* to = &x.red[grp][w4][8 * b + q2 + e][16 * y];
                         if constexpr (QZ) {
-                            *reinterpret_cast<float2*>(to + 2 * g8) = make_float2(z[e] * f[b][e], z[2 + e] * f[b][e]);
+                            *reinterpret_cast<float2*>(to + 2 * g8) = make_float2(z[e] * f[b][e] * f[b][e], z[2 + e] * f[b][e] * f[b][e]);
                         } else {
                             to[g8] = z[e] * f[b][e];
                             to[8 + g8] = z[2 + e] * f[b][e];

@@ -85,3 +85,123 @@ def test_pieces_that_begin_at_an_items_last_block(L, gen, quant, d, Hq, Hkv, pre
         assert torch.equal(out, lay.decode_shared(q, *s.args()))
     quiet(L)
     s.check(q, out)
+
+
+# ---------------------------------------------------------------------------------------
+# powers of two that lie far apart
+# ---------------------------------------------------------------------------------------
+# A row's numbers and its power of two enter the products exactly, whatever the powers of other rows are.  What is left:
+# float32 products (attn_parity's ds), q to 2^-39 of its row's largest number, weights of 11 bits (22 in float32 io) or,
+# where they are small, to 2^-25 in the unit in which the largest of p_j 2^f_j (f_j: a value row's power) is at least 2^-1:
+# it is kept times 2^15 below a maximum of 2^0, which is at most 8 bits above the blocks' maxima, and those 8 above the
+# rows' where a block is taken as one.  Codes are at most 448 and a row's largest one at least 224: 2^-23 of the
+# largest p_j max|v_j| a key (rows of zeros have no error).  Everything is relative to what the row sees with its weights.
+
+def check_apart(q, k, v, out, lse, codes_most=448 / 224, what=""):
+    Hq, d = q.shape
+    c, u = 1 / math.sqrt(d), {BF: 2.0 ** -8, F32: 2.0 ** -24}[q.dtype]
+    weights = {BF: 2.0 ** -11, F32: 2.0 ** -22}[q.dtype]
+    n = k.shape[0]
+    for h in range(Hq):
+        g = h * k.shape[1] // Hq
+        x, K, V = q[h].double(), k[:, g].double(), v[:, g].double()
+        s = c * (K @ x)
+        norm = torch.logsumexp(s, 0)
+        p = torch.exp(s - norm)
+        o, A = p @ V, p @ V.abs()
+        B = (p * V.abs().amax(-1)).amax()
+        # (a score counts as far as its weight does: 2^-40 of the largest is nothing)
+        near = p > 2.0 ** -60 * p.amax()
+        lost = 2.0 ** -38 * x.abs().amax() * (x != 0) if q.dtype == F32 else 0 * x      # (zeros, and bfloat16 numbers, whole)
+        ds = c * (K.abs() @ ((d + 4) * 2.0 ** -23 * x.abs() + lost))[near].amax() + 2.0 ** -22
+        if q.dtype == F32:
+            ds = ds + 2.0 ** -17                          # (s + f and m in float32, |f| < 2^7, in K11's exponents)
+        tol = u * o.abs() + (1 + u) * (2 * ds + weights + 2.0 ** -17 + (n + 8) * 2.0 ** -23) * A + n * codes_most * 2.0 ** -24 * B
+        err = (out[h].double() - o).abs()
+        assert bool(torch.isfinite(out[h]).all()), f"{what} head {h}: not finite"
+        worst = float((err / tol.clamp(min=1e-300)).max())
+        assert worst <= 1, f"{what} head {h}: {worst:.3g} of the bound"
+        if lse is not None:
+            assert abs(float(lse[h].double() - norm)) <= float(ds) + (n + 8) * 2.0 ** -23 + abs(float(norm)) * 2.0 ** -22, f"lse of {what} head {h}"
+
+
+def place(c, w, b, codes, power):
+    """Codes [n, Hkv, d] and biased powers [n, Hkv] of sequence b's rows, written as they are."""
+    pos = torch.arange(codes.shape[0], device="cuda")
+    at = c.table[b].long()[pos // c.page], pos % c.page
+    getattr(c, w + "_pool").view(torch.uint8)[at[0], :, at[1]] = codes.view(torch.uint8)
+    getattr(c, w + "_scale").view(torch.uint8)[at[0], :, at[1]] = power
+    getattr(c, w)[b] = codes.double() * 2.0 ** (power.double() - 127)[..., None]
+
+
+def far_apart(gen, c, kind, Hkv, d):
+    """Rewrites every sequence of the cache.  Queries have 0 in channel 0 and 8 in channel 1."""
+    for b, n in enumerate(c.lens):
+        pos = torch.arange(n, device="cuda")
+        k, v = randn(gen, n, Hkv, d, dtype=F32), randn(gen, n, Hkv, d, dtype=F32)
+        k[..., 1] = 0.0
+        unseen = torch.zeros(n, dtype=torch.bool, device="cuda")
+        if kind == "one value":                              # one row 2^30 times the others, without weight
+            unseen[n // 2:n // 2 + 1] = True
+            v[unseen] *= 2.0 ** 30
+        elif kind == "values":
+            unseen = pos % 50 == 7
+            v *= torch.exp2(torch.randint(-6, 3, (n, 1, 1), generator=gen, device="cuda").float())
+            v[unseen] *= torch.exp2(torch.randint(9, 60, (int(unseen.sum()), 1, 1), generator=gen, device="cuda").float())
+        elif kind == "keys":                                 # large in a channel that no query has
+            big = pos % 77 == 5
+            k[big] = 0.0
+            k[big, :, 0] = torch.exp2(torch.randint(12, 40, (int(big.sum()), 1), generator=gen, device="cuda").float())
+        elif kind == "zeros":                                # blocks of rows of zeros, and of large ones
+            v *= torch.where(pos // 128 % 2 == 0, 0.0, 2.0 ** 60)[:, None, None]
+        elif kind == "zero rows":
+            v *= torch.where(pos % 2 == 0, 0.0, 2.0 ** 45)[:, None, None]
+        elif kind == "apart":                                # small ones by blocks, and large ones, all of the same weight
+            v *= torch.where(pos // 128 % 3 == 0, 2.0 ** -85, 2.0 ** 50)[:, None, None]
+        k[unseen, :, 1] = -300.0
+        if kind == "high":                                   # the largest powers that a caller may write, of small codes
+            place(c, "v", b, v.clamp(-1, 1).to(torch.float8_e4m3fn), torch.full((n, Hkv), 254, dtype=torch.uint8, device="cuda"))
+        else:
+            c.v[b] = c.store("v", b, pos, v)
+        c.k[b] = c.store("k", b, pos, k)
+
+
+APART = ["one value", "values", "keys", "zeros", "zero rows", "apart", "high"]
+
+
+def apart_queries(gen, n, Hq, d, dtype):
+    q = randn(gen, n, Hq, d, dtype=dtype)
+    q[..., 0], q[..., 1] = 0.0, 8.0
+    return q
+
+
+@pytest.mark.parametrize("kind", APART)
+@pytest.mark.parametrize("dtype,d,Hq,Hkv", [(BF, 128, 8, 2), (BF, 64, 12, 1), (F32, 128, 4, 1), (F32, 64, 10, 1)])
+def test_decode_powers_far_apart(L, gen, dtype, d, Hq, Hkv, kind):
+    lens = [1500, 17, 300, 1]
+    c = QPaged(gen, lens, Hkv, d, 32, dtype)
+    far_apart(gen, c, kind, Hkv, d)
+    q = apart_queries(gen, len(lens), Hq, d, dtype)
+    lse = torch.empty(len(lens), Hq, dtype=F32, device="cuda")
+    out = c.layer(L, Hq, Hkv, d, dtype).decode_step(q, c.kv_len, c.table, lse=lse)
+    quiet(L)
+    for b in range(len(lens)):
+        check_apart(q[b], c.k[b], c.v[b], out[b], lse[b], 1 if kind == "high" else 2, f"sequence {b}")
+
+
+@pytest.mark.parametrize("kind", APART)
+@pytest.mark.parametrize("once", [False], ids=["few"])
+@pytest.mark.parametrize("dtype,d,Hq,Hkv,members", [(BF, 128, 8, 2, 5), (BF, 128, 8, 1, 40), (BF, 64, 12, 1, 9), (BF, 64, 12, 1, 30),
+                                                    (F32, 128, 4, 1, 5)])
+def test_shared_powers_far_apart(L, gen, dtype, d, Hq, Hkv, members, once, kind):
+    """Behind a prefix: rows of one tile and of two, both forms of the call."""
+    lens = [(i * 37) % 140 for i in range(members)]
+    s = Behind(gen, True, [2500], [members], lens, Hkv, d, 32, dtype, once)
+    far_apart(gen, s.c, kind, Hkv, d)
+    q = apart_queries(gen, members, Hq, d, dtype)
+    lse = torch.empty(members, Hq, dtype=F32, device="cuda")
+    out = s.layer(L, Hq, Hkv, d, dtype).decode_shared(q, *s.args(), lse=lse)
+    quiet(L)
+    for b in range(0, members, max(1, members // 6)):
+        k, v = (torch.cat([x[i] for x in s.parts(b)]) for i in (0, 1))
+        check_apart(q[b], k, v, out[b], lse[b], 1 if kind == "high" else 2, f"sequence {b}")
