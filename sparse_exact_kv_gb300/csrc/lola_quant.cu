@@ -10,8 +10,8 @@
 //   s_j = c 2^{e_j} q . code_j,   w_j = 2^{s_j + f_j - m},   O = sum_j w_j code'_j,   l = sum_j 2^{s_j - r},
 // m set above the largest s_j + f_j, r, a lane's own, above its largest s_j: everything but the exponentials, the weights'
 // rounding and the sums is exact, however far the powers lie apart (l as a sum of w_j 2^{-f_j} lost rows whose power is
-// 2^-110 of another's: of zeros, which have 2^-100, beside numbers of 2^20).  At a segment's end O comes to 2^{m - r}, and
-// from there on m and l are the scores'.
+// 2^-110 of another's: of zeros, which have 2^-100, beside numbers of 2^20).  At a segment's end O comes to 2^{m - r}, r
+// above all lanes' and with room for sums of large values (kRoom), and from there on m and l are the scores'.
 // q comes as float16 numbers of its row's own power of two (its largest number in [2^14, 2^15): a bfloat16 number
 // loses nothing down to 2^-28 of that; a float32 number is kept in two parts, to 2^-39 of it), the weights as
 // float16 numbers of 2^15 w_j (rounded by 2^-12 of themselves, or by 2^-40 where they are small; float32 io: two parts).
@@ -379,8 +379,8 @@ __global__ void __launch_bounds__(TSmem<T, TO, D, NB>::kAll * kWarp, 1) decode_t
                     top = ml[b][e];
 #pragma unroll
                     for (int z = 4; z < kWarp; z <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, z));
-                    l[b][e] *= ex2(ml[b][e] - top);
-                    top = top == kNone ? -INFINITY : top;
+                    l[b][e] *= ex2(ml[b][e] - top - kRoom);
+                    top = top == kNone ? -INFINITY : top + kRoom;
                 }
 #pragma unroll
                 for (int z = 4; z < kWarp; z <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], z);
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(TSmem<T, TO, D, NB>::kAll * kWarp, 1) decode_t
                 float mm = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < 4; ++w) mm = fmaxf(mm, x.ms[grp][w][8 * b + q2 + e]);
-                // (QZ: 2^{m - mm} / kUp, which may be far from one, by its square root)
+                // (QZ: 2^{m - 15 - mm}, which may be far from one, by its square root)
                 const float to = m[b][e] - (mm == -INFINITY ? 0.f : mm);
                 f[b][e] = QZ ? ex2(0.5f * (to - kUpBits)) : ex2(to);
             }

@@ -158,6 +158,8 @@ def far_apart(gen, c, kind, Hkv, d):
             v *= torch.where(pos % 2 == 0, 0.0, 2.0 ** 45)[:, None, None]
         elif kind == "apart":                                # small ones by blocks, and large ones, all of the same weight
             v *= torch.where(pos // 128 % 3 == 0, 2.0 ** -85, 2.0 ** 50)[:, None, None]
+        elif kind == "top":                                  # sums far behind float32's range, means that are in it
+            v = 2.5e38 + 0.4e38 * torch.rand(v.shape, generator=gen, device="cuda")
         k[unseen, :, 1] = -300.0
         if kind == "high":                                   # the largest powers that a caller may write, of small codes
             place(c, "v", b, v.clamp(-1, 1).to(torch.float8_e4m3fn), torch.full((n, Hkv), 254, dtype=torch.uint8, device="cuda"))
@@ -166,7 +168,7 @@ def far_apart(gen, c, kind, Hkv, d):
         c.k[b] = c.store("k", b, pos, k)
 
 
-APART = ["one value", "values", "keys", "zeros", "zero rows", "apart", "high"]
+APART = ["one value", "values", "keys", "zeros", "zero rows", "apart", "high", "top"]
 
 
 def apart_queries(gen, n, Hq, d, dtype):
