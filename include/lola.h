@@ -518,9 +518,10 @@ int32_t lola_quant_read(const lola_attn_config* cfg, const lola_paged_kv* kv, co
                         const lola_rows* K, const lola_rows* V, int32_t* cu, void* stream);
 
 /* lola_paged_decode over a quantised cache: the same arguments, workspace and rules.  Codes and powers enter the
- * products exactly.  With bfloat16 io q keeps all its bits down to 2^-28 of its row's largest number, and the weights
- * are rounded to 11 bits; with float32 io both are good to float32's own rounding of the row's largest.  |q_i| is at
- * most 2^100. */
+ * products exactly, however far rows' powers lie apart.  With bfloat16 io q keeps all its bits down to 2^-28 of its
+ * row's largest number, and the weights are rounded to 11 bits (small ones to 2^-32 of the largest product of a weight and
+ * its value's power, behind a prefix that is read once for all to 2^-24 of it); with float32 io both are good to float32's
+ * own rounding of the row's largest.  |q_i| is at most 2^100. */
 int32_t lola_quant_decode(const lola_attn_config* cfg, const lola_paged_kv* kv, const lola_kv_scales* scales, const lola_rows* Q,
                           const lola_rows* O, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 

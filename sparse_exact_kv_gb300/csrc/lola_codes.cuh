@@ -16,10 +16,8 @@ __device__ __forceinline__ uint32_t half2_of(float x, float y) {
     const __half2 h = __floats2half2_rn(x, y);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-// 2^(127 - b) for a byte b < 255 (2^-127, of b = 254, is no normal number)
-__device__ __forceinline__ float power_down(uint32_t b) { return __uint_as_float(b < 254u ? (254u - b) << 23 : 0x400000u); }
 
-constexpr float kUpBits = 15.f, kUp = 32768.f;            // the weights' factor 2^15
+constexpr float kUpBits = 15.f;           // the weights' factor: 2^15
 // Parts of softmaxes are left against 2^20 times the largest score's weight: sums of that many values of float32's largest
 // size stay in its range, and means of rows of the smallest powers, 2^-100, nearly all their bits.
 constexpr float kRoom = 20.f;

@@ -13,11 +13,13 @@
 // softmax runs beside the other's products, and the halves are added at the segment's end.
 // Warps: 0-3, 4-7 softmax of tile 0, 1 (one thread per row: Q rows to shared memory, S into registers, maximum, weights, P
 // into TMEM over S, at the end O out of TMEM); 8 products (one thread); 9 pages and loads, a ring of K and V blocks.
-// QZ, a quantised cache: the ring's blocks are written by warps 12-15 (or, by turns, 12-15 and 16-19), as float16 numbers code 2^(e - E), from e4m3 numbers
-// and powers of two that a second ring brings; E is the block's largest power, of its keys or of its values (numbers 2^-33
-// and less of the largest one that these may hold round or vanish: as small against the block's scores, or outputs, as
-// float32's own rounding).  A key's 2^E is a factor of the scores, a value's joins the weights' exponent, as in
-// lola_quant.cu, from where the rows of Q with powers of two of their own and the weights times 2^15 come too.
+// QZ, a quantised cache: the ring's blocks are written by warps 12-15 (or, by turns, 12-15 and 16-19), as float16 numbers,
+// from e4m3 numbers and powers of two that a second ring brings.  Where the powers of a block's keys, or of its values, lie
+// close together (kApart), the numbers are code 2^(e - E), E the largest of them, exactly; a key's 2^E is a factor of the
+// block's scores, a value's joins the weights' exponent.  Else they are the codes as they stand, and the softmax takes every
+// token's powers out of a table in shared memory: score by score, a branch that blocks of the other kind pass by.  So no row
+// costs others their bits, whatever its power and its weight.  The rows of Q with powers of two of their own, the weights
+// times 2^15, and l in the scores' unit, apart from the weights', are lola_quant.cu's.
 // (Blocks of bfloat16 numbers code 2^e, by shifts, two products a pair and a look for NaN, took the four warps 3.4 us for
 // K and V.)
 // m is raised lazily, as in lola_attn_tc.cu: it is set 8 above a maximum, so that no weight is above one.
@@ -40,7 +42,15 @@ constexpr int kN = 128;                  // keys of a block
 constexpr int kItem = kPrefixRows;       // rows of an item: two tiles
 static_assert(kItem == 2 * kM, "two tiles");
 constexpr int kBad = 8;                  // blocks whose pages and powers are remembered: more than the loader is ahead
-constexpr float kWeightBits = 15.f;      // QZ: weights are kept times kUp
+// QZ: how far a block's powers lie apart at most to enter its numbers.  Keys: code 2^-15 is still a multiple of 2^-24, which
+// float16 has.  Values: m is set above a block's largest score and largest power, which may be different tokens'; the
+// largest weight is then 2^-16 at least, 2^-8 for that and 2^-8 for m's own distance, and weights keep their 11 bits down
+// to 2^-13 of it (2^-29, below which float16 numbers of 2^15 w have fewer).
+constexpr int kApartKeys = 15, kApartValues = 8;
+// Blocks whose tokens' powers are kept, converted and not yet weighed: without block j's weights its V stays in the ring, and
+// the conversion comes kRing - 1 stages, two key blocks (two tiles) or three (one: V of j is stage 2 j + 2), further.
+constexpr int kTables = 4;
+constexpr int kTableBytes = 2 * kN;
 
 // CV: groups of four converting warps.
 template <int D, bool QZ, int CV> struct PCfg {
@@ -50,8 +60,11 @@ template <int D, bool QZ, int CV> struct PCfg {
     static constexpr int kRing = D == 128 ? (QZ ? 3 : 5) : (QZ ? 4 : 8);
     static constexpr int kRaw = QZ ? (D == 128 ? 4 : 8) : 1;            // blocks of codes (K or V)
     static constexpr int kRawBytes = QZ ? kN * D + 2 * kN : 0;         // codes, their powers, behind keys the values' powers too
-    static constexpr int kSmem = (2 + kRing) * kTileBytes + kRaw * kRawBytes + 1024;
-    // Registers of a softmax thread and of the others: what the block was launched with, 168 or 128 a thread, given out
+    // (behind that: QZ the tables, else what aligning takes)
+    static constexpr int kTableAt = (2 + kRing) * kTileBytes + kRaw * kRawBytes;
+    static constexpr int kSmem = kTableAt + 1024;
+    static_assert(kTables * kTableBytes <= 1024, "tables");
+    // Registers of a softmax thread and of the others: what the block was launched with, 168, 128 or 96 a thread, given out
     // anew, so that a row's 128 scores fit.  QZ at d = 64: the scores come first here too (64 sequences behind 64000 tokens,
     // 32/8 heads: 60 us, 68 with 128 and 128).
     static constexpr int kSoftmaxRegs = QZ ? (D == 128 ? 128 : 192) : 208, kOtherRegs = QZ ? (D == 64 ? 64 : CV == 2 ? 72 : 128) : 88;
@@ -74,6 +87,99 @@ struct PSeg {
     int whole, k, np, rec;     // as in Seg; rec: the item's first record
 };
 
+// Which of columns x0 .. x0 + 31 of a block are tokens that are seen.
+__device__ __forceinline__ uint32_t seen_columns(int x0, int valid, uint32_t bad, int lb) {
+    uint32_t seen = valid >= x0 + 32 ? ~0u : valid <= x0 ? 0u : (1u << (valid - x0)) - 1u;
+    for (int x = 0; x < 32; x += 1 << min(lb, 5))
+        if ((bad >> ((x0 + x) >> lb)) & 1u) seen &= lb >= 5 ? 0u : ~(((1u << (1 << lb)) - 1u) << x);
+    return seen;
+}
+
+// The row's outputs, `width` columns from `to` on, times f.
+__device__ __forceinline__ void scale_output(uint32_t to, int width, float f) {
+#pragma unroll 1
+    for (int x = 0; x < width; x += 16) {
+        uint32_t o[16];
+        tmem_ld16(to + x, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+        tmem_st16(to + x, o);
+    }
+}
+// QZ, a block whose powers lie too far apart: a row's softmax score by score, m, l and ml before and after it in x.  (A call,
+// so that these blocks' code costs the others no registers.)
+struct ByToken {
+    uint32_t ts, to, table, bad;  // TMEM: S, O; shared memory: 128 powers of the keys, 128 of the values (biased)
+    float c;
+    int valid, lb, width;
+};
+__device__ __forceinline__ uint32_t table_word(uint32_t at) {
+    uint32_t w;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(at));
+    return w;
+}
+// columns x0 .. x0 + 31: scores, minus infinity for tokens that are not seen; and the values' powers, which their weights'
+// exponents have besides
+__device__ __forceinline__ void token_scores(const ByToken& t, int x0, float (&s)[32]) {
+    tmem_ld32(t.ts + x0, s);
+    tmem_wait_ld();
+    const uint32_t seen = seen_columns(x0, t.valid, t.bad, t.lb);
+#pragma unroll
+    for (int x = 0; x < 32; x += 4) {
+        const uint32_t w = table_word(t.table + x0 + x);
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+            s[x + y] = (seen >> (x + y)) & 1u ? s[x + y] * t.c * __uint_as_float(((w >> (8 * y)) & 255u) << 23) : -INFINITY;
+    }
+}
+__device__ __forceinline__ void token_powers(const ByToken& t, int x0, float (&s)[32]) {
+#pragma unroll
+    for (int x = 0; x < 32; x += 4) {
+        const uint32_t w = table_word(t.table + kN + x0 + x);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) s[x + y] += (float)(int)((w >> (8 * y)) & 255u) - 127.f;
+    }
+}
+__device__ __noinline__ float3 by_token_block(const ByToken t, bool first, float3 x) {
+    float m = x.x, l = x.y, high = x.z, top = -INFINITY;
+#pragma unroll 1
+    for (int x0 = 0; x0 < kN; x0 += 32) {
+        float s[32], now = high;
+        token_scores(t, x0, s);
+#pragma unroll
+        for (int y = 0; y < 32; ++y) now = fmaxf(now, s[y]);
+        const float r = now == -INFINITY ? 0.f : now;
+        l *= ex2(high - r);
+#pragma unroll
+        for (int y = 0; y < 32; ++y) l += ex2(s[y] - r);
+        high = now;
+        token_powers(t, x0, s);
+#pragma unroll
+        for (int y = 0; y < 32; ++y) top = fmaxf(top, s[y]);
+    }
+    top += kRaise;
+    const bool need = top > m + kRaise;
+    if (first) {
+        m = top;
+    } else if (__any_sync(0xffffffffu, need)) {
+        scale_output(t.to, t.width, need ? ex2(m - top) : 1.f);
+        if (need) m = top;
+    }
+    const float off = kUpBits - (m == -INFINITY ? 0.f : m);
+#pragma unroll 1
+    for (int x0 = 0; x0 < kN; x0 += 32) {
+        float s[32];
+        token_scores(t, x0, s);
+        token_powers(t, x0, s);
+        uint32_t w[16];
+#pragma unroll
+        for (int y = 0; y < 16; ++y) w[y] = half2_of(ex2(s[2 * y] + off), ex2(s[2 * y + 1] + off));
+        tmem_st16(t.ts + x0 / 2, w);
+    }
+    return make_float3(m, l, high);
+}
+
 template <int D, bool QZ, int CV>
 __global__ void __launch_bounds__(PCfg<D, QZ, CV>::kThreads, 1) prefix_tc_kernel(const __grid_constant__ Maps maps, const Args a) {
     using C = PCfg<D, QZ, CV>;
@@ -81,6 +187,11 @@ __global__ void __launch_bounds__(PCfg<D, QZ, CV>::kThreads, 1) prefix_tc_kernel
     extern __shared__ __align__(1024) uint8_t smraw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(sm);
+    // (QZ: the array's own alignment leaves the last 1024 bytes to the tables)
+    if (QZ && sm != smraw) {
+        if (threadIdx.x == 0) atomicOr(&g_status, (int)LOLA_ATTN_TIMEOUT);
+        return;
+    }
     enum {
         B_SEG = 0, B_SEGFREE = 2, B_Q = 4, B_S = 6, B_P = 8, B_O = 10, B_ML = 12, B_READ, B_DONE, B_FULL,
         B_EMPTY = B_FULL + kRing, B_RFULL = B_EMPTY + kRing, B_REMPTY = B_RFULL + kRaw, B_N = B_REMPTY + kRaw
@@ -88,7 +199,8 @@ __global__ void __launch_bounds__(PCfg<D, QZ, CV>::kThreads, 1) prefix_tc_kernel
     __shared__ __align__(8) uint64_t bars[B_N];
     __shared__ PSeg segs[2];
     __shared__ uint32_t tmem_base, bad_sm[kBad];
-    __shared__ uint32_t power_sm[kBad];      // QZ: the largest powers of a block's keys and values (biased; in the second byte)
+    // QZ: the largest powers of a block's keys and values (biased; in the second byte), and whether its tokens' are in a table
+    __shared__ uint32_t power_sm[kBad];
     __shared__ int4 raw_sm[kRaw];            // of a raw block: tokens (< 0: no more blocks), bad boxes, the block's number (>= 0: keys)
     __shared__ int abort_sm;
     const PagedArgs& p = a.p;
@@ -387,6 +499,9 @@ __global__ void __launch_bounds__(PCfg<D, QZ, CV>::kThreads, 1) prefix_tc_kernel
         } else if (QZ && warp >= C::kConvWarp) {
             // ================================ codes to float16 ================================
             const int t = tid & 127;
+            // CV == 1: of the blocks (two at most) whose keys are converted and whose values are not, the oldest first: largest
+            // power of the values, whether they lie apart, 512
+            uint32_t values = 0u;
             for (int n = CV == 1 ? 0 : (warp - C::kConvWarp) >> 2;; n += CV) {
                 const int r = n % kRaw, s = n % kRing;
                 if (!wait_all(B_RFULL + r, (uint32_t)(n / kRaw))) break;
@@ -398,28 +513,54 @@ __global__ void __launch_bounds__(PCfg<D, QZ, CV>::kThreads, 1) prefix_tc_kernel
                 const int lb = 31 - __clz(min(p.page, kN));
                 const bool some = info.x < kN || info.y;
                 auto hidden = [&](int k) { return k >= info.x || (info.y >> (k >> lb)) & 1; };
-                // the largest of 128 powers, of tokens that are seen
-                auto largest = [&](const uint8_t* powers) {
-                    uint32_t w = *reinterpret_cast<const uint32_t*>(powers + 4 * lane);
+                // the largest of 128 powers, of tokens that are seen, and whether others are further below it than `most`
+                struct Range {
+                    uint32_t top;
+                    bool wide;
+                };
+                auto range = [&](const uint8_t* powers, int most) {
+                    const uint32_t w = *reinterpret_cast<const uint32_t*>(powers + 4 * lane);
+                    auto largest = [](uint32_t x) { return max(max(x & 255u, (x >> 8) & 255u), max((x >> 16) & 255u, x >> 24)); };
+                    auto smallest = [](uint32_t x) { return min(min(x & 255u, (x >> 8) & 255u), min((x >> 16) & 255u, x >> 24)); };
+                    uint32_t hi = largest(w), lo = smallest(w);
                     if (some) {
                         const int left = info.x - 4 * lane;
-                        if (hidden(4 * lane)) w = 0;
-                        else if (left < 4) w &= (1u << (8 * left)) - 1u;
+                        const uint32_t seen = hidden(4 * lane) ? 0u : left < 4 ? (1u << (8 * left)) - 1u : ~0u;
+                        hi = largest(w & seen);
+                        lo = smallest(w | ~seen);
                     }
-                    return __reduce_max_sync(0xffffffffu, max(max(w & 255u, (w >> 8) & 255u), max((w >> 16) & 255u, w >> 24)));
+                    hi = __reduce_max_sync(0xffffffffu, hi);
+                    return Range{hi, (bool)__any_sync(0xffffffffu, (int)(hi - lo) > most)};
                 };
-                const uint32_t E = largest(raw + kN * D);
+                Range E;
+                if (info.w && CV == 1) {
+                    // (these four warps have converted the block's keys, in the same order as the values)
+                    E = Range{values & 255u, (bool)(values & 256u)};
+                    values >>= 16;
+                } else {
+                    E = range(raw + kN * D, info.w ? kApartValues : kApartKeys);
+                }
                 if (!info.w) {
-                    const uint32_t F = largest(raw + kN * (D + 1));
-                    if (t == 0) power_sm[info.z % kBad] = E | F << 8;
+                    const Range F = range(raw + kN * (D + 1), kApartValues);
+                    const bool table = E.wide || F.wide;
+                    if (t == 0) power_sm[info.z % kBad] = E.top | F.top << 8 | (uint32_t)table << 16;
+                    if (table && t < kWarp) {
+                        // (powers that the block's numbers do not have in them)
+                        uint32_t* to = reinterpret_cast<uint32_t*>(sm + C::kTableAt + info.z % kTables * kTableBytes) + lane;
+                        to[0] = E.wide ? *reinterpret_cast<const uint32_t*>(raw + kN * D + 4 * lane) : E.top * 0x01010101u;
+                        to[kN / 4] = F.wide ? *reinterpret_cast<const uint32_t*>(raw + kN * (D + 1) + 4 * lane) : F.top * 0x01010101u;
+                    }
+                    const uint32_t next = F.top | (uint32_t)F.wide << 8 | 512u;
+                    values = values & 512u ? values & 0xffffu | next << 16 : next;
                 }
                 // 16 codes a thread: CH such chunks a token, a warp takes PT tokens of every 128 / CH.  Each lane finds one
-                // token's factor, 2^(e - E) in float16: down to 2^-14, then to 2^-24, then none.  (Loads before stores, which
-                // might be the same place for all the compiler knows: a block took one warp a scheduler 1190 clocks, now 560.)
+                // token's factor, 2^(e - E) in float16: down to 2^-14, then 2^-15.  (Loads before stores, which might be the same
+                // place for all the compiler knows: a block took one warp a scheduler 1190 clocks, now 560.)
                 constexpr int CH = D / 16, PT = 32 / CH, kBatch = 4;
                 const int own = 128 / CH * (lane / PT) + PT * (warp & 3) + lane % PT;
-                const int down = max(0, (int)E - (int)raw[kN * D + own]);
-                const uint32_t factor = (down < 15 ? (15u - down) << 10 : down < 25 ? 1u << (24 - down) : 0u) * 0x10001u;
+                // (of tokens that are not seen: anything)
+                const int down = E.wide ? 0 : min(max(0, (int)E.top - (int)raw[kN * D + own]), 15);
+                const uint32_t factor = (down < 15 ? (15u - down) << 10 : 1u << 9) * 0x10001u;
 #pragma unroll
                 for (int x0 = 0; x0 < CH; x0 += kBatch) {
                     uint4 w[kBatch];
@@ -507,6 +648,7 @@ __global__ void __launch_bounds__(PCfg<D, QZ, CV>::kThreads, 1) prefix_tc_kernel
                 if (lane == 0) mbar_arrive1(bar(B_Q + i));
             }
             float m = -INFINITY, l = 0.f;
+            [[maybe_unused]] float ml = -INFINITY;                              // QZ: the largest score, against which l is kept
             bool ok = true;
             for (int jj = 0; jj < n && ok; ++jj) {
                 const int j = two ? jj : 2 * jj + i;
@@ -522,12 +664,27 @@ __global__ void __launch_bounds__(PCfg<D, QZ, CV>::kThreads, 1) prefix_tc_kernel
                 auto hide = [&](int at, int x0) {
                     if (!some) return;
                     asm volatile("" ::: "memory");
-                    uint32_t seen = valid >= x0 + 32 ? ~0u : valid <= x0 ? 0u : (1u << (valid - x0)) - 1u;
-                    for (int x = 0; x < 32; x += 1 << min(lb, 5))
-                        if ((bad >> ((x0 + x) >> lb)) & 1u) seen &= lb >= 5 ? 0u : ~(((1u << (1 << lb)) - 1u) << x);
+                    const uint32_t seen = seen_columns(x0, valid, bad, lb);
 #pragma unroll
                     for (int x = 0; x < 32; ++x) s[at + x] = (seen >> x) & 1u ? s[at + x] : -INFINITY;
                 };
+                auto weighed = [&] {
+                    tmem_wait_st();
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive1(bar(B_P + i));
+                };
+                [[maybe_unused]] uint32_t powers = 0u;
+                if constexpr (QZ) {
+                    powers = power_sm[(g.blk0 + j) % kBad];
+                    if (powers >> 16) {
+                        const uint32_t table = sb + C::kTableAt + (uint32_t)((g.blk0 + j) % kTables) * kTableBytes;
+                        const float3 x = by_token_block(ByToken{ts, to, table, bad, c, valid, lb, D}, jj == 0, make_float3(m, l, ml));
+                        m = x.x, l = x.y, ml = x.z;
+                        weighed();
+                        continue;
+                    }
+                }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
                 for (int x0 = kN - kHeld; x0 >= 0; x0 -= kHeld) {
@@ -550,35 +707,29 @@ __global__ void __launch_bounds__(PCfg<D, QZ, CV>::kThreads, 1) prefix_tc_kernel
                 }
                 // the scores' factor, and what their weights' exponents have besides
                 float cb = c, add = 0.f;
-                [[maybe_unused]] uint32_t F = 127u;
+                const float largest = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 if constexpr (QZ) {
-                    const uint32_t powers = power_sm[(g.blk0 + j) % kBad];
-                    F = powers >> 8;
-                    cb = fmaxf(c * __uint_as_float((powers & 255u) << 23), 1.2e-38f);     // (0 would make NaN of hidden scores)
-                    add = (float)(int)F - 127.f;
+                    // (0 would make NaN of hidden scores, an infinity of those that are 0)
+                    cb = fminf(fmaxf(c * __uint_as_float((powers & 255u) << 23), 1.2e-38f), 3.0e38f);
+                    add = (float)(int)(powers >> 8) - 127.f;
                 }
-                const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), cb, add + kRaise);
+                const float top = fmaf(largest, cb, add + kRaise);
                 const bool need = top > m + kRaise;
                 if (jj == 0) {
                     m = top;
                 } else if (__any_sync(0xffffffffu, need)) {
                     // (O is quiet: S of this block was issued behind the tile's last P V, and is done)
                     const float f = need ? ex2(m - top) : 1.f;
-                    l *= f;
-#pragma unroll 1
-                    for (int x = 0; x < D; x += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(to + x, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-                        tmem_st16(to + x, o);
-                    }
+                    if (!QZ) l *= f;
+                    scale_output(to, D, f);
                     if (need) m = top;
                 }
                 const float base = m == -INFINITY ? 0.f : m;
                 float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                const float off = QZ ? add + kWeightBits - base : -base;
+                float off = QZ ? add + kUpBits - base : -base;
+                // (QZ: a block whose weights are nothing beside m still counts in l: numbers that float16 takes to 0)
+                const float high = largest * cb;
+                if (QZ && high + add < base - 60.f && high > -INFINITY) off = -high - 40.f;
                 const float2 c2 = make_float2(cb, cb), b2 = make_float2(off, off);
                 // weights of the 32 scores in s[at ..], columns x on, over the scores
                 auto weigh = [&](int at, int x) {
@@ -608,11 +759,15 @@ __global__ void __launch_bounds__(PCfg<D, QZ, CV>::kThreads, 1) prefix_tc_kernel
                     for (int x = 0; x < kN; x += 32) weigh(x, x);
                 }
                 const float sum = (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
-                l = QZ ? fmaf(sum, power_down(F) * (1.f / kUp), l) : l + sum;
-                tmem_wait_st();
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive1(bar(B_P + i));
+                if constexpr (QZ) {
+                    const float now = fmaxf(ml, high), r = now == -INFINITY ? 0.f : now;
+                    l *= ex2(ml - r);
+                    if (sum != 0.f) l = fmaf(sum, ex2(-off - r), l);
+                    ml = now;
+                } else {
+                    l += sum;
+                }
+                weighed();
             }
             // ---- the segment's part: for the row, m, l and O ----
             if (n > 0 && ok) ok = wait_all(B_O + i, (uint32_t)no);
@@ -620,24 +775,45 @@ __global__ void __launch_bounds__(PCfg<D, QZ, CV>::kThreads, 1) prefix_tc_kernel
             fence_after();
             ns += n;
             no += n > 0;
-            constexpr float kDown = QZ ? 1.f / kUp : 1.f;
-            float f0 = kDown, f1 = 0.f;
-            if (pair) {
-                // both halves' m and l, in the place of their Q rows
+            // QZ: O is in the weights' unit, 2^{m - 15}, l in the scores', 2^ml: the factor from one to the other, which may be
+            // far from one, by its square root
+            [[maybe_unused]] auto root = [](float m, float ml) {
+                return m == -INFINITY ? 0.f : ex2(0.5f * (m - kUpBits - (ml == -INFINITY ? 0.f : ml)));
+            };
+            float f0 = QZ ? root(m, ml + kRoom) : 1.f, f1 = 0.f;
+            if constexpr (QZ) {
+                if (pair) {
+                    // both halves' m and l, in the place of their Q rows
+                    reinterpret_cast<float4*>(Qt)[r] = make_float4(m, l, ml, 0.f);
+                }
+            } else if (pair) {
                 reinterpret_cast<float2*>(Qt)[r] = make_float2(m, l);
+            }
+            if (pair) {
                 fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive1(bar(B_ML));
                 if (!wait_all(B_ML, (uint32_t)pairs)) break;
                 fence_after();                                                  // (the other half's O is read here too)
-                const float2 x = reinterpret_cast<const float2*>(sm)[r], y = reinterpret_cast<const float2*>(sm + C::kTileBytes)[r];
-                m = fmaxf(x.x, y.x);
-                const float base = m == -INFINITY ? 0.f : m;
-                f0 = ex2(x.x - base);
-                f1 = ex2(y.x - base);
-                l = f0 * x.y + f1 * y.y;
-                f0 *= kDown;
-                f1 *= kDown;
+                if constexpr (QZ) {
+                    const float4 x = reinterpret_cast<const float4*>(sm)[r], y = reinterpret_cast<const float4*>(sm + C::kTileBytes)[r];
+                    ml = fmaxf(x.z, y.z);
+                    const float base = ml == -INFINITY ? 0.f : ml;
+                    l = ex2(x.z - base) * x.y + ex2(y.z - base) * y.y;
+                    f0 = root(x.x, ml + kRoom);
+                    f1 = root(y.x, ml + kRoom);
+                } else {
+                    const float2 x = reinterpret_cast<const float2*>(sm)[r], y = reinterpret_cast<const float2*>(sm + C::kTileBytes)[r];
+                    m = fmaxf(x.x, y.x);
+                    const float base = m == -INFINITY ? 0.f : m;
+                    f0 = ex2(x.x - base);
+                    f1 = ex2(y.x - base);
+                    l = f0 * x.y + f1 * y.y;
+                }
+            }
+            if (QZ) {
+                m = ml + kRoom;
+                l *= ex2(-kRoom);
             }
             const int row = tile_row + r, flat = g.r0 + row, seq = flat / p.G;
             const bool mine = row < g.R && n > 0;
@@ -656,13 +832,13 @@ __global__ void __launch_bounds__(PCfg<D, QZ, CV>::kThreads, 1) prefix_tc_kernel
                         tmem_ld32(tb + lo + C::TO(1) + x, z);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) o[y] = fmaf(f0, o[y], f1 * z[y]);
+                        for (int y = 0; y < 32; ++y) o[y] = QZ ? fmaf(f0 * o[y], f0, f1 * z[y] * f1) : fmaf(f0, o[y], f1 * z[y]);
                     } else {
                         tmem_ld32(to + x, o);
                         tmem_wait_ld();
                         if (QZ) {
 #pragma unroll
-                            for (int y = 0; y < 32; ++y) o[y] *= f0;
+                            for (int y = 0; y < 32; ++y) o[y] = o[y] * f0 * f0;
                         }
                     }
                     if (mine) {
@@ -722,7 +898,8 @@ cudaError_t launch_prefix_tc(const DecodeArgs& a, cudaStream_t st) {
     if (!a.p.Ks) return a.p.d == 128 ? launch_tc<128, false, 0>(a, st) : launch_tc<64, false, 0>(a, st);
     if (a.p.d == 64) return launch_tc<64, true, 1>(a, st);
     // One tile of rows whatever the prefixes' sequences are: half of the softmax, and the conversion is what counts (32
-    // sequences behind 131072 tokens, 32/8 heads: 101 us, 116 with four converting warps; 64: 142 and 131).
+    // sequences with up to 100 tokens of their own behind 131072, 32/8 heads, the whole call: 120 us, 127 with four
+    // converting warps).
     return (int64_t)a.sh.n_seq * a.p.G <= kM ? launch_tc<128, true, 2>(a, st) : launch_tc<128, true, 1>(a, st);
 }
 

@@ -192,7 +192,7 @@ def test_decode_powers_far_apart(L, gen, dtype, d, Hq, Hkv, kind):
 
 
 @pytest.mark.parametrize("kind", APART)
-@pytest.mark.parametrize("once", [False], ids=["few"])
+@pytest.mark.parametrize("once", [False, True], ids=["few", "once"])
 @pytest.mark.parametrize("dtype,d,Hq,Hkv,members", [(BF, 128, 8, 2, 5), (BF, 128, 8, 1, 40), (BF, 64, 12, 1, 9), (BF, 64, 12, 1, 30),
                                                     (F32, 128, 4, 1, 5)])
 def test_shared_powers_far_apart(L, gen, dtype, d, Hq, Hkv, members, once, kind):
@@ -207,3 +207,23 @@ def test_shared_powers_far_apart(L, gen, dtype, d, Hq, Hkv, members, once, kind)
     for b in range(0, members, max(1, members // 6)):
         k, v = (torch.cat([x[i] for x in s.parts(b)]) for i in (0, 1))
         check_apart(q[b], k, v, out[b], lse[b], 1 if kind == "high" else 2, f"sequence {b}")
+
+
+@pytest.mark.parametrize("d,Hq,Hkv,members", [(128, 8, 1, 5), (128, 8, 1, 40), (64, 12, 1, 30)])
+def test_shared_powers_far_apart_beside_bad_pages(L, gen, d, Hq, Hkv, members):
+    """Tokens on pages outside the cache have no weight, and their places' powers no say."""
+    page, n = 16, 1300
+    s = Behind(gen, True, [n], [members], [3] * members, Hkv, d, page, BF)
+    far_apart(gen, s.c, "values", Hkv, d)
+    table = s.prefix_table.clone()
+    table[0, 2::5] = -1
+    pos = torch.arange(n, device="cuda")
+    seen = table[0, pos // page] >= 0
+    q = apart_queries(gen, members, Hq, d, BF)
+    lse = torch.empty(members, Hq, dtype=F32, device="cuda")
+    lay = s.layer(L, Hq, Hkv, d, BF)
+    out = lay.decode_shared(q, s.kv_len, s.table, s.prefix_len, table, s.cu, lse=lse)
+    assert L.lola_attn_status() == (L.LOLA_ERR_DEVICE, L.LOLA_ATTN_BAD_PAGE)
+    for b in range(0, members, 4):
+        k, v = (torch.cat([x[0][seen], x[1 + b]]) for x in (s.c.k, s.c.v))
+        check_apart(q[b], k, v, out[b], lse[b], 2, f"sequence {b}")
