@@ -547,9 +547,9 @@ int64_t lola_shared_decode_workspace_bytes(const lola_attn_config* cfg, int32_t 
  * read for each sequence, by one kernel.)
  * kv describes the pools and the sequences' own tokens (kv_len 0: none; the tokens are counted from 0 behind the
  * prefix, so that an append of them takes explicit positions).  A sequence outside cu[0] .. cu[n] - 1 has no prefix.
- * Offsets that decrease or pass n_seq leave their prefix without sequences and set LOLA_ATTN_BAD_OFFSETS; sequences
- * that then belong to several see one of them, or none.  Pages outside the cache and lengths beyond the tables are
- * treated as in lola_paged_decode.  The same inputs give the same bits. */
+ * Offsets that decrease or pass n_seq leave their prefix without sequences and set LOLA_ATTN_BAD_OFFSETS; where
+ * sequences then belong to several prefixes, their results mean nothing.  Pages outside the cache and lengths beyond
+ * the tables are treated as in lola_paged_decode.  The same inputs give the same bits. */
 int32_t lola_shared_decode(const lola_attn_config* cfg, const lola_paged_kv* kv, const lola_kv_scales* scales,
                            const lola_prefixes* prefixes, const lola_rows* Q, const lola_rows* O, float* lse, void* workspace,
                            size_t workspace_bytes, void* stream);

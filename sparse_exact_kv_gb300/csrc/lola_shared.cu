@@ -25,23 +25,31 @@ struct JoinArgs {
     float* lse;
 };
 
-// The prefix of sequence b (one warp), if it has one with tokens, or -1: where offsets are malformed, only one whose
-// kernel has worked for b too.
+// The prefix of sequence b (one warp), if it has one with tokens, or -1.  A prefix has sequence b if its own two offsets say
+// so, whatever the others are, as for the kernels before.
 __device__ __forceinline__ int prefix_of(const JoinArgs& a, int b, int lane) {
-    int g = 0, lo, n, bad = 0;
-    if (a.cu && a.prefix.n_seq < kWarp) {
+    const int n = a.prefix.n_seq;
+    auto holds = [&](int begin, int end) { return begin >= 0 && begin <= b && b < end && end <= a.p.n_seq; };
+    int g = 0;
+    if (a.cu && n < kWarp) {
         // (few prefixes: all offsets and lengths at once)
-        const int c = lane <= a.prefix.n_seq ? a.cu[lane] : 0x7fffffff, len = lane < a.prefix.n_seq ? a.prefix.kv_len[lane] : 0;
-        g = 31 - __clz(__ballot_sync(0xffffffffu, c <= b));
-        const int begin = __shfl_sync(0xffffffffu, c, max(g, 0)), end = __shfl_sync(0xffffffffu, c, min(g + 1, kWarp - 1));
+        const int c = lane <= n ? a.cu[lane] : 0x7fffffff, len = lane < n ? a.prefix.kv_len[lane] : 0;
+        const int end = __shfl_down_sync(0xffffffffu, c, 1);
+        g = 31 - __clz(__ballot_sync(0xffffffffu, lane < n && holds(c, end)));
         const int tokens = __shfl_sync(0xffffffffu, len, max(g, 0));
-        return g >= 0 && g < a.prefix.n_seq && begin >= 0 && end > b && end <= a.p.n_seq && paged_tokens(a.prefix, tokens) > 0 ? g : -1;
+        return g >= 0 && paged_tokens(a.prefix, tokens) > 0 ? g : -1;
     }
     if (a.cu) {
-        g = warp_find_seq(a.cu, a.prefix.n_seq, b, lane);
-        if (g < 0 || g >= a.prefix.n_seq) return -1;
-        seq_rows(a.cu, g, a.p.n_seq, &lo, &n, &bad);
-        if (b < lo || b >= lo + n) return -1;
+        g = warp_find_seq(a.cu, n, b, lane);
+        if (g < 0 || g >= n || !holds(a.cu[g], a.cu[g + 1])) {
+            // (none, or offsets that do not increase: all of them)
+            int own = -1;
+#pragma unroll 4
+            for (int x = lane; x < n; x += kWarp)
+                if (holds(a.cu[x], a.cu[x + 1])) own = x;
+            g = __reduce_max_sync(0xffffffffu, own);
+            if (g < 0) return -1;
+        }
     }
     return paged_tokens(a.prefix, a.prefix.kv_len[g]) > 0 ? g : -1;
 }

@@ -227,3 +227,40 @@ def test_shared_powers_far_apart_beside_bad_pages(L, gen, d, Hq, Hkv, members):
     for b in range(0, members, 4):
         k, v = (torch.cat([x[0][seen], x[1 + b]]) for x in (s.c.k, s.c.v))
         check_apart(q[b], k, v, out[b], lse[b], 2, f"sequence {b}")
+
+
+# ---------------------------------------------------------------------------------------
+# malformed offsets
+# ---------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("once", [False, True], ids=["few", "once"])
+@pytest.mark.parametrize("dtype,quant", [(BF, False), (BF, True), (F32, False), (F32, True)])
+@pytest.mark.parametrize("cu,of", [([0, 2, 4, 0], [0, 0, 1, 1, -1, -1]), ([4, 2, 4, 6], [-1, -1, 1, 1, 2, 2]),
+                                   ([5, 0, 3, 1], [1, 1, 1, -1, -1, -1]), ([0, 3, -1, 7], [0, 0, 0, -1, -1, -1])])
+def test_prefixes_with_sound_offsets_keep_their_sequences(L, gen, dtype, quant, cu, of, once):
+    """Offsets that decrease or leave the batch cost their own prefix its sequences, and no other."""
+    s = Behind(gen, quant, [90, 80, 70], [2, 2, 2], [5, 6, 7, 8, 9, 10], 1, 64, 16, dtype, once)
+    q = randn(gen, 6, 2, 64, dtype=dtype)
+    s.cu, s.of = ints(cu), of
+    out = s.layer(L, 2, 1, 64, dtype).decode_shared(q, *s.args())
+    assert L.lola_attn_status() == (L.LOLA_ERR_DEVICE, L.LOLA_ATTN_BAD_OFFSETS)
+    s.check(q, out)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_many_prefixes_with_sound_offsets_keep_their_sequences(L, gen, quant):
+    """More prefixes than one look takes in, the last offset (or one in between) below the others."""
+    k, n = 70, 80
+    s = Behind(gen, quant, [20 + i for i in range(k)], [1] * k, [3] * n, 1, 64, 16, BF, start=4)
+    q = randn(gen, n, 2, 64, dtype=BF)
+    lay = s.layer(L, 2, 1, 64, BF)
+    s.check(q, lay.decode_shared(q, *s.args()))
+    quiet(L)
+    well = s.cu.tolist()
+    for at, to, lost in ((k, 0, [k - 1]), (0, 70, [0]), (33, -5, [32, 33]), (50, 999, [49, 50])):
+        cu = list(well)
+        cu[at] = to
+        s.cu, s.of = ints(cu), [-1] * 4 + [-1 if g in lost else g for g in range(k)] + [-1] * (n - k - 4)
+        out = lay.decode_shared(q, *s.args())
+        assert L.lola_attn_status() == (L.LOLA_ERR_DEVICE, L.LOLA_ATTN_BAD_OFFSETS), cu
+        s.check(q, out)
