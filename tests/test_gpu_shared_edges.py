@@ -264,3 +264,21 @@ def test_many_prefixes_with_sound_offsets_keep_their_sequences(L, gen, quant):
         out = lay.decode_shared(q, *s.args())
         assert L.lola_attn_status() == (L.LOLA_ERR_DEVICE, L.LOLA_ATTN_BAD_OFFSETS), cu
         s.check(q, out)
+
+
+# ---------------------------------------------------------------------------------------
+# many rows
+# ---------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("quant,d,Hq,Hkv,prefixes,members,own", [
+    (False, 128, 8, 1, [900, 400, 1300], [40, 3, 70], 5),      # several items of 256 rows, of prefixes that are not alone
+    (True, 128, 8, 1, [900, 400, 1300], [40, 3, 70], 5), (True, 64, 32, 1, [500, 640], [17, 30], 3),
+    (False, 64, 64, 1, [300], [310], 2),                       # one prefix, 78 items: more than half of the CTAs
+    (True, 64, 64, 1, [300], [310], 2), (False, 64, 64, 1, [129], [150], 0)])
+def test_shared_many_rows(L, gen, quant, d, Hq, Hkv, prefixes, members, own):
+    n = sum(members)
+    s = Behind(gen, quant, prefixes, members, [own] * n, Hkv, d, 64, BF)
+    q = randn(gen, n, Hq, d, dtype=BF)
+    out = s.layer(L, Hq, Hkv, d, BF).decode_shared(q, *s.args())
+    quiet(L)
+    s.check(q, out, only=range(0, n, 9))
