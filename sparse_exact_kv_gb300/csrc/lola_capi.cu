@@ -386,9 +386,11 @@ int32_t quant_check(const lola_attn_config* c, const lola_paged_kv* kv, const lo
 }
 constexpr int64_t kMostRows = (int64_t)1 << 28;     // (sequence, query head) rows of a lola_shared_decode
 // Bytes of prefixes, counted for each sequence that might see them, up to which lola_shared_decode reads them so, from L2
-// for the most part (one kernel and three, us a call: d = 128, 32/8 heads, 4 sequences behind 300 tokens, bfloat16, 5 MB, 11
-// and 19; 16 behind 1000, 67 MB, 18.1 and 19.3; behind 2000, 134 MB, 23.8 and 20.2; 16 behind 2000, e4m3, 67 MB, 21 and 24;
-// d = 64, 8/4 heads, float32, 66 MB, 18.8 and 18.6).
+// for the most part.  One kernel and three, us a call, d = 128, 32/8 heads, pages of 16, own tokens of 30: 4 sequences
+// behind 300 tokens, bfloat16, 5 MB, 12.0 and 19.6; 16 behind 900, 60 MB, 21.3 and 20.6; 16 behind 1940, e4m3, 64 MB, 24.5
+// and 25.1; pages of 64: 16 behind 1000, bfloat16, 67 MB, 18.1 and 19.3, behind 2000, 134 MB, 23.8 and 20.2.  d = 64: 8/4
+// heads, float32, 66 MB, 18.8 and 18.6; 24/4 heads, e4m3, 32 behind 3800, 62 MB, 31.3 and 24.8 (groups of six share a key's
+// bytes, but not its products).  So they meet between some 40 and 90 MB, and one limit serves all types and heads.
 constexpr double kReadAgain = 64e6;
 }  // namespace
 

@@ -25,7 +25,7 @@ constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint64_t kDrainNs = 50000000ull;   // ... for copies in flight, when a wait has given up
 
 struct Maps {
-    CUtensorMap k, v;   // [n_pages * Hkv][page][d] as 128-byte columns, boxes of min(page, 64) rows (e4m3: of 128
+    CUtensorMap k, v;   // [n_pages * Hkv][page][d] as 128-byte columns, boxes of min(page, a tile's tokens) rows (e4m3: of 128
                         // bytes, which are two tokens at d = 64)
 };
 
@@ -257,7 +257,7 @@ __device__ __forceinline__ bool find_start(const Args& a, Start* st) {
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
     int bits = 0;
     auto count = [&](int b) -> int64_t { return b < p.n_seq ? units_of<SH, TILE, ROWS, PRE>(a, b, &bits) : 0; };
-    const int64_t own = count(threadIdx.x);            // (the whole of it up to 288 sequences)
+    const int64_t own = count(threadIdx.x);            // (the whole of it up to NT sequences)
     int64_t rest = 0;
     for (int b = threadIdx.x + NT; b < p.n_seq; b += NT) rest += count(b);
     st->total = block_total<NT>(own + rest, sums);

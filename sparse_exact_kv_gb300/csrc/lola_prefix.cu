@@ -24,7 +24,7 @@
 // K and V.)
 // m is raised lazily, as in lola_attn_tc.cu: it is set 8 above a maximum, so that no weight is above one.
 // Long prefixes: bfloat16, 128 sequences behind 131072 tokens, 32/8 heads, d = 128, 198 us, 1390 TFLOP/s, bound by the way from
-// scores to weights beside the products; a quantised cache 256 us, 1070 TFLOP/s, bound by the conversion beside that (a block
+// scores to weights beside the products; a quantised cache 259 us, 1060 TFLOP/s, bound by the conversion beside that (a block
 // of K or V takes its four warps 560 clocks alone, 1300 there).  Short ones by their start: 64 sequences behind 16001
 // tokens take 33 us, of which lookups, TMEM and the first block are 6 and the first pass through the softmax's code, which
 // comes into the instruction caches meanwhile, another 5 (a pass over an empty block ahead of the first one, less code, and
@@ -71,7 +71,7 @@ template <int D, bool QZ, int CV> struct PCfg {
     static constexpr int kLaunchRegs = QZ ? (CV == 2 ? 96 : 128) : 168;
     static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs, "more than the block has");
     // Scores in registers.  QZ at d = 128 is bound by the conversion, whose warps need their 128 registers and the schedulers'
-    // time: the softmax goes over S twice there, 32 columns at a time (128 sequences behind 131072 tokens, 32/8 heads: 256 us;
+    // time: the softmax goes over S twice there, 32 columns at a time (128 sequences behind 131072 tokens, 32/8 heads: 256 us,
     // half of the scores held 300, all of them, with 192 and 64 registers, 334).  Elsewhere S is
     // read once (bfloat16, the same size: 198 us, 221 in the loop; QZ, d = 64, 24/4 heads: 162 and 171).
     static constexpr int kHeld = QZ && D == 128 ? 32 : kN;
@@ -187,11 +187,6 @@ __global__ void __launch_bounds__(PCfg<D, QZ, CV>::kThreads, 1) prefix_tc_kernel
     extern __shared__ __align__(1024) uint8_t smraw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(sm);
-    // (QZ: the array's own alignment leaves the last 1024 bytes to the tables)
-    if (QZ && sm != smraw) {
-        if (threadIdx.x == 0) atomicOr(&g_status, (int)LOLA_ATTN_TIMEOUT);
-        return;
-    }
     enum {
         B_SEG = 0, B_SEGFREE = 2, B_Q = 4, B_S = 6, B_P = 8, B_O = 10, B_ML = 12, B_READ, B_DONE, B_FULL,
         B_EMPTY = B_FULL + kRing, B_RFULL = B_EMPTY + kRing, B_REMPTY = B_RFULL + kRaw, B_N = B_REMPTY + kRaw
@@ -231,6 +226,11 @@ __global__ void __launch_bounds__(PCfg<D, QZ, CV>::kThreads, 1) prefix_tc_kernel
         abort_sm = 0;
     }
     wait_for_last_kernel();
+    // (QZ: the array's own alignment leaves the last 1024 bytes to the tables)
+    if (QZ && sm != smraw) {
+        if (tid == 0) atomicOr(&g_status, (int)LOLA_ATTN_TIMEOUT);
+        return;
+    }
     Start st;
     int share = 1;                           // CTAs of a piece, one for each row item
     if (p.n_seq == 1) {

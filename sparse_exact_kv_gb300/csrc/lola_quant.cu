@@ -67,7 +67,8 @@ template <typename T, typename TO, int D, int NB> struct TSmem {
 // Tile n is group n % kGroups', a warp has a quarter of its tokens, 16 at a time.  A group that is done with its tiles of a
 // segment adds its warps up and goes on to the next segment; the last of a segment's groups to be done adds the groups up, in
 // their order.  So a sequence of one tile takes one group, and the others' tiles run beside its end (all warps at the segment's
-// end together: 64 sequences of 1000-8000 tokens, 32/8 heads, d = 128, e4m3, 94 us; 1024 items of 64 tokens 37 us).
+// end together: 64 sequences of 1000-8000 tokens, 32/8 heads, d = 128, e4m3, 94 us, by turns 88; 1024 items of 64 tokens
+// 37 and 18 us).
 template <typename T, typename TO, int D, int NB, bool SH, bool PRE>
 __global__ void __launch_bounds__(TSmem<T, TO, D, NB>::kAll * kWarp, 1) decode_t_kernel(const __grid_constant__ Maps maps, const Args a) {
     using M = TSmem<T, TO, D, NB>;

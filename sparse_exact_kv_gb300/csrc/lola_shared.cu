@@ -6,8 +6,9 @@
 //   m = max_k m_k,  l = sum_k 2^{m_k - m} l_k,  o = sum_k 2^{m_k - m} z_k / l,
 // the prefix' parts first, in the order of the pieces: the same inputs give the same bits.
 // Bound by its chain of accesses (which parts, the parts): two rows a CTA, their parts dealt out to eight warps,
-// which have three of them in flight each (64 sequences behind 16001 tokens, 32 heads, 19 prefix parts a row: 10 us).  (When the kernel over the own tokens read the prefix' parts itself, row
-// after row, 64 sequences behind 16001 tokens took it 92 us, 8 heads, d = 128.)
+// which have three of them in flight each (64 sequences behind 16001 tokens, 32 heads, 19 prefix parts a row: 10 us).
+// (When the kernel over the own tokens read the prefix' parts itself, row after row, 64 sequences behind 16001 tokens took
+// it 92 us, 8 heads, d = 128.)
 // Three kernels take 20 us whatever there is to do; few tokens altogether go to K10's and K11's kernels in a form whose
 // sequences' tiles are those of the prefix, then their own (PRE).
 #include <algorithm>
